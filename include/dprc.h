@@ -393,6 +393,135 @@ dprc_status dprc_philox_words(uint32_t* out, int64_t n_blocks, uint64_t first_bl
                               uint64_t seed, uint64_t step, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The operators around the norm path: the embedding, dropout, the linear map.
+ *
+ * With them a model of embeddings, linear maps (bias, activation, dropout,
+ * residual) and its per-sample clipping runs on this library: the norms of
+ * linear weights come from the entry points above, the embedding's and a
+ * bias's from dprc_embed_norm.  Tensors are dense, row-major and 16-byte
+ * aligned; widths are arbitrary.  The workspaces and plans of these calls need
+ * no zeroing, and results repeat bitwise for fixed inputs, sizes and device.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Embedding lookup:  out[j] = scale * W[tokens[j]]  (formed in fp32, rounded
+ * once to dtype).
+ *  W device [V][d], out device [N][d], both dtype; tokens device [N], int32
+ *  (token_bytes 4) or int64 (8).  A negative token is "no token" (padding): its
+ *  row is zero.  A token >= V reads nothing either, and sets
+ *  DPRC_DEVERR_TOKEN in the device error word.
+ *  N >= 0, 1 <= V <= 2^30, d >= 1, scale finite.
+ */
+dprc_status dprc_embed_lookup(const void* W, dprc_dtype dtype, const void* tokens,
+                              int token_bytes, int64_t N, int64_t V, int64_t d, float scale,
+                              void* out, void* stream);
+
+/*
+ * The order in which an embedding's gradient is summed: the N tokens sorted
+ * stably with their positions ("no token" last).  One plan serves every
+ * dprc_embed_norm and dprc_embed_grad call on the same tokens.
+ *  plan device, dprc_embed_plan_bytes(N, V) bytes (0 for invalid sizes).
+ *  Tokens as for dprc_embed_lookup.
+ */
+size_t dprc_embed_plan_bytes(int64_t N, int64_t V);
+dprc_status dprc_embed_plan(const void* tokens, int token_bytes, int64_t N, int64_t V, void* plan,
+                            size_t plan_bytes, void* stream);
+
+/*
+ * Exact squared norm of each sample's embedding gradient:
+ *     n[i] (+)= scale^2 sum_v || sum_{t: tok_it = v} G_it ||^2
+ * The row of the gradient of token v is the sum of G over the positions that
+ * hold v, so the norm needs those sums and not the [V][d] matrix.  A bias is an
+ * embedding of one row that every position reads: with V = 1 and all tokens 0
+ * this is || sum_t G_it ||^2, the norm of a bias's gradient.
+ *  G device [B][T][d] of dtype (the gradient of the lookup's output); plan of
+ *  the B*T tokens (position i T + t); n device float [B]; accumulate as above.
+ *  ws device, dprc_embed_workspace_bytes(dtype, B, T, d) bytes.
+ *  1 <= B <= 65535, T >= 0 (T = 0: zero norms).  Sums in fp32.  G at positions
+ *  without a token is not read.
+ */
+size_t dprc_embed_workspace_bytes(dprc_dtype dtype, int64_t B, int64_t T, int64_t d);
+dprc_status dprc_embed_norm(const void* G, dprc_dtype dtype, int64_t B, int64_t T, int64_t V,
+                            int64_t d, float scale, const void* plan, size_t plan_bytes, float* n,
+                            int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The (clipped) gradient of an embedding, summed over the samples:
+ *     dW[v] (+)= scale sum_i c[i] sum_{t: tok_it = v} G_it
+ *  c device float [B] (clip factors), or NULL for all 1.  dW device [V][d] of
+ *  dtype: every row is written (zero where no position holds v); with
+ *  accumulate != 0 the sums are added to it (in fp32, rounded once) and rows
+ *  without a token stay untouched.  The rest as for dprc_embed_norm.
+ */
+dprc_status dprc_embed_grad(const void* G, dprc_dtype dtype, const float* c, int64_t B, int64_t T,
+                            int64_t V, int64_t d, float scale, const void* plan,
+                            size_t plan_bytes, void* dW, int accumulate, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * Dropout with an optional residual; the mask comes from the Philox stream of
+ * dprc_philox_words and is never stored:
+ *     y[i] = residual[i] + (dropped(first_element + i) ? 0 : x[i] * s)
+ * Element e is dropped when half (e & 7) of block e >> 3 (its four words as
+ * eight 16-bit halves, the low half of a word first) is below
+ * t = floor(65536 p + 1/2), and s = 65536 / (65536 - t), so the mean is kept
+ * exactly.  The gradient with respect to x is the same call on dy without a
+ * residual.  A dropped element is 0 whatever x holds (NaN and infinity too).
+ * Use a seed of its own: the noise of the same (seed, step) reads the same words.
+ *  x, residual (or NULL), y device [N] of dtype; y may be x or residual.
+ *  0 <= p <= 1; formed in fp32, rounded once.
+ */
+dprc_status dprc_dropout(const void* x, const void* residual, dprc_dtype dtype, int64_t N,
+                         uint64_t first_element, double p, uint64_t seed, uint64_t step, void* y,
+                         void* stream);
+
+/* Activations.  GELU is z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2, SiLU
+ * z / (1 + exp(-z)). */
+typedef enum {
+    DPRC_ACT_NONE = 0,
+    DPRC_ACT_RELU = 1,
+    DPRC_ACT_GELU = 2,
+    DPRC_ACT_SILU = 3
+} dprc_act;
+
+/*
+ * Linear map with its epilogue:
+ *     z = X W^T + bias,   Y = residual + drop(act(z))
+ *  X device [M][K] (M tokens), W device [N][K], bias [N] or NULL, residual
+ *  [M][N] or NULL, Y [M][N], all dtype.  Z [M][N] or NULL receives z (needed by
+ *  the gradient of an activation).  drop is dprc_dropout's with first_element 0
+ *  on the [M][N] tensor; p = 0 drops nothing.  Y may be residual.
+ *  Sums and epilogue in fp32, each output rounded once.  bf16 products are
+ *  exact; fp32 products are formed from three bf16 parts of each factor (an
+ *  error near 2^-24 of each product's size; a row with a non-finite value gives
+ *  a non-finite or NaN result).
+ *  M >= 0, 1 <= K, N <= 2^20.
+ *  ws device, dprc_linear_workspace_bytes(dtype, M, K, N, 0) bytes.
+ */
+size_t dprc_linear_workspace_bytes(dprc_dtype dtype, int64_t M, int64_t K, int64_t N, int grad);
+dprc_status dprc_linear(const void* X, const void* W, const void* bias, const void* residual,
+                        dprc_dtype dtype, int64_t M, int64_t K, int64_t N, dprc_act act, double p,
+                        uint64_t seed, uint64_t step, void* Z, void* Y, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/*
+ * Gradient of dprc_linear (act, p, seed and step as in its call):
+ *     dZ = drop(dY) act'(Z),  dX = dZ W,  dW = dZ^T X,  db = sum over tokens of dZ
+ *  (the gradient with respect to the residual is dY).  Any of dX [M][K],
+ *  dW [N][K], db [N], dZ [M][N] may be NULL and is then not computed; not all.
+ *  Z [M][N] is required for an activation; X for dW, W for dX.  dZ with the
+ *  layer's input are the G and A of the norm estimates.
+ *  For bf16, dZ enters the products rounded to bf16; db sums it unrounded.
+ *  ws device, dprc_linear_workspace_bytes(dtype, M, K, N, 1) bytes.
+ */
+dprc_status dprc_linear_grad(const void* dY, const void* X, const void* W, const void* Z,
+                             dprc_dtype dtype, int64_t M, int64_t K, int64_t N, dprc_act act,
+                             double p, uint64_t seed, uint64_t step, void* dX, void* dW, void* db,
+                             void* dZ, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Reads (and, if reset != 0, clears) the device error word of the current
  * device.  Nonzero means a bounded in-kernel wait ran out, or a kernel
  * refused a launch shape it was not planned for (the value encodes which: see
@@ -410,6 +539,7 @@ dprc_status dprc_philox_words(uint32_t* out, int64_t n_blocks, uint64_t first_bl
 #define DPRC_DEVERR_BOUNDS 7      /* bounds-checked build only (libdprc_debug.so): an index
                                      failed its check and the access was skipped; the
                                      word's bits above the low 8 hold the source line */
+#define DPRC_DEVERR_TOKEN 8       /* a token id of V or more was read (as "no token") */
 dprc_status dprc_device_error(int32_t* out, int reset);
 
 /*

@@ -17,6 +17,8 @@ norms   exact norm (direct, ghost, trace forms), Hutchinson, Hutch++, layerwise
 philox  Philox4x32-10 counter-based generator (Salmon et al., SC'11), the
         uniform -> normal transform and the Gaussian noise add.
 rademacher  the +-1 projection variant (signs from the Philox stream, 1/k scale).
+operators  the embedding (lookup, per-sample norm, clipped gradient), dropout and
+        the linear map with its epilogue and gradient.
 cost    the analytic FLOP / memory counts behind the pages' efficiency table.
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test against
@@ -47,4 +49,4 @@ from .rademacher import (  # noqa: F401
     hutch_norm_rademacher,
     rademacher_variance,
 )
-from . import cost  # noqa: F401
+from . import cost, operators  # noqa: F401

@@ -8,6 +8,7 @@ the tests and the benchmark.
 """
 
 from .binding import (  # noqa: F401
+    DPRC_ACTS,
     DPRC_BF16,
     DPRC_EXACT_AUTO,
     DPRC_EXACT_DIRECT,
@@ -23,13 +24,21 @@ from .binding import (  # noqa: F401
     DPRC_OP_HUTCHPP,
     EXPORTED,
     DprcError,
+    EmbedPlan,
     dprc_abi_version,
     dprc_add_noise,
     dprc_add_noise_at,
     dprc_clip_factors,
     dprc_device_error,
+    dprc_dropout,
+    dprc_embed_grad,
+    dprc_embed_lookup,
+    dprc_embed_norm,
+    dprc_embed_plan,
     dprc_exact_norm,
     dprc_exact_norm_plan,
+    dprc_linear,
+    dprc_linear_grad,
     dprc_norm_hutch,
     dprc_norm_hutch_clip,
     dprc_norm_hutch_clip_host,

@@ -94,6 +94,33 @@ _PROTOS = [
      [_c.c_int, _c.c_uint64, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
       _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_size_t,
       _c.c_void_p]),
+    ("dprc_embed_plan_bytes", _c.c_size_t, [_c.c_int64, _c.c_int64]),
+    ("dprc_embed_workspace_bytes", _c.c_size_t, [_c.c_int, _c.c_int64, _c.c_int64, _c.c_int64]),
+    ("dprc_embed_lookup", _c.c_int,
+     [_c.c_void_p, _c.c_int, _c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64,
+      _c.c_float, _c.c_void_p, _c.c_void_p]),
+    ("dprc_embed_plan", _c.c_int,
+     [_c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    ("dprc_embed_norm", _c.c_int,
+     [_c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_float,
+      _c.c_void_p, _c.c_size_t, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    ("dprc_embed_grad", _c.c_int,
+     [_c.c_void_p, _c.c_int, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64,
+      _c.c_float, _c.c_void_p, _c.c_size_t, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_size_t,
+      _c.c_void_p]),
+    ("dprc_dropout", _c.c_int,
+     [_c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int64, _c.c_uint64, _c.c_double, _c.c_uint64,
+      _c.c_uint64, _c.c_void_p, _c.c_void_p]),
+    ("dprc_linear_workspace_bytes", _c.c_size_t,
+     [_c.c_int, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int]),
+    ("dprc_linear", _c.c_int,
+     [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64,
+      _c.c_int64, _c.c_int, _c.c_double, _c.c_uint64, _c.c_uint64, _c.c_void_p, _c.c_void_p,
+      _c.c_void_p, _c.c_size_t, _c.c_void_p]),
+    ("dprc_linear_grad", _c.c_int,
+     [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int64, _c.c_int64,
+      _c.c_int64, _c.c_int, _c.c_double, _c.c_uint64, _c.c_uint64, _c.c_void_p, _c.c_void_p,
+      _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t, _c.c_void_p]),
 ]
 EXPORTED = tuple(name for name, _, _ in _PROTOS)
 
@@ -337,7 +364,8 @@ def dprc_norm_hutch_noalloc(A, G, P, n, accumulate=False, stream=None):
 
 # Device error codes (DPRC_DEVERR_* of include/dprc.h).
 (DPRC_DEVERR_PIPE_FULL, DPRC_DEVERR_PIPE_EMPTY, DPRC_DEVERR_ACCUM, DPRC_DEVERR_CLUSTER,
- DPRC_DEVERR_READY, DPRC_DEVERR_LAUNCH, DPRC_DEVERR_BOUNDS) = (1, 2, 3, 4, 5, 6, 7)
+ DPRC_DEVERR_READY, DPRC_DEVERR_LAUNCH, DPRC_DEVERR_BOUNDS,
+ DPRC_DEVERR_TOKEN) = (1, 2, 3, 4, 5, 6, 7, 8)
 FAULT_READY_NEVER_MET, FAULT_CLUSTER_SHAPE = 0, 1
 
 
@@ -460,3 +488,186 @@ def dprc_set_phase_events(events):
     arr = (ctypes.c_void_p * len(events))(*[ctypes.c_void_p(e.cuda_event) for e in events])
     _events_keepalive = (arr, events)
     _check("dprc_set_phase_events", lib().dprc_set_phase_events(arr, len(events)))
+
+
+# ---------------------------------------------------------------------------
+# The operators around the norm path (include/dprc.h says what each computes).
+# ---------------------------------------------------------------------------
+DPRC_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+_U64 = 2**64 - 1
+
+
+def _same(name, t, dtype, shape=None, device=None):
+    """An optional tensor of the call's dtype (and shape and device)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, the call's tensors are {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} is needed")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {device}")
+
+
+def _token_bytes(tokens):
+    if tokens.dtype == torch.int64:
+        return 8
+    if tokens.dtype == torch.int32:
+        return 4
+    raise TypeError(f"tokens are int32 or int64, not {tokens.dtype}")
+
+
+def dprc_embed_lookup(W, tokens, scale=1.0, out=None, stream=None):
+    """out[..., :] = scale * W[tokens[...]], zero rows for negative tokens."""
+    V, d = W.shape
+    if out is None:
+        out = torch.empty((*tokens.shape, d), dtype=W.dtype, device=W.device)
+    _need_cuda(W, tokens, out)
+    _same("out", out, W.dtype, (*tokens.shape, d), W.device)
+    _check("dprc_embed_lookup",
+           lib().dprc_embed_lookup(W.data_ptr(), _dtype_code(W), tokens.data_ptr(),
+                                   _token_bytes(tokens), tokens.numel(), V, d, scale,
+                                   out.data_ptr(), _stream(W, stream)))
+    return out
+
+
+class EmbedPlan:
+    """The sorted token order of tokens [B][T] over a vocabulary of V
+    (dprc_embed_plan), as dprc_embed_norm and dprc_embed_grad take it."""
+
+    __slots__ = ("B", "T", "V", "buf")
+
+    def __init__(self, B, T, V, buf):
+        self.B, self.T, self.V, self.buf = B, T, V, buf
+
+
+def dprc_embed_plan(tokens, V, buf=None, stream=None):
+    """Sorts tokens [B][T]; returns an EmbedPlan.  buf: a uint8 device buffer
+    of dprc_embed_plan_bytes(B * T, V) bytes to keep it in."""
+    B, T = tokens.shape
+    size = _token_bytes(tokens)
+    if buf is None:
+        n = lib().dprc_embed_plan_bytes(B * T, V)
+        if n == 0:
+            raise DprcError("dprc_embed_plan_bytes", 2)
+        buf = torch.empty(n, dtype=torch.uint8, device=tokens.device)
+    _need_cuda(tokens, buf)
+    _check("dprc_embed_plan",
+           lib().dprc_embed_plan(tokens.data_ptr(), size, B * T, V,
+                                 buf.data_ptr(), buf.numel(), _stream(tokens, stream)))
+    return EmbedPlan(B, T, int(V), buf)
+
+
+def _embed_ws(G, plan, ws):
+    if G.dim() != 3 or G.shape[0] != plan.B or G.shape[1] != plan.T:
+        raise ValueError(f"G has shape {tuple(G.shape)}, the plan is of {plan.B} x {plan.T} tokens")
+    if ws is None:
+        n = lib().dprc_embed_workspace_bytes(_dtype_code(G), plan.B, plan.T, G.shape[2])
+        if n == 0:
+            raise DprcError("dprc_embed_workspace_bytes", 2)
+        ws = torch.empty(n, dtype=torch.uint8, device=G.device)
+    return ws
+
+
+def dprc_embed_norm(G, plan, n, scale=1.0, accumulate=False, ws=None, stream=None):
+    """n[i] (+)= scale^2 sum_v ||sum_{t: tok_it = v} G_it||^2, exactly."""
+    ws = _embed_ws(G, plan, ws)
+    _need_cuda(G, n, ws, plan.buf)
+    _same("n", n, torch.float32, (plan.B,), G.device)
+    _check("dprc_embed_norm",
+           lib().dprc_embed_norm(G.data_ptr(), _dtype_code(G), plan.B, plan.T, plan.V, G.shape[2],
+                                 scale, plan.buf.data_ptr(), plan.buf.numel(), n.data_ptr(),
+                                 int(bool(accumulate)), ws.data_ptr(), ws.numel(),
+                                 _stream(G, stream)))
+    return n
+
+
+def dprc_embed_grad(G, plan, dW, c=None, scale=1.0, accumulate=False, ws=None, stream=None):
+    """dW[v] (+)= scale sum_i c[i] sum_{t: tok_it = v} G_it (c None: all 1)."""
+    ws = _embed_ws(G, plan, ws)
+    _need_cuda(G, dW, c, ws, plan.buf)
+    _same("dW", dW, G.dtype, (plan.V, G.shape[2]), G.device)
+    _same("c", c, torch.float32, (plan.B,), G.device)
+    _check("dprc_embed_grad",
+           lib().dprc_embed_grad(G.data_ptr(), _dtype_code(G), _ptr(c), plan.B, plan.T, plan.V,
+                                 G.shape[2], scale, plan.buf.data_ptr(), plan.buf.numel(),
+                                 dW.data_ptr(), int(bool(accumulate)), ws.data_ptr(), ws.numel(),
+                                 _stream(G, stream)))
+    return dW
+
+
+def dprc_dropout(x, p, seed, step, residual=None, first_element=0, out=None, stream=None):
+    """residual + dropout(x) with the mask of (seed, step) from element
+    first_element on; the gradient is the same call on dy without residual."""
+    if out is None:
+        out = torch.empty_like(x)
+    _need_cuda(x, residual, out)
+    _same("residual", residual, x.dtype, x.shape, x.device)
+    _same("out", out, x.dtype, x.shape, x.device)
+    _check("dprc_dropout",
+           lib().dprc_dropout(x.data_ptr(), _ptr(residual), _dtype_code(x), x.numel(),
+                              int(first_element) & _U64, p, int(seed) & _U64, int(step) & _U64,
+                              out.data_ptr(), _stream(x, stream)))
+    return out
+
+
+def _linear_ws(like, M, K, N, grad, ws):
+    if ws is None:
+        n = lib().dprc_linear_workspace_bytes(_dtype_code(like), M, K, N, grad)
+        if n == 0:
+            raise DprcError("dprc_linear_workspace_bytes", 2)
+        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+    return ws
+
+
+def dprc_linear(X, W, bias=None, act="none", p=0.0, seed=0, step=0, residual=None, Z=None,
+                out=None, ws=None, stream=None):
+    """Y = residual + dropout(act(X W^T + bias)) for X [..., K], W [N][K]; Z
+    receives X W^T + bias (needed by the gradient of an activation)."""
+    N, K = W.shape
+    if X.shape[-1] != K:
+        raise ValueError(f"X has width {X.shape[-1]}, W {K}")
+    shape = (*X.shape[:-1], N)
+    M = X.numel() // K
+    if out is None:
+        out = torch.empty(shape, dtype=X.dtype, device=X.device)
+    ws = _linear_ws(X, M, K, N, 0, ws)
+    _need_cuda(X, W, bias, residual, Z, out, ws)
+    dt, dev = X.dtype, X.device
+    _same("W", W, dt, None, dev)
+    _same("bias", bias, dt, (N,), dev)
+    _same("residual", residual, dt, shape, dev)
+    _same("Z", Z, dt, shape, dev)
+    _same("out", out, dt, shape, dev)
+    _check("dprc_linear",
+           lib().dprc_linear(X.data_ptr(), W.data_ptr(), _ptr(bias), _ptr(residual),
+                             _dtype_code(X), M, K, N, DPRC_ACTS[act], p, int(seed) & _U64,
+                             int(step) & _U64, _ptr(Z), out.data_ptr(), ws.data_ptr(), ws.numel(),
+                             _stream(X, stream)))
+    return out
+
+
+def dprc_linear_grad(dY, X, W, Z=None, act="none", p=0.0, seed=0, step=0, dX=None, dW=None,
+                     db=None, dZ=None, ws=None, stream=None):
+    """Gradient of dprc_linear into those of dX [..., K], dW [N][K], db [N] and
+    dZ [..., N] that are given (act, p, seed, step as in its call)."""
+    N, K = W.shape
+    M = dY.numel() // N
+    lead = tuple(dY.shape[:-1])
+    ws = _linear_ws(dY, M, K, N, 1, ws)
+    _need_cuda(dY, X, W, Z, dX, dW, db, dZ, ws)
+    dt, dev = dY.dtype, dY.device
+    if dY.shape[-1] != N:
+        raise ValueError(f"dY has width {dY.shape[-1]}, W {N} rows")
+    _same("X", X, dt, (*lead, K), dev)
+    _same("W", W, dt, None, dev)
+    _same("Z", Z, dt, (*lead, N), dev)
+    _same("dX", dX, dt, (*lead, K), dev)
+    _same("dW", dW, dt, (N, K), dev)
+    _same("db", db, dt, (N,), dev)
+    _same("dZ", dZ, dt, (*lead, N), dev)
+    _check("dprc_linear_grad",
+           lib().dprc_linear_grad(dY.data_ptr(), _ptr(X), W.data_ptr(), _ptr(Z), _dtype_code(dY),
+                                  M, K, N, DPRC_ACTS[act], p, int(seed) & _U64, int(step) & _U64,
+                                  _ptr(dX), _ptr(dW), _ptr(db), _ptr(dZ), ws.data_ptr(),
+                                  ws.numel(), _stream(dY, stream)))

@@ -67,6 +67,8 @@ int64_t tpad_of(int64_t T) { return (T + 63) / 64 * 64; }
 
 }  // namespace
 
+bool device_supported() { return device_ok(); }
+
 int device_sm_count() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return kDefaultSms;
@@ -1198,7 +1200,9 @@ dprc_status dprc_device_error(int32_t* out, int reset) {
                                                      read_device_error_hutch,
                                                      read_device_error_exact,
                                                      read_device_error_qr,
-                                                     read_device_error_narrow};
+                                                     read_device_error_narrow,
+                                                     read_device_error_embed,
+                                                     read_device_error_linear};
   int32_t first = 0;
   for (auto rd : readers) {
     int32_t v = 0;

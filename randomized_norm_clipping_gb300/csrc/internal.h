@@ -348,4 +348,60 @@ cudaError_t launch_noise_at(void* grad, dprc_dtype dt, int64_t N, uint64_t first
 cudaError_t launch_philox_words(uint32_t* out, int64_t n_blocks, uint64_t first_block,
                                 uint64_t seed, uint64_t step, cudaStream_t s);
 
+// ---- the embedding (embed.cu) ----------------------------------------------
+// True if the current device is an sm_103 GPU.
+bool device_supported();
+cudaError_t read_device_error_embed(int32_t* out, bool reset);
+// The sorted token order: u32 keys [N] and int32 positions [N] at the front,
+// the sort's second buffers and counts behind them.
+size_t embed_plan_bytes(int64_t N, int64_t V);
+// Workspace of the norm (the gradient needs no more).
+size_t embed_norm_ws_bytes(dprc_dtype dt, int64_t N, int64_t d);
+cudaError_t launch_embed_lookup(const void* W, dprc_dtype dt, const void* tokens,
+                                int token_bytes, int64_t N, int64_t V, int64_t d, float scale,
+                                void* out, cudaStream_t s);
+cudaError_t launch_embed_plan(const void* tokens, int token_bytes, int64_t N, int64_t V,
+                              void* plan, cudaStream_t s);
+struct EmbedCall {
+  const void* G = nullptr;  // [B][T][d]
+  dprc_dtype dtype = DPRC_BF16;
+  int64_t B = 0, T = 0, V = 0, d = 0;
+  float scale = 1.f;
+  const void* plan = nullptr;
+  int accumulate = 0;
+};
+cudaError_t launch_embed_norm(const EmbedCall& c, float* n, void* ws, cudaStream_t s);
+cudaError_t launch_embed_grad(const EmbedCall& c, const float* clip, void* dW, void* ws,
+                              cudaStream_t s);
+
+// ---- dropout (dropout.cu) --------------------------------------------------
+cudaError_t launch_dropout(const void* x, const void* res, dprc_dtype dt, int64_t n,
+                           uint64_t first, double p, uint64_t seed, uint64_t step, void* y,
+                           cudaStream_t s);
+
+// ---- the linear map (linear.cu, linear_gemm.cu) ------------------------------
+cudaError_t read_device_error_linear(int32_t* out, bool reset);
+size_t linear_ws_bytes(dprc_dtype dt, int64_t M, int64_t K, int64_t N);
+size_t linear_grad_ws_bytes(dprc_dtype dt, int64_t M, int64_t K, int64_t N);
+struct LinearCall {
+  const void *X = nullptr, *W = nullptr, *bias = nullptr, *res = nullptr;
+  dprc_dtype dtype = DPRC_BF16;
+  int64_t M = 0, K = 0, N = 0;
+  int act = DPRC_ACT_NONE;
+  double p = 0.0;
+  uint64_t seed = 0, step = 0;
+  void *Z = nullptr, *Y = nullptr;
+};
+cudaError_t launch_linear(const LinearCall& c, void* ws, cudaStream_t s);
+struct LinearGradCall {
+  const void *dY = nullptr, *X = nullptr, *W = nullptr, *Z = nullptr;
+  dprc_dtype dtype = DPRC_BF16;
+  int64_t M = 0, K = 0, N = 0;
+  int act = DPRC_ACT_NONE;
+  double p = 0.0;
+  uint64_t seed = 0, step = 0;
+  void *dX = nullptr, *dW = nullptr, *db = nullptr, *dZ = nullptr;
+};
+cudaError_t launch_linear_grad(const LinearGradCall& c, void* ws, cudaStream_t s);
+
 }  // namespace dprc

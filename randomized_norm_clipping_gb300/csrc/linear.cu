@@ -1,0 +1,515 @@
+// The linear map with its epilogue, and its gradient: operand preparation, the
+// elementwise part of the gradient, the sums of partial products, and the
+// order of the launches.  The products themselves are in linear_gemm.cu.
+//
+//   Z = X W^T + b,  Y = res + drop(act(Z))
+//   dZ = drop(dY) act'(Z),  dX = dZ W,  dW = dZ^T X,  db = sum_m dZ
+//
+// Operands reach the tensor cores as they are stored when they are bf16 with
+// rows of a multiple of 16 bytes.  fp32 operands are split into three bf16
+// planes, and rows of another length are copied to a padded pitch, by one
+// streaming pass before the product.
+
+#include "linear.cuh"
+
+#include <algorithm>
+
+namespace dprc {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Operand preparation: src [rows][cols] into bf16 planes [P][rows][ld], P = 3
+// for fp32, 1 for bf16.  Up to two operands per launch (blockIdx.y).
+// ---------------------------------------------------------------------------
+struct PackJob {
+  const void* src = nullptr;
+  __nv_bfloat16* dst = nullptr;
+  long long rows = 0;
+  int cols = 0, ld = 0;
+  long long plane = 0;
+};
+struct PackArgs {
+  PackJob job[2];
+};
+
+__device__ __forceinline__ uint4 pack_bf16x8(const __nv_bfloat16* h) {
+  return *reinterpret_cast<const uint4*>(h);
+}
+
+// x = x0 + x1 + x2, each the bf16 rounding of what is left.  A value that
+// bf16 rounds to infinity, or that is no number, is its first plane alone.
+__device__ __forceinline__ void split3(float x, __nv_bfloat16* p) {
+  p[0] = __float2bfloat16_rn(x);
+  const float r0 = __bfloat162float(p[0]);
+  const float r = isfinite(r0) ? x - r0 : 0.f;
+  p[1] = __float2bfloat16_rn(r);
+  p[2] = __float2bfloat16_rn(r - __bfloat162float(p[1]));
+}
+
+template <typename T>
+__device__ __forceinline__ void store_planes(__nv_bfloat16* dst, long long plane, const float* v) {
+  if constexpr (sizeof(T) == 2) {
+    st8(dst, v);
+  } else {
+    __align__(16) __nv_bfloat16 h[3][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      __nv_bfloat16 t[3];
+      split3(v[e], t);
+      h[0][e] = t[0];
+      h[1][e] = t[1];
+      h[2][e] = t[2];
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      *reinterpret_cast<uint4*>(dst + p * plane) = pack_bf16x8(h[p]);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) linear_pack_kernel(const PackArgs a) {
+  const PackJob& j = a.job[blockIdx.y];
+  const int groups = j.ld / 8;
+  const long long total = j.rows * groups;
+  const bool vec = j.cols % 8 == 0;
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += stride) {
+    const long long row = i / groups;
+    const int c = static_cast<int>(i - row * groups) * 8;
+    float v[8];
+    ld_n<T>(static_cast<const T*>(j.src) + row * j.cols + c, min(8, j.cols - c), vec, v);
+    store_planes<T>(j.dst + row * j.ld + c, j.plane, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dZ = drop(dY) act'(Z), elementwise in fp32, rounded once to bf16 (or split
+// into planes) for the products; and its column sums, which take the unrounded
+// values.  A CTA takes kDzRows rows of 256 columns; its 8 warps take every 8th
+// row, and their column sums are added in warp order.  The rounding of dZ to
+// bf16 is the product's operand type: relative 2^-9 per element, as the
+// rounding of the results.
+// ---------------------------------------------------------------------------
+constexpr int kDzRows = 64;
+constexpr int kDzWarps = 8;
+constexpr int kDzAhead = 4;
+
+struct DzArgs {
+  const void* dY;
+  const void* Z;
+  long long M;
+  int N, vec, act;
+  DropArgs drop;
+  __nv_bfloat16* planes;  // or null
+  long long plane;
+  int ldp;
+  void* dZ;               // the caller's, or null
+  float* colsum;          // [row blocks][N], or null
+};
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kDzWarps) linear_dz_kernel(const DzArgs a) {
+  __shared__ float s_sum[kDzWarps][256];
+  constexpr bool kFast = sizeof(T) == 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ncb = (a.N + 255) / 256;
+  const int rb = static_cast<int>(blockIdx.x / ncb), cb = static_cast<int>(blockIdx.x % ncb);
+  const int n0 = cb * 256 + lane * 8;
+  const int cnt = min(8, a.N - n0);
+  const long long m0 = static_cast<long long>(rb) * kDzRows;
+  const RoundKeys rk = round_keys(a.drop.seed);
+  const bool vec = a.vec != 0;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (cnt > 0) {
+    for (int r0 = warp; r0 < kDzRows; r0 += kDzWarps * kDzAhead) {
+      float g[kDzAhead][8], z[kDzAhead][8];
+#pragma unroll
+      for (int u = 0; u < kDzAhead; ++u) {
+        const long long m = m0 + r0 + u * kDzWarps;
+        if (m >= a.M) continue;
+        ld_n<T>(static_cast<const T*>(a.dY) + m * a.N + n0, cnt, vec, g[u]);
+        if (a.act != DPRC_ACT_NONE)
+          ld_n<T>(static_cast<const T*>(a.Z) + m * a.N + n0, cnt, vec, z[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kDzAhead; ++u) {
+        const long long m = m0 + r0 + u * kDzWarps;
+        if (m >= a.M) continue;
+        if (a.drop.thr != 0)
+          drop8_at(g[u], static_cast<uint64_t>(m * a.N + n0), a.drop, rk);
+        if (a.act != DPRC_ACT_NONE) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[u][e] *= act_slope<kFast>(z[u][e], a.act);
+        }
+        if (a.colsum != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[e] += e < cnt ? g[u][e] : 0.f;
+        }
+        if (a.dZ != nullptr) st_n<T>(static_cast<T*>(a.dZ) + m * a.N + n0, cnt, vec, g[u]);
+        if (a.planes != nullptr && DPRC_IN(m < a.M && n0 + 8 <= a.ldp)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[u][e] = e < cnt ? g[u][e] : 0.f;
+          store_planes<T>(a.planes + m * a.ldp + n0, a.plane, g[u]);
+        }
+      }
+    }
+  }
+  if (a.colsum == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s_sum[warp][lane * 8 + e] = sum[e];
+  __syncthreads();
+  const int c = cb * 256 + threadIdx.x;
+  if (c < a.N) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDzWarps; ++w) t += s_sum[w][threadIdx.x];
+    a.colsum[static_cast<long long>(rb) * a.N + c] = t;
+  }
+}
+
+// db[n] = sum over the row blocks, 32 columns and 8 shares per CTA.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    linear_db_kernel(const float* __restrict__ colsum, int nblocks, int N, T* __restrict__ db) {
+  __shared__ float s_sum[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = static_cast<int>(blockIdx.x) * 32 + lane;
+  const int share = (nblocks + 7) / 8;
+  const int b0 = warp * share, b1 = min(b0 + share, nblocks);
+  float t = 0.f;
+  if (c < N) {
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) t += __ldcg(colsum + static_cast<long long>(b) * N + c);
+  }
+  s_sum[warp][lane] = t;
+  __syncthreads();
+  if (warp == 0 && c < N) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += s_sum[w][lane];
+    st1(db + c, s);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The shares of a product added in order, then the epilogue: 8 outputs a thread.
+// ---------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256)
+    linear_finish_kernel(const float* __restrict__ part, long long ldpart, long long stride,
+                         int split, const LinearEpi e) {
+  const int groups = (e.N + 7) / 8;
+  const long long total = e.M * groups;
+  const RoundKeys rk = round_keys(e.drop.seed);
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+       i += step) {
+    const long long m = i / groups;
+    const int n = static_cast<int>(i - m * groups) * 8;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const float* p = part + m * ldpart + n;
+#pragma unroll 4
+    for (int s = 0; s < split; ++s) {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(p + s * stride));
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(p + s * stride) + 1);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    linear_out<T, 1>(e, m, n, v, rk);
+  }
+}
+
+size_t up1k(size_t x) { return (x + 1023) / 1024 * 1024; }
+int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+
+unsigned stride_grid(int64_t threads) {
+  int64_t ctas = (threads + 255) / 256;
+  const int64_t cap = static_cast<int64_t>(device_sm_count()) * 32;
+  return static_cast<unsigned>(ctas < 1 ? 1 : ctas > cap ? cap : ctas);
+}
+
+cudaError_t launch_pack(dprc_dtype dt, const PackJob* jobs, int n, cudaStream_t s) {
+  PackArgs a;
+  int64_t most = 0;
+  for (int i = 0; i < n; ++i) {
+    a.job[i] = jobs[i];
+    most = std::max<int64_t>(most, jobs[i].rows * (jobs[i].ld / 8));
+  }
+  const dim3 grid(stride_grid(most), n);
+  if (dt == DPRC_F32)
+    linear_pack_kernel<float><<<grid, 256, 0, s>>>(a);
+  else
+    linear_pack_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// A product and, where it is in shares, their sum.
+cudaError_t run_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A,
+                     const GemmOperand& B, dprc_dtype dt, const LinearEpi& epi, void* part,
+                     cudaStream_t s) {
+  cudaError_t e = launch_gemm(g, p, A, B, dt, epi, part, s);
+  if (e != cudaSuccess || p.part_bytes == 0) return e;
+  const unsigned grid = stride_grid(epi.M * ((epi.N + 7) / 8));
+  const long long stride = (g.transposed ? g.cols : g.rows) * p.ldpart;
+  if (dt == DPRC_F32)
+    linear_finish_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float*>(part), p.ldpart,
+                                                     stride, p.split, epi);
+  else
+    linear_finish_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
+        static_cast<const float*>(part), p.ldpart, stride, p.split, epi);
+  return cudaGetLastError();
+}
+
+// At most this many tokens take the tile's columns and the weights its lanes
+// (linear_gemm.cu); with more, the tokens fill half a tile's lanes or more.
+constexpr int64_t kFewTokens = 64;
+
+// Sizes and workspace of a forward call.
+struct LinearPlan {
+  bool pack = false;
+  int planes = 1;
+  int64_t ld = 0;
+  GemmShape g;
+  GemmPlan p;
+  size_t x_off = 0, w_off = 0, part_off = 0, total = 0;
+};
+
+LinearPlan linear_plan(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
+  LinearPlan l;
+  l.planes = dt == DPRC_F32 ? 3 : 1;
+  l.pack = dt == DPRC_F32 || K % 8 != 0;
+  l.ld = l.pack ? up8(K) : K;
+  l.g.transposed = M <= kFewTokens;
+  l.g.rows = l.g.transposed ? N : M;
+  l.g.cols = l.g.transposed ? M : N;
+  l.g.K = K;
+  l.g.planes = l.planes;
+  l.p = plan_gemm(l.g);
+  size_t off = 0;
+  if (l.pack) {
+    l.x_off = off;
+    off = up1k(off + static_cast<size_t>(l.planes) * M * l.ld * 2);
+    l.w_off = off;
+    off = up1k(off + static_cast<size_t>(l.planes) * N * l.ld * 2);
+  }
+  l.part_off = off;
+  off = up1k(off + l.p.part_bytes);
+  l.total = off > 0 ? off : 1024;
+  return l;
+}
+
+// Sizes and workspace of a gradient call.
+struct LinearGradPlan {
+  bool pack = false;
+  int planes = 1;
+  int64_t ldk = 0, ldn = 0, nblocks = 0;
+  GemmShape gx, gw;
+  GemmPlan px, pw;
+  size_t dz_off = 0, x_off = 0, w_off = 0, sum_off = 0, part_off = 0, total = 0;
+};
+
+LinearGradPlan linear_grad_plan(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
+  LinearGradPlan l;
+  l.planes = dt == DPRC_F32 ? 3 : 1;
+  l.pack = dt == DPRC_F32 || K % 8 != 0;
+  l.ldk = l.pack ? up8(K) : K;
+  l.ldn = up8(N);
+  l.nblocks = (M + kDzRows - 1) / kDzRows;
+  l.gx.transposed = M <= kFewTokens;
+  l.gx.rows = l.gx.transposed ? K : M;
+  l.gx.cols = l.gx.transposed ? M : K;
+  l.gx.K = N;
+  l.gx.planes = l.planes;
+  l.px = plan_gemm(l.gx);
+  l.gw.rows = N;
+  l.gw.cols = K;
+  l.gw.K = M;
+  l.gw.planes = l.planes;
+  l.pw = plan_gemm(l.gw);
+  size_t off = 0;
+  l.dz_off = off;
+  off = up1k(off + static_cast<size_t>(l.planes) * M * l.ldn * 2);
+  if (l.pack) {
+    l.x_off = off;
+    off = up1k(off + static_cast<size_t>(l.planes) * M * l.ldk * 2);
+    l.w_off = off;
+    off = up1k(off + static_cast<size_t>(l.planes) * N * l.ldk * 2);
+  }
+  l.sum_off = off;
+  off = up1k(off + static_cast<size_t>(l.nblocks) * N * 4);
+  // the two products run one after the other on the stream and share this
+  l.part_off = off;
+  off = up1k(off + std::max(l.px.part_bytes, l.pw.part_bytes));
+  l.total = off > 0 ? off : 1024;
+  return l;
+}
+
+}  // namespace
+
+size_t linear_ws_bytes(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
+  return linear_plan(dt, M, K, N).total;
+}
+size_t linear_grad_ws_bytes(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
+  return linear_grad_plan(dt, M, K, N).total;
+}
+
+cudaError_t launch_linear(const LinearCall& c, void* ws, cudaStream_t s) {
+  if (c.M == 0) return cudaSuccess;
+  const LinearPlan l = linear_plan(c.dtype, c.M, c.K, c.N);
+  char* w = static_cast<char*>(ws);
+  GemmOperand x, wt;
+  x.data = c.X;
+  wt.data = c.W;
+  x.ld = wt.ld = l.ld;
+  x.plane = c.M * l.ld;
+  wt.plane = c.N * l.ld;
+  if (l.pack) {
+    PackJob jobs[2];
+    const void* src[2] = {c.X, c.W};
+    const int64_t rows[2] = {c.M, c.N};
+    const size_t off[2] = {l.x_off, l.w_off};
+    for (int i = 0; i < 2; ++i) {
+      jobs[i].src = src[i];
+      jobs[i].dst = reinterpret_cast<__nv_bfloat16*>(w + off[i]);
+      jobs[i].rows = rows[i];
+      jobs[i].cols = static_cast<int>(c.K);
+      jobs[i].ld = static_cast<int>(l.ld);
+      jobs[i].plane = rows[i] * l.ld;
+    }
+    const cudaError_t e = launch_pack(c.dtype, jobs, 2, s);
+    if (e != cudaSuccess) return e;
+    x.data = jobs[0].dst;
+    wt.data = jobs[1].dst;
+  }
+  LinearEpi epi;
+  epi.M = c.M;
+  epi.N = static_cast<int>(c.N);
+  epi.vec = c.N % 8 == 0;
+  epi.act = c.act;
+  epi.bias = c.bias;
+  epi.res = c.res;
+  epi.Z = c.Z;
+  epi.Y = c.Y;
+  epi.drop = drop_args(c.p, c.seed, c.step);
+  return run_gemm(l.g, l.p, l.g.transposed ? wt : x, l.g.transposed ? x : wt, c.dtype, epi,
+                  w + l.part_off, s);
+}
+
+cudaError_t launch_linear_grad(const LinearGradCall& c, void* ws, cudaStream_t s) {
+  const int elem = c.dtype == DPRC_F32 ? 4 : 2;
+  if (c.M == 0) {  // no tokens: nothing to add up
+    cudaError_t e = cudaSuccess;
+    if (c.dW != nullptr) e = cudaMemsetAsync(c.dW, 0, static_cast<size_t>(c.N) * c.K * elem, s);
+    if (e == cudaSuccess && c.db != nullptr)
+      e = cudaMemsetAsync(c.db, 0, static_cast<size_t>(c.N) * elem, s);
+    return e;
+  }
+  const LinearGradPlan l = linear_grad_plan(c.dtype, c.M, c.K, c.N);
+  char* w = static_cast<char*>(ws);
+  const DropArgs drop = drop_args(c.p, c.seed, c.step);
+  const bool products = c.dX != nullptr || c.dW != nullptr;
+  const bool direct = c.dtype == DPRC_BF16 && c.N % 8 == 0;  // TMA reads [M][N] as it is
+  const bool same = c.act == DPRC_ACT_NONE && drop.thr == 0;  // dZ = dY
+  cudaError_t e = cudaSuccess;
+
+  GemmOperand dz;
+  dz.ld = l.ldn;
+  dz.plane = c.M * l.ldn;
+  __nv_bfloat16* planes = nullptr;
+  if (same && direct) {
+    dz.data = c.dY;
+  } else if (direct && c.dZ != nullptr) {
+    dz.data = c.dZ;
+  } else if (products) {
+    planes = reinterpret_cast<__nv_bfloat16*>(w + l.dz_off);
+    dz.data = planes;
+  }
+  if (planes != nullptr || c.dZ != nullptr || c.db != nullptr) {
+    DzArgs a;
+    a.dY = c.dY;
+    a.Z = c.Z;
+    a.M = c.M;
+    a.N = static_cast<int>(c.N);
+    a.vec = c.N % 8 == 0;
+    a.act = c.act;
+    a.drop = drop;
+    a.planes = planes;
+    a.plane = dz.plane;
+    a.ldp = static_cast<int>(l.ldn);
+    a.dZ = c.dZ;
+    a.colsum = c.db != nullptr ? reinterpret_cast<float*>(w + l.sum_off) : nullptr;
+    const unsigned grid = static_cast<unsigned>((c.N + 255) / 256 * l.nblocks);
+    if (c.dtype == DPRC_F32)
+      linear_dz_kernel<float><<<grid, 32 * kDzWarps, 0, s>>>(a);
+    else
+      linear_dz_kernel<__nv_bfloat16><<<grid, 32 * kDzWarps, 0, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (c.db != nullptr) {
+    const unsigned grid = static_cast<unsigned>((c.N + 31) / 32);
+    const float* cs = reinterpret_cast<const float*>(w + l.sum_off);
+    const int nb = static_cast<int>(l.nblocks), N = static_cast<int>(c.N);
+    if (c.dtype == DPRC_F32)
+      linear_db_kernel<float><<<grid, 256, 0, s>>>(cs, nb, N, static_cast<float*>(c.db));
+    else
+      linear_db_kernel<__nv_bfloat16>
+          <<<grid, 256, 0, s>>>(cs, nb, N, static_cast<__nv_bfloat16*>(c.db));
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (!products) return cudaSuccess;
+
+  GemmOperand x, wt;
+  x.data = c.X;
+  wt.data = c.W;
+  x.ld = wt.ld = l.ldk;
+  x.plane = c.M * l.ldk;
+  wt.plane = c.N * l.ldk;
+  if (l.pack) {
+    PackJob jobs[2];
+    int n = 0;
+    if (c.dW != nullptr) {
+      jobs[n].src = c.X;
+      jobs[n].dst = reinterpret_cast<__nv_bfloat16*>(w + l.x_off);
+      jobs[n].rows = c.M;
+      x.data = jobs[n++].dst;
+    }
+    if (c.dX != nullptr) {
+      jobs[n].src = c.W;
+      jobs[n].dst = reinterpret_cast<__nv_bfloat16*>(w + l.w_off);
+      jobs[n].rows = c.N;
+      wt.data = jobs[n++].dst;
+    }
+    for (int i = 0; i < n; ++i) {
+      jobs[i].cols = static_cast<int>(c.K);
+      jobs[i].ld = static_cast<int>(l.ldk);
+      jobs[i].plane = jobs[i].rows * l.ldk;
+    }
+    e = launch_pack(c.dtype, jobs, n, s);
+    if (e != cudaSuccess) return e;
+  }
+  LinearEpi epi;
+  epi.N = static_cast<int>(c.K);
+  epi.vec = c.K % 8 == 0;
+  if (c.dX != nullptr) {
+    epi.M = c.M;
+    epi.Y = c.dX;
+    GemmOperand wm = wt, dk = dz;
+    wm.mn_major = true;
+    e = run_gemm(l.gx, l.px, l.gx.transposed ? wm : dk, l.gx.transposed ? dk : wm, c.dtype, epi,
+                 w + l.part_off, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (c.dW != nullptr) {
+    epi.M = c.N;
+    epi.Y = c.dW;
+    GemmOperand dm = dz, xm = x;
+    dm.mn_major = xm.mn_major = true;
+    e = run_gemm(l.gw, l.pw, dm, xm, c.dtype, epi, w + l.part_off, s);
+  }
+  return e;
+}
+
+}  // namespace dprc

@@ -1,0 +1,212 @@
+// The linear map's epilogue and the plan of its products, shared by the
+// kernels of linear.cu and linear_gemm.cu.
+#pragma once
+
+#include "common.cuh"
+#include "dropout.cuh"
+#include "internal.h"
+
+namespace dprc {
+
+// What happens to 8 neighbouring outputs of a product:
+//   z = v + bias;  Z = z (kept for the gradient);  y = res + drop(act(z)).
+struct LinearEpi {
+  long long M = 0;
+  int N = 0;
+  int vec = 0;               // N is a multiple of 8: 16-byte accesses
+  int act = DPRC_ACT_NONE;
+  const void* bias = nullptr;  // [N]
+  const void* res = nullptr;   // [M][N]
+  void* Z = nullptr;           // [M][N]
+  void* Y = nullptr;           // [M][N]
+  DropArgs drop;
+};
+
+// sigmoid; kFast: the hardware exponential and reciprocal (a few ulp of fp32,
+// far below the rounding of a bf16 result).
+template <bool kFast>
+__device__ __forceinline__ float sigmoid_f(float x) {
+  if (kFast) return __fdividef(1.f, 1.f + __expf(-x));
+  return 1.f / (1.f + expf(-x));
+}
+
+constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+// gelu(z) = z (1 + tanh u) / 2 = z sigmoid(2 u), u = sqrt(2/pi) (z + 0.044715 z^3)
+template <bool kFast>
+__device__ __forceinline__ float act_value(float z, int act) {
+  if (act == DPRC_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+  if (act == DPRC_ACT_GELU)
+    return z * sigmoid_f<kFast>(kGelu2C * fmaf(kGeluA * z * z, z, z));
+  if (act == DPRC_ACT_SILU) return z * sigmoid_f<kFast>(z);
+  return z;
+}
+
+template <bool kFast>
+__device__ __forceinline__ float act_slope(float z, int act) {
+  if (act == DPRC_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+  if (act == DPRC_ACT_GELU) {
+    const float s = sigmoid_f<kFast>(kGelu2C * fmaf(kGeluA * z * z, z, z));
+    return fmaf(z * s * (1.f - s), kGelu2C * fmaf(3.f * kGeluA * z, z, 1.f), s);
+  }
+  if (act == DPRC_ACT_SILU) {
+    const float s = sigmoid_f<kFast>(z);
+    return fmaf(z * s, 1.f - s, s);
+  }
+  return 1.f;
+}
+
+__device__ __forceinline__ void ld8(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  const float4 b = *(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void ld8(const __nv_bfloat16* p, float* v) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(u[e] << 16);
+    v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void st8(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void st8(__nv_bfloat16* p, const float* v) {
+  uint32_t u[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+    u[e] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void st1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void st1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// cnt (1..8) values at p, by 16-byte accesses where vec.
+template <typename T>
+__device__ __forceinline__ void ld_n(const T* p, int cnt, bool vec, float* v) {
+  if (vec) {
+    ld8(p, v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < cnt ? to_f32<T>(p[e]) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void st_n(T* p, int cnt, bool vec, const float* v) {
+  if (vec) {
+    st8(p, v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < cnt) st1(p + e, v[e]);
+}
+
+// Drops elements e0 .. e0 + 7 of a tensor (dropout.cuh); e0 of any residue.
+__device__ __forceinline__ void drop8_at(float* v, uint64_t e0, const DropArgs& d,
+                                         const RoundKeys& rk) {
+  const uint4 w0 = philox_block(e0 >> 3, d.step, rk);
+  if ((e0 & 7) == 0) {
+    drop8(v, w0, d.thr, d.keep);
+    return;
+  }
+  const uint4 w1 = philox_block((e0 >> 3) + 1, d.step, rk);
+  uint32_t keep = 0;
+#pragma unroll
+  for (int h = 0; h < 8; ++h) {
+    keep |= (drop_keep(w0, h, d.thr) ? 1u : 0u) << h;
+    keep |= (drop_keep(w1, h, d.thr) ? 1u : 0u) << (h + 8);
+  }
+  keep >>= static_cast<int>(e0 & 7);
+#pragma unroll
+  for (int h = 0; h < 8; ++h) v[h] = ((keep >> h) & 1u) ? v[h] * d.keep : 0.f;
+}
+
+// Outputs (m, n0 .. n0 + 8 kG) from the fp32 sums v: the loads of all groups
+// first, so that a row's residual is on its way while the rest is computed.
+template <typename T, int kG>
+__device__ __forceinline__ void linear_out(const LinearEpi& e, long long m, int n0, float* v,
+                                           const RoundKeys& rk) {
+  constexpr bool kFast = sizeof(T) == 2;
+  const long long base = m * e.N;
+  const bool vec = e.vec != 0;
+  float r[kG][8];
+  if (e.res != nullptr) {
+    const T* res = static_cast<const T*>(e.res) + base;
+#pragma unroll
+    for (int g = 0; g < kG; ++g)
+      if (n0 + 8 * g < e.N) ld_n<T>(res + n0 + 8 * g, min(8, e.N - n0 - 8 * g), vec, r[g]);
+  }
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    const int n = n0 + 8 * g;
+    const int cnt = min(8, e.N - n);
+    if (cnt <= 0 || !DPRC_IN(m < e.M)) continue;
+    float* x = v + 8 * g;
+    if (e.bias != nullptr) {
+      float b[8];
+      ld_n<T>(static_cast<const T*>(e.bias) + n, cnt, vec, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] += b[j];
+    }
+    if (e.Z != nullptr) st_n<T>(static_cast<T*>(e.Z) + base + n, cnt, vec, x);
+    if (e.act != DPRC_ACT_NONE) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = act_value<kFast>(x[j], e.act);
+    }
+    if (e.drop.thr != 0) drop8_at(x, static_cast<uint64_t>(base + n), e.drop, rk);
+    if (e.res != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] += r[g][j];
+    }
+    st_n<T>(static_cast<T*>(e.Y) + base + n, cnt, vec, x);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One product D [rows][cols] = sum over the contraction of A(row, .) B(col, .).
+// An operand is bf16 planes [planes][dim][ld]: one plane for bf16 data; fp32
+// data is three planes whose sum is the value to 24 bits (x = x0 + x1 + x2,
+// each the rounding of what is left), and a product of two such values is the
+// six plane products whose size is above 2^-24 of it.
+// K-major: the contraction runs along a stored row; otherwise (MN-major) the
+// rows or columns of D do.
+// ---------------------------------------------------------------------------
+struct GemmOperand {
+  const void* data = nullptr;
+  bool mn_major = false;
+  int64_t ld = 0;           // elements between stored rows
+  int64_t plane = 0;        // elements between planes
+};
+
+struct GemmShape {
+  int64_t rows = 0, cols = 0, K = 0;
+  int planes = 1;           // 1 (bf16) or 3 (fp32)
+  bool transposed = false;  // D is stored [cols][rows] (the tokens are cols)
+};
+
+// How a product is cut: tiles of 128 x tn, the contraction in `split` shares
+// whose fp32 partial sums a second kernel adds.
+struct GemmPlan {
+  int tn = 256;
+  int split = 1;
+  int64_t units = 0;        // contraction units of 64 (times plane products)
+  int64_t ldpart = 0;       // row stride of a partial result
+  size_t part_bytes = 0;
+};
+
+GemmPlan plan_gemm(const GemmShape& g);
+// D into epi (split == 1) or the partial sums into `part`, then epi by
+// launch_linear_finish.  T of the epilogue's tensors: dt.
+cudaError_t launch_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A,
+                        const GemmOperand& B, dprc_dtype dt, const LinearEpi& epi, void* part,
+                        cudaStream_t s);
+
+}  // namespace dprc
