@@ -15,6 +15,8 @@
 // What bounds them: bytes.  The lookup writes N d values, the norm reads them
 // once, the gradient reads them once and writes all V rows.
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -80,6 +82,40 @@ __device__ __forceinline__ typename Raw<AW>::type pack(const float* v) {
   return raw;
 }
 
+// Two fp32 operations in one instruction (sm_100 and later).
+__device__ __forceinline__ unsigned long long pair(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b,
+                                                   unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float pair_sum(unsigned long long a) {
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a));
+  return lo + hi;
+}
+
+// Sum of squares of n values (n a power of two), in up to four chains.
+template <int n>
+__device__ __forceinline__ float square_sum(const float* v) {
+  if constexpr (n == 1) {
+    return v[0] * v[0];
+  } else {
+    unsigned long long s[2] = {0ull, 0ull};
+#pragma unroll
+    for (int e = 0; e < n; e += 2) {
+      const unsigned long long x = pair(v[e], v[e + 1]);
+      s[(e >> 1) & 1] = fma2(x, x, s[(e >> 1) & 1]);
+    }
+    return pair_sum(s[0]) + pair_sum(s[1]);
+  }
+}
+
 // A token as a sort key: ids outside [0, V) become V, the last key.  A
 // negative id means "no token"; one of V or more is a mistake of the caller
 // and is recorded in the device error word.
@@ -140,381 +176,552 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// Stable radix sort of (token, position), one launch of one cluster.
-//
-// Keys have `bits` bits (tokens and the key V of "no token"), taken in
-// `passes` digits of `dbits` <= 10 bits, least significant first.  Every warp
-// of the cluster owns a contiguous range of the input; per pass it counts its
-// digits in shared memory, the counts become start offsets (over digits, then
-// CTAs, then warps: the order of a stable sort), and it writes its range out
-// 32 entries at a time, each rank being the number of equal digits in lower
-// lanes.  The passes are separated by the cluster's hardware barrier, so
-// nothing spins, and the data goes through L2, so any N fits.
-//
-// One cluster of 8 CTAs and not the whole GPU: a grid-wide barrier needs a
-// cooperative launch and spinning, and the sort moves 16 bytes per token and
-// pass against the 2 d or 4 d bytes per token of the pass over G.
+// The order, up to kRankMax tokens: an entry's place is the number of entries
+// that come before it, keys_j < key_i or equal with j < i, counted by
+// comparison.  Every CTA holds all keys in shared memory, a warp counts for
+// four entries, its lanes over the keys.  N^2 comparisons over the whole GPU
+// take less than the barriers of a radix sort: RANKUS.
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortMaxDigit = 1024;
-constexpr int kSortBatch = 8;  // entries a lane loads ahead
+constexpr int kRankMax = 8192;
+constexpr int kRankWarps = 8;
+constexpr int kRankPer = 4;  // entries of a warp
+
+template <typename TOK>
+__global__ void __launch_bounds__(32 * kRankWarps)
+    token_rank_kernel(const TOK* __restrict__ tokens, int N, int V, uint32_t* __restrict__ key_out,
+                      int* __restrict__ pos_out) {
+  extern __shared__ __align__(16) uint32_t s_key[];  // [N rounded up to 128]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int padded = (N + 127) / 128 * 128;
+  pdl_launch_dependents();
+  for (int j = threadIdx.x; j < padded; j += 32 * kRankWarps)
+    s_key[j] = j < N ? token_key(tokens[j], V) : 0xFFFFFFFFu;  // before no entry
+  __syncthreads();
+  const int i0 = (static_cast<int>(blockIdx.x) * kRankWarps + warp) * kRankPer;
+  if (i0 >= N) return;
+  uint32_t k[kRankPer];
+  int count[kRankPer];
+#pragma unroll
+  for (int e = 0; e < kRankPer; ++e) {
+    k[e] = s_key[min(i0 + e, N - 1)];
+    count[e] = 0;
+  }
+  // blocks of 128 keys: all before the warp's entries, the one that holds
+  // them (kRankPer divides 128), all after
+  const int own = i0 / 128, nb = padded / 128;
+  const uint4* keys = reinterpret_cast<const uint4*>(s_key) + lane;
+  auto add = [&](int block, uint32_t equal) {
+    const uint4 x = keys[block * 32];
+#pragma unroll
+    for (int e = 0; e < kRankPer; ++e) {
+      const uint32_t bound = k[e] + equal;
+      count[e] += (x.x < bound) + (x.y < bound) + (x.z < bound) + (x.w < bound);
+    }
+  };
+#pragma unroll 4
+  for (int b = 0; b < own; ++b) add(b, 1u);
+  {
+    const uint4 x = keys[own * 32];
+    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int j = own * 128 + lane * 4 + c;
+#pragma unroll
+      for (int e = 0; e < kRankPer; ++e) count[e] += v[c] < k[e] + (j < i0 + e ? 1u : 0u);
+    }
+  }
+#pragma unroll 4
+  for (int b = own + 1; b < nb; ++b) add(b, 0u);
+#pragma unroll
+  for (int e = 0; e < kRankPer; ++e) {
+    const int at = __reduce_add_sync(0xffffffffu, count[e]);
+    if (lane == e && i0 + e < N && DPRC_IN(at >= 0 && at < N)) {
+      key_out[at] = k[e];
+      pos_out[at] = i0 + e;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The order of more tokens: a stable radix sort, least significant digit
+// first, two launches a digit.
+//
+// A CTA owns a contiguous tile.  token_count_kernel counts its digits;
+// token_scatter_kernel adds up the counts (over digits, then tiles, then the
+// tile's warps: the order of a stable sort) and moves the entries: an entry's
+// rank among its warp's equal digits is the count so far plus the equal digits
+// in lower lanes.  Keys have as many bits as V (the key of "no token") needs,
+// in digits of at most 10 bits.
+//
+// Launches and not barriers inside one launch: one cluster of 8 CTAs, with the
+// hardware's cluster barrier between the steps, took 44 us for 65536 tokens
+// (its 8 SMs' scattered stores alone 18 us), these launches SORTUS us.
+// ---------------------------------------------------------------------------
+constexpr int kSortWarps = 8;
+constexpr int kSortThreads = 32 * kSortWarps;
+constexpr int kSortBatch = 4;   // entries of a lane that are loaded together
+constexpr int kSortMaxBits = 10;
+constexpr int kSortTile = kSortThreads * kSortBatch;
+constexpr int kSortMaxTiles = 128;
 
 struct SortArgs {
-  long long N;
-  int V, passes, dbits;
-  uint32_t* key[2];  // [0] holds the result
-  int* pos[2];
-  int* ghist;        // [CTAs][digits], per-CTA digit counts of the current pass
+  int N, per;        // entries; of one warp
+  int V, shift, bits;
+  const uint32_t* key_in;  // null in the first pass: the tokens themselves
+  const int* pos_in;
+  uint32_t* key_out;
+  int* pos_out;
+  int* counts;       // [tiles][digits]
 };
 
 template <typename TOK>
-__global__ void __launch_bounds__(kSortThreads, 1)
-    token_sort_kernel(const TOK* __restrict__ tokens, const SortArgs a) {
-  extern __shared__ int s_hist[];  // [kSortWarps][digits]
+__device__ __forceinline__ uint32_t sort_key(const TOK* tokens, const SortArgs& a, int i) {
+  return a.key_in == nullptr ? token_key(tokens[i], a.V) : __ldg(a.key_in + i);
+}
+
+// The lanes with this lane's digit, one vote per bit (the match instruction
+// took 2 us a step here: it loops over the distinct values).  Bits above the
+// digit are zero in every lane and change nothing.
+__device__ __forceinline__ uint32_t equal_lanes(uint32_t digit, bool live) {
+  uint32_t same = __ballot_sync(0xffffffffu, live);
+#pragma unroll
+  for (int bit = 0; bit < kSortMaxBits; ++bit) {
+    const uint32_t v = __ballot_sync(0xffffffffu, (digit >> bit) & 1u);
+    same &= ~(v ^ (0u - ((digit >> bit) & 1u)));
+  }
+  return same;
+}
+
+template <typename TOK>
+__global__ void __launch_bounds__(kSortThreads)
+    token_count_kernel(const TOK* __restrict__ tokens, const SortArgs a) {
+  __shared__ int s_hist[1 << kSortMaxBits];
+  pdl_launch_dependents();
+  const int nd = 1 << a.bits;
+  for (int d = threadIdx.x; d < nd; d += kSortThreads) s_hist[d] = 0;
+  __syncthreads();
+  pdl_wait();
+  const int lo = static_cast<int>(blockIdx.x) * kSortWarps * a.per;
+  const int hi = min(lo + kSortWarps * a.per, a.N);
+  for (int i0 = lo; i0 < hi; i0 += kSortTile) {
+    uint32_t k[kSortBatch];
+#pragma unroll
+    for (int j = 0; j < kSortBatch; ++j) {
+      const int i = i0 + j * kSortThreads + threadIdx.x;
+      k[j] = i < hi ? sort_key(tokens, a, i) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < kSortBatch; ++j) {
+      const int i = i0 + j * kSortThreads + threadIdx.x;
+      if (i < hi) atomicAdd(&s_hist[(k[j] >> a.shift) & (nd - 1)], 1);  // whole numbers: any order
+    }
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < nd; d += kSortThreads)
+    a.counts[static_cast<long long>(blockIdx.x) * nd + d] = s_hist[d];
+}
+
+template <typename TOK>
+__global__ void __launch_bounds__(kSortThreads)
+    token_scatter_kernel(const TOK* __restrict__ tokens, const SortArgs a) {
+  extern __shared__ int s_dyn[];
   __shared__ int s_scan[kSortWarps];
-  const int nd = 1 << a.dbits;
+  pdl_launch_dependents();
+  const int nd = 1 << a.bits;
+  int* const s_hist = s_dyn;                     // [warps][digits]
+  int* const s_all = s_hist + kSortWarps * nd;   // [digits], all tiles
+  int* const s_base = s_all + nd;                // [digits], lower tiles; then the start
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cta = blockIdx.x, ctas = gridDim.x;
-  const long long per =
-      ((a.N + static_cast<long long>(ctas) * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
-  const long long lo = (static_cast<long long>(cta) * kSortWarps + warp) * per;
-  const long long hi = lo + per < a.N ? lo + per : a.N;
-  int* hist = s_hist + warp * nd;
   const uint32_t lt = (1u << lane) - 1u;
+  const int lo = min((static_cast<int>(blockIdx.x) * kSortWarps + warp) * a.per, a.N);
+  const int hi = min(lo + a.per, a.N);
+  int* const hist = s_hist + warp * nd;
+  for (int i = threadIdx.x; i < kSortWarps * nd; i += kSortThreads) s_hist[i] = 0;
+  __syncthreads();
+  pdl_wait();
 
-  for (int p = 0; p < a.passes; ++p) {
-    const int shift = p * a.dbits;
-    // the last pass writes buffer 0; before it they alternate
-    const int dst = (a.passes - 1 - p) & 1, src = dst ^ 1;
-    for (int i = threadIdx.x; i < kSortWarps * nd; i += kSortThreads) s_hist[i] = 0;
-    __syncthreads();
-
-    for (long long b0 = lo; b0 < hi; b0 += 32 * kSortBatch) {
-      uint32_t key[kSortBatch];
+  // this warp's digits
+  for (int i0 = lo; i0 < hi; i0 += 32 * kSortBatch) {
+    uint32_t k[kSortBatch];
 #pragma unroll
-      for (int j = 0; j < kSortBatch; ++j) {
-        const long long i = b0 + j * 32 + lane;
-        if (i < hi) key[j] = p == 0 ? token_key(tokens[i], a.V) : __ldcg(a.key[src] + i);
-      }
+    for (int j = 0; j < kSortBatch; ++j) {
+      const int i = i0 + j * 32 + lane;
+      k[j] = i < hi ? sort_key(tokens, a, i) : 0u;
+    }
 #pragma unroll
-      for (int j = 0; j < kSortBatch; ++j) {
-        const bool live = b0 + j * 32 + lane < hi;
-        const uint32_t dg = live ? (key[j] >> shift) & (nd - 1) : 0xFFFFFFFFu;
-        const uint32_t same = __match_any_sync(0xffffffffu, dg);
-        if (live && (same & lt) == 0) hist[dg] += __popc(same);
-        __syncwarp();
-      }
-    }
-    __syncthreads();
-
-    // per digit: this CTA's count, and each warp's offset within the CTA
-    const int dg = threadIdx.x;  // digits <= threads
-    if (dg < nd) {
-      int run = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int c = s_hist[w * nd + dg];
-        s_hist[w * nd + dg] = run;
-        run += c;
-      }
-      __stcg(a.ghist + cta * nd + dg, run);
-    }
-    cluster_sync_all();
-    // start of each digit over the cluster, then of this CTA's share of it
+    for (int j = 0; j < kSortBatch; ++j)
+      if (i0 + j * 32 + lane < hi) atomicAdd(&hist[(k[j] >> a.shift) & (nd - 1)], 1);
+  }
+  // all tiles' counts of each digit, and the lower tiles' share
+  for (int d = threadIdx.x; d < nd; d += kSortThreads) {
     int total = 0, before = 0;
-    if (dg < nd) {
-      for (int c = 0; c < ctas; ++c) {
-        const int v = __ldcg(a.ghist + c * nd + dg);
-        if (c < cta) before += v;
-        total += v;
-      }
+#pragma unroll 8
+    for (int t = 0; t < static_cast<int>(gridDim.x); ++t) {
+      const int v = __ldg(a.counts + t * nd + d);
+      total += v;
+      before += t < static_cast<int>(blockIdx.x) ? v : 0;
     }
-    int incl = total;
+    s_all[d] = total;
+    s_base[d] = before;
+  }
+  __syncthreads();
+  // scan over the digits, dpt neighbours a thread
+  const int dpt = (nd + kSortThreads - 1) / kSortThreads;
+  const int d0 = threadIdx.x * dpt;
+  int total = 0;
+  for (int j = 0; j < dpt; ++j) total += d0 + j < nd ? s_all[d0 + j] : 0;
+  int incl = total;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += v;
-    }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    if (warp == 0) {
-      int v = s_scan[lane];
-      int sum = v;
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int base = incl - total + __reduce_add_sync(0xffffffffu, lane < warp ? s_scan[lane] : 0);
+  for (int j = 0; j < dpt && d0 + j < nd; ++j) {
+    int run = s_base[d0 + j] + base;
+    base += s_all[d0 + j];
+    // hist[w][d] becomes where warp w's entries of digit d start
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += o;
-      }
-      s_scan[lane] = sum - v;
+    for (int w = 0; w < kSortWarps; ++w) {
+      const int c = s_hist[w * nd + d0 + j];
+      s_hist[w * nd + d0 + j] = run;
+      run += c;
     }
-    __syncthreads();
-    if (dg < nd) {
-      const int base = s_scan[warp] + incl - total + before;
-      for (int w = 0; w < kSortWarps; ++w) s_hist[w * nd + dg] += base;
-    }
-    __syncthreads();
+  }
+  __syncthreads();
 
-    for (long long b0 = lo; b0 < hi; b0 += 32 * kSortBatch) {
-      uint32_t key[kSortBatch];
-      int pos[kSortBatch];
+  for (int i0 = lo; i0 < hi; i0 += 32 * kSortBatch) {
+    uint32_t k[kSortBatch];
+    int p[kSortBatch];
 #pragma unroll
-      for (int j = 0; j < kSortBatch; ++j) {
-        const long long i = b0 + j * 32 + lane;
-        if (i < hi) {
-          key[j] = p == 0 ? token_key(tokens[i], a.V) : __ldcg(a.key[src] + i);
-          pos[j] = p == 0 ? static_cast<int>(i) : __ldcg(a.pos[src] + i);
-        }
-      }
+    for (int j = 0; j < kSortBatch; ++j) {
+      const int i = i0 + j * 32 + lane;
+      k[j] = i < hi ? sort_key(tokens, a, i) : 0u;
+      p[j] = i < hi && a.pos_in != nullptr ? __ldg(a.pos_in + i) : i;
+    }
 #pragma unroll
-      for (int j = 0; j < kSortBatch; ++j) {
-        const bool live = b0 + j * 32 + lane < hi;
-        const uint32_t dgt = live ? (key[j] >> shift) & (nd - 1) : 0xFFFFFFFFu;
-        const uint32_t same = __match_any_sync(0xffffffffu, dgt);
-        int at = 0;
-        if (live) at = hist[dgt] + __popc(same & lt);
-        __syncwarp();
-        if (live && (same & lt) == 0) hist[dgt] += __popc(same);
-        __syncwarp();
-        if (live && DPRC_IN(at >= 0 && at < a.N)) {
-          __stcg(a.key[dst] + at, key[j]);
-          __stcg(a.pos[dst] + at, pos[j]);
-        }
+    for (int j = 0; j < kSortBatch; ++j) {
+      if (i0 + j * 32 >= hi) break;  // uniform over the warp
+      const bool live = i0 + j * 32 + lane < hi;
+      const uint32_t digit = live ? (k[j] >> a.shift) & (nd - 1) : 0u;
+      const uint32_t same = equal_lanes(digit, live);
+      const int at = live ? hist[digit] + __popc(same & lt) : 0;
+      __syncwarp();
+      if (live && (same & lt) == 0) hist[digit] += __popc(same);
+      __syncwarp();
+      if (live && DPRC_IN(at >= 0 && at < a.N)) {
+        a.key_out[at] = k[j];
+        a.pos_out[at] = p[j];
       }
     }
-    cluster_sync_all();
   }
 }
 
 // ---------------------------------------------------------------------------
 // The pass over G in sorted order.
 //
-// A warp takes `R` <= 32 consecutive entries [a, a + R) of the order and one
-// slice of the columns, and adds up rows in fp32 registers, run by run.  A run
-// of up to kShortRun entries belongs whole to the warp whose range holds its
-// first entry (which then reads past its range), so most results need no
-// second step.  A longer run is cut at the ranges' ends: each piece leaves its
-// partial sum in the workspace and embed_long_kernel adds a run's pieces in
-// order.  A range holds at most two such pieces: one that covers its first
-// entry (slot 0) and one that begins later and reaches past its end (slot 1).
+// A CTA takes kRange = 16 consecutive entries of the order (a range) and up to
+// 256 accesses of their rows' columns, one per thread, and adds up rows in fp32
+// registers, run by run.  A run of up to 16 entries belongs whole to the CTA
+// whose range holds its first entry (which then reads past its range), so most
+// results need no second step.  A longer run is cut at the ranges' ends: each
+// piece leaves its partial sum in the workspace and embed_long_kernel adds a
+// run's pieces in order.  A range holds at most two such pieces: one that
+// covers its first entry (slot 0) and one that begins later and reaches past
+// its end (slot 1).
 //
 // The entries' runs come from comparing neighbours in a window of 32 entries
-// before the range, the range, and up to 64 after its first entry; bit masks
-// of run starts then answer every question about a run's extent.
+// before the range and 64 after its first entry; bit masks of run starts then
+// answer every question about a run's extent.
 //
-// Rows are prefetched kRowsAhead at a time across run boundaries: most runs
-// are one row long, and bytes in flight are what the pass lives on.
+// Rows are read kBatch at a time into registers, all of a batch before one is
+// used: with 256 threads of 16 bytes that is 32 KB in flight per CTA and four
+// CTAs per SM.  (All 31 rows of a CTA in one unrolled loop took 27 us where
+// this takes NORMSEG us on 4 x 4096 tokens of 2048 bf16: its code did not fit
+// the instruction cache.)  One warp works out the runs for the CTA.
 // ---------------------------------------------------------------------------
-constexpr int kShortRun = 32;
-constexpr int kRowsAhead = 4;
-constexpr int kSegWarps = 4;  // warps per CTA of the segment pass
+constexpr int kRange = 16;
+constexpr int kMaxRows = 2 * kRange;   // rows of a CTA, at most 31
+constexpr int kSegThreads = 256;
+constexpr int kBatch = 8;
 
 struct SegArgs {
   const uint32_t* key;
   const int* pos;
-  long long N;        // entries
-  long long T;        // tokens per sample
+  int N;              // entries
+  int T;              // tokens per sample
+  unsigned long long t_inv;  // for pos / T
   int V;
   long long d;
-  int R;              // entries per range
-  int nslices;
-  long long nranges;
+  int nblk;           // column blocks
+  int nranges;
   float scale;
-  // norm: squared sums by original position [nslices][N]; grad: the weights
+  // norm: squared sums by original position [N][nblk]; grad: the weights
   float* sq;
   float* long_sq;     // norm: [nranges][column blocks] squares of the long runs
   const float* c;     // per-sample factors or null
   int accumulate;
   float* part;        // [nranges][2][dpad] partial sums of long runs
   long long dpad;
-  int* long_at;       // [nranges]: 0, or 1 + slot of the long run that begins here
+  int* long_at;       // [nranges]: 0, or 1 + slot of the long run that begins here, + 4 if
+                      // a long run reaches from here into the next range
   // grad: rows no token names
   long long zero_units;
 };
 
-// kNorm: runs are equal (token, sample) pairs; otherwise equal tokens.
-template <bool kNorm>
-__device__ __forceinline__ bool run_starts(const SegArgs& a, long long i, uint32_t k, int p) {
-  if (i == 0) return true;
-  const uint32_t kp = __ldg(a.key + i - 1);
-  if (kp != k) return true;
-  if (kNorm) return __ldg(a.pos + i - 1) / static_cast<int>(a.T) != p / static_cast<int>(a.T);
-  return false;
+// Sample of a position: pos / T by a multiplication (Lemire, Kaser and Kurz,
+// "Faster remainder by direct computation", 2019: exact for 32-bit operands
+// with t_inv = ceil(2^64 / T); T = 1 has t_inv = 0).
+__device__ __forceinline__ int sample_of(const SegArgs& a, int pos) {
+  return a.t_inv == 0 ? pos
+                      : static_cast<int>(__umul64hi(a.t_inv, static_cast<unsigned long long>(pos)));
 }
 
-template <typename T, int AW, int NV, bool kNorm>
-__device__ __forceinline__ void segment_range(const SegArgs& a, const T* __restrict__ G,
-                                              T* __restrict__ dW, long long range, int slice) {
-  using RawT = typename Raw<AW>::type;
-  constexpr int VE = AW / static_cast<int>(sizeof(T));
-  constexpr int NA = NV * VE;
-  const int lane = threadIdx.x & 31;
-  const long long a0 = range * a.R;
-  const int R = static_cast<int>(a.N - a0 < a.R ? a.N - a0 : a.R);
+// Rows of a range: lane l holds row l (l < rows).
+struct RangeRows {
+  uint32_t key;    // its token
+  int pos;         // its position
+  int rows;
+  uint32_t E;      // bit r: row r ends a run or a piece of one
+  uint32_t L;      // bit r: row r belongs to a long run
+  int slot;        // slot of the piece that starts at row 0 (the others are slot 1)
+  uint32_t none;   // bit j: entry j of the range holds no token
+};
 
-  // run starts: S0 bit j = entry a0 - 32 + j, M bit j = entry a0 + j; entries
-  // past the last token count as starts (they end the run before them)
-  uint32_t S0 = 0;
-  unsigned long long M = 0;
-  uint32_t key1 = 0, key2 = 0;
-  int pos1 = 0, pos2 = 0;
-  unsigned long long none = 0;  // entries that hold no token
+template <bool kNorm>
+__device__ __forceinline__ RangeRows range_rows(const SegArgs& a, int range, bool tell) {
+  using u64 = unsigned long long;
+  const int lane = threadIdx.x & 31;
+  const int a0 = range * kRange;
+  const int R = min(a.N - a0, kRange);
+  const uint32_t V = static_cast<uint32_t>(a.V);
+  // Run starts: S0 bit j = entry a0 - 32 + j, M bit j = entry a0 + j; entries
+  // past the last token count as starts (they end the run before them).
+  // (kNorm) runs are equal (token, sample) pairs, otherwise equal tokens.  The
+  // window's first entry counts as no start: a run from there on is long.
+  uint32_t kw[3], st[3], nt[3];
+  int pw[3];
 #pragma unroll
   for (int w = 0; w < 3; ++w) {
-    const long long i = a0 - 32 + w * 32 + lane;
+    const int i = a0 - 32 + w * 32 + lane;
     const bool in = i >= 0 && i < a.N;
-    const uint32_t k = in ? __ldg(a.key + i) : static_cast<uint32_t>(a.V);
-    const int p = in ? __ldg(a.pos + i) : 0;
-    const bool tok = in && k < static_cast<uint32_t>(a.V);
-    const bool st = i >= 0 && (!tok || run_starts<kNorm>(a, i, k, p));
-    const uint32_t b = __ballot_sync(0xffffffffu, st);
-    const uint32_t nt = __ballot_sync(0xffffffffu, !tok);
-    if (w == 0) S0 = b;
-    if (w == 1) { M = b; none = nt; key1 = k; pos1 = p; }
-    if (w == 2) {
-      M |= static_cast<unsigned long long>(b) << 32;
-      none |= static_cast<unsigned long long>(nt) << 32;
-      key2 = k;
-      pos2 = p;
-    }
+    kw[w] = in ? __ldg(a.key + i) : V;
+    pw[w] = in ? __ldg(a.pos + i) : 0;
   }
+  uint32_t klast = kw[0];
+  int slast = 0;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) {
+    const int i = a0 - 32 + w * 32 + lane;
+    const int smp = kNorm ? sample_of(a, pw[w]) : 0;
+    uint32_t kp = __shfl_up_sync(0xffffffffu, kw[w], 1);
+    int sp = kNorm ? __shfl_up_sync(0xffffffffu, smp, 1) : 0;
+    if (lane == 0) {
+      kp = w == 0 ? kw[0] : klast;
+      sp = w == 0 ? smp : slast;
+    }
+    klast = __shfl_sync(0xffffffffu, kw[w], 31);
+    if (kNorm) slast = __shfl_sync(0xffffffffu, smp, 31);
+    const bool none = kw[w] >= V;
+    st[w] = __ballot_sync(0xffffffffu,
+                          i >= 0 && (none || i == 0 || kp != kw[w] || (kNorm && sp != smp)));
+    nt[w] = __ballot_sync(0xffffffffu, none);
+  }
+  const uint32_t S0 = st[0];
+  const u64 M = st[1] | static_cast<u64>(st[2]) << 32;
+  const uint32_t inside = (1u << R) - 1u;
+  RangeRows q;
+  q.none = nt[1] & inside;
   // entries of the range that hold a token come first
-  const int Rt = none == 0 ? R : min(R, __ffsll(static_cast<long long>(none)) - 1);
+  const int Rt = q.none == 0 ? R : __ffs(static_cast<int>(q.none)) - 1;
 
-  // rows [first, last) of the window are this warp's; E bit: last row of a run
-  // or piece, Lg bit: a row of a long run
-  int first = 0, last = 0;
-  unsigned long long E = 0, Lg = 0;
-  int begins = 0;  // 1 + slot of the long run that begins here
-  int o = 0;
-  if (Rt > 0 && (M & 1ull) == 0) {
+  // Rows [first, last) of the window are this CTA's.  A row ends a run where
+  // the next entry starts one, or where a long run is cut; rows below head or
+  // from tail on belong to long runs.
+  int first = 0, last = 0, head = 0, tail = 32;
+  u64 E = M >> 1;
+  int flags = 0;
+  if (Rt > 0 && (M & 1) == 0) {
     // the range begins inside a run
     const int e = M == 0 ? 64 : __ffsll(static_cast<long long>(M)) - 1;
     const int before = S0 == 0 ? 64 : 32 - (31 - __clz(S0));
-    if (before + e > kShortRun) {
-      const int cut = min(e, R);
-      Lg |= cut >= 64 ? ~0ull : (1ull << cut) - 1ull;
-      E |= 1ull << (cut - 1);
-      last = cut;
-      o = cut;
+    if (before + e > kRange) {
+      head = last = min(e, R);
+      if (e > R) flags |= 4;
+      E |= 1ull << (head - 1);
     } else {
-      first = e;
-      last = e;
-      o = e;
+      first = last = e;
     }
   }
-  while (o < Rt) {
-    const unsigned long long rest = o >= 63 ? 0ull : M >> (o + 1);
+  const uint32_t S = st[1] & ((1u << Rt) - 1u);  // starts in the range
+  if (S != 0) {
+    const int o = 31 - __clz(S);  // only the last run can leave the range
+    const u64 rest = M >> (o + 1);
     const int len = rest == 0 ? 64 : __ffsll(static_cast<long long>(rest));
-    if (len > kShortRun) {  // reaches past the range (R <= kShortRun)
-      Lg |= ((1ull << R) - 1ull) & ~((1ull << o) - 1ull);
-      E |= 1ull << (R - 1);
-      begins = o == 0 ? 1 : 2;
+    if (len > kRange) {
+      flags |= 4 | (o == 0 ? 1 : 2);
+      tail = o;
       last = R;
-      break;
+      E |= 1ull << (R - 1);
+    } else {
+      last = o + len;
     }
-    E |= 1ull << (o + len - 1);
-    o += len;
-    last = o;
   }
-  if (slice == 0 && lane == 0 && DPRC_IN(range < a.nranges)) a.long_at[range] = begins;
+  if (tell && lane == 0 && DPRC_IN(range < a.nranges)) a.long_at[range] = flags;
+  q.rows = last - first;  // <= 31
+  q.E = static_cast<uint32_t>(E >> first) & ((1u << q.rows) - 1u);
+  const uint32_t hm = (1u << head) - 1u, tm = tail >= 32 ? 0u : ~((1u << tail) - 1u);
+  q.L = (hm | tm) >> first;  // first > 0 only where head is 0
+  q.slot = first == 0 ? 0 : 1;
+  const int o = first + lane;
+  const uint32_t k1 = __shfl_sync(0xffffffffu, kw[1], o & 31);
+  const uint32_t k2 = __shfl_sync(0xffffffffu, kw[2], o & 31);
+  const int p1 = __shfl_sync(0xffffffffu, pw[1], o & 31);
+  const int p2 = __shfl_sync(0xffffffffu, pw[2], o & 31);
+  q.key = o < 32 ? k1 : k2;
+  q.pos = o < 32 ? p1 : p2;
+  return q;
+}
+
+// What a CTA knows of its range.
+struct RangeShared {
+  int pos[kMaxRows];
+  uint32_t key[kMaxRows];
+  float w[kMaxRows];               // grad: the row's factor
+  float q[kSegThreads / 32][kMaxRows];  // norm: each warp's part of a row's square
+  uint32_t E, L, none;
+  int rows, slot;
+};
+
+template <typename T, int AW, bool kNorm>
+__device__ __forceinline__ void segment_range(const SegArgs& a, const T* __restrict__ G,
+                                              T* __restrict__ dW, int range, int blk,
+                                              RangeShared& s) {
+  using RawT = typename Raw<AW>::type;
+  constexpr int VE = AW / static_cast<int>(sizeof(T));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    const RangeRows q = range_rows<kNorm>(a, range, blk == 0);
+    s.pos[lane] = q.pos;
+    s.key[lane] = q.key;
+    if (!kNorm && a.c != nullptr && lane < q.rows) s.w[lane] = __ldg(a.c + sample_of(a, q.pos));
+    if (lane == 0) {
+      s.E = q.E;
+      s.L = q.L;
+      s.none = q.none;
+      s.rows = q.rows;
+      s.slot = q.slot;
+    }
+  }
+  __syncthreads();
+  const int rows = s.rows;
+  const uint32_t E = s.E, L = s.L;
 
   const int nvec = static_cast<int>(a.d / VE);
-  const int v0 = slice * 32 * NV + lane;  // this lane's accesses: v0 + 32 j
-  float acc[NA];
+  const int v = blk * kSegThreads + threadIdx.x;  // this thread's access of a row
+  const bool mine = v < nvec;
+  const RawT* const col = reinterpret_cast<const RawT*>(G) + (mine ? v : 0);
+  float acc[VE];
 #pragma unroll
-  for (int e = 0; e < NA; ++e) acc[e] = 0.f;
-  float sq1 = 0.f, sq2 = 0.f;  // norm: squares by window entry lane, lane + 32
-  int run0 = first;
+  for (int e = 0; e < VE; ++e) acc[e] = 0.f;
 
-  for (int r0 = first; r0 < last; r0 += kRowsAhead) {
-    RawT raw[kRowsAhead][NV];
-    float wgt[kRowsAhead];
+#pragma unroll 1
+  for (int base = 0; base < rows; base += kBatch) {
+    RawT raw[kBatch];
 #pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      const int r = r0 + u;
-      const int p = __shfl_sync(0xffffffffu, r < 32 ? pos1 : pos2, r & 31);
-      wgt[u] = 1.f;
-      if (r < last) {
-        const RawT* row = reinterpret_cast<const RawT*>(G + static_cast<long long>(p) * a.d);
+    for (int r = 0; r < kBatch; ++r) {
+      raw[r] = RawT{};
+      if (base + r < rows && DPRC_IN(s.pos[base + r] >= 0 && s.pos[base + r] < a.N))
+        raw[r] = __ldcs(col + static_cast<long long>(s.pos[base + r]) * nvec);
+    }
+    // bits of the batch's rows: ends of runs, ends of long runs' pieces, starts
+    const uint32_t Eb = E >> base, Pb = (E & L) >> base;
+    const uint32_t Bb = base == 0 ? (E << 1) | 1u : E >> (base - 1);
+    float sum[kNorm ? kBatch : 1];
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (v0 + 32 * j < nvec && DPRC_IN(p >= 0 && p < a.N)) raw[u][j] = __ldcs(row + v0 + 32 * j);
-        if (!kNorm && a.c != nullptr) wgt[u] = __ldg(a.c + p / static_cast<int>(a.T));
+    for (int r = 0; r < kBatch; ++r) {
+      // A run's first row takes the sums from zero: a mask and not a branch,
+      // which would cost more than the eight additions (rows past the last are
+      // zero and end no run)
+      float f[VE];
+      unpack<T, AW>(raw[r], f);
+      const uint32_t keep = ((Bb >> r) & 1u) - 1u;
+      const float w = !kNorm && a.c != nullptr ? s.w[(base + r) & (kMaxRows - 1)] : 1.f;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float old = __uint_as_float(__float_as_uint(acc[e]) & keep);
+        acc[e] = kNorm ? old + f[e] : fmaf(w, f[e], old);
+      }
+      if (kNorm) {
+        const float q = square_sum<VE>(acc);
+        sum[r] = mine && ((Eb >> r) & 1u) ? q : 0.f;
+      }
+      if (kNorm ? (Pb >> r) & 1u : (Eb >> r) & 1u) {
+        if ((Pb >> r) & 1u) {
+          // a piece of a long run: the one over the range's first entry is slot 0
+          const int slot = s.slot == 0 && (E & ((1u << (base + r)) - 1u)) == 0 ? 0 : 1;
+          float* out = a.part + (static_cast<long long>(range) * 2 + slot) * a.dpad +
+                       static_cast<long long>(v) * VE;
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e)
+              if (DPRC_IN(static_cast<long long>(v) * VE + e < a.dpad)) out[e] = acc[e];
+          }
+          if (kNorm) sum[r] = 0.f;
+        } else if (!kNorm) {
+          const uint32_t k = s.key[base + r];
+          RawT* out = reinterpret_cast<RawT*>(dW) + static_cast<long long>(k) * nvec + v;
+          if (mine && DPRC_IN(k < static_cast<uint32_t>(a.V))) {
+            if (a.accumulate) {
+              unpack<T, AW>(*out, f);
+#pragma unroll
+              for (int e = 0; e < VE; ++e) f[e] = fmaf(a.scale, acc[e], f[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < VE; ++e) f[e] = a.scale * acc[e];
+            }
+            __stcs(out, pack<T, AW>(f));
+          }
+        }
       }
     }
+    if constexpr (kNorm) {
+      // the batch's squares over the warp's lanes, all at once: lanes h apart
+      // share the rows out between them, which leaves lane l with row l >> 2
 #pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      const int r = r0 + u;
-      if (r >= last) break;
+      for (int h = 16, n = kBatch / 2; n > 0; h >>= 1, n >>= 1) {
+        const bool up = (lane & h) != 0;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (v0 + 32 * j < nvec) {
-          float f[VE];
-          unpack<T, AW>(raw[u][j], f);
-#pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            if (kNorm)
-              acc[j * VE + e] += f[e];
-            else
-              acc[j * VE + e] = fmaf(wgt[u], f[e], acc[j * VE + e]);
-          }
+        for (int r = 0; r < n; ++r) {
+          const float give = up ? sum[r] : sum[r + n];
+          const float keep = up ? sum[r + n] : sum[r];
+          sum[r] = keep + __shfl_xor_sync(0xffffffffu, give, h);
         }
       }
-      if ((E >> r) & 1ull) {
-        if ((Lg >> r) & 1ull) {
-          // a piece of a long run: the one over the range's first entry is slot 0
-          const int slot = run0 == 0 ? 0 : 1;
-          float* out = a.part + (range * 2 + slot) * a.dpad;
-#pragma unroll
-          for (int j = 0; j < NV; ++j)
-            if (v0 + 32 * j < nvec)
-#pragma unroll
-              for (int e = 0; e < VE; ++e)
-                if (DPRC_IN((v0 + 32 * j) * VE + e < a.dpad))
-                  out[static_cast<long long>(v0 + 32 * j) * VE + e] = acc[j * VE + e];
-        } else if (kNorm) {
-          float s = 0.f;
-#pragma unroll
-          for (int e = 0; e < NA; ++e) s = fmaf(acc[e], acc[e], s);
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-          if (lane == (run0 & 31)) {
-            if (run0 < 32) sq1 = s; else sq2 = s;
-          }
-        } else {
-          const uint32_t k = __shfl_sync(0xffffffffu, r < 32 ? key1 : key2, r & 31);
-          RawT* out = reinterpret_cast<RawT*>(dW + static_cast<long long>(k) * a.d);
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            if (v0 + 32 * j < nvec && DPRC_IN(k < static_cast<uint32_t>(a.V))) {
-              float f[VE];
-              if (a.accumulate) {
-                unpack<T, AW>(out[v0 + 32 * j], f);
-#pragma unroll
-                for (int e = 0; e < VE; ++e) f[e] = fmaf(a.scale, acc[j * VE + e], f[e]);
-              } else {
-#pragma unroll
-                for (int e = 0; e < VE; ++e) f[e] = a.scale * acc[j * VE + e];
-              }
-              __stcs(out + v0 + 32 * j, pack<T, AW>(f));
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < NA; ++e) acc[e] = 0.f;
-        run0 = r + 1;
-      }
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
+      if ((lane & 3) == 0) s.q[warp][base + (lane >> 2)] = sum[0];
     }
   }
-  if (kNorm) {
-    // every entry is written once: by the warp that took its row (a run's
-    // square at its first entry, zero at the others), or here if it holds no token
-    float* sq = a.sq + static_cast<long long>(slice) * a.N;
-    const int o1 = lane, o2 = lane + 32;
-    const bool w1 = (o1 >= first && o1 < last) || (o1 >= Rt && o1 < R);
-    const bool w2 = o2 >= first && o2 < last;
-    if (w1 && DPRC_IN(pos1 >= 0 && pos1 < a.N)) sq[pos1] = sq1;
-    if (w2 && DPRC_IN(pos2 >= 0 && pos2 < a.N)) sq[pos2] = sq2;
+
+  if constexpr (kNorm) {
+    __syncthreads();
+    if (warp == 0) {
+      // every entry is written once: by the CTA that took its row (a run's
+      // square stands at its last row, zero at the others), or here if it
+      // holds no token
+      float t = 0.f;
+      const int nw = blockDim.x >> 5;
+      if (lane < rows) {
+        for (int w = 0; w < nw; ++w) t += s.q[w][lane];
+        const int p = s.pos[lane];
+        if (DPRC_IN(p >= 0 && p < a.N)) a.sq[static_cast<long long>(p) * a.nblk + blk] = t;
+      }
+      if ((s.none >> lane) & 1u)
+        a.sq[static_cast<long long>(__ldg(a.pos + range * kRange + lane)) * a.nblk + blk] = 0.f;
+    }
   }
 }
 
@@ -555,37 +762,43 @@ __device__ __forceinline__ void zero_rows(const SegArgs& a, T* __restrict__ dW, 
   }
 }
 
-template <typename T, int AW, int NV, bool kNorm>
-__global__ void __launch_bounds__(32 * kSegWarps)
+template <typename T, int AW, bool kNorm>
+__global__ void __launch_bounds__(kSegThreads, 4)
     embed_segment_kernel(const SegArgs a, const T* __restrict__ G, T* __restrict__ dW) {
-  const long long w = static_cast<long long>(blockIdx.x) * kSegWarps + (threadIdx.x >> 5);
-  const long long units = a.nranges * a.nslices;
-  if (w < units) {
-    // neighbouring warps take the slices of one range, so a row's bytes are
-    // read together
-    const long long range = w / a.nslices;
-    segment_range<T, AW, NV, kNorm>(a, G, dW, range, static_cast<int>(w - range * a.nslices));
-  } else if (!kNorm && w - units < a.zero_units) {
-    zero_rows<T, AW>(a, dW, w - units);
+  __shared__ RangeShared s_range;
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long units = static_cast<long long>(a.nranges) * a.nblk;
+  if (blockIdx.x < units) {
+    const int range = static_cast<int>(blockIdx.x / a.nblk);
+    segment_range<T, AW, kNorm>(a, G, dW, range, static_cast<int>(blockIdx.x) - range * a.nblk,
+                                s_range);
+  } else if (!kNorm) {
+    const long long u = (blockIdx.x - units) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (u < a.zero_units) zero_rows<T, AW>(a, dW, u);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Long runs: the pieces of a run added in order.  One CTA looks at 32 ranges
-// (blockIdx.x) and one block of kLongCols columns (blockIdx.y); for each range
-// in which a long run begins, its warps take the run's pieces in contiguous
-// shares, add them, and the shares are added in warp order.
+// Long runs: the pieces of a run added in order.  One CTA looks at kLongRanges
+// ranges (blockIdx.x) and one block of kLongCols columns (blockIdx.y); for each
+// range in which a long run begins, its warps take the run's pieces in
+// contiguous shares, add them, and the shares are added in warp order.  Where a
+// run ends is read off the ranges' flags, 32 at a time.
 // ---------------------------------------------------------------------------
-constexpr int kLongWarps = 16;
+constexpr int kLongWarps = 8;
+constexpr int kLongRanges = 16;
 constexpr int kLongCols = 128;  // 4 per lane
 
 template <typename T, bool kNorm>
 __global__ void __launch_bounds__(32 * kLongWarps)
     embed_long_kernel(const SegArgs a, T* __restrict__ dW) {
   __shared__ float4 s_sum[kLongWarps][32];
+  pdl_launch_dependents();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long rbase = static_cast<long long>(blockIdx.x) * 32;
-  const int at = rbase + lane < a.nranges ? a.long_at[rbase + lane] : 0;
+  const long long rbase = static_cast<long long>(blockIdx.x) * kLongRanges;
+  const int at = lane < kLongRanges && rbase + lane < a.nranges ? a.long_at[rbase + lane] & 3 : 0;
   uint32_t todo = __ballot_sync(0xffffffffu, at != 0);
   const long long col = static_cast<long long>(blockIdx.y) * kLongCols + lane * 4;  // < dpad
   while (todo != 0) {
@@ -593,22 +806,23 @@ __global__ void __launch_bounds__(32 * kLongWarps)
     todo &= todo - 1;
     const int slot = __shfl_sync(0xffffffffu, at, j) - 1;
     const long long range = rbase + j;
-    // the run's first entry, and by a search over its successors its end
-    const long long b = min((range + 1) * a.R, a.N);
-    const uint32_t k = __ldg(a.key + b - 1);
-    const int sample = __ldg(a.pos + b - 1) / static_cast<int>(a.T);
-    long long lo = b, hi = a.N;  // first entry >= b that is not of the run
-    while (lo < hi) {
-      const long long m = (lo + hi) >> 1;
-      const bool same = __ldg(a.key + m) == k &&
-                        (!kNorm || __ldg(a.pos + m) / static_cast<int>(a.T) == sample);
-      if (same) lo = m + 1; else hi = m;
+    // the run's last range: the first after `range` from which no long run
+    // reaches on, or in which another begins
+    long long end = range + 1;
+    while (true) {
+      const int f = end + lane < a.nranges ? a.long_at[end + lane] : 0;
+      const uint32_t stop = __ballot_sync(0xffffffffu, (f & 4) == 0 || (f & 3) == 2);
+      if (stop != 0) {
+        end += __ffs(static_cast<int>(stop)) - 1;
+        break;
+      }
+      end += 32;
     }
-    const long long pieces = (lo - 1) / a.R - range + 1;  // ranges range .. range + pieces - 1
+    const long long pieces = end - range + 1;
     const long long share = (pieces + kLongWarps - 1) / kLongWarps;
     const long long p0 = warp * share, p1 = min(p0 + share, pieces);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (long long p = p0; p < p1; ++p) {
       const long long slot_row = (range + p) * 2 + (p == 0 ? slot : 0);
       if (DPRC_IN(range + p < a.nranges && col + 3 < a.dpad)) {
@@ -640,6 +854,7 @@ __global__ void __launch_bounds__(32 * kLongWarps)
         for (int off = 16; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
         if (lane == 0) a.long_sq[range * gridDim.y + blockIdx.y] = q;
       } else {
+        const uint32_t k = __ldg(a.key + (range + 1) * kRange - 1);  // the run reaches past `range`
         T* out = dW + static_cast<long long>(k) * a.d;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -667,20 +882,20 @@ __global__ void __launch_bounds__(256)
     embed_norm_finish_kernel(const SegArgs a, int ncb, float* __restrict__ n) {
   __shared__ float s_warp[8];
   __shared__ float s_cta[8];
+  pdl_wait();
   const uint32_t rank = cluster_ctarank(), cl = cluster_nctarank();
   const long long i = blockIdx.x / cl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = static_cast<int>(rank) * 256 + threadIdx.x, step = static_cast<int>(cl) * 256;
   float s = 0.f;
-  for (int sl = 0; sl < a.nslices; ++sl) {
-    const float* sq = a.sq + static_cast<long long>(sl) * a.N + i * a.T;
-#pragma unroll 4
-    for (long long t = t0; t < a.T; t += step) s += __ldcg(sq + t);
-  }
+  const long long count = static_cast<long long>(a.T) * a.nblk;
+  const float* sq = a.sq + i * count;
+#pragma unroll 8
+  for (long long t = t0; t < count; t += step) s += __ldcg(sq + t);
   for (long long r = t0; r < a.nranges; r += step) {
-    if (a.long_at[r] == 0) continue;
-    const long long e = min((r + 1) * a.R, a.N) - 1;  // an entry of the run that begins in r
-    if (__ldg(a.pos + e) / static_cast<int>(a.T) != i) continue;
+    if ((a.long_at[r] & 3) == 0) continue;
+    const long long e = (r + 1) * kRange - 1;  // an entry of the run that begins in r
+    if (sample_of(a, __ldg(a.pos + e)) != i) continue;
     for (int b = 0; b < ncb; ++b) s += __ldcg(a.long_sq + r * ncb + b);
   }
 #pragma unroll
@@ -720,21 +935,8 @@ int access_bytes(int64_t d, int elem) {
   return row % 16 == 0 ? 16 : row % 8 == 0 ? 8 : row % 4 == 0 ? 4 : 2;
 }
 
-// Accesses per lane and row: 16 columns of bf16 or 8 of fp32 per lane, so a
-// slice is 512 or 256 columns and four rows ahead fit in registers.
-constexpr int accesses(int aw) { return aw == 16 ? 2 : aw == 8 ? 4 : 8; }
-
-// Entries per range: as many as leave about 32 warps for each of 152 SMs,
-// between 4 (below it the window of neighbours costs more than the rows) and
-// 32 (the longest run a warp may take whole).
-int range_entries(int64_t N, int64_t nslices) {
-  int R = 4;
-  while (R < 32 && N * nslices > int64_t(4864) * R) R *= 2;
-  return R;
-}
-
 struct SegPlan {
-  int aw = 16, nslices = 1, R = 4, ncb = 1;
+  int aw = 16, nblk = 1, threads = 32, ncb = 1;
   int64_t nranges = 0, dpad = 0;
   size_t part_off = 0, long_off = 0, lsq_off = 0, sq_off = 0, total = 0;
 };
@@ -743,10 +945,10 @@ SegPlan seg_plan(dprc_dtype dt, int64_t N, int64_t d, bool norm) {
   SegPlan s;
   const int elem = dt == DPRC_F32 ? 4 : 2;
   s.aw = access_bytes(d, elem);
-  const int64_t cols = int64_t(32) * accesses(s.aw) * (s.aw / elem);
-  s.nslices = static_cast<int>((d + cols - 1) / cols);
-  s.R = range_entries(N, s.nslices);
-  s.nranges = (N + s.R - 1) / s.R;
+  const int64_t nvec = d * elem / s.aw;
+  s.nblk = static_cast<int>((nvec + kSegThreads - 1) / kSegThreads);
+  s.threads = nvec >= kSegThreads ? kSegThreads : static_cast<int>((nvec + 31) / 32 * 32);
+  s.nranges = (N + kRange - 1) / kRange;
   s.dpad = (d + kLongCols - 1) / kLongCols * kLongCols;
   s.ncb = static_cast<int>(s.dpad / kLongCols);
   size_t off = 0;
@@ -758,56 +960,64 @@ SegPlan seg_plan(dprc_dtype dt, int64_t N, int64_t d, bool norm) {
     s.lsq_off = off;
     off = up256(off + static_cast<size_t>(s.nranges) * s.ncb * 4);
     s.sq_off = off;
-    off = up256(off + static_cast<size_t>(s.nslices) * N * 4);
+    off = up256(off + static_cast<size_t>(s.nblk) * N * 4);
   }
   s.total = off > 0 ? off : 256;
   return s;
 }
 
+// The plan: sorted keys and positions at the front; behind them, where the
+// radix sort runs, its second buffers and counts.
 struct SortPlan {
-  int passes = 1, dbits = 1, ctas = 1;
-  size_t key_off[2], pos_off[2], hist_off = 0, total = 0;
+  int passes = 0, bits = 0, tiles = 0;  // passes 0: by ranks
+  int64_t per = 0;
+  size_t key_off[2] = {0, 0}, pos_off[2] = {0, 0}, count_off = 0, total = 0;
 };
 
 SortPlan sort_plan(int64_t N, int64_t V) {
   SortPlan s;
-  int bits = 1;
-  while ((int64_t(1) << bits) <= V) ++bits;  // keys 0..V
-  s.passes = (bits + 9) / 10;
-  s.dbits = (bits + s.passes - 1) / s.passes;
-  s.ctas = N <= 4096 ? 1 : 8;
   size_t off = 0;
-  for (int b = 0; b < 2; ++b) {
+  for (int b = 0; b < (N > kRankMax ? 2 : 1); ++b) {
     s.key_off[b] = off;
     off = up256(off + static_cast<size_t>(N) * 4);
     s.pos_off[b] = off;
     off = up256(off + static_cast<size_t>(N) * 4);
   }
-  s.hist_off = off;
-  off = up256(off + static_cast<size_t>(8) * kSortMaxDigit * 4);
-  s.total = off;
+  if (N > kRankMax) {
+    int bits = 1;
+    while ((int64_t(1) << bits) <= V) ++bits;  // keys 0..V
+    s.passes = (bits + kSortMaxBits - 1) / kSortMaxBits;
+    s.bits = (bits + s.passes - 1) / s.passes;
+    const int64_t tiles = std::min<int64_t>((N + kSortTile - 1) / kSortTile, kSortMaxTiles);
+    s.per = ((N + tiles * kSortWarps - 1) / (tiles * kSortWarps) + 31) / 32 * 32;
+    s.tiles = static_cast<int>((N + s.per * kSortWarps - 1) / (s.per * kSortWarps));
+    s.count_off = off;
+    off = up256(off + (static_cast<size_t>(s.tiles) << s.bits) * 4);
+  }
+  s.total = off > 0 ? off : 256;
   return s;
 }
 
-template <typename TOK>
-cudaError_t launch_sort_t(const TOK* tokens, const SortArgs& a, int ctas, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(kSortWarps) * (size_t(1) << a.dbits) * 4;
-  cudaError_t e = cudaFuncSetAttribute(token_sort_kernel<TOK>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSortWarps * kSortMaxDigit * 4);
-  if (e != cudaSuccess) return e;
+// Launches `kernel` so that it may start while the kernel before it in the
+// stream ends; the kernel waits for that one (pdl_wait) before it reads or
+// writes anything.  cl: CTAs per cluster.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int cl, cudaStream_t s,
+                         size_t smem, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kSortThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, token_sort_kernel<TOK>, tokens, a);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cl;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cl > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 SegArgs seg_args(const EmbedCall& c, const SegPlan& p, const SortPlan& sp, char* ws) {
@@ -815,13 +1025,13 @@ SegArgs seg_args(const EmbedCall& c, const SegPlan& p, const SortPlan& sp, char*
   const char* plan = static_cast<const char*>(c.plan);
   a.key = reinterpret_cast<const uint32_t*>(plan + sp.key_off[0]);
   a.pos = reinterpret_cast<const int*>(plan + sp.pos_off[0]);
-  a.N = c.B * c.T;
-  a.T = c.T > 0 ? c.T : 1;
+  a.N = static_cast<int>(c.B * c.T);
+  a.T = static_cast<int>(c.T > 0 ? c.T : 1);
+  a.t_inv = a.T == 1 ? 0 : ~0ull / static_cast<unsigned>(a.T) + 1;
   a.V = static_cast<int>(c.V);
   a.d = c.d;
-  a.R = p.R;
-  a.nslices = p.nslices;
-  a.nranges = p.nranges;
+  a.nblk = p.nblk;
+  a.nranges = static_cast<int>(p.nranges);
   a.scale = c.scale;
   a.sq = reinterpret_cast<float*>(ws + p.sq_off);
   a.long_sq = reinterpret_cast<float*>(ws + p.lsq_off);
@@ -837,19 +1047,18 @@ SegArgs seg_args(const EmbedCall& c, const SegPlan& p, const SortPlan& sp, char*
 template <typename T, int AW, bool kNorm>
 cudaError_t launch_segments_t(const SegArgs& a, const SegPlan& p, const void* G, void* dW,
                               cudaStream_t s) {
-  const long long warps = a.nranges * a.nslices + a.zero_units;
-  if (warps > 0) {
-    const long long ctas = (warps + kSegWarps - 1) / kSegWarps;
-    embed_segment_kernel<T, AW, accesses(AW), kNorm>
-        <<<static_cast<unsigned>(ctas), 32 * kSegWarps, 0, s>>>(a, static_cast<const T*>(G),
-                                                                static_cast<T*>(dW));
-    const cudaError_t e = cudaGetLastError();
+  const long long zero_ctas = (a.zero_units * 32 + p.threads - 1) / p.threads;
+  const long long ctas = static_cast<long long>(a.nranges) * a.nblk + zero_ctas;
+  if (ctas > 0) {
+    const cudaError_t e =
+        launch_after(embed_segment_kernel<T, AW, kNorm>, dim3(static_cast<unsigned>(ctas)),
+                     p.threads, 1, s, 0, a, static_cast<const T*>(G), static_cast<T*>(dW));
     if (e != cudaSuccess) return e;
   }
-  if (a.N > kShortRun) {
-    const dim3 grid(static_cast<unsigned>((a.nranges + 31) / 32), static_cast<unsigned>(p.ncb));
-    embed_long_kernel<T, kNorm><<<grid, 32 * kLongWarps, 0, s>>>(a, static_cast<T*>(dW));
-    return cudaGetLastError();
+  if (a.N > kRange) {
+    const dim3 grid(static_cast<unsigned>((a.nranges + kLongRanges - 1) / kLongRanges), static_cast<unsigned>(p.ncb));
+    return launch_after(embed_long_kernel<T, kNorm>, grid, 32 * kLongWarps, 1, s, 0, a,
+                        static_cast<T*>(dW));
   }
   return cudaSuccess;
 }
@@ -888,6 +1097,47 @@ cudaError_t launch_lookup_t(const void* W, const void* tokens, int64_t N, int64_
       static_cast<const T*>(W), static_cast<const TOK*>(tokens), N, static_cast<int>(V), d, scale,
       static_cast<T*>(out), lanes, static_cast<int>(upr));
   return cudaGetLastError();
+}
+
+template <typename TOK>
+cudaError_t launch_plan_t(const TOK* tokens, int64_t N, int64_t V, char* plan, cudaStream_t s) {
+  const SortPlan sp = sort_plan(N, V);
+  uint32_t* key[2];
+  int* pos[2];
+  for (int b = 0; b < 2; ++b) {
+    key[b] = reinterpret_cast<uint32_t*>(plan + sp.key_off[b]);
+    pos[b] = reinterpret_cast<int*>(plan + sp.pos_off[b]);
+  }
+  if (sp.passes == 0) {
+    const int64_t warps = (N + kRankPer - 1) / kRankPer;
+    const unsigned ctas = static_cast<unsigned>((warps + kRankWarps - 1) / kRankWarps);
+    const size_t smem = static_cast<size_t>((N + 127) / 128 * 128) * 4;  // at most 32 KB
+    token_rank_kernel<TOK><<<ctas, 32 * kRankWarps, smem, s>>>(
+        tokens, static_cast<int>(N), static_cast<int>(V), key[0], pos[0]);
+    return cudaGetLastError();
+  }
+  SortArgs a;
+  a.N = static_cast<int>(N);
+  a.per = static_cast<int>(sp.per);
+  a.V = static_cast<int>(V);
+  a.bits = sp.bits;
+  a.counts = reinterpret_cast<int*>(plan + sp.count_off);
+  const size_t smem = static_cast<size_t>(kSortWarps + 2) * (size_t(1) << sp.bits) * 4;  // <= 40 KB
+  for (int p = 0; p < sp.passes; ++p) {
+    const int dst = (sp.passes - 1 - p) & 1;  // the last pass writes buffer 0
+    a.shift = p * sp.bits;
+    a.key_in = p == 0 ? nullptr : key[dst ^ 1];
+    a.pos_in = p == 0 ? nullptr : pos[dst ^ 1];
+    a.key_out = key[dst];
+    a.pos_out = pos[dst];
+    cudaError_t e = launch_after(token_count_kernel<TOK>, dim3(sp.tiles), kSortThreads, 1, s, 0,
+                                 tokens, a);
+    if (e != cudaSuccess) return e;
+    e = launch_after(token_scatter_kernel<TOK>, dim3(sp.tiles), kSortThreads, 1, s, smem, tokens,
+                     a);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 template <typename TOK>
@@ -934,21 +1184,9 @@ cudaError_t launch_embed_lookup(const void* W, dprc_dtype dt, const void* tokens
 cudaError_t launch_embed_plan(const void* tokens, int token_bytes, int64_t N, int64_t V,
                               void* plan, cudaStream_t s) {
   if (N == 0) return cudaSuccess;
-  const SortPlan sp = sort_plan(N, V);
   char* p = static_cast<char*>(plan);
-  SortArgs a;
-  a.N = N;
-  a.V = static_cast<int>(V);
-  a.passes = sp.passes;
-  a.dbits = sp.dbits;
-  for (int b = 0; b < 2; ++b) {
-    a.key[b] = reinterpret_cast<uint32_t*>(p + sp.key_off[b]);
-    a.pos[b] = reinterpret_cast<int*>(p + sp.pos_off[b]);
-  }
-  a.ghist = reinterpret_cast<int*>(p + sp.hist_off);
-  return token_bytes == 4
-             ? launch_sort_t<int32_t>(static_cast<const int32_t*>(tokens), a, sp.ctas, s)
-             : launch_sort_t<long long>(static_cast<const long long*>(tokens), a, sp.ctas, s);
+  return token_bytes == 4 ? launch_plan_t(static_cast<const int32_t*>(tokens), N, V, p, s)
+                          : launch_plan_t(static_cast<const long long*>(tokens), N, V, p, s);
 }
 
 cudaError_t launch_embed_norm(const EmbedCall& c, float* n, void* ws, cudaStream_t s) {
@@ -962,18 +1200,9 @@ cudaError_t launch_embed_norm(const EmbedCall& c, float* n, void* ws, cudaStream
   cudaError_t e = launch_segments<true>(c.dtype, a, p, c.G, nullptr, s);
   if (e != cudaSuccess) return e;
   // one CTA per sample where a sample has few values, else a cluster of 8
-  const int cl = a.T * p.nslices + a.nranges > 8192 ? 8 : 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(c.B * cl));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cl;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, embed_norm_finish_kernel, a, p.ncb, n);
+  const int cl = static_cast<int64_t>(a.T) * p.nblk + a.nranges > 4096 ? 8 : 1;
+  return launch_after(embed_norm_finish_kernel, dim3(static_cast<unsigned>(c.B * cl)), 256, cl, s,
+                      0, a, p.ncb, n);
 }
 
 cudaError_t launch_embed_grad(const EmbedCall& c, const float* clip, void* dW, void* ws,

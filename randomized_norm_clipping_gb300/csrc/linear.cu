@@ -95,6 +95,41 @@ constexpr int kDzRows = 64;
 constexpr int kDzWarps = 8;
 constexpr int kDzAhead = 4;
 
+// Eight values as they are stored, so that rows on their way cost few registers.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void raw_ld(const T* p, int cnt, bool vec, Raw8<T>& r) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+      r.v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  } else {
+    T* e = reinterpret_cast<T*>(r.v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = i < cnt ? p[i] : static_cast<T>(0.f);
+  }
+}
+__device__ __forceinline__ void raw_get(const Raw8<float>& r, float* v) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.v[i].x);
+    v[4 * i + 1] = __uint_as_float(r.v[i].y);
+    v[4 * i + 2] = __uint_as_float(r.v[i].z);
+    v[4 * i + 3] = __uint_as_float(r.v[i].w);
+  }
+}
+__device__ __forceinline__ void raw_get(const Raw8<__nv_bfloat16>& r, float* v) {
+  const uint32_t u[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(u[e] << 16);
+    v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+  }
+}
+
 struct DzArgs {
   const void* dY;
   const void* Z;
@@ -109,7 +144,7 @@ struct DzArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kDzWarps) linear_dz_kernel(const DzArgs a) {
+__global__ void __launch_bounds__(32 * kDzWarps, 2) linear_dz_kernel(const DzArgs a) {
   __shared__ float s_sum[kDzWarps][256];
   constexpr bool kFast = sizeof(T) == 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -122,36 +157,37 @@ __global__ void __launch_bounds__(32 * kDzWarps) linear_dz_kernel(const DzArgs a
   const bool vec = a.vec != 0;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (cnt > 0) {
+#pragma unroll 1
     for (int r0 = warp; r0 < kDzRows; r0 += kDzWarps * kDzAhead) {
-      float g[kDzAhead][8], z[kDzAhead][8];
+      Raw8<T> g8[kDzAhead], z8[kDzAhead];
 #pragma unroll
       for (int u = 0; u < kDzAhead; ++u) {
         const long long m = m0 + r0 + u * kDzWarps;
         if (m >= a.M) continue;
-        ld_n<T>(static_cast<const T*>(a.dY) + m * a.N + n0, cnt, vec, g[u]);
+        raw_ld(static_cast<const T*>(a.dY) + m * a.N + n0, cnt, vec, g8[u]);
         if (a.act != DPRC_ACT_NONE)
-          ld_n<T>(static_cast<const T*>(a.Z) + m * a.N + n0, cnt, vec, z[u]);
+          raw_ld(static_cast<const T*>(a.Z) + m * a.N + n0, cnt, vec, z8[u]);
       }
 #pragma unroll
       for (int u = 0; u < kDzAhead; ++u) {
         const long long m = m0 + r0 + u * kDzWarps;
         if (m >= a.M) continue;
-        if (a.drop.thr != 0)
-          drop8_at(g[u], static_cast<uint64_t>(m * a.N + n0), a.drop, rk);
+        float g[8], z[8];
+        raw_get(g8[u], g);
+        if (a.drop.thr != 0) drop8_at(g, static_cast<uint64_t>(m * a.N + n0), a.drop, rk);
         if (a.act != DPRC_ACT_NONE) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[u][e] *= act_slope<kFast>(z[u][e], a.act);
+          raw_get(z8[u], z);
+          act_slope8<kFast>(g, z, a.act);
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = e < cnt ? g[e] : 0.f;
         if (a.colsum != nullptr) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] += e < cnt ? g[u][e] : 0.f;
+          for (int e = 0; e < 8; ++e) sum[e] += g[e];
         }
-        if (a.dZ != nullptr) st_n<T>(static_cast<T*>(a.dZ) + m * a.N + n0, cnt, vec, g[u]);
-        if (a.planes != nullptr && DPRC_IN(m < a.M && n0 + 8 <= a.ldp)) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) g[u][e] = e < cnt ? g[u][e] : 0.f;
-          store_planes<T>(a.planes + m * a.ldp + n0, a.plane, g[u]);
-        }
+        if (a.dZ != nullptr) st_n<T>(static_cast<T*>(a.dZ) + m * a.N + n0, cnt, vec, g);
+        if (a.planes != nullptr && DPRC_IN(m < a.M && n0 + 8 <= a.ldp))
+          store_planes<T>(a.planes + m * a.ldp + n0, a.plane, g);
       }
     }
   }
@@ -306,6 +342,7 @@ struct LinearGradPlan {
   int64_t ldk = 0, ldn = 0, nblocks = 0;
   GemmShape gx, gw;
   GemmPlan px, pw;
+  bool together = false;    // dX and dW in one launch
   size_t dz_off = 0, x_off = 0, w_off = 0, sum_off = 0, part_off = 0, total = 0;
 };
 
@@ -327,6 +364,9 @@ LinearGradPlan linear_grad_plan(dprc_dtype dt, int64_t M, int64_t K, int64_t N) 
   l.gw.K = M;
   l.gw.planes = l.planes;
   l.pw = plan_gemm(l.gw);
+  const bool w_first = M >= N;
+  l.together = w_first ? gemm_together(l.gw, l.pw, l.gx, l.px)
+                       : gemm_together(l.gx, l.px, l.gw, l.pw);
   size_t off = 0;
   l.dz_off = off;
   off = up1k(off + static_cast<size_t>(l.planes) * M * l.ldn * 2);
@@ -490,26 +530,34 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, void* ws, cudaStream_t s
     e = launch_pack(c.dtype, jobs, n, s);
     if (e != cudaSuccess) return e;
   }
-  LinearEpi epi;
-  epi.N = static_cast<int>(c.K);
-  epi.vec = c.K % 8 == 0;
-  if (c.dX != nullptr) {
-    epi.M = c.M;
-    epi.Y = c.dX;
-    GemmOperand wm = wt, dk = dz;
-    wm.mn_major = true;
-    e = run_gemm(l.gx, l.px, l.gx.transposed ? wm : dk, l.gx.transposed ? dk : wm, c.dtype, epi,
-                 w + l.part_off, s);
+  GemmTask tx, tw;
+  tx.shape = &l.gx;
+  tx.plan = &l.px;
+  GemmOperand wm = wt;
+  wm.mn_major = true;
+  tx.A = l.gx.transposed ? wm : dz;
+  tx.B = l.gx.transposed ? dz : wm;
+  tw.shape = &l.gw;
+  tw.plan = &l.pw;
+  tw.A = dz;
+  tw.B = x;
+  tw.A.mn_major = tw.B.mn_major = true;
+  tx.epi.N = tw.epi.N = static_cast<int>(c.K);
+  tx.epi.vec = tw.epi.vec = c.K % 8 == 0;
+  tx.epi.M = c.M;
+  tx.epi.Y = c.dX;
+  tw.epi.M = c.N;
+  tw.epi.Y = c.dW;
+  if (c.dX != nullptr && c.dW != nullptr && l.together) {
+    const bool w_first = l.gw.K >= l.gx.K;
+    return launch_gemm_two(w_first ? tw : tx, w_first ? tx : tw, c.dtype, s);
+  }
+  for (const GemmTask* t : {&tx, &tw}) {
+    if (t->epi.Y == nullptr) continue;
+    e = run_gemm(*t->shape, *t->plan, t->A, t->B, c.dtype, t->epi, w + l.part_off, s);
     if (e != cudaSuccess) return e;
   }
-  if (c.dW != nullptr) {
-    epi.M = c.N;
-    epi.Y = c.dW;
-    GemmOperand dm = dz, xm = x;
-    dm.mn_major = xm.mn_major = true;
-    e = run_gemm(l.gw, l.pw, dm, xm, c.dtype, epi, w + l.part_off, s);
-  }
-  return e;
+  return cudaSuccess;
 }
 
 }  // namespace dprc

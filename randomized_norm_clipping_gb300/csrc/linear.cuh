@@ -35,26 +35,40 @@ constexpr float kGeluA = 0.044715f;
 
 // gelu(z) = z (1 + tanh u) / 2 = z sigmoid(2 u), u = sqrt(2/pi) (z + 0.044715 z^3)
 template <bool kFast>
-__device__ __forceinline__ float act_value(float z, int act) {
-  if (act == DPRC_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
-  if (act == DPRC_ACT_GELU)
-    return z * sigmoid_f<kFast>(kGelu2C * fmaf(kGeluA * z * z, z, z));
-  if (act == DPRC_ACT_SILU) return z * sigmoid_f<kFast>(z);
-  return z;
+__device__ __forceinline__ void act_value8(float* z, int act) {
+  if (act == DPRC_ACT_SILU) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] *= sigmoid_f<kFast>(z[e]);
+  } else if (act == DPRC_ACT_GELU) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      z[e] *= sigmoid_f<kFast>(kGelu2C * fmaf(kGeluA * z[e] * z[e], z[e], z[e]));
+  } else if (act == DPRC_ACT_RELU) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = z[e] <= 0.f ? 0.f : z[e];  // NaN stays
+  }
 }
 
+// g *= act'(z)
 template <bool kFast>
-__device__ __forceinline__ float act_slope(float z, int act) {
-  if (act == DPRC_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
-  if (act == DPRC_ACT_GELU) {
-    const float s = sigmoid_f<kFast>(kGelu2C * fmaf(kGeluA * z * z, z, z));
-    return fmaf(z * s * (1.f - s), kGelu2C * fmaf(3.f * kGeluA * z, z, 1.f), s);
-  }
+__device__ __forceinline__ void act_slope8(float* g, const float* z, int act) {
   if (act == DPRC_ACT_SILU) {
-    const float s = sigmoid_f<kFast>(z);
-    return fmaf(z * s, 1.f - s, s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float s = sigmoid_f<kFast>(z[e]);
+      g[e] *= fmaf(z[e] * s, 1.f - s, s);
+    }
+  } else if (act == DPRC_ACT_GELU) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q = z[e] * z[e];
+      const float s = sigmoid_f<kFast>(kGelu2C * fmaf(kGeluA * q, z[e], z[e]));
+      g[e] *= fmaf(z[e] * s * (1.f - s), kGelu2C * fmaf(3.f * kGeluA, q, 1.f), s);
+    }
+  } else if (act == DPRC_ACT_RELU) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] *= z[e] > 0.f ? 1.f : (z[e] <= 0.f ? 0.f : z[e]);
   }
-  return 1.f;
 }
 
 __device__ __forceinline__ void ld8(const float* p, float* v) {
@@ -157,10 +171,7 @@ __device__ __forceinline__ void linear_out(const LinearEpi& e, long long m, int 
       for (int j = 0; j < 8; ++j) x[j] += b[j];
     }
     if (e.Z != nullptr) st_n<T>(static_cast<T*>(e.Z) + base + n, cnt, vec, x);
-    if (e.act != DPRC_ACT_NONE) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = act_value<kFast>(x[j], e.act);
-    }
+    act_value8<kFast>(x, e.act);
     if (e.drop.thr != 0) drop8_at(x, static_cast<uint64_t>(base + n), e.drop, rk);
     if (e.res != nullptr) {
 #pragma unroll
@@ -196,10 +207,12 @@ struct GemmShape {
 // whose fp32 partial sums a second kernel adds.
 struct GemmPlan {
   int tn = 256;
+  bool pair = false;        // 256 x 256 tiles on CTA pairs
   int split = 1;
   int64_t units = 0;        // contraction units of 64 (times plane products)
   int64_t ldpart = 0;       // row stride of a partial result
   size_t part_bytes = 0;
+  double cost = 0.0;        // estimated cycles
 };
 
 GemmPlan plan_gemm(const GemmShape& g);
@@ -208,5 +221,18 @@ GemmPlan plan_gemm(const GemmShape& g);
 cudaError_t launch_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A,
                         const GemmOperand& B, dprc_dtype dt, const LinearEpi& epi, void* part,
                         cudaStream_t s);
+
+// Two products in one launch (no shares), the longer contraction first;
+// gemm_together: whether that is estimated to be faster than one by one.
+struct GemmTask {
+  const GemmShape* shape = nullptr;
+  const GemmPlan* plan = nullptr;
+  GemmOperand A, B;
+  LinearEpi epi;
+};
+bool gemm_together(const GemmShape& g0, const GemmPlan& p0, const GemmShape& g1,
+                   const GemmPlan& p1);
+cudaError_t launch_gemm_two(const GemmTask& t0, const GemmTask& t1, dprc_dtype dt,
+                            cudaStream_t s);
 
 }  // namespace dprc

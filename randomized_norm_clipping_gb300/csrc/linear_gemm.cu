@@ -16,10 +16,12 @@
 // its kTn columns (16 to 64), so the weights stream through once and the
 // tokens cost what they are; D is then stored transposed, by partial sums.
 //
-// Tiles are walked in blocks of kGroupRows row tiles, all columns of a block
-// before the next, so the tiles in flight at one time share their operands in
-// L2.
+// Tiles are walked in groups of row tiles, all columns of a group before the
+// next: as many rows as make a group about one wave where there are few
+// columns (then each row of A comes from memory once), eight otherwise, so the
+// tiles in flight at one time share their operands in L2.
 
+#include <algorithm>
 #include <atomic>
 
 #include "linear.cuh"
@@ -30,7 +32,6 @@ namespace {
 constexpr int kTm = 128;
 constexpr int kTk = 64;
 constexpr int kRing = 192 * 1024;
-constexpr int kGroupRows = 16;
 
 template <int kTn>
 struct GemmCfg {
@@ -45,10 +46,49 @@ struct GemmCfg {
   static constexpr int kSmem = kStages * kStage + 1024 + 512;
 };
 
+// One thread's bounded wait for a phase of a barrier of this CTA: like
+// mbar_wait_lim, but each try suspends the thread for up to kSuspendNs in the
+// hardware, and a warp waits with one lane (mbar_wait_warp).  Eight epilogue
+// warps polling with all lanes slowed the MMAs' shared memory down: POLLUS.
+constexpr uint32_t kSuspendNs = 20000;
+
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int code,
+                                          const volatile int* abort) {
+  if (try_wait_long(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    if (try_wait_long(bar, parity)) return true;
+    if (abort != nullptr && *abort != 0) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      record_error(code);
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int code,
+                                          const volatile int* abort) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_long(bar, parity, code, abort) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
 struct GemmArgs {
   long long rows;
   int cols;
-  int mt, nt;               // tiles
+  int mt, nt, group;        // tiles, and row tiles per group
   int split;
   int units, per_split;     // contraction units, and of one share
   int npairs;               // plane products per 64 of the contraction (1 or 6)
@@ -69,20 +109,93 @@ struct GemmUnit {
   int m, n, split, u0, u1;
 };
 
-__device__ __forceinline__ GemmUnit gemm_unit(const GemmArgs& a, long long w) {
+// The stages of a ring in turn, with the parity of the current round.  (Stage
+// and parity from a running 64-bit count, as quotient and remainder, cost the
+// copying and the issuing thread a tenth of the kernel's time: they are the
+// serial path that every stage passes.)
+template <int kStages>
+struct RingPos {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == kStages) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// Which plane products a unit is, in turn.
+struct UnitPos {
+  int kb, pair, npairs;
+  __device__ __forceinline__ UnitPos(int u, int n) : kb(n > 1 ? u / n : u), pair(0), npairs(n) {
+    if (n > 1) pair = u - kb * n;
+  }
+  __device__ __forceinline__ void next() {
+    if (++pair >= npairs) {
+      pair = 0;
+      ++kb;
+    }
+  }
+};
+
+__device__ __forceinline__ GemmUnit gemm_unit(const GemmArgs& a, int w) {
   GemmUnit g;
-  const long long tile = w / a.split;
-  g.split = static_cast<int>(w - tile * a.split);
-  const long long per_group = static_cast<long long>(kGroupRows) * a.nt;
-  const int grp = static_cast<int>(tile / per_group);
-  const int rem = static_cast<int>(tile - grp * per_group);
-  const int gr = min(kGroupRows, a.mt - grp * kGroupRows);
+  const int tile = a.split == 1 ? w : w / a.split;
+  g.split = w - tile * a.split;
+  const int per_group = a.group * a.nt;
+  const int grp = tile / per_group;
+  const int rem = tile - grp * per_group;
+  const int gr = min(a.group, a.mt - grp * a.group);
   g.n = rem / gr;
-  g.m = grp * kGroupRows + rem - g.n * gr;
+  g.m = grp * a.group + rem - g.n * gr;
   g.u0 = g.split * a.per_split;
   g.u1 = min(g.u0 + a.per_split, a.units);
   return g;
 }
+
+// kCols finished sums of one row (this thread's TMEM lane) from tb on, the
+// first of them column col0 of D: through the epilogue, or to the partial sums.
+template <typename T, int kCols>
+__device__ __forceinline__ void gemm_rows(const GemmArgs& a, const GemmUnit& g, uint32_t tb,
+                                          long long row, int col0, const RoundKeys& rk) {
+  constexpr int kStep = kCols < 32 ? kCols : 32;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kCols; c0 += kStep) {
+    const int col = col0 + c0;
+    if (col >= a.cols) break;  // uniform over the warp
+    float v[kStep];
+    tmem_ld_cols<kStep>(tb + c0, v);
+    if (row >= a.rows) continue;
+    if (a.transposed) {
+      float* out = a.part + g.split * a.part_stride + row;
+#pragma unroll
+      for (int t = 0; t < kStep; ++t)
+        if (col + t < a.cols) out[(col + t) * a.ldpart] = v[t];
+    } else if (a.part != nullptr) {
+      float* out = a.part + g.split * a.part_stride + row * a.ldpart + col;
+#pragma unroll
+      for (int t = 0; t < kStep; t += 4)
+        if (col + t < a.cols && DPRC_IN(col + t + 4 <= a.ldpart))
+          *reinterpret_cast<float4*>(out + t) = make_float4(v[t], v[t + 1], v[t + 2], v[t + 3]);
+    } else {
+      linear_out<T, kStep / 8>(a.epi, row, col, v, rk);
+    }
+  }
+}
+
+// Matrix descriptors of an operand's K = 16 steps.  K-major, 128-byte swizzle:
+// 8-row atoms 1 KB apart (SBO), a step is 32 B along the row.  MN-major: a step
+// is 16 rows of 128 B, 64-wide atoms along M or N one 8 KB box apart (LBO).
+// The address field (bits 0..13, in 16 bytes) has room for all of shared
+// memory, so stages and steps are added to it.
+struct StepDesc {
+  uint64_t base;
+  uint32_t step;
+  __device__ __forceinline__ StepDesc(uint32_t addr, bool mn)
+      : base(make_sdesc(addr, mn ? kTk * 128 : 16, 1024, kSwz128)), step(mn ? 2048 / 16 : 32 / 16) {}
+  __device__ __forceinline__ uint64_t at(uint32_t bytes) const { return base + (bytes >> 4); }
+};
 
 template <int kTn, typename T>
 __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
@@ -101,8 +214,9 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long nwork = static_cast<long long>(a.mt) * a.nt * a.split;
-  const long long mine = nwork > blockIdx.x ? (nwork - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+  const int nwork = a.mt * a.nt * a.split;  // the host checks that it fits
+  const int first = static_cast<int>(blockIdx.x), stride = static_cast<int>(gridDim.x);
+  const int mine = nwork > first ? (nwork - 1 - first) / stride + 1 : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -132,82 +246,77 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0 && mine > 0) {
-      long long it = 0;
+      RingPos<kStages> pos;
+      long long issued = 0;
       bool ok = true;
-      for (long long j = 0; j < mine && ok; ++j) {
-        const GemmUnit g = gemm_unit(a, blockIdx.x + j * gridDim.x);
-        for (int u = g.u0; u < g.u1; ++u, ++it) {
-          const int s = static_cast<int>(it % kStages);
-          const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1;
-          if (!mbar_wait_lim(&empty[s], ph ^ 1, DPRC_DEVERR_PIPE_EMPTY, kWaitLimitNs, abort_flag)) {
+      const bool a_mn = a.a_mn != 0, b_mn = a.b_mn != 0;
+      for (int j = 0; j < mine && ok; ++j) {
+        const GemmUnit g = gemm_unit(a, first + j * stride);
+        const int row = g.m * kTm, col = g.n * kTn;
+        UnitPos at(g.u0, a.npairs);
+        for (int u = g.u0; u < g.u1; ++u, pos.next(), at.next()) {
+          const int s = pos.s;
+          if (!wait_long(&empty[s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
-          int pa = 0, pb = 0, kb = u;
-          if (a.npairs > 1) {
-            kb = u / a.npairs;
-            plane_pair(u - kb * a.npairs, pa, pb);
-          }
+          int pa = 0, pb = 0;
+          if (at.npairs > 1) plane_pair(at.pair, pa, pb);
+          const int k = at.kb * kTk;
           uint8_t* sa = ring + s * Cfg::kStage;
           uint8_t* sb = sa + Cfg::kA;
           mbar_arrive_expect_tx(&full[s], Cfg::kStage);
-          if (a.a_mn) {
+          if (a_mn) {
 #pragma unroll
             for (int h = 0; h < kTm / 64; ++h)
-              tma_load_3d(sa + h * (kTk * 128), &map_a, &full[s], g.m * kTm + h * 64, kb * kTk, pa);
+              tma_load_3d(sa + h * (kTk * 128), &map_a, &full[s], row + h * 64, k, pa);
           } else {
-            tma_load_3d(sa, &map_a, &full[s], kb * kTk, g.m * kTm, pa);
+            tma_load_3d(sa, &map_a, &full[s], k, row, pa);
           }
-          if (a.b_mn) {
+          if (b_mn) {
 #pragma unroll
             for (int h = 0; h < (kTn + 63) / 64; ++h)
-              tma_load_3d(sb + h * (kTk * 128), &map_b, &full[s], g.n * kTn + h * 64, kb * kTk, pb);
+              tma_load_3d(sb + h * (kTk * 128), &map_b, &full[s], col + h * 64, k, pb);
           } else {
-            tma_load_3d(sb, &map_b, &full[s], kb * kTk, g.n * kTn, pb);
+            tma_load_3d(sb, &map_b, &full[s], k, col, pb);
           }
+          ++issued;
         }
       }
       // let the copies this thread issued land before the CTA can exit
-      for (long long k = it - 1; k >= 0 && k >= it - kStages; --k)
+      for (long long k = issued - 1; k >= 0 && k >= issued - kStages; --k)
         mbar_wait(&full[k % kStages], (k / kStages) & 1, DPRC_DEVERR_PIPE_FULL);
     }
   } else if (warp == 1) {
     if (lane == 0 && mine > 0) {
       const uint32_t idesc = make_idesc_bf16(kTm, kTn, a.a_mn != 0, a.b_mn != 0);
-      // K-major, 128-byte swizzle: 8-row atoms 1 KB apart (SBO), a K = 16 step
-      // is 32 B along the row.  MN-major: a K = 16 step is 16 rows of 128 B,
-      // 64-wide atoms along M or N one 8 KB box apart (LBO).
-      const uint32_t a_lbo = a.a_mn ? kTk * 128 : 16, a_step = a.a_mn ? 2048 : 32;
-      const uint32_t b_lbo = a.b_mn ? kTk * 128 : 16, b_step = a.b_mn ? 2048 : 32;
-      long long it = 0;
+      const StepDesc da(smem_u32(ring), a.a_mn != 0), db(smem_u32(ring) + Cfg::kA, a.b_mn != 0);
+      RingPos<kStages> pos;
       bool ok = true, issued = false;
-      for (long long j = 0; j < mine && ok; ++j) {
-        const GemmUnit g = gemm_unit(a, blockIdx.x + j * gridDim.x);
-        const int abuf = static_cast<int>(j & 1);
-        if (!mbar_wait_lim(&acce[abuf], static_cast<uint32_t>((j >> 1) & 1) ^ 1, DPRC_DEVERR_ACCUM,
-                           kWaitLimitNs, abort_flag)) {
+      for (int j = 0; j < mine && ok; ++j) {
+        const GemmUnit g = gemm_unit(a, first + j * stride);
+        const int abuf = j & 1;
+        if (!wait_long(&acce[abuf], static_cast<uint32_t>((j >> 1) & 1) ^ 1, DPRC_DEVERR_ACCUM,
+                       abort_flag)) {
           *abort_flag = 1;
           break;
         }
         tc_fence_after();
-        for (int u = g.u0; u < g.u1; ++u, ++it) {
-          const int s = static_cast<int>(it % kStages);
-          const uint32_t ph = static_cast<uint32_t>(it / kStages) & 1;
-          if (!mbar_wait_lim(&full[s], ph, DPRC_DEVERR_PIPE_FULL, kWaitLimitNs, abort_flag)) {
+        const uint32_t acc = tmem + abuf * kTn;
+        for (int u = g.u0; u < g.u1; ++u, pos.next()) {
+          const int s = pos.s;
+          if (!wait_long(&full[s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(ring + s * Cfg::kStage);
-          const uint32_t sb = sa + Cfg::kA;
+          const uint64_t ad = da.at(s * Cfg::kStage), bd = db.at(s * Cfg::kStage);
 #pragma unroll
-          for (int kk = 0; kk < kTk / 16; ++kk) {
-            const uint64_t ad = make_sdesc(sa + kk * a_step, a_lbo, 1024, kSwz128);
-            const uint64_t bd = make_sdesc(sb + kk * b_step, b_lbo, 1024, kSwz128);
-            umma_bf16(tmem + abuf * kTn, ad, bd, idesc, (u == g.u0 && kk == 0) ? 0u : 1u);
-          }
+          for (int kk = 0; kk < kTk / 16; ++kk)
+            umma_bf16(acc, ad + kk * da.step, bd + kk * db.step, idesc,
+                      (u == g.u0 && kk == 0) ? 0u : 1u);
           umma_commit(&empty[s]);
           issued = true;
         }
@@ -221,43 +330,17 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
     const int c_lo = (ew >> 2) * Cfg::kCols;
     const RoundKeys rk = round_keys(a.epi.drop.seed);
     bool ok = true;
-    for (long long j = 0; j < mine; ++j) {
-      const GemmUnit g = gemm_unit(a, blockIdx.x + j * gridDim.x);
-      const int abuf = static_cast<int>(j & 1);
-      bool live = ok && mbar_wait_lim(&accf[abuf], static_cast<uint32_t>((j >> 1) & 1),
-                                      DPRC_DEVERR_ACCUM, kWaitLimitNs, abort_flag) &&
-                  *abort_flag == 0;
-      live = __all_sync(0xffffffffu, live);
+    for (int j = 0; j < mine; ++j) {
+      const GemmUnit g = gemm_unit(a, first + j * stride);
+      const int abuf = j & 1;
+      const bool live = ok && wait_warp(&accf[abuf], static_cast<uint32_t>((j >> 1) & 1),
+                                        DPRC_DEVERR_ACCUM, abort_flag);
       if (!live) ok = false;
       tc_fence_after();
       if (live) {
         const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + abuf * kTn + c_lo;
         const long long row = static_cast<long long>(g.m) * kTm + q * 32 + lane;
-        constexpr int kStep = Cfg::kCols < 32 ? Cfg::kCols : 32;
-#pragma unroll 1
-        for (int c0 = 0; c0 < Cfg::kCols; c0 += kStep) {
-          const int col = g.n * kTn + c_lo + c0;
-          if (col >= a.cols) break;  // uniform over the warp
-          float v[kStep];
-          tmem_ld_cols<kStep>(tb + c0, v);
-          if (row < a.rows) {
-            if (a.transposed) {
-              float* out = a.part + g.split * a.part_stride + row;
-#pragma unroll
-              for (int t = 0; t < kStep; ++t)
-                if (col + t < a.cols) out[(col + t) * a.ldpart] = v[t];
-            } else if (a.part != nullptr) {
-              float* out = a.part + g.split * a.part_stride + row * a.ldpart + col;
-#pragma unroll
-              for (int t = 0; t < kStep; t += 4)
-                if (col + t < a.cols && DPRC_IN(col + t + 4 <= a.ldpart))
-                  *reinterpret_cast<float4*>(out + t) =
-                      make_float4(v[t], v[t + 1], v[t + 2], v[t + 3]);
-            } else {
-              linear_out<T, kStep / 8>(a.epi, row, col, v, rk);
-            }
-          }
-        }
+        gemm_rows<T, Cfg::kCols>(a, g, tb, row, g.n * kTn + c_lo, rk);
       }
       tc_fence_before();
       __syncwarp();
@@ -274,21 +357,329 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
   }
 }
 
-template <int kTn, typename T>
-cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a,
-                          cudaStream_t s) {
-  using Cfg = GemmCfg<kTn>;
+// Allows a kernel its shared memory, once per device; kTag: one per kernel.
+template <int kTag, typename F>
+cudaError_t set_smem_once(F* kernel, int bytes) {
   constexpr int kMaxDev = 64;
   static std::atomic<int> done[kMaxDev];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDev || !done[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(linear_gemm_kernel<kTn, T>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDev) done[dev].store(1, std::memory_order_release);
+  if (dev >= 0 && dev < kMaxDev && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < kMaxDev) done[dev].store(1, std::memory_order_release);
+  return e;
+}
+
+// ---------------------------------------------------------------------------
+// CTA pairs: two SMs on one 256 x 256 tile (cta_group::2).  Each CTA of a pair
+// holds 128 rows of A and 128 columns of B of a stage, and the accumulator of
+// its 128 rows; the leader (rank 0) issues the MMAs, which read both CTAs'
+// shared memory.  A stage is 32 KB per SM instead of 48 KB for the same MMA
+// time, which is what the single-CTA tile was bound by: copies into shared
+// memory.
+//
+// Barriers: full[s] lives in the leader and counts both CTAs' bytes; empty[s]
+// and accf[b] are signalled in both CTAs by the leader's commits; acce[b] lives
+// in the leader and counts both CTAs' epilogue warps.
+// ---------------------------------------------------------------------------
+constexpr int kPairTile = 256;
+constexpr double kPairStep = 600.0;  // cycles of a 64-deep step
+constexpr int kPairA = kTm * kTk * 2;
+constexpr int kPairStage = 2 * kPairA;
+constexpr int kPairStages = 7;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kPairSmem = kPairStages * kPairStage + 1024 + 512;
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst_smem)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs once every MMA issued so
+// far by this thread has completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// A tile copy whose bytes count on the barrier at `bar` (shared::cluster
+// address, in either CTA of the pair).
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
+                                                 int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// One or two products in a launch.  The first one's units go round the pairs;
+// those that got one unit more of them (the first `extra` pairs) take the
+// first extra * a_units units of the second product, the other pairs the rest,
+// a_units chosen on the host so that both finish together.
+struct GemmBatch {
+  GemmArgs p[2];
+  int n0, n1;  // units
+  int extra, a_units;
+};
+
+struct PairWork {
+  int mine0, mine1;
+  int first0, step0, first1, step1;
+  __device__ __forceinline__ int at(int j) const {
+    return j < mine0 ? first0 + j * step0 : first1 + (j - mine0) * step1;
   }
+};
+
+__device__ __forceinline__ PairWork pair_work(const GemmBatch& b, int me, int pairs) {
+  PairWork w;
+  w.first0 = me;
+  w.step0 = pairs;
+  w.mine0 = b.n0 > me ? (b.n0 - 1 - me) / pairs + 1 : 0;
+  const int cut = min(b.extra * b.a_units, b.n1);
+  const bool ahead = me < b.extra;
+  w.first1 = ahead ? me : cut + me - b.extra;
+  w.step1 = ahead ? b.extra : pairs - b.extra;
+  const int end = ahead ? cut : b.n1;
+  w.mine1 = end > w.first1 ? (end - 1 - w.first1) / w.step1 + 1 : 0;
+  return w;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+    linear_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a0,
+                            const __grid_constant__ CUtensorMap map_b0,
+                            const __grid_constant__ CUtensorMap map_a1,
+                            const __grid_constant__ CUtensorMap map_b1,
+                            const __grid_constant__ GemmBatch batch) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = align_1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kPairStages * kPairStage);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* accf = empty + kPairStages;  // [2]
+  uint64_t* acce = accf + 2;             // [2]
+  uint64_t* drain = acce + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  if (cluster_nctarank() != 2) {  // a launch of another shape has no peer to address
+    if (threadIdx.x == 0) record_error(DPRC_DEVERR_LAUNCH);
+    return;
+  }
+  const int pairs = static_cast<int>(gridDim.x) / 2, me = static_cast<int>(blockIdx.x) / 2;
+  const PairWork work = pair_work(batch, me, pairs);
+  const int mine = work.mine0 + work.mine1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accf[b], 1);
+      mbar_init(&acce[b], 2 * kPairEpiWarps);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&map_a0);
+    tma_prefetch_desc(&map_b0);
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0 && mine > 0) {
+      RingPos<kPairStages> pos;
+      long long issued = 0;
+      bool ok = true;
+      const uint32_t full0 = map_to_rank(full, 0);
+      for (int j = 0; j < mine && ok; ++j) {
+        const GemmArgs& a = batch.p[j >= work.mine0];
+        const CUtensorMap* map_a = j >= work.mine0 ? &map_a1 : &map_a0;
+        const CUtensorMap* map_b = j >= work.mine0 ? &map_b1 : &map_b0;
+        const GemmUnit g = gemm_unit(a, work.at(j));
+        const int row = g.m * kPairTile + rank * kTm, col = g.n * kPairTile + rank * kTm;
+        const bool a_mn = a.a_mn != 0, b_mn = a.b_mn != 0;
+        UnitPos at(g.u0, a.npairs);
+        for (int u = g.u0; u < g.u1; ++u, pos.next(), at.next()) {
+          const int s = pos.s;
+          if (!wait_long(&empty[s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          int pa = 0, pb = 0;
+          if (at.npairs > 1) plane_pair(at.pair, pa, pb);
+          const int k = at.kb * kTk;
+          uint8_t* sa = ring + s * kPairStage;
+          uint8_t* sb = sa + kPairA;
+          const uint32_t bar = full0 + s * 8;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStage);
+          if (a_mn) {
+            tma_load_3d_pair(sa, map_a, bar, row, k, pa);
+            tma_load_3d_pair(sa + kTk * 128, map_a, bar, row + 64, k, pa);
+          } else {
+            tma_load_3d_pair(sa, map_a, bar, k, row, pa);
+          }
+          if (b_mn) {
+            tma_load_3d_pair(sb, map_b, bar, col, k, pb);
+            tma_load_3d_pair(sb + kTk * 128, map_b, bar, col + 64, k, pb);
+          } else {
+            tma_load_3d_pair(sb, map_b, bar, k, col, pb);
+          }
+          ++issued;
+        }
+      }
+      // let both CTAs' copies land before either can exit (the closing
+      // cluster barrier holds the other one)
+      if (rank == 0)
+        for (long long k = issued - 1; k >= 0 && k >= issued - kPairStages; --k)
+          mbar_wait(&full[k % kPairStages], (k / kPairStages) & 1, DPRC_DEVERR_PIPE_FULL);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0 && mine > 0) {
+      RingPos<kPairStages> pos;
+      bool ok = true, issued = false;
+      for (int j = 0; j < mine && ok; ++j) {
+        const GemmArgs& a = batch.p[j >= work.mine0];
+        const uint32_t idesc = make_idesc_bf16(kPairTile, kPairTile, a.a_mn != 0, a.b_mn != 0);
+        const StepDesc da(smem_u32(ring), a.a_mn != 0);
+        const StepDesc db(smem_u32(ring) + kPairA, a.b_mn != 0);
+        const GemmUnit g = gemm_unit(a, work.at(j));
+        const int abuf = j & 1;
+        if (!wait_long(&acce[abuf], static_cast<uint32_t>((j >> 1) & 1) ^ 1,
+                       DPRC_DEVERR_ACCUM, abort_flag)) {
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = tmem + abuf * kPairTile;
+        for (int u = g.u0; u < g.u1; ++u, pos.next()) {
+          const int s = pos.s;
+          if (!wait_long(&full[s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = da.at(s * kPairStage), bd = db.at(s * kPairStage);
+#pragma unroll
+          for (int kk = 0; kk < kTk / 16; ++kk)
+            umma_bf16_pair(acc, ad + kk * da.step, bd + kk * db.step, idesc,
+                           (u == g.u0 && kk == 0) ? 0u : 1u);
+          umma_commit_pair(&empty[s]);
+          issued = true;
+        }
+        if (ok) umma_commit_pair(&accf[abuf]);
+      }
+      if (issued) {
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                smem_u32(drain))
+            : "memory");
+        mbar_wait_lim(drain, 0, DPRC_DEVERR_ACCUM, kWaitLimitNs, nullptr);
+      }
+    }
+  } else {
+    const int ew = warp - 2;
+    const int q = warp & 3;  // TMEM lane quadrant this warp may read
+    const int c_lo = (ew >> 2) * kTm;
+    const RoundKeys rk = round_keys(batch.p[0].epi.drop.seed);  // a pair of problems drops nothing
+    bool ok = true;
+    for (int j = 0; j < mine; ++j) {
+      const GemmArgs& a = batch.p[j >= work.mine0];
+      const GemmUnit g = gemm_unit(a, work.at(j));
+      const int abuf = j & 1;
+      const bool live = ok && wait_warp(&accf[abuf], static_cast<uint32_t>((j >> 1) & 1),
+                                        DPRC_DEVERR_ACCUM, abort_flag);
+      if (!live) ok = false;
+      tc_fence_after();
+      if (live) {
+        const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + abuf * kPairTile + c_lo;
+        const long long row =
+            static_cast<long long>(g.m) * kPairTile + rank * kTm + q * 32 + lane;
+        gemm_rows<T, kTm>(a, g, tb, row, g.n * kPairTile + c_lo, rk);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(map_to_rank(&acce[abuf], 0));
+    }
+  }
+
+  __syncwarp();  // reconverge each warp before the cluster barrier
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <typename T>
+cudaError_t launch_gemm_pair(const CUtensorMap* maps, const GemmBatch& batch, cudaStream_t s) {
+  const cudaError_t e = set_smem_once<2 + sizeof(T)>(linear_gemm_pair_kernel<T>, kPairSmem);
+  if (e != cudaSuccess) return e;
+  const long long pairs = std::min<long long>(static_cast<long long>(batch.n0) + batch.n1, device_sm_count() / 2);
+  linear_gemm_pair_kernel<T><<<static_cast<unsigned>(2 * pairs), kPairThreads, kPairSmem, s>>>(
+      maps[0], maps[1], maps[2], maps[3], batch);
+  return cudaGetLastError();
+}
+
+// How the second product's units are dealt (GemmBatch), and the busiest pair's
+// load: units of u0 and u1 steps.
+long long deal_units(long long n0, int u0, long long n1, int u1, long long pairs, int& extra,
+                     int& a_units) {
+  extra = static_cast<int>(n0 % pairs);
+  const long long base = n0 / pairs;
+  a_units = 0;
+  long long best = -1;
+  for (int a = 0; a <= (extra > 0 ? 4096 : 0); ++a) {
+    const long long rest = std::max<long long>(n1 - static_cast<long long>(extra) * a, 0);
+    const long long b = (rest + pairs - extra - 1) / (pairs - extra);
+    const long long load = std::max((base + 1) * u0 * (extra > 0) + static_cast<long long>(a) * u1,
+                                    base * u0 + b * u1);
+    if (best < 0 || load < best) {
+      best = load;
+      a_units = a;
+    }
+    if (rest == 0) break;
+  }
+  return best;
+}
+
+template <int kTn, typename T>
+cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a,
+                          cudaStream_t s) {
+  using Cfg = GemmCfg<kTn>;
+  cudaError_t e = set_smem_once<kTn * 8 + sizeof(T)>(linear_gemm_kernel<kTn, T>, Cfg::kSmem);
+  if (e != cudaSuccess) return e;
   const long long work = static_cast<long long>(a.mt) * a.nt * a.split;
   const long long grid = work < device_sm_count() ? work : device_sm_count();
   linear_gemm_kernel<kTn, T>
@@ -329,33 +720,41 @@ GemmPlan plan_gemm(const GemmShape& g) {
   GemmPlan p;
   p.units = (g.K + kTk - 1) / kTk * (g.planes > 1 ? 6 : 1);
   const int sms = device_sm_count();
-  const int64_t mt = (g.rows + kTm - 1) / kTm;
-  // Candidates: the tile widths and contraction shares; the cost of one is its
-  // waves of units (in cycles: a 64-deep step of a 128 x tn tile takes about
-  // 2 tn cycles on the tensor core and no less than 192 to copy in), plus
-  // what a unit costs outside its MMAs, plus the partial sums' way out and in.
-  const int wide[] = {256, 128, 64};
-  const int few[] = {16, 32, 64};
+  // Candidates: the tile shapes and contraction shares; the cost of one is its
+  // waves of units (in cycles of a 64-deep step, measured: the pair's step runs
+  // at the tensor core's rate, the single CTA's steps at that of the copies
+  // into shared memory), plus what a unit costs outside its MMAs, plus the
+  // partial sums' way out and in.
+  struct Shape {
+    int tm, tn, ctas;
+    double step;
+  };
+  const Shape wide[] = {{256, 256, 2, kPairStep}, {128, 256, 1, 632.0}, {128, 128, 1, 450.0},
+                        {128, 64, 1, 260.0}};
+  const Shape few[] = {{128, 16, 1, 200.0}, {128, 32, 1, 210.0}, {128, 64, 1, 260.0}};
+  const Shape* shapes = g.transposed ? few : wide;
+  const int nshapes = g.transposed ? 3 : 4;
   double best = 1e300;
-  for (int i = 0; i < 3; ++i) {
-    int tn = g.transposed ? few[i] : wide[i];
-    if (g.transposed && i < 2 && g.cols > tn) continue;
-    const int64_t nt = (g.cols + tn - 1) / tn;
-    const int64_t tiles = mt * nt;
+  for (int i = 0; i < nshapes; ++i) {
+    const Shape& sh = shapes[i];
+    if (g.transposed && i < 2 && g.cols > sh.tn) continue;
+    const int64_t tiles = (g.rows + sh.tm - 1) / sh.tm * ((g.cols + sh.tn - 1) / sh.tn);
+    const int64_t slots = sms / sh.ctas;
     const int64_t max_split = p.units < 4 ? 1 : (p.units / 4 < 64 ? p.units / 4 : 64);
     for (int64_t want = 1; want <= max_split; ++want) {
       const int64_t per = (p.units + want - 1) / want;
       const int64_t split = (p.units + per - 1) / per;
       if (split != want) continue;
-      const int64_t waves = (tiles * split + sms - 1) / sms;
-      const double step = tn >= 96 ? 2.0 * tn : 192.0;
-      double cost = static_cast<double>(waves) * (per * step + 200.0) + 2.0 * tn * 4.0;
+      const int64_t waves = (tiles * split + slots - 1) / slots;
+      double cost = static_cast<double>(waves) * (per * sh.step + 200.0) + 8.0 * sh.tn;
       const bool partial = split > 1 || g.transposed;
       if (partial)  // written and read through L2 at some 5 KB a cycle, and a launch
         cost += 3000.0 + static_cast<double>(split) * g.rows * g.cols * 8.0 / 5000.0;
       if (cost < best) {
         best = cost;
-        p.tn = tn;
+        p.cost = cost;
+        p.tn = sh.tn;
+        p.pair = sh.ctas == 2;
         p.split = static_cast<int>(split);
       }
       if (tiles * split >= 4 * static_cast<int64_t>(sms)) break;
@@ -370,18 +769,25 @@ GemmPlan plan_gemm(const GemmShape& g) {
   return p;
 }
 
-cudaError_t launch_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A,
-                        const GemmOperand& B, dprc_dtype dt, const LinearEpi& epi, void* part,
-                        cudaStream_t s) {
+namespace {
+long long unit_count(const GemmArgs& a) {
+  return static_cast<long long>(a.mt) * a.nt * a.split;
+}
+
+cudaError_t prepare_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A,
+                         const GemmOperand& B, const LinearEpi& epi, void* part, CUtensorMap* maps,
+                         GemmArgs& a) {
   if (B.mn_major && p.tn < 64) return cudaErrorInvalidValue;  // its boxes are 64 wide
-  CUtensorMap ma, mb;
-  if (!operand_map(&ma, A, g.rows, g.K, g.planes, kTm)) return cudaErrorInvalidValue;
-  if (!operand_map(&mb, B, g.cols, g.K, g.planes, p.tn)) return cudaErrorInvalidValue;
-  GemmArgs a;
+  const int tile_m = p.pair ? kPairTile : kTm, tile_n = p.pair ? kPairTile : p.tn;
+  if (!operand_map(&maps[0], A, g.rows, g.K, g.planes, kTm)) return cudaErrorInvalidValue;
+  if (!operand_map(&maps[1], B, g.cols, g.K, g.planes, p.pair ? kTm : p.tn))
+    return cudaErrorInvalidValue;
   a.rows = g.rows;
   a.cols = static_cast<int>(g.cols);
-  a.mt = static_cast<int>((g.rows + kTm - 1) / kTm);
-  a.nt = static_cast<int>((g.cols + p.tn - 1) / p.tn);
+  a.mt = static_cast<int>((g.rows + tile_m - 1) / tile_m);
+  a.nt = static_cast<int>((g.cols + tile_n - 1) / tile_n);
+  const int wave = device_sm_count() / (p.pair ? 2 : 1);
+  a.group = std::max(8, (wave + a.nt - 1) / a.nt);
   a.split = p.split;
   a.units = static_cast<int>(p.units);
   a.per_split = static_cast<int>((p.units + p.split - 1) / p.split);
@@ -393,8 +799,69 @@ cudaError_t launch_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand
   a.ldpart = p.ldpart;
   a.part_stride = (g.transposed ? g.cols : g.rows) * p.ldpart;
   a.epi = epi;
-  return dt == DPRC_F32 ? launch_gemm_tn<float>(p.tn, ma, mb, a, s)
-                        : launch_gemm_tn<__nv_bfloat16>(p.tn, ma, mb, a, s);
+  return unit_count(a) < (int64_t(1) << 30) ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A,
+                        const GemmOperand& B, dprc_dtype dt, const LinearEpi& epi, void* part,
+                        cudaStream_t s) {
+  CUtensorMap maps[4];
+  if (p.pair) {
+    GemmBatch batch;
+    const cudaError_t e = prepare_gemm(g, p, A, B, epi, part, maps, batch.p[0]);
+    if (e != cudaSuccess) return e;
+    batch.p[1] = batch.p[0];
+    maps[2] = maps[0];
+    maps[3] = maps[1];
+    batch.n0 = static_cast<int>(unit_count(batch.p[0]));
+    batch.n1 = batch.extra = batch.a_units = 0;
+    return dt == DPRC_F32 ? launch_gemm_pair<float>(maps, batch, s)
+                          : launch_gemm_pair<__nv_bfloat16>(maps, batch, s);
+  }
+  GemmArgs a;
+  const cudaError_t e = prepare_gemm(g, p, A, B, epi, part, maps, a);
+  if (e != cudaSuccess) return e;
+  return dt == DPRC_F32 ? launch_gemm_tn<float>(p.tn, maps[0], maps[1], a, s)
+                        : launch_gemm_tn<__nv_bfloat16>(p.tn, maps[0], maps[1], a, s);
+}
+
+// The cheaper of two products one after the other and both in one launch.
+bool gemm_together(const GemmShape& g0, const GemmPlan& p0, const GemmShape& g1,
+                   const GemmPlan& p1) {
+  if (g0.transposed || g1.transposed) return false;
+  const auto tiles = [](const GemmShape& g) {
+    return (g.rows + kPairTile - 1) / kPairTile * ((g.cols + kPairTile - 1) / kPairTile);
+  };
+  if (tiles(g0) + tiles(g1) < device_sm_count() / 2) return false;  // shares fill the GPU better
+  int extra, a_units;
+  const long long load =
+      deal_units(tiles(g0), static_cast<int>(p0.units), tiles(g1), static_cast<int>(p1.units),
+                 device_sm_count() / 2, extra, a_units);
+  return load * kPairStep + 2048.0 < p0.cost + p1.cost;
+}
+
+cudaError_t launch_gemm_two(const GemmTask& t0, const GemmTask& t1, dprc_dtype dt,
+                            cudaStream_t s) {
+  CUtensorMap maps[4];
+  GemmBatch batch;
+  const GemmTask* t[2] = {&t0, &t1};
+  for (int i = 0; i < 2; ++i) {
+    GemmPlan p;
+    p.pair = true;
+    p.units = t[i]->plan->units;
+    const cudaError_t e = prepare_gemm(*t[i]->shape, p, t[i]->A, t[i]->B, t[i]->epi, nullptr,
+                                       maps + 2 * i, batch.p[i]);
+    if (e != cudaSuccess) return e;
+  }
+  batch.n0 = static_cast<int>(unit_count(batch.p[0]));
+  batch.n1 = static_cast<int>(unit_count(batch.p[1]));
+  const long long pairs = std::min<long long>(static_cast<long long>(batch.n0) + batch.n1, device_sm_count() / 2);
+  deal_units(batch.n0, batch.p[0].units, batch.n1, batch.p[1].units, pairs, batch.extra,
+             batch.a_units);
+  return dt == DPRC_F32 ? launch_gemm_pair<float>(maps, batch, s)
+                        : launch_gemm_pair<__nv_bfloat16>(maps, batch, s);
 }
 
 }  // namespace dprc
