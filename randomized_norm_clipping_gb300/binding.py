@@ -497,16 +497,40 @@ DPRC_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 _U64 = 2**64 - 1
 
 
-def _same(name, t, dtype, shape=None, device=None):
-    """An optional tensor of the call's dtype (and shape and device)."""
-    if t is None:
+_scratch_kept = threading.local()
+_SCRATCH_KEEP = 64 << 20  # larger workspaces are allocated per call
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
+
+
+def _scratch(nbytes, device, stream):
+    """A device workspace of nbytes for one call without a ws argument: kept
+    per host thread, device and stream (calls of one thread on one stream run
+    one after the other) and grown as needed, so that a call does not pay for
+    an allocation.  Large ones, and any during a graph capture (which owns what
+    it allocates), are allocated fresh."""
+    if nbytes > _SCRATCH_KEEP or _capturing is None or _capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    kept = _scratch_kept.__dict__
+    key = (device.index, stream.value)
+    have = kept.get(key)
+    if have is None or have[-1].numel() < nbytes:
+        size = 1 << max(16, (nbytes - 1).bit_length())
+        # outgrown buffers stay: work on the stream may still use them
+        have = (have or ()) + (torch.empty(size, dtype=torch.uint8, device=device),)
+        kept[key] = have
+    return have[-1]
+
+
+def _same(name, t, dtype, shape, device):
+    """An optional tensor of the call's dtype, shape and device."""
+    if t is None or (t.dtype is dtype and t.device == device
+                     and (shape is None or t.shape == shape)):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, the call's tensors are {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} is needed")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's tensors are on {device}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} is needed")
 
 
 def _token_bytes(tokens):
@@ -558,41 +582,42 @@ def dprc_embed_plan(tokens, V, buf=None, stream=None):
     return EmbedPlan(B, T, int(V), buf)
 
 
-def _embed_ws(G, plan, ws):
+def _embed_ws(G, plan, ws, stream):
     if G.dim() != 3 or G.shape[0] != plan.B or G.shape[1] != plan.T:
         raise ValueError(f"G has shape {tuple(G.shape)}, the plan is of {plan.B} x {plan.T} tokens")
     if ws is None:
         n = lib().dprc_embed_workspace_bytes(_dtype_code(G), plan.B, plan.T, G.shape[2])
         if n == 0:
             raise DprcError("dprc_embed_workspace_bytes", 2)
-        ws = torch.empty(n, dtype=torch.uint8, device=G.device)
+        ws = _scratch(n, G.device, stream)
     return ws
 
 
 def dprc_embed_norm(G, plan, n, scale=1.0, accumulate=False, ws=None, stream=None):
     """n[i] (+)= scale^2 sum_v ||sum_{t: tok_it = v} G_it||^2, exactly."""
-    ws = _embed_ws(G, plan, ws)
     _need_cuda(G, n, ws, plan.buf)
     _same("n", n, torch.float32, (plan.B,), G.device)
+    st = _stream(G, stream)
+    ws = _embed_ws(G, plan, ws, st)
     _check("dprc_embed_norm",
            lib().dprc_embed_norm(G.data_ptr(), _dtype_code(G), plan.B, plan.T, plan.V, G.shape[2],
                                  scale, plan.buf.data_ptr(), plan.buf.numel(), n.data_ptr(),
-                                 int(bool(accumulate)), ws.data_ptr(), ws.numel(),
-                                 _stream(G, stream)))
+                                 1 if accumulate else 0, ws.data_ptr(), ws.numel(), st))
     return n
 
 
 def dprc_embed_grad(G, plan, dW, c=None, scale=1.0, accumulate=False, ws=None, stream=None):
     """dW[v] (+)= scale sum_i c[i] sum_{t: tok_it = v} G_it (c None: all 1)."""
-    ws = _embed_ws(G, plan, ws)
     _need_cuda(G, dW, c, ws, plan.buf)
     _same("dW", dW, G.dtype, (plan.V, G.shape[2]), G.device)
     _same("c", c, torch.float32, (plan.B,), G.device)
+    st = _stream(G, stream)
+    ws = _embed_ws(G, plan, ws, st)
     _check("dprc_embed_grad",
            lib().dprc_embed_grad(G.data_ptr(), _dtype_code(G), _ptr(c), plan.B, plan.T, plan.V,
                                  G.shape[2], scale, plan.buf.data_ptr(), plan.buf.numel(),
-                                 dW.data_ptr(), int(bool(accumulate)), ws.data_ptr(), ws.numel(),
-                                 _stream(G, stream)))
+                                 dW.data_ptr(), 1 if accumulate else 0, ws.data_ptr(), ws.numel(),
+                                 st))
     return dW
 
 
@@ -611,12 +636,12 @@ def dprc_dropout(x, p, seed, step, residual=None, first_element=0, out=None, str
     return out
 
 
-def _linear_ws(like, M, K, N, grad, ws):
+def _linear_ws(like, M, K, N, grad, ws, stream):
     if ws is None:
         n = lib().dprc_linear_workspace_bytes(_dtype_code(like), M, K, N, grad)
         if n == 0:
             raise DprcError("dprc_linear_workspace_bytes", 2)
-        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+        ws = _scratch(n, like.device, stream)
     return ws
 
 
@@ -629,21 +654,22 @@ def dprc_linear(X, W, bias=None, act="none", p=0.0, seed=0, step=0, residual=Non
         raise ValueError(f"X has width {X.shape[-1]}, W {K}")
     shape = (*X.shape[:-1], N)
     M = X.numel() // K
-    if out is None:
-        out = torch.empty(shape, dtype=X.dtype, device=X.device)
-    ws = _linear_ws(X, M, K, N, 0, ws)
-    _need_cuda(X, W, bias, residual, Z, out, ws)
     dt, dev = X.dtype, X.device
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+    _need_cuda(X, W, bias, residual, Z, out, ws)
     _same("W", W, dt, None, dev)
     _same("bias", bias, dt, (N,), dev)
     _same("residual", residual, dt, shape, dev)
     _same("Z", Z, dt, shape, dev)
     _same("out", out, dt, shape, dev)
+    st = _stream(X, stream)
+    ws = _linear_ws(X, M, K, N, 0, ws, st)
     _check("dprc_linear",
            lib().dprc_linear(X.data_ptr(), W.data_ptr(), _ptr(bias), _ptr(residual),
                              _dtype_code(X), M, K, N, DPRC_ACTS[act], p, int(seed) & _U64,
                              int(step) & _U64, _ptr(Z), out.data_ptr(), ws.data_ptr(), ws.numel(),
-                             _stream(X, stream)))
+                             st))
     return out
 
 
@@ -653,21 +679,22 @@ def dprc_linear_grad(dY, X, W, Z=None, act="none", p=0.0, seed=0, step=0, dX=Non
     dZ [..., N] that are given (act, p, seed, step as in its call)."""
     N, K = W.shape
     M = dY.numel() // N
-    lead = tuple(dY.shape[:-1])
-    ws = _linear_ws(dY, M, K, N, 1, ws)
-    _need_cuda(dY, X, W, Z, dX, dW, db, dZ, ws)
+    lead = dY.shape[:-1]
     dt, dev = dY.dtype, dY.device
     if dY.shape[-1] != N:
         raise ValueError(f"dY has width {dY.shape[-1]}, W {N} rows")
+    _need_cuda(dY, X, W, Z, dX, dW, db, dZ, ws)
     _same("X", X, dt, (*lead, K), dev)
     _same("W", W, dt, None, dev)
-    _same("Z", Z, dt, (*lead, N), dev)
+    _same("Z", Z, dt, dY.shape, dev)
     _same("dX", dX, dt, (*lead, K), dev)
     _same("dW", dW, dt, (N, K), dev)
     _same("db", db, dt, (N,), dev)
-    _same("dZ", dZ, dt, (*lead, N), dev)
+    _same("dZ", dZ, dt, dY.shape, dev)
+    st = _stream(dY, stream)
+    ws = _linear_ws(dY, M, K, N, 1, ws, st)
     _check("dprc_linear_grad",
            lib().dprc_linear_grad(dY.data_ptr(), _ptr(X), W.data_ptr(), _ptr(Z), _dtype_code(dY),
                                   M, K, N, DPRC_ACTS[act], p, int(seed) & _U64, int(step) & _U64,
                                   _ptr(dX), _ptr(dW), _ptr(db), _ptr(dZ), ws.data_ptr(),
-                                  ws.numel(), _stream(dY, stream)))
+                                  ws.numel(), st))

@@ -194,8 +194,20 @@ __global__ void __launch_bounds__(32 * kRankWarps)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int padded = (N + 127) / 128 * 128;
   pdl_launch_dependents();
-  for (int j = threadIdx.x; j < padded; j += 32 * kRankWarps)
-    s_key[j] = j < N ? token_key(tokens[j], V) : 0xFFFFFFFFu;  // before no entry
+  // (loads first: the error word's atomic keeps them from being moved up)
+  for (int j0 = threadIdx.x; j0 < padded; j0 += 8 * 32 * kRankWarps) {
+    TOK t[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = j0 + u * 32 * kRankWarps;
+      t[u] = j < N ? __ldg(tokens + j) : TOK(0);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int j = j0 + u * 32 * kRankWarps;
+      if (j < padded) s_key[j] = j < N ? token_key(t[u], V) : 0xFFFFFFFFu;  // before no entry
+    }
+  }
   __syncthreads();
   const int i0 = (static_cast<int>(blockIdx.x) * kRankWarps + warp) * kRankPer;
   if (i0 >= N) return;
@@ -267,16 +279,27 @@ constexpr int kSortMaxTiles = 128;
 struct SortArgs {
   int N, per;        // entries; of one warp
   int V, shift, bits;
-  const uint32_t* key_in;  // null in the first pass: the tokens themselves
-  const int* pos_in;
+  const int* pos_in;       // null in the first pass
   uint32_t* key_out;
   int* pos_out;
   int* counts;       // [tiles][digits]
 };
 
+// kSortBatch keys, `step` entries apart from i0 on (0 past hi): all loads
+// before the first use.  TOK uint32_t: keys; else tokens.
 template <typename TOK>
-__device__ __forceinline__ uint32_t sort_key(const TOK* tokens, const SortArgs& a, int i) {
-  return a.key_in == nullptr ? token_key(tokens[i], a.V) : __ldg(a.key_in + i);
+__device__ __forceinline__ void sort_keys(const TOK* src, int V, int i0, int step, int hi,
+                                          uint32_t* k) {
+  TOK t[kSortBatch];
+#pragma unroll
+  for (int j = 0; j < kSortBatch; ++j) t[j] = i0 + j * step < hi ? __ldg(src + i0 + j * step) : TOK(0);
+#pragma unroll
+  for (int j = 0; j < kSortBatch; ++j) {
+    if constexpr (sizeof(TOK) == 4 && TOK(-1) > TOK(0))
+      k[j] = t[j];
+    else
+      k[j] = token_key(t[j], V);
+  }
 }
 
 // The lanes with this lane's digit, one vote per bit (the match instruction
@@ -294,7 +317,7 @@ __device__ __forceinline__ uint32_t equal_lanes(uint32_t digit, bool live) {
 
 template <typename TOK>
 __global__ void __launch_bounds__(kSortThreads)
-    token_count_kernel(const TOK* __restrict__ tokens, const SortArgs a) {
+    token_count_kernel(const TOK* __restrict__ src, const SortArgs a) {
   __shared__ int s_hist[1 << kSortMaxBits];
   pdl_launch_dependents();
   const int nd = 1 << a.bits;
@@ -305,11 +328,7 @@ __global__ void __launch_bounds__(kSortThreads)
   const int hi = min(lo + kSortWarps * a.per, a.N);
   for (int i0 = lo; i0 < hi; i0 += kSortTile) {
     uint32_t k[kSortBatch];
-#pragma unroll
-    for (int j = 0; j < kSortBatch; ++j) {
-      const int i = i0 + j * kSortThreads + threadIdx.x;
-      k[j] = i < hi ? sort_key(tokens, a, i) : 0u;
-    }
+    sort_keys(src, a.V, i0 + static_cast<int>(threadIdx.x), kSortThreads, hi, k);
 #pragma unroll
     for (int j = 0; j < kSortBatch; ++j) {
       const int i = i0 + j * kSortThreads + threadIdx.x;
@@ -323,7 +342,7 @@ __global__ void __launch_bounds__(kSortThreads)
 
 template <typename TOK>
 __global__ void __launch_bounds__(kSortThreads)
-    token_scatter_kernel(const TOK* __restrict__ tokens, const SortArgs a) {
+    token_scatter_kernel(const TOK* __restrict__ src, const SortArgs a) {
   extern __shared__ int s_dyn[];
   __shared__ int s_scan[kSortWarps];
   pdl_launch_dependents();
@@ -343,26 +362,34 @@ __global__ void __launch_bounds__(kSortThreads)
   // this warp's digits
   for (int i0 = lo; i0 < hi; i0 += 32 * kSortBatch) {
     uint32_t k[kSortBatch];
-#pragma unroll
-    for (int j = 0; j < kSortBatch; ++j) {
-      const int i = i0 + j * 32 + lane;
-      k[j] = i < hi ? sort_key(tokens, a, i) : 0u;
-    }
+    sort_keys(src, a.V, i0 + lane, 32, hi, k);
 #pragma unroll
     for (int j = 0; j < kSortBatch; ++j)
       if (i0 + j * 32 + lane < hi) atomicAdd(&hist[(k[j] >> a.shift) & (nd - 1)], 1);
   }
-  // all tiles' counts of each digit, and the lower tiles' share
-  for (int d = threadIdx.x; d < nd; d += kSortThreads) {
-    int total = 0, before = 0;
-#pragma unroll 8
-    for (int t = 0; t < static_cast<int>(gridDim.x); ++t) {
-      const int v = __ldg(a.counts + t * nd + d);
-      total += v;
-      before += t < static_cast<int>(blockIdx.x) ? v : 0;
+  // all tiles' counts of each digit, and the lower tiles' share: two
+  // neighbouring digits a thread
+  for (int d = 2 * threadIdx.x; d < nd; d += 2 * kSortThreads) {
+    int2 total = make_int2(0, 0), before = make_int2(0, 0);
+    const int tiles = static_cast<int>(gridDim.x), me = static_cast<int>(blockIdx.x);
+    for (int t0 = 0; t0 < tiles; t0 += 16) {
+      int2 v[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        v[u] = t0 + u < tiles ? __ldg(reinterpret_cast<const int2*>(a.counts + (t0 + u) * nd + d))
+                              : make_int2(0, 0);
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        total.x += v[u].x;
+        total.y += v[u].y;
+        before.x += t0 + u < me ? v[u].x : 0;
+        before.y += t0 + u < me ? v[u].y : 0;
+      }
     }
-    s_all[d] = total;
-    s_base[d] = before;
+    s_all[d] = total.x;
+    s_all[d + 1] = total.y;
+    s_base[d] = before.x;
+    s_base[d + 1] = before.y;
   }
   __syncthreads();
   // scan over the digits, dpt neighbours a thread
@@ -398,9 +425,9 @@ __global__ void __launch_bounds__(kSortThreads)
 #pragma unroll
     for (int j = 0; j < kSortBatch; ++j) {
       const int i = i0 + j * 32 + lane;
-      k[j] = i < hi ? sort_key(tokens, a, i) : 0u;
       p[j] = i < hi && a.pos_in != nullptr ? __ldg(a.pos_in + i) : i;
     }
+    sort_keys(src, a.V, i0 + lane, 32, hi, k);
 #pragma unroll
     for (int j = 0; j < kSortBatch; ++j) {
       if (i0 + j * 32 >= hi) break;  // uniform over the warp
@@ -780,15 +807,66 @@ __global__ void __launch_bounds__(kSegThreads, 4)
 }
 
 // ---------------------------------------------------------------------------
-// Long runs: the pieces of a run added in order.  One CTA looks at kLongRanges
-// ranges (blockIdx.x) and one block of kLongCols columns (blockIdx.y); for each
-// range in which a long run begins, its warps take the run's pieces in
-// contiguous shares, add them, and the shares are added in warp order.  Where a
-// run ends is read off the ranges' flags, 32 at a time.
+// Long runs: the pieces of a run added in order.  A CTA looks at kLongRanges
+// ranges (blockIdx.x) and one block of kLongCols columns (blockIdx.y).  Its
+// warps deal the long runs that begin there among them; runs of more than
+// kLongAlone pieces are shared by all: the warps take contiguous shares of the
+// pieces, and the shares are added in warp order.  Where a run ends is read off
+// the ranges' flags, 32 at a time.
 // ---------------------------------------------------------------------------
 constexpr int kLongWarps = 8;
-constexpr int kLongRanges = 16;
+constexpr int kLongRanges = 32;
 constexpr int kLongCols = 128;  // 4 per lane
+constexpr int kLongAlone = 16;
+
+// Pieces [p0, p1) of the run that begins in `range`, added.
+__device__ __forceinline__ float4 add_pieces(const SegArgs& a, long long range, int slot,
+                                             long long p0, long long p1, long long col) {
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (long long p = p0; p < p1; ++p) {
+    const long long row = (range + p) * 2 + (p == 0 ? slot : 0);
+    if (DPRC_IN(range + p < a.nranges && col + 3 < a.dpad)) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + row * a.dpad + col));
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+  }
+  return s;
+}
+
+// What becomes of a long run's sums over one block of columns (a warp's).
+template <typename T, bool kNorm>
+__device__ __forceinline__ void finish_run(const SegArgs& a, T* __restrict__ dW, long long range,
+                                           long long col, float4 s) {
+  const float f[4] = {s.x, s.y, s.z, s.w};
+  if (kNorm) {
+    // columns past d hold whatever the workspace held
+    float q = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < a.d) q = fmaf(f[e], f[e], q);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
+    if ((threadIdx.x & 31) == 0) a.long_sq[range * gridDim.y + blockIdx.y] = q;
+  } else {
+    const uint32_t k = __ldg(a.key + (range + 1) * kRange - 1);  // the run reaches past `range`
+    T* out = dW + static_cast<long long>(k) * a.d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (col + e < a.d && DPRC_IN(k < static_cast<uint32_t>(a.V))) {
+        const float prev = a.accumulate ? to_f32<T>(out[col + e]) : 0.f;
+        const float v = fmaf(a.scale, f[e], prev);
+        if constexpr (sizeof(T) == 4)
+          out[col + e] = v;
+        else
+          out[col + e] = __float2bfloat16_rn(v);
+      }
+    }
+  }
+}
 
 template <typename T, bool kNorm>
 __global__ void __launch_bounds__(32 * kLongWarps)
@@ -798,78 +876,53 @@ __global__ void __launch_bounds__(32 * kLongWarps)
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long rbase = static_cast<long long>(blockIdx.x) * kLongRanges;
-  const int at = lane < kLongRanges && rbase + lane < a.nranges ? a.long_at[rbase + lane] & 3 : 0;
-  uint32_t todo = __ballot_sync(0xffffffffu, at != 0);
   const long long col = static_cast<long long>(blockIdx.y) * kLongCols + lane * 4;  // < dpad
-  while (todo != 0) {
+  const int f0 = rbase + lane < a.nranges ? a.long_at[rbase + lane] : 0;
+  uint32_t todo = __ballot_sync(0xffffffffu, (f0 & 3) != 0);
+  // a run ends in the first range after its own from which no long run reaches
+  // on, or in which another begins
+  const uint32_t stop0 = __ballot_sync(0xffffffffu, (f0 & 4) == 0 || (f0 & 3) == 2);
+  for (int turn = 0; todo != 0; todo &= todo - 1, ++turn) {
     const int j = __ffs(static_cast<int>(todo)) - 1;
-    todo &= todo - 1;
-    const int slot = __shfl_sync(0xffffffffu, at, j) - 1;
+    const int slot = (__shfl_sync(0xffffffffu, f0, j) & 3) - 1;
     const long long range = rbase + j;
-    // the run's last range: the first after `range` from which no long run
-    // reaches on, or in which another begins
-    long long end = range + 1;
-    while (true) {
-      const int f = end + lane < a.nranges ? a.long_at[end + lane] : 0;
-      const uint32_t stop = __ballot_sync(0xffffffffu, (f & 4) == 0 || (f & 3) == 2);
-      if (stop != 0) {
-        end += __ffs(static_cast<int>(stop)) - 1;
-        break;
+    long long end = rbase + 32;
+    const uint32_t here = j == 31 ? 0u : stop0 & ~((2u << j) - 1u);
+    if (here != 0) {
+      end = rbase + __ffs(static_cast<int>(here)) - 1;
+    } else {
+      while (true) {
+        const int f = end + lane < a.nranges ? a.long_at[end + lane] : 0;
+        const uint32_t stop = __ballot_sync(0xffffffffu, (f & 4) == 0 || (f & 3) == 2);
+        if (stop != 0) {
+          end += __ffs(static_cast<int>(stop)) - 1;
+          break;
+        }
+        end += 32;
       }
-      end += 32;
     }
     const long long pieces = end - range + 1;
-    const long long share = (pieces + kLongWarps - 1) / kLongWarps;
-    const long long p0 = warp * share, p1 = min(p0 + share, pieces);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (long long p = p0; p < p1; ++p) {
-      const long long slot_row = (range + p) * 2 + (p == 0 ? slot : 0);
-      if (DPRC_IN(range + p < a.nranges && col + 3 < a.dpad)) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + slot_row * a.dpad + col));
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
-      }
-    }
-    s_sum[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0) {
-      float f[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int w = 0; w < kLongWarps; ++w) {
-        const float4 v = s_sum[w][lane];
-        f[0] += v.x;
-        f[1] += v.y;
-        f[2] += v.z;
-        f[3] += v.w;
-      }
-      if (kNorm) {
-        // columns past d hold whatever the workspace held
-        float q = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < a.d) q = fmaf(f[e], f[e], q);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
-        if (lane == 0) a.long_sq[range * gridDim.y + blockIdx.y] = q;
-      } else {
-        const uint32_t k = __ldg(a.key + (range + 1) * kRange - 1);  // the run reaches past `range`
-        T* out = dW + static_cast<long long>(k) * a.d;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (col + e < a.d && DPRC_IN(k < static_cast<uint32_t>(a.V))) {
-            const float prev = a.accumulate ? to_f32<T>(out[col + e]) : 0.f;
-            const float v = fmaf(a.scale, f[e], prev);
-            if constexpr (sizeof(T) == 4)
-              out[col + e] = v;
-            else
-              out[col + e] = __float2bfloat16_rn(v);
-          }
+    if (pieces <= kLongAlone) {
+      if (turn % kLongWarps == warp)
+        finish_run<T, kNorm>(a, dW, range, col, add_pieces(a, range, slot, 0, pieces, col));
+    } else {  // the same for every warp
+      const long long share = (pieces + kLongWarps - 1) / kLongWarps;
+      const long long p0 = warp * share;
+      s_sum[warp][lane] = add_pieces(a, range, slot, p0, min(p0 + share, pieces), col);
+      __syncthreads();
+      if (turn % kLongWarps == warp) {
+        float4 s = s_sum[0][lane];
+        for (int w = 1; w < kLongWarps; ++w) {
+          const float4 v = s_sum[w][lane];
+          s.x += v.x;
+          s.y += v.y;
+          s.z += v.z;
+          s.w += v.w;
         }
+        finish_run<T, kNorm>(a, dW, range, col, s);
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -1056,7 +1109,8 @@ cudaError_t launch_segments_t(const SegArgs& a, const SegPlan& p, const void* G,
     if (e != cudaSuccess) return e;
   }
   if (a.N > kRange) {
-    const dim3 grid(static_cast<unsigned>((a.nranges + kLongRanges - 1) / kLongRanges), static_cast<unsigned>(p.ncb));
+    const dim3 grid(static_cast<unsigned>((a.nranges + kLongRanges - 1) / kLongRanges),
+                    static_cast<unsigned>(p.ncb));
     return launch_after(embed_long_kernel<T, kNorm>, grid, 32 * kLongWarps, 1, s, 0, a,
                         static_cast<T*>(dW));
   }
@@ -1126,15 +1180,18 @@ cudaError_t launch_plan_t(const TOK* tokens, int64_t N, int64_t V, char* plan, c
   for (int p = 0; p < sp.passes; ++p) {
     const int dst = (sp.passes - 1 - p) & 1;  // the last pass writes buffer 0
     a.shift = p * sp.bits;
-    a.key_in = p == 0 ? nullptr : key[dst ^ 1];
     a.pos_in = p == 0 ? nullptr : pos[dst ^ 1];
     a.key_out = key[dst];
     a.pos_out = pos[dst];
-    cudaError_t e = launch_after(token_count_kernel<TOK>, dim3(sp.tiles), kSortThreads, 1, s, 0,
-                                 tokens, a);
+    const dim3 grid(sp.tiles);
+    const uint32_t* in = key[dst ^ 1];
+    cudaError_t e =
+        p == 0 ? launch_after(token_count_kernel<TOK>, grid, kSortThreads, 1, s, 0, tokens, a)
+               : launch_after(token_count_kernel<uint32_t>, grid, kSortThreads, 1, s, 0, in, a);
     if (e != cudaSuccess) return e;
-    e = launch_after(token_scatter_kernel<TOK>, dim3(sp.tiles), kSortThreads, 1, s, smem, tokens,
-                     a);
+    e = p == 0
+            ? launch_after(token_scatter_kernel<TOK>, grid, kSortThreads, 1, s, smem, tokens, a)
+            : launch_after(token_scatter_kernel<uint32_t>, grid, kSortThreads, 1, s, smem, in, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
