@@ -210,6 +210,7 @@ struct GemmPlan {
   bool pair = false;        // 256 x 256 tiles on CTA pairs
   int split = 1;
   int64_t units = 0;        // contraction units of 64 (times plane products)
+  int64_t per = 0;          // units of a share
   int64_t ldpart = 0;       // row stride of a partial result
   size_t part_bytes = 0;
   double cost = 0.0;        // estimated cycles

@@ -33,6 +33,12 @@ constexpr int kTm = 128;
 constexpr int kTk = 64;
 constexpr int kRing = 192 * 1024;
 
+// Accumulators of a set, and sets (the pair's fp32 set takes all of TMEM).
+template <typename T>
+constexpr int kAccs = sizeof(T) == 4 ? 2 : 1;
+template <typename T>
+constexpr int kPairSets = sizeof(T) == 4 ? 1 : 2;
+
 template <int kTn>
 struct GemmCfg {
   static constexpr int kA = kTm * kTk * 2;
@@ -42,7 +48,6 @@ struct GemmCfg {
   static constexpr int kEpiWarps = kTn >= 64 ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kCols = kTn / (kEpiWarps / 4);  // columns per epilogue warp
-  static constexpr int kTmem = 2 * kTn;
   static constexpr int kSmem = kStages * kStage + 1024 + 512;
 };
 
@@ -154,34 +159,105 @@ __device__ __forceinline__ GemmUnit gemm_unit(const GemmArgs& a, int w) {
   return g;
 }
 
-// kCols finished sums of one row (this thread's TMEM lane) from tb on, the
-// first of them column col0 of D: through the epilogue, or to the partial sums.
-template <typename T, int kCols>
-__device__ __forceinline__ void gemm_rows(const GemmArgs& a, const GemmUnit& g, uint32_t tb,
-                                          long long row, int col0, const RoundKeys& rk) {
-  constexpr int kStep = kCols < 32 ? kCols : 32;
-#pragma unroll 1
-  for (int c0 = 0; c0 < kCols; c0 += kStep) {
-    const int col = col0 + c0;
-    if (col >= a.cols) break;  // uniform over the warp
-    float v[kStep];
-    tmem_ld_cols<kStep>(tb + c0, v);
-    if (row >= a.rows) continue;
-    if (a.transposed) {
-      float* out = a.part + g.split * a.part_stride + row;
+// kN finished sums of one row, the first of them column col of D: through the
+// epilogue, or to the partial sums.
+template <typename T, int kN>
+__device__ __forceinline__ void gemm_emit(const GemmArgs& a, int split, long long row, int col,
+                                          float* v, const RoundKeys& rk) {
+  if (row >= a.rows || col >= a.cols) return;
+  if (a.transposed) {
+    float* out = a.part + split * a.part_stride + row;
 #pragma unroll
-      for (int t = 0; t < kStep; ++t)
-        if (col + t < a.cols) out[(col + t) * a.ldpart] = v[t];
-    } else if (a.part != nullptr) {
-      float* out = a.part + g.split * a.part_stride + row * a.ldpart + col;
+    for (int t = 0; t < kN; ++t)
+      if (col + t < a.cols) out[(col + t) * a.ldpart] = v[t];
+  } else if (a.part != nullptr) {
+    float* out = a.part + split * a.part_stride + row * a.ldpart + col;
 #pragma unroll
-      for (int t = 0; t < kStep; t += 4)
-        if (col + t < a.cols && DPRC_IN(col + t + 4 <= a.ldpart))
-          *reinterpret_cast<float4*>(out + t) = make_float4(v[t], v[t + 1], v[t + 2], v[t + 3]);
-    } else {
-      linear_out<T, kStep / 8>(a.epi, row, col, v, rk);
+    for (int t = 0; t < kN; t += 4)
+      if (col + t < a.cols && DPRC_IN(col + t + 4 <= a.ldpart))
+        *reinterpret_cast<float4*>(out + t) = make_float4(v[t], v[t + 1], v[t + 2], v[t + 3]);
+  } else {
+    linear_out<T, kN / 8>(a.epi, row, col, v, rk);
+  }
+}
+
+// Accumulators.  bf16: one per tile, two sets in turn, so that a tile's
+// epilogue runs under the next tile's MMAs.  fp32: the tensor core's additions
+// truncate, which showed over a contraction's six plane products per step
+// (2.2e-6 of the result at K = 1001, where a plain fp32 product has 5.4e-7).
+// So the first plane product, which makes the result's size, has an
+// accumulator of its own, the five others, 2^-8 of it and less, a second one,
+// and every kAccUnits units (512 of the contraction) the epilogue warps add
+// both to sums in registers: FPREC.
+template <typename T>
+constexpr int kAccUnits = sizeof(T) == 4 ? 48 : 1 << 30;
+
+// Set `count` of kSets accumulator sets.
+template <int kSets>
+struct AccPos {
+  int set = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++set == kSets) {
+      set = 0;
+      parity ^= 1u;
     }
   }
+};
+
+// The sums of one unit of work for this thread's row (TMEM lane), kCols of
+// them from column tmem of each accumulator on (kAcc columns apart), first
+// column col0 of D.  `release(set)` frees a set.
+template <typename T, int kCols, int kAcc, int kSets, typename Release>
+__device__ __forceinline__ bool gemm_collect(const GemmArgs& a, const GemmUnit& g, uint32_t tmem,
+                                             long long row, int col0, const RoundKeys& rk,
+                                             uint64_t* accf, AccPos<kSets>& pos,
+                                             const volatile int* abort_flag, bool ok,
+                                             Release release) {
+  if constexpr (sizeof(T) == 2) {
+    constexpr int kStep = kCols < 32 ? kCols : 32;
+    ok = ok && wait_warp(&accf[pos.set], pos.parity, DPRC_DEVERR_ACCUM, abort_flag);
+    tc_fence_after();
+    if (ok) {
+#pragma unroll 1
+      for (int c0 = 0; c0 < kCols; c0 += kStep) {
+        if (col0 + c0 >= a.cols) break;  // uniform over the warp
+        float v[kStep];
+        tmem_ld_cols<kStep>(tmem + pos.set * kAcc + c0, v);
+        gemm_emit<T, kStep>(a, g.split, row, col0 + c0, v, rk);
+      }
+    }
+    release(pos.set);
+    pos.next();
+  } else {
+    constexpr int kStep = 16;
+    float acc[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+    for (int u = g.u0; u < g.u1; u += kAccUnits<T>) {
+      ok = ok && wait_warp(&accf[pos.set], pos.parity, DPRC_DEVERR_ACCUM, abort_flag);
+      tc_fence_after();
+      if (ok) {
+        const uint32_t t0 = tmem + pos.set * 2 * kAcc;
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += kStep) {
+          float v[kStep], w[kStep];
+          tmem_ld_cols<kStep>(t0 + c0, v);
+          tmem_ld_cols<kStep>(t0 + kAcc + c0, w);
+#pragma unroll
+          for (int t = 0; t < kStep; ++t) acc[c0 + t] += v[t] + w[t];
+        }
+      }
+      release(pos.set);
+      pos.next();
+    }
+    if (ok) {
+#pragma unroll
+      for (int c0 = 0; c0 < kCols; c0 += 8)
+        gemm_emit<T, 8>(a, g.split, row, col0 + c0, acc + c0, rk);
+    }
+  }
+  return ok;
 }
 
 // Matrix descriptors of an operand's K = 16 steps.  K-major, 128-byte swizzle:
@@ -236,7 +312,7 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
     tma_prefetch_desc(&map_b);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, Cfg::kTmem);
+    tmem_alloc(tmem_slot, 2 * kAccs<T> * kTn);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -293,34 +369,41 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
       const uint32_t idesc = make_idesc_bf16(kTm, kTn, a.a_mn != 0, a.b_mn != 0);
       const StepDesc da(smem_u32(ring), a.a_mn != 0), db(smem_u32(ring) + Cfg::kA, a.b_mn != 0);
       RingPos<kStages> pos;
+      AccPos<2> set;
       bool ok = true, issued = false;
       for (int j = 0; j < mine && ok; ++j) {
         const GemmUnit g = gemm_unit(a, first + j * stride);
-        const int abuf = j & 1;
-        if (!wait_long(&acce[abuf], static_cast<uint32_t>((j >> 1) & 1) ^ 1, DPRC_DEVERR_ACCUM,
-                       abort_flag)) {
-          *abort_flag = 1;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t acc = tmem + abuf * kTn;
-        for (int u = g.u0; u < g.u1; ++u, pos.next()) {
-          const int s = pos.s;
-          if (!wait_long(&full[s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag)) {
+        UnitPos at(g.u0, a.npairs);
+        for (int c0 = g.u0, c1; c0 < g.u1 && ok; c0 = c1, set.next()) {
+          c1 = g.u1 - c0 < kAccUnits<T> ? g.u1 : c0 + kAccUnits<T>;
+          if (!wait_long(&acce[set.set], set.parity ^ 1, DPRC_DEVERR_ACCUM, abort_flag)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = da.at(s * Cfg::kStage), bd = db.at(s * Cfg::kStage);
+          const uint32_t acc = tmem + set.set * kAccs<T> * kTn;
+          uint32_t begun = 0;  // bit i: accumulator i of the set holds sums
+          for (int u = c0; u < c1; ++u, pos.next(), at.next()) {
+            const int s = pos.s;
+            if (!wait_long(&full[s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag)) {
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = da.at(s * Cfg::kStage), bd = db.at(s * Cfg::kStage);
+            const int which = kAccs<T> == 2 && at.pair != 0 ? 1 : 0;
 #pragma unroll
-          for (int kk = 0; kk < kTk / 16; ++kk)
-            umma_bf16(acc, ad + kk * da.step, bd + kk * db.step, idesc,
-                      (u == g.u0 && kk == 0) ? 0u : 1u);
-          umma_commit(&empty[s]);
-          issued = true;
+            for (int kk = 0; kk < kTk / 16; ++kk)
+              umma_bf16(acc + which * kTn, ad + kk * da.step, bd + kk * db.step, idesc,
+                 ((begun >> which) & 1u) | (kk != 0));
+            begun |= 1u << which;
+            umma_commit(&empty[s]);
+            issued = true;
+          }
+          if (ok) umma_commit(&accf[set.set]);
         }
-        if (ok) umma_commit(&accf[abuf]);
       }
       if (issued) umma_drain(drain, kWaitLimitNs);
     }
@@ -329,22 +412,19 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
     const int q = warp & 3;  // TMEM lane quadrant this warp may read
     const int c_lo = (ew >> 2) * Cfg::kCols;
     const RoundKeys rk = round_keys(a.epi.drop.seed);
+    const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + c_lo;
+    const auto release = [&](int buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acce[buf]);
+    };
+    AccPos<2> pos;
     bool ok = true;
     for (int j = 0; j < mine; ++j) {
       const GemmUnit g = gemm_unit(a, first + j * stride);
-      const int abuf = j & 1;
-      const bool live = ok && wait_warp(&accf[abuf], static_cast<uint32_t>((j >> 1) & 1),
-                                        DPRC_DEVERR_ACCUM, abort_flag);
-      if (!live) ok = false;
-      tc_fence_after();
-      if (live) {
-        const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + abuf * kTn + c_lo;
-        const long long row = static_cast<long long>(g.m) * kTm + q * 32 + lane;
-        gemm_rows<T, Cfg::kCols>(a, g, tb, row, g.n * kTn + c_lo, rk);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acce[abuf]);
+      const long long row = static_cast<long long>(g.m) * kTm + q * 32 + lane;
+      ok = gemm_collect<T, Cfg::kCols, kTn, 2>(a, g, tb, row, g.n * kTn + c_lo, rk, accf, pos,
+                                            abort_flag, ok, release);
     }
   }
 
@@ -353,7 +433,7 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, Cfg::kTmem);
+    tmem_dealloc(tmem, 2 * kAccs<T> * kTn);
   }
 }
 
@@ -388,8 +468,9 @@ constexpr double kPairStep = 600.0;  // cycles of a 64-deep step
 constexpr int kPairA = kTm * kTk * 2;
 constexpr int kPairStage = 2 * kPairA;
 constexpr int kPairStages = 7;
-constexpr int kPairEpiWarps = 8;
-constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+// Epilogue warps: fp32 keeps its sums in registers, 64 columns a warp.
+template <typename T>
+constexpr int kPairEpiWarps = sizeof(T) == 4 ? 16 : 8;
 constexpr int kPairSmem = kPairStages * kPairStage + 1024 + 512;
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
@@ -465,12 +546,13 @@ __device__ __forceinline__ PairWork pair_work(const GemmBatch& b, int me, int pa
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims__(2, 1, 1)
     linear_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a0,
                             const __grid_constant__ CUtensorMap map_b0,
                             const __grid_constant__ CUtensorMap map_a1,
                             const __grid_constant__ CUtensorMap map_b1,
                             const __grid_constant__ GemmBatch batch) {
+  constexpr int kEpi = kPairEpiWarps<T>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align_1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + kPairStages * kPairStage);
@@ -498,7 +580,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accf[b], 1);
-      mbar_init(&acce[b], 2 * kPairEpiWarps);
+      mbar_init(&acce[b], 2 * kEpi);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -566,6 +648,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp == 1) {
     if (rank == 0 && lane == 0 && mine > 0) {
       RingPos<kPairStages> pos;
+      AccPos<kPairSets<T>> set;
       bool ok = true, issued = false;
       for (int j = 0; j < mine && ok; ++j) {
         const GemmArgs& a = batch.p[j >= work.mine0];
@@ -573,31 +656,37 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         const StepDesc da(smem_u32(ring), a.a_mn != 0);
         const StepDesc db(smem_u32(ring) + kPairA, a.b_mn != 0);
         const GemmUnit g = gemm_unit(a, work.at(j));
-        const int abuf = j & 1;
-        if (!wait_long(&acce[abuf], static_cast<uint32_t>((j >> 1) & 1) ^ 1,
-                       DPRC_DEVERR_ACCUM, abort_flag)) {
-          *abort_flag = 1;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t acc = tmem + abuf * kPairTile;
-        for (int u = g.u0; u < g.u1; ++u, pos.next()) {
-          const int s = pos.s;
-          if (!wait_long(&full[s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag)) {
+        UnitPos at(g.u0, a.npairs);
+        for (int c0 = g.u0, c1; c0 < g.u1 && ok; c0 = c1, set.next()) {
+          c1 = g.u1 - c0 < kAccUnits<T> ? g.u1 : c0 + kAccUnits<T>;
+          if (!wait_long(&acce[set.set], set.parity ^ 1, DPRC_DEVERR_ACCUM, abort_flag)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = da.at(s * kPairStage), bd = db.at(s * kPairStage);
+          const uint32_t acc = tmem + set.set * kAccs<T> * kPairTile;
+          uint32_t begun = 0;  // bit i: accumulator i of the set holds sums
+          for (int u = c0; u < c1; ++u, pos.next(), at.next()) {
+            const int s = pos.s;
+            if (!wait_long(&full[s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag)) {
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = da.at(s * kPairStage), bd = db.at(s * kPairStage);
+            const int which = kAccs<T> == 2 && at.pair != 0 ? 1 : 0;
 #pragma unroll
-          for (int kk = 0; kk < kTk / 16; ++kk)
-            umma_bf16_pair(acc, ad + kk * da.step, bd + kk * db.step, idesc,
-                           (u == g.u0 && kk == 0) ? 0u : 1u);
-          umma_commit_pair(&empty[s]);
-          issued = true;
+            for (int kk = 0; kk < kTk / 16; ++kk)
+              umma_bf16_pair(acc + which * kPairTile, ad + kk * da.step, bd + kk * db.step, idesc,
+                 ((begun >> which) & 1u) | (kk != 0));
+            begun |= 1u << which;
+            umma_commit_pair(&empty[s]);
+            issued = true;
+          }
+          if (ok) umma_commit_pair(&accf[set.set]);
         }
-        if (ok) umma_commit_pair(&accf[abuf]);
       }
       if (issued) {
         asm volatile(
@@ -610,26 +699,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   } else {
     const int ew = warp - 2;
     const int q = warp & 3;  // TMEM lane quadrant this warp may read
-    const int c_lo = (ew >> 2) * kTm;
+    constexpr int kCols = kPairTile / (kEpi / 4);
+    const int c_lo = (ew >> 2) * kCols;
     const RoundKeys rk = round_keys(batch.p[0].epi.drop.seed);  // a pair of problems drops nothing
+    const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + c_lo;
+    const uint32_t acce0 = map_to_rank(acce, 0);
+    const auto release = [&](int buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(acce0 + buf * 8);
+    };
+    AccPos<kPairSets<T>> pos;
     bool ok = true;
     for (int j = 0; j < mine; ++j) {
       const GemmArgs& a = batch.p[j >= work.mine0];
       const GemmUnit g = gemm_unit(a, work.at(j));
-      const int abuf = j & 1;
-      const bool live = ok && wait_warp(&accf[abuf], static_cast<uint32_t>((j >> 1) & 1),
-                                        DPRC_DEVERR_ACCUM, abort_flag);
-      if (!live) ok = false;
-      tc_fence_after();
-      if (live) {
-        const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + abuf * kPairTile + c_lo;
-        const long long row =
-            static_cast<long long>(g.m) * kPairTile + rank * kTm + q * 32 + lane;
-        gemm_rows<T, kTm>(a, g, tb, row, g.n * kPairTile + c_lo, rk);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(map_to_rank(&acce[abuf], 0));
+      const long long row = static_cast<long long>(g.m) * kPairTile + rank * kTm + q * 32 + lane;
+      ok = gemm_collect<T, kCols, kPairTile, kPairSets<T>>(
+          a, g, tb, row, g.n * kPairTile + c_lo, rk, accf, pos, abort_flag, ok, release);
     }
   }
 
@@ -647,7 +734,7 @@ cudaError_t launch_gemm_pair(const CUtensorMap* maps, const GemmBatch& batch, cu
   const cudaError_t e = set_smem_once<2 + sizeof(T)>(linear_gemm_pair_kernel<T>, kPairSmem);
   if (e != cudaSuccess) return e;
   const long long pairs = std::min<long long>(static_cast<long long>(batch.n0) + batch.n1, device_sm_count() / 2);
-  linear_gemm_pair_kernel<T><<<static_cast<unsigned>(2 * pairs), kPairThreads, kPairSmem, s>>>(
+  linear_gemm_pair_kernel<T><<<static_cast<unsigned>(2 * pairs), 64 + 32 * kPairEpiWarps<T>, kPairSmem, s>>>(
       maps[0], maps[1], maps[2], maps[3], batch);
   return cudaGetLastError();
 }
@@ -695,7 +782,9 @@ cudaError_t launch_gemm_tn(int tn, const CUtensorMap& ma, const CUtensorMap& mb,
     case 32: return launch_gemm_t<32, T>(ma, mb, a, s);
     case 64: return launch_gemm_t<64, T>(ma, mb, a, s);
     case 128: return launch_gemm_t<128, T>(ma, mb, a, s);
-    default: return launch_gemm_t<256, T>(ma, mb, a, s);
+    default:
+      if constexpr (sizeof(T) == 2) return launch_gemm_t<256, T>(ma, mb, a, s);
+      return cudaErrorInvalidValue;
   }
 }
 
@@ -734,15 +823,18 @@ GemmPlan plan_gemm(const GemmShape& g) {
   const Shape few[] = {{128, 16, 1, 200.0}, {128, 32, 1, 210.0}, {128, 64, 1, 260.0}};
   const Shape* shapes = g.transposed ? few : wide;
   const int nshapes = g.transposed ? 3 : 4;
+  const int64_t whole = g.planes > 1 ? 6 : 1;
   double best = 1e300;
   for (int i = 0; i < nshapes; ++i) {
     const Shape& sh = shapes[i];
     if (g.transposed && i < 2 && g.cols > sh.tn) continue;
+    if (g.planes > 1 && sh.tn == 256 && sh.ctas == 1) continue;  // 128 sums a thread
     const int64_t tiles = (g.rows + sh.tm - 1) / sh.tm * ((g.cols + sh.tn - 1) / sh.tn);
     const int64_t slots = sms / sh.ctas;
     const int64_t max_split = p.units < 4 ? 1 : (p.units / 4 < 64 ? p.units / 4 : 64);
     for (int64_t want = 1; want <= max_split; ++want) {
-      const int64_t per = (p.units + want - 1) / want;
+      // (whole steps of the contraction: both accumulators of fp32 get a share)
+      const int64_t per = ((p.units + want - 1) / want + whole - 1) / whole * whole;
       const int64_t split = (p.units + per - 1) / per;
       if (split != want) continue;
       const int64_t waves = (tiles * split + slots - 1) / slots;
@@ -756,6 +848,7 @@ GemmPlan plan_gemm(const GemmShape& g) {
         p.tn = sh.tn;
         p.pair = sh.ctas == 2;
         p.split = static_cast<int>(split);
+        p.per = per;
       }
       if (tiles * split >= 4 * static_cast<int64_t>(sms)) break;
     }
@@ -790,7 +883,7 @@ cudaError_t prepare_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperan
   a.group = std::max(8, (wave + a.nt - 1) / a.nt);
   a.split = p.split;
   a.units = static_cast<int>(p.units);
-  a.per_split = static_cast<int>((p.units + p.split - 1) / p.split);
+  a.per_split = static_cast<int>(p.per);
   a.npairs = g.planes > 1 ? 6 : 1;
   a.a_mn = A.mn_major;
   a.b_mn = B.mn_major;
@@ -850,7 +943,7 @@ cudaError_t launch_gemm_two(const GemmTask& t0, const GemmTask& t1, dprc_dtype d
   for (int i = 0; i < 2; ++i) {
     GemmPlan p;
     p.pair = true;
-    p.units = t[i]->plan->units;
+    p.units = p.per = t[i]->plan->units;
     const cudaError_t e = prepare_gemm(*t[i]->shape, p, t[i]->A, t[i]->B, t[i]->epi, nullptr,
                                        maps + 2 * i, batch.p[i]);
     if (e != cudaSuccess) return e;
