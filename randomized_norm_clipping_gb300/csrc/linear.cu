@@ -86,12 +86,11 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const PackArgs a) {
 // ---------------------------------------------------------------------------
 // dZ = drop(dY) act'(Z), elementwise in fp32, rounded once to bf16 (or split
 // into planes) for the products; and its column sums, which take the unrounded
-// values.  A CTA takes kDzRows rows of 256 columns; its 8 warps take every 8th
+// values.  A CTA takes a block of rows of 256 columns; its 8 warps take every 8th
 // row, and their column sums are added in warp order.  The rounding of dZ to
 // bf16 is the product's operand type: relative 2^-9 per element, as the
 // rounding of the results.
 // ---------------------------------------------------------------------------
-constexpr int kDzRows = 64;
 constexpr int kDzWarps = 8;
 constexpr int kDzAhead = 4;
 
@@ -134,7 +133,7 @@ struct DzArgs {
   const void* dY;
   const void* Z;
   long long M;
-  int N, vec, act;
+  int N, vec, act, rows;  // rows of a CTA
   DropArgs drop;
   __nv_bfloat16* planes;  // or null
   long long plane;
@@ -152,18 +151,18 @@ __global__ void __launch_bounds__(32 * kDzWarps, 2) linear_dz_kernel(const DzArg
   const int rb = static_cast<int>(blockIdx.x / ncb), cb = static_cast<int>(blockIdx.x % ncb);
   const int n0 = cb * 256 + lane * 8;
   const int cnt = min(8, a.N - n0);
-  const long long m0 = static_cast<long long>(rb) * kDzRows;
+  const long long m0 = static_cast<long long>(rb) * a.rows;
   const RoundKeys rk = round_keys(a.drop.seed);
   const bool vec = a.vec != 0;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (cnt > 0) {
 #pragma unroll 1
-    for (int r0 = warp; r0 < kDzRows; r0 += kDzWarps * kDzAhead) {
+    for (int r0 = warp; r0 < a.rows; r0 += kDzWarps * kDzAhead) {
       Raw8<T> g8[kDzAhead], z8[kDzAhead];
 #pragma unroll
       for (int u = 0; u < kDzAhead; ++u) {
         const long long m = m0 + r0 + u * kDzWarps;
-        if (m >= a.M) continue;
+        if (r0 + u * kDzWarps >= a.rows || m >= a.M) continue;
         raw_ld(static_cast<const T*>(a.dY) + m * a.N + n0, cnt, vec, g8[u]);
         if (a.act != DPRC_ACT_NONE)
           raw_ld(static_cast<const T*>(a.Z) + m * a.N + n0, cnt, vec, z8[u]);
@@ -171,7 +170,7 @@ __global__ void __launch_bounds__(32 * kDzWarps, 2) linear_dz_kernel(const DzArg
 #pragma unroll
       for (int u = 0; u < kDzAhead; ++u) {
         const long long m = m0 + r0 + u * kDzWarps;
-        if (m >= a.M) continue;
+        if (r0 + u * kDzWarps >= a.rows || m >= a.M) continue;
         float g[8], z[8];
         raw_get(g8[u], g);
         if (a.drop.thr != 0) drop8_at(g, static_cast<uint64_t>(m * a.N + n0), a.drop, rk);
@@ -301,9 +300,22 @@ cudaError_t run_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A
 // (linear_gemm.cu); with more, the tokens fill half a tile's lanes or more.
 constexpr int64_t kFewTokens = 64;
 
+// Whether the forward map of M tokens runs on the CUDA cores (linear_few.cu).
+// Measured with the weights in turn in L2 and memory (us, CUDA cores / tensor
+// cores): bf16 2048 x 8192 M = 1 7.4 / 11.2, M = 4 10.9 / 12.3, M = 8 20 / 12.3;
+// 2048 x 512 M = 16 3.8 / 7.4, M = 32 6.1 / 7.7, M = 64 10.6 / 7.9; fp32
+// 2048 x 8192 M = 8 29 / 73, M = 24 56 / 74, M = 32 69 / 74, 2048 x 512 M = 64
+// 12.8 / 19.6.  The cores' time grows with N K M, the other's with N K: they
+// cross where N K (M - m) is a constant.
+bool few_tokens(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
+  if (M > kFewTokens) return false;
+  const int64_t nk = N * K;
+  return dt == DPRC_F32 ? nk * (M - 23) <= 100000000 : nk * (M - 2) <= 40000000;
+}
+
 // Sizes and workspace of a forward call.
 struct LinearPlan {
-  bool pack = false;
+  bool few = false, pack = false;
   int planes = 1;
   int64_t ld = 0;
   GemmShape g;
@@ -313,6 +325,11 @@ struct LinearPlan {
 
 LinearPlan linear_plan(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
   LinearPlan l;
+  l.few = few_tokens(dt, M, K, N);
+  if (l.few) {
+    l.total = 1024;  // none; a call without a workspace stays an error
+    return l;
+  }
   l.planes = dt == DPRC_F32 ? 3 : 1;
   l.pack = dt == DPRC_F32 || K % 8 != 0;
   l.ld = l.pack ? up8(K) : K;
@@ -340,6 +357,7 @@ struct LinearGradPlan {
   bool pack = false;
   int planes = 1;
   int64_t ldk = 0, ldn = 0, nblocks = 0;
+  int dz_rows = 64;
   GemmShape gx, gw;
   GemmPlan px, pw;
   bool together = false;    // dX and dW in one launch
@@ -352,7 +370,12 @@ LinearGradPlan linear_grad_plan(dprc_dtype dt, int64_t M, int64_t K, int64_t N) 
   l.pack = dt == DPRC_F32 || K % 8 != 0;
   l.ldk = l.pack ? up8(K) : K;
   l.ldn = up8(N);
-  l.nblocks = (M + kDzRows - 1) / kDzRows;
+  // rows of a CTA: 64 while that fills the GPU twice, at least one per warp
+  l.dz_rows = 64;
+  while (l.dz_rows > kDzWarps &&
+         (M + l.dz_rows - 1) / l.dz_rows * ((N + 255) / 256) < 4 * int64_t(device_sm_count()))
+    l.dz_rows /= 2;
+  l.nblocks = (M + l.dz_rows - 1) / l.dz_rows;
   l.gx.transposed = M <= kFewTokens;
   l.gx.rows = l.gx.transposed ? K : M;
   l.gx.cols = l.gx.transposed ? M : K;
@@ -397,6 +420,18 @@ size_t linear_grad_ws_bytes(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
 cudaError_t launch_linear(const LinearCall& c, void* ws, cudaStream_t s) {
   if (c.M == 0) return cudaSuccess;
   const LinearPlan l = linear_plan(c.dtype, c.M, c.K, c.N);
+  LinearEpi epi;
+  epi.M = c.M;
+  epi.N = static_cast<int>(c.N);
+  epi.vec = c.N % 8 == 0;
+  epi.act = c.act;
+  epi.bias = c.bias;
+  epi.res = c.res;
+  epi.Z = c.Z;
+  epi.Y = c.Y;
+  epi.drop = drop_args(c.p, c.seed, c.step);
+  if (l.few) return launch_linear_few(c.X, c.W, c.dtype, c.M, c.K, c.N, epi, s);
+
   char* w = static_cast<char*>(ws);
   GemmOperand x, wt;
   x.data = c.X;
@@ -422,16 +457,6 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, cudaStream_t s) {
     x.data = jobs[0].dst;
     wt.data = jobs[1].dst;
   }
-  LinearEpi epi;
-  epi.M = c.M;
-  epi.N = static_cast<int>(c.N);
-  epi.vec = c.N % 8 == 0;
-  epi.act = c.act;
-  epi.bias = c.bias;
-  epi.res = c.res;
-  epi.Z = c.Z;
-  epi.Y = c.Y;
-  epi.drop = drop_args(c.p, c.seed, c.step);
   return run_gemm(l.g, l.p, l.g.transposed ? wt : x, l.g.transposed ? x : wt, c.dtype, epi,
                   w + l.part_off, s);
 }
@@ -473,6 +498,7 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, void* ws, cudaStream_t s
     a.N = static_cast<int>(c.N);
     a.vec = c.N % 8 == 0;
     a.act = c.act;
+    a.rows = l.dz_rows;
     a.drop = drop;
     a.planes = planes;
     a.plane = dz.plane;

@@ -209,7 +209,7 @@ struct GemmPlan {
   int tn = 256;
   bool pair = false;        // 256 x 256 tiles on CTA pairs
   int split = 1;
-  int64_t units = 0;        // contraction units of 64 (times plane products)
+  int64_t units = 0;        // contraction units of 64
   int64_t per = 0;          // units of a share
   int64_t ldpart = 0;       // row stride of a partial result
   size_t part_bytes = 0;
@@ -222,6 +222,10 @@ GemmPlan plan_gemm(const GemmShape& g);
 cudaError_t launch_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A,
                         const GemmOperand& B, dprc_dtype dt, const LinearEpi& epi, void* part,
                         cudaStream_t s);
+
+// The whole map for a few tokens on the CUDA cores (linear_few.cu).
+cudaError_t launch_linear_few(const void* X, const void* W, dprc_dtype dt, int64_t M, int64_t K,
+                              int64_t N, const LinearEpi& epi, cudaStream_t s);
 
 // Two products in one launch (no shares), the longer contraction first;
 // gemm_together: whether that is estimated to be faster than one by one.

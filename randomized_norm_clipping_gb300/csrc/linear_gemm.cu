@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kTm = 128;
 constexpr int kTk = 64;
-constexpr int kRing = 192 * 1024;
+constexpr int kRing = 216 * 1024;
 
 // Accumulators of a set, and sets (the pair's fp32 set takes all of TMEM).
 template <typename T>
@@ -39,12 +39,18 @@ constexpr int kAccs = sizeof(T) == 4 ? 2 : 1;
 template <typename T>
 constexpr int kPairSets = sizeof(T) == 4 ? 1 : 2;
 
-template <int kTn>
+// Planes of an operand.  A stage holds all planes of its 64 of the contraction,
+// so that the six plane products read what was copied once.
+template <typename T>
+constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+
+template <int kTn, typename T>
 struct GemmCfg {
-  static constexpr int kA = kTm * kTk * 2;
+  static constexpr int kA = kTm * kTk * 2;   // of a plane
   static constexpr int kB = kTn * kTk * 2;
-  static constexpr int kStage = kA + kB;
-  static constexpr int kStages = kRing / kStage < 10 ? kRing / kStage : 10;
+  static constexpr int kStage = kPlanes<T> * (kA + kB);
+  static constexpr int kFit = kRing / kStage;
+  static constexpr int kStages = kFit < 2 ? 2 : kFit < 10 ? kFit : 10;
   static constexpr int kEpiWarps = kTn >= 64 ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kCols = kTn / (kEpiWarps / 4);  // columns per epilogue warp
@@ -95,8 +101,7 @@ struct GemmArgs {
   int cols;
   int mt, nt, group;        // tiles, and row tiles per group
   int split;
-  int units, per_split;     // contraction units, and of one share
-  int npairs;               // plane products per 64 of the contraction (1 or 6)
+  int units, per_split;     // contraction units of 64, and of one share
   int a_mn, b_mn;
   int transposed;
   float* part;              // partial sums, or null: the epilogue
@@ -105,9 +110,14 @@ struct GemmArgs {
 };
 
 // Plane products of fp32 operands, by size: 1, 2^-8 (2), 2^-16 (3).
-__device__ __forceinline__ void plane_pair(int i, int& a, int& b) {
-  a = i == 0 || i == 1 || i == 3 ? 0 : i == 5 ? 2 : 1;
-  b = i == 0 || i == 2 || i == 5 ? 0 : i == 3 ? 2 : 1;
+template <typename T>
+constexpr int kProducts = sizeof(T) == 4 ? 6 : 1;
+
+__device__ __forceinline__ constexpr int plane_a(int i) {
+  return i == 0 || i == 1 || i == 3 ? 0 : i == 5 ? 2 : 1;
+}
+__device__ __forceinline__ constexpr int plane_b(int i) {
+  return i == 0 || i == 2 || i == 5 ? 0 : i == 3 ? 2 : 1;
 }
 
 struct GemmUnit {
@@ -126,20 +136,6 @@ struct RingPos {
     if (++s == kStages) {
       s = 0;
       parity ^= 1u;
-    }
-  }
-};
-
-// Which plane products a unit is, in turn.
-struct UnitPos {
-  int kb, pair, npairs;
-  __device__ __forceinline__ UnitPos(int u, int n) : kb(n > 1 ? u / n : u), pair(0), npairs(n) {
-    if (n > 1) pair = u - kb * n;
-  }
-  __device__ __forceinline__ void next() {
-    if (++pair >= npairs) {
-      pair = 0;
-      ++kb;
     }
   }
 };
@@ -190,7 +186,7 @@ __device__ __forceinline__ void gemm_emit(const GemmArgs& a, int split, long lon
 // and every kAccUnits units (512 of the contraction) the epilogue warps add
 // both to sums in registers: FPREC.
 template <typename T>
-constexpr int kAccUnits = sizeof(T) == 4 ? 48 : 1 << 30;
+constexpr int kAccUnits = sizeof(T) == 4 ? 8 : 1 << 30;
 
 // Set `count` of kSets accumulator sets.
 template <int kSets>
@@ -274,10 +270,10 @@ struct StepDesc {
 };
 
 template <int kTn, typename T>
-__global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
+__global__ void __launch_bounds__(GemmCfg<kTn, T>::kThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, const GemmArgs a) {
-  using Cfg = GemmCfg<kTn>;
+  using Cfg = GemmCfg<kTn, T>;
   constexpr int kStages = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align_1024(smem_raw);
@@ -329,33 +325,33 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
       for (int j = 0; j < mine && ok; ++j) {
         const GemmUnit g = gemm_unit(a, first + j * stride);
         const int row = g.m * kTm, col = g.n * kTn;
-        UnitPos at(g.u0, a.npairs);
-        for (int u = g.u0; u < g.u1; ++u, pos.next(), at.next()) {
+        for (int u = g.u0; u < g.u1; ++u, pos.next()) {
           const int s = pos.s;
           if (!wait_long(&empty[s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
-          int pa = 0, pb = 0;
-          if (at.npairs > 1) plane_pair(at.pair, pa, pb);
-          const int k = at.kb * kTk;
+          const int k = u * kTk;
           uint8_t* sa = ring + s * Cfg::kStage;
-          uint8_t* sb = sa + Cfg::kA;
+          uint8_t* sb = sa + kPlanes<T> * Cfg::kA;
           mbar_arrive_expect_tx(&full[s], Cfg::kStage);
-          if (a_mn) {
 #pragma unroll
-            for (int h = 0; h < kTm / 64; ++h)
-              tma_load_3d(sa + h * (kTk * 128), &map_a, &full[s], row + h * 64, k, pa);
-          } else {
-            tma_load_3d(sa, &map_a, &full[s], k, row, pa);
-          }
-          if (b_mn) {
+          for (int p = 0; p < kPlanes<T>; ++p, sa += Cfg::kA, sb += Cfg::kB) {
+            if (a_mn) {
 #pragma unroll
-            for (int h = 0; h < (kTn + 63) / 64; ++h)
-              tma_load_3d(sb + h * (kTk * 128), &map_b, &full[s], col + h * 64, k, pb);
-          } else {
-            tma_load_3d(sb, &map_b, &full[s], k, col, pb);
+              for (int h = 0; h < kTm / 64; ++h)
+                tma_load_3d(sa + h * (kTk * 128), &map_a, &full[s], row + h * 64, k, p);
+            } else {
+              tma_load_3d(sa, &map_a, &full[s], k, row, p);
+            }
+            if (b_mn) {
+#pragma unroll
+              for (int h = 0; h < (kTn + 63) / 64; ++h)
+                tma_load_3d(sb + h * (kTk * 128), &map_b, &full[s], col + h * 64, k, p);
+            } else {
+              tma_load_3d(sb, &map_b, &full[s], k, col, p);
+            }
           }
           ++issued;
         }
@@ -367,13 +363,12 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && mine > 0) {
       const uint32_t idesc = make_idesc_bf16(kTm, kTn, a.a_mn != 0, a.b_mn != 0);
-      const StepDesc da(smem_u32(ring), a.a_mn != 0), db(smem_u32(ring) + Cfg::kA, a.b_mn != 0);
+      const StepDesc da(smem_u32(ring), a.a_mn != 0), db(smem_u32(ring) + kPlanes<T> * Cfg::kA, a.b_mn != 0);
       RingPos<kStages> pos;
       AccPos<2> set;
       bool ok = true, issued = false;
       for (int j = 0; j < mine && ok; ++j) {
         const GemmUnit g = gemm_unit(a, first + j * stride);
-        UnitPos at(g.u0, a.npairs);
         for (int c0 = g.u0, c1; c0 < g.u1 && ok; c0 = c1, set.next()) {
           c1 = g.u1 - c0 < kAccUnits<T> ? g.u1 : c0 + kAccUnits<T>;
           if (!wait_long(&acce[set.set], set.parity ^ 1, DPRC_DEVERR_ACCUM, abort_flag)) {
@@ -383,8 +378,7 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
           }
           tc_fence_after();
           const uint32_t acc = tmem + set.set * kAccs<T> * kTn;
-          uint32_t begun = 0;  // bit i: accumulator i of the set holds sums
-          for (int u = c0; u < c1; ++u, pos.next(), at.next()) {
+          for (int u = c0; u < c1; ++u, pos.next()) {
             const int s = pos.s;
             if (!wait_long(&full[s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag)) {
               *abort_flag = 1;
@@ -393,12 +387,16 @@ __global__ void __launch_bounds__(GemmCfg<kTn>::kThreads, 1)
             }
             tc_fence_after();
             const uint64_t ad = da.at(s * Cfg::kStage), bd = db.at(s * Cfg::kStage);
-            const int which = kAccs<T> == 2 && at.pair != 0 ? 1 : 0;
 #pragma unroll
-            for (int kk = 0; kk < kTk / 16; ++kk)
-              umma_bf16(acc + which * kTn, ad + kk * da.step, bd + kk * db.step, idesc,
-                 ((begun >> which) & 1u) | (kk != 0));
-            begun |= 1u << which;
+            for (int i = 0; i < kProducts<T>; ++i) {
+              // the first product in one accumulator, the small ones in the other
+              const uint32_t d = acc + (i == 0 ? 0 : kTn);
+              const uint64_t ai = ad + plane_a(i) * (Cfg::kA >> 4), bi = bd + plane_b(i) * (Cfg::kB >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kTk / 16; ++kk)
+                umma_bf16(d, ai + kk * da.step, bi + kk * db.step, idesc,
+                   (u == c0 && i <= 1 && kk == 0) ? 0u : 1u);
+            }
             umma_commit(&empty[s]);
             issued = true;
           }
@@ -466,12 +464,16 @@ cudaError_t set_smem_once(F* kernel, int bytes) {
 constexpr int kPairTile = 256;
 constexpr double kPairStep = 600.0;  // cycles of a 64-deep step
 constexpr int kPairA = kTm * kTk * 2;
-constexpr int kPairStage = 2 * kPairA;
-constexpr int kPairStages = 7;
+// bf16: seven stages of 32 KB; fp32: two of 96 KB, which feed 24 MMAs each.
+template <typename T>
+constexpr int kPairStageBytes = kPlanes<T> * 2 * kPairA;
+template <typename T>
+constexpr int kPairRing = sizeof(T) == 4 ? 2 : 7;
 // Epilogue warps: fp32 keeps its sums in registers, 64 columns a warp.
 template <typename T>
 constexpr int kPairEpiWarps = sizeof(T) == 4 ? 16 : 8;
-constexpr int kPairSmem = kPairStages * kPairStage + 1024 + 512;
+template <typename T>
+constexpr int kPairSmem = kPairRing<T> * kPairStageBytes<T> + 1024 + 512;
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -553,11 +555,12 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
                             const __grid_constant__ CUtensorMap map_b1,
                             const __grid_constant__ GemmBatch batch) {
   constexpr int kEpi = kPairEpiWarps<T>;
+  constexpr int kStages = kPairRing<T>, kStage = kPairStageBytes<T>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align_1024(smem_raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kPairStages * kPairStage);
-  uint64_t* empty = full + kPairStages;
-  uint64_t* accf = empty + kPairStages;  // [2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * kStage);
+  uint64_t* empty = full + kStages;
+  uint64_t* accf = empty + kStages;  // [2]
   uint64_t* acce = accf + 2;             // [2]
   uint64_t* drain = acce + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -574,7 +577,7 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
   const int mine = work.mine0 + work.mine1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
 
   if (warp == 0) {
     if (lane == 0 && mine > 0) {
-      RingPos<kPairStages> pos;
+      RingPos<kStages> pos;
       long long issued = 0;
       bool ok = true;
       const uint32_t full0 = map_to_rank(full, 0);
@@ -609,32 +612,32 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
         const GemmUnit g = gemm_unit(a, work.at(j));
         const int row = g.m * kPairTile + rank * kTm, col = g.n * kPairTile + rank * kTm;
         const bool a_mn = a.a_mn != 0, b_mn = a.b_mn != 0;
-        UnitPos at(g.u0, a.npairs);
-        for (int u = g.u0; u < g.u1; ++u, pos.next(), at.next()) {
+        for (int u = g.u0; u < g.u1; ++u, pos.next()) {
           const int s = pos.s;
           if (!wait_long(&empty[s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
             *abort_flag = 1;
             ok = false;
             break;
           }
-          int pa = 0, pb = 0;
-          if (at.npairs > 1) plane_pair(at.pair, pa, pb);
-          const int k = at.kb * kTk;
-          uint8_t* sa = ring + s * kPairStage;
-          uint8_t* sb = sa + kPairA;
+          const int k = u * kTk;
+          uint8_t* sa = ring + s * kStage;
+          uint8_t* sb = sa + kPlanes<T> * kPairA;
           const uint32_t bar = full0 + s * 8;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStage);
-          if (a_mn) {
-            tma_load_3d_pair(sa, map_a, bar, row, k, pa);
-            tma_load_3d_pair(sa + kTk * 128, map_a, bar, row + 64, k, pa);
-          } else {
-            tma_load_3d_pair(sa, map_a, bar, k, row, pa);
-          }
-          if (b_mn) {
-            tma_load_3d_pair(sb, map_b, bar, col, k, pb);
-            tma_load_3d_pair(sb + kTk * 128, map_b, bar, col + 64, k, pb);
-          } else {
-            tma_load_3d_pair(sb, map_b, bar, k, col, pb);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+#pragma unroll
+          for (int p = 0; p < kPlanes<T>; ++p, sa += kPairA, sb += kPairA) {
+            if (a_mn) {
+              tma_load_3d_pair(sa, map_a, bar, row, k, p);
+              tma_load_3d_pair(sa + kTk * 128, map_a, bar, row + 64, k, p);
+            } else {
+              tma_load_3d_pair(sa, map_a, bar, k, row, p);
+            }
+            if (b_mn) {
+              tma_load_3d_pair(sb, map_b, bar, col, k, p);
+              tma_load_3d_pair(sb + kTk * 128, map_b, bar, col + 64, k, p);
+            } else {
+              tma_load_3d_pair(sb, map_b, bar, k, col, p);
+            }
           }
           ++issued;
         }
@@ -642,21 +645,20 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
       // let both CTAs' copies land before either can exit (the closing
       // cluster barrier holds the other one)
       if (rank == 0)
-        for (long long k = issued - 1; k >= 0 && k >= issued - kPairStages; --k)
-          mbar_wait(&full[k % kPairStages], (k / kPairStages) & 1, DPRC_DEVERR_PIPE_FULL);
+        for (long long k = issued - 1; k >= 0 && k >= issued - kStages; --k)
+          mbar_wait(&full[k % kStages], (k / kStages) & 1, DPRC_DEVERR_PIPE_FULL);
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0 && mine > 0) {
-      RingPos<kPairStages> pos;
+      RingPos<kStages> pos;
       AccPos<kPairSets<T>> set;
       bool ok = true, issued = false;
       for (int j = 0; j < mine && ok; ++j) {
         const GemmArgs& a = batch.p[j >= work.mine0];
         const uint32_t idesc = make_idesc_bf16(kPairTile, kPairTile, a.a_mn != 0, a.b_mn != 0);
         const StepDesc da(smem_u32(ring), a.a_mn != 0);
-        const StepDesc db(smem_u32(ring) + kPairA, a.b_mn != 0);
+        const StepDesc db(smem_u32(ring) + kPlanes<T> * kPairA, a.b_mn != 0);
         const GemmUnit g = gemm_unit(a, work.at(j));
-        UnitPos at(g.u0, a.npairs);
         for (int c0 = g.u0, c1; c0 < g.u1 && ok; c0 = c1, set.next()) {
           c1 = g.u1 - c0 < kAccUnits<T> ? g.u1 : c0 + kAccUnits<T>;
           if (!wait_long(&acce[set.set], set.parity ^ 1, DPRC_DEVERR_ACCUM, abort_flag)) {
@@ -666,8 +668,7 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
           }
           tc_fence_after();
           const uint32_t acc = tmem + set.set * kAccs<T> * kPairTile;
-          uint32_t begun = 0;  // bit i: accumulator i of the set holds sums
-          for (int u = c0; u < c1; ++u, pos.next(), at.next()) {
+          for (int u = c0; u < c1; ++u, pos.next()) {
             const int s = pos.s;
             if (!wait_long(&full[s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag)) {
               *abort_flag = 1;
@@ -675,13 +676,17 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
               break;
             }
             tc_fence_after();
-            const uint64_t ad = da.at(s * kPairStage), bd = db.at(s * kPairStage);
-            const int which = kAccs<T> == 2 && at.pair != 0 ? 1 : 0;
+            const uint64_t ad = da.at(s * kStage), bd = db.at(s * kStage);
 #pragma unroll
-            for (int kk = 0; kk < kTk / 16; ++kk)
-              umma_bf16_pair(acc + which * kPairTile, ad + kk * da.step, bd + kk * db.step, idesc,
-                 ((begun >> which) & 1u) | (kk != 0));
-            begun |= 1u << which;
+            for (int i = 0; i < kProducts<T>; ++i) {
+              // the first product in one accumulator, the small ones in the other
+              const uint32_t d = acc + (i == 0 ? 0 : kPairTile);
+              const uint64_t ai = ad + plane_a(i) * (kPairA >> 4), bi = bd + plane_b(i) * (kPairA >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kTk / 16; ++kk)
+                umma_bf16_pair(d, ai + kk * da.step, bi + kk * db.step, idesc,
+                   (u == c0 && i <= 1 && kk == 0) ? 0u : 1u);
+            }
             umma_commit_pair(&empty[s]);
             issued = true;
           }
@@ -731,10 +736,10 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
 
 template <typename T>
 cudaError_t launch_gemm_pair(const CUtensorMap* maps, const GemmBatch& batch, cudaStream_t s) {
-  const cudaError_t e = set_smem_once<2 + sizeof(T)>(linear_gemm_pair_kernel<T>, kPairSmem);
+  const cudaError_t e = set_smem_once<2 + sizeof(T)>(linear_gemm_pair_kernel<T>, kPairSmem<T>);
   if (e != cudaSuccess) return e;
   const long long pairs = std::min<long long>(static_cast<long long>(batch.n0) + batch.n1, device_sm_count() / 2);
-  linear_gemm_pair_kernel<T><<<static_cast<unsigned>(2 * pairs), 64 + 32 * kPairEpiWarps<T>, kPairSmem, s>>>(
+  linear_gemm_pair_kernel<T><<<static_cast<unsigned>(2 * pairs), 64 + 32 * kPairEpiWarps<T>, kPairSmem<T>, s>>>(
       maps[0], maps[1], maps[2], maps[3], batch);
   return cudaGetLastError();
 }
@@ -764,7 +769,7 @@ long long deal_units(long long n0, int u0, long long n1, int u1, long long pairs
 template <int kTn, typename T>
 cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a,
                           cudaStream_t s) {
-  using Cfg = GemmCfg<kTn>;
+  using Cfg = GemmCfg<kTn, T>;
   cudaError_t e = set_smem_once<kTn * 8 + sizeof(T)>(linear_gemm_kernel<kTn, T>, Cfg::kSmem);
   if (e != cudaSuccess) return e;
   const long long work = static_cast<long long>(a.mt) * a.nt * a.split;
@@ -807,7 +812,7 @@ cudaError_t read_device_error_linear(int32_t* out, bool reset) {
 
 GemmPlan plan_gemm(const GemmShape& g) {
   GemmPlan p;
-  p.units = (g.K + kTk - 1) / kTk * (g.planes > 1 ? 6 : 1);
+  p.units = (g.K + kTk - 1) / kTk;
   const int sms = device_sm_count();
   // Candidates: the tile shapes and contraction shares; the cost of one is its
   // waves of units (in cycles of a 64-deep step, measured: the pair's step runs
@@ -823,7 +828,8 @@ GemmPlan plan_gemm(const GemmShape& g) {
   const Shape few[] = {{128, 16, 1, 200.0}, {128, 32, 1, 210.0}, {128, 64, 1, 260.0}};
   const Shape* shapes = g.transposed ? few : wide;
   const int nshapes = g.transposed ? 3 : 4;
-  const int64_t whole = g.planes > 1 ? 6 : 1;
+  const double products = g.planes > 1 ? 6.0 : 1.0;
+  const int64_t least = g.planes > 1 ? 1 : 4;  // units of a share
   double best = 1e300;
   for (int i = 0; i < nshapes; ++i) {
     const Shape& sh = shapes[i];
@@ -831,14 +837,14 @@ GemmPlan plan_gemm(const GemmShape& g) {
     if (g.planes > 1 && sh.tn == 256 && sh.ctas == 1) continue;  // 128 sums a thread
     const int64_t tiles = (g.rows + sh.tm - 1) / sh.tm * ((g.cols + sh.tn - 1) / sh.tn);
     const int64_t slots = sms / sh.ctas;
-    const int64_t max_split = p.units < 4 ? 1 : (p.units / 4 < 64 ? p.units / 4 : 64);
-    for (int64_t want = 1; want <= max_split; ++want) {
-      // (whole steps of the contraction: both accumulators of fp32 get a share)
-      const int64_t per = ((p.units + want - 1) / want + whole - 1) / whole * whole;
+    const int64_t max_split = std::max<int64_t>(1, std::min<int64_t>(p.units / least, 64));
+    for (int64_t want : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64}) {
+      if (want > max_split) break;
+      const int64_t per = (p.units + want - 1) / want;
       const int64_t split = (p.units + per - 1) / per;
       if (split != want) continue;
       const int64_t waves = (tiles * split + slots - 1) / slots;
-      double cost = static_cast<double>(waves) * (per * sh.step + 200.0) + 8.0 * sh.tn;
+      double cost = static_cast<double>(waves) * (per * sh.step * products + 200.0) + 8.0 * sh.tn;
       const bool partial = split > 1 || g.transposed;
       if (partial)  // written and read through L2 at some 5 KB a cycle, and a launch
         cost += 3000.0 + static_cast<double>(split) * g.rows * g.cols * 8.0 / 5000.0;
@@ -871,6 +877,7 @@ cudaError_t prepare_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperan
                          const GemmOperand& B, const LinearEpi& epi, void* part, CUtensorMap* maps,
                          GemmArgs& a) {
   if (B.mn_major && p.tn < 64) return cudaErrorInvalidValue;  // its boxes are 64 wide
+  if (p.per < 1) return cudaErrorInvalidValue;                // no work: the waits would run out
   const int tile_m = p.pair ? kPairTile : kTm, tile_n = p.pair ? kPairTile : p.tn;
   if (!operand_map(&maps[0], A, g.rows, g.K, g.planes, kTm)) return cudaErrorInvalidValue;
   if (!operand_map(&maps[1], B, g.cols, g.K, g.planes, p.pair ? kTm : p.tn))
@@ -884,7 +891,6 @@ cudaError_t prepare_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperan
   a.split = p.split;
   a.units = static_cast<int>(p.units);
   a.per_split = static_cast<int>(p.per);
-  a.npairs = g.planes > 1 ? 6 : 1;
   a.a_mn = A.mn_major;
   a.b_mn = B.mn_major;
   a.transposed = g.transposed;
@@ -932,7 +938,7 @@ bool gemm_together(const GemmShape& g0, const GemmPlan& p0, const GemmShape& g1,
   const long long load =
       deal_units(tiles(g0), static_cast<int>(p0.units), tiles(g1), static_cast<int>(p1.units),
                  device_sm_count() / 2, extra, a_units);
-  return load * kPairStep + 2048.0 < p0.cost + p1.cost;
+  return load * kPairStep * (g0.planes > 1 ? 6.0 : 1.0) + 2048.0 < p0.cost + p1.cost;
 }
 
 cudaError_t launch_gemm_two(const GemmTask& t0, const GemmTask& t1, dprc_dtype dt,
