@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const PackArgs a) {
 // rounding of the results.
 // ---------------------------------------------------------------------------
 constexpr int kDzWarps = 8;
-constexpr int kDzAhead = 4;
+constexpr int kDzAhead = 2;
 
 // Eight values as they are stored, so that rows on their way cost few registers.
 template <typename T>
@@ -143,7 +143,7 @@ struct DzArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kDzWarps, 2) linear_dz_kernel(const DzArgs a) {
+__global__ void __launch_bounds__(32 * kDzWarps, 4) linear_dz_kernel(const DzArgs a) {
   __shared__ float s_sum[kDzWarps][256];
   constexpr bool kFast = sizeof(T) == 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -200,6 +200,34 @@ __global__ void __launch_bounds__(32 * kDzWarps, 2) linear_dz_kernel(const DzArg
 #pragma unroll
     for (int w = 0; w < kDzWarps; ++w) t += s_sum[w][threadIdx.x];
     a.colsum[static_cast<long long>(rb) * a.N + c] = t;
+  }
+}
+
+// dZ without the column sums, where its rows are whole 16-byte accesses: then
+// [M][N] is one run of groups of 8, and threads with little state stream it at
+// 0.98 of the copy rate (16384 x 8192 bf16, SiLU: 121 us; the kernel above 139,
+// with dropout 197 against 122).
+template <typename T, bool kDrop>
+__global__ void __launch_bounds__(256) linear_dz_flat_kernel(const DzArgs a) {
+  constexpr bool kFast = sizeof(T) == 2;
+  const long long groups = a.M * (a.N / 8);
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  const RoundKeys rk = round_keys(a.drop.seed);
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < groups;
+       i += stride) {
+    Raw8<T> g8, z8;
+    raw_ld(static_cast<const T*>(a.dY) + 8 * i, 8, true, g8);
+    if (a.act != DPRC_ACT_NONE) raw_ld(static_cast<const T*>(a.Z) + 8 * i, 8, true, z8);
+    float g[8], z[8];
+    raw_get(g8, g);
+    if (kDrop)
+      drop8(g, philox_block(static_cast<uint64_t>(i), a.drop.step, rk), a.drop.thr, a.drop.keep);
+    if (a.act != DPRC_ACT_NONE) {
+      raw_get(z8, z);
+      act_slope8<kFast>(g, z, a.act);
+    }
+    if (a.dZ != nullptr) st8(static_cast<T*>(a.dZ) + 8 * i, g);
+    if (a.planes != nullptr) store_planes<T>(a.planes + 8 * i, a.plane, g);
   }
 }
 
@@ -506,7 +534,21 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, void* ws, cudaStream_t s
     a.dZ = c.dZ;
     a.colsum = c.db != nullptr ? reinterpret_cast<float*>(w + l.sum_off) : nullptr;
     const unsigned grid = static_cast<unsigned>((c.N + 255) / 256 * l.nblocks);
-    if (c.dtype == DPRC_F32)
+    if (c.db == nullptr && a.vec) {
+      const int64_t groups = c.M * (c.N / 8);
+      const unsigned flat = static_cast<unsigned>(
+          std::min<int64_t>((groups + 255) / 256, int64_t(device_sm_count()) * 64));
+      if (c.dtype == DPRC_F32) {
+        if (drop.thr != 0)
+          linear_dz_flat_kernel<float, true><<<flat, 256, 0, s>>>(a);
+        else
+          linear_dz_flat_kernel<float, false><<<flat, 256, 0, s>>>(a);
+      } else if (drop.thr != 0) {
+        linear_dz_flat_kernel<__nv_bfloat16, true><<<flat, 256, 0, s>>>(a);
+      } else {
+        linear_dz_flat_kernel<__nv_bfloat16, false><<<flat, 256, 0, s>>>(a);
+      }
+    } else if (c.dtype == DPRC_F32)
       linear_dz_kernel<float><<<grid, 32 * kDzWarps, 0, s>>>(a);
     else
       linear_dz_kernel<__nv_bfloat16><<<grid, 32 * kDzWarps, 0, s>>>(a);
