@@ -2,9 +2,11 @@
 
 The compute lives in libdprc.so (C ABI: include/dprc.h): tensor-core
 Hutchinson and Hutch++ per-sample gradient-norm estimation, the exact norm
-(direct and ghost-clipping forms), clip factors and Philox Gaussian noise.
-This package is its ctypes binding plus the seeded synthetic workloads used by
-the tests and the benchmark.
+(direct and ghost-clipping forms), clip factors and Philox Gaussian noise; and
+the operators around that path: the embedding (lookup, per-sample norm, clipped
+gradient), dropout and the linear map with its epilogue and gradient.
+This package is its ctypes binding, torch modules over it (layers), the training
+step, and the seeded synthetic workloads used by the tests and the benchmark.
 """
 
 from .binding import (  # noqa: F401
@@ -56,4 +58,5 @@ from .binding import (  # noqa: F401
     lib,
     workspace,
 )
+from . import layers  # noqa: F401,E402
 from .step import RandomizedClippingStep  # noqa: F401,E402

@@ -1,0 +1,158 @@
+"""torch.nn modules over the operators around the norm path.
+
+`Embedding`, `Linear` (bias, activation, dropout and residual in one call) and
+`Dropout` run on libdprc (dprc_embed_*, dprc_linear*, dprc_dropout) in both
+directions, and `RandomizedClippingStep` takes their parameters: the embedding
+and the biases by their exact per-sample norms, the linear weights by the
+estimates.  Device tensors of float32 or bfloat16 only; the library raises on
+anything else.
+
+Dropout masks come from the library's Philox stream under (seed, step): `seed`
+is the module's, `step` counts its training forward passes (set `step` to
+repeat or resume a run).  A mask is not stored: the backward passes of one
+forward pass, a clipping step has two, draw it again.
+"""
+
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import binding as rnc
+
+
+def _dense(t):
+    """t as the library takes it: contiguous, from a 16-byte boundary on."""
+    if t is None:
+        return None
+    t = t.detach().contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+class _Lookup(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, weight, scale):
+        tokens = _dense(tokens)
+        ctx.save_for_backward(tokens)
+        ctx.scale, ctx.shape, ctx.dtype = scale, weight.shape, weight.dtype
+        return rnc.dprc_embed_lookup(_dense(weight), tokens, scale=scale)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (tokens,) = ctx.saved_tensors
+        V, d = ctx.shape
+        flat = tokens.reshape(1, -1)
+        plan = rnc.dprc_embed_plan(flat, V)
+        dW = torch.empty((V, d), dtype=ctx.dtype, device=grad.device)
+        G = _dense(grad.to(ctx.dtype)).view(1, -1, d)
+        return None, rnc.dprc_embed_grad(G, plan, dW, scale=ctx.scale), None
+
+
+class Embedding(torch.nn.Module):
+    """Rows of `weight` [num_embeddings][embedding_dim] times `scale`; a
+    negative token gives a zero row and has no gradient."""
+
+    def __init__(self, num_embeddings, embedding_dim, scale=1.0, device=None, dtype=None):
+        super().__init__()
+        self.num_embeddings, self.embedding_dim = int(num_embeddings), int(embedding_dim)
+        self.scale = float(scale)
+        self.weight = torch.nn.Parameter(
+            torch.randn(num_embeddings, embedding_dim, device=device, dtype=dtype))
+
+    def forward(self, tokens):
+        return _Lookup.apply(tokens, self.weight, self.scale)
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, step):
+        ctx.args = (p, seed, step)
+        return rnc.dprc_dropout(_dense(x), p, seed, step, residual=_dense(residual))
+
+    @staticmethod
+    def backward(ctx, grad):
+        dx = rnc.dprc_dropout(_dense(grad), *ctx.args) if ctx.needs_input_grad[0] else None
+        return dx, grad if ctx.needs_input_grad[1] else None, None, None, None
+
+
+class Dropout(torch.nn.Module):
+    """residual + dropout(x); the identity (plus the residual) outside training."""
+
+    def __init__(self, p=0.1, seed=0):
+        super().__init__()
+        self.p, self.seed, self.step = float(p), int(seed), 0
+
+    def forward(self, x, residual=None):
+        if not self.training or self.p == 0.0:
+            return x if residual is None else x + residual
+        self.step += 1
+        return _Dropout.apply(x, residual, self.p, self.seed, self.step)
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, module, p, step, keep):
+        x, w = _dense(x), _dense(weight)
+        z = None
+        if keep and module.act != "none":
+            z = torch.empty((*x.shape[:-1], w.shape[0]), dtype=x.dtype, device=x.device)
+        ctx.save_for_backward(x, w, z)
+        ctx.module, ctx.p, ctx.step = module, p, step
+        module._last = (z, p, step)
+        return rnc.dprc_linear(x, w, bias=_dense(bias), act=module.act, p=p,
+                               seed=module.seed, step=step, residual=_dense(residual), Z=z)
+
+    @staticmethod
+    def backward(ctx, grad):
+        x, w, z = ctx.saved_tensors
+        m = ctx.module
+        grad = _dense(grad)
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        if m.norm_pass:  # the clipping step's first backward: no weight gradients
+            need_w = need_b = False
+        dx = torch.empty_like(x) if need_x else None
+        dw = torch.empty_like(w) if need_w else None
+        db = torch.empty(w.shape[0], dtype=w.dtype, device=w.device) if need_b else None
+        if need_x or need_w or need_b:
+            rnc.dprc_linear_grad(grad, x, w, Z=z, act=m.act, p=ctx.p, seed=m.seed, step=ctx.step,
+                                 dX=dx, dW=dw, db=db)
+        return dx, dw, db, grad if need_r else None, None, None, None, None
+
+
+class Linear(torch.nn.Module):
+    """residual + dropout(act(x W^T + bias)), in one call."""
+
+    def __init__(self, in_features, out_features, bias=False, act="none", p=0.0, seed=0,
+                 device=None, dtype=None):
+        super().__init__()
+        if act not in rnc.DPRC_ACTS:
+            raise ValueError(f"act must be one of {sorted(rnc.DPRC_ACTS)}")
+        self.in_features, self.out_features = int(in_features), int(out_features)
+        self.act, self.p, self.seed, self.step = act, float(p), int(seed), 0
+        self.norm_pass = False
+        self._last = None
+        self.weight = torch.nn.Parameter(
+            torch.randn(out_features, in_features, device=device, dtype=dtype)
+            / math.sqrt(in_features))
+        self.bias = (torch.nn.Parameter(torch.zeros(out_features, device=device, dtype=dtype))
+                     if bias else None)
+
+    def forward(self, x, residual=None):
+        p = self.p if self.training else 0.0
+        if p > 0.0:
+            self.step += 1
+        return _Linear.apply(x, self.weight, self.bias, residual, self, p, self.step,
+                             torch.is_grad_enabled())
+
+    def preactivation_grad(self, dy, last):
+        """The gradient with respect to x W^T + bias, from that with respect to
+        the output: what the norm estimates take as G.  `last` is what the
+        forward pass left in `_last`."""
+        z, p, step = last
+        if self.act == "none" and p == 0.0:
+            return dy
+        g = torch.empty_like(dy)
+        rnc.dprc_linear_grad(dy, None, _dense(self.weight), Z=z, act=self.act, p=p,
+                             seed=self.seed, step=step, dZ=g)
+        return g

@@ -23,11 +23,16 @@ asks autograd only for the gradients with respect to the recorded layer
 outputs, so no weight gradient is formed before the clip factors are known.
 
 Scope: every trainable parameter must be the weight of an nn.Linear without
-bias (per-sample norms of other parameter kinds need their own per-sample
-gradients, which the method does not cover); each layer runs once per
+bias, the weight or bias of a `layers.Linear`, or the weight of an embedding
+(`layers.Embedding`, or a plain nn.Embedding); the norms of biases and
+embeddings are exact and cheap (dprc_embed_norm: a group sum of the output
+gradients), other kinds (normalisation gains) would need their own per-sample
+gradients, which the method does not cover.  Each layer runs once per
 forward pass on inputs (B, ..., d) (every position between the batch and the
 feature axis counts as a token), and the per-sample losses must not couple
-samples.  Projections are drawn fresh per (layer, step) from a seeded
+samples.  An embedding's clipped gradient is formed from the recorded output
+gradients and the clip factors (dprc_embed_grad), so the second backward stops
+at the linear parameters.  Projections are drawn fresh per (layer, step) from a seeded
 generator (a reading of the pages, which do not say how often P is redrawn):
 P ~ N(0, 1/k) for Hutchinson, S and P ~ N(0, 1) for Hutch++.  Dividing the
 noisy sum by the batch size is left to the optimiser.
@@ -38,6 +43,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as rnc
+from . import layers as lay
 
 _MIX = 0x9E3779B97F4A7C15
 
@@ -52,11 +58,11 @@ def _seed(*parts):
 
 
 class RandomizedClippingStep:
-    """DP-SGD-RC gradient step for the nn.Linear weights of `model`.
+    """DP-SGD-RC gradient step for the parameters of `model`.
 
     Args:
-      model: the module; all its trainable parameters must be bias-free
-        nn.Linear weights.
+      model: the module; its trainable parameters must be those of bias-free
+        nn.Linear, of `layers.Linear` and of embeddings.
       C: clipping threshold.
       sigma: noise multiplier (0 disables the noise).
       k: projection width (Hutchinson) or r (Hutch++, k = 16).
@@ -74,19 +80,37 @@ class RandomizedClippingStep:
         self.method = method
         self.seed = int(seed)
         self.layers = [m for m in model.modules()
-                       if isinstance(m, torch.nn.Linear) and m.weight.requires_grad]
+                       if isinstance(m, (torch.nn.Linear, lay.Linear)) and m.weight.requires_grad]
+        self.biased = [m for m in model.modules() if isinstance(m, lay.Linear)
+                       and m.bias is not None and m.bias.requires_grad]
+        self.embeddings = [m for m in model.modules()
+                           if isinstance(m, (torch.nn.Embedding, lay.Embedding))
+                           and m.weight.requires_grad]
         covered = {id(m.weight) for m in self.layers}
+        for m in self.embeddings:
+            if id(m.weight) in covered:
+                raise ValueError("an embedding's weight is shared with another layer; the norm of "
+                                 "a sum of two layers' gradients is not the sum of their norms")
+            covered.add(id(m.weight))
+            if getattr(m, "max_norm", None) is not None or getattr(m, "scale_grad_by_freq", False) \
+                    or getattr(m, "sparse", False):
+                raise ValueError("nn.Embedding with max_norm, scale_grad_by_freq or sparse "
+                                 "gradients is not supported")
+        covered |= {id(m.bias) for m in self.biased}
         for name, prm in model.named_parameters():
             if prm.requires_grad and id(prm) not in covered:
                 raise ValueError(f"trainable parameter {name!r} is not a bias-free "
                                  "nn.Linear weight; per-sample norms cover only those")
         for m in self.layers:
-            if m.bias is not None and m.bias.requires_grad:
+            if isinstance(m, torch.nn.Linear) and m.bias is not None and m.bias.requires_grad:
                 raise ValueError("nn.Linear layers with a trainable bias are not supported")
         self._acts = {}
         self._outs = {}
-        self._handles = [m.register_forward_hook(self._record) for m in self.layers]
+        self._lasts = {}
+        recorded = list(dict.fromkeys(self.layers + self.biased + self.embeddings))
+        self._handles = [m.register_forward_hook(self._record) for m in recorded]
         self._ws = {}
+        self._bias_plans = {}
 
     def close(self):
         """Removes the hooks."""
@@ -98,6 +122,22 @@ class RandomizedClippingStep:
         if torch.is_grad_enabled():
             self._acts[module] = inputs[0]
             self._outs[module] = output
+            if isinstance(module, lay.Linear):
+                self._lasts[module] = module._last
+
+    def parameters(self):
+        """The trainable parameters in the order the noise stream runs over
+        them: linear weights, biases, embeddings."""
+        return ([m.weight for m in self.layers] + [m.bias for m in self.biased]
+                + [m.weight for m in self.embeddings])
+
+    def _bias_plan(self, B, T, device):
+        """The plan of the one-row embedding that a bias is: every position 0."""
+        key = (B, T, device)
+        if key not in self._bias_plans:
+            self._bias_plans = {key: rnc.dprc_embed_plan(
+                torch.zeros((B, T), dtype=torch.int32, device=device), 1)}
+        return self._bias_plans[key]
 
     def projections(self, step):
         """The projection(s) of every layer for `step`: P [p][k] (Hutchinson)
@@ -147,29 +187,58 @@ class RandomizedClippingStep:
         if losses.dim() != 1:
             raise ValueError("per_sample_losses must have shape [B]")
         B = losses.shape[0]
-        missing = [m for m in self.layers if m not in self._outs]
-        if missing:
+        recorded = list(dict.fromkeys(self.layers + self.biased + self.embeddings))
+        if any(m not in self._outs for m in self.layers):
             raise RuntimeError("no forward pass recorded for some linear layers")
-        outs = [self._outs[m] for m in self.layers]
+        if any(m not in self._outs for m in recorded):
+            raise RuntimeError("no forward pass recorded for some layers")
         # step 2: gradients with respect to the layer outputs only
-        grads = torch.autograd.grad(losses.sum(), outs, retain_graph=True)
+        fused = [m for m in recorded if isinstance(m, lay.Linear)]
+        for m in fused:
+            m.norm_pass = True
+        try:
+            grads = torch.autograd.grad(losses.sum(), [self._outs[m] for m in recorded],
+                                        retain_graph=True)
+        finally:
+            for m in fused:
+                m.norm_pass = False
+        G_of = {}
+        for m, G in zip(recorded, grads):
+            dt = m.weight.dtype if m in self.embeddings else self._acts[m].dtype
+            G = lay._dense(G.to(dt))
+            if isinstance(m, lay.Linear):
+                G = m.preactivation_grad(G, self._lasts[m])
+            G_of[m] = G.reshape(B, -1, G.shape[-1])
         proj = self.projections(step) if projections is None else projections
         # step 3: layerwise sum of the per-sample estimates
         n = torch.zeros(B, dtype=torch.float32, device=losses.device)
         c = torch.empty_like(n)
+        # the exact norms of biases and embeddings come first, the estimates add
+        for m in self.biased:
+            G = G_of[m]
+            rnc.dprc_embed_norm(G, self._bias_plan(B, G.shape[1], G.device), n, accumulate=True)
+        plans = {}
+        for m in self.embeddings:
+            tokens = self._acts[m].detach().reshape(B, -1)
+            if getattr(m, "padding_idx", None) is not None:
+                tokens = torch.where(tokens == m.padding_idx, -1, tokens)
+            plans[m] = rnc.dprc_embed_plan(lay._dense(tokens), m.weight.shape[0])
+            rnc.dprc_embed_norm(G_of[m], plans[m], n, scale=getattr(m, "scale", 1.0),
+                                accumulate=True)
         As, Gs = [], []
-        for m, G in zip(self.layers, grads):
+        for m in self.layers:
             A = self._acts[m]
             # (B, ..., d): every position between batch and features is a token
             As.append(A.detach().reshape(B, -1, A.shape[-1]).contiguous())
-            Gs.append(G.detach().reshape(B, -1, G.shape[-1]).to(A.dtype).contiguous())
-        one_call = (self.method == "hutch" and len({A.shape[1] for A in As}) == 1
+            Gs.append(G_of[m])
+        more = bool(self.biased or self.embeddings)
+        one_call = (self.method == "hutch" and As and len({A.shape[1] for A in As}) == 1
                     and len({P.shape[1] for P in proj}) == 1 and len({A.dtype for A in As}) == 1)
         if one_call:
             # every layer in one call (persistent launches of up to 56 layers),
             # the clip factors of the layer sum in the same call (step 4)
             ws = self._layers_workspace(As, Gs, proj)
-            rnc.dprc_norm_hutch_layers(As, Gs, proj, n, ws=ws, C=self.C, c=c)
+            rnc.dprc_norm_hutch_layers(As, Gs, proj, n, accumulate=more, ws=ws, C=self.C, c=c)
         else:
             last = len(self.layers) - 1
             for j, (A, G) in enumerate(zip(As, Gs)):
@@ -178,31 +247,44 @@ class RandomizedClippingStep:
                 if self.method == "hutch":
                     ws = self._workspace(rnc.DPRC_OP_HUTCH, A, Bt, T, d, p, proj[j].shape[1])
                     if j == last:  # step 4's clip factors come with the last layer's norms
-                        rnc.dprc_norm_hutch_clip(A, G, proj[j], n, self.C, c, accumulate=j > 0,
-                                                 ws=ws)
+                        rnc.dprc_norm_hutch_clip(A, G, proj[j], n, self.C, c,
+                                                 accumulate=more or j > 0, ws=ws)
                     else:
-                        rnc.dprc_norm_hutch(A, G, proj[j], n, accumulate=j > 0, ws=ws)
+                        rnc.dprc_norm_hutch(A, G, proj[j], n, accumulate=more or j > 0, ws=ws)
                 else:
                     S, P = proj[j]
                     ws = self._workspace(rnc.DPRC_OP_HUTCHPP, A, Bt, T, d, p, S.shape[1])
-                    rnc.dprc_norm_hutchpp(A, G, S, P, n, accumulate=j > 0, ws=ws)
+                    rnc.dprc_norm_hutchpp(A, G, S, P, n, accumulate=more or j > 0, ws=ws)
         # step 4: clip factors (Hutch++: here) and the rescaled second backward
-        if self.method != "hutch":
+        if self.method != "hutch" or not As:
             rnc.dprc_clip_factors(n, self.C, c)
-        for m in self.layers:
-            m.weight.grad = None
-        (c.to(losses.dtype) * losses).sum().backward()
-        # step 5: noise on the aggregated gradient, in place: the weights'
-        # gradients laid end to end in layer order are that gradient, and each
+        for prm in self.parameters():
+            prm.grad = None
+        loss = (c.to(losses.dtype) * losses).sum()
+        if not more:
+            loss.backward()
+        elif self.layers or self.biased:
+            torch.autograd.backward(loss, inputs=[m.weight for m in self.layers]
+                                    + [m.bias for m in self.biased])
+        for m in self.embeddings:
+            dW = torch.empty_like(m.weight)
+            rnc.dprc_embed_grad(G_of[m], plans[m], dW, c=c, scale=getattr(m, "scale", 1.0))
+            m.weight.grad = dW
+        # step 5: noise on the aggregated gradient, in place: the parameters'
+        # gradients laid end to end in parameters() order are that gradient, and each
         # gets the stretch of the one noise stream its position there selects
         if self.sigma > 0.0:
             off = 0
-            for m in self.layers:
-                g = m.weight.grad
+            for prm in self.parameters():
+                g = prm.grad
                 if not g.is_contiguous():
                     raise RuntimeError("weight gradients must be contiguous")
                 rnc.dprc_add_noise_at(g, off, self.sigma, self.C, _seed(self.seed, 2), step)
                 off += g.numel()
         self._acts.clear()
         self._outs.clear()
+        self._lasts.clear()
+        for m in self.layers + self.biased:
+            if isinstance(m, lay.Linear):
+                m._last = None
         return {"n": n, "c": c}
