@@ -502,21 +502,31 @@ _SCRATCH_KEEP = 64 << 20  # larger workspaces are allocated per call
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
 
 
-def _scratch(nbytes, device, stream):
+def _empty(shape, dtype, device, stream, given):
+    """torch.empty for a call on `stream` (a c_void_p): allocated on that stream
+    where the caller gave one (`given` not None), so that the memory's earlier
+    and later uses are ordered against the call."""
+    if given is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream.value or 0, device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(nbytes, device, stream, given):
     """A device workspace of nbytes for one call without a ws argument: kept
     per host thread, device and stream (calls of one thread on one stream run
     one after the other) and grown as needed, so that a call does not pay for
     an allocation.  Large ones, and any during a graph capture (which owns what
     it allocates), are allocated fresh."""
     if nbytes > _SCRATCH_KEEP or _capturing is None or _capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return _empty(nbytes, torch.uint8, device, stream, given)
     kept = _scratch_kept.__dict__
     key = (device.index, stream.value)
     have = kept.get(key)
     if have is None or have[-1].numel() < nbytes:
         size = 1 << max(16, (nbytes - 1).bit_length())
         # outgrown buffers stay: work on the stream may still use them
-        have = (have or ()) + (torch.empty(size, dtype=torch.uint8, device=device),)
+        have = (have or ()) + (_empty(size, torch.uint8, device, stream, given),)
         kept[key] = have
     return have[-1]
 
@@ -544,14 +554,17 @@ def _token_bytes(tokens):
 def dprc_embed_lookup(W, tokens, scale=1.0, out=None, stream=None):
     """out[..., :] = scale * W[tokens[...]], zero rows for negative tokens."""
     V, d = W.shape
-    if out is None:
-        out = torch.empty((*tokens.shape, d), dtype=W.dtype, device=W.device)
     _need_cuda(W, tokens, out)
-    _same("out", out, W.dtype, (*tokens.shape, d), W.device)
+    st = _stream(W, stream)
+    shape = (*tokens.shape, d)
+    if out is None:
+        out = _empty(shape, W.dtype, W.device, st, stream)
+    else:
+        _same("out", out, W.dtype, shape, W.device)
     _check("dprc_embed_lookup",
            lib().dprc_embed_lookup(W.data_ptr(), _dtype_code(W), tokens.data_ptr(),
                                    _token_bytes(tokens), tokens.numel(), V, d, scale,
-                                   out.data_ptr(), _stream(W, stream)))
+                                   out.data_ptr(), st))
     return out
 
 
@@ -574,7 +587,8 @@ def dprc_embed_plan(tokens, V, buf=None, stream=None):
         n = lib().dprc_embed_plan_bytes(B * T, V)
         if n == 0:
             raise DprcError("dprc_embed_plan_bytes", 2)
-        buf = torch.empty(n, dtype=torch.uint8, device=tokens.device)
+        _need_cuda(tokens)
+        buf = _empty(n, torch.uint8, tokens.device, _stream(tokens, stream), stream)
     _need_cuda(tokens, buf)
     _check("dprc_embed_plan",
            lib().dprc_embed_plan(tokens.data_ptr(), size, B * T, V,
@@ -582,14 +596,14 @@ def dprc_embed_plan(tokens, V, buf=None, stream=None):
     return EmbedPlan(B, T, int(V), buf)
 
 
-def _embed_ws(G, plan, ws, stream):
+def _embed_ws(G, plan, ws, stream, given):
     if G.dim() != 3 or G.shape[0] != plan.B or G.shape[1] != plan.T:
         raise ValueError(f"G has shape {tuple(G.shape)}, the plan is of {plan.B} x {plan.T} tokens")
     if ws is None:
         n = lib().dprc_embed_workspace_bytes(_dtype_code(G), plan.B, plan.T, G.shape[2])
         if n == 0:
             raise DprcError("dprc_embed_workspace_bytes", 2)
-        ws = _scratch(n, G.device, stream)
+        ws = _scratch(n, G.device, stream, given)
     return ws
 
 
@@ -598,7 +612,7 @@ def dprc_embed_norm(G, plan, n, scale=1.0, accumulate=False, ws=None, stream=Non
     _need_cuda(G, n, ws, plan.buf)
     _same("n", n, torch.float32, (plan.B,), G.device)
     st = _stream(G, stream)
-    ws = _embed_ws(G, plan, ws, st)
+    ws = _embed_ws(G, plan, ws, st, stream)
     _check("dprc_embed_norm",
            lib().dprc_embed_norm(G.data_ptr(), _dtype_code(G), plan.B, plan.T, plan.V, G.shape[2],
                                  scale, plan.buf.data_ptr(), plan.buf.numel(), n.data_ptr(),
@@ -612,7 +626,7 @@ def dprc_embed_grad(G, plan, dW, c=None, scale=1.0, accumulate=False, ws=None, s
     _same("dW", dW, G.dtype, (plan.V, G.shape[2]), G.device)
     _same("c", c, torch.float32, (plan.B,), G.device)
     st = _stream(G, stream)
-    ws = _embed_ws(G, plan, ws, st)
+    ws = _embed_ws(G, plan, ws, st, stream)
     _check("dprc_embed_grad",
            lib().dprc_embed_grad(G.data_ptr(), _dtype_code(G), _ptr(c), plan.B, plan.T, plan.V,
                                  G.shape[2], scale, plan.buf.data_ptr(), plan.buf.numel(),
@@ -624,24 +638,25 @@ def dprc_embed_grad(G, plan, dW, c=None, scale=1.0, accumulate=False, ws=None, s
 def dprc_dropout(x, p, seed, step, residual=None, first_element=0, out=None, stream=None):
     """residual + dropout(x) with the mask of (seed, step) from element
     first_element on; the gradient is the same call on dy without residual."""
-    if out is None:
-        out = torch.empty_like(x)
     _need_cuda(x, residual, out)
+    st = _stream(x, stream)
+    if out is None:
+        out = _empty(x.shape, x.dtype, x.device, st, stream)
     _same("residual", residual, x.dtype, x.shape, x.device)
     _same("out", out, x.dtype, x.shape, x.device)
     _check("dprc_dropout",
            lib().dprc_dropout(x.data_ptr(), _ptr(residual), _dtype_code(x), x.numel(),
                               int(first_element) & _U64, p, int(seed) & _U64, int(step) & _U64,
-                              out.data_ptr(), _stream(x, stream)))
+                              out.data_ptr(), st))
     return out
 
 
-def _linear_ws(like, M, K, N, grad, ws, stream):
+def _linear_ws(like, M, K, N, grad, ws, stream, given):
     if ws is None:
         n = lib().dprc_linear_workspace_bytes(_dtype_code(like), M, K, N, grad)
         if n == 0:
             raise DprcError("dprc_linear_workspace_bytes", 2)
-        ws = _scratch(n, like.device, stream)
+        ws = _scratch(n, like.device, stream, given)
     return ws
 
 
@@ -655,16 +670,16 @@ def dprc_linear(X, W, bias=None, act="none", p=0.0, seed=0, step=0, residual=Non
     shape = (*X.shape[:-1], N)
     M = X.numel() // K
     dt, dev = X.dtype, X.device
-    if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
     _need_cuda(X, W, bias, residual, Z, out, ws)
+    st = _stream(X, stream)
+    if out is None:
+        out = _empty(shape, dt, dev, st, stream)
     _same("W", W, dt, None, dev)
     _same("bias", bias, dt, (N,), dev)
     _same("residual", residual, dt, shape, dev)
     _same("Z", Z, dt, shape, dev)
     _same("out", out, dt, shape, dev)
-    st = _stream(X, stream)
-    ws = _linear_ws(X, M, K, N, 0, ws, st)
+    ws = _linear_ws(X, M, K, N, 0, ws, st, stream)
     _check("dprc_linear",
            lib().dprc_linear(X.data_ptr(), W.data_ptr(), _ptr(bias), _ptr(residual),
                              _dtype_code(X), M, K, N, DPRC_ACTS[act], p, int(seed) & _U64,
@@ -692,7 +707,7 @@ def dprc_linear_grad(dY, X, W, Z=None, act="none", p=0.0, seed=0, step=0, dX=Non
     _same("db", db, dt, (N,), dev)
     _same("dZ", dZ, dt, dY.shape, dev)
     st = _stream(dY, stream)
-    ws = _linear_ws(dY, M, K, N, 1, ws, st)
+    ws = _linear_ws(dY, M, K, N, 1, ws, st, stream)
     _check("dprc_linear_grad",
            lib().dprc_linear_grad(dY.data_ptr(), _ptr(X), W.data_ptr(), _ptr(Z), _dtype_code(dY),
                                   M, K, N, DPRC_ACTS[act], p, int(seed) & _U64, int(step) & _U64,

@@ -1202,7 +1202,9 @@ dprc_status dprc_device_error(int32_t* out, int reset) {
                                                      read_device_error_qr,
                                                      read_device_error_narrow,
                                                      read_device_error_embed,
-                                                     read_device_error_linear};
+                                                     read_device_error_linear,
+                                                     read_device_error_linear_prep,
+                                                     read_device_error_linear_few};
   int32_t first = 0;
   for (auto rd : readers) {
     int32_t v = 0;

@@ -487,13 +487,13 @@ struct SegArgs {
   float scale;
   // norm: squared sums by original position [N][nblk]; grad: the weights
   float* sq;
-  float* long_sq;     // norm: [nranges][column blocks] squares of the long runs
   const float* c;     // per-sample factors or null
   int accumulate;
   float* part;        // [nranges][2][dpad] partial sums of long runs
   long long dpad;
-  int* long_at;       // [nranges]: 0, or 1 + slot of the long run that begins here, + 4 if
-                      // a long run reaches from here into the next range
+  int* long_at;       // [nranges]: bits 0..1: 0, or 1 + slot of the long run that begins here;
+                      // bit 2: a long run reaches from here into the next range; bits 4..7:
+                      // the entry of the range that the run beginning here begins with
   // grad: rows no token names
   long long zero_units;
 };
@@ -588,7 +588,7 @@ __device__ __forceinline__ RangeRows range_rows(const SegArgs& a, int range, boo
     const u64 rest = M >> (o + 1);
     const int len = rest == 0 ? 64 : __ffsll(static_cast<long long>(rest));
     if (len > kRange) {
-      flags |= 4 | (o == 0 ? 1 : 2);
+      flags |= 4 | (o == 0 ? 1 : 2) | o << 4;
       tail = o;
       last = R;
       E |= 1ull << (R - 1);
@@ -840,7 +840,7 @@ __device__ __forceinline__ float4 add_pieces(const SegArgs& a, long long range, 
 // What becomes of a long run's sums over one block of columns (a warp's).
 template <typename T, bool kNorm>
 __device__ __forceinline__ void finish_run(const SegArgs& a, T* __restrict__ dW, long long range,
-                                           long long col, float4 s) {
+                                           int first, long long col, float4 s) {
   const float f[4] = {s.x, s.y, s.z, s.w};
   if (kNorm) {
     // columns past d hold whatever the workspace held
@@ -850,7 +850,15 @@ __device__ __forceinline__ void finish_run(const SegArgs& a, T* __restrict__ dW,
       if (col + e < a.d) q = fmaf(f[e], f[e], q);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
-    if ((threadIdx.x & 31) == 0) a.long_sq[range * gridDim.y + blockIdx.y] = q;
+    // The run's rows hold zeros in a.sq.  It has at least kRange + 1 of them, and
+    // there are at most kRange times as many of these column blocks as of
+    // a.sq's, so each block's square gets a place of its own among the first.
+    if ((threadIdx.x & 31) == 0) {
+      const int at = static_cast<int>(range) * kRange + first + static_cast<int>(blockIdx.y) % kRange;
+      const int blk = static_cast<int>(blockIdx.y) / kRange;
+      if (DPRC_IN(at < a.N && blk < a.nblk))
+        a.sq[static_cast<long long>(__ldg(a.pos + at)) * a.nblk + blk] = q;
+    }
   } else {
     const uint32_t k = __ldg(a.key + (range + 1) * kRange - 1);  // the run reaches past `range`
     T* out = dW + static_cast<long long>(k) * a.d;
@@ -884,7 +892,8 @@ __global__ void __launch_bounds__(32 * kLongWarps)
   const uint32_t stop0 = __ballot_sync(0xffffffffu, (f0 & 4) == 0 || (f0 & 3) == 2);
   for (int turn = 0; todo != 0; todo &= todo - 1, ++turn) {
     const int j = __ffs(static_cast<int>(todo)) - 1;
-    const int slot = (__shfl_sync(0xffffffffu, f0, j) & 3) - 1;
+    const int fj = __shfl_sync(0xffffffffu, f0, j);
+    const int slot = (fj & 3) - 1, first = fj >> 4;
     const long long range = rbase + j;
     long long end = rbase + 32;
     const uint32_t here = j == 31 ? 0u : stop0 & ~((2u << j) - 1u);
@@ -904,7 +913,7 @@ __global__ void __launch_bounds__(32 * kLongWarps)
     const long long pieces = end - range + 1;
     if (pieces <= kLongAlone) {
       if (turn % kLongWarps == warp)
-        finish_run<T, kNorm>(a, dW, range, col, add_pieces(a, range, slot, 0, pieces, col));
+        finish_run<T, kNorm>(a, dW, range, first, col, add_pieces(a, range, slot, 0, pieces, col));
     } else {  // the same for every warp
       const long long share = (pieces + kLongWarps - 1) / kLongWarps;
       const long long p0 = warp * share;
@@ -919,7 +928,7 @@ __global__ void __launch_bounds__(32 * kLongWarps)
           s.z += v.z;
           s.w += v.w;
         }
-        finish_run<T, kNorm>(a, dW, range, col, s);
+        finish_run<T, kNorm>(a, dW, range, first, col, s);
       }
       __syncthreads();
     }
@@ -927,12 +936,12 @@ __global__ void __launch_bounds__(32 * kLongWarps)
 }
 
 // ---------------------------------------------------------------------------
-// n_i (+)= s^2 (sum of sample i's squares): its positions' squares of every
-// slice, then the long runs that are its own, in a fixed order.  A sample's
-// sum is split over the CTAs of a cluster, which add their parts in rank order.
+// n_i (+)= s^2 (sum of sample i's squares), its positions' squares of every
+// column block in a fixed order.  A sample's sum is split over the CTAs of a
+// cluster, which add their parts in rank order.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
-    embed_norm_finish_kernel(const SegArgs a, int ncb, float* __restrict__ n) {
+    embed_norm_finish_kernel(const SegArgs a, float* __restrict__ n) {
   __shared__ float s_warp[8];
   __shared__ float s_cta[8];
   pdl_wait();
@@ -945,12 +954,6 @@ __global__ void __launch_bounds__(256)
   const float* sq = a.sq + i * count;
 #pragma unroll 8
   for (long long t = t0; t < count; t += step) s += __ldcg(sq + t);
-  for (long long r = t0; r < a.nranges; r += step) {
-    if ((a.long_at[r] & 3) == 0) continue;
-    const long long e = (r + 1) * kRange - 1;  // an entry of the run that begins in r
-    if (sample_of(a, __ldg(a.pos + e)) != i) continue;
-    for (int b = 0; b < ncb; ++b) s += __ldcg(a.long_sq + r * ncb + b);
-  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
   if (lane == 0) s_warp[warp] = s;
@@ -991,7 +994,7 @@ int access_bytes(int64_t d, int elem) {
 struct SegPlan {
   int aw = 16, nblk = 1, threads = 32, ncb = 1;
   int64_t nranges = 0, dpad = 0;
-  size_t part_off = 0, long_off = 0, lsq_off = 0, sq_off = 0, total = 0;
+  size_t part_off = 0, long_off = 0, sq_off = 0, total = 0;
 };
 
 SegPlan seg_plan(dprc_dtype dt, int64_t N, int64_t d, bool norm) {
@@ -1010,8 +1013,6 @@ SegPlan seg_plan(dprc_dtype dt, int64_t N, int64_t d, bool norm) {
   s.part_off = off;
   off = up256(off + static_cast<size_t>(s.nranges) * 2 * s.dpad * 4);
   if (norm) {
-    s.lsq_off = off;
-    off = up256(off + static_cast<size_t>(s.nranges) * s.ncb * 4);
     s.sq_off = off;
     off = up256(off + static_cast<size_t>(s.nblk) * N * 4);
   }
@@ -1087,7 +1088,6 @@ SegArgs seg_args(const EmbedCall& c, const SegPlan& p, const SortPlan& sp, char*
   a.nranges = static_cast<int>(p.nranges);
   a.scale = c.scale;
   a.sq = reinterpret_cast<float*>(ws + p.sq_off);
-  a.long_sq = reinterpret_cast<float*>(ws + p.lsq_off);
   a.c = nullptr;
   a.accumulate = c.accumulate;
   a.part = reinterpret_cast<float*>(ws + p.part_off);
@@ -1257,9 +1257,9 @@ cudaError_t launch_embed_norm(const EmbedCall& c, float* n, void* ws, cudaStream
   cudaError_t e = launch_segments<true>(c.dtype, a, p, c.G, nullptr, s);
   if (e != cudaSuccess) return e;
   // one CTA per sample where a sample has few values, else a cluster of 8
-  const int cl = static_cast<int64_t>(a.T) * p.nblk + a.nranges > 4096 ? 8 : 1;
+  const int cl = static_cast<int64_t>(a.T) * p.nblk > 4096 ? 8 : 1;
   return launch_after(embed_norm_finish_kernel, dim3(static_cast<unsigned>(c.B * cl)), 256, cl, s,
-                      0, a, p.ncb, n);
+                      0, a, n);
 }
 
 cudaError_t launch_embed_grad(const EmbedCall& c, const float* clip, void* dW, void* ws,

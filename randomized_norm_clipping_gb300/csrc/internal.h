@@ -381,6 +381,8 @@ cudaError_t launch_dropout(const void* x, const void* res, dprc_dtype dt, int64_
 
 // ---- the linear map (linear.cu, linear_gemm.cu) ------------------------------
 cudaError_t read_device_error_linear(int32_t* out, bool reset);
+cudaError_t read_device_error_linear_prep(int32_t* out, bool reset);
+cudaError_t read_device_error_linear_few(int32_t* out, bool reset);
 size_t linear_ws_bytes(dprc_dtype dt, int64_t M, int64_t K, int64_t N);
 size_t linear_grad_ws_bytes(dprc_dtype dt, int64_t M, int64_t K, int64_t N);
 struct LinearCall {

@@ -36,10 +36,12 @@ __device__ __forceinline__ uint4 pack_bf16x8(const __nv_bfloat16* h) {
   return *reinterpret_cast<const uint4*>(h);
 }
 
-// x = x0 + x1 + x2, each the bf16 rounding of what is left.  A value that
-// bf16 rounds to infinity, or that is no number, is its first plane alone.
+// x = x0 + x1 + x2, each the bf16 rounding of what is left (the first one
+// towards zero where rounding to nearest would leave bf16's range).  An
+// infinity or NaN is its first plane alone.
 __device__ __forceinline__ void split3(float x, __nv_bfloat16* p) {
   p[0] = __float2bfloat16_rn(x);
+  if (isinf(__bfloat162float(p[0]))) p[0] = __float2bfloat16_rz(x);
   const float r0 = __bfloat162float(p[0]);
   const float r = isfinite(r0) ? x - r0 : 0.f;
   p[1] = __float2bfloat16_rn(r);
@@ -437,6 +439,10 @@ LinearGradPlan linear_grad_plan(dprc_dtype dt, int64_t M, int64_t K, int64_t N) 
 }
 
 }  // namespace
+
+cudaError_t read_device_error_linear_prep(int32_t* out, bool reset) {
+  return read_tu_device_error(out, reset);
+}
 
 size_t linear_ws_bytes(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
   return linear_plan(dt, M, K, N).total;

@@ -63,7 +63,9 @@ __device__ __forceinline__ void act_slope8(float* g, const float* z, int act) {
     for (int e = 0; e < 8; ++e) {
       const float q = z[e] * z[e];
       const float s = sigmoid_f<kFast>(kGelu2C * fmaf(kGeluA * q, z[e], z[e]));
-      g[e] *= fmaf(z[e] * s * (1.f - s), kGelu2C * fmaf(3.f * kGeluA, q, 1.f), s);
+      // (where s (1 - s) has underflowed the slope is s, however large z^2)
+      const float b = z[e] * s * (1.f - s);
+      g[e] *= b == 0.f ? s : fmaf(b, kGelu2C * fmaf(3.f * kGeluA, q, 1.f), s);
     }
   } else if (act == DPRC_ACT_RELU) {
 #pragma unroll

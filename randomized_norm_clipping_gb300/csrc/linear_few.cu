@@ -201,6 +201,10 @@ cudaError_t launch_few_t(const FewArgs& a, int tok, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t read_device_error_linear_few(int32_t* out, bool reset) {
+  return read_tu_device_error(out, reset);
+}
+
 cudaError_t launch_linear_few(const void* X, const void* W, dprc_dtype dt, int64_t M, int64_t K,
                               int64_t N, const LinearEpi& epi, cudaStream_t s) {
   FewArgs a;

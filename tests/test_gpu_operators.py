@@ -447,3 +447,57 @@ def test_operators_on_another_stream():
     nref = ops.embed_norm(ref, tok.cpu().numpy(), 50)
     assert np.allclose(to_f64(n), nref, rtol=1e-4)
     assert np.allclose(to_f64(z), ops.dropout(to_f64(y), 0.1, 1, 1), rtol=1e-6)
+
+
+def test_calls_on_a_given_stream_allocate_there():
+    """out, plan and workspace left to the binding, the stream given by handle."""
+    s = torch.cuda.Stream()
+    x = torch.randn(300, 64, device=DEV)
+    W = torch.randn(40, 64, device=DEV)
+    tok = torch.randint(0, 40, (3, 100), device=DEV)
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        y = rnc.dprc_linear(x, W, act="gelu", stream=stream)
+        e = rnc.dprc_embed_lookup(W, tok, stream=stream)
+        plan = rnc.dprc_embed_plan(tok, 40, stream=stream)
+        n = torch.zeros(3, device=DEV)
+        torch.cuda.synchronize()
+        rnc.dprc_embed_norm(e, plan, n, stream=stream)
+        d = rnc.dprc_dropout(y, 0.5, 1, 2, stream=stream)
+        s.synchronize()
+        ref = ops.linear(to_f64(x), to_f64(W), None, "gelu")[0]
+        assert np.allclose(to_f64(y), ref, rtol=1e-4, atol=1e-4)
+        assert np.allclose(to_f64(d), ops.dropout(to_f64(y), 0.5, 1, 2), rtol=1e-6)
+        assert np.allclose(to_f64(n), ops.embed_norm(to_f64(e), tok.cpu().numpy(), 40), rtol=1e-5)
+
+
+@pytest.mark.parametrize("B,T", [(300, 40), (1500, 17)])
+def test_many_samples_with_long_runs(B, T):
+    """More than 16 equal tokens in every sample, many samples."""
+    tok = torch.randint(0, 2, (B, T), generator=_gen(1)) * 3
+    tok[::3] = 1
+    G = _randn((B, T, 300), "bf16", 2)
+    n = torch.empty(B, device=DEV)
+    rnc.dprc_embed_norm(G.to(DEV), rnc.dprc_embed_plan(tok.to(DEV), 5), n)
+    ref = ops.embed_norm(to_f64(G), tok.numpy(), 5)
+    size = ops.embed_norm(np.abs(to_f64(G)), tok.numpy(), 5)
+    _close(n, ref, (2 * (T + 2) + 40 + np.log2(T * 300)) * ULP * size)
+
+
+def test_values_at_the_ends_of_the_range():
+    """fp32 maps of values next to the largest, and the slopes of large z."""
+    X = torch.zeros(70, 64)
+    X[:, 0] = 3.4e38
+    X[:, 1] = 1.0
+    W = torch.zeros(8, 64)
+    W[:, 0], W[:, 1] = 0.5, 2.0
+    for rows in (4, 70):  # both paths
+        y = rnc.dprc_linear(X[:rows].to(DEV), W.to(DEV))
+        assert torch.isfinite(y).all()
+        ref = to_f64(X[:rows]) @ to_f64(W).T
+        _close(y, ref, 8 * ULP * np.abs(ref))
+    Z = torch.tensor([[3e19, -3e19, 1e30, -1e30, 0.0, 80.0, -80.0, 5.0]] * 3)
+    dZ = torch.empty(3, 8, device=DEV)
+    rnc.dprc_linear_grad(torch.ones(3, 8, device=DEV), None, torch.zeros(8, 16, device=DEV),
+                         Z=Z.to(DEV), act="gelu", dZ=dZ)
+    assert np.allclose(dZ.cpu().numpy()[:, :7], [1, 0, 1, 0, 0.5, 1, 0], atol=1e-6)
