@@ -343,6 +343,14 @@ bool few_tokens(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
   return dt == DPRC_F32 ? nk * (M - 23) <= 100000000 : nk * (M - 2) <= 40000000;
 }
 
+// LinearEpi::vec for rows of N elements at these addresses (null: not used).
+int row_access(dprc_dtype dt, int64_t N, const void* a, const void* b, const void* c) {
+  if (N % 8 != 0) return 0;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+                        reinterpret_cast<uintptr_t>(c);
+  return dt == DPRC_BF16 && N % 16 == 0 && all % 32 == 0 ? 2 : 1;
+}
+
 // Sizes and workspace of a forward call.
 struct LinearPlan {
   bool few = false, pack = false;
@@ -457,7 +465,7 @@ cudaError_t launch_linear(const LinearCall& c, void* ws, cudaStream_t s) {
   LinearEpi epi;
   epi.M = c.M;
   epi.N = static_cast<int>(c.N);
-  epi.vec = c.N % 8 == 0;
+  epi.vec = row_access(c.dtype, c.N, c.res, c.Z, c.Y);
   epi.act = c.act;
   epi.bias = c.bias;
   epi.res = c.res;
@@ -617,7 +625,8 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, void* ws, cudaStream_t s
   tw.B = x;
   tw.A.mn_major = tw.B.mn_major = true;
   tx.epi.N = tw.epi.N = static_cast<int>(c.K);
-  tx.epi.vec = tw.epi.vec = c.K % 8 == 0;
+  tx.epi.vec = row_access(c.dtype, c.K, c.dX, nullptr, nullptr);
+  tw.epi.vec = row_access(c.dtype, c.K, c.dW, nullptr, nullptr);
   tx.epi.M = c.M;
   tx.epi.Y = c.dX;
   tw.epi.M = c.N;

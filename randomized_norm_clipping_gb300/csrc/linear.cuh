@@ -13,7 +13,8 @@ namespace dprc {
 struct LinearEpi {
   long long M = 0;
   int N = 0;
-  int vec = 0;               // N is a multiple of 8: 16-byte accesses
+  int vec = 0;               // 1: N is a multiple of 8, 16-byte accesses; 2: bf16 rows of whole
+                             // 32 bytes, and accesses of as many where a thread has them
   int act = DPRC_ACT_NONE;
   const void* bias = nullptr;  // [N]
   const void* res = nullptr;   // [M][N]
@@ -145,42 +146,95 @@ __device__ __forceinline__ void drop8_at(float* v, uint64_t e0, const DropArgs& 
   for (int h = 0; h < 8; ++h) v[h] = ((keep >> h) & 1u) ? v[h] * d.keep : 0.f;
 }
 
-// Outputs (m, n0 .. n0 + 8 kG) from the fp32 sums v: the loads of all groups
-// first, so that a row's residual is on its way while the rest is computed.
+// 16 bf16 values as one 32-byte access (sm_100 and later): a whole sector, where
+// two accesses of 16 bytes go to L2 as two halves of one.
+__device__ __forceinline__ void ld16_bf16(const __nv_bfloat16* p, float* v) {
+  uint32_t u[8];
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]),
+                 "=r"(u[6]), "=r"(u[7])
+               : "l"(p));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[2 * e] = __uint_as_float(u[e] << 16);
+    v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void st16_bf16(__nv_bfloat16* p, const float* v) {
+  uint32_t u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+    u[e] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]),
+               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+
+// kG groups of 8 neighbouring values of a row from p on (column n of N), to or
+// from memory, by the widest access that vec allows.
+template <typename T, int kG>
+__device__ __forceinline__ void row_ld(const T* p, int n, int N, int vec, float* v) {
+  if constexpr (sizeof(T) == 2 && kG % 2 == 0) {
+    if (vec == 2) {
+#pragma unroll
+      for (int g = 0; g < kG; g += 2)
+        if (n + 8 * g < N) ld16_bf16(p + 8 * g, v + 8 * g);
+      return;
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < kG; ++g)
+    if (n + 8 * g < N) ld_n<T>(p + 8 * g, min(8, N - n - 8 * g), vec != 0, v + 8 * g);
+}
+template <typename T, int kG>
+__device__ __forceinline__ void row_st(T* p, int n, int N, int vec, const float* v) {
+  if constexpr (sizeof(T) == 2 && kG % 2 == 0) {
+    if (vec == 2) {
+#pragma unroll
+      for (int g = 0; g < kG; g += 2)
+        if (n + 8 * g < N) st16_bf16(p + 8 * g, v + 8 * g);
+      return;
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < kG; ++g)
+    if (n + 8 * g < N) st_n<T>(p + 8 * g, min(8, N - n - 8 * g), vec != 0, v + 8 * g);
+}
+
+// Outputs (m, n0 .. n0 + 8 kG) from the fp32 sums v; the residual first, so
+// that it is on its way while the rest is computed.
 template <typename T, int kG>
 __device__ __forceinline__ void linear_out(const LinearEpi& e, long long m, int n0, float* v,
                                            const RoundKeys& rk) {
   constexpr bool kFast = sizeof(T) == 2;
-  const long long base = m * e.N;
-  const bool vec = e.vec != 0;
-  float r[kG][8];
-  if (e.res != nullptr) {
-    const T* res = static_cast<const T*>(e.res) + base;
+  const long long base = m * e.N + n0;
+  if (!DPRC_IN(m < e.M && n0 < e.N)) return;
+  float r[kG * 8];
+  if (e.res != nullptr) row_ld<T, kG>(static_cast<const T*>(e.res) + base, n0, e.N, e.vec, r);
+  if (e.bias != nullptr) {
 #pragma unroll
-    for (int g = 0; g < kG; ++g)
-      if (n0 + 8 * g < e.N) ld_n<T>(res + n0 + 8 * g, min(8, e.N - n0 - 8 * g), vec, r[g]);
+    for (int g = 0; g < kG; ++g) {
+      const int cnt = min(8, e.N - n0 - 8 * g);
+      if (cnt <= 0) continue;
+      float b[8];
+      ld_n<T>(static_cast<const T*>(e.bias) + n0 + 8 * g, cnt, e.vec != 0, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * g + j] += b[j];
+    }
   }
+  if (e.Z != nullptr) row_st<T, kG>(static_cast<T*>(e.Z) + base, n0, e.N, e.vec, v);
 #pragma unroll
   for (int g = 0; g < kG; ++g) {
-    const int n = n0 + 8 * g;
-    const int cnt = min(8, e.N - n);
-    if (cnt <= 0 || !DPRC_IN(m < e.M)) continue;
-    float* x = v + 8 * g;
-    if (e.bias != nullptr) {
-      float b[8];
-      ld_n<T>(static_cast<const T*>(e.bias) + n, cnt, vec, b);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] += b[j];
-    }
-    if (e.Z != nullptr) st_n<T>(static_cast<T*>(e.Z) + base + n, cnt, vec, x);
-    act_value8<kFast>(x, e.act);
-    if (e.drop.thr != 0) drop8_at(x, static_cast<uint64_t>(base + n), e.drop, rk);
-    if (e.res != nullptr) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] += r[g][j];
-    }
-    st_n<T>(static_cast<T*>(e.Y) + base + n, cnt, vec, x);
+    act_value8<kFast>(v + 8 * g, e.act);
+    if (e.drop.thr != 0) drop8_at(v + 8 * g, static_cast<uint64_t>(base + 8 * g), e.drop, rk);
   }
+  if (e.res != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8 * kG; ++j) v[j] += r[j];
+  }
+  row_st<T, kG>(static_cast<T*>(e.Y) + base, n0, e.N, e.vec, v);
 }
 
 // ---------------------------------------------------------------------------
