@@ -211,7 +211,7 @@ __device__ __forceinline__ bool gemm_collect(const GemmArgs& a, const GemmUnit& 
                                              const volatile int* abort_flag, bool ok,
                                              Release release) {
   if constexpr (sizeof(T) == 2) {
-    constexpr int kStep = kCols < 32 ? kCols : 32;
+    constexpr int kStep = kCols < 16 ? kCols : 16;
     ok = ok && wait_warp(&accf[pos.set], pos.parity, DPRC_DEVERR_ACCUM, abort_flag);
     tc_fence_after();
     if (ok) {
@@ -471,7 +471,7 @@ template <typename T>
 constexpr int kPairRing = sizeof(T) == 4 ? 2 : 7;
 // Epilogue warps: fp32 keeps its sums in registers, 64 columns a warp.
 template <typename T>
-constexpr int kPairEpiWarps = sizeof(T) == 4 ? 16 : 8;
+constexpr int kPairEpiWarps = 16;
 template <typename T>
 constexpr int kPairSmem = kPairRing<T> * kPairStageBytes<T> + 1024 + 512;
 
@@ -545,6 +545,15 @@ __device__ __forceinline__ PairWork pair_work(const GemmBatch& b, int me, int pa
   const int end = ahead ? cut : b.n1;
   w.mine1 = end > w.first1 ? (end - 1 - w.first1) / w.step1 + 1 : 0;
   return w;
+}
+
+// Arrives on a barrier of either CTA of the pair.  Relaxed: what it announces
+// is that this warp's TMEM loads have completed (tcgen05.wait::ld); a release at
+// cluster scope would first wait for the tile's global stores (41 -> ARRIVEUS us
+// at 16384 x 1024 x 1024).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
 }
 
 template <typename T>
@@ -712,7 +721,7 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
     const auto release = [&](int buf) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(acce0 + buf * 8);
+      if (lane == 0) mbar_arrive_remote_relaxed(acce0 + buf * 8);
     };
     AccPos<kPairSets<T>> pos;
     bool ok = true;
