@@ -10,6 +10,7 @@
 // planes, and rows of another length are copied to a padded pitch, by one
 // streaming pass before the product.
 
+#include "launch.cuh"
 #include "linear.cuh"
 
 #include <algorithm>
@@ -70,6 +71,8 @@ __device__ __forceinline__ void store_planes(__nv_bfloat16* dst, long long plane
 
 template <typename T>
 __global__ void __launch_bounds__(256) linear_pack_kernel(const PackArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
   const PackJob& j = a.job[blockIdx.y];
   const int groups = j.ld / 8;
   const long long total = j.rows * groups;
@@ -147,6 +150,8 @@ struct DzArgs {
 template <typename T>
 __global__ void __launch_bounds__(32 * kDzWarps, 4) linear_dz_kernel(const DzArgs a) {
   __shared__ float s_sum[kDzWarps][256];
+  pdl_launch_dependents();
+  pdl_wait();
   constexpr bool kFast = sizeof(T) == 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ncb = (a.N + 255) / 256;
@@ -211,6 +216,8 @@ __global__ void __launch_bounds__(32 * kDzWarps, 4) linear_dz_kernel(const DzArg
 // with dropout 197 against 122).
 template <typename T, bool kDrop>
 __global__ void __launch_bounds__(256) linear_dz_flat_kernel(const DzArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
   constexpr bool kFast = sizeof(T) == 2;
   const long long groups = a.M * (a.N / 8);
   const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
@@ -238,6 +245,8 @@ template <typename T>
 __global__ void __launch_bounds__(256)
     linear_db_kernel(const float* __restrict__ colsum, int nblocks, int N, T* __restrict__ db) {
   __shared__ float s_sum[8][32];
+  pdl_launch_dependents();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = static_cast<int>(blockIdx.x) * 32 + lane;
   const int share = (nblocks + 7) / 8;
@@ -264,6 +273,8 @@ template <typename T>
 __global__ void __launch_bounds__(256)
     linear_finish_kernel(const float* __restrict__ part, long long ldpart, long long stride,
                          int split, const LinearEpi e) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int groups = (e.N + 7) / 8;
   const long long total = e.M * groups;
   const RoundKeys rk = round_keys(e.drop.seed);
@@ -302,11 +313,8 @@ cudaError_t launch_pack(dprc_dtype dt, const PackJob* jobs, int n, cudaStream_t 
     most = std::max<int64_t>(most, jobs[i].rows * (jobs[i].ld / 8));
   }
   const dim3 grid(stride_grid(most), n);
-  if (dt == DPRC_F32)
-    linear_pack_kernel<float><<<grid, 256, 0, s>>>(a);
-  else
-    linear_pack_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return dt == DPRC_F32 ? launch_after(linear_pack_kernel<float>, grid, 256, 1, s, 0, a)
+                        : launch_after(linear_pack_kernel<__nv_bfloat16>, grid, 256, 1, s, 0, a);
 }
 
 // A product and, where it is in shares, their sum.
@@ -317,13 +325,12 @@ cudaError_t run_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A
   if (e != cudaSuccess || p.part_bytes == 0) return e;
   const unsigned grid = stride_grid(epi.M * ((epi.N + 7) / 8));
   const long long stride = (g.transposed ? g.cols : g.rows) * p.ldpart;
-  if (dt == DPRC_F32)
-    linear_finish_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float*>(part), p.ldpart,
-                                                     stride, p.split, epi);
-  else
-    linear_finish_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(
-        static_cast<const float*>(part), p.ldpart, stride, p.split, epi);
-  return cudaGetLastError();
+  const float* sums = static_cast<const float*>(part);
+  const long long ld = p.ldpart;
+  return dt == DPRC_F32 ? launch_after(linear_finish_kernel<float>, grid, 256, 1, s, 0, sums, ld,
+                                       stride, p.split, epi)
+                        : launch_after(linear_finish_kernel<__nv_bfloat16>, grid, 256, 1, s, 0,
+                                       sums, ld, stride, p.split, epi);
 }
 
 // At most this many tokens take the tile's columns and the weights its lanes
@@ -548,37 +555,31 @@ cudaError_t launch_linear_grad(const LinearGradCall& c, void* ws, cudaStream_t s
     a.dZ = c.dZ;
     a.colsum = c.db != nullptr ? reinterpret_cast<float*>(w + l.sum_off) : nullptr;
     const unsigned grid = static_cast<unsigned>((c.N + 255) / 256 * l.nblocks);
+    using bf16 = __nv_bfloat16;
     if (c.db == nullptr && a.vec) {
       const int64_t groups = c.M * (c.N / 8);
       const unsigned flat = static_cast<unsigned>(
           std::min<int64_t>((groups + 255) / 256, int64_t(device_sm_count()) * 64));
-      if (c.dtype == DPRC_F32) {
-        if (drop.thr != 0)
-          linear_dz_flat_kernel<float, true><<<flat, 256, 0, s>>>(a);
-        else
-          linear_dz_flat_kernel<float, false><<<flat, 256, 0, s>>>(a);
-      } else if (drop.thr != 0) {
-        linear_dz_flat_kernel<__nv_bfloat16, true><<<flat, 256, 0, s>>>(a);
-      } else {
-        linear_dz_flat_kernel<__nv_bfloat16, false><<<flat, 256, 0, s>>>(a);
-      }
-    } else if (c.dtype == DPRC_F32)
-      linear_dz_kernel<float><<<grid, 32 * kDzWarps, 0, s>>>(a);
-    else
-      linear_dz_kernel<__nv_bfloat16><<<grid, 32 * kDzWarps, 0, s>>>(a);
-    e = cudaGetLastError();
+      auto* kernel = c.dtype == DPRC_F32
+                         ? (drop.thr != 0 ? linear_dz_flat_kernel<float, true>
+                                          : linear_dz_flat_kernel<float, false>)
+                         : (drop.thr != 0 ? linear_dz_flat_kernel<bf16, true>
+                                          : linear_dz_flat_kernel<bf16, false>);
+      e = launch_after(kernel, dim3(flat), 256, 1, s, 0, a);
+    } else {
+      auto* kernel = c.dtype == DPRC_F32 ? linear_dz_kernel<float> : linear_dz_kernel<bf16>;
+      e = launch_after(kernel, dim3(grid), 32 * kDzWarps, 1, s, 0, a);
+    }
     if (e != cudaSuccess) return e;
   }
   if (c.db != nullptr) {
-    const unsigned grid = static_cast<unsigned>((c.N + 31) / 32);
+    const dim3 grid(static_cast<unsigned>((c.N + 31) / 32));
     const float* cs = reinterpret_cast<const float*>(w + l.sum_off);
     const int nb = static_cast<int>(l.nblocks), N = static_cast<int>(c.N);
-    if (c.dtype == DPRC_F32)
-      linear_db_kernel<float><<<grid, 256, 0, s>>>(cs, nb, N, static_cast<float*>(c.db));
-    else
-      linear_db_kernel<__nv_bfloat16>
-          <<<grid, 256, 0, s>>>(cs, nb, N, static_cast<__nv_bfloat16*>(c.db));
-    e = cudaGetLastError();
+    e = c.dtype == DPRC_F32 ? launch_after(linear_db_kernel<float>, grid, 256, 1, s, 0, cs, nb, N,
+                                           static_cast<float*>(c.db))
+                            : launch_after(linear_db_kernel<__nv_bfloat16>, grid, 256, 1, s, 0, cs,
+                                           nb, N, static_cast<__nv_bfloat16*>(c.db));
     if (e != cudaSuccess) return e;
   }
   if (!products) return cudaSuccess;

@@ -15,6 +15,7 @@
 // features to fill the GPU, and add up through shared memory.  More tokens
 // than kTok: another row of CTAs, whose weights come from L2.
 
+#include "launch.cuh"
 #include "linear.cuh"
 
 namespace dprc {
@@ -99,6 +100,8 @@ __global__ void __launch_bounds__(32 * kFewWarps) linear_few_kernel(const FewArg
   constexpr int kVals = kFeat * kTok;  // sums of a warp
   static_assert(kVals <= 32 && (kVals & (kVals - 1)) == 0, "one lane per sum");
   __shared__ float s_sum[kFewWarps][kVals];
+  pdl_launch_dependents();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = kFewWarps / a.ksplit;  // feature groups of the CTA
   const int group = warp / a.ksplit, share = warp % a.ksplit;
@@ -190,13 +193,11 @@ cudaError_t launch_few_t(const FewArgs& a, int tok, cudaStream_t s) {
   const int per = groups * kFeat;
   const dim3 grid(static_cast<unsigned>((a.N + per - 1) / per),
                   static_cast<unsigned>((a.M + tok - 1) / tok));
-  switch (tok) {
-    case 1: linear_few_kernel<T, kVec, 1><<<grid, 32 * kFewWarps, 0, s>>>(a); break;
-    case 2: linear_few_kernel<T, kVec, 2><<<grid, 32 * kFewWarps, 0, s>>>(a); break;
-    case 4: linear_few_kernel<T, kVec, 4><<<grid, 32 * kFewWarps, 0, s>>>(a); break;
-    default: linear_few_kernel<T, kVec, 8><<<grid, 32 * kFewWarps, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  auto* kernel = tok == 1   ? linear_few_kernel<T, kVec, 1>
+                 : tok == 2 ? linear_few_kernel<T, kVec, 2>
+                 : tok == 4 ? linear_few_kernel<T, kVec, 4>
+                            : linear_few_kernel<T, kVec, 8>;
+  return launch_after(kernel, grid, 32 * kFewWarps, 1, s, 0, a);
 }
 
 }  // namespace

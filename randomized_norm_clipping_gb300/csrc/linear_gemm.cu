@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "launch.cuh"
 #include "linear.cuh"
 
 namespace dprc {
@@ -58,16 +59,19 @@ struct GemmCfg {
 };
 
 // One thread's bounded wait for a phase of a barrier of this CTA: like
-// mbar_wait_lim, but each try suspends the thread for up to kSuspendNs in the
-// hardware, and a warp waits with one lane (mbar_wait_warp).  Eight epilogue
-// warps polling with all lanes slowed the MMAs' shared memory down: POLLUS.
+// mbar_wait_lim, but each try may suspend the thread for up to kSuspendNs, and a
+// warp waits with one lane (wait_warp).  Warps that poll take issue slots and
+// shared memory from the thread that feeds the tensor core: eight epilogue warps
+// polling with all lanes made it 703,000 cycles and not 478,000 for
+// 16384 x 2048 x 8192, one lane each without the hint 363 us and not 324.  (One
+// polling warp and a hardware barrier for the others: 336 us.)
 constexpr uint32_t kSuspendNs = 20000;
 
 __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
@@ -184,7 +188,7 @@ __device__ __forceinline__ void gemm_emit(const GemmArgs& a, int split, long lon
 // So the first plane product, which makes the result's size, has an
 // accumulator of its own, the five others, 2^-8 of it and less, a second one,
 // and every kAccUnits units (512 of the contraction) the epilogue warps add
-// both to sums in registers: FPREC.
+// both to sums in registers: 1.7e-7 (1001 x 517 x 263; the plain product 4.1e-7).
 template <typename T>
 constexpr int kAccUnits = sizeof(T) == 4 ? 8 : 1 << 30;
 
@@ -315,6 +319,9 @@ __global__ void __launch_bounds__(GemmCfg<kTn, T>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // all of the above overlaps the end of the kernel before; nothing below does
+  pdl_launch_dependents();
+  pdl_wait();
 
   if (warp == 0) {
     if (lane == 0 && mine > 0) {
@@ -549,7 +556,7 @@ __device__ __forceinline__ PairWork pair_work(const GemmBatch& b, int me, int pa
 
 // Arrives on a barrier of either CTA of the pair.  Relaxed: what it announces
 // is that this warp's TMEM loads have completed (tcgen05.wait::ld); a release at
-// cluster scope would first wait for the tile's global stores (41 -> ARRIVEUS us
+// cluster scope would first wait for the tile's global stores (41 and not 36 us
 // at 16384 x 1024 x 1024).
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
@@ -607,6 +614,9 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // all of the above overlaps the end of the kernel before; nothing below does
+  pdl_launch_dependents();
+  pdl_wait();
 
   if (warp == 0) {
     if (lane == 0 && mine > 0) {
@@ -748,9 +758,9 @@ cudaError_t launch_gemm_pair(const CUtensorMap* maps, const GemmBatch& batch, cu
   const cudaError_t e = set_smem_once<2 + sizeof(T)>(linear_gemm_pair_kernel<T>, kPairSmem<T>);
   if (e != cudaSuccess) return e;
   const long long pairs = std::min<long long>(static_cast<long long>(batch.n0) + batch.n1, device_sm_count() / 2);
-  linear_gemm_pair_kernel<T><<<static_cast<unsigned>(2 * pairs), 64 + 32 * kPairEpiWarps<T>, kPairSmem<T>, s>>>(
-      maps[0], maps[1], maps[2], maps[3], batch);
-  return cudaGetLastError();
+  return launch_after(linear_gemm_pair_kernel<T>, dim3(static_cast<unsigned>(2 * pairs)),
+                      64 + 32 * kPairEpiWarps<T>, 1, s, kPairSmem<T>, maps[0], maps[1], maps[2],
+                      maps[3], batch);
 }
 
 // How the second product's units are dealt (GemmBatch), and the busiest pair's
@@ -783,9 +793,8 @@ cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const Ge
   if (e != cudaSuccess) return e;
   const long long work = static_cast<long long>(a.mt) * a.nt * a.split;
   const long long grid = work < device_sm_count() ? work : device_sm_count();
-  linear_gemm_kernel<kTn, T>
-      <<<static_cast<unsigned>(grid), Cfg::kThreads, Cfg::kSmem, s>>>(ma, mb, a);
-  return cudaGetLastError();
+  return launch_after(linear_gemm_kernel<kTn, T>, dim3(static_cast<unsigned>(grid)), Cfg::kThreads,
+                      1, s, Cfg::kSmem, ma, mb, a);
 }
 
 template <typename T>
