@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include "common.cuh"
+
 namespace dprc {
 
 // Launches `kernel` so that it may start while the kernel before it in the
@@ -27,6 +29,19 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int cl, c
   cfg.attrs = attr;
   cfg.numAttrs = cl > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The two ends of a kernel that may run beside the one before it (launch_after).
+// It may where nothing it reads or writes is that kernel's, and that kernel let
+// it start only after its own wait (as beside_begin does), so that everything
+// before that kernel is complete.  The wait that is left out at the start comes
+// at the end: the next kernel's wait then covers both.
+__device__ __forceinline__ void beside_begin(bool beside) {
+  if (!beside) pdl_wait();
+  pdl_launch_dependents();
+}
+__device__ __forceinline__ void beside_end(bool beside) {
+  if (beside && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) pdl_wait();
 }
 
 }  // namespace dprc

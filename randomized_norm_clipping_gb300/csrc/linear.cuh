@@ -273,11 +273,11 @@ struct GemmPlan {
 };
 
 GemmPlan plan_gemm(const GemmShape& g);
-// D into epi (split == 1) or the partial sums into `part`, then epi by
-// launch_linear_finish.  T of the epilogue's tensors: dt.
+// D into epi (split == 1) or the partial sums into `part`.  T of the epilogue's
+// tensors: dt.  beside: runs beside the kernel before it (launch.cuh).
 cudaError_t launch_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A,
                         const GemmOperand& B, dprc_dtype dt, const LinearEpi& epi, void* part,
-                        cudaStream_t s);
+                        bool beside, cudaStream_t s);
 
 // The whole map for a few tokens on the CUDA cores (linear_few.cu).
 cudaError_t launch_linear_few(const void* X, const void* W, dprc_dtype dt, int64_t M, int64_t K,

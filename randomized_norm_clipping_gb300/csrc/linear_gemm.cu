@@ -110,6 +110,7 @@ struct GemmArgs {
   int transposed;
   float* part;              // partial sums, or null: the epilogue
   long long ldpart, part_stride;
+  int beside;               // runs beside the kernel before (launch.cuh)
   LinearEpi epi;
 };
 
@@ -319,9 +320,8 @@ __global__ void __launch_bounds__(GemmCfg<kTn, T>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // all of the above overlaps the end of the kernel before; nothing below does
-  pdl_launch_dependents();
-  pdl_wait();
+  // all of the above overlaps the end of the kernel before
+  beside_begin(a.beside != 0);
 
   if (warp == 0) {
     if (lane == 0 && mine > 0) {
@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(GemmCfg<kTn, T>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 2 * kAccs<T> * kTn);
   }
+  beside_end(a.beside != 0);
 }
 
 // Allows a kernel its shared memory, once per device; kTag: one per kernel.
@@ -614,9 +615,8 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // all of the above overlaps the end of the kernel before; nothing below does
-  pdl_launch_dependents();
-  pdl_wait();
+  // all of the above overlaps the end of the kernel before
+  beside_begin(batch.p[0].beside != 0);
 
   if (warp == 0) {
     if (lane == 0 && mine > 0) {
@@ -751,6 +751,7 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
+  beside_end(batch.p[0].beside != 0);
 }
 
 template <typename T>
@@ -915,6 +916,7 @@ cudaError_t prepare_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperan
   a.part = p.part_bytes > 0 ? static_cast<float*>(part) : nullptr;
   a.ldpart = p.ldpart;
   a.part_stride = (g.transposed ? g.cols : g.rows) * p.ldpart;
+  a.beside = 0;
   a.epi = epi;
   return unit_count(a) < (int64_t(1) << 30) ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -923,12 +925,13 @@ cudaError_t prepare_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperan
 
 cudaError_t launch_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand& A,
                         const GemmOperand& B, dprc_dtype dt, const LinearEpi& epi, void* part,
-                        cudaStream_t s) {
+                        bool beside, cudaStream_t s) {
   CUtensorMap maps[4];
   if (p.pair) {
     GemmBatch batch;
     const cudaError_t e = prepare_gemm(g, p, A, B, epi, part, maps, batch.p[0]);
     if (e != cudaSuccess) return e;
+    batch.p[0].beside = beside;
     batch.p[1] = batch.p[0];
     maps[2] = maps[0];
     maps[3] = maps[1];
@@ -940,6 +943,7 @@ cudaError_t launch_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperand
   GemmArgs a;
   const cudaError_t e = prepare_gemm(g, p, A, B, epi, part, maps, a);
   if (e != cudaSuccess) return e;
+  a.beside = beside;
   return dt == DPRC_F32 ? launch_gemm_tn<float>(p.tn, maps[0], maps[1], a, s)
                         : launch_gemm_tn<__nv_bfloat16>(p.tn, maps[0], maps[1], a, s);
 }
