@@ -153,12 +153,14 @@ def lib():
     return _lib
 
 
+_CODES = {torch.float32: DPRC_F32, torch.bfloat16: DPRC_BF16}
+
+
 def _dtype_code(t):
-    if t.dtype == torch.float32:
-        return DPRC_F32
-    if t.dtype == torch.bfloat16:
-        return DPRC_BF16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -166,14 +168,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(t, stream):
     if stream is not None:
-        return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+        return getattr(stream, "cuda_stream", stream)
     if _raw_stream is not None:  # the current stream's handle without a Stream object
-        return ctypes.c_void_p(_raw_stream(t.device.index))
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None
 
 
 def _check(fn, status):
@@ -183,10 +185,10 @@ def _check(fn, status):
 
 def _need_cuda(*ts):
     for t in ts:
-        if t is not None and not t.is_cuda:
-            raise ValueError("libdprc takes device tensors")
-        if t is not None and not t.is_contiguous():
-            raise ValueError("libdprc takes contiguous tensors")
+        if t is None or (t.is_cuda and t.is_contiguous()):
+            continue
+        raise ValueError("libdprc takes device tensors" if not t.is_cuda
+                         else "libdprc takes contiguous tensors")
 
 
 def dprc_abi_version():
@@ -502,39 +504,42 @@ _SCRATCH_KEEP = 64 << 20  # larger workspaces are allocated per call
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
 
 
-def _empty(shape, dtype, device, stream, given):
-    """torch.empty for a call on `stream` (a c_void_p): allocated on that stream
-    where the caller gave one (`given` not None), so that the memory's earlier
-    and later uses are ordered against the call."""
-    if given is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream.value or 0, device=device)):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _empty(like, shape, stream, given, dtype=None):
+    """An uninitialised tensor on like's device, of its dtype if none is given,
+    for a call on the stream handle `stream`: allocated on that stream where the
+    caller gave one (`given` not None), so that the memory's earlier and later
+    uses are ordered against the call."""
+    if dtype is None:
+        dtype = like.dtype
+    if given is None:  # (sizes as arguments of their own: 1 to 2 us less than a tuple or Size)
+        return torch.empty(*shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device)):
+        return torch.empty(*shape, dtype=dtype, device=like.device)
 
 
-def _scratch(nbytes, device, stream, given):
+def _scratch(nbytes, like, stream, given):
     """A device workspace of nbytes for one call without a ws argument: kept
     per host thread, device and stream (calls of one thread on one stream run
     one after the other) and grown as needed, so that a call does not pay for
     an allocation.  Large ones, and any during a graph capture (which owns what
     it allocates), are allocated fresh."""
     if nbytes > _SCRATCH_KEEP or _capturing is None or _capturing():
-        return _empty(nbytes, torch.uint8, device, stream, given)
+        return _empty(like, (nbytes,), stream, given, torch.uint8)
     kept = _scratch_kept.__dict__
-    key = (device.index, stream.value)
+    key = (like.get_device(), stream)
     have = kept.get(key)
     if have is None or have[-1].numel() < nbytes:
         size = 1 << max(16, (nbytes - 1).bit_length())
         # outgrown buffers stay: work on the stream may still use them
-        have = (have or ()) + (_empty(size, torch.uint8, device, stream, given),)
+        have = (have or ()) + (_empty(like, (size,), stream, given, torch.uint8),)
         kept[key] = have
     return have[-1]
 
 
 def _same(name, t, dtype, shape, device):
     """An optional tensor of the call's dtype, shape and device."""
-    if t is None or (t.dtype is dtype and t.device == device
-                     and (shape is None or t.shape == shape)):
+    if t is None or (t.dtype is dtype and (shape is None or t.shape == shape)
+                     and t.device == device):
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, the call's tensors are {dtype}")
@@ -558,7 +563,7 @@ def dprc_embed_lookup(W, tokens, scale=1.0, out=None, stream=None):
     st = _stream(W, stream)
     shape = (*tokens.shape, d)
     if out is None:
-        out = _empty(shape, W.dtype, W.device, st, stream)
+        out = _empty(W, shape, st, stream)
     else:
         _same("out", out, W.dtype, shape, W.device)
     _check("dprc_embed_lookup",
@@ -583,16 +588,16 @@ def dprc_embed_plan(tokens, V, buf=None, stream=None):
     of dprc_embed_plan_bytes(B * T, V) bytes to keep it in."""
     B, T = tokens.shape
     size = _token_bytes(tokens)
+    _need_cuda(tokens, buf)
+    st = _stream(tokens, stream)
     if buf is None:
         n = lib().dprc_embed_plan_bytes(B * T, V)
         if n == 0:
             raise DprcError("dprc_embed_plan_bytes", 2)
-        _need_cuda(tokens)
-        buf = _empty(n, torch.uint8, tokens.device, _stream(tokens, stream), stream)
-    _need_cuda(tokens, buf)
+        buf = _empty(tokens, (n,), st, stream, torch.uint8)
     _check("dprc_embed_plan",
            lib().dprc_embed_plan(tokens.data_ptr(), size, B * T, V,
-                                 buf.data_ptr(), buf.numel(), _stream(tokens, stream)))
+                                 buf.data_ptr(), buf.numel(), st))
     return EmbedPlan(B, T, int(V), buf)
 
 
@@ -603,7 +608,7 @@ def _embed_ws(G, plan, ws, stream, given):
         n = lib().dprc_embed_workspace_bytes(_dtype_code(G), plan.B, plan.T, G.shape[2])
         if n == 0:
             raise DprcError("dprc_embed_workspace_bytes", 2)
-        ws = _scratch(n, G.device, stream, given)
+        ws = _scratch(n, G, stream, given)
     return ws
 
 
@@ -641,9 +646,11 @@ def dprc_dropout(x, p, seed, step, residual=None, first_element=0, out=None, str
     _need_cuda(x, residual, out)
     st = _stream(x, stream)
     if out is None:
-        out = _empty(x.shape, x.dtype, x.device, st, stream)
-    _same("residual", residual, x.dtype, x.shape, x.device)
-    _same("out", out, x.dtype, x.shape, x.device)
+        out = _empty(x, x.shape, st, stream) if x.dim() > 0 else torch.empty_like(x)
+    else:
+        _same("out", out, x.dtype, x.shape, x.device)
+    if residual is not None:
+        _same("residual", residual, x.dtype, x.shape, x.device)
     _check("dprc_dropout",
            lib().dprc_dropout(x.data_ptr(), _ptr(residual), _dtype_code(x), x.numel(),
                               int(first_element) & _U64, p, int(seed) & _U64, int(step) & _U64,
@@ -656,7 +663,7 @@ def _linear_ws(like, M, K, N, grad, ws, stream, given):
         n = lib().dprc_linear_workspace_bytes(_dtype_code(like), M, K, N, grad)
         if n == 0:
             raise DprcError("dprc_linear_workspace_bytes", 2)
-        ws = _scratch(n, like.device, stream, given)
+        ws = _scratch(n, like, stream, given)
     return ws
 
 
@@ -672,13 +679,13 @@ def dprc_linear(X, W, bias=None, act="none", p=0.0, seed=0, step=0, residual=Non
     dt, dev = X.dtype, X.device
     _need_cuda(X, W, bias, residual, Z, out, ws)
     st = _stream(X, stream)
-    if out is None:
-        out = _empty(shape, dt, dev, st, stream)
     _same("W", W, dt, None, dev)
     _same("bias", bias, dt, (N,), dev)
     _same("residual", residual, dt, shape, dev)
     _same("Z", Z, dt, shape, dev)
     _same("out", out, dt, shape, dev)
+    if out is None:
+        out = _empty(X, shape, st, stream)
     ws = _linear_ws(X, M, K, N, 0, ws, st, stream)
     _check("dprc_linear",
            lib().dprc_linear(X.data_ptr(), W.data_ptr(), _ptr(bias), _ptr(residual),
