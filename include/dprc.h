@@ -400,8 +400,10 @@ dprc_status dprc_philox_words(uint32_t* out, int64_t n_blocks, uint64_t first_bl
  * residual) and its per-sample clipping runs on this library: the norms of
  * linear weights come from the entry points above, the embedding's and a
  * bias's from dprc_embed_norm.  Tensors are dense, row-major and 16-byte
- * aligned; widths are arbitrary.  The workspaces and plans of these calls need
- * no zeroing, and results repeat bitwise for fixed inputs, sizes and device.
+ * aligned; widths are arbitrary.  Outputs and workspaces overlap neither one
+ * another nor an input, except where a call says so.  The workspaces and plans
+ * of these calls need no zeroing.  Results repeat bitwise for fixed inputs,
+ * sizes, device and set of requested outputs.
  * ---------------------------------------------------------------------------
  */
 
@@ -438,7 +440,8 @@ dprc_status dprc_embed_plan(const void* tokens, int token_bytes, int64_t N, int6
  * this is || sum_t G_it ||^2, the norm of a bias's gradient.
  *  G device [B][T][d] of dtype (the gradient of the lookup's output); plan of
  *  the B*T tokens (position i T + t); n device float [B]; accumulate as above.
- *  ws device, dprc_embed_workspace_bytes(dtype, B, T, d) bytes.
+ *  ws device, dprc_embed_workspace_bytes(dtype, B, T, d) bytes (two fp32 rows
+ *  of d for every 16 positions: about a quarter of a bf16 G).
  *  1 <= B <= 65535, T >= 0 (T = 0: zero norms).  Sums in fp32.  G at positions
  *  without a token is not read.
  */

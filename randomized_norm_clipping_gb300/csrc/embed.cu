@@ -7,7 +7,7 @@
 // so  ||dW_i||^2 = s^2 sum_v || sum_{t: tok_it = v} G_it ||^2   and
 //     sum_i c_i dW_i[v] = s sum_i c_i sum_{t: tok_it = v} G_it.
 // Both are sums over groups of equal tokens.  The tokens are sorted once,
-// stably, with their positions (token_sort_kernel); a group is then a run of
+// stably, with their positions (dprc_embed_plan); a group is then a run of
 // consecutive entries, a token's entries of one sample are a run inside it,
 // and one pass over the rows of G in that order gives either result with no
 // atomics: every sum has one fixed order, so results repeat bitwise.
@@ -1236,8 +1236,10 @@ cudaError_t launch_embed_norm(const EmbedCall& c, float* n, void* ws, cudaStream
   const SegArgs a = seg_args(c, p, sort_plan(c.B * c.T, c.V), static_cast<char*>(ws));
   cudaError_t e = launch_segments<true>(c.dtype, a, p, c.G, nullptr, s);
   if (e != cudaSuccess) return e;
-  // one CTA per sample where a sample has few values, else a cluster of 8
-  const int cl = static_cast<int64_t>(a.T) * p.nblk > 4096 ? 8 : 1;
+  // One CTA per sample where a sample has at most two values a thread, else a
+  // cluster of 8: whole norms of 4 x 4096 tokens of 2048 bf16 24.2 and 20.9 us, of
+  // 3 x 1000 of 321 fp32 13.3 and 11.4; of 4 x 128 of 64 fp32 5.6 with one CTA.
+  const int cl = static_cast<int64_t>(a.T) * p.nblk > 512 ? 8 : 1;
   return launch_after(embed_norm_finish_kernel, dim3(static_cast<unsigned>(c.B * cl)), 256, cl, s,
                       0, a, n);
 }

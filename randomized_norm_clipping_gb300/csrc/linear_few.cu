@@ -61,6 +61,19 @@ struct FewAccess {
       raw.x = in ? __float_as_uint(to_f32<T>(*p)) : 0u;
     }
   }
+  // A weight, read once: not kept in L1, which is X's (fp32, 2048 x 8192, four
+  // tokens: 29.5 us with both in L1, 22 so, 16 with four steps at a time).
+  __device__ __forceinline__ void load_once(const T* p, bool in) {
+    if constexpr (kVec) {
+      raw = make_uint4(0u, 0u, 0u, 0u);
+      if (in)
+        asm("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+            : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
+            : "l"(p));
+    } else {
+      load(p, in);
+    }
+  }
   __device__ __forceinline__ void pairs(unsigned long long* v) const {
     if constexpr (!kVec) {
       v[0] = few_pair(__uint_as_float(raw.x), 0.f);
@@ -129,15 +142,18 @@ __global__ void __launch_bounds__(32 * kFewWarps) linear_few_kernel(const FewArg
 #pragma unroll
     for (int t = 0; t < kTok; ++t) acc[f][t] = 0ull;
 
-  // (two steps' loads together; four features and not two: what a step waits
-  // for is X from L1, and two features read it twice as often: 32 us and not
-  // 20 us for 8 tokens, 2048 x 8192 bf16)
-#pragma unroll 2
+  // (the loads of two steps together, of four where an access is only four
+  // values: fp32 with 2, 4, 8 tokens 16.3, 22, 31.5 us by twos and 15.7, 16.1,
+  // 27.7 by fours, bf16 9.7, 10.2, 19.7 and 9.1, 16.3, 20.5; four features and
+  // not two: what a step waits for is X from L1, and two features read it twice
+  // as often: 32 us and not 20 us for 8 tokens, 2048 x 8192 bf16)
+  constexpr int kAhead = kVec && sizeof(T) == 4 ? 4 : 2;
+#pragma unroll kAhead
   for (int k = k_lo + lane * Access::kElems; k - lane * Access::kElems < k_hi; k += kStep) {
     const bool in = k < k_hi;
     Access wa[kFeat];
 #pragma unroll
-    for (int f = 0; f < kFeat; ++f) wa[f].load(w[f] + k, in);
+    for (int f = 0; f < kFeat; ++f) wa[f].load_once(w[f] + k, in);
     unsigned long long wp[kFeat][Access::kPairs];
 #pragma unroll
     for (int f = 0; f < kFeat; ++f) wa[f].pairs(wp[f]);

@@ -501,3 +501,41 @@ def test_values_at_the_ends_of_the_range():
     rnc.dprc_linear_grad(torch.ones(3, 8, device=DEV), None, torch.zeros(8, 16, device=DEV),
                          Z=Z.to(DEV), act="gelu", dZ=dZ)
     assert np.allclose(dZ.cpu().numpy()[:, :7], [1, 0, 1, 0, 0.5, 1, 0], atol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_calls_back_to_back_on_one_workspace(dtype):
+    """Kernels of a call run side by side and its successor starts while it
+    ends: calls on one workspace in turn give what each gives alone."""
+    sizes = [(1001, 517, 263), (40, 264, 136), (300, 128, 776), (5, 1000, 333), (513, 96, 72)]
+    problems, ws_bytes = [], 1
+    for j, (M, K, N) in enumerate(sizes):
+        dY, X = _randn((M, N), dtype, 10 * j).to(DEV), _randn((M, K), dtype, 10 * j + 1).to(DEV)
+        W, Z = _randn((N, K), dtype, 10 * j + 2).to(DEV), _randn((M, N), dtype, 10 * j + 3).to(DEV)
+        outs = [torch.empty_like(t) for t in (X, W, W[:, 0].contiguous(), dY)]
+        problems.append((dY, X, W, Z, outs))
+        ws_bytes = max(ws_bytes, rnc.binding.lib().dprc_linear_workspace_bytes(
+            rnc.DPRC_F32 if dtype == "f32" else rnc.DPRC_BF16, M, K, N, 1))
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=DEV)
+
+    def call(j):
+        dY, X, W, Z, (dX, dW, db, dZ) = problems[j]
+        rnc.dprc_linear_grad(dY, X, W, Z=Z, act="silu", p=0.1, seed=3, step=j, dX=dX, dW=dW,
+                             db=db, dZ=dZ if j % 2 else None, ws=ws)
+
+    alone = []
+    for j in range(len(sizes)):
+        torch.cuda.synchronize()
+        call(j)
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in problems[j][4][:3]])
+    order, results = torch.randint(len(sizes), (60,), generator=_gen(9)).tolist(), []
+    for j in order:
+        for t in problems[j][4]:
+            t.fill_(float("nan"))
+        call(j)
+        results.append([t.clone() for t in problems[j][4][:3]])
+    torch.cuda.synchronize()
+    for j, got in zip(order, results):
+        for a, b in zip(got, alone[j]):
+            assert torch.equal(a, b)
