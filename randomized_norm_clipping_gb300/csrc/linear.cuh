@@ -148,12 +148,15 @@ __device__ __forceinline__ void drop8_at(float* v, uint64_t e0, const DropArgs& 
 
 // 16 bf16 values as one 32-byte access (sm_100 and later): a whole sector, where
 // two accesses of 16 bytes go to L2 as two halves of one.
-__device__ __forceinline__ void ld16_bf16(const __nv_bfloat16* p, float* v) {
-  uint32_t u[8];
+__device__ __forceinline__ void ld16_raw(const __nv_bfloat16* p, uint32_t* u) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]),
                  "=r"(u[6]), "=r"(u[7])
                : "l"(p));
+}
+__device__ __forceinline__ void ld16_bf16(const __nv_bfloat16* p, float* v) {
+  uint32_t u[8];
+  ld16_raw(p, u);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     v[2 * e] = __uint_as_float(u[e] << 16);
@@ -204,16 +207,18 @@ __device__ __forceinline__ void row_st(T* p, int n, int N, int vec, const float*
 }
 
 // Outputs (m, n0 .. n0 + 8 kG) from the fp32 sums v; the residual first, so
-// that it is on its way while the rest is computed.
-template <typename T, int kG>
+// that it is on its way while the rest is computed.  kReady: the bias is in v,
+// and the residual, if there is one, in `ready` (bf16 pairs as they are stored).
+template <typename T, int kG, bool kReady = false>
 __device__ __forceinline__ void linear_out(const LinearEpi& e, long long m, int n0, float* v,
-                                           const RoundKeys& rk) {
+                                           const RoundKeys& rk,
+                                           const uint32_t* ready = nullptr) {
   constexpr bool kFast = sizeof(T) == 2;
   const long long base = m * e.N + n0;
   if (!DPRC_IN(m < e.M && n0 < e.N)) return;
   float r[kG * 8];
-  if (e.res != nullptr) row_ld<T, kG>(static_cast<const T*>(e.res) + base, n0, e.N, e.vec, r);
-  if (e.bias != nullptr) {
+  if (!kReady && e.res != nullptr) row_ld<T, kG>(static_cast<const T*>(e.res) + base, n0, e.N, e.vec, r);
+  if (!kReady && e.bias != nullptr) {
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
       const int cnt = min(8, e.N - n0 - 8 * g);
@@ -231,8 +236,16 @@ __device__ __forceinline__ void linear_out(const LinearEpi& e, long long m, int 
     if (e.drop.thr != 0) drop8_at(v + 8 * g, static_cast<uint64_t>(base + 8 * g), e.drop, rk);
   }
   if (e.res != nullptr) {
+    if constexpr (kReady) {
 #pragma unroll
-    for (int j = 0; j < 8 * kG; ++j) v[j] += r[j];
+      for (int j = 0; j < 4 * kG; ++j) {
+        v[2 * j] += __uint_as_float(ready[j] << 16);
+        v[2 * j + 1] += __uint_as_float(ready[j] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8 * kG; ++j) v[j] += r[j];
+    }
   }
   row_st<T, kG>(static_cast<T*>(e.Y) + base, n0, e.N, e.vec, v);
 }

@@ -206,6 +206,65 @@ struct AccPos {
   }
 };
 
+// gemm_collect for bf16 outputs whose rows are whole 32 bytes: the bias (two
+// columns a lane) and the residual's first kAhead steps are on their way before
+// the accumulator is finished, later ones kAhead steps ahead.  A load of the
+// epilogue queues behind the operand tiles that are in flight into the SM, some
+// 2 us: 16384 x 2048 x 8192 with bias and residual took 571,000 cycles with the
+// loads where they are needed, 499,000 so (475,000 without either); with dropout
+// too 406 and 369 us, 16384 x 1024 x 1024 63 and 53 us (three steps ahead: 387
+// and 62, for want of registers).
+template <int kCols, int kAcc, int kSets, typename Release>
+__device__ __forceinline__ bool gemm_collect_ahead(const GemmArgs& a, uint32_t tmem, long long row,
+                                                   int col0, const RoundKeys& rk, uint64_t* accf,
+                                                   AccPos<kSets>& pos,
+                                                   const volatile int* abort_flag, bool ok,
+                                                   Release release) {
+  using T = __nv_bfloat16;
+  constexpr int kStep = 16, kAhead = 2;
+  static_assert(kCols == 64, "a lane holds the bias of two columns");
+  const LinearEpi& e = a.epi;
+  const int lane = threadIdx.x & 31;
+  const bool mine = row < a.rows;
+  const T* res = static_cast<const T*>(e.res) + (mine ? row : 0) * e.N + col0;
+  uint32_t ahead[kAhead][8];
+  const auto fetch = [&](uint32_t* u, int c) {
+    if (mine && c < kCols && col0 + c < a.cols) ld16_raw(res + c, u);
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) fetch(ahead[s], s * kStep);
+  uint32_t bias = 0;
+  if (e.bias != nullptr && col0 + 2 * lane < a.cols)
+    bias = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const T*>(e.bias) + col0) + lane);
+  ok = ok && wait_warp(&accf[pos.set], pos.parity, DPRC_DEVERR_ACCUM, abort_flag);
+  tc_fence_after();
+  if (ok) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < kCols; c0 += kStep) {
+      if (col0 + c0 >= a.cols) break;  // uniform over the warp
+      float v[kStep];
+      tmem_ld_cols<kStep>(tmem + pos.set * kAcc + c0, v);
+      if (e.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kStep / 2; ++j) {
+          const uint32_t b = __shfl_sync(0xffffffffu, bias, c0 / 2 + j);
+          v[2 * j] += __uint_as_float(b << 16);
+          v[2 * j + 1] += __uint_as_float(b & 0xFFFF0000u);
+        }
+      }
+      if (mine) linear_out<T, kStep / 8, true>(e, row, col0 + c0, v, rk, ahead[0]);
+#pragma unroll
+      for (int s = 0; s + 1 < kAhead; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ahead[s][j] = ahead[s + 1][j];
+      fetch(ahead[kAhead - 1], c0 + kAhead * kStep);
+    }
+  }
+  release(pos.set);
+  pos.next();
+  return ok;
+}
+
 // The sums of one unit of work for this thread's row (TMEM lane), kCols of
 // them from column tmem of each accumulator on (kAcc columns apart), first
 // column col0 of D.  `release(set)` frees a set.
@@ -564,7 +623,10 @@ __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr
                : "memory");
 }
 
-template <typename T>
+// kRes: bf16 whole outputs with a residual, whose epilogue loads ahead; an
+// instantiation of its own, since both epilogues in one kernel cost the plain one
+// registers (16384 x 1024 x 1024: 33 -> 35 to 40 us).
+template <typename T, bool kRes>
 __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims__(2, 1, 1)
     linear_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a0,
                             const __grid_constant__ CUtensorMap map_b0,
@@ -739,8 +801,12 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
       const GemmArgs& a = batch.p[j >= work.mine0];
       const GemmUnit g = gemm_unit(a, work.at(j));
       const long long row = static_cast<long long>(g.m) * kPairTile + rank * kTm + q * 32 + lane;
-      ok = gemm_collect<T, kCols, kPairTile, kPairSets<T>>(
-          a, g, tb, row, g.n * kPairTile + c_lo, rk, accf, pos, abort_flag, ok, release);
+      if constexpr (kRes)
+        ok = gemm_collect_ahead<kCols, kPairTile>(a, tb, row, g.n * kPairTile + c_lo, rk, accf,
+                                                  pos, abort_flag, ok, release);
+      else
+        ok = gemm_collect<T, kCols, kPairTile, kPairSets<T>>(
+            a, g, tb, row, g.n * kPairTile + c_lo, rk, accf, pos, abort_flag, ok, release);
     }
   }
 
@@ -754,14 +820,25 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
   beside_end(batch.p[0].beside != 0);
 }
 
+template <typename T, bool kRes>
+cudaError_t launch_gemm_pair_t(const CUtensorMap* maps, const GemmBatch& batch, cudaStream_t s) {
+  auto* kernel = linear_gemm_pair_kernel<T, kRes>;
+  const cudaError_t e = set_smem_once<2 + sizeof(T) + kRes>(kernel, kPairSmem<T>);
+  if (e != cudaSuccess) return e;
+  const long long pairs =
+      std::min<long long>(static_cast<long long>(batch.n0) + batch.n1, device_sm_count() / 2);
+  return launch_after(kernel, dim3(static_cast<unsigned>(2 * pairs)), 64 + 32 * kPairEpiWarps<T>, 1,
+                      s, kPairSmem<T>, maps[0], maps[1], maps[2], maps[3], batch);
+}
+
 template <typename T>
 cudaError_t launch_gemm_pair(const CUtensorMap* maps, const GemmBatch& batch, cudaStream_t s) {
-  const cudaError_t e = set_smem_once<2 + sizeof(T)>(linear_gemm_pair_kernel<T>, kPairSmem<T>);
-  if (e != cudaSuccess) return e;
-  const long long pairs = std::min<long long>(static_cast<long long>(batch.n0) + batch.n1, device_sm_count() / 2);
-  return launch_after(linear_gemm_pair_kernel<T>, dim3(static_cast<unsigned>(2 * pairs)),
-                      64 + 32 * kPairEpiWarps<T>, 1, s, kPairSmem<T>, maps[0], maps[1], maps[2],
-                      maps[3], batch);
+  if constexpr (sizeof(T) == 2) {
+    const GemmArgs& a = batch.p[0];
+    if (batch.n1 == 0 && a.part == nullptr && a.epi.vec == 2 && a.epi.res != nullptr)
+      return launch_gemm_pair_t<T, true>(maps, batch, s);
+  }
+  return launch_gemm_pair_t<T, false>(maps, batch, s);
 }
 
 // How the second product's units are dealt (GemmBatch), and the busiest pair's

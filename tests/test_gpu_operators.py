@@ -539,3 +539,41 @@ def test_calls_back_to_back_on_one_workspace(dtype):
     for j, got in zip(order, results):
         for a, b in zip(got, alone[j]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,K,N", [(5001, 200, 4112), (3001, 512, 2000)])
+@pytest.mark.parametrize("name,bias,p", [("none", False, 0.0), ("none", True, 0.1),
+                                         ("gelu", True, 0.0)])
+def test_linear_of_many_tiles(M, K, N, name, bias, p):
+    """Sizes of a hundred 256 x 256 tiles and more, with ragged edges: the
+    residual added, read and written in place, and the gradient."""
+    X, W = _randn((M, K), "bf16", 21), _randn((N, K), "bf16", 22, K ** -0.5)
+    b = _randn((N,), "bf16", 23) if bias else None
+    r, dY = _randn((M, N), "bf16", 24), _randn((M, N), "bf16", 25)
+    Xd, Wd, rd, gd = (t.to(DEV) for t in (X, W, r, dY))
+    bd = None if b is None else b.to(DEV)
+    f = [None if t is None else to_f64(t) for t in (X, W, b, r)]
+    y, z = ops.linear(f[0], f[1], f[2], name, p, 41, 3, f[3])
+    ez, ea = _linear_bounds("bf16", f[0], f[1], f[2], z, name)
+    kw = dict(bias=bd, act=name, p=p, seed=41, step=3)
+    Z = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+    out = rnc.dprc_linear(Xd, Wd, residual=rd, Z=Z, **kw)
+    _close(Z, z, _round("bf16", z) + ez)
+    _close(out, y, _round("bf16", y) + ea / (1 - p) + 3 * ULP * np.abs(y))
+    assert torch.equal(out, rnc.dprc_linear(Xd, Wd, residual=rd, **kw))
+    acc = rd.clone()
+    rnc.dprc_linear(Xd, Wd, residual=acc, out=acc, **kw)
+    assert torch.equal(out, acc)
+
+    # the gradient at the kernel's own Z, which both sides then hold exactly
+    dX, dW = torch.empty_like(Xd), torch.empty_like(Wd)
+    db, dZ = torch.empty(N, dtype=torch.bfloat16, device=DEV), torch.empty_like(Z)
+    rnc.dprc_linear_grad(gd, Xd, Wd, Z=Z, act=name, p=p, seed=41, step=3, dX=dX, dW=dW, db=db, dZ=dZ)
+    gX, gW, gb, gZ = ops.linear_grad(to_f64(dY), f[0], f[1], to_f64(Z), name, p, 41, 3)
+    ez = 2.0 ** -17 * np.abs(to_f64(dY)) * (1 + np.abs(to_f64(Z)))
+    _close(dZ, gZ, _round("bf16", gZ) + ez)
+    eZ = 2.0 ** -8 * np.abs(gZ) + ez  # dZ as it enters the products
+    aX, aW = np.abs(f[0]), np.abs(f[1])
+    _close(dX, gX, _round("bf16", gX) + eZ @ aW + (N / 16 + 80) * ULP * (np.abs(gZ) @ aW))
+    _close(dW, gW, _round("bf16", gW) + eZ.T @ aX + (M / 16 + 80) * ULP * (np.abs(gZ).T @ aX))
+    _close(db, gb, _round("bf16", gb) + ez.sum(0) + M * ULP * np.abs(gZ).sum(0))
