@@ -368,15 +368,15 @@ constexpr int64_t kFewTokens = 64;
 
 // Whether the forward map of M tokens runs on the CUDA cores (linear_few.cu).
 // Measured with the weights in turn in L2 and memory (us, CUDA cores / tensor
-// cores): bf16 2048 x 8192 M = 1 6.9 / 10.3, M = 4 10.2 / 10.5, M = 8 19.7 / 10.5;
-// 2048 x 512 M = 16 3.1 / 6.2, M = 32 5.6 / 6.5, M = 64 10.3 / 7.0; fp32
+// cores): bf16 2048 x 8192 M = 1 6.9 / 10.0, M = 4 10.1 / 10.2, M = 8 19.7 / 10.2;
+// 2048 x 512 M = 16 3.1 / 5.6, M = 32 5.6 / 6.3, M = 64 10.3 / 7.0; fp32
 // 2048 x 8192 M = 8 28 / 72, M = 24 51 / 67, M = 32 63 / 67, M = 64 111 / 71;
 // 8192 x 2048 M = 32 70 / 68; 2048 x 512 M = 64 11.3 / 17.9.  The cores' time grows with N K M, the other's with N K: they
 // cross where N K (M - m) is a constant.
 bool few_tokens(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
   if (M > kFewTokens) return false;
   const int64_t nk = N * K;
-  return dt == DPRC_F32 ? nk * (M - 26) <= 100000000 : nk * (M - 2) <= 40000000;
+  return dt == DPRC_F32 ? nk * (M - 26) <= 100000000 : nk * (M - 2) <= 32000000;
 }
 
 // LinearEpi::vec for rows of N elements at these addresses (null: not used).

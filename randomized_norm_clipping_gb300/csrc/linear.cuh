@@ -277,6 +277,7 @@ struct GemmShape {
 struct GemmPlan {
   int tn = 256;
   bool pair = false;        // 256 x 256 tiles on CTA pairs
+  bool join = false;        // the shares of a tile are a cluster: no partial sums in memory
   int split = 1;
   int64_t units = 0;        // contraction units of 64
   int64_t per = 0;          // units of a share

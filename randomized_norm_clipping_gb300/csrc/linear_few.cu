@@ -4,8 +4,8 @@
 // The weights are read once, at their own width, and that is the bound: with M
 // tokens there are M multiply-adds per weight, below what the cores do while
 // the weights arrive up to some eight tokens.  The tensor-core path
-// (linear_gemm.cu) needs a second launch for the sum of its shares and, for
-// fp32, a pass that writes the weights' three planes; one launch here does all.
+// (linear_gemm.cu) pays for its start and the sum of its shares and, for fp32, a
+// pass that writes the weights' three planes; here the cores start at once.
 //
 // A warp takes kFeat features (rows of W) and up to kTok tokens: a lane reads
 // one 16-byte access of each row and of each token per step, lanes side by

@@ -14,7 +14,8 @@
 //
 // Few tokens: the weights' rows take the 128 lanes of the tile and the tokens
 // its kTn columns (16 to 64), so the weights stream through once and the
-// tokens cost what they are; D is then stored transposed, by partial sums.
+// tokens cost what they are; D is then stored transposed, by partial sums in
+// memory or in the shared memory of a cluster (GemmPlan::join).
 //
 // Tiles are walked in groups of row tiles, all columns of a group before the
 // next: as many rows as make a group about one wave where there are few
@@ -23,6 +24,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "launch.cuh"
 #include "linear.cuh"
@@ -55,7 +57,10 @@ struct GemmCfg {
   static constexpr int kEpiWarps = kTn >= 64 ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kCols = kTn / (kEpiWarps / 4);  // columns per epilogue warp
-  static constexpr int kSmem = kStages * kStage + 1024 + 512;
+  // the sums a CTA gives its cluster (GemmPlan::join), [kTn][kTm] behind the barriers
+  static constexpr bool kJoin = sizeof(T) == 2 && kTn <= 32;
+  static constexpr int kSmem = kStages * kStage + 1024 + 512 + (kJoin ? kTn * kTm * 4 : 0);
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
 // One thread's bounded wait for a phase of a barrier of this CTA: like
@@ -108,6 +113,7 @@ struct GemmArgs {
   int units, per_split;     // contraction units of 64, and of one share
   int a_mn, b_mn;
   int transposed;
+  int join;                 // the shares of a tile are a cluster, which adds them up
   float* part;              // partial sums, or null: the epilogue
   long long ldpart, part_stride;
   int beside;               // runs beside the kernel before (launch.cuh)
@@ -180,6 +186,15 @@ __device__ __forceinline__ void gemm_emit(const GemmArgs& a, int split, long lon
   } else {
     linear_out<T, kN / 8>(a.epi, row, col, v, rk);
   }
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 // Accumulators.  bf16: one per tile, two sets in turn, so that a tile's
@@ -268,12 +283,12 @@ __device__ __forceinline__ bool gemm_collect_ahead(const GemmArgs& a, uint32_t t
 // The sums of one unit of work for this thread's row (TMEM lane), kCols of
 // them from column tmem of each accumulator on (kAcc columns apart), first
 // column col0 of D.  `release(set)` frees a set.
-template <typename T, int kCols, int kAcc, int kSets, typename Release>
+// emit(N, c, v): takes the N sums v from column c of them on.
+template <typename T, int kCols, int kAcc, int kSets, typename Release, typename Emit>
 __device__ __forceinline__ bool gemm_collect(const GemmArgs& a, const GemmUnit& g, uint32_t tmem,
-                                             long long row, int col0, const RoundKeys& rk,
-                                             uint64_t* accf, AccPos<kSets>& pos,
+                                             int col0, uint64_t* accf, AccPos<kSets>& pos,
                                              const volatile int* abort_flag, bool ok,
-                                             Release release) {
+                                             Release release, Emit emit) {
   if constexpr (sizeof(T) == 2) {
     constexpr int kStep = kCols < 16 ? kCols : 16;
     ok = ok && wait_warp(&accf[pos.set], pos.parity, DPRC_DEVERR_ACCUM, abort_flag);
@@ -284,7 +299,7 @@ __device__ __forceinline__ bool gemm_collect(const GemmArgs& a, const GemmUnit& 
         if (col0 + c0 >= a.cols) break;  // uniform over the warp
         float v[kStep];
         tmem_ld_cols<kStep>(tmem + pos.set * kAcc + c0, v);
-        gemm_emit<T, kStep>(a, g.split, row, col0 + c0, v, rk);
+        emit(std::integral_constant<int, kStep>{}, c0, v);
       }
     }
     release(pos.set);
@@ -313,8 +328,7 @@ __device__ __forceinline__ bool gemm_collect(const GemmArgs& a, const GemmUnit& 
     }
     if (ok) {
 #pragma unroll
-      for (int c0 = 0; c0 < kCols; c0 += 8)
-        gemm_emit<T, 8>(a, g.split, row, col0 + c0, acc + c0, rk);
+      for (int c0 = 0; c0 < kCols; c0 += 8) emit(std::integral_constant<int, 8>{}, c0, acc + c0);
     }
   }
   return ok;
@@ -348,7 +362,12 @@ __global__ void __launch_bounds__(GemmCfg<kTn, T>::kThreads, 1)
   uint64_t* drain = acce + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* sums = reinterpret_cast<float*>(ring + kStages * Cfg::kStage + 512);  // kJoin
 
+  if (Cfg::kJoin && a.join && cluster_nctarank() != static_cast<uint32_t>(a.split)) {
+    if (threadIdx.x == 0) record_error(DPRC_DEVERR_LAUNCH);  // no peers to read from
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nwork = a.mt * a.nt * a.split;  // the host checks that it fits
   const int first = static_cast<int>(blockIdx.x), stride = static_cast<int>(gridDim.x);
@@ -487,13 +506,50 @@ __global__ void __launch_bounds__(GemmCfg<kTn, T>::kThreads, 1)
     for (int j = 0; j < mine; ++j) {
       const GemmUnit g = gemm_unit(a, first + j * stride);
       const long long row = static_cast<long long>(g.m) * kTm + q * 32 + lane;
-      ok = gemm_collect<T, Cfg::kCols, kTn, 2>(a, g, tb, row, g.n * kTn + c_lo, rk, accf, pos,
-                                            abort_flag, ok, release);
+      const int col = g.n * kTn + c_lo;
+      const auto emit = [&](auto n, int c, float* v) {
+        constexpr int kN = decltype(n)::value;
+        if constexpr (Cfg::kJoin) {
+          if (a.join) {
+#pragma unroll
+            for (int t = 0; t < kN; ++t) sums[(c_lo + c + t) * kTm + q * 32 + lane] = v[t];
+            return;
+          }
+        }
+        gemm_emit<T, kN>(a, g.split, row, col + c, v, rk);
+      };
+      ok = gemm_collect<T, Cfg::kCols, kTn, 2>(a, g, tb, col, accf, pos, abort_flag, ok, release,
+                                               emit);
     }
   }
 
   __syncwarp();  // reconverge each warp before the CTA barrier
   tc_fence_before();
+  if constexpr (Cfg::kJoin) {
+    if (a.join) {
+      // each CTA of the cluster adds up its part of the tile's outputs, the
+      // shares in order
+      cluster_sync_all();
+      const GemmUnit g = gemm_unit(a, first);
+      const RoundKeys rk = round_keys(a.epi.drop.seed);
+      const int total = a.cols * (kTm / 8), each = (total + a.split - 1) / a.split;
+      const int end = min((g.split + 1) * each, total);
+      for (int i = g.split * each + static_cast<int>(threadIdx.x); i < end; i += Cfg::kThreads) {
+        const int t = i / (kTm / 8), f = i % (kTm / 8) * 8;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < a.split; ++s) {
+          const uint32_t from = map_to_rank(sums + t * kTm + f, s);
+          const float4 x = ld_cluster_f4(from), y = ld_cluster_f4(from + 16);
+          v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+          v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+        }
+        const long long n = static_cast<long long>(g.m) * kTm + f;
+        if (n < a.rows) linear_out<T, 1>(a.epi, t, static_cast<int>(n), v, rk);
+      }
+      __syncwarp();
+      cluster_sync_all();  // nobody leaves while its sums are read
+    }
+  }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -801,12 +857,15 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
       const GemmArgs& a = batch.p[j >= work.mine0];
       const GemmUnit g = gemm_unit(a, work.at(j));
       const long long row = static_cast<long long>(g.m) * kPairTile + rank * kTm + q * 32 + lane;
+      const int col = g.n * kPairTile + c_lo;
       if constexpr (kRes)
-        ok = gemm_collect_ahead<kCols, kPairTile>(a, tb, row, g.n * kPairTile + c_lo, rk, accf,
-                                                  pos, abort_flag, ok, release);
+        ok = gemm_collect_ahead<kCols, kPairTile>(a, tb, row, col, rk, accf, pos, abort_flag, ok,
+                                                  release);
       else
         ok = gemm_collect<T, kCols, kPairTile, kPairSets<T>>(
-            a, g, tb, row, g.n * kPairTile + c_lo, rk, accf, pos, abort_flag, ok, release);
+            a, g, tb, col, accf, pos, abort_flag, ok, release, [&](auto n, int c, float* v) {
+              gemm_emit<T, decltype(n)::value>(a, g.split, row, col + c, v, rk);
+            });
     }
   }
 
@@ -872,7 +931,7 @@ cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const Ge
   const long long work = static_cast<long long>(a.mt) * a.nt * a.split;
   const long long grid = work < device_sm_count() ? work : device_sm_count();
   return launch_after(linear_gemm_kernel<kTn, T>, dim3(static_cast<unsigned>(grid)), Cfg::kThreads,
-                      1, s, Cfg::kSmem, ma, mb, a);
+                      a.join ? a.split : 1, s, Cfg::kSmem, ma, mb, a);
 }
 
 template <typename T>
@@ -941,13 +1000,22 @@ GemmPlan plan_gemm(const GemmShape& g) {
       if (split != want) continue;
       const int64_t waves = (tiles * split + slots - 1) / slots;
       double cost = static_cast<double>(waves) * (per * sh.step * products + 200.0) + 8.0 * sh.tn;
-      const bool partial = split > 1 || g.transposed;
+      // Few tokens: a tile's shares as a cluster that adds them up through shared
+      // memory, where all tiles run at once.  How many clusters that is depends on
+      // the GPCs: 32 clusters of 4 do (4096 x 4096, 8 tokens: 10.2 us, by partial
+      // sums 10.7), 16 of 8 do not (8192 x 2048: 18.2, by partial sums 11.2).
+      const int64_t at_once = split <= 2 ? sms : split == 4 ? sms * 7 / 8 : split == 8 ? sms / 2 : 0;
+      const bool join =
+          g.transposed && g.planes == 1 && sh.tn <= 32 && tiles * split <= at_once;
+      const bool partial = !join && (split > 1 || g.transposed);
+      if (join) cost += 1500.0;
       if (partial)  // written and read through L2 at some 5 KB a cycle, and a launch
         cost += 3000.0 + static_cast<double>(split) * g.rows * g.cols * 8.0 / 5000.0;
       if (cost < best) {
         best = cost;
         p.cost = cost;
         p.tn = sh.tn;
+        p.join = join;
         p.pair = sh.ctas == 2;
         p.split = static_cast<int>(split);
         p.per = per;
@@ -955,7 +1023,7 @@ GemmPlan plan_gemm(const GemmShape& g) {
       if (tiles * split >= 4 * static_cast<int64_t>(sms)) break;
     }
   }
-  if (p.split > 1 || g.transposed) {
+  if (!p.join && (p.split > 1 || g.transposed)) {
     const int64_t out_rows = g.transposed ? g.cols : g.rows;
     const int64_t out_cols = g.transposed ? g.rows : g.cols;
     p.ldpart = (out_cols + 7) / 8 * 8;
@@ -990,6 +1058,7 @@ cudaError_t prepare_gemm(const GemmShape& g, const GemmPlan& p, const GemmOperan
   a.a_mn = A.mn_major;
   a.b_mn = B.mn_major;
   a.transposed = g.transposed;
+  a.join = p.join;
   a.part = p.part_bytes > 0 ? static_cast<float*>(part) : nullptr;
   a.ldpart = p.ldpart;
   a.part_stride = (g.transposed ? g.cols : g.rows) * p.ldpart;
