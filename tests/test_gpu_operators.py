@@ -577,3 +577,19 @@ def test_linear_of_many_tiles(M, K, N, name, bias, p):
     _close(dX, gX, _round("bf16", gX) + eZ @ aW + (N / 16 + 80) * ULP * (np.abs(gZ) @ aW))
     _close(dW, gW, _round("bf16", gW) + eZ.T @ aX + (M / 16 + 80) * ULP * (np.abs(gZ).T @ aX))
     _close(db, gb, _round("bf16", gb) + ez.sum(0) + M * ULP * np.abs(gZ).sum(0))
+
+
+@pytest.mark.parametrize("N,V", [(8193, 1 << 30), (200_003, (1 << 21) + 3), (65_537, 300)])
+def test_plans_in_one_buffer(N, V):
+    """Orders of several digits, one after the other in the same memory."""
+    buf = torch.empty(rnc.binding.lib().dprc_embed_plan_bytes(N, V), dtype=torch.uint8, device=DEV)
+    step = (4 * N + 255) // 256 * 256
+    for seed in range(4):
+        tok = torch.randint(-1, V, (1, N), generator=_gen(seed))
+        tok[0, :N // 2] = torch.randint(0, 1 + seed, (N // 2,), generator=_gen(seed + 9))
+        rnc.dprc_embed_plan(tok.to(DEV), V, buf=buf)
+        key = np.where(tok[0].numpy() < 0, V, tok[0].numpy())
+        order = np.argsort(key, kind="stable")
+        raw = buf.cpu().numpy()
+        assert (raw[:4 * N].view(np.uint32) == key[order]).all()
+        assert (raw[step:step + 4 * N].view(np.int32) == order).all()
