@@ -167,11 +167,20 @@ __device__ __forceinline__ GemmUnit gemm_unit(const GemmArgs& a, int w) {
 }
 
 // kN finished sums of one row, the first of them column col of D: through the
-// epilogue, or to the partial sums.
-template <typename T, int kN>
+// epilogue, or to the partial sums.  kOdd: bf16 rows of D that may be no whole
+// 16-byte accesses (a lane's eight fp32 values are a whole 32-byte sector without
+// turning: 4097 x 1001 x 1001 with GELU, dropout and Z 114 us, turned 129).
+template <typename T, int kN, bool kOdd>
 __device__ __forceinline__ void gemm_emit(const GemmArgs& a, int split, long long row, int col,
                                           float* v, const RoundKeys& rk) {
-  if (row >= a.rows || col >= a.cols) return;
+  if (col >= a.cols) return;  // the same for a warp
+  if constexpr (kOdd) {
+    if (a.part == nullptr && a.epi.vec == 0) {
+      linear_out_odd<T, kN>(a.epi, row, col, v, rk);
+      return;
+    }
+  }
+  if (row >= a.rows) return;
   if (a.transposed) {
     float* out = a.part + split * a.part_stride + row;
 #pragma unroll
@@ -516,7 +525,7 @@ __global__ void __launch_bounds__(GemmCfg<kTn, T>::kThreads, 1)
             return;
           }
         }
-        gemm_emit<T, kN>(a, g.split, row, col + c, v, rk);
+        gemm_emit<T, kN, kTn >= 64 && sizeof(T) == 2>(a, g.split, row, col + c, v, rk);
       };
       ok = gemm_collect<T, Cfg::kCols, kTn, 2>(a, g, tb, col, accf, pos, abort_flag, ok, release,
                                                emit);
@@ -679,10 +688,11 @@ __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr
                : "memory");
 }
 
-// kRes: bf16 whole outputs with a residual, whose epilogue loads ahead; an
-// instantiation of its own, since both epilogues in one kernel cost the plain one
-// registers (16384 x 1024 x 1024: 33 -> 35 to 40 us).
-template <typename T, bool kRes>
+// The pair's epilogues are instantiations of their own, since two in one kernel
+// cost the plain one registers (16384 x 1024 x 1024: 33 -> 35 to 40 us): rows of
+// whole 16-byte accesses and fp32, bf16 with a residual (loaded ahead), other bf16.
+enum PairEpilogue { kWholeRows, kResidual, kOddRows };
+template <typename T, PairEpilogue kEpilogue>
 __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims__(2, 1, 1)
     linear_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a0,
                             const __grid_constant__ CUtensorMap map_b0,
@@ -858,13 +868,13 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
       const GemmUnit g = gemm_unit(a, work.at(j));
       const long long row = static_cast<long long>(g.m) * kPairTile + rank * kTm + q * 32 + lane;
       const int col = g.n * kPairTile + c_lo;
-      if constexpr (kRes)
+      if constexpr (kEpilogue == kResidual)
         ok = gemm_collect_ahead<kCols, kPairTile>(a, tb, row, col, rk, accf, pos, abort_flag, ok,
                                                   release);
       else
         ok = gemm_collect<T, kCols, kPairTile, kPairSets<T>>(
             a, g, tb, col, accf, pos, abort_flag, ok, release, [&](auto n, int c, float* v) {
-              gemm_emit<T, decltype(n)::value>(a, g.split, row, col + c, v, rk);
+              gemm_emit<T, decltype(n)::value, kEpilogue == kOddRows>(a, g.split, row, col + c, v, rk);
             });
     }
   }
@@ -879,10 +889,10 @@ __global__ void __launch_bounds__(64 + 32 * kPairEpiWarps<T>, 1) __cluster_dims_
   beside_end(batch.p[0].beside != 0);
 }
 
-template <typename T, bool kRes>
+template <typename T, PairEpilogue kEpilogue>
 cudaError_t launch_gemm_pair_t(const CUtensorMap* maps, const GemmBatch& batch, cudaStream_t s) {
-  auto* kernel = linear_gemm_pair_kernel<T, kRes>;
-  const cudaError_t e = set_smem_once<2 + sizeof(T) + kRes>(kernel, kPairSmem<T>);
+  auto* kernel = linear_gemm_pair_kernel<T, kEpilogue>;
+  const cudaError_t e = set_smem_once<sizeof(T) * 4 + kEpilogue>(kernel, kPairSmem<T>);
   if (e != cudaSuccess) return e;
   const long long pairs =
       std::min<long long>(static_cast<long long>(batch.n0) + batch.n1, device_sm_count() / 2);
@@ -892,12 +902,14 @@ cudaError_t launch_gemm_pair_t(const CUtensorMap* maps, const GemmBatch& batch, 
 
 template <typename T>
 cudaError_t launch_gemm_pair(const CUtensorMap* maps, const GemmBatch& batch, cudaStream_t s) {
+  const GemmArgs& a = batch.p[0];  // two products have rows of one length
   if constexpr (sizeof(T) == 2) {
-    const GemmArgs& a = batch.p[0];
+    if (a.part == nullptr && a.epi.vec == 0)
+      return launch_gemm_pair_t<T, kOddRows>(maps, batch, s);
     if (batch.n1 == 0 && a.part == nullptr && a.epi.vec == 2 && a.epi.res != nullptr)
-      return launch_gemm_pair_t<T, true>(maps, batch, s);
+      return launch_gemm_pair_t<T, kResidual>(maps, batch, s);
   }
-  return launch_gemm_pair_t<T, false>(maps, batch, s);
+  return launch_gemm_pair_t<T, kWholeRows>(maps, batch, s);
 }
 
 // How the second product's units are dealt (GemmBatch), and the busiest pair's

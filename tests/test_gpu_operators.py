@@ -593,3 +593,30 @@ def test_plans_in_one_buffer(N, V):
         raw = buf.cpu().numpy()
         assert (raw[:4 * N].view(np.uint32) == key[order]).all()
         assert (raw[step:step + 4 * N].view(np.int32) == order).all()
+
+
+@pytest.mark.parametrize("M,K,N", [(3001, 475, 2466), (2300, 264, 2049), (5001, 2049, 136)])
+@pytest.mark.parametrize("name,bias,p", [("none", True, 0.1), ("gelu", False, 0.4)])
+def test_linear_of_many_odd_tiles(M, K, N, name, bias, p):
+    test_linear_of_many_tiles(M, K, N, name, bias, p)
+
+
+@pytest.mark.parametrize("M,K,N", [(2305, 130, 2049), (3001, 1027, 70)])
+def test_linear_of_many_odd_tiles_f32(M, K, N):
+    X, W = _randn((M, K), "f32", 31), _randn((N, K), "f32", 32, K ** -0.5)
+    b, r = _randn((N,), "f32", 33), _randn((M, N), "f32", 34)
+    f = [to_f64(t) for t in (X, W, b, r)]
+    y, z = ops.linear(f[0], f[1], f[2], "silu", 0.2, 51, 4, f[3])
+    ez, ea = _linear_bounds("f32", f[0], f[1], f[2], z, "silu")
+    Z = torch.empty((M, N), device=DEV)
+    out = rnc.dprc_linear(X.to(DEV), W.to(DEV), bias=b.to(DEV), act="silu", p=0.2, seed=51, step=4,
+                          residual=r.to(DEV), Z=Z)
+    _close(Z, z, _round("f32", z) + ez)
+    _close(out, y, _round("f32", y) + ea / 0.8 + 3 * ULP * np.abs(y))
+    dX, dW = torch.empty((M, K), device=DEV), torch.empty((N, K), device=DEV)
+    rnc.dprc_linear_grad(r.to(DEV), X.to(DEV), W.to(DEV), dX=dX, dW=dW)
+    aX, aW, ar = (np.abs(t) for t in (f[0], f[1], f[3]))
+    ref = f[3] @ f[1]
+    _close(dX, ref, _round("f32", ref) + (6 * N / 16 + 84) * ULP * (ar @ aW))
+    ref = f[3].T @ f[0]
+    _close(dW, ref, _round("f32", ref) + (6 * M / 16 + 84) * ULP * (ar.T @ aX))
