@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(kSortThreads)
       __syncwarp();
       if (live && (same & lt) == 0) hist[digit] += __popc(same);
       __syncwarp();
-      if (live && DPRC_IN(at >= 0 && at < a.N)) {
+      // (tokens that another stream changes meanwhile would not be where they were counted)
+      if (live && DPRC_IN(at >= 0 && at < a.N) && at < a.N) {
         a.key_out[at] = k[j];
         a.pos_out[at] = p[j];
         if (a.next != nullptr)
@@ -514,6 +515,7 @@ struct SegArgs {
                       // the entry of the range that the run beginning here begins with
   // grad: rows no token names
   long long zero_units;
+  int zero_chunks;    // of kZeroBytes, of a row
 };
 
 // Sample of a position: pos / T by a multiplication (Lemire, Kaser and Kurz,
@@ -522,6 +524,13 @@ struct SegArgs {
 __device__ __forceinline__ int sample_of(const SegArgs& a, int pos) {
   return a.t_inv == 0 ? pos
                       : static_cast<int>(__umul64hi(a.t_inv, static_cast<unsigned long long>(pos)));
+}
+
+// Position of sorted entry i.  A plan is memory of the caller's: one that is not
+// what dprc_embed_plan wrote (read on another stream before it was written, say)
+// gives wrong sums, but no access outside the tensors.
+__device__ __forceinline__ int plan_pos(const SegArgs& a, long long i) {
+  return static_cast<int>(min(static_cast<uint32_t>(__ldg(a.pos + i)), static_cast<uint32_t>(a.N - 1)));
 }
 
 // Rows of a range: lane l holds row l (l < rows).
@@ -552,8 +561,8 @@ __device__ __forceinline__ RangeRows range_rows(const SegArgs& a, int range, boo
   for (int w = 0; w < 3; ++w) {
     const int i = a0 - 32 + w * 32 + lane;
     const bool in = i >= 0 && i < a.N;
-    kw[w] = in ? __ldg(a.key + i) : V;
-    pw[w] = in ? __ldg(a.pos + i) : 0;
+    kw[w] = in ? min(__ldg(a.key + i), V) : V;
+    pw[w] = in ? plan_pos(a, i) : 0;
   }
   uint32_t klast = kw[0];
   int slast = 0;
@@ -765,7 +774,7 @@ __device__ __forceinline__ void segment_range(const SegArgs& a, const T* __restr
         if (DPRC_IN(p >= 0 && p < a.N)) a.sq[static_cast<long long>(p) * a.nblk + blk] = t;
       }
       if ((s.none >> lane) & 1u)
-        a.sq[static_cast<long long>(__ldg(a.pos + range * kRange + lane)) * a.nblk + blk] = 0.f;
+        a.sq[static_cast<long long>(plan_pos(a, range * kRange + lane)) * a.nblk + blk] = 0.f;
     }
   }
 }
@@ -780,13 +789,18 @@ __device__ __forceinline__ long long lower_bound(const uint32_t* key, long long 
   return lo;
 }
 
-// Rows of dW that no token names are zero: 32 rows per warp, one search per lane.
+// Rows of dW that no token names are zero: kZeroBytes of 32 rows per warp, one
+// search per lane.  (Whole rows per warp left too few warps where rows are long:
+// gradients of 8361 rows of 6688 bf16 54 us and not 26, 51463 of 5216 173 and
+// not 102.)
+constexpr int kZeroBytes = 4096;
 template <typename T, int AW>
 __device__ __forceinline__ void zero_rows(const SegArgs& a, T* __restrict__ dW, long long unit) {
   using RawT = typename Raw<AW>::type;
   constexpr int VE = AW / static_cast<int>(sizeof(T));
   const int lane = threadIdx.x & 31;
-  const long long v = unit * 32 + lane;
+  const long long v0 = unit / a.zero_chunks * 32, v = v0 + lane;
+  const int chunk = static_cast<int>(unit % a.zero_chunks);
   bool absent = false;
   if (v < a.V) {
     const long long i = lower_bound(a.key, a.N, static_cast<uint32_t>(v));
@@ -801,9 +815,11 @@ __device__ __forceinline__ void zero_rows(const SegArgs& a, T* __restrict__ dW, 
   while (todo != 0) {
     const int j = __ffs(static_cast<int>(todo)) - 1;
     todo &= todo - 1;
-    RawT* row = reinterpret_cast<RawT*>(dW + (unit * 32 + j) * a.d);
-    for (long long x = lane; x < nvec; x += 32)
-      if (DPRC_IN(unit * 32 + j < a.V)) __stcs(row + x, zero);
+    RawT* row = reinterpret_cast<RawT*>(dW + (v0 + j) * a.d);
+    const long long x0 = static_cast<long long>(chunk) * (kZeroBytes / AW);
+    const long long x1 = x0 + kZeroBytes / AW < nvec ? x0 + kZeroBytes / AW : nvec;
+    for (long long x = x0 + lane; x < x1; x += 32)
+      if (DPRC_IN(v0 + j < a.V)) __stcs(row + x, zero);
   }
 }
 
@@ -875,10 +891,11 @@ __device__ __forceinline__ void finish_run(const SegArgs& a, T* __restrict__ dW,
       const int at = static_cast<int>(range) * kRange + first + static_cast<int>(blockIdx.y) % kRange;
       const int blk = static_cast<int>(blockIdx.y) / kRange;
       if (DPRC_IN(at < a.N && blk < a.nblk))
-        a.sq[static_cast<long long>(__ldg(a.pos + at)) * a.nblk + blk] = q;
+        a.sq[static_cast<long long>(plan_pos(a, min(at, a.N - 1))) * a.nblk + blk] = q;
     }
   } else {
-    const uint32_t k = __ldg(a.key + (range + 1) * kRange - 1);  // the run reaches past `range`
+    // (the run reaches past `range`)
+    const uint32_t k = min(__ldg(a.key + (range + 1) * kRange - 1), static_cast<uint32_t>(a.V - 1));
     T* out = dW + static_cast<long long>(k) * a.d;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -1090,6 +1107,7 @@ SegArgs seg_args(const EmbedCall& c, const SegPlan& p, const SortPlan& sp, char*
   a.dpad = p.dpad;
   a.long_at = reinterpret_cast<int*>(ws + p.long_off);
   a.zero_units = 0;
+  a.zero_chunks = 1;
   return a;
 }
 
@@ -1266,7 +1284,9 @@ cudaError_t launch_embed_grad(const EmbedCall& c, const float* clip, void* dW, v
   const SegPlan p = seg_plan(c.dtype, c.B * c.T, c.d, false);
   SegArgs a = seg_args(c, p, sort_plan(c.B * c.T, c.V), static_cast<char*>(ws));
   a.c = clip;
-  a.zero_units = c.accumulate ? 0 : (c.V + 31) / 32;
+  a.zero_chunks = static_cast<int>(
+      (c.d * (c.dtype == DPRC_F32 ? 4 : 2) + kZeroBytes - 1) / kZeroBytes);
+  a.zero_units = c.accumulate ? 0 : (c.V + 31) / 32 * a.zero_chunks;
   return launch_segments<false>(c.dtype, a, p, c.G, dW, s);
 }
 
