@@ -973,12 +973,15 @@ __global__ void __launch_bounds__(32 * kLongWarps)
 // ---------------------------------------------------------------------------
 // n_i (+)= s^2 (sum of sample i's squares), its positions' squares of every
 // column block in a fixed order.  A sample's sum is split over the CTAs of a
-// cluster, which add their parts in rank order.
+// cluster, which add their parts in rank order.  Rank 0's shared memory takes the
+// parts, so no CTA stores its own before every CTA has started: each arrives at the
+// cluster's barrier first and waits for it after its loads, which hide it.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
     embed_norm_finish_kernel(const SegArgs a, float* __restrict__ n) {
   __shared__ float s_warp[8];
   __shared__ float s_cta[8];
+  cluster_arrive();
   pdl_wait();
   const uint32_t rank = cluster_ctarank(), cl = cluster_nctarank();
   const long long i = blockIdx.x / cl;
@@ -993,6 +996,7 @@ __global__ void __launch_bounds__(256)
   for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
   if (lane == 0) s_warp[warp] = s;
   __syncthreads();
+  cluster_wait();
   if (threadIdx.x == 0) {
     float t = 0.f;
     for (int w = 0; w < 8; ++w) t += s_warp[w];
