@@ -58,8 +58,8 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 // generator's work); else they are one block.
 template <typename T, bool kRes, bool kShift>
 __global__ void __launch_bounds__(kDropThreads)
-    dropout_kernel(const T* x, const T* __restrict__ res, long long n,
-                   uint64_t first, const DropArgs a, T* y) {
+    dropout_kernel(const T* x, const T* res, long long n, uint64_t first, const DropArgs a,
+                   T* y) {
   const RoundKeys rk = round_keys(a.seed);
   pdl_launch_dependents();
   pdl_wait();

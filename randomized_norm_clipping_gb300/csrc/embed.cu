@@ -138,9 +138,8 @@ constexpr int kLookupUnroll = 4;
 
 template <typename T, int AW, typename TOK>
 __global__ void __launch_bounds__(256)
-    embed_lookup_kernel(const T* __restrict__ W, const TOK* __restrict__ tokens, long long N,
-                        int V, long long d, float scale, T* __restrict__ out, int lanes,
-                        int units_per_row) {
+    embed_lookup_kernel(const T* W, const TOK* tokens, long long N, int V, long long d,
+                        float scale, T* out, int lanes, int units_per_row) {
   using R = typename Raw<AW>::type;
   constexpr int VE = AW / static_cast<int>(sizeof(T));
   pdl_launch_dependents();
@@ -161,7 +160,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int j = 0; j < kLookupUnroll; ++j) {
       const int v = v0 + j * lanes;
-      if (have && v < nvec) raw[j] = __ldg(src + v);
+      if (have && v < nvec) raw[j] = src[v];
     }
 #pragma unroll
     for (int j = 0; j < kLookupUnroll; ++j) {
@@ -195,8 +194,7 @@ constexpr int kRankPer = 4;  // entries of a warp
 
 template <typename TOK>
 __global__ void __launch_bounds__(32 * kRankWarps)
-    token_rank_kernel(const TOK* __restrict__ tokens, int N, int V, uint32_t* __restrict__ key_out,
-                      int* __restrict__ pos_out) {
+    token_rank_kernel(const TOK* tokens, int N, int V, uint32_t* key_out, int* pos_out) {
   extern __shared__ __align__(16) uint32_t s_key[];  // [N rounded up to 128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int padded = (N + 127) / 128 * 128;
@@ -208,7 +206,7 @@ __global__ void __launch_bounds__(32 * kRankWarps)
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int j = j0 + u * 32 * kRankWarps;
-      t[u] = j < N ? __ldg(tokens + j) : TOK(0);
+      t[u] = j < N ? __ldcg(tokens + j) : TOK(0);
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -305,7 +303,7 @@ __device__ __forceinline__ void sort_keys(const TOK* src, int V, int i0, int ste
                                           uint32_t* k) {
   TOK t[kSortBatch];
 #pragma unroll
-  for (int j = 0; j < kSortBatch; ++j) t[j] = i0 + j * step < hi ? __ldg(src + i0 + j * step) : TOK(0);
+  for (int j = 0; j < kSortBatch; ++j) t[j] = i0 + j * step < hi ? __ldcg(src + i0 + j * step) : TOK(0);
 #pragma unroll
   for (int j = 0; j < kSortBatch; ++j) {
     if constexpr (sizeof(TOK) == 4 && TOK(-1) > TOK(0))
@@ -330,7 +328,7 @@ __device__ __forceinline__ uint32_t equal_lanes(uint32_t digit, bool live) {
 
 template <typename TOK>
 __global__ void __launch_bounds__(kSortThreads)
-    token_count_kernel(const TOK* __restrict__ src, const SortArgs a) {
+    token_count_kernel(const TOK* src, const SortArgs a) {
   __shared__ int s_hist[1 << kSortMaxBits];
   pdl_launch_dependents();
   const int nd = 1 << a.bits;
@@ -358,7 +356,7 @@ __global__ void __launch_bounds__(kSortThreads)
 
 template <typename TOK>
 __global__ void __launch_bounds__(kSortThreads)
-    token_scatter_kernel(const TOK* __restrict__ src, const SortArgs a) {
+    token_scatter_kernel(const TOK* src, const SortArgs a) {
   extern __shared__ int s_dyn[];
   __shared__ int s_scan[kSortWarps];
   pdl_launch_dependents();
@@ -392,7 +390,7 @@ __global__ void __launch_bounds__(kSortThreads)
       int2 v[16];
 #pragma unroll
       for (int u = 0; u < 16; ++u)
-        v[u] = t0 + u < tiles ? __ldg(reinterpret_cast<const int2*>(a.counts + (t0 + u) * nd + d))
+        v[u] = t0 + u < tiles ? __ldcg(reinterpret_cast<const int2*>(a.counts + (t0 + u) * nd + d))
                               : make_int2(0, 0);
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
@@ -441,7 +439,7 @@ __global__ void __launch_bounds__(kSortThreads)
 #pragma unroll
     for (int j = 0; j < kSortBatch; ++j) {
       const int i = i0 + j * 32 + lane;
-      p[j] = i < hi && a.pos_in != nullptr ? __ldg(a.pos_in + i) : i;
+      p[j] = i < hi && a.pos_in != nullptr ? __ldcg(a.pos_in + i) : i;
     }
     sort_keys(src, a.V, i0 + lane, 32, hi, k);
 #pragma unroll
@@ -530,7 +528,7 @@ __device__ __forceinline__ int sample_of(const SegArgs& a, int pos) {
 // what dprc_embed_plan wrote (read on another stream before it was written, say)
 // gives wrong sums, but no access outside the tensors.
 __device__ __forceinline__ int plan_pos(const SegArgs& a, long long i) {
-  return static_cast<int>(min(static_cast<uint32_t>(__ldg(a.pos + i)), static_cast<uint32_t>(a.N - 1)));
+  return static_cast<int>(min(static_cast<uint32_t>(__ldcg(a.pos + i)), static_cast<uint32_t>(a.N - 1)));
 }
 
 // Rows of a range: lane l holds row l (l < rows).
@@ -561,7 +559,7 @@ __device__ __forceinline__ RangeRows range_rows(const SegArgs& a, int range, boo
   for (int w = 0; w < 3; ++w) {
     const int i = a0 - 32 + w * 32 + lane;
     const bool in = i >= 0 && i < a.N;
-    kw[w] = in ? min(__ldg(a.key + i), V) : V;
+    kw[w] = in ? min(__ldcg(a.key + i), V) : V;
     pw[w] = in ? plan_pos(a, i) : 0;
   }
   uint32_t klast = kw[0];
@@ -650,9 +648,8 @@ struct RangeShared {
 };
 
 template <typename T, int AW, bool kNorm>
-__device__ __forceinline__ void segment_range(const SegArgs& a, const T* __restrict__ G,
-                                              T* __restrict__ dW, int range, int blk,
-                                              RangeShared& s) {
+__device__ __forceinline__ void segment_range(const SegArgs& a, const T* G, T* dW, int range,
+                                              int blk, RangeShared& s) {
   using RawT = typename Raw<AW>::type;
   constexpr int VE = AW / static_cast<int>(sizeof(T));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -660,7 +657,7 @@ __device__ __forceinline__ void segment_range(const SegArgs& a, const T* __restr
     const RangeRows q = range_rows<kNorm>(a, range, blk == 0);
     s.pos[lane] = q.pos;
     s.key[lane] = q.key;
-    if (!kNorm && a.c != nullptr && lane < q.rows) s.w[lane] = __ldg(a.c + sample_of(a, q.pos));
+    if (!kNorm && a.c != nullptr && lane < q.rows) s.w[lane] = __ldcg(a.c + sample_of(a, q.pos));
     if (lane == 0) {
       s.E = q.E;
       s.L = q.L;
@@ -784,7 +781,7 @@ __device__ __forceinline__ long long lower_bound(const uint32_t* key, long long 
   long long lo = 0, hi = N;
   while (lo < hi) {
     const long long m = (lo + hi) >> 1;
-    if (__ldg(key + m) < v) lo = m + 1; else hi = m;
+    if (key[m] < v) lo = m + 1; else hi = m;
   }
   return lo;
 }
@@ -795,7 +792,7 @@ __device__ __forceinline__ long long lower_bound(const uint32_t* key, long long 
 // not 102.)
 constexpr int kZeroBytes = 4096;
 template <typename T, int AW>
-__device__ __forceinline__ void zero_rows(const SegArgs& a, T* __restrict__ dW, long long unit) {
+__device__ __forceinline__ void zero_rows(const SegArgs& a, T* dW, long long unit) {
   using RawT = typename Raw<AW>::type;
   constexpr int VE = AW / static_cast<int>(sizeof(T));
   const int lane = threadIdx.x & 31;
@@ -804,7 +801,7 @@ __device__ __forceinline__ void zero_rows(const SegArgs& a, T* __restrict__ dW, 
   bool absent = false;
   if (v < a.V) {
     const long long i = lower_bound(a.key, a.N, static_cast<uint32_t>(v));
-    absent = i >= a.N || __ldg(a.key + i) != static_cast<uint32_t>(v);
+    absent = i >= a.N || a.key[i] != static_cast<uint32_t>(v);
   }
   uint32_t todo = __ballot_sync(0xffffffffu, absent);
   const long long nvec = a.d / VE;
@@ -825,7 +822,7 @@ __device__ __forceinline__ void zero_rows(const SegArgs& a, T* __restrict__ dW, 
 
 template <typename T, int AW, bool kNorm>
 __global__ void __launch_bounds__(kSegThreads, 4)
-    embed_segment_kernel(const SegArgs a, const T* __restrict__ G, T* __restrict__ dW) {
+    embed_segment_kernel(const SegArgs a, const T* G, T* dW) {
   __shared__ RangeShared s_range;
   pdl_launch_dependents();
   pdl_wait();
@@ -873,8 +870,8 @@ __device__ __forceinline__ float4 add_pieces(const SegArgs& a, long long range, 
 
 // What becomes of a long run's sums over one block of columns (a warp's).
 template <typename T, bool kNorm>
-__device__ __forceinline__ void finish_run(const SegArgs& a, T* __restrict__ dW, long long range,
-                                           int first, long long col, float4 s) {
+__device__ __forceinline__ void finish_run(const SegArgs& a, T* dW, long long range, int first,
+                                           long long col, float4 s) {
   const float f[4] = {s.x, s.y, s.z, s.w};
   if (kNorm) {
     // columns past d hold whatever the workspace held
@@ -895,7 +892,7 @@ __device__ __forceinline__ void finish_run(const SegArgs& a, T* __restrict__ dW,
     }
   } else {
     // (the run reaches past `range`)
-    const uint32_t k = min(__ldg(a.key + (range + 1) * kRange - 1), static_cast<uint32_t>(a.V - 1));
+    const uint32_t k = min(__ldcg(a.key + (range + 1) * kRange - 1), static_cast<uint32_t>(a.V - 1));
     T* out = dW + static_cast<long long>(k) * a.d;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -913,7 +910,7 @@ __device__ __forceinline__ void finish_run(const SegArgs& a, T* __restrict__ dW,
 
 template <typename T, bool kNorm>
 __global__ void __launch_bounds__(32 * kLongWarps)
-    embed_long_kernel(const SegArgs a, T* __restrict__ dW) {
+    embed_long_kernel(const SegArgs a, T* dW) {
   __shared__ float4 s_sum[kLongWarps][32];
   pdl_launch_dependents();
   pdl_wait();
@@ -978,7 +975,7 @@ __global__ void __launch_bounds__(32 * kLongWarps)
 // cluster's barrier first and waits for it after its loads, which hide it.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
-    embed_norm_finish_kernel(const SegArgs a, float* __restrict__ n) {
+    embed_norm_finish_kernel(const SegArgs a, float* n) {
   __shared__ float s_warp[8];
   __shared__ float s_cta[8];
   cluster_arrive();

@@ -295,8 +295,7 @@ __global__ void __launch_bounds__(256) linear_dz_flat_kernel(const DzArgs a) {
 // db[n] = sum over the row blocks, 32 columns and 8 shares per CTA.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    linear_db_kernel(const float* __restrict__ colsum, int nblocks, int N, T* __restrict__ db,
-                     int beside) {
+    linear_db_kernel(const float* colsum, int nblocks, int N, T* db, int beside) {
   __shared__ float s_sum[8][32];
   beside_begin(beside != 0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -324,8 +323,8 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(256)
-    linear_finish_kernel(const float* __restrict__ part, long long ldpart, long long stride,
-                         int split, const LinearEpi e) {
+    linear_finish_kernel(const float* part, long long ldpart, long long stride, int split,
+                         const LinearEpi e) {
   pdl_launch_dependents();
   pdl_wait();
   const int groups = (e.N + 7) / 8;

@@ -52,3 +52,25 @@ def test_cluster_barrier_before_the_first_remote_access(file, name, body):
     """A CTA of a cluster may be addressed only once it is known to run."""
     joined = JOINED.search(body)
     assert joined and joined.start() < REMOTE.search(body).start(), f"{file}: {name}"
+
+
+# The files whose kernels may start while the kernel before them still writes
+# what they read (launch.cuh).
+AFTER = [p for p in sorted(glob.glob(os.path.join(CSRC, "*.cu*")))
+         if '#include "launch.cuh"' in open(p).read() or p.endswith(("launch.cuh", "linear.cuh"))]
+
+
+@pytest.mark.parametrize("path", AFTER, ids=os.path.basename)
+def test_early_kernels_read_by_coherent_loads(path):
+    """Loads of the read-only path are defined only for data that nobody writes
+    while the kernel lives."""
+    text = _text(path)
+    for what in (r"\b__ldg\s*\(", r"\bld\.global\.nc\b",
+                 r"\bconst\s+[\w:]+\s*\*\s*__restrict__"):
+        found = re.search(what, text)
+        assert found is None, text[max(0, found.start() - 60): found.end() + 60]
+
+
+def test_early_kernels_are_looked_at():
+    names = {os.path.basename(p) for p in AFTER}
+    assert {"embed.cu", "dropout.cu", "linear.cu", "linear_gemm.cu", "linear_few.cu"} <= names
