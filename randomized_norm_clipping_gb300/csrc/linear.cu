@@ -464,6 +464,10 @@ struct LinearGradPlan {
 
 LinearGradPlan linear_grad_plan(dprc_dtype dt, int64_t M, int64_t K, int64_t N) {
   LinearGradPlan l;
+  if (M == 0) {
+    l.total = 1024;  // no product runs; a call without a workspace stays an error
+    return l;
+  }
   l.planes = dt == DPRC_F32 ? 3 : 1;
   l.pack = dt == DPRC_F32 || K % 8 != 0;
   l.ldk = l.pack ? up8(K) : K;

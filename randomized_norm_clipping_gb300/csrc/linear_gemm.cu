@@ -980,6 +980,7 @@ cudaError_t read_device_error_linear(int32_t* out, bool reset) {
 GemmPlan plan_gemm(const GemmShape& g) {
   GemmPlan p;
   p.units = (g.K + kTk - 1) / kTk;
+  if (p.units == 0) return p;  // nothing to cut (prepare_gemm refuses it)
   const int sms = device_sm_count();
   // Candidates: the tile shapes and contraction shares; the cost of one is its
   // waves of units (in cycles of a 64-deep step, measured: the pair's step runs
