@@ -30,6 +30,12 @@ def _dense(t):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+def _in_backward():
+    """Whether this runs inside a backward pass (as activation checkpointing's
+    repeated forward passes do)."""
+    return torch._C._current_graph_task_id() != -1
+
+
 class _Lookup(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, weight, scale):

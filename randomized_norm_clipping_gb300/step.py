@@ -29,8 +29,11 @@ embeddings are exact and cheap (dprc_embed_norm: a group sum of the output
 gradients), other kinds (normalisation gains) would need their own per-sample
 gradients, which the method does not cover.  Each layer runs once per
 forward pass on inputs (B, ..., d) (every position between the batch and the
-feature axis counts as a token), and the per-sample losses must not couple
-samples.  An embedding's clipped gradient is formed from the recorded output
+feature axis counts as a token), or on rows of one sample after another; positions
+that the samples share (an embedding of arange(T)) are expanded to [B, T] first.
+A layer that runs twice and an input that mixes samples are refused, since a
+sample's norm would not be that of its gradient.  The per-sample losses must not
+couple samples.  An embedding's clipped gradient is formed from the recorded output
 gradients and the clip factors (dprc_embed_grad), so the second backward stops
 at the linear parameters.  Projections are drawn fresh per (layer, step) from a seeded
 generator (a reading of the pages, which do not say how often P is redrawn):
@@ -107,6 +110,9 @@ class RandomizedClippingStep:
         self._acts = {}
         self._outs = {}
         self._lasts = {}
+        self._runs = {}
+        self._mark = object()
+        self._apart = set()
         recorded = list(dict.fromkeys(self.layers + self.biased + self.embeddings))
         self._handles = [m.register_forward_hook(self._record) for m in recorded]
         self._ws = {}
@@ -119,11 +125,69 @@ class RandomizedClippingStep:
         self._handles = []
 
     def _record(self, module, inputs, output):
-        if torch.is_grad_enabled():
+        # (a pass inside a backward pass is activation checkpointing's repetition
+        # of one that is recorded)
+        if torch.is_grad_enabled() and not lay._in_backward():
             self._acts[module] = inputs[0]
             self._outs[module] = output
+            self._runs[module] = self._runs.get(module, 0) + 1
+            if output.grad_fn is not None:
+                output.grad_fn.metadata[self._mark] = module
             if isinstance(module, lay.Linear):
                 self._lasts[module] = module._last
+
+    def _refuse_repeats(self, losses):
+        """Raises if a layer stands in the losses' graph more than once."""
+        if all(n == 1 for n in self._runs.values()):
+            return
+        # (several passes may have been made and only the last one be stepped on)
+        todo, seen, met = [losses.grad_fn], set(), set()
+        while todo:
+            node = todo.pop()
+            if node is None or node in seen:
+                continue
+            seen.add(node)
+            m = node.metadata.get(self._mark)
+            if m is not None and m in met:
+                raise ValueError(f"{type(m).__name__} runs more than once in the losses' forward "
+                                 "pass; its gradient is a sum whose norm is not covered")
+            met.add(m)
+            todo.extend(n for n, _ in node.next_functions)
+
+    def _refuse_mixed(self, recorded, losses):
+        """Raises unless every layer's positions fall into B equal shares, one after
+        another, that belong to one sample each.  Inputs with the batch and a
+        position axis in front are taken at their word.  Others (rows; an
+        embedding's [B]) may be shared positions as well: once per layer and
+        share, the first and the last sample's losses must have no gradient
+        outside their own share."""
+        B = losses.shape[0]
+        doubtful = []
+        for m in recorded:
+            x = self._acts[m]
+            rows = x.shape[0] if x.dim() > 0 else 1
+            if B <= 1:
+                continue
+            if rows % B != 0:
+                raise ValueError(f"{type(m).__name__}: an input of shape {tuple(x.shape)} does not "
+                                 f"hold the positions of {B} samples; shared positions need an "
+                                 "entry for every sample")
+            if (m, rows // B) in self._apart or (
+                    rows == B and (x.dim() > 1 or m not in self.embeddings)):
+                continue
+            doubtful.append(m)
+        for i in (0, B - 1) if doubtful else ():
+            grads = torch.autograd.grad(losses[i], [self._outs[m] for m in doubtful],
+                                        retain_graph=True, allow_unused=True)
+            for m, g in zip(doubtful, grads):
+                if g is None:
+                    continue
+                n = g.shape[0] // B
+                # (a NaN is what 0 becomes beside an infinity)
+                if any(bool(((r != 0) & (r == r)).any()) for r in (g[:i * n], g[(i + 1) * n:])):
+                    raise ValueError(f"{type(m).__name__}: rows of an input of shape "
+                                     f"{tuple(self._acts[m].shape)} belong to more than one sample")
+        self._apart.update((m, self._acts[m].shape[0] // B) for m in doubtful)
 
     def parameters(self):
         """The trainable parameters in the order the noise stream runs over
@@ -192,11 +256,13 @@ class RandomizedClippingStep:
             raise RuntimeError("no forward pass recorded for some linear layers")
         if any(m not in self._outs for m in recorded):
             raise RuntimeError("no forward pass recorded for some layers")
+        self._refuse_repeats(losses)
         # step 2: gradients with respect to the layer outputs only
         fused = [m for m in recorded if isinstance(m, lay.Linear)]
         for m in fused:
             m.norm_pass = True
         try:
+            self._refuse_mixed(recorded, losses)
             grads = torch.autograd.grad(losses.sum(), [self._outs[m] for m in recorded],
                                         retain_graph=True)
         finally:
@@ -284,6 +350,7 @@ class RandomizedClippingStep:
         self._acts.clear()
         self._outs.clear()
         self._lasts.clear()
+        self._runs.clear()
         for m in self.layers + self.biased:
             if isinstance(m, lay.Linear):
                 m._last = None
