@@ -5,7 +5,7 @@
 directions, and `RandomizedClippingStep` takes their parameters: the embedding
 and the biases by their exact per-sample norms, the linear weights by the
 estimates.  Device tensors of float32 or bfloat16 only; the library raises on
-anything else.
+anything else.  Gradients can be taken once; a gradient of a gradient raises.
 
 Dropout masks come from the library's Philox stream under (seed, step): `seed`
 is the module's, `step` counts its training forward passes (set `step` to
@@ -18,6 +18,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as rnc
 
@@ -45,6 +46,7 @@ class _Lookup(torch.autograd.Function):
         return rnc.dprc_embed_lookup(_dense(weight), tokens, scale=scale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         (tokens,) = ctx.saved_tensors
         V, d = ctx.shape
@@ -77,6 +79,7 @@ class _Dropout(torch.autograd.Function):
         return rnc.dprc_dropout(_dense(x), p, seed, step, residual=_dense(residual))
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         dx = rnc.dprc_dropout(_dense(grad), *ctx.args) if ctx.needs_input_grad[0] else None
         return dx, grad if ctx.needs_input_grad[1] else None, None, None, None
@@ -110,6 +113,7 @@ class _Linear(torch.autograd.Function):
                                seed=module.seed, step=step, residual=_dense(residual), Z=z)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         x, w, z = ctx.saved_tensors
         m = ctx.module

@@ -1,0 +1,38 @@
+"""The torch modules without a GPU: the library's calls come from the oracle."""
+
+import pytest
+import torch
+
+import host_library
+from randomized_norm_clipping_gb300 import layers as lay
+
+
+@pytest.fixture(autouse=True)
+def _host(monkeypatch):
+    host_library.install(monkeypatch)
+    torch.manual_seed(3)
+
+
+# ---- second derivatives ----------------------------------------------------
+@pytest.mark.parametrize("which", ["embedding", "dropout", "linear"])
+def test_second_derivatives_are_an_error(which):
+    """The backward passes run outside the graph; a gradient of a gradient would
+    take them for constants."""
+    x = torch.randn(4, 6, requires_grad=True)
+    if which == "embedding":
+        m = lay.Embedding(5, 6)
+        y, wrt = m(torch.tensor([[0, 1, 4, 4]])).tanh(), m.weight
+    elif which == "dropout":
+        y, wrt = lay.Dropout(0.4, seed=2)(x).tanh(), x
+    else:
+        y, wrt = lay.Linear(6, 3, act="gelu")(x).tanh(), x
+    (g,) = torch.autograd.grad(y.sum(), wrt, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        (g ** 2).sum().backward()
+
+
+def test_first_derivatives_may_be_taken_twice():
+    m, x = lay.Linear(6, 3, bias=True, act="silu", p=0.3, seed=4), torch.randn(5, 6)
+    y = m(x)
+    g = [torch.autograd.grad(y.sum(), m.weight, retain_graph=True)[0] for _ in range(2)]
+    assert torch.equal(g[0], g[1])
