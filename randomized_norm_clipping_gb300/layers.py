@@ -107,26 +107,25 @@ class _Linear(torch.autograd.Function):
         if keep and module.act != "none":
             z = torch.empty((*x.shape[:-1], w.shape[0]), dtype=x.dtype, device=x.device)
         ctx.save_for_backward(x, w, z)
-        ctx.module, ctx.p, ctx.step = module, p, step
-        module._last = (z, p, step)
-        return rnc.dprc_linear(x, w, bias=_dense(bias), act=module.act, p=p,
-                               seed=module.seed, step=step, residual=_dense(residual), Z=z)
+        # the module may change before the backward pass: what it was is kept
+        ctx.module = module
+        ctx.args = dict(act=module.act, p=p, seed=module.seed, step=step)
+        module._last = (z, ctx.args)
+        return rnc.dprc_linear(x, w, bias=_dense(bias), residual=_dense(residual), Z=z, **ctx.args)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
         x, w, z = ctx.saved_tensors
-        m = ctx.module
         grad = _dense(grad)
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
-        if m.norm_pass:  # the clipping step's first backward: no weight gradients
+        if ctx.module.norm_pass:  # the clipping step's first backward: no weight gradients
             need_w = need_b = False
         dx = torch.empty_like(x) if need_x else None
         dw = torch.empty_like(w) if need_w else None
         db = torch.empty(w.shape[0], dtype=w.dtype, device=w.device) if need_b else None
         if need_x or need_w or need_b:
-            rnc.dprc_linear_grad(grad, x, w, Z=z, act=m.act, p=ctx.p, seed=m.seed, step=ctx.step,
-                                 dX=dx, dW=dw, db=db)
+            rnc.dprc_linear_grad(grad, x, w, Z=z, dX=dx, dW=dw, db=db, **ctx.args)
         return dx, dw, db, grad if need_r else None, None, None, None, None
 
 
@@ -159,10 +158,9 @@ class Linear(torch.nn.Module):
         """The gradient with respect to x W^T + bias, from that with respect to
         the output: what the norm estimates take as G.  `last` is what the
         forward pass left in `_last`."""
-        z, p, step = last
-        if self.act == "none" and p == 0.0:
+        z, args = last
+        if args["act"] == "none" and args["p"] == 0.0:
             return dy
         g = torch.empty_like(dy)
-        rnc.dprc_linear_grad(dy, None, _dense(self.weight), Z=z, act=self.act, p=p,
-                             seed=self.seed, step=step, dZ=g)
+        rnc.dprc_linear_grad(dy, None, _dense(self.weight), Z=z, dZ=g, **args)
         return g

@@ -36,3 +36,20 @@ def test_first_derivatives_may_be_taken_twice():
     y = m(x)
     g = [torch.autograd.grad(y.sum(), m.weight, retain_graph=True)[0] for _ in range(2)]
     assert torch.equal(g[0], g[1])
+
+
+# ---- what a backward pass goes by ------------------------------------------
+@pytest.mark.parametrize("change", ["seed", "act", "p", "step"])
+def test_backward_goes_by_the_call_and_not_by_the_module(change):
+    m = lay.Linear(6, 3, bias=True, act="silu", p=0.4, seed=4)
+    x = torch.randn(50, 6, requires_grad=True)
+    wrt = [x, m.weight, m.bias]
+    want = torch.autograd.grad(m(x).sum(), wrt)
+    m.step = 0
+    y = m(x)
+    last, dy = m._last, torch.ones(50, 3)
+    dz = m.preactivation_grad(dy, last)
+    setattr(m, change, {"seed": 9, "act": "relu", "p": 0.1, "step": 5}[change])
+    got = torch.autograd.grad(y.sum(), wrt)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.equal(m.preactivation_grad(dy, last), dz)
