@@ -10,7 +10,10 @@ anything else.  Gradients can be taken once; a gradient of a gradient raises.
 Dropout masks come from the library's Philox stream under (seed, step): `seed`
 is the module's, `step` counts its training forward passes (set `step` to
 repeat or resume a run).  A mask is not stored: the backward passes of one
-forward pass, a clipping step has two, draw it again.
+forward pass, a clipping step has two, draw it again, and so does a forward pass
+that activation checkpointing repeats (preserve_rng_state, its default, is needed:
+a training forward pass with dropout draws once from torch's CPU generator, by
+which its repetition is known).
 """
 
 from __future__ import annotations
@@ -85,18 +88,48 @@ class _Dropout(torch.autograd.Function):
         return dx, grad if ctx.needs_input_grad[1] else None, None, None, None
 
 
-class Dropout(torch.nn.Module):
+_PASSES_KEPT = 1024
+
+
+class _Masked(torch.nn.Module):
+    """A module with a dropout mask of its own in every training forward pass."""
+
+    def __init__(self, p, seed):
+        super().__init__()
+        self.p, self.seed, self.step = float(p), int(seed), 0
+        self._passes = {}
+
+    def _next_step(self):
+        """The step of a training forward pass.  Activation checkpointing runs a pass
+        again inside the backward pass, after it has put torch's generators back
+        where they were: each pass draws a ticket from the CPU's, and a pass that
+        is run again finds its step by that."""
+        ticket = int(torch.randint(1 << 62, (), device="cpu"))
+        if _in_backward():
+            if ticket not in self._passes:
+                raise RuntimeError(
+                    "a training forward pass inside a backward pass repeats none of the last "
+                    f"{_PASSES_KEPT}, so that its dropout mask is unknown; activation checkpointing "
+                    "needs preserve_rng_state=True")
+            return self._passes[ticket]
+        self.step += 1
+        self._passes.pop(ticket, None)
+        self._passes[ticket] = self.step
+        if len(self._passes) > _PASSES_KEPT:
+            del self._passes[next(iter(self._passes))]
+        return self.step
+
+
+class Dropout(_Masked):
     """residual + dropout(x); the identity (plus the residual) outside training."""
 
     def __init__(self, p=0.1, seed=0):
-        super().__init__()
-        self.p, self.seed, self.step = float(p), int(seed), 0
+        super().__init__(p, seed)
 
     def forward(self, x, residual=None):
         if not self.training or self.p == 0.0:
             return x if residual is None else x + residual
-        self.step += 1
-        return _Dropout.apply(x, residual, self.p, self.seed, self.step)
+        return _Dropout.apply(x, residual, self.p, self.seed, self._next_step())
 
 
 class _Linear(torch.autograd.Function):
@@ -129,16 +162,16 @@ class _Linear(torch.autograd.Function):
         return dx, dw, db, grad if need_r else None, None, None, None, None
 
 
-class Linear(torch.nn.Module):
+class Linear(_Masked):
     """residual + dropout(act(x W^T + bias)), in one call."""
 
     def __init__(self, in_features, out_features, bias=False, act="none", p=0.0, seed=0,
                  device=None, dtype=None):
-        super().__init__()
+        super().__init__(p, seed)
         if act not in rnc.DPRC_ACTS:
             raise ValueError(f"act must be one of {sorted(rnc.DPRC_ACTS)}")
         self.in_features, self.out_features = int(in_features), int(out_features)
-        self.act, self.p, self.seed, self.step = act, float(p), int(seed), 0
+        self.act = act
         self.norm_pass = False
         self._last = None
         self.weight = torch.nn.Parameter(
@@ -149,9 +182,8 @@ class Linear(torch.nn.Module):
 
     def forward(self, x, residual=None):
         p = self.p if self.training else 0.0
-        if p > 0.0:
-            self.step += 1
-        return _Linear.apply(x, self.weight, self.bias, residual, self, p, self.step,
+        step = self._next_step() if p > 0.0 else self.step
+        return _Linear.apply(x, self.weight, self.bias, residual, self, p, step,
                              torch.is_grad_enabled())
 
     def preactivation_grad(self, dy, last):

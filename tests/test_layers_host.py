@@ -1,5 +1,7 @@
 """The torch modules without a GPU: the library's calls come from the oracle."""
 
+import os
+
 import pytest
 import torch
 
@@ -53,3 +55,77 @@ def test_backward_goes_by_the_call_and_not_by_the_module(change):
     got = torch.autograd.grad(y.sum(), wrt)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert torch.equal(m.preactivation_grad(dy, last), dz)
+
+
+# ---- activation checkpointing ----------------------------------------------
+def checkpoint(*args, **kw):
+    # (it imports triton, which tests/test_oracle.py runs in its interpreter)
+    os.environ["TRITON_INTERPRET"] = "1"
+    from torch.utils import checkpoint as c
+    return c.checkpoint(*args, **kw)
+
+
+class _Blocks(torch.nn.Module):
+    """Maps with dropout, one dropout shared by all, checkpointed or not."""
+
+    def __init__(self, n=3):
+        super().__init__()
+        self.maps = torch.nn.ModuleList(lay.Linear(6, 6, act="silu", p=0.3, seed=10 + i)
+                                        for i in range(n))
+        self.drop = lay.Dropout(0.4, seed=77)
+
+    def block(self, i, x):
+        return self.drop(self.maps[i](x, residual=x)) + torch.rand(())  # (draws of its own too)
+
+    def forward(self, x, how):
+        for i in range(len(self.maps)):
+            if how == "plain":
+                x = self.block(i, x)
+            elif how == "nested":
+                x = checkpoint(lambda v, i=i: checkpoint(self.block, i, v, use_reentrant=False),
+                               x, use_reentrant=False)
+            else:
+                x = checkpoint(self.block, i, x, use_reentrant=how == "reentrant")
+        return x
+
+
+def _run(model, how, batches):
+    """Outputs and gradients of several passes in flight at once."""
+    torch.manual_seed(8)
+    for m in [*model.maps, model.drop]:
+        m.step = 0
+    model.zero_grad()
+    xs = [x.clone().requires_grad_() for x in batches]
+    ys = [model(x, how) for x in xs]
+    for y in reversed(ys):
+        (y ** 2).sum().backward()
+    return ([y.detach() for y in ys], [x.grad for x in xs]
+            + [p.grad.clone() for p in model.parameters()], [m.step for m in model.maps],
+            model.drop.step)
+
+
+@pytest.mark.parametrize("how", ["reentrant", "non-reentrant", "nested"])
+def test_a_repeated_forward_pass_draws_the_same_mask(how):
+    model = _Blocks()
+    batches = [torch.randn(20, 6) for _ in range(3)]
+    y0, g0, s0, d0 = _run(model, "plain", batches)
+    y1, g1, s1, d1 = _run(model, how, batches)
+    assert all(torch.equal(a, b) for a, b in zip(y0, y1))
+    for a, b in zip(g0, g1):
+        assert torch.allclose(a, b, rtol=1e-6, atol=1e-6)
+    assert s1 == s0 == [3, 3, 3] and d1 == d0 == 9  # repetitions do not count
+
+
+def test_a_repetition_that_cannot_be_told_is_an_error():
+    m, x = lay.Linear(6, 3, p=0.4, seed=1), torch.randn(50, 6, requires_grad=True)
+    y = checkpoint(m, x, use_reentrant=False, preserve_rng_state=False)
+    torch.rand(3)
+    with pytest.raises(RuntimeError, match="preserve_rng_state"):
+        y.tanh().sum().backward()
+
+
+def test_step_repeats_a_run():
+    m, x = lay.Dropout(0.4, seed=1), torch.ones(200)
+    a = [m(x) for _ in range(3)]
+    m.step = 0
+    assert all(torch.equal(m(x), v) for v in a) and not torch.equal(a[0], a[1])

@@ -188,3 +188,40 @@ def test_an_earlier_forward_pass_does_not_count(kind):
         return _losses(model, tok)
 
     _check(model, losses, lambda i: _losses(model, tok[i:i + 1]).sum())
+
+
+def test_checkpointed_blocks_step_as_others():
+    """A block that is repeated in each of the step's backward passes, with dropout."""
+    import os
+    os.environ["TRITON_INTERPRET"] = "1"  # (checkpoint imports triton: tests/test_oracle.py)
+    from torch.utils.checkpoint import checkpoint
+
+    class Model(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.embed = lay.Embedding(10, D)
+            self.up = lay.Linear(D, D, bias=True, act="gelu", p=0.3, seed=5)
+            self.drop = lay.Dropout(0.2, seed=6)
+            self.head = torch.nn.Linear(D, D, bias=False)
+            self.repeat = False
+
+        def block(self, x):
+            return self.drop(self.up(x), residual=x)
+
+        def forward(self, tok):
+            x = self.embed(tok)
+            x = checkpoint(self.block, x, use_reentrant=False) if self.repeat else self.block(x)
+            return self.head(x)
+
+    model, tok = Model(), torch.randint(0, 10, (B, T))
+    step = RandomizedClippingStep(model, C=0.05, sigma=0.0, k=D)
+    eye = [torch.eye(m.out_features) for m in step.layers]
+    got = []
+    for repeat in (False, True):
+        model.repeat, model.up.step, model.drop.step = repeat, 0, 0
+        out = step(_losses(model, tok), step=0, projections=eye)
+        got.append([out["n"], out["c"]] + [p.grad.clone() for p in step.parameters()])
+        assert model.up.step == model.drop.step == 1
+    step.close()
+    for a, b in zip(*got):
+        assert torch.allclose(a, b, rtol=1e-5, atol=1e-7)
