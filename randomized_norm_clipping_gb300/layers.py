@@ -8,7 +8,7 @@ estimates.  Device tensors of float32 or bfloat16 only; the library raises on
 anything else.  Gradients can be taken once; a gradient of a gradient raises.
 
 Dropout masks come from the library's Philox stream under (seed, step): `seed`
-is the module's, `step` counts its training forward passes (set `step` to
+is the module's (one of its own where none is given), `step` counts its training forward passes (set `step` to
 repeat or resume a run).  A mask is not stored: the backward passes of one
 forward pass, a clipping step has two, draw it again, and so does a forward pass
 that activation checkpointing repeats (preserve_rng_state, its default, is needed:
@@ -18,6 +18,7 @@ which its repetition is known).
 
 from __future__ import annotations
 
+import itertools
 import math
 
 import torch
@@ -89,6 +90,17 @@ class _Dropout(torch.autograd.Function):
 
 
 _PASSES_KEPT = 1024
+_modules_built = itertools.count(1)
+
+
+def _own_seed():
+    """A seed that no other module of the process got, from torch's initial seed and
+    the number of modules built (Steele, Lea and Flood's splitmix64 of the two)."""
+    m = (1 << 64) - 1
+    h = (torch.initial_seed() + next(_modules_built) * 0x9E3779B97F4A7C15) & m
+    h = ((h ^ (h >> 30)) * 0xBF58476D1CE4E5B9) & m
+    h = ((h ^ (h >> 27)) * 0x94D049BB133111EB) & m
+    return (h ^ (h >> 31)) >> 1
 
 
 class _Masked(torch.nn.Module):
@@ -96,7 +108,8 @@ class _Masked(torch.nn.Module):
 
     def __init__(self, p, seed):
         super().__init__()
-        self.p, self.seed, self.step = float(p), int(seed), 0
+        self.p, self.step = float(p), 0
+        self.seed = _own_seed() if seed is None else int(seed)
         self._passes = {}
 
     def _next_step(self):
@@ -123,7 +136,7 @@ class _Masked(torch.nn.Module):
 class Dropout(_Masked):
     """residual + dropout(x); the identity (plus the residual) outside training."""
 
-    def __init__(self, p=0.1, seed=0):
+    def __init__(self, p=0.1, seed=None):
         super().__init__(p, seed)
 
     def forward(self, x, residual=None):
@@ -165,7 +178,7 @@ class _Linear(torch.autograd.Function):
 class Linear(_Masked):
     """residual + dropout(act(x W^T + bias)), in one call."""
 
-    def __init__(self, in_features, out_features, bias=False, act="none", p=0.0, seed=0,
+    def __init__(self, in_features, out_features, bias=False, act="none", p=0.0, seed=None,
                  device=None, dtype=None):
         super().__init__(p, seed)
         if act not in rnc.DPRC_ACTS:

@@ -129,3 +129,22 @@ def test_step_repeats_a_run():
     a = [m(x) for _ in range(3)]
     m.step = 0
     assert all(torch.equal(m(x), v) for v in a) and not torch.equal(a[0], a[1])
+
+
+# ---- seeds -----------------------------------------------------------------
+def test_modules_built_with_the_defaults_draw_masks_of_their_own():
+    x = torch.ones(4000)
+    ms = [lay.Dropout(0.5) for _ in range(4)]
+    kept = torch.stack([m(x) != 0 for m in ms]).double()
+    # independent masks agree in half of the elements (five standard errors)
+    for i in range(4):
+        for j in range(i):
+            same = float((kept[i] == kept[j]).double().mean())
+            assert abs(same - 0.5) < 5 * 0.5 / 4000 ** 0.5
+    seeds = {lay.Linear(3, 3, p=0.1).seed for _ in range(50)} | {m.seed for m in ms}
+    assert len(seeds) == 54 and all(0 <= s < 1 << 63 for s in seeds)
+
+
+def test_a_given_seed_is_kept():
+    assert [lay.Dropout(0.5, seed=s).seed for s in (0, 7)] == [0, 7]
+    assert lay.Linear(3, 3, p=0.1, seed=5).seed == 5
