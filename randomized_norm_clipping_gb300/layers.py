@@ -8,8 +8,8 @@ estimates.  Device tensors of float32 or bfloat16 only; the library raises on
 anything else.  Gradients can be taken once; a gradient of a gradient raises.
 
 Dropout masks come from the library's Philox stream under (seed, step): `seed`
-is the module's (one of its own where none is given), `step` counts its training forward passes (set `step` to
-repeat or resume a run).  A mask is not stored: the backward passes of one
+is the module's (one of its own, in copies too, where none is given), `step` counts
+its training forward passes (set `step` to repeat or resume a run).  A mask is not stored: the backward passes of one
 forward pass, a clipping step has two, draw it again, and so does a forward pass
 that activation checkpointing repeats (preserve_rng_state, its default, is needed:
 a training forward pass with dropout draws once from torch's CPU generator, by
@@ -18,6 +18,7 @@ which its repetition is known).
 
 from __future__ import annotations
 
+import copy
 import itertools
 import math
 
@@ -110,7 +111,17 @@ class _Masked(torch.nn.Module):
         super().__init__()
         self.p, self.step = float(p), 0
         self.seed = _own_seed() if seed is None else int(seed)
+        self._seed_given = seed is not None
         self._passes = {}
+
+    def __deepcopy__(self, memo):
+        """A copy, which gets a seed of its own where this module has one."""
+        new = self.__class__.__new__(self.__class__)
+        memo[id(self)] = new
+        new.__dict__.update(copy.deepcopy(self.__dict__, memo))
+        if not self._seed_given:
+            new.seed = _own_seed()
+        return new
 
     def _next_step(self):
         """The step of a training forward pass.  Activation checkpointing runs a pass

@@ -1,5 +1,6 @@
 """The torch modules without a GPU: the library's calls come from the oracle."""
 
+import copy
 import os
 
 import pytest
@@ -148,3 +149,15 @@ def test_modules_built_with_the_defaults_draw_masks_of_their_own():
 def test_a_given_seed_is_kept():
     assert [lay.Dropout(0.5, seed=s).seed for s in (0, 7)] == [0, 7]
     assert lay.Linear(3, 3, p=0.1, seed=5).seed == 5
+
+
+def test_copies_of_a_module_draw_masks_of_their_own():
+    block = torch.nn.Sequential(lay.Linear(3, 3, p=0.2), lay.Dropout(0.5))
+    copies = [copy.deepcopy(block) for _ in range(3)]
+    assert len({m.seed for b in [block, *copies] for m in b}) == 8
+    assert torch.equal(copies[0][0].weight, block[0].weight)
+    assert copies[0][0].weight is not block[0].weight
+    given = lay.Dropout(0.5, seed=4)
+    assert copy.deepcopy(given).seed == 4
+    twice = copy.deepcopy(torch.nn.ModuleList([given, given]))  # one module stays one module
+    assert twice[0] is twice[1]
