@@ -9,7 +9,8 @@ anything else.  Gradients can be taken once; a gradient of a gradient raises.
 
 Dropout masks come from the library's Philox stream under (seed, step): `seed`
 is the module's (one of its own, in copies too, where none is given), `step` counts
-its training forward passes (set `step` to repeat or resume a run).  A mask is not stored: the backward passes of one
+its training forward passes (set `step` to repeat a run; a module with dropout has
+both in its state_dict, so that a restored run goes on).  A mask is not stored: the backward passes of one
 forward pass, a clipping step has two, draw it again, and so does a forward pass
 that activation checkpointing repeats (preserve_rng_state, its default, is needed:
 a training forward pass with dropout draws once from torch's CPU generator, by
@@ -91,6 +92,7 @@ class _Dropout(torch.autograd.Function):
 
 
 _PASSES_KEPT = 1024
+_MASK_KEY = "mask_seed_step"
 _modules_built = itertools.count(1)
 
 
@@ -122,6 +124,23 @@ class _Masked(torch.nn.Module):
         if not self._seed_given:
             new.seed = _own_seed()
         return new
+
+    def _save_to_state_dict(self, destination, prefix, keep_vars):
+        super()._save_to_state_dict(destination, prefix, keep_vars)
+        if self.p > 0.0:  # (else the keys of the plain module)
+            signed = (self.seed + (1 << 63)) % (1 << 64) - (1 << 63)
+            destination[prefix + _MASK_KEY] = torch.tensor([signed, self.step])
+
+    def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys,
+                              unexpected_keys, error_msgs):
+        super()._load_from_state_dict(state_dict, prefix, local_metadata, strict, missing_keys,
+                                      unexpected_keys, error_msgs)
+        key = prefix + _MASK_KEY
+        if key in state_dict:
+            seed, self.step = (int(v) for v in state_dict[key])
+            self.seed = seed % (1 << 64)
+            if key in unexpected_keys:
+                unexpected_keys.remove(key)
 
     def _next_step(self):
         """The step of a training forward pass.  Activation checkpointing runs a pass

@@ -161,3 +161,37 @@ def test_copies_of_a_module_draw_masks_of_their_own():
     assert copy.deepcopy(given).seed == 4
     twice = copy.deepcopy(torch.nn.ModuleList([given, given]))  # one module stays one module
     assert twice[0] is twice[1]
+
+
+# ---- state -----------------------------------------------------------------
+def _net():
+    return torch.nn.Sequential(lay.Linear(5, 5, p=0.3), lay.Dropout(0.4),
+                               torch.nn.Sequential(lay.Linear(5, 5, p=0.2, seed=(1 << 64) - 3)))
+
+
+def test_a_restored_run_goes_on_with_its_masks():
+    x, a = torch.randn(30, 5), _net()
+    for _ in range(3):
+        a(x)
+    b = _net()
+    assert b[0].seed != a[0].seed
+    b.load_state_dict(a.state_dict())
+    assert [m.step for m in (b[0], b[1], b[2][0])] == [3, 3, 3]
+    assert b[2][0].seed == (1 << 64) - 3
+    assert torch.equal(a(x), b(x)) and torch.equal(a(x), b(x))
+
+
+def test_states_without_masks_load_as_before():
+    a = _net()
+    for _ in range(2):
+        a(torch.randn(3, 5))
+    seed = a[0].seed
+    plain = {k: v for k, v in a.state_dict().items() if k.endswith("weight")}
+    a.load_state_dict(plain)  # as saved by modules that kept no masks
+    assert a[0].seed == seed and a[0].step == 2
+    # a map without dropout has the keys of torch.nn.Linear
+    m = lay.Linear(5, 4, bias=True)
+    torch.nn.Linear(5, 4).load_state_dict(m.state_dict())
+    assert set(m.state_dict()) == {"weight", "bias"}
+    with pytest.raises(RuntimeError, match="nexpected"):
+        m.load_state_dict({**m.state_dict(), "mask": torch.zeros(2)})
