@@ -129,7 +129,7 @@ class _Masked(torch.nn.Module):
         super()._save_to_state_dict(destination, prefix, keep_vars)
         if self.p > 0.0:  # (else the keys of the plain module)
             signed = (self.seed + (1 << 63)) % (1 << 64) - (1 << 63)
-            destination[prefix + _MASK_KEY] = torch.tensor([signed, self.step])
+            destination[prefix + _MASK_KEY] = torch.tensor([signed, self.step], device="cpu")
 
     def _load_from_state_dict(self, state_dict, prefix, local_metadata, strict, missing_keys,
                               unexpected_keys, error_msgs):
@@ -186,13 +186,17 @@ class _Linear(torch.autograd.Function):
         # the module may change before the backward pass: what it was is kept
         ctx.module = module
         ctx.args = dict(act=module.act, p=p, seed=module.seed, step=step)
-        module._last = (z, ctx.args)
+        if not _in_backward():  # (a repeated pass has its place already)
+            module._last = (z, ctx.args)
         return rnc.dprc_linear(x, w, bias=_dense(bias), residual=_dense(residual), Z=z, **ctx.args)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
         x, w, z = ctx.saved_tensors
+        last = ctx.module._last
+        if last is not None and last[1] is ctx.args:  # Z is kept by the graph alone from here on
+            ctx.module._last = None
         grad = _dense(grad)
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
         if ctx.module.norm_pass:  # the clipping step's first backward: no weight gradients

@@ -1,7 +1,9 @@
 """The torch modules without a GPU: the library's calls come from the oracle."""
 
 import copy
+import gc
 import os
+import weakref
 
 import pytest
 import torch
@@ -195,3 +197,24 @@ def test_states_without_masks_load_as_before():
     assert set(m.state_dict()) == {"weight", "bias"}
     with pytest.raises(RuntimeError, match="nexpected"):
         m.load_state_dict({**m.state_dict(), "mask": torch.zeros(2)})
+
+
+# ---- memory ----------------------------------------------------------------
+def test_nothing_of_a_pass_is_kept_after_its_backward_pass():
+    m = lay.Linear(6, 3, act="silu")
+    y = m(torch.randn(4, 6))
+    kept = weakref.ref(m._last[0].untyped_storage())
+    assert kept() is not None
+    y.sum().backward()
+    del y
+    gc.collect()
+    assert m._last is None and kept() is None
+    # a later forward pass's is not the earlier one's to clear
+    a, b = m(torch.randn(4, 6)), m(torch.randn(4, 6))
+    a.sum().backward()
+    assert m._last is not None
+    b.sum().backward()
+    assert m._last is None
+    y = checkpoint(m, torch.randn(4, 6, requires_grad=True), use_reentrant=False)
+    y.sum().backward()
+    assert m._last is None
