@@ -49,6 +49,7 @@ from . import binding as rnc
 from . import layers as lay
 
 _MIX = 0x9E3779B97F4A7C15
+_BIAS_PLANS_KEPT = 16
 
 
 def _seed(*parts):
@@ -196,12 +197,29 @@ class RandomizedClippingStep:
                 + [m.weight for m in self.embeddings])
 
     def _bias_plan(self, B, T, device):
-        """The plan of the one-row embedding that a bias is: every position 0."""
+        """The plan of the one-row embedding that a bias is: every position 0.  Kept
+        for the last sizes; the current stream waits for the one that made it."""
+        def make():
+            return rnc.dprc_embed_plan(torch.zeros((B, T), dtype=torch.int32, device=device), 1)
+
+        on_gpu = device.type == "cuda"
+        if on_gpu and torch.cuda.is_current_stream_capturing():
+            return make()  # a graph cannot wait for what was recorded outside of it
         key = (B, T, device)
         if key not in self._bias_plans:
-            self._bias_plans = {key: rnc.dprc_embed_plan(
-                torch.zeros((B, T), dtype=torch.int32, device=device), 1)}
-        return self._bias_plans[key]
+            plan, made = make(), None
+            if on_gpu:
+                made = torch.cuda.Event()
+                made.record(torch.cuda.current_stream(device))
+            if len(self._bias_plans) == _BIAS_PLANS_KEPT:
+                del self._bias_plans[next(iter(self._bias_plans))]
+            self._bias_plans[key] = plan, made
+        plan, made = self._bias_plans[key]
+        if on_gpu:
+            stream = torch.cuda.current_stream(device)
+            stream.wait_event(made)
+            plan.buf.record_stream(stream)
+        return plan
 
     def projections(self, step):
         """The projection(s) of every layer for `step`: P [p][k] (Hutchinson)

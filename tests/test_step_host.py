@@ -225,3 +225,27 @@ def test_checkpointed_blocks_step_as_others():
     step.close()
     for a, b in zip(*got):
         assert torch.allclose(a, b, rtol=1e-5, atol=1e-7)
+
+
+def test_bias_plans_are_made_once_a_size(monkeypatch):
+    class TwoLengths(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.a, self.b = lay.Linear(D, D, bias=True), lay.Linear(D, D, bias=True)
+
+        def forward(self, x):
+            return self.b(self.a(x)[:, ::2])
+
+    made = []
+    plan = host_library.embed_plan
+    monkeypatch.setattr(host_library.binding, "dprc_embed_plan",
+                        lambda tok, V, **kw: (made.append(tuple(tok.shape)), plan(tok, V))[1])
+    model = TwoLengths()
+    step = RandomizedClippingStep(model, C=1.0, sigma=0.0, k=D)
+    for b in (B, B, B + 1, B):
+        step(_losses(model, torch.randn(b, T, D)), step=0)
+    assert sorted(made) == [(B, T // 2), (B, T), (B + 1, T // 2), (B + 1, T)]
+    for b in range(1, 60):
+        step(_losses(model, torch.randn(b, T, D)), step=0)
+    assert len(step._bias_plans) <= 16  # sizes come and go
+    step.close()
