@@ -517,23 +517,43 @@ def _empty(like, shape, stream, given, dtype=None):
         return torch.empty(*shape, dtype=dtype, device=like.device)
 
 
+def _current_stream_id(device):
+    """torch's number of the current stream: the handle itself for a stream that
+    torch does not own."""
+    return torch._C._cuda_getCurrentStream(device)[0]
+
+
+def _keeps_scratch(like, stream, given):
+    """Whether a workspace may be kept for the stream: one of torch's own, which
+    are never destroyed (the handle of another may come to name a new stream while
+    the old one's work is pending), and not being captured, since a graph owns
+    what it allocates."""
+    if _capturing is None:
+        return False
+    if given is None:
+        return not _capturing() and (stream == 0 or _current_stream_id(like.get_device()) != stream)
+    if not isinstance(given, torch.cuda.Stream) or isinstance(given, torch.cuda.ExternalStream):
+        return False
+    with torch.cuda.stream(given):
+        return not _capturing()
+
+
 def _scratch(nbytes, like, stream, given):
     """A device workspace of nbytes for one call without a ws argument: kept
     per host thread, device and stream (calls of one thread on one stream run
     one after the other) and grown as needed, so that a call does not pay for
-    an allocation.  Large ones, and any during a graph capture (which owns what
-    it allocates), are allocated fresh."""
-    if nbytes > _SCRATCH_KEEP or _capturing is None or _capturing():
+    an allocation.  Large ones are allocated fresh."""
+    if nbytes > _SCRATCH_KEEP or not _keeps_scratch(like, stream, given):
         return _empty(like, (nbytes,), stream, given, torch.uint8)
     kept = _scratch_kept.__dict__
     key = (like.get_device(), stream)
     have = kept.get(key)
-    if have is None or have[-1].numel() < nbytes:
+    if have is None or have.numel() < nbytes:
         size = 1 << max(16, (nbytes - 1).bit_length())
-        # outgrown buffers stay: work on the stream may still use them
-        have = (have or ()) + (_empty(like, (size,), stream, given, torch.uint8),)
-        kept[key] = have
-    return have[-1]
+        # (the outgrown one was allocated on this stream, and its memory goes to later
+        # work there, behind what may still use it)
+        have = kept[key] = _empty(like, (size,), stream, given, torch.uint8)
+    return have
 
 
 def _same(name, t, dtype, shape, device):
