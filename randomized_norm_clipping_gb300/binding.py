@@ -568,6 +568,12 @@ def _same(name, t, dtype, shape, device):
     raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} is needed")
 
 
+def _beside(name, t, like):
+    """A tensor on the call's device, of whatever type."""
+    if t is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {like.device}")
+
+
 def _token_bytes(tokens):
     if tokens.dtype == torch.int64:
         return 8
@@ -580,6 +586,7 @@ def dprc_embed_lookup(W, tokens, scale=1.0, out=None, stream=None):
     """out[..., :] = scale * W[tokens[...]], zero rows for negative tokens."""
     V, d = W.shape
     _need_cuda(W, tokens, out)
+    _beside("tokens", tokens, W)
     st = _stream(W, stream)
     shape = (*tokens.shape, d)
     if out is None:
@@ -609,6 +616,7 @@ def dprc_embed_plan(tokens, V, buf=None, stream=None):
     B, T = tokens.shape
     size = _token_bytes(tokens)
     _need_cuda(tokens, buf)
+    _beside("buf", buf, tokens)
     st = _stream(tokens, stream)
     if buf is None:
         n = lib().dprc_embed_plan_bytes(B * T, V)
@@ -624,6 +632,8 @@ def dprc_embed_plan(tokens, V, buf=None, stream=None):
 def _embed_ws(G, plan, ws, stream, given):
     if G.dim() != 3 or G.shape[0] != plan.B or G.shape[1] != plan.T:
         raise ValueError(f"G has shape {tuple(G.shape)}, the plan is of {plan.B} x {plan.T} tokens")
+    _beside("the plan", plan.buf, G)
+    _beside("ws", ws, G)
     if ws is None:
         n = lib().dprc_embed_workspace_bytes(_dtype_code(G), plan.B, plan.T, G.shape[2])
         if n == 0:
@@ -679,6 +689,7 @@ def dprc_dropout(x, p, seed, step, residual=None, first_element=0, out=None, str
 
 
 def _linear_ws(like, M, K, N, grad, ws, stream, given):
+    _beside("ws", ws, like)
     if ws is None:
         n = lib().dprc_linear_workspace_bytes(_dtype_code(like), M, K, N, grad)
         if n == 0:
