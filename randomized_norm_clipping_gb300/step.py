@@ -103,8 +103,8 @@ class RandomizedClippingStep:
         covered |= {id(m.bias) for m in self.biased}
         for name, prm in model.named_parameters():
             if prm.requires_grad and id(prm) not in covered:
-                raise ValueError(f"trainable parameter {name!r} is not a bias-free "
-                                 "nn.Linear weight; per-sample norms cover only those")
+                raise ValueError(f"trainable parameter {name!r} has no per-sample norm here; covered "
+                                 "are linear weights, the biases of layers.Linear and embeddings")
         for m in self.layers:
             if isinstance(m, torch.nn.Linear) and m.bias is not None and m.bias.requires_grad:
                 raise ValueError("nn.Linear layers with a trainable bias are not supported")

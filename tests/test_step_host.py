@@ -249,3 +249,9 @@ def test_bias_plans_are_made_once_a_size(monkeypatch):
         step(_losses(model, torch.randn(b, T, D)), step=0)
     assert len(step._bias_plans) <= 16  # sizes come and go
     step.close()
+
+
+def test_the_refusal_names_what_is_covered():
+    model = torch.nn.Sequential(lay.Embedding(5, D), torch.nn.LayerNorm(D))
+    with pytest.raises(ValueError, match="'1.weight'.*linear weights.*layers.Linear.*embeddings"):
+        RandomizedClippingStep(model, C=1.0, sigma=0.0)
