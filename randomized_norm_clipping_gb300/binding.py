@@ -574,6 +574,13 @@ def _beside(name, t, like):
         raise ValueError(f"{name} is on {t.device}, the call's tensors are on {like.device}")
 
 
+def _act(name):
+    code = DPRC_ACTS.get(name)
+    if code is None:
+        raise ValueError(f"act is one of {sorted(DPRC_ACTS)}, not {name!r}")
+    return code
+
+
 def _token_bytes(tokens):
     if tokens.dtype == torch.int64:
         return 8
@@ -706,7 +713,7 @@ def dprc_linear(X, W, bias=None, act="none", p=0.0, seed=0, step=0, residual=Non
     if X.shape[-1] != K:
         raise ValueError(f"X has width {X.shape[-1]}, W {K}")
     shape = (*X.shape[:-1], N)
-    M = X.numel() // K
+    M = X.numel() // K if K > 0 else 0
     dt, dev = X.dtype, X.device
     _need_cuda(X, W, bias, residual, Z, out, ws)
     st = _stream(X, stream)
@@ -720,7 +727,7 @@ def dprc_linear(X, W, bias=None, act="none", p=0.0, seed=0, step=0, residual=Non
     ws = _linear_ws(X, M, K, N, 0, ws, st, stream)
     _check("dprc_linear",
            lib().dprc_linear(X.data_ptr(), W.data_ptr(), _ptr(bias), _ptr(residual),
-                             _dtype_code(X), M, K, N, DPRC_ACTS[act], p, int(seed) & _U64,
+                             _dtype_code(X), M, K, N, _act(act), p, int(seed) & _U64,
                              int(step) & _U64, _ptr(Z), out.data_ptr(), ws.data_ptr(), ws.numel(),
                              st))
     return out
@@ -731,7 +738,7 @@ def dprc_linear_grad(dY, X, W, Z=None, act="none", p=0.0, seed=0, step=0, dX=Non
     """Gradient of dprc_linear into those of dX [..., K], dW [N][K], db [N] and
     dZ [..., N] that are given (act, p, seed, step as in its call)."""
     N, K = W.shape
-    M = dY.numel() // N
+    M = dY.numel() // N if N > 0 else 0
     lead = dY.shape[:-1]
     dt, dev = dY.dtype, dY.device
     if dY.shape[-1] != N:
@@ -748,6 +755,6 @@ def dprc_linear_grad(dY, X, W, Z=None, act="none", p=0.0, seed=0, step=0, dX=Non
     ws = _linear_ws(dY, M, K, N, 1, ws, st, stream)
     _check("dprc_linear_grad",
            lib().dprc_linear_grad(dY.data_ptr(), _ptr(X), W.data_ptr(), _ptr(Z), _dtype_code(dY),
-                                  M, K, N, DPRC_ACTS[act], p, int(seed) & _U64, int(step) & _U64,
+                                  M, K, N, _act(act), p, int(seed) & _U64, int(step) & _U64,
                                   _ptr(dX), _ptr(dW), _ptr(db), _ptr(dZ), ws.data_ptr(),
                                   ws.numel(), st))

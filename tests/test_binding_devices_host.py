@@ -96,3 +96,23 @@ def test_tensors_of_two_gpus_are_refused(lib, call):
     with pytest.raises(ValueError, match="cuda:1"):
         call(1)
     assert len(lib.made) == 1
+
+
+# ---- arguments that must be refused in the binding's own words ---------------
+def test_widths_of_zero_are_refused_by_the_library(lib, monkeypatch):
+    monkeypatch.setattr(Calls, "__getattr__",
+                        lambda self, name: lambda *a: 0 if name.endswith("_bytes") else 2)
+    with pytest.raises(binding.DprcError):
+        binding.dprc_linear(Fake((4, 0)), Fake((6, 0)))
+    with pytest.raises(binding.DprcError):
+        binding.dprc_linear_grad(Fake((4, 0)), Fake((4, 8)), Fake((0, 8)), dX=Fake((4, 8)))
+
+
+def test_unknown_activations_are_refused(lib):
+    ws = Fake((64,), torch.uint8)
+    with pytest.raises(ValueError, match="tanh"):
+        binding.dprc_linear(Fake((4, 8)), Fake((6, 8)), act="tanh", ws=ws)
+    with pytest.raises(ValueError, match="tanh"):
+        binding.dprc_linear_grad(Fake((4, 6)), Fake((4, 8)), Fake((6, 8)), act="tanh",
+                                 dX=Fake((4, 8)), ws=ws)
+    assert not lib.made
