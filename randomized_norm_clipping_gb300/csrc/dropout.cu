@@ -22,14 +22,14 @@ template <typename T>
 __device__ __forceinline__ void load8(const T* p, float* v);
 template <>
 __device__ __forceinline__ void load8<float>(const float* p, float* v) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = ld_stream(reinterpret_cast<const float4*>(p));
+  const float4 b = ld_stream(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 template <>
 __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
-  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint4 a = ld_stream(reinterpret_cast<const uint4*>(p));
   const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(32 * kRankWarps)
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int j = j0 + u * 32 * kRankWarps;
-      t[u] = j < N ? __ldcg(tokens + j) : TOK(0);
+      t[u] = j < N ? ld_l2(tokens + j) : TOK(0);
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -303,7 +303,7 @@ __device__ __forceinline__ void sort_keys(const TOK* src, int V, int i0, int ste
                                           uint32_t* k) {
   TOK t[kSortBatch];
 #pragma unroll
-  for (int j = 0; j < kSortBatch; ++j) t[j] = i0 + j * step < hi ? __ldcg(src + i0 + j * step) : TOK(0);
+  for (int j = 0; j < kSortBatch; ++j) t[j] = i0 + j * step < hi ? ld_l2(src + i0 + j * step) : TOK(0);
 #pragma unroll
   for (int j = 0; j < kSortBatch; ++j) {
     if constexpr (sizeof(TOK) == 4 && TOK(-1) > TOK(0))
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kSortThreads)
       int2 v[16];
 #pragma unroll
       for (int u = 0; u < 16; ++u)
-        v[u] = t0 + u < tiles ? __ldcg(reinterpret_cast<const int2*>(a.counts + (t0 + u) * nd + d))
+        v[u] = t0 + u < tiles ? ld_l2(reinterpret_cast<const int2*>(a.counts + (t0 + u) * nd + d))
                               : make_int2(0, 0);
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kSortThreads)
 #pragma unroll
     for (int j = 0; j < kSortBatch; ++j) {
       const int i = i0 + j * 32 + lane;
-      p[j] = i < hi && a.pos_in != nullptr ? __ldcg(a.pos_in + i) : i;
+      p[j] = i < hi && a.pos_in != nullptr ? ld_l2(a.pos_in + i) : i;
     }
     sort_keys(src, a.V, i0 + lane, 32, hi, k);
 #pragma unroll
@@ -528,7 +528,7 @@ __device__ __forceinline__ int sample_of(const SegArgs& a, int pos) {
 // what dprc_embed_plan wrote (read on another stream before it was written, say)
 // gives wrong sums, but no access outside the tensors.
 __device__ __forceinline__ int plan_pos(const SegArgs& a, long long i) {
-  return static_cast<int>(min(static_cast<uint32_t>(__ldcg(a.pos + i)), static_cast<uint32_t>(a.N - 1)));
+  return static_cast<int>(min(static_cast<uint32_t>(ld_l2(a.pos + i)), static_cast<uint32_t>(a.N - 1)));
 }
 
 // Rows of a range: lane l holds row l (l < rows).
@@ -559,7 +559,7 @@ __device__ __forceinline__ RangeRows range_rows(const SegArgs& a, int range, boo
   for (int w = 0; w < 3; ++w) {
     const int i = a0 - 32 + w * 32 + lane;
     const bool in = i >= 0 && i < a.N;
-    kw[w] = in ? min(__ldcg(a.key + i), V) : V;
+    kw[w] = in ? min(ld_l2(a.key + i), V) : V;
     pw[w] = in ? plan_pos(a, i) : 0;
   }
   uint32_t klast = kw[0];
@@ -657,7 +657,7 @@ __device__ __forceinline__ void segment_range(const SegArgs& a, const T* G, T* d
     const RangeRows q = range_rows<kNorm>(a, range, blk == 0);
     s.pos[lane] = q.pos;
     s.key[lane] = q.key;
-    if (!kNorm && a.c != nullptr && lane < q.rows) s.w[lane] = __ldcg(a.c + sample_of(a, q.pos));
+    if (!kNorm && a.c != nullptr && lane < q.rows) s.w[lane] = ld_l2(a.c + sample_of(a, q.pos));
     if (lane == 0) {
       s.E = q.E;
       s.L = q.L;
@@ -685,7 +685,7 @@ __device__ __forceinline__ void segment_range(const SegArgs& a, const T* G, T* d
     for (int r = 0; r < kBatch; ++r) {
       raw[r] = RawT{};
       if (base + r < rows && DPRC_IN(s.pos[base + r] >= 0 && s.pos[base + r] < a.N))
-        raw[r] = __ldcs(col + static_cast<long long>(s.pos[base + r]) * nvec);
+        raw[r] = ld_stream(col + static_cast<long long>(s.pos[base + r]) * nvec);
     }
     // bits of the batch's rows: ends of runs, ends of long runs' pieces, starts
     const uint32_t Eb = E >> base, Pb = (E & L) >> base;
@@ -858,7 +858,7 @@ __device__ __forceinline__ float4 add_pieces(const SegArgs& a, long long range, 
   for (long long p = p0; p < p1; ++p) {
     const long long row = (range + p) * 2 + (p == 0 ? slot : 0);
     if (DPRC_IN(range + p < a.nranges && col + 3 < a.dpad)) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + row * a.dpad + col));
+      const float4 v = ld_l2(reinterpret_cast<const float4*>(a.part + row * a.dpad + col));
       s.x += v.x;
       s.y += v.y;
       s.z += v.z;
@@ -892,7 +892,7 @@ __device__ __forceinline__ void finish_run(const SegArgs& a, T* dW, long long ra
     }
   } else {
     // (the run reaches past `range`)
-    const uint32_t k = min(__ldcg(a.key + (range + 1) * kRange - 1), static_cast<uint32_t>(a.V - 1));
+    const uint32_t k = min(ld_l2(a.key + (range + 1) * kRange - 1), static_cast<uint32_t>(a.V - 1));
     T* out = dW + static_cast<long long>(k) * a.d;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -988,7 +988,7 @@ __global__ void __launch_bounds__(256)
   const long long count = static_cast<long long>(a.T) * a.nblk;
   const float* sq = a.sq + i * count;
 #pragma unroll 8
-  for (long long t = t0; t < count; t += step) s += __ldcg(sq + t);
+  for (long long t = t0; t < count; t += step) s += ld_l2(sq + t);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
   if (lane == 0) s_warp[warp] = s;

@@ -34,6 +34,40 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int cl, c
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Loads of such a kernel with a cache policy: coherent, and volatile, so that the
+// compiler leaves each behind the kernel's wait.  ld_l2: from L2, not kept in L1;
+// ld_stream: to be evicted first; ld_once: a coherent load that leaves L1 as it is.
+#define DPRC_LOAD(name, op)                                                                 \
+  template <typename T>                                                                     \
+  __device__ __forceinline__ T name(const T* p) {                                           \
+    static_assert(sizeof(T) == 2 || sizeof(T) == 4 || sizeof(T) == 8 || sizeof(T) == 16,    \
+                  "one access");                                                            \
+    T r;                                                                                    \
+    if constexpr (sizeof(T) == 2) {                                                         \
+      asm volatile("ld.global" op ".b16 %0, [%1];"                                          \
+                   : "=h"(*reinterpret_cast<unsigned short*>(&r))                           \
+                   : "l"(p));                                                               \
+    } else if constexpr (sizeof(T) == 4) {                                                  \
+      asm volatile("ld.global" op ".b32 %0, [%1];"                                          \
+                   : "=r"(*reinterpret_cast<uint32_t*>(&r))                                 \
+                   : "l"(p));                                                               \
+    } else if constexpr (sizeof(T) == 8) {                                                  \
+      asm volatile("ld.global" op ".b64 %0, [%1];"                                          \
+                   : "=l"(*reinterpret_cast<unsigned long long*>(&r))                       \
+                   : "l"(p));                                                               \
+    } else {                                                                                \
+      uint32_t* u = reinterpret_cast<uint32_t*>(&r);                                        \
+      asm volatile("ld.global" op ".v4.b32 {%0, %1, %2, %3}, [%4];"                         \
+                   : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])                         \
+                   : "l"(p));                                                               \
+    }                                                                                       \
+    return r;                                                                               \
+  }
+DPRC_LOAD(ld_l2, ".cg")
+DPRC_LOAD(ld_stream, ".cs")
+DPRC_LOAD(ld_once, ".L1::no_allocate")
+#undef DPRC_LOAD
+
 // The two ends of a kernel that may run beside the one before it (launch_after).
 // It may where nothing it reads or writes is that kernel's, and that kernel let
 // it start only after its own wait (as beside_begin does), so that everything

@@ -72,19 +72,19 @@ __device__ __forceinline__ void store_planes(__nv_bfloat16* dst, long long plane
 
 // One value, not through L1: a kernel beside another one reads what was written
 // before both.
-__device__ __forceinline__ float ld_l2(const float* p) { return __ldcg(p); }
-__device__ __forceinline__ float ld_l2(const __nv_bfloat16* p) {
-  const unsigned short u = __ldcg(reinterpret_cast<const unsigned short*>(p));
+__device__ __forceinline__ float ld1_l2(const float* p) { return ld_l2(p); }
+__device__ __forceinline__ float ld1_l2(const __nv_bfloat16* p) {
+  const unsigned short u = ld_l2(reinterpret_cast<const unsigned short*>(p));
   return __uint_as_float(static_cast<uint32_t>(u) << 16);
 }
 __device__ __forceinline__ void ld8_l2(const float* p, float* v) {
-  const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = ld_l2(reinterpret_cast<const float4*>(p));
+  const float4 b = ld_l2(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 __device__ __forceinline__ void ld8_l2(const __nv_bfloat16* p, float* v) {
-  const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p));
+  const uint4 a = ld_l2(reinterpret_cast<const uint4*>(p));
   const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(256) linear_pack_kernel(const PackArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int c = c0 + 32 * e + lane;
-        v[e] = c < j.cols ? ld_l2(p + c) : 0.f;
+        v[e] = c < j.cols ? ld1_l2(p + c) : 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) reinterpret_cast<float*>(mine)[32 * e + lane] = v[e];
@@ -163,7 +163,7 @@ __device__ __forceinline__ void raw_ld(const T* p, int cnt, bool vec, Raw8<T>& r
   if (vec) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-      r.v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+      r.v[i] = ld_stream(reinterpret_cast<const uint4*>(p) + i);
   } else {
     T* e = reinterpret_cast<T*>(r.v);
 #pragma unroll
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(256)
   float t = 0.f;
   if (c < N) {
 #pragma unroll 8
-    for (int b = b0; b < b1; ++b) t += __ldcg(colsum + static_cast<long long>(b) * N + c);
+    for (int b = b0; b < b1; ++b) t += ld_l2(colsum + static_cast<long long>(b) * N + c);
   }
   s_sum[warp][lane] = t;
   __syncthreads();
@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(256)
     const float* p = part + m * ldpart + n;
 #pragma unroll 4
     for (int s = 0; s < split; ++s) {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(p + s * stride));
-      const float4 b = __ldcg(reinterpret_cast<const float4*>(p + s * stride) + 1);
+      const float4 a = ld_l2(reinterpret_cast<const float4*>(p + s * stride));
+      const float4 b = ld_l2(reinterpret_cast<const float4*>(p + s * stride) + 1);
       v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
       v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
     }

@@ -62,10 +62,11 @@ struct FewAccess {
     }
   }
   // A weight, read once: not kept in L1, which is X's (fp32, 2048 x 8192, four
-  // tokens: 29.5 us with both in L1, 22 so, 16 with four steps at a time).
+  // tokens: 29.5 us with both in L1, 22 so, 16.5 with four steps at a time; 18.9 with
+  // .cg loads instead).
   __device__ __forceinline__ void load_once(const T* p, bool in) {
     if constexpr (kVec) {
-      raw = in ? __ldcg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+      raw = in ? ld_once(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
     } else {
       load(p, in);
     }
@@ -139,8 +140,8 @@ __global__ void __launch_bounds__(32 * kFewWarps) linear_few_kernel(const FewArg
     for (int t = 0; t < kTok; ++t) acc[f][t] = 0ull;
 
   // (the loads of two steps together, of four where an access is only four
-  // values: fp32 with 2, 4, 8 tokens 16.3, 22, 31.5 us by twos and 15.7, 16.1,
-  // 27.7 by fours, bf16 9.7, 10.2, 19.7 and 9.1, 16.3, 20.5; four features and
+  // values: fp32 with 2, 4, 8 tokens 16.3, 22, 31.5 us by twos and 15.7, 16.5,
+  // 28.1 by fours, bf16 9.7, 10.2, 19.7 and 9.1, 16.3, 20.5; four features and
   // not two: what a step waits for is X from L1, and two features read it twice
   // as often: 32 us and not 20 us for 8 tokens, 2048 x 8192 bf16)
   constexpr int kAhead = kVec && sizeof(T) == 4 ? 4 : 2;

@@ -259,7 +259,7 @@ __device__ __forceinline__ bool gemm_collect_ahead(const GemmArgs& a, uint32_t t
   for (int s = 0; s < kAhead; ++s) fetch(ahead[s], s * kStep);
   uint32_t bias = 0;
   if (e.bias != nullptr && col0 + 2 * lane < a.cols)
-    bias = __ldcg(reinterpret_cast<const uint32_t*>(static_cast<const T*>(e.bias) + col0) + lane);
+    bias = ld_l2(reinterpret_cast<const uint32_t*>(static_cast<const T*>(e.bias) + col0) + lane);
   ok = ok && wait_warp(&accf[pos.set], pos.parity, DPRC_DEVERR_ACCUM, abort_flag);
   tc_fence_after();
   if (ok) {

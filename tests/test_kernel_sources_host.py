@@ -74,3 +74,13 @@ def test_early_kernels_read_by_coherent_loads(path):
 def test_early_kernels_are_looked_at():
     names = {os.path.basename(p) for p in AFTER}
     assert {"embed.cu", "dropout.cu", "linear.cu", "linear_gemm.cu", "linear_few.cu"} <= names
+
+
+@pytest.mark.parametrize("path", AFTER, ids=os.path.basename)
+def test_early_kernels_read_behind_their_wait(path):
+    """The loads of a cache policy are volatile assembly, which the compiler keeps in
+    the order of the wait; what the built-in ones are is not said."""
+    text = _text(path)
+    assert re.search(r"\b__ld(cg|cs|ca|cv|lu)\s*\(", text) is None
+    for m in re.finditer(r'asm\s+(volatile)?\s*\(\s*"ld\.', text):
+        assert m.group(1), text[m.start(): m.start() + 80]
