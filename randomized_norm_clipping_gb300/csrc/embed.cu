@@ -271,12 +271,13 @@ __global__ void __launch_bounds__(32 * kRankWarps)
 // in lower lanes.  It also counts the next digit by the tiles the entries go to
 // (whole numbers: the order of the additions changes nothing; with a counting
 // launch a digit 16384 tokens took 11.2 us and not 10.9, 65536 19.8 and not
-// 18.8, and the caller's time for the launch).  Keys have as many bits as V (the
+// 18.8, and the caller's time for the launch; 11.1 and 19.2 with coherent loads,
+// launch.cuh).  Keys have as many bits as V (the
 // key of "no token") needs, in digits of at most 10 bits.
 //
 // Launches and not barriers inside one launch: one cluster of 8 CTAs, with the
 // hardware's cluster barrier between the steps, took 44 us for 65536 tokens
-// (its 8 SMs' scattered stores alone 18 us), these launches 18.8 us.
+// (its 8 SMs' scattered stores alone 18 us), these launches 19.2 us.
 // ---------------------------------------------------------------------------
 constexpr int kSortWarps = 8;
 constexpr int kSortThreads = 32 * kSortWarps;
