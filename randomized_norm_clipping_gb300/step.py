@@ -29,7 +29,7 @@ embeddings are exact and cheap (dprc_embed_norm: a group sum of the output
 gradients), other kinds (normalisation gains) would need their own per-sample
 gradients, which the method does not cover.  Each layer runs once per
 forward pass on inputs (B, ..., d) (every position between the batch and the
-feature axis counts as a token), or on rows of one sample after another; positions
+feature axis counts as a token), or on one sample after another; positions
 that the samples share (an embedding of arange(T)) are expanded to [B, T] first.
 A layer that runs twice and an input that mixes samples are refused, since a
 sample's norm would not be that of its gradient.  The per-sample losses must not
@@ -158,37 +158,35 @@ class RandomizedClippingStep:
     def _refuse_mixed(self, recorded, losses):
         """Raises unless every layer's positions fall into B equal shares, one after
         another, that belong to one sample each.  Inputs with the batch and a
-        position axis in front are taken at their word.  Others (rows; an
-        embedding's [B]) may be shared positions as well: once per layer and
+        position axis in front are taken at their word.  Others (rows, packed
+        sequences, an embedding's [B]) may be shared positions as well: once per layer and
         share, the first and the last sample's losses must have no gradient
         outside their own share."""
         B = losses.shape[0]
-        doubtful = []
-        for m in recorded:
+        shares = {}
+        for m in recorded if B > 1 else ():
             x = self._acts[m]
-            rows = x.shape[0] if x.dim() > 0 else 1
-            if B <= 1:
-                continue
-            if rows % B != 0:
+            table = m in self.embeddings
+            positions = x.numel() if table else x.numel() // max(x.shape[-1], 1)
+            if positions % B != 0:
                 raise ValueError(f"{type(m).__name__}: an input of shape {tuple(x.shape)} does not "
                                  f"hold the positions of {B} samples; shared positions need an "
                                  "entry for every sample")
-            if (m, rows // B) in self._apart or (
-                    rows == B and (x.dim() > 1 or m not in self.embeddings)):
-                continue
-            doubtful.append(m)
-        for i in (0, B - 1) if doubtful else ():
-            grads = torch.autograd.grad(losses[i], [self._outs[m] for m in doubtful],
+            whole = x.dim() > 1 and x.shape[0] == B  # (an embedding's [B] has one axis)
+            if not whole and (m, positions // B) not in self._apart:
+                shares[m] = positions // B
+        for i in (0, B - 1) if shares else ():
+            grads = torch.autograd.grad(losses[i], [self._outs[m] for m in shares],
                                         retain_graph=True, allow_unused=True)
-            for m, g in zip(doubtful, grads):
+            for (m, n), g in zip(shares.items(), grads):
                 if g is None:
                     continue
-                n = g.shape[0] // B
+                g = g.reshape(B * n, -1)
                 # (a NaN is what 0 becomes beside an infinity)
                 if any(bool(((r != 0) & (r == r)).any()) for r in (g[:i * n], g[(i + 1) * n:])):
-                    raise ValueError(f"{type(m).__name__}: rows of an input of shape "
+                    raise ValueError(f"{type(m).__name__}: positions of an input of shape "
                                      f"{tuple(self._acts[m].shape)} belong to more than one sample")
-        self._apart.update((m, self._acts[m].shape[0] // B) for m in doubtful)
+        self._apart.update(shares.items())
 
     def parameters(self):
         """The trainable parameters in the order the noise stream runs over

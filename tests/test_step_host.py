@@ -255,3 +255,19 @@ def test_the_refusal_names_what_is_covered():
     model = torch.nn.Sequential(lay.Embedding(5, D), torch.nn.LayerNorm(D))
     with pytest.raises(ValueError, match="'1.weight'.*linear weights.*layers.Linear.*embeddings"):
         RandomizedClippingStep(model, C=1.0, sigma=0.0)
+
+
+def test_packed_samples_are_taken():
+    """All samples' positions behind a leading axis of one, sample after sample."""
+    class Packed(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.embed, self.up = lay.Embedding(10, D), lay.Linear(D, D, bias=True, act="silu")
+            self.head = torch.nn.Linear(D, D, bias=False)
+
+        def forward(self, tok):
+            n, t = tok.shape
+            return self.head(self.up(self.embed(tok.reshape(1, n * t)))).view(n, t, D)
+
+    model, tok = Packed(), torch.randint(0, 10, (B, T))
+    _check(model, lambda: _losses(model, tok), lambda i: _losses(model, tok[i:i + 1]).sum())
