@@ -9,11 +9,11 @@ namespace dprc {
 
 // Launches `kernel` so that it may start while the kernel before it in the
 // stream ends; the kernel waits for that one (pdl_wait) before it reads or
-// writes anything.  Its data may so be written while it lives, and the loads are
-// coherent ones for that reason: never __ldg, ld.global.nc, or a plain read of what
-// a const __restrict__ parameter points to, which the compiler may turn into one.
-// A tensor-core map of 16384 x 1024 x 1024 bf16 takes 32 us
+// writes anything.  A tensor-core map of 16384 x 1024 x 1024 bf16 takes 32 us
 // back to back where it takes 37 us behind the full end of the kernel before.
+// What such a kernel reads may be written while it lives, so that it reads by
+// coherent loads only: never __ldg, ld.global.nc, or a plain read of what a
+// const __restrict__ parameter points to, which the compiler may turn into one.
 // cl: CTAs per cluster.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int cl, cudaStream_t s,

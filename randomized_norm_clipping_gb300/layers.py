@@ -116,6 +116,11 @@ class _Masked(torch.nn.Module):
         self._seed_given = seed is not None
         self._passes = {}
 
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        self.__dict__.setdefault("_seed_given", True)  # (pickled without these two)
+        self.__dict__.setdefault("_passes", {})
+
     def __deepcopy__(self, memo):
         """A copy, which gets a seed of its own where this module has one."""
         new = self.__class__.__new__(self.__class__)

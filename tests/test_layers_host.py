@@ -3,6 +3,7 @@
 import copy
 import gc
 import os
+import pickle
 import weakref
 
 import pytest
@@ -218,3 +219,14 @@ def test_nothing_of_a_pass_is_kept_after_its_backward_pass():
     y = checkpoint(m, torch.randn(4, 6, requires_grad=True), use_reentrant=False)
     y.sum().backward()
     assert m._last is None
+
+
+def test_modules_pickled_before_they_kept_passes_load():
+    m = lay.Linear(5, 3, act="silu", p=0.2, seed=4)
+    old = {k: v for k, v in m.__dict__.items() if k not in ("_passes", "_seed_given")}
+    new = lay.Linear.__new__(lay.Linear)
+    new.__setstate__(old)
+    x = torch.randn(6, 5)
+    assert torch.equal(new(x), m(x)) and copy.deepcopy(new).seed == 4
+    again = pickle.loads(pickle.dumps(m))
+    assert (again.seed, again.step) == (4, 1) and torch.equal(again(x), m(x))
