@@ -394,7 +394,8 @@ dprc_status dprc_philox_words(uint32_t* out, int64_t n_blocks, uint64_t first_bl
 
 /*
  * ---------------------------------------------------------------------------
- * The operators around the norm path: the embedding, dropout, the linear map.
+ * The operators around the norm path: the embedding, dropout, the linear map,
+ * normalisation, rotary positions and attention.
  *
  * With them a model of embeddings, linear maps (bias, activation, dropout,
  * residual) and its per-sample clipping runs on this library: the norms of
@@ -523,6 +524,116 @@ dprc_status dprc_linear_grad(const void* dY, const void* X, const void* W, const
                              dprc_dtype dtype, int64_t M, int64_t K, int64_t N, dprc_act act,
                              double p, uint64_t seed, uint64_t step, void* dX, void* dW, void* db,
                              void* dZ, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Layer normalisation of the last axis (center != 0), or its form without the
+ * mean (RMS normalisation):
+ *     mu = mean(x) (or 0),  r = (mean((x - mu)^2) + eps)^(-1/2)
+ *     y  = weight (x - mu) r + bias
+ *  X, Y device [B][T][d], weight and bias [d] or NULL (1 and 0), all dtype; Y may
+ *  be X.  stats, if not NULL, receives (mu, r) of every token, float [B][T][2]: the
+ *  gradient needs it.  Statistics and sums in fp32, the output rounded once.
+ *  1 <= B <= 65535, T >= 0, 1 <= d <= 16384, eps >= 0.
+ */
+dprc_status dprc_layernorm(const void* X, const void* weight, const void* bias, dprc_dtype dtype,
+                           int64_t B, int64_t T, int64_t d, float eps, int center, void* Y,
+                           float* stats, void* stream);
+
+/*
+ * Gradient of dprc_layernorm, with the per-sample norms of its parameters'
+ * gradients.  With xh = (x - mu) r, g = dY weight and sample i's sums
+ * W_i = sum_t dY_it xh_it, b_i = sum_t dY_it:
+ *     dX = r (g - mean(g) - xh mean(g xh))       (without mean(g) if center = 0)
+ *     dW = sum_i c_i W_i,  db = sum_i c_i b_i    (c float [B], or NULL for all 1)
+ *     n_i (+)= ||W_i||^2 (+ ||b_i||^2 if norm_of_bias != 0)
+ *  dX [B][T][d], dW, db [d] of dtype and n float [B] may be NULL and are then not
+ *  formed; not all.  accumulate != 0 adds to n.  dX may be dY.  stats as the
+ *  forward call left it; weight as in that call.  Sums in fp32.
+ *  ws device, dprc_layernorm_workspace_bytes(B, T, d, n != NULL) bytes.
+ */
+size_t dprc_layernorm_workspace_bytes(int64_t B, int64_t T, int64_t d, int norms);
+dprc_status dprc_layernorm_grad(const void* dY, const void* X, const float* stats,
+                                const void* weight, dprc_dtype dtype, int64_t B, int64_t T,
+                                int64_t d, int center, void* dX, void* dW, void* db, float* n,
+                                int norm_of_bias, int accumulate, const float* c, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/*
+ * Rotary positions with one or several axes (time, height, width).  The first 2 P
+ * elements of a head, P = sum of sections, are P pairs: (p, P + p), or neighbours
+ * (2p, 2p + 1) if interleaved != 0.  The first sections[0] pairs belong to axis 0, the
+ * next sections[1] to axis 1, and so on.  Pair p of axis a at a token's position
+ * pos[a] is turned by the angle pos[a] freqs[p] (inverse != 0: by minus that, which is
+ * the gradient of the call without it).  Elements behind the pairs are copied.
+ *  X and out device, [B][T][H][D] of dtype with the strides x_stride and out_stride
+ *  (host, of B, T and H, in elements; a head's elements lie together); any alignment
+ *  of the type.  out may be X (with the same strides), else the two do not overlap.
+ *  positions device [B][T][axes], int32 (position_bytes 4) or int64 (8); freqs device
+ *  double [P], radians; sections host [axes].
+ *  B, T >= 0, 1 <= H <= 65535, 1 <= D <= 4096, 1 <= axes <= 8, 2 P <= D.
+ *  Angles are reduced in fp64 (positions to 2^53 count); sines and products in fp32.
+ */
+dprc_status dprc_rotary(const void* X, const int64_t* x_stride, dprc_dtype dtype, int64_t B,
+                        int64_t T, int64_t H, int64_t D, const void* positions,
+                        int position_bytes, int axes, const int64_t* sections,
+                        const double* freqs, int interleaved, int inverse, void* out,
+                        const int64_t* out_stride, void* stream);
+
+/*
+ * Attention.  Query t of sample b stands at position i = first[b] + t, key j at j;
+ * head h of the queries reads head h / (H / Hkv) of the keys:
+ *     s = scale q.k;  s = cap tanh(s / cap) if cap > 0;  s -= slopes[h] |i - j|
+ *     out = sum_j softmax_j(s) v_j over the keys that the query sees
+ * It sees key j if j < lengths[b], and (causal != 0) j <= i or j < prefix[b], and (docs
+ * given) docs[b][i] = docs[b][j] >= 0.  A query outside 0 <= i < Tk has no document.
+ * A query that sees nothing gets zeros, and lse -inf.
+ *  Q device [B][Tq][H][D], K and V [B][Tk][Hkv][D], of dtype, with strides (of B, T
+ *  and H, in elements; a head's elements lie together; any alignment of the type).
+ *  slopes float [H]; docs int32 [B][Tk] (a negative id is padding); prefix, lengths
+ *  (clamped to 0..Tk) and first int32 [B]; NULL: slopes 0, one document, no prefix,
+ *  all Tk keys, first = Tk - Tq.
+ *  out [B][Tq][H][D] of dtype, dense; lse float [B][H][Tq] or NULL: the logarithm of
+ *  the sum of exp(s), which the gradient needs.
+ *  Keys behind lengths[b], behind what any query of the call sees, or of a negative
+ *  document are not used, whatever they hold.  A key that some queries see and
+ *  others do not must be finite (a NaN or infinity in it may reach both).
+ *  Scores, softmax and sums in fp32.  For bf16 the softmax's weights (and the
+ *  gradient of the scores) enter the products rounded to bf16.
+ *  1 <= D <= 128, Tq, Tk <= 2^20, B Hkv <= 65535, Tq H / Hkv <= 2^28, H / Hkv <= 4096.
+ *  bf16 runs on the tensor cores where D, the strides and the addresses are multiples of
+ *  8 elements (16 bytes) and H / Hkv <= 128, else on the CUDA cores (the gradient: dO's
+ *  too).
+ *  ws device, dprc_attention_workspace_bytes(a, 0) bytes.
+ */
+typedef struct {
+    const void *Q, *K, *V;
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    dprc_dtype dtype;
+    int64_t B, Tq, Tk, H, Hkv, D;
+    float scale, cap;
+    int causal;
+    const float* slopes;
+    const int32_t *docs, *prefix, *lengths, *first;
+} dprc_attention_args;
+size_t dprc_attention_workspace_bytes(const dprc_attention_args* a, int grad);
+dprc_status dprc_attention(const dprc_attention_args* a, void* out, float* lse, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of dprc_attention (the same arguments): dQ, dK and dV, each with strides as
+ * Q, K and V have them (the tensors' elements do not overlap); any may be NULL and is
+ * then not formed, not all.  A head of keys gets the sum over its queries' heads.
+ *  dO and O device [B][Tq][H][D] of dtype with strides like Q's, and lse: the output's
+ *  gradient and what the forward call gave.  Every element of the gradients is written; those of
+ *  queries that see nothing and keys that are not seen are zero.  dO of a query that
+ *  sees nothing is not used.
+ *  ws device, dprc_attention_workspace_bytes(a, 1) bytes.
+ */
+dprc_status dprc_attention_grad(const dprc_attention_args* a, const void* dO,
+                                const int64_t* do_stride, const void* O, const int64_t* o_stride,
+                                const float* lse, void* dQ, const int64_t* dq_stride, void* dK,
+                                const int64_t* dk_stride, void* dV, const int64_t* dv_stride,
+                                void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Reads (and, if reset != 0, clears) the device error word of the current

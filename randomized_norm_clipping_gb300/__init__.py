@@ -4,7 +4,8 @@ The compute lives in libdprc.so (C ABI: include/dprc.h): tensor-core
 Hutchinson and Hutch++ per-sample gradient-norm estimation, the exact norm
 (direct and ghost-clipping forms), clip factors and Philox Gaussian noise; and
 the operators around that path: the embedding (lookup, per-sample norm, clipped
-gradient), dropout and the linear map with its epilogue and gradient.
+gradient), dropout, the linear map with its epilogue and gradient, normalisation
+with the per-sample norms of its parameters, rotary positions and attention.
 This package is its ctypes binding, torch modules over it (layers), the training
 step, and the seeded synthetic workloads used by the tests and the benchmark.
 """
@@ -30,6 +31,8 @@ from .binding import (  # noqa: F401
     dprc_abi_version,
     dprc_add_noise,
     dprc_add_noise_at,
+    dprc_attention,
+    dprc_attention_grad,
     dprc_clip_factors,
     dprc_device_error,
     dprc_dropout,
@@ -39,6 +42,8 @@ from .binding import (  # noqa: F401
     dprc_embed_plan,
     dprc_exact_norm,
     dprc_exact_norm_plan,
+    dprc_layernorm,
+    dprc_layernorm_grad,
     dprc_linear,
     dprc_linear_grad,
     dprc_norm_hutch,
@@ -51,6 +56,7 @@ from .binding import (  # noqa: F401
     dprc_norm_hutchpp,
     dprc_norm_hutchpp_launches,
     dprc_philox_words,
+    dprc_rotary,
     dprc_set_phase_events,
     dprc_test_hutch_fault,
     dprc_workspace_bytes,

@@ -28,6 +28,7 @@ DEBUG_LIB_PATH = os.path.join(PKG_DIR, "libdprc_debug.so")
 
 SOURCES = ["api.cu", "tc_proj.cu", "tc_exact.cu", "tc_narrow.cu", "tc_hutch.cu", "simt.cu", "qr.cu", "qr_cluster.cu", "hutchpp.cu", "noise.cu", "noalloc.cu",
            "embed.cu", "dropout.cu", "linear.cu", "linear_gemm.cu", "linear_few.cu",
+           "layernorm.cu", "rotary.cu", "attention.cu", "attention_simt.cu", "attention_tc.cu",
            "ops_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 VARIANTS = {"release": ([], LIB_PATH), "debug": (["-DDPRC_DEBUG"], DEBUG_LIB_PATH)}

@@ -357,6 +357,22 @@ bool make_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t dim0, uint64
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// dims and box: width first; strides of the other axes in elements, multiples of 8.
+bool make_tmap_4d_bf16(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                       const uint64_t (&strides)[3], const uint32_t (&box)[4]) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4];
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  for (int k = 0; k < 4; ++k) d[k] = dims[k];
+  for (int k = 0; k < 3; ++k) st[k] = strides[k] * 2;
+  for (int k = 0; k < 4; ++k) bx[k] = box[k];
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, bx, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace dprc
 
 using namespace dprc;
@@ -1204,7 +1220,11 @@ dprc_status dprc_device_error(int32_t* out, int reset) {
                                                      read_device_error_embed,
                                                      read_device_error_linear,
                                                      read_device_error_linear_prep,
-                                                     read_device_error_linear_few};
+                                                     read_device_error_linear_few,
+                                                     read_device_error_attention,
+                                                     read_device_error_attention_simt,
+                                                     read_device_error_layernorm,
+                                                     read_device_error_rotary};
   int32_t first = 0;
   for (auto rd : readers) {
     int32_t v = 0;

@@ -1,0 +1,259 @@
+// Attention's calls: which kernels take them, and the small kernels around them
+// (what spans of keys hold of documents, the gradient's row sums, joining the
+// shares of rows whose keys were split).
+
+#include <algorithm>
+
+#include "attention.cuh"
+#include "vec.cuh"
+
+namespace dprc {
+namespace {
+
+// One warp a span: its documents' least and greatest id, so that a tile of keys
+// is met only by the rows whose documents it may hold.
+__global__ void __launch_bounds__(256) attention_spans_kernel(const int* docs, int Tk, int spans,
+                                                              long long total, DocSpan* out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (w >= total) return;
+  const int lane = threadIdx.x & 31;
+  const long long b = w / spans;
+  const int j0 = static_cast<int>(w - b * spans) * kDocSpan;
+  int lo = 0x7fffffff, hi = -1, pad = 0;
+#pragma unroll
+  for (int k = 0; k < kDocSpan; k += 32) {
+    const int j = j0 + k + lane;
+    if (j >= Tk) continue;
+    const int d = docs[b * Tk + j];
+    if (d >= 0) {
+      lo = min(lo, d);
+      hi = max(hi, d);
+    } else {
+      pad = 1;
+    }
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    pad |= __shfl_xor_sync(0xffffffffu, pad, o);
+  }
+  if (lane == 0) out[w] = {lo, hi, pad, 0};
+}
+
+// delta[b][h][t] = sum over the width of dO O: eight threads a row, 16 bytes of
+// both at a time where the width allows.  Bound by bytes: both are read once.
+template <typename T, int kE>
+__global__ void __launch_bounds__(256)
+    attention_delta_kernel(const AttnArgs a, long long rows) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long r = static_cast<long long>(blockIdx.x) * 32 + (threadIdx.x >> 3);
+  const int t = threadIdx.x & 7;
+  float s = 0.f;
+  const long long bt = r / a.H, b = bt / a.Tq, h = r - bt * a.H, tok = bt - b * a.Tq;
+  if (r < rows) {
+    const T* dO = static_cast<const T*>(a.dO) + b * a.dob + tok * a.dot + h * a.doh;
+    const T* O = static_cast<const T*>(a.O) + b * a.ob + tok * a.ot + h * a.oh;
+    for (int c = t * kE; c < a.D; c += 8 * kE) {
+      Raw<T, kE> x, y;
+      float u[kE], v[kE];
+      x.load(dO + c);
+      y.load(O + c);
+      x.get(u);
+      y.get(v);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) s = fmaf(u[e], v[e], s);
+    }
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (r < rows && t == 0) a.delta[(b * a.H + h) * a.Tq + tok] = s;
+}
+
+// The shares of a row's keys, in order: a warp a row.
+template <typename T>
+__global__ void __launch_bounds__(128)
+    attention_join_kernel(const AttnArgs a, long long rows) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (r >= rows) return;
+  const float* stats = a.part + rows * a.splits * a.D;
+  float m = -INFINITY;
+  for (int z = lane; z < a.splits; z += 32) m = fmaxf(m, ld_l2(stats + (z * rows + r) * 2));
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float at = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int z0 = 0; z0 < a.splits; z0 += 32) {
+    const int z = z0 + lane;
+    float w = 0.f, mine = 0.f;
+    if (z < a.splits) {
+      const float2 st = ld_l2(reinterpret_cast<const float2*>(stats + (z * rows + r) * 2));
+      w = exp2f(st.x - at);
+      mine = w * st.y;
+    }
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    l += mine;
+    const int n = min(32, a.splits - z0);
+    for (int k = 0; k < n; ++k) {
+      const float f = __shfl_sync(0xffffffffu, w, k);
+      const float* p = a.part + ((z0 + k) * rows + r) * a.D;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c * 32 + lane < a.D) acc[c] = fmaf(f, ld_l2(p + c * 32 + lane), acc[c]);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const int per = a.Tq * a.G;
+  const long long bh = r / per, b = bh / a.Hkv;
+  const int p = static_cast<int>(r - bh * per), t = p / a.G;
+  const int h = static_cast<int>(bh - b * a.Hkv) * a.G + p - t * a.G;
+  T* out = static_cast<T*>(a.out) + ((b * a.Tq + t) * a.H + h) * a.D;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c * 32 + lane < a.D) out[c * 32 + lane] = T(acc[c] * inv);
+  if (a.lse != nullptr && lane == 0) a.lse[(b * a.H + h) * a.Tq + t] = m * kLn2 + logf(l);
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t round16(size_t v) { return (v + 15) / 16 * 16; }
+
+size_t span_bytes(const AttentionCall& c) {
+  return c.docs != nullptr ? round16(c.B * cdiv(c.Tk, kDocSpan) * sizeof(DocSpan)) : 0;
+}
+
+// Shares of the keys: as many as fill the GPU where the rows alone do not, each
+// of at least kLeast tiles (a share costs a partial row of its own).
+constexpr int kLeast = 2;
+struct Split {
+  int splits, per;
+};
+Split split_keys(const AttentionCall& c, int tile_rows, int tile_keys, int resident) {
+  const int64_t ctas = std::max<int64_t>(1, cdiv(c.Tq * (c.H / c.Hkv), tile_rows) * c.B * c.Hkv);
+  const int64_t tiles = std::max<int64_t>(1, cdiv(c.Tk, tile_keys));
+  int64_t want = std::max<int64_t>(1, resident / ctas);
+  want = std::min(want, std::max<int64_t>(1, tiles / kLeast));
+  Split s;
+  s.per = static_cast<int>(cdiv(tiles, want));
+  s.splits = static_cast<int>(cdiv(tiles, s.per));
+  return s;
+}
+
+Split plan_split(const AttentionCall& c) {
+  const int rows = static_cast<int>(c.Tq * (c.H / c.Hkv));
+  if (attention_tc_takes(c)) {
+    const int n = attention_tc_rows(c);
+    return split_keys(c, n, 128, 152);
+  }
+  return split_keys(c, attention_simt_rows(rows), 64, 304);
+}
+
+AttnArgs args_of(const AttentionCall& c, char* ws) {
+  AttnArgs a = {};
+  a.Q = c.Q; a.K = c.K; a.V = c.V;
+  a.qb = c.qs[0]; a.qt = c.qs[1]; a.qh = c.qs[2];
+  a.kb = c.ks[0]; a.kt = c.ks[1]; a.kh = c.ks[2];
+  a.vb = c.vs[0]; a.vt = c.vs[1]; a.vh = c.vs[2];
+  a.B = static_cast<int>(c.B);
+  a.Tq = static_cast<int>(c.Tq);
+  a.Tk = static_cast<int>(c.Tk);
+  a.H = static_cast<int>(c.H);
+  a.Hkv = static_cast<int>(c.Hkv);
+  a.D = static_cast<int>(c.D);
+  a.G = static_cast<int>(c.H / c.Hkv);
+  a.scale = c.scale;
+  a.cap = c.cap;
+  a.causal = c.causal;
+  a.slopes = c.slopes;
+  a.docs = c.docs;
+  a.prefix = c.prefix;
+  a.lengths = c.lengths;
+  a.first = c.first;
+  a.spans = c.docs != nullptr ? reinterpret_cast<const DocSpan*>(ws) : nullptr;
+  return a;
+}
+
+cudaError_t prepare_spans(const AttentionCall& c, char* ws, cudaStream_t s) {
+  if (c.docs == nullptr || c.Tk == 0) return cudaSuccess;
+  const int spans = static_cast<int>(cdiv(c.Tk, kDocSpan));
+  const long long total = c.B * spans;
+  return launch_after(attention_spans_kernel, dim3(static_cast<unsigned>(cdiv(total, 8))), 256, 1,
+                      s, 0, c.docs, static_cast<int>(c.Tk), spans, total,
+                      reinterpret_cast<DocSpan*>(ws));
+}
+
+template <typename T>
+cudaError_t delta_rows(const AttnArgs& a, cudaStream_t s) {
+  const long long rows = static_cast<long long>(a.B) * a.Tq * a.H;
+  const dim3 grid(static_cast<unsigned>(cdiv(rows, 32)));
+  const long long all = a.D | a.dob | a.dot | a.doh | a.ob | a.ot | a.oh;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.dO) | reinterpret_cast<uintptr_t>(a.O);
+  if (all % kVec16<T> == 0 && at % 16 == 0)
+    return launch_after(attention_delta_kernel<T, kVec16<T>>, grid, 256, 1, s, 0, a, rows);
+  return launch_after(attention_delta_kernel<T, 1>, grid, 256, 1, s, 0, a, rows);
+}
+
+}  // namespace
+
+size_t attention_ws_bytes(const AttentionCall& c) {
+  const Split sp = plan_split(c);
+  const size_t part = sp.splits > 1
+      ? static_cast<size_t>(sp.splits) * c.B * c.Tq * c.H * (c.D + 2) * 4 : 0;
+  return span_bytes(c) + part + 16;
+}
+
+size_t attention_grad_ws_bytes(const AttentionCall& c) {
+  return span_bytes(c) + static_cast<size_t>(c.B) * c.Tq * c.H * 4 + 16;
+}
+
+cudaError_t launch_attention(const AttentionCall& c, void* out, float* lse, void* ws,
+                             cudaStream_t s) {
+  char* w = static_cast<char*>(ws);
+  cudaError_t e = prepare_spans(c, w, s);
+  if (e != cudaSuccess) return e;
+  const Split sp = plan_split(c);
+  AttnArgs a = args_of(c, w);
+  a.out = out;
+  a.lse = lse;
+  a.splits = sp.splits;
+  a.per_split = sp.per;
+  a.part = reinterpret_cast<float*>(w + span_bytes(c));
+  e = attention_tc_takes(c) ? launch_attention_tc(a, s) : launch_attention_simt(a, c.dtype, s);
+  if (e != cudaSuccess || sp.splits == 1) return e;
+  const long long rows = static_cast<long long>(c.B) * c.Tq * c.H;
+  const dim3 grid(static_cast<unsigned>(cdiv(rows, 4)));
+  if (c.dtype == DPRC_F32)
+    return launch_after(attention_join_kernel<float>, grid, 128, 1, s, 0, a, rows);
+  return launch_after(attention_join_kernel<__nv_bfloat16>, grid, 128, 1, s, 0, a, rows);
+}
+
+cudaError_t launch_attention_grad(const AttentionGradCall& c, void* ws, cudaStream_t s) {
+  char* w = static_cast<char*>(ws);
+  cudaError_t e = prepare_spans(c.f, w, s);
+  if (e != cudaSuccess) return e;
+  AttnArgs a = args_of(c.f, w);
+  a.dO = c.dO;
+  a.O = c.O;
+  a.dob = c.dos[0]; a.dot = c.dos[1]; a.doh = c.dos[2];
+  a.ob = c.os[0]; a.ot = c.os[1]; a.oh = c.os[2];
+  a.lse_in = c.lse;
+  a.delta = reinterpret_cast<float*>(w + span_bytes(c.f));
+  a.dQ = c.dQ; a.dK = c.dK; a.dV = c.dV;
+  a.dqb = c.dqs[0]; a.dqt = c.dqs[1]; a.dqh = c.dqs[2];
+  a.dkb = c.dks[0]; a.dkt = c.dks[1]; a.dkh = c.dks[2];
+  a.dvb = c.dvs[0]; a.dvt = c.dvs[1]; a.dvh = c.dvs[2];
+  if (c.f.Tq > 0) {
+    e = c.f.dtype == DPRC_F32 ? delta_rows<float>(a, s) : delta_rows<__nv_bfloat16>(a, s);
+    if (e != cudaSuccess) return e;
+  } else {
+    a.dQ = nullptr;
+  }
+  if (c.f.Tk == 0) a.dK = a.dV = nullptr;
+  if (attention_tc_takes_grad(c)) return launch_attention_grad_tc(a, s);
+  return launch_attention_grad_simt(a, c.f.dtype, s);
+}
+
+}  // namespace dprc

@@ -1,0 +1,120 @@
+// What the attention kernels share: the arguments, what a row sees, and the
+// partial results of rows whose keys are split.
+//
+// The rows of a product are the queries of all heads that share a head of keys,
+// token by token: row p is token p / G and head p % G of the G = H / Hkv.  So a tile
+// of keys is read once for all of them, a few tokens still fill a tile, and the
+// sums over the heads of a group (gradients of keys and values) are sums over rows.
+#pragma once
+
+#include <atomic>
+
+#include "common.cuh"
+#include "internal.h"
+#include "launch.cuh"
+
+namespace dprc {
+
+// What a span of kDocSpan keys holds of documents: the least and greatest id
+// (of those that are no padding) and whether there is padding.
+constexpr int kDocSpan = 64;
+struct DocSpan {
+  int lo, hi, pad, unused;
+};
+
+struct AttnArgs {
+  const void *Q, *K, *V;
+  long long qb, qt, qh, kb, kt, kh, vb, vt, vh;  // strides in elements
+  int B, Tq, Tk, H, Hkv, D, G;
+  float scale, cap;
+  int causal;
+  const float* slopes;
+  const int *docs, *prefix, *lengths, *first;
+  const DocSpan* spans;  // [B][ceil(Tk / kDocSpan)], with docs
+  // forward
+  void* out;             // [B][Tq][H][D]
+  float* lse;            // [B][H][Tq] or null
+  int splits, per_split; // shares of the keys, in tiles
+  float* part;           // [splits][B][Hkv][Tq G][D] sums, then [..][2] maximum and sum
+  // gradient
+  const void *dO, *O;    // [B][Tq][H][D]
+  long long dob, dot, doh, ob, ot, oh;
+  const float* lse_in;
+  float* delta;          // [B][H][Tq]
+  void *dQ, *dK, *dV;
+  long long dqb, dqt, dqh, dkb, dkt, dkh, dvb, dvt, dvh;
+};
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+constexpr int kFar = 1 << 29;  // positions beyond are taken as this one
+
+// Keys of sample b that exist.
+__device__ __forceinline__ int attn_keys(const AttnArgs& a, int b) {
+  return a.lengths != nullptr ? min(max(a.lengths[b], 0), a.Tk) : a.Tk;
+}
+__device__ __forceinline__ int attn_first(const AttnArgs& a, int b) {
+  const int f = a.first != nullptr ? a.first[b] : a.Tk - a.Tq;
+  return min(max(f, -kFar), kFar);
+}
+
+// What one query sees: the keys below `lim` whose document is `doc` (with
+// documents; doc < 0: none).  A key before the causal border or inside the prefix is
+// below their maximum.
+struct RowSees {
+  int pos, lim, doc;
+};
+__device__ __forceinline__ RowSees attn_row(const AttnArgs& a, int b, int t, int keys, int first) {
+  RowSees r;
+  r.pos = first + t;
+  r.lim = keys;
+  if (a.causal) {
+    int see = r.pos + 1;
+    if (a.prefix != nullptr) see = max(see, a.prefix[b]);
+    r.lim = max(0, min(see, keys));
+  }
+  r.doc = 0;
+  if (a.docs != nullptr) {
+    r.doc = r.pos >= 0 && r.pos < a.Tk ? a.docs[static_cast<long long>(b) * a.Tk + r.pos] : -1;
+    if (r.doc < 0) r.lim = 0;
+  }
+  return r;
+}
+
+// The score of a key from the product z = q k scale, and its slope by z.
+__device__ __forceinline__ float attn_capped(const AttnArgs& a, float z, float* slope) {
+  if (a.cap <= 0.f) {
+    *slope = 1.f;
+    return z;
+  }
+  const float t = tanhf(z / a.cap);
+  *slope = 1.f - t * t;
+  return t * a.cap;
+}
+
+// Allows a kernel its shared memory, once per device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> done[kMaxDev];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kMaxDev;
+  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev].store(1, std::memory_order_release);
+  return e;
+}
+
+// The kernels (attention_simt.cu, attention_tc.cu).
+int attention_simt_rows(int rows);
+cudaError_t launch_attention_simt(const AttnArgs& a, dprc_dtype dt, cudaStream_t s);
+cudaError_t launch_attention_grad_simt(const AttnArgs& a, dprc_dtype dt, cudaStream_t s);
+bool attention_tc_takes(const AttentionCall& c);
+bool attention_tc_takes_grad(const AttentionGradCall& c);
+int attention_tc_rows(const AttentionCall& c);  // of a CTA
+cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attention_grad_tc(const AttnArgs& a, cudaStream_t s);
+
+}  // namespace dprc

@@ -1,0 +1,732 @@
+// Attention on the tensor cores (tcgen05, bf16 operands, fp32 accumulators in tensor
+// memory), forward and backward.
+//
+//   forward   S = Q K^T, P = exp2(S c - m), O += P V, with the running maximum m and sum of
+//             a row (one pass over the keys); O is rescaled only when m grows by 2^8
+//   dQ        per tile of rows:  S, dP = dO V^T, dS = P (dP - delta), dQ += dS K
+//   dK, dV    per tile of keys:  the same transposed, dV += P^T dO, dK += dS^T Q
+//
+// P and dS never leave the SM: a thread owns a lane of tensor memory (a row, or a key),
+// reads the scores, and writes the weights back as the bf16 first operand of the next
+// product.  One warp copies tiles by TMA into a ring, one thread issues the products,
+// eight warps do the softmax.
+//
+// The rows of a tile are the queries of all G heads that share a head of keys
+// (attention.cuh): 128 / G tokens, brought by one box of G heads by tokens.  So few
+// tokens fill a tile, a causal border costs 128 / G tokens and not 128, and the sum over
+// the heads of a group in dK and dV is the product's.
+//
+// The backward pass forms S and dP in both of its kernels (seven products for five):
+// with one kernel, dQ is a sum over CTAs, whose order would have to be kept or its
+// roundings change from run to run.
+
+#include <algorithm>
+
+#include "attention.cuh"
+#include "tmem.cuh"
+#include "vec.cuh"
+
+namespace dprc {
+namespace {
+
+constexpr int kTile = 128;           // rows, and keys, of a tile
+constexpr int kBlock = kTile * 128;  // bytes of a tile's 64 columns
+constexpr int kWarps = 8;            // of the softmax
+// A third group of four warps copies and issues; it gives registers to the softmax's,
+// which hold a row of 128 scores: 2 * 224 + 56 = 3 * 168, what the block is launched with.
+constexpr int kThreads = 32 * (kWarps + 4);
+constexpr int kRegsMore = 224, kRegsLess = 56;
+static_assert(kThreads * 168 == 256 * kRegsMore + 128 * kRegsLess, "registers of the block");
+constexpr int kMaxKeyTiles = (1 << 20) / kTile;
+constexpr float kLazy = 8.f;  // a row is rescaled when its maximum grows by 2^kLazy
+
+constexpr uint32_t kSuspendNs = 20000;
+
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait; false once it ran out (recorded) or another role has.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int code,
+                                         volatile int* abort) {
+  if (try_wait_long(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    if (try_wait_long(bar, parity)) return true;
+    if (*abort != 0) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      record_error(code);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
+// The same for a warp, which waits with one lane (polling lanes take issue slots).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int code,
+                                          volatile int* abort) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity, code, abort) ? 1 : 0;
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_less() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Descriptors of a tile [128][64 kBlocks] at a 1024-byte boundary.  As the operand
+// whose width is summed over (K-major): a step of 16 is 32 bytes, a block of 64 kBlock
+// bytes.  As the operand whose rows are summed over (MN-major): a step is 16 rows.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return make_sdesc(addr, 16, 1024, kSwz128);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+  return make_sdesc(addr, kBlock, 1024, kSwz128);
+}
+
+// acc = A B^T over the width D (both tiles' widths are summed over).
+__device__ __forceinline__ void mma_width(uint32_t acc, uint64_t a, uint64_t b, uint32_t idesc,
+                                          int steps) {
+  for (int k = 0; k < steps; ++k) {
+    const uint32_t at = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+    umma_bf16(acc, a + at, b + at, idesc, k > 0 ? 1u : 0u);
+  }
+}
+
+// acc (+)= A B with A [128][128] in tensor memory and B's rows summed over.
+__device__ __forceinline__ void mma_rows(uint32_t acc, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                         bool accumulate) {
+#pragma unroll
+  for (int k = 0; k < kTile / 16; ++k)
+    umma_bf16_ts(acc, a_tmem + k * 8, b + ((k * 2048) >> 4), idesc, accumulate || k > 0 ? 1u : 0u);
+}
+
+struct TcArgs {
+  AttnArgs a;
+  int nt;        // tokens of a tile of rows
+  int row_tiles; // tiles of rows of a head of keys
+  int groups;    // CTAs' groups of row tiles
+  int steps;     // D / 16, rounded up
+  float c;       // scale log2(e)
+  float c_cap;   // 2 scale log2(e) / cap
+  float cap2;    // cap log2(e)
+};
+
+// A stage and the parity of its round.
+struct Pos {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// The set bits of a list of words, in order.
+struct Bits {
+  const uint32_t* words;
+  int n, w = 0;
+  uint32_t left;
+  __device__ __forceinline__ Bits(const uint32_t* words, int n)
+      : words(words), n(n), left(n > 0 ? words[0] : 0u) {}
+  __device__ __forceinline__ int next() {  // -1: no more
+    while (left == 0u) {
+      if (++w >= n) return -1;
+      left = words[w];
+    }
+    const int b = __ffs(left) - 1;
+    left &= left - 1;
+    return w * 32 + b;
+  }
+};
+
+// Scores of one row in units of log2: what stands in z is q k; kForm 0: z times c is
+// the score (taken by the caller); 1: with the bias; 2: capped, with the bias.
+template <int kForm, int kN>
+__device__ __forceinline__ void scores(const TcArgs& x, float (&z)[kN], float slope2, float dist0) {
+  if constexpr (kForm == 2) {
+    // tanh(u) = 1 - 2 / (1 + exp(2 u)), to 2^-22 of the cap
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      const float t = fmaf(-2.f, rcp(1.f + ex2(z[j] * x.c_cap)), 1.f);
+      z[j] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(j)), t * x.cap2);
+    }
+  } else if constexpr (kForm == 1) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j)
+      z[j] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(j)), z[j] * x.c);
+  }
+}
+
+// Bits of 32 consecutive columns, of which the first n are set.
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
+// The columns whose document is this lane's, `theirs` being that of column `lane`: a
+// ballot for each document that the warp's lanes have, mostly one or two.
+__device__ __forceinline__ uint32_t same_docs(int doc, int theirs) {
+  uint32_t left = 0xffffffffu, mine = 0u;
+  while (left != 0u) {  // (the same for the warp)
+    const int d = __shfl_sync(0xffffffffu, doc, __ffs(left) - 1);
+    const uint32_t cols = __ballot_sync(0xffffffffu, theirs == d);
+    const bool is = doc == d;
+    if (is) mine = cols;
+    left &= ~__ballot_sync(0xffffffffu, is);
+  }
+  return mine;
+}
+
+// -inf in the columns, kN from key j0 on, that a row does not see.
+template <int kN>
+__device__ __forceinline__ void hide(float (&z)[kN], const RowSees& see, const int* docs, int j0,
+                                     int Tk, bool by_doc) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < kN / 32; ++q) {
+    uint32_t bits = first_bits(see.lim - j0 - q * 32);
+    if (by_doc) {
+      const int j = j0 + q * 32 + lane;
+      bits &= same_docs(see.doc, j < Tk ? docs[j] : -2);
+    }
+#pragma unroll
+    for (int u = 0; u < 32; ++u)
+      if (!((bits >> u) & 1u)) z[q * 32 + u] = -INFINITY;
+  }
+}
+
+// What the rows of this warp, of this CTA see, for the choice of tiles and masks.
+struct Extent {
+  int min_lim, max_lim, lo, hi;
+};
+__device__ __forceinline__ Extent warp_extent(bool mine, const RowSees& r, bool docs) {
+  Extent e;
+  e.min_lim = mine ? r.lim : 0x7fffffff;
+  e.max_lim = mine ? r.lim : 0;
+  e.lo = mine && r.doc >= 0 ? r.doc : 0x7fffffff;
+  e.hi = mine && r.doc >= 0 ? r.doc : -1;
+  for (int o = 16; o > 0; o >>= 1) {
+    e.min_lim = min(e.min_lim, __shfl_xor_sync(0xffffffffu, e.min_lim, o));
+    e.max_lim = max(e.max_lim, __shfl_xor_sync(0xffffffffu, e.max_lim, o));
+    e.lo = min(e.lo, __shfl_xor_sync(0xffffffffu, e.lo, o));
+    e.hi = max(e.hi, __shfl_xor_sync(0xffffffffu, e.hi, o));
+  }
+  return e;
+}
+
+// Documents in the 128 keys of a tile.
+__device__ __forceinline__ DocSpan key_tile_docs(const AttnArgs& a, int b, int tile) {
+  const int spans = (a.Tk + kDocSpan - 1) / kDocSpan;
+  const DocSpan* s = a.spans + static_cast<long long>(b) * spans;
+  DocSpan r = s[2 * tile];
+  if (2 * tile + 1 < spans) {
+    const DocSpan q = s[2 * tile + 1];
+    r.lo = min(r.lo, q.lo);
+    r.hi = max(r.hi, q.hi);
+    r.pad |= q.pad;
+  }
+  return r;
+}
+
+// Key tiles [t0, t1) that some row of the CTA may see, as bits.
+__device__ __forceinline__ void key_tile_bits(const AttnArgs& a, int b, int t0, int t1, int lo,
+                                              int hi, uint32_t* bits, int words) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  for (int w = warp; w < words; w += warps) {
+    const int tile = w * 32 + lane;
+    bool ok = tile >= t0 && tile < t1;
+    if (ok && a.docs != nullptr) {
+      const DocSpan s = key_tile_docs(a, b, tile);
+      ok = s.lo <= hi && lo <= s.hi;
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) bits[w] = m;
+  }
+}
+
+// Zeroes, by the 128 threads of a group, the rows of a tile that must not be read: 128
+// bytes of each of the blocks.
+template <int kBlocks>
+__device__ __forceinline__ void zero_row(uint8_t* tile, int r) {
+#pragma unroll
+  for (int q = 0; q < kBlocks; ++q) {
+    uint4* p = reinterpret_cast<uint4*>(tile + q * kBlock + r * 128);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
+template <int kBlocks, int kTiles>
+struct FwdCfg {
+  static constexpr int kQ = kTiles * kBlocks * kBlock;
+  static constexpr int kSlot = kBlocks * kBlock;
+  static constexpr int kStages = kBlocks == 1 ? 8 : (kTiles == 1 ? 5 : 4);
+  static constexpr int kSmem = kQ + kStages * kSlot + 1024 + 1024 + kMaxKeyTiles / 8;
+  static constexpr int kO = 128 * kTiles;  // first column of the sums
+  static constexpr int kTmem = kTiles == 2 || kBlocks == 2 ? (kTiles == 2 ? 512 : 256) : 256;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
+
+// Two tiles of rows in turn: while a group of four warps takes the exponentials of its
+// tile, the tensor core forms the other's products.  kTiles 1: few rows.
+template <int kBlocks, int kTiles, int kForm>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_tc_kernel(const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const TcArgs x) {
+  using Cfg = FwdCfg<kBlocks, kTiles>;
+  constexpr int kStages = Cfg::kStages;
+  const AttnArgs& a = x.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* qs = align_1024(smem_raw);
+  uint8_t* ring = qs + Cfg::kQ;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * Cfg::kSlot);
+  uint64_t* empty = full + kStages;
+  uint64_t* qfull = empty + kStages;
+  uint64_t* sfull = qfull + 1;   // [2]
+  uint64_t* pfull = sfull + 2;   // [2]
+  uint64_t* ofull = pfull + 2;   // [2]
+  uint64_t* drain = ofull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* ext = reinterpret_cast<int*>(tmem_slot + 2);  // greatest limit, least and greatest document
+  uint32_t* bits = reinterpret_cast<uint32_t*>(ring + kStages * Cfg::kSlot + 512);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bhs = a.B * a.Hkv;
+  const int bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  const int grp = x.groups - 1 - blockIdx.x / bhs;  // the longest rows first
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(qfull, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&sfull[w], 1);
+      mbar_init(&pfull[w], 4);
+      mbar_init(&ofull[w], 1);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+    ext[0] = 0;
+    ext[1] = 0x7fffffff;
+    ext[2] = -1;
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  if (warp == kWarps + 1) {
+    tmem_alloc(tmem_slot, Cfg::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int keys = attn_keys(a, b), first = attn_first(a, b);
+  const int w = warp >> 2;  // the tile of rows of a softmax warp
+  const int r = threadIdx.x & (kTile - 1);
+  const int tt = r / a.G, tok = (grp * kTiles + w) * x.nt + tt;
+  const bool mine = warp < 4 * kTiles && tt < x.nt && tok < a.Tq;
+  RowSees see = {0, 0, -1};
+  Extent e = {};
+  if (warp < 4 * kTiles) {
+    if (mine) see = attn_row(a, b, tok, keys, first);
+    e = warp_extent(mine, see, a.docs != nullptr);
+    if (lane == 0) {
+      atomicMax(&ext[0], e.max_lim);
+      atomicMin(&ext[1], e.lo);
+      atomicMax(&ext[2], e.hi);
+    }
+  }
+  __syncthreads();
+  const int top = ext[0];
+  const int t0 = blockIdx.z * a.per_split, t1 = min(t0 + a.per_split, (top + kTile - 1) / kTile);
+  const int words = max(0, (t1 + 31) / 32);
+  key_tile_bits(a, b, t0, t1, ext[1], ext[2], bits, words);
+  __syncthreads();
+
+  if (warp >= kWarps) {
+    regs_less<kRegsLess>();
+    if (warp == kWarps && lane == 0) {
+      Bits it(bits, words);
+      Pos pos;
+      int j = it.next(), issued = 0;
+      bool ok = true;
+      if (j >= 0) {
+        mbar_arrive_expect_tx(qfull, kTiles * kBlocks * x.nt * a.G * 128);
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+          for (int q = 0; q < kBlocks; ++q)
+            tma_load_4d(qs + (u * kBlocks + q) * kBlock, &map_q, qfull, q * 64, hk * a.G,
+                        (grp * kTiles + u) * x.nt, b);
+      }
+      const bool any = j >= 0;
+      for (; j >= 0 && ok; j = it.next()) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!wait_bar(&empty[pos.s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[pos.s], Cfg::kSlot);
+#pragma unroll
+          for (int q = 0; q < kBlocks; ++q)
+            tma_load_4d(ring + pos.s * Cfg::kSlot + q * kBlock, kv == 0 ? &map_k : &map_v,
+                        &full[pos.s], q * 64, hk, j * kTile, b);
+          ++issued;
+          pos.next(kStages);
+        }
+      }
+      // copies still under way land before the CTA can exit
+      if (any) mbar_wait(qfull, 0, DPRC_DEVERR_PIPE_FULL);
+      for (int k = issued - 1; k >= 0 && k >= issued - kStages; --k)
+        mbar_wait(&full[k % kStages], (k / kStages) & 1, DPRC_DEVERR_PIPE_FULL);
+    } else if (warp == kWarps + 1 && lane == 0) {
+      Bits it(bits, words);
+      const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
+      const uint32_t id_o = make_idesc_bf16(kTile, x.steps * 16, false, true);
+      const uint64_t dq = desc_k(smem_u32(qs));
+      const uint64_t dk = desc_k(smem_u32(ring)), dv = desc_mn(smem_u32(ring));
+      Pos pos;
+      int j = it.next(), n = 0;
+      bool ok = true, issued = false;
+      if (j >= 0) {
+        ok = wait_bar(qfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
+             wait_bar(&full[0], 0, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        if (ok) {
+          tc_fence_after();
+          issued = true;
+#pragma unroll
+          for (int u = 0; u < kTiles; ++u) {
+            mma_width(tmem + u * 128, dq + ((u * kBlocks * kBlock) >> 4), dk, id_s, x.steps);
+            umma_commit(&sfull[u]);
+          }
+          umma_commit(&empty[0]);
+          pos.next(kStages);
+        }
+      }
+      while (j >= 0 && ok) {
+        j = it.next();
+        const Pos v = pos;
+        pos.next(kStages);
+        const Pos k = pos;
+        if (j >= 0) pos.next(kStages);
+        ok = wait_bar(&full[v.s], v.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        if (ok && j >= 0) ok = wait_bar(&full[k.s], k.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u) {
+          ok = ok && wait_bar(&pfull[u], n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          mma_rows(tmem + Cfg::kO + u * 128, tmem + u * 128, dv + ((v.s * Cfg::kSlot) >> 4), id_o,
+                   n > 0);
+          if (j >= 0) {
+            mma_width(tmem + u * 128, dq + ((u * kBlocks * kBlock) >> 4),
+                      dk + ((k.s * Cfg::kSlot) >> 4), id_s, x.steps);
+            umma_commit(&sfull[u]);
+          } else {
+            umma_commit(&ofull[u]);
+          }
+        }
+        if (ok) {
+          umma_commit(&empty[v.s]);
+          if (j >= 0) umma_commit(&empty[k.s]);
+        }
+        ++n;
+      }
+      if (issued) umma_drain(drain, kWaitLimitNs);
+    }
+  } else {
+    regs_more<kRegsMore>();
+    if (warp < 4 * kTiles) {
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + Cfg::kO + w * 128;
+      const int h = hk * a.G + r - tt * a.G;
+      const float slope2 =
+          kForm > 0 && a.slopes != nullptr && mine ? a.slopes[h] * kLog2e : 0.f;
+      const int* docs = a.docs != nullptr ? a.docs + static_cast<long long>(b) * a.Tk : nullptr;
+      const int cols = x.steps * 16;
+      Bits it(bits, words);
+      Pos vpos;  // the ring's place of this tile's values
+      vpos.next(kStages);
+      float m = -INFINITY, l = 0.f;
+      int n = 0;
+      bool ok = true;
+      for (int j = it.next(); j >= 0; j = it.next(), ++n) {
+        ok = wait_warp(&sfull[w], n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const int j0 = j * kTile;
+        bool dirty = j0 + kTile > top, by_doc = false;
+        if (docs != nullptr) {
+          const DocSpan s = key_tile_docs(a, b, j);
+          by_doc = s.pad || s.lo != s.hi || e.lo != s.lo || e.hi != s.lo;
+          dirty = dirty || s.pad;
+        }
+        float z[kTile];
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          float part[32];
+          tmem_ld_32cols(ts + c, part);
+#pragma unroll
+          for (int u = 0; u < 32; ++u) z[c + u] = part[u];
+        }
+        scores<kForm>(x, z, slope2, static_cast<float>(see.pos - j0));
+        if (j0 + kTile > e.min_lim || by_doc) hide(z, see, docs, j0, a.Tk, by_doc);
+        const float mul = kForm == 0 ? x.c : 1.f;
+        float mx[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+        for (int c = 4; c < kTile; c += 4)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], z[c + u]);
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+        const bool grow = mt > m + kLazy || (m == -INFINITY && mt > m);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2(m - mt) : 1.f;
+          if (grow) m = mt;
+          l *= f;
+          if (n > 0) {
+            for (int c = 0; c < cols; c += 16) {
+              float o[16];
+              tmem_ld_16cols(to + c, o);
+              uint32_t u[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(o[q] * f);
+              tmem_st_16cols(to + c, u);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c0 = 0; c0 < kTile; c0 += 64) {
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float p0 = ex2(fmaf(z[c0 + c], mul, off)), p1 = ex2(fmaf(z[c0 + c + 1], mul, off));
+            sum[c & 2] += p0;
+            sum[(c & 2) + 1] += p1;
+            p[c / 2] = pack_bf16(p0, p1);
+          }
+          tmem_st_32cols(ts + c0 / 2, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        if (dirty && w == 0) {
+          // values that no row of the CTA sees may be anything, and 0 times NaN is NaN
+          ok = wait_warp(&full[vpos.s], vpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+          if (!ok) break;
+          const int key = j0 + r;
+          if (key >= top || (docs != nullptr && docs[key] < 0))
+            zero_row<kBlocks>(ring + vpos.s * Cfg::kSlot, r);
+          fence_proxy_async_smem();
+        }
+        vpos.next(kStages);
+        vpos.next(kStages);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[w]);
+      }
+      if (n > 0 && ok) ok = wait_warp(&ofull[w], 0, DPRC_DEVERR_ACCUM, abort_flag);
+      tc_fence_after();
+      if (ok) {
+        const bool parts = a.splits > 1;
+        const float inv = parts ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
+        const int rows = a.Tq * a.G;
+        const long long prow =
+            (static_cast<long long>(blockIdx.z) * bhs + bh) * rows + tok * a.G + r - tt * a.G;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                             ((static_cast<long long>(b) * a.Tq + tok) * a.H + h) * a.D;
+        for (int c = 0; c < cols; c += 16) {
+          float o[16];
+          if (n > 0) {
+            tmem_ld_16cols(to + c, o);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o[q] = 0.f;
+          }
+          if (!mine) continue;
+#pragma unroll
+          for (int q = 0; q < 16; q += 8) {
+            if (c + q >= a.D) continue;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) o[q + u] *= inv;
+            if (parts) {
+              store_row<4>(a.part + prow * a.D + c + q, o + q);
+              store_row<4>(a.part + prow * a.D + c + q + 4, o + q + 4);
+            } else {
+              store_row<8>(out + c + q, o + q);
+            }
+          }
+        }
+        if (mine && parts) {
+          float* st = a.part + static_cast<long long>(bhs) * rows * a.splits * a.D + prow * 2;
+          st[0] = m;
+          st[1] = l;
+        } else if (mine && a.lse != nullptr) {
+          a.lse[(static_cast<long long>(b) * a.H + h) * a.Tq + tok] = m * kLn2 + logf(l);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::kTmem);
+  }
+}
+
+template <int kBlocks, int kTiles, int kForm>
+cudaError_t launch_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                       const TcArgs& x, cudaStream_t s) {
+  constexpr int bytes = FwdCfg<kBlocks, kTiles>::kSmem;
+  const cudaError_t e = allow_smem<attention_tc_kernel<kBlocks, kTiles, kForm>>(bytes);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(x.a.B * x.a.Hkv * x.groups, 1, x.a.splits);
+  return launch_after(attention_tc_kernel<kBlocks, kTiles, kForm>, grid, kThreads, 1, s, bytes, q,
+                      k, v, x);
+}
+
+template <int kBlocks, int kTiles>
+cudaError_t launch_fwd_form(int form, const CUtensorMap& q, const CUtensorMap& k,
+                            const CUtensorMap& v, const TcArgs& x, cudaStream_t s) {
+  if (form == 0) return launch_fwd<kBlocks, kTiles, 0>(q, k, v, x, s);
+  if (form == 1) return launch_fwd<kBlocks, kTiles, 1>(q, k, v, x, s);
+  return launch_fwd<kBlocks, kTiles, 2>(q, k, v, x, s);
+}
+
+// A tensor [B][T][H][D] as boxes of 64 of the width, `heads` heads and `tokens` tokens.
+bool map_of(CUtensorMap* m, const void* p, long long B, long long T, long long H, long long D,
+            long long sb, long long st, long long sh, int heads, int tokens) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(H),
+                            static_cast<uint64_t>(T), static_cast<uint64_t>(B)};
+  // (an axis of one has any stride)
+  const uint64_t strides[3] = {static_cast<uint64_t>(H > 1 ? sh : 8),
+                               static_cast<uint64_t>(T > 1 ? st : 8),
+                               static_cast<uint64_t>(B > 1 ? sb : 8)};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(heads), static_cast<uint32_t>(tokens), 1};
+  return make_tmap_4d_bf16(m, p, dims, strides, box);
+}
+
+TcArgs tc_args(const AttnArgs& a, int tiles) {
+  TcArgs x;
+  x.a = a;
+  x.nt = kTile / a.G;
+  x.row_tiles = (a.Tq + x.nt - 1) / x.nt;
+  x.groups = (x.row_tiles + tiles - 1) / tiles;
+  x.steps = (a.D + 15) / 16;
+  x.c = a.scale * kLog2e;
+  x.c_cap = a.cap > 0.f ? 2.f * a.scale * kLog2e / a.cap : 0.f;
+  x.cap2 = a.cap * kLog2e;
+  return x;
+}
+
+int form_of(const AttnArgs& a) {
+  return a.cap > 0.f ? 2 : a.slopes != nullptr || !(a.scale > 0.f) ? 1 : 0;
+}
+
+bool strides_fit(const int64_t* s, int64_t B, int64_t T, int64_t H) {
+  const int64_t n[3] = {B, T, H};
+  for (int k = 0; k < 3; ++k)
+    if (n[k] > 1 && (s[k] < 8 || s[k] % 8 != 0 || s[k] >= (int64_t(1) << 38))) return false;
+  return true;
+}
+bool address_fits(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+}  // namespace
+
+// What the tensor copies take: 16-byte boundaries, and a group's heads in a tile.
+bool attention_tc_takes(const AttentionCall& c) {
+  const int64_t G = c.H / c.Hkv;
+  return c.dtype == DPRC_BF16 && c.D % 8 == 0 && G <= kTile && c.Tk > 0 && c.Tq > 0 &&
+         c.Tq <= (int64_t(1) << 16) * (kTile / G) && address_fits(c.Q) && address_fits(c.K) &&
+         address_fits(c.V) && strides_fit(c.qs, c.B, c.Tq, c.H) &&
+         strides_fit(c.ks, c.B, c.Tk, c.Hkv) && strides_fit(c.vs, c.B, c.Tk, c.Hkv) &&
+         c.B * c.Hkv * ((c.Tq + kTile / G - 1) / (kTile / G)) < (int64_t(1) << 31);
+}
+
+bool attention_tc_takes_grad(const AttentionGradCall& c) {
+  return attention_tc_takes(c.f) && address_fits(c.dO) &&
+         strides_fit(c.dos, c.f.B, c.f.Tq, c.f.H);
+}
+
+int attention_tc_rows(const AttentionCall& c) {
+  const int G = static_cast<int>(c.H / c.Hkv), nt = kTile / G;
+  return c.Tq > nt ? 2 * nt * G : nt * G;
+}
+
+cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t s) {
+  const int nt = kTile / a.G, tiles = a.Tq > nt ? 2 : 1, form = form_of(a);
+  const TcArgs x = tc_args(a, tiles);
+  CUtensorMap q, k, v;
+  if (!map_of(&q, a.Q, a.B, a.Tq, a.H, a.D, a.qb, a.qt, a.qh, a.G, nt) ||
+      !map_of(&k, a.K, a.B, a.Tk, a.Hkv, a.D, a.kb, a.kt, a.kh, 1, kTile) ||
+      !map_of(&v, a.V, a.B, a.Tk, a.Hkv, a.D, a.vb, a.vt, a.vh, 1, kTile))
+    return cudaErrorInvalidValue;
+  if (a.D <= 64)
+    return tiles == 2 ? launch_fwd_form<1, 2>(form, q, k, v, x, s)
+                      : launch_fwd_form<1, 1>(form, q, k, v, x, s);
+  return tiles == 2 ? launch_fwd_form<2, 2>(form, q, k, v, x, s)
+                    : launch_fwd_form<2, 1>(form, q, k, v, x, s);
+}
+
+cudaError_t launch_attention_grad_tc(const AttnArgs& a, cudaStream_t s) {
+  return launch_attention_grad_simt(a, DPRC_BF16, s);
+}
+
+cudaError_t read_device_error_attention(int32_t* out, bool reset) {
+  return read_tu_device_error(out, reset);
+}
+
+}  // namespace dprc

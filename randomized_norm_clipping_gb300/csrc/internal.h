@@ -123,6 +123,8 @@ size_t plan_exact_bytes(dprc_dtype dt, int64_t B, int64_t T, int64_t d, int64_t 
 // 3-D bf16 tensor map over [dim2][dim1][dim0] (dim0 contiguous) with row
 // strides in elements, a box of (box0, box1, 1) and the given swizzle bytes
 // (0, 32, 64 or 128).
+bool make_tmap_4d_bf16(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                       const uint64_t (&strides)[3], const uint32_t (&box)[4]);
 bool make_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t dim1,
                        uint64_t dim2, uint64_t stride1_elems, uint64_t stride2_elems,
                        uint32_t box0, uint32_t box1, int swizzle_bytes);
@@ -405,5 +407,72 @@ struct LinearGradCall {
   void *dX = nullptr, *dW = nullptr, *db = nullptr, *dZ = nullptr;
 };
 cudaError_t launch_linear_grad(const LinearGradCall& c, void* ws, cudaStream_t s);
+
+// ---- normalisation (layernorm.cu) --------------------------------------------
+struct LayernormCall {
+  const void *X = nullptr, *weight = nullptr, *bias = nullptr;
+  dprc_dtype dtype = DPRC_BF16;
+  int64_t B = 0, T = 0, d = 0;
+  float eps = 0.f;
+  int center = 1;
+  void* Y = nullptr;
+  float* stats = nullptr;
+};
+cudaError_t launch_layernorm(const LayernormCall& c, cudaStream_t s);
+struct LayernormGradCall {
+  const void *dY = nullptr, *X = nullptr, *weight = nullptr;
+  const float *stats = nullptr, *c = nullptr;
+  dprc_dtype dtype = DPRC_BF16;
+  int64_t B = 0, T = 0, d = 0;
+  int center = 1, norm_of_bias = 0, accumulate = 0;
+  void *dX = nullptr, *dW = nullptr, *db = nullptr;
+  float* n = nullptr;
+};
+size_t layernorm_grad_ws_bytes(int64_t B, int64_t T, int64_t d, int with_norms);
+cudaError_t launch_layernorm_grad(const LayernormGradCall& c, void* ws, cudaStream_t s);
+
+// ---- rotary positions (rotary.cu) --------------------------------------------
+constexpr int kMaxRotAxes = 8;
+struct RotaryCall {
+  const void* X = nullptr;
+  dprc_dtype dtype = DPRC_BF16;
+  int64_t B = 0, T = 0, H = 0, D = 0, pairs = 0;
+  int64_t xs[3] = {0, 0, 0}, os[3] = {0, 0, 0};
+  const void* positions = nullptr;
+  int position_bytes = 8, axes = 1;
+  int64_t sections[kMaxRotAxes] = {};
+  const double* freqs = nullptr;
+  int interleaved = 0, inverse = 0;
+  void* out = nullptr;
+};
+cudaError_t launch_rotary(const RotaryCall& c, cudaStream_t s);
+
+// ---- attention (attention.cu, attention_simt.cu, attention_tc.cu) --------------
+struct AttentionCall {
+  const void *Q = nullptr, *K = nullptr, *V = nullptr;
+  int64_t qs[3] = {}, ks[3] = {}, vs[3] = {};
+  dprc_dtype dtype = DPRC_BF16;
+  int64_t B = 0, Tq = 0, Tk = 0, H = 0, Hkv = 0, D = 0;
+  float scale = 1.f, cap = 0.f;
+  int causal = 1;
+  const float* slopes = nullptr;
+  const int32_t *docs = nullptr, *prefix = nullptr, *lengths = nullptr, *first = nullptr;
+};
+struct AttentionGradCall {
+  AttentionCall f;
+  const void *dO = nullptr, *O = nullptr;
+  const float* lse = nullptr;
+  void *dQ = nullptr, *dK = nullptr, *dV = nullptr;
+  int64_t dos[3] = {}, os[3] = {}, dqs[3] = {}, dks[3] = {}, dvs[3] = {};
+};
+size_t attention_ws_bytes(const AttentionCall& c);
+size_t attention_grad_ws_bytes(const AttentionCall& c);
+cudaError_t launch_attention(const AttentionCall& c, void* out, float* lse, void* ws,
+                             cudaStream_t s);
+cudaError_t launch_attention_grad(const AttentionGradCall& c, void* ws, cudaStream_t s);
+cudaError_t read_device_error_attention(int32_t* out, bool reset);
+cudaError_t read_device_error_attention_simt(int32_t* out, bool reset);
+cudaError_t read_device_error_layernorm(int32_t* out, bool reset);
+cudaError_t read_device_error_rotary(int32_t* out, bool reset);
 
 }  // namespace dprc

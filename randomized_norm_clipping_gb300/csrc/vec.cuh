@@ -1,0 +1,73 @@
+// Loads and stores of the row operators: 16 bytes at a time as fp32 values, or
+// one element, coherent and behind the kernel's wait (launch.cuh).
+#pragma once
+
+#include "common.cuh"
+#include "launch.cuh"
+
+namespace dprc {
+
+// Elements of a 16-byte access.
+template <typename T>
+constexpr int kVec16 = 16 / static_cast<int>(sizeof(T));
+
+// kE elements from p: kVec16<T> of them as one access, or one.
+template <typename T, int kE>
+struct Raw;
+template <>
+struct Raw<float, 4> {
+  float4 a;
+  __device__ __forceinline__ void load(const float* p) {
+    a = ld_once(reinterpret_cast<const float4*>(p));
+  }
+  __device__ __forceinline__ void zero() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+};
+template <>
+struct Raw<__nv_bfloat16, 8> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    a = ld_once(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float* v) const {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(u[e] << 16);
+      v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+    }
+  }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T a;
+  __device__ __forceinline__ void load(const T* p) { a = ld_once(p); }
+  __device__ __forceinline__ void zero() { a = T(0.f); }
+  __device__ __forceinline__ void get(float* v) const { v[0] = to_f32<T>(a); }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int kE>
+__device__ __forceinline__ void store_row(float* p, const float* v) {
+  if constexpr (kE == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *p = v[0];
+}
+template <int kE>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float* v) {
+  if constexpr (kE == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  else
+    *p = __float2bfloat16_rn(v[0]);
+}
+
+}  // namespace dprc
