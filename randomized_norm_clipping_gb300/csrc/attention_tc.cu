@@ -111,6 +111,14 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+// Four values from shared memory, not ahead of what is volatile before it (hoisted, the
+// 64 columns' loads take more registers than a thread has).
+__device__ __forceinline__ void ld_shared4(const float* p, float (&v)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(smem_u32(p)));
+}
+
 // Descriptors of a tile [128][64 kBlocks] at a 1024-byte boundary.  As the operand
 // whose width is summed over (K-major): a step of 16 is 32 bytes, a block of 64 kBlock
 // bytes.  As the operand whose rows are summed over (MN-major): a step is 16 rows.
@@ -216,22 +224,56 @@ __device__ __forceinline__ uint32_t same_docs(int doc, int theirs) {
   return mine;
 }
 
+// Bits of the columns, 32 kWords from key j0 on, that a row sees.
+template <int kWords>
+__device__ __forceinline__ void seen_bits(uint32_t (&bits)[kWords], const RowSees& see,
+                                          const int* docs, int j0, int Tk, bool by_doc) {
+#pragma unroll
+  for (int q = 0; q < kWords; ++q) {
+    bits[q] = first_bits(see.lim - j0 - q * 32);
+    if (by_doc) {
+      const int j = j0 + q * 32 + (threadIdx.x & 31);
+      bits[q] &= same_docs(see.doc, j < Tk ? docs[j] : -2);
+    }
+  }
+}
+
 // -inf in the columns, kN from key j0 on, that a row does not see.
 template <int kN>
 __device__ __forceinline__ void hide(float (&z)[kN], const RowSees& see, const int* docs, int j0,
                                      int Tk, bool by_doc) {
-  const int lane = threadIdx.x & 31;
+  uint32_t bits[kN / 32];
+  seen_bits(bits, see, docs, j0, Tk, by_doc);
 #pragma unroll
-  for (int q = 0; q < kN / 32; ++q) {
-    uint32_t bits = first_bits(see.lim - j0 - q * 32);
-    if (by_doc) {
-      const int j = j0 + q * 32 + lane;
-      bits &= same_docs(see.doc, j < Tk ? docs[j] : -2);
-    }
-#pragma unroll
-    for (int u = 0; u < 32; ++u)
-      if (!((bits >> u) & 1u)) z[q * 32 + u] = -INFINITY;
+  for (int j = 0; j < kN; ++j)
+    if (!((bits[j / 32] >> (j & 31)) & 1u)) z[j] = -INFINITY;
+}
+
+// The softmax's weight of the product z (off: -lse, in units of log2), and in z that
+// weight times the cap's slope 1 - t^2.
+template <int kForm>
+__device__ __forceinline__ float weight(const TcArgs& x, float& z, float slope2, float dist,
+                                        float off) {
+  if constexpr (kForm == 2) {
+    const float t = fmaf(-2.f, rcp(1.f + ex2(z * x.c_cap)), 1.f);
+    const float p = ex2(fmaf(-slope2, dist, fmaf(t, x.cap2, off)));
+    z = p * fmaf(-t, t, 1.f);
+    return p;
+  } else {
+    float s = fmaf(z, x.c, off);
+    if constexpr (kForm == 1) s = fmaf(-slope2, dist, s);
+    z = ex2(s);
+    return z;
   }
+}
+
+// The same of a row's consecutive columns.
+template <int kForm, int kN>
+__device__ __forceinline__ void weights(const TcArgs& x, float (&z)[kN], float slope2, float dist0,
+                                        float off) {
+#pragma unroll
+  for (int j = 0; j < kN; ++j)
+    weight<kForm>(x, z[j], slope2, fabsf(dist0 - static_cast<float>(j)), off);
 }
 
 // What the rows of this warp, of this CTA see, for the choice of tiles and masks.
@@ -646,6 +688,801 @@ cudaError_t launch_fwd_form(int form, const CUtensorMap& q, const CUtensorMap& k
   return launch_fwd<kBlocks, kTiles, 2>(q, k, v, x, s);
 }
 
+// ---------------------------------------------------------------------------
+// Backward.  The eight warps of the softmax share a tile: a thread has a lane and 64 of
+// the 128 columns.  Its weights go back into the first half of the columns that it read
+// (a product's steps of 16 take their operand from there, mma_halves), so no other
+// thread's scores are overwritten.  While the weights' gradient is formed, the tensor
+// core forms the next scores; while those are taken to the exponential, the gradients'
+// products and the next dP.
+// ---------------------------------------------------------------------------
+constexpr int kHalf = kTile / 2;
+
+__device__ __forceinline__ void mma_halves(uint32_t acc, uint32_t a_tmem, uint64_t b,
+                                           uint32_t idesc, bool accumulate) {
+#pragma unroll
+  for (int k = 0; k < kTile / 16; ++k)
+    umma_bf16_ts(acc, a_tmem + (k >> 2) * kHalf + (k & 3) * 8, b + ((k * 2048) >> 4), idesc,
+                 accumulate || k > 0 ? 1u : 0u);
+}
+
+// This thread's 64 columns: ds = w (dp - delta), 0 where `bits` says that the key is not
+// seen (dp may be anything there), as bf16 into the first 32 of them.
+// delta(c, d): those of columns c to c + 3.
+template <typename Delta>
+__device__ __forceinline__ void put_ds(uint32_t taddr, const float (&w)[kHalf], bool masked,
+                                       const uint32_t (&bits)[2], Delta delta) {
+#pragma unroll
+  for (int c0 = 0; c0 < kHalf; c0 += 32) {
+    float dp[32];
+    tmem_ld_32cols(taddr + c0, dp);
+#pragma unroll
+    for (int u = 0; u < 32; u += 4) {
+      float d[4];
+      delta(c0 + u, d);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dp[u + k] = w[c0 + u + k] * (dp[u + k] - d[k]);
+    }
+    if (masked) {
+#pragma unroll
+      for (int u = 0; u < 32; ++u)
+        if (!((bits[c0 / 32] >> u) & 1u)) dp[u] = 0.f;
+    }
+    uint32_t p[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) p[u] = pack_bf16(dp[2 * u], dp[2 * u + 1]);
+    // (columns 0..15 of the half, then 16..31: read before, c0 = 0 holds them)
+    tmem_st_16cols(taddr + c0 / 2, p);
+  }
+}
+
+// Eight values to an address of any alignment of the type.
+__device__ __forceinline__ void store_any(__nv_bfloat16* p, const float* v) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if (at % 16 == 0) {
+    store_row<8>(p, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = __float2bfloat16_rn(v[e]);
+  }
+}
+
+// Rows of a gradient from tensor memory: this thread's lane, every second 16 columns.
+__device__ __forceinline__ void store_grad(__nv_bfloat16* out, bool mine, uint32_t taddr, int half,
+                                           int cols, int D, float scale, bool any) {
+  for (int c = half * 16; c < cols; c += 32) {
+    float o[16];
+    if (any) {
+      tmem_ld_16cols(taddr + c, o);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) o[q] = 0.f;
+    }
+    if (!mine) continue;
+#pragma unroll
+    for (int q = 0; q < 16; q += 8) {
+      if (c + q >= D) continue;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) o[q + u] *= scale;
+      store_any(out + c + q, o + q);
+    }
+  }
+}
+
+template <int kBlocks>
+struct DqCfg {
+  static constexpr int kSlot = kBlocks * kBlock;
+  static constexpr int kStages = kBlocks == 1 ? 8 : 4;
+  static constexpr int kSmem = (2 + kStages) * kSlot + 1024 + 1024 + kMaxKeyTiles / 8;
+  static constexpr int kS = 0, kDp = 128, kAcc = 256;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
+
+template <int kBlocks, int kForm>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q,
+                           const __grid_constant__ CUtensorMap map_o,
+                           const __grid_constant__ CUtensorMap map_k,
+                           const __grid_constant__ CUtensorMap map_v, const TcArgs x) {
+  using Cfg = DqCfg<kBlocks>;
+  constexpr int kStages = Cfg::kStages;
+  const AttnArgs& a = x.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* qs = align_1024(smem_raw);
+  uint8_t* os = qs + Cfg::kSlot;
+  uint8_t* ring = os + Cfg::kSlot;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * Cfg::kSlot);
+  uint64_t* empty = full + kStages;
+  uint64_t* qfull = empty + kStages;
+  uint64_t* sfull = qfull + 1;
+  uint64_t* sread = sfull + 1;
+  uint64_t* dpfull = sread + 1;
+  uint64_t* dsfull = dpfull + 1;
+  uint64_t* ofull = dsfull + 1;
+  uint64_t* drain = ofull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* ext = reinterpret_cast<int*>(tmem_slot + 2);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(ring + kStages * Cfg::kSlot + 512);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bhs = a.B * a.Hkv;
+  const int bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  const int grp = x.groups - 1 - blockIdx.x / bhs;  // the longest rows first
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(sfull, 1);
+    mbar_init(sread, kWarps);
+    mbar_init(dpfull, 1);
+    mbar_init(dsfull, kWarps);
+    mbar_init(ofull, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+    ext[0] = 0;
+    ext[1] = 0x7fffffff;
+    ext[2] = -1;
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_o);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  if (warp == kWarps + 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int keys = attn_keys(a, b), first = attn_first(a, b);
+  const int r = threadIdx.x & (kTile - 1), half = warp >> 2;
+  const int tt = r / a.G, tok = grp * x.nt + tt;
+  const bool mine = warp < kWarps && tt < x.nt && tok < a.Tq;
+  RowSees see = {0, 0, -1};
+  Extent e = {};
+  if (warp < kWarps) {
+    if (mine) see = attn_row(a, b, tok, keys, first);
+    e = warp_extent(mine, see, a.docs != nullptr);
+    if (lane == 0) {
+      atomicMax(&ext[0], e.max_lim);
+      atomicMin(&ext[1], e.lo);
+      atomicMax(&ext[2], e.hi);
+    }
+  }
+  __syncthreads();
+  const int top = ext[0], t1 = (top + kTile - 1) / kTile, words = (t1 + 31) / 32;
+  key_tile_bits(a, b, 0, t1, ext[1], ext[2], bits, words);
+  __syncthreads();
+
+  if (warp >= kWarps) {
+    if (warp == kWarps && lane == 0) {
+      Bits it(bits, words);
+      Pos pos;
+      int j = it.next(), issued = 0;
+      const bool any = j >= 0;
+      bool ok = true;
+      if (any) {
+        mbar_arrive_expect_tx(qfull, 2 * kBlocks * x.nt * a.G * 128);
+#pragma unroll
+        for (int q = 0; q < kBlocks; ++q) {
+          tma_load_4d(qs + q * kBlock, &map_q, qfull, q * 64, hk * a.G, grp * x.nt, b);
+          tma_load_4d(os + q * kBlock, &map_o, qfull, q * 64, hk * a.G, grp * x.nt, b);
+        }
+      }
+      for (; j >= 0 && ok; j = it.next()) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!wait_bar(&empty[pos.s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[pos.s], Cfg::kSlot);
+#pragma unroll
+          for (int q = 0; q < kBlocks; ++q)
+            tma_load_4d(ring + pos.s * Cfg::kSlot + q * kBlock, kv == 0 ? &map_k : &map_v,
+                        &full[pos.s], q * 64, hk, j * kTile, b);
+          ++issued;
+          pos.next(kStages);
+        }
+      }
+      if (any) mbar_wait(qfull, 0, DPRC_DEVERR_PIPE_FULL);
+      for (int k = issued - 1; k >= 0 && k >= issued - kStages; --k)
+        mbar_wait(&full[k % kStages], (k / kStages) & 1, DPRC_DEVERR_PIPE_FULL);
+    } else if (warp == kWarps + 1 && lane == 0) {
+      Bits it(bits, words);
+      const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
+      const uint32_t id_g = make_idesc_bf16(kTile, x.steps * 16, false, true);
+      const uint64_t dq = desc_k(smem_u32(qs)), dO = desc_k(smem_u32(os));
+      const uint64_t dk = desc_k(smem_u32(ring)), dkm = desc_mn(smem_u32(ring));
+      Pos pos;
+      int j = it.next(), n = 0;
+      bool ok = j >= 0, issued = false;
+      const auto filled = [&](const Pos& p) {
+        const bool f = wait_bar(&full[p.s], p.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        tc_fence_after();
+        return f;
+      };
+      const auto scores_of = [&](const Pos& p) {
+        mma_width(tmem + Cfg::kS, dq, dk + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
+        umma_commit(sfull);
+      };
+      const auto dp_of = [&](const Pos& p) {
+        mma_width(tmem + Cfg::kDp, dO, dk + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
+        umma_commit(dpfull);
+        umma_commit(&empty[p.s]);
+      };
+      Pos kp = pos;
+      pos.next(kStages);
+      Pos vp = pos;
+      pos.next(kStages);
+      ok = ok && wait_bar(qfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) && filled(kp);
+      if (ok) {
+        issued = true;
+        scores_of(kp);
+        ok = filled(vp);
+        if (ok) dp_of(vp);
+      }
+      while (ok && j >= 0) {
+        j = it.next();
+        Pos kn = kp, vn = vp;
+        if (j >= 0) {
+          kn = pos;
+          pos.next(kStages);
+          vn = pos;
+          pos.next(kStages);
+          ok = filled(kn) && wait_bar(sread, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          scores_of(kn);
+        }
+        ok = wait_bar(dsfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        mma_halves(tmem + Cfg::kAcc, tmem + Cfg::kDp, dkm + ((kp.s * Cfg::kSlot) >> 4), id_g, n > 0);
+        umma_commit(&empty[kp.s]);
+        if (j >= 0) {
+          ok = filled(vn);
+          if (ok) dp_of(vn);
+        } else {
+          umma_commit(ofull);
+        }
+        kp = kn;
+        vp = vn;
+        ++n;
+      }
+      if (issued) umma_drain(drain, kWaitLimitNs);
+    }
+  } else {
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + Cfg::kS + half * kHalf;
+    const uint32_t td = tmem + lanes + Cfg::kDp + half * kHalf;
+    const int h = hk * a.G + r - tt * a.G;
+    const long long at = (static_cast<long long>(b) * a.H + h) * a.Tq + tok;
+    const float slope2 = kForm > 0 && a.slopes != nullptr && mine ? a.slopes[h] * kLog2e : 0.f;
+    const float lse = mine ? a.lse_in[at] : 0.f, delta = mine ? a.delta[at] : 0.f;
+    const float off = lse == -INFINITY ? 0.f : -lse * kLog2e;
+    const int* docs = a.docs != nullptr ? a.docs + static_cast<long long>(b) * a.Tk : nullptr;
+    Bits it(bits, words);
+    Pos kpos;
+    int n = 0;
+    bool ok = true;
+    for (int j = it.next(); j >= 0; j = it.next(), ++n) {
+      ok = wait_warp(sfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const int j0 = j * kTile, jh = j0 + half * kHalf;
+      bool dirty = j0 + kTile > top, by_doc = false;
+      if (docs != nullptr) {
+        const DocSpan s = key_tile_docs(a, b, j);
+        by_doc = s.pad || s.lo != s.hi || e.lo != s.lo || e.hi != s.lo;
+        dirty = dirty || s.pad;
+      }
+      float z[kHalf];
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 32) {
+        float part[32];
+        tmem_ld_32cols(ts + c, part);
+#pragma unroll
+        for (int u = 0; u < 32; ++u) z[c + u] = part[u];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sread);
+      uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+      const bool masked = jh + kHalf > e.min_lim || by_doc;
+      if (masked) seen_bits(seen, see, docs, jh, a.Tk, by_doc);
+      weights<kForm>(x, z, slope2, static_cast<float>(see.pos - jh), off);
+      if (dirty && half == 0) {
+        // keys that no row of the CTA sees may be anything, and 0 times NaN is NaN
+        ok = wait_warp(&full[kpos.s], kpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        if (!ok) break;
+        const int key = j0 + r;
+        if (key >= top || (docs != nullptr && docs[key] < 0))
+          zero_row<kBlocks>(ring + kpos.s * Cfg::kSlot, r);
+        fence_proxy_async_smem();
+      }
+      kpos.next(kStages);
+      kpos.next(kStages);
+      ok = wait_warp(dpfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      put_ds(td, z, masked, seen, [&](int, float (&d)[4]) { d[0] = d[1] = d[2] = d[3] = delta; });
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dsfull);
+    }
+    if (n > 0 && ok) ok = wait_warp(ofull, 0, DPRC_DEVERR_ACCUM, abort_flag);
+    tc_fence_after();
+    if (ok)
+      store_grad(static_cast<__nv_bfloat16*>(a.dQ) + b * a.dqb + tok * a.dqt + h * a.dqh, mine,
+                 tmem + lanes + Cfg::kAcc, half, x.steps * 16, a.D, a.scale, n > 0);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// What the keys' kernel reads of a tile's rows, two tiles in turn.
+struct RowStage {
+  float off[kTile];    // -lse log2(e)
+  float delta[kTile];
+  float slope2[kTile];
+  float pos[kTile];    // against the first key of the tile
+  int lim[kTile];
+  int doc[kTile];
+  int min_lim, lo, hi, dirty;
+};
+constexpr int kMaxRowTiles = 1 << 16;
+
+template <int kBlocks>
+struct DkvCfg {
+  static constexpr int kSlot = kBlocks * kBlock;
+  static constexpr int kStages = kBlocks == 1 ? 6 : 4;
+  static constexpr int kBits = kMaxRowTiles / 8;
+  static constexpr int kSmem =
+      (2 + kStages) * kSlot + 1024 + 512 + kBits + 2 * static_cast<int>(sizeof(RowStage));
+  static constexpr int kS = 0, kDp = 128, kDv = 256, kDk = 384;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
+
+template <int kBlocks, int kForm>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_dkv_tc_kernel(const __grid_constant__ CUtensorMap map_q,
+                            const __grid_constant__ CUtensorMap map_o,
+                            const __grid_constant__ CUtensorMap map_k,
+                            const __grid_constant__ CUtensorMap map_v, const TcArgs x) {
+  using Cfg = DkvCfg<kBlocks>;
+  constexpr int kStages = Cfg::kStages;
+  const AttnArgs& a = x.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ks = align_1024(smem_raw);
+  uint8_t* vs = ks + Cfg::kSlot;
+  uint8_t* ring = vs + Cfg::kSlot;
+  uint8_t* rest = ring + kStages * Cfg::kSlot;
+  uint64_t* full = reinterpret_cast<uint64_t*>(rest);
+  uint64_t* empty = full + kStages;
+  uint64_t* kvfull = empty + kStages;
+  uint64_t* sfull = kvfull + 1;
+  uint64_t* pfull = sfull + 1;
+  uint64_t* dpfull = pfull + 1;
+  uint64_t* dsfull = dpfull + 1;
+  uint64_t* rfull = dsfull + 1;   // [2]
+  uint64_t* rempty = rfull + 2;   // [2]
+  uint64_t* ofull = rempty + 2;
+  uint64_t* drain = ofull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(rest + 512);
+  RowStage* stages = reinterpret_cast<RowStage*>(rest + 512 + Cfg::kBits);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bhs = a.B * a.Hkv;
+  const int bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  const int jt = blockIdx.x / bhs, j0 = jt * kTile;  // (the first keys have the most rows)
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(kvfull, 1);
+    mbar_init(sfull, 1);
+    mbar_init(pfull, kWarps);
+    mbar_init(dpfull, 1);
+    mbar_init(dsfull, kWarps);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&rfull[s], 1);
+      mbar_init(&rempty[s], kWarps);
+    }
+    mbar_init(ofull, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_o);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  if (warp == kWarps + 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  // rows of a slot behind the last whole token are never copied: zero, as they are
+  // summed over
+  const int tail = x.nt * a.G;
+  for (int i = threadIdx.x; i < kStages * (kTile - tail); i += kThreads)
+    zero_row<kBlocks>(ring + (i / (kTile - tail)) * Cfg::kSlot, tail + i % (kTile - tail));
+  if (tail < kTile) fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int keys = attn_keys(a, b), first = attn_first(a, b);
+  // tiles of rows that may see a key of this tile
+  DocSpan kd = {0, 0, 0, 0};
+  if (a.docs != nullptr) kd = key_tile_docs(a, b, jt);
+  const int words = j0 < keys ? (x.row_tiles + 31) / 32 : 0;
+  for (int w = warp; w < words; w += kThreads / 32) {
+    const int i = w * 32 + lane, tok0 = i * x.nt;
+    bool ok = tok0 < a.Tq;
+    if (ok) {
+      const int tok1 = min(tok0 + x.nt, a.Tq) - 1;
+      if (a.causal) {
+        int see = first + tok1 + 1;
+        if (a.prefix != nullptr) see = max(see, a.prefix[b]);
+        ok = see > j0;
+      }
+      if (a.docs != nullptr) {
+        const int spans = (a.Tk + kDocSpan - 1) / kDocSpan;
+        const int p0 = max(0, first + tok0), p1 = min(a.Tk - 1, first + tok1);
+        bool meets = false;
+        for (int q = p0 / kDocSpan; p0 <= p1 && q <= p1 / kDocSpan; ++q) {
+          const DocSpan s = a.spans[static_cast<long long>(b) * spans + q];
+          meets = meets || (s.lo <= kd.hi && kd.lo <= s.hi);
+        }
+        ok = ok && meets;
+      }
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) bits[w] = m;
+  }
+  __syncthreads();
+
+  if (warp >= kWarps) {
+    if (warp == kWarps && lane == 0) {
+      Bits it(bits, words);
+      Pos pos;
+      int i = it.next(), issued = 0;
+      const bool any = i >= 0;
+      bool ok = true;
+      if (any) {
+        mbar_arrive_expect_tx(kvfull, 2 * Cfg::kSlot);
+#pragma unroll
+        for (int q = 0; q < kBlocks; ++q) {
+          tma_load_4d(ks + q * kBlock, &map_k, kvfull, q * 64, hk, j0, b);
+          tma_load_4d(vs + q * kBlock, &map_v, kvfull, q * 64, hk, j0, b);
+        }
+      }
+      for (; i >= 0 && ok; i = it.next()) {
+#pragma unroll
+        for (int qo = 0; qo < 2; ++qo) {
+          if (!wait_bar(&empty[pos.s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[pos.s], kBlocks * x.nt * a.G * 128);
+#pragma unroll
+          for (int q = 0; q < kBlocks; ++q)
+            tma_load_4d(ring + pos.s * Cfg::kSlot + q * kBlock, qo == 0 ? &map_q : &map_o,
+                        &full[pos.s], q * 64, hk * a.G, i * x.nt, b);
+          ++issued;
+          pos.next(kStages);
+        }
+      }
+      if (any) mbar_wait(kvfull, 0, DPRC_DEVERR_PIPE_FULL);
+      for (int k = issued - 1; k >= 0 && k >= issued - kStages; --k)
+        mbar_wait(&full[k % kStages], (k / kStages) & 1, DPRC_DEVERR_PIPE_FULL);
+    } else if (warp == kWarps + 1 && lane == 0) {
+      Bits it(bits, words);
+      const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
+      const uint32_t id_g = make_idesc_bf16(kTile, x.steps * 16, false, true);
+      const uint64_t dk = desc_k(smem_u32(ks)), dv = desc_k(smem_u32(vs));
+      const uint64_t dr = desc_k(smem_u32(ring)), drm = desc_mn(smem_u32(ring));
+      Pos pos;
+      int i = it.next(), n = 0;
+      bool ok = i >= 0, issued = false;
+      const auto filled = [&](const Pos& p) {
+        const bool f = wait_bar(&full[p.s], p.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        tc_fence_after();
+        return f;
+      };
+      const auto scores_of = [&](const Pos& p) {
+        mma_width(tmem + Cfg::kS, dk, dr + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
+        umma_commit(sfull);
+      };
+      const auto dp_of = [&](const Pos& p) {
+        mma_width(tmem + Cfg::kDp, dv, dr + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
+        umma_commit(dpfull);
+      };
+      Pos qp = pos;
+      pos.next(kStages);
+      Pos op = pos;
+      pos.next(kStages);
+      ok = ok && wait_bar(kvfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) && filled(qp);
+      if (ok) {
+        issued = true;
+        scores_of(qp);
+        ok = filled(op);
+        if (ok) dp_of(op);
+      }
+      while (ok && i >= 0) {
+        i = it.next();
+        Pos qn = qp, on = op;
+        ok = wait_bar(pfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        mma_halves(tmem + Cfg::kDv, tmem + Cfg::kS, drm + ((op.s * Cfg::kSlot) >> 4), id_g, n > 0);
+        umma_commit(&empty[op.s]);
+        if (i >= 0) {
+          qn = pos;
+          pos.next(kStages);
+          on = pos;
+          pos.next(kStages);
+          ok = filled(qn);
+          if (!ok) break;
+          scores_of(qn);
+        }
+        ok = wait_bar(dsfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        mma_halves(tmem + Cfg::kDk, tmem + Cfg::kDp, drm + ((qp.s * Cfg::kSlot) >> 4), id_g, n > 0);
+        umma_commit(&empty[qp.s]);
+        if (i >= 0) {
+          ok = filled(on);
+          if (ok) dp_of(on);
+        } else {
+          umma_commit(ofull);
+        }
+        qp = qn;
+        op = on;
+        ++n;
+      }
+      if (issued) umma_drain(drain, kWaitLimitNs);
+    } else if (warp == kWarps + 2) {
+      // what the rows see, their statistics and where they stand
+      Bits it(bits, words);
+      int n = 0;
+      // Rows that are none stand as zeros, and their weights are of no account, unless
+      // the tile has keys that nobody sees: those may be anything, and NaN times 0 is NaN.
+      int all = keys;
+      if (a.causal) {
+        all = min(keys, first + a.Tq);
+        if (a.prefix != nullptr) all = max(all, min(keys, a.prefix[b]));
+      }
+      const int none = kd.pad || j0 + kTile > all ? 0 : 0x7fffffff;
+      for (int i = it.next(); i >= 0; i = it.next(), ++n) {
+        RowStage& st = stages[n & 1];
+        if (!wait_warp(&rempty[n & 1], ((n >> 1) & 1) ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) break;
+        int min_lim = 0x7fffffff, lo = 0x7fffffff, hi = -1, dirty = 0;
+#pragma unroll
+        for (int q = 0; q < kTile; q += 32) {
+          const int r = q + lane, tt = r / a.G, tok = i * x.nt + tt, h = hk * a.G + r - tt * a.G;
+          RowSees see = {0, none, -3};
+          float lse = 0.f, del = 0.f, slope = 0.f;
+          if (tt < x.nt && tok < a.Tq) {
+            see = attn_row(a, b, tok, keys, first);
+            const long long at = (static_cast<long long>(b) * a.H + h) * a.Tq + tok;
+            lse = a.lse_in[at];
+            del = a.delta[at];
+            if (kForm > 0 && a.slopes != nullptr) slope = a.slopes[h] * kLog2e;
+            if (see.doc >= 0) {
+              lo = min(lo, see.doc);
+              hi = max(hi, see.doc);
+            }
+            dirty |= see.lim == 0;
+          }
+          min_lim = min(min_lim, see.lim);
+          st.off[r] = lse == -INFINITY ? 0.f : -lse * kLog2e;
+          st.delta[r] = del;
+          st.slope2[r] = slope;
+          st.pos[r] = static_cast<float>(see.pos - j0);
+          st.lim[r] = see.lim;
+          st.doc[r] = see.doc;
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+          min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, o));
+          lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+          dirty |= __shfl_xor_sync(0xffffffffu, dirty, o);
+        }
+        if (lane == 0) {
+          st.min_lim = min_lim;
+          st.lo = lo;
+          st.hi = hi;
+          st.dirty = dirty;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rfull[n & 1]);
+      }
+    }
+  } else {
+    const int r = threadIdx.x & (kTile - 1), half = warp >> 2, key = j0 + r;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + Cfg::kS + half * kHalf;
+    const uint32_t td = tmem + lanes + Cfg::kDp + half * kHalf;
+    const float keyf = static_cast<float>(r);
+    const int kdoc =
+        a.docs != nullptr ? (key < a.Tk ? a.docs[static_cast<long long>(b) * a.Tk + key] : -2) : 0;
+    const int kdoc0 = __shfl_sync(0xffffffffu, kdoc, 0);
+    const bool one_doc = __all_sync(0xffffffffu, kdoc == kdoc0);
+    const int last_key = j0 + (warp & 3) * 32 + 31;
+    Bits it(bits, words);
+    Pos pos;
+    int n = 0;
+    bool ok = true;
+    for (int i = it.next(); i >= 0; i = it.next(), ++n) {
+      const RowStage& st = stages[n & 1];
+      const int c0 = half * kHalf;
+      ok = wait_warp(&rfull[n & 1], (n >> 1) & 1, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
+           wait_warp(sfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      float z[kHalf];
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 32) {
+        float part[32];
+        tmem_ld_32cols(ts + c, part);
+#pragma unroll
+        for (int u = 0; u < 32; ++u) z[c + u] = part[u];
+      }
+      const bool by_doc =
+          a.docs != nullptr && (!one_doc || st.lo != kdoc0 || st.hi != kdoc0);
+      const bool masked = last_key >= st.min_lim || by_doc;
+      uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+      if (masked) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t m = 0u;
+#pragma unroll 1
+          for (int u = 0; u < 32; u += 4) {
+            const int4 l = *reinterpret_cast<const int4*>(&st.lim[c0 + q * 32 + u]);
+            m |= (key < l.x ? 1u << u : 0u) | (key < l.y ? 2u << u : 0u) |
+                 (key < l.z ? 4u << u : 0u) | (key < l.w ? 8u << u : 0u);
+          }
+          if (by_doc) m &= same_docs(kdoc, st.doc[c0 + q * 32 + lane]);
+          seen[q] = m;
+        }
+      }
+      // P into the scores' place; z becomes P (1 - t^2)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t p[16];
+#pragma unroll
+        for (int u = 0; u < 32; u += 4) {
+          const int c = q * 32 + u;
+          float of[4], sl[4] = {0.f, 0.f, 0.f, 0.f}, ps[4] = {0.f, 0.f, 0.f, 0.f};
+          ld_shared4(&st.off[c0 + c], of);
+          if constexpr (kForm > 0) {
+            ld_shared4(&st.slope2[c0 + c], sl);
+            ld_shared4(&st.pos[c0 + c], ps);
+          }
+          float w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w[k] = weight<kForm>(x, z[c + k], sl[k], fabsf(ps[k] - keyf), of[k]);
+            if (masked && !((seen[q] >> (u + k)) & 1u)) w[k] = z[c + k] = 0.f;
+          }
+          p[u / 2] = pack_bf16(w[0], w[1]);
+          p[u / 2 + 1] = pack_bf16(w[2], w[3]);
+        }
+        tmem_st_16cols(ts + q * 16, p);
+      }
+      tmem_st_wait();
+      if (st.dirty) {
+        // rows that see nothing may be anything, and 0 times NaN is NaN: their queries
+        // and gradients are summed over (dP, which reads them too, is complete)
+        ok = wait_warp(dpfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (half == 0) {
+          Pos op = pos;
+          op.next(kStages);
+          ok = wait_warp(&full[pos.s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
+               wait_warp(&full[op.s], op.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+          if (!ok) break;
+          if (st.lim[r] == 0) {
+            zero_row<kBlocks>(ring + pos.s * Cfg::kSlot, r);
+            zero_row<kBlocks>(ring + op.s * Cfg::kSlot, r);
+          }
+          fence_proxy_async_smem();
+        }
+      }
+      pos.next(kStages);
+      pos.next(kStages);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pfull);
+      ok = wait_warp(dpfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      put_ds(td, z, masked, seen, [&](int c, float (&d)[4]) { ld_shared4(&st.delta[c0 + c], d); });
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(dsfull);
+        mbar_arrive(&rempty[n & 1]);
+      }
+    }
+    if (n > 0 && ok) ok = wait_warp(ofull, 0, DPRC_DEVERR_ACCUM, abort_flag);
+    tc_fence_after();
+    if (ok) {
+      const bool mine = key < a.Tk;
+      const int cols = x.steps * 16;
+      if (a.dV != nullptr)
+        store_grad(static_cast<__nv_bfloat16*>(a.dV) + b * a.dvb + key * a.dvt + hk * a.dvh, mine,
+                   tmem + lanes + Cfg::kDv, half, cols, a.D, 1.f, n > 0);
+      if (a.dK != nullptr)
+        store_grad(static_cast<__nv_bfloat16*>(a.dK) + b * a.dkb + key * a.dkt + hk * a.dkh, mine,
+                   tmem + lanes + Cfg::kDk, half, cols, a.D, a.scale, n > 0);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+struct GradMaps {
+  CUtensorMap q, o, k, v;
+};
+
+template <int kBlocks, int kForm>
+cudaError_t launch_grad(const GradMaps& m, const TcArgs& x, cudaStream_t s) {
+  const int bhs = x.a.B * x.a.Hkv;
+  cudaError_t e = cudaSuccess;
+  if (x.a.dQ != nullptr) {
+    constexpr int bytes = DqCfg<kBlocks>::kSmem;
+    e = allow_smem<attention_dq_tc_kernel<kBlocks, kForm>>(bytes);
+    if (e != cudaSuccess) return e;
+    e = launch_after(attention_dq_tc_kernel<kBlocks, kForm>, dim3(bhs * x.groups), kThreads, 1, s,
+                     bytes, m.q, m.o, m.k, m.v, x);
+    if (e != cudaSuccess) return e;
+  }
+  if (x.a.dK == nullptr && x.a.dV == nullptr) return e;
+  constexpr int bytes = DkvCfg<kBlocks>::kSmem;
+  e = allow_smem<attention_dkv_tc_kernel<kBlocks, kForm>>(bytes);
+  if (e != cudaSuccess) return e;
+  return launch_after(attention_dkv_tc_kernel<kBlocks, kForm>,
+                      dim3(bhs * ((x.a.Tk + kTile - 1) / kTile)), kThreads, 1, s, bytes, m.q, m.o,
+                      m.k, m.v, x);
+}
+
+template <int kBlocks>
+cudaError_t launch_grad_form(int form, const GradMaps& m, const TcArgs& x, cudaStream_t s) {
+  if (form == 0) return launch_grad<kBlocks, 0>(m, x, s);
+  if (form == 1) return launch_grad<kBlocks, 1>(m, x, s);
+  return launch_grad<kBlocks, 2>(m, x, s);
+}
+
 // A tensor [B][T][H][D] as boxes of 64 of the width, `heads` heads and `tokens` tokens.
 bool map_of(CUtensorMap* m, const void* p, long long B, long long T, long long H, long long D,
             long long sb, long long st, long long sh, int heads, int tokens) {
@@ -722,7 +1559,15 @@ cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_attention_grad_tc(const AttnArgs& a, cudaStream_t s) {
-  return launch_attention_grad_simt(a, DPRC_BF16, s);
+  const TcArgs x = tc_args(a, 1);
+  GradMaps m;
+  if (!map_of(&m.q, a.Q, a.B, a.Tq, a.H, a.D, a.qb, a.qt, a.qh, a.G, x.nt) ||
+      !map_of(&m.o, a.dO, a.B, a.Tq, a.H, a.D, a.dob, a.dot, a.doh, a.G, x.nt) ||
+      !map_of(&m.k, a.K, a.B, a.Tk, a.Hkv, a.D, a.kb, a.kt, a.kh, 1, kTile) ||
+      !map_of(&m.v, a.V, a.B, a.Tk, a.Hkv, a.D, a.vb, a.vt, a.vh, 1, kTile))
+    return cudaErrorInvalidValue;
+  const int form = form_of(a);
+  return a.D <= 64 ? launch_grad_form<1>(form, m, x, s) : launch_grad_form<2>(form, m, x, s);
 }
 
 cudaError_t read_device_error_attention(int32_t* out, bool reset) {
