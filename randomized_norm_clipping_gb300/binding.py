@@ -855,7 +855,7 @@ def _head_strides(name, t):
 def _on_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
+            raise ValueError("libdprc takes device tensors")
 
 
 def dprc_rotary(X, positions, freqs, sections=None, interleaved=False, inverse=False, out=None,

@@ -1,10 +1,11 @@
 """torch.nn modules over the operators around the norm path.
 
-`Embedding`, `Linear` (bias, activation, dropout and residual in one call) and
-`Dropout` run on libdprc (dprc_embed_*, dprc_linear*, dprc_dropout) in both
-directions, and `RandomizedClippingStep` takes their parameters: the embedding
-and the biases by their exact per-sample norms, the linear weights by the
-estimates.  Device tensors of float32 or bfloat16 only; the library raises on
+`Embedding`, `Linear` (bias, activation, dropout and residual in one call),
+`Dropout`, `LayerNorm` (also its RMS form) and `Attention` (with rotary positions)
+run on libdprc (dprc_embed_*, dprc_linear*, dprc_dropout, dprc_layernorm*,
+dprc_rotary, dprc_attention*) in both directions, and `RandomizedClippingStep` takes
+their parameters: the embedding, the biases and the normalisations by their exact
+per-sample norms, the linear weights by the estimates.  Device tensors of float32 or bfloat16 only; the library raises on
 anything else.  Gradients can be taken once; a gradient of a gradient raises.
 
 Dropout masks come from the library's Philox stream under (seed, step): `seed`
@@ -248,3 +249,207 @@ class Linear(_Masked):
         g = torch.empty_like(dy)
         rnc.dprc_linear_grad(dy, None, _dense(self.weight), Z=z, dZ=g, **args)
         return g
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, module, keep):
+        x, w = _dense(x), _dense(weight)
+        stats = None
+        if keep:
+            stats = torch.empty((*x.shape[:-1], 2), dtype=torch.float32, device=x.device)
+        ctx.save_for_backward(x, w, stats)
+        ctx.module, ctx.center = module, module.center
+        if not _in_backward():  # (a repeated pass has its place already)
+            module._last = stats
+        return rnc.dprc_layernorm(x, w, _dense(bias), eps=module.eps, center=module.center,
+                                  stats=stats)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        x, w, stats = ctx.saved_tensors
+        if ctx.module._last is stats:  # kept by the graph alone from here on
+            ctx.module._last = None
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        if ctx.module.norm_pass:  # the clipping step's first backward: no parameter gradients
+            need_w = need_b = False
+        grad = _dense(grad)
+        dx = torch.empty_like(x) if need_x else None
+        dw = torch.empty(x.shape[-1], dtype=x.dtype, device=x.device) if need_w else None
+        db = torch.empty(x.shape[-1], dtype=x.dtype, device=x.device) if need_b else None
+        if need_x or need_w or need_b:
+            rnc.dprc_layernorm_grad(grad, x, stats, w, center=ctx.center, dX=dx, dW=dw, db=db)
+        return dx, dw, db, None, None
+
+
+class LayerNorm(torch.nn.Module):
+    """Layer normalisation of the last axis, or with center=False RMS normalisation."""
+
+    def __init__(self, width, eps=1e-5, center=True, weight=True, bias=True, device=None,
+                 dtype=None):
+        super().__init__()
+        self.width, self.eps, self.center = int(width), float(eps), bool(center)
+        self.norm_pass = False
+        self._last = None
+        new = lambda f: torch.nn.Parameter(f(width, device=device, dtype=dtype))  # noqa: E731
+        self.weight = new(torch.ones) if weight else None
+        self.bias = new(torch.zeros) if bias else None
+
+    def forward(self, x):
+        return _LayerNorm.apply(x, self.weight, self.bias, self, torch.is_grad_enabled())
+
+
+def _heads(t):
+    """t as the library takes [B][T][H][D]: any strides, a head's elements together."""
+    t = t.detach()
+    return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, positions, freqs, sections, interleaved):
+        ctx.save_for_backward(positions, freqs)
+        ctx.args = dict(sections=sections, interleaved=interleaved)
+        return rnc.dprc_rotary(_heads(x), positions, freqs, **ctx.args)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        positions, freqs = ctx.saved_tensors
+        dx = rnc.dprc_rotary(_heads(grad), positions, freqs, inverse=True, **ctx.args)
+        return dx, None, None, None, None
+
+
+def rotary(x, positions, freqs, sections=None, interleaved=False):
+    """dprc_rotary with its gradient (by x)."""
+    return _Rotary.apply(x, _dense(positions), _dense(freqs), sections, interleaved)
+
+
+def rotary_freqs(pairs, base=10000.0, sections=None):
+    """base^(-p / n) for the pairs p of each section of n (one of them all, if none given)."""
+    return torch.cat([base ** (-torch.arange(n, dtype=torch.float64) / max(n, 1))
+                      for n in (sections or [pairs])])
+
+
+def _plain(mask):
+    """The arguments of a mask, dense; the library's types are the caller's to give."""
+    for name, t in mask.items():
+        if isinstance(t, torch.Tensor):
+            if t.requires_grad:
+                raise ValueError(f"{name} has no gradient here")
+            mask[name] = _dense(t)
+    return mask
+
+
+class _Attend(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, args, keep):
+        q, k, v = _heads(q), _heads(k), _heads(v)
+        lse = None
+        if keep:
+            lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
+                              device=q.device)
+        out = rnc.dprc_attention(q, k, v, lse=lse, **args)
+        ctx.save_for_backward(q, k, v, out, lse)
+        ctx.args = args
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        q, k, v, out, lse = ctx.saved_tensors
+        d = [torch.empty(t.shape, dtype=t.dtype, device=t.device) if need else None
+             for t, need in zip((q, k, v), ctx.needs_input_grad)]
+        if any(t is not None for t in d):
+            rnc.dprc_attention_grad(_heads(grad), q, k, v, out, lse, dQ=d[0], dK=d[1], dV=d[2],
+                                    **ctx.args)
+        return *d, None, None
+
+
+def attend(q, k, v, scale=None, causal=True, cap=0.0, slopes=None, docs=None, prefix=None,
+           lengths=None, first=None):
+    """dprc_attention of q [B][Tq][H][D] over k, v [B][Tk][Hkv][D], with its gradient."""
+    args = _plain(dict(scale=scale, causal=causal, cap=cap, slopes=slopes, docs=docs,
+                       prefix=prefix, lengths=lengths, first=first))
+    return _Attend.apply(q, k, v, args, torch.is_grad_enabled())
+
+
+class _SelfAttend(torch.autograd.Function):
+    """Attention from the rows [q | k | v] of one product, with rotary positions: the
+    gradient is written in place into rows of the same form."""
+
+    @staticmethod
+    def forward(ctx, rows, positions, freqs, heads, turn, args, keep):
+        H, Hkv, D = heads
+        B, T, _ = rows.shape
+        rows = _dense(rows).view(B, T, H + 2 * Hkv, D)
+        qk, v = rows[:, :, :H + Hkv], rows[:, :, H + Hkv:]
+        if freqs is not None:
+            qk = rnc.dprc_rotary(qk, positions, freqs, **turn)
+        q, k = qk[:, :, :H], qk[:, :, H:]
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=rows.device) if keep else None
+        out = rnc.dprc_attention(q, k, v, lse=lse, **args)
+        ctx.save_for_backward(q, k, v, out, lse, positions, freqs)
+        ctx.heads, ctx.turn, ctx.args = heads, turn, args
+        return out.view(B, T, H * D)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        q, k, v, out, lse, positions, freqs = ctx.saved_tensors
+        H, Hkv, D = ctx.heads
+        B, T = q.shape[:2]
+        d = torch.empty((B, T, H + 2 * Hkv, D), dtype=q.dtype, device=q.device)
+        dqk = d[:, :, :H + Hkv]
+        rnc.dprc_attention_grad(_dense(grad).view(B, T, H, D), q, k, v, out, lse, dQ=d[:, :, :H],
+                                dK=dqk[:, :, H:], dV=d[:, :, H + Hkv:], **ctx.args)
+        if freqs is not None:
+            rnc.dprc_rotary(dqk, positions, freqs, inverse=True, out=dqk, **ctx.turn)
+        return d.view(B, T, -1), None, None, None, None, None, None
+
+
+class Attention(torch.nn.Module):
+    """Self-attention of rows [q | k | v] (heads, key heads, key heads, of `width` each),
+    as one product gives them, to [B][T][heads width].  With `freqs` (radians of the
+    pairs, rotary_freqs), queries and keys are turned by their positions [B][T] (or
+    [B][T][axes] with the pairs of each axis in sections; None: 0, 1, 2, ..)."""
+
+    def __init__(self, heads, kv_heads, width, causal=True, cap=0.0, slopes=None, scale=None,
+                 freqs=None, sections=None, interleaved=False):
+        super().__init__()
+        if heads % kv_heads != 0:
+            raise ValueError(f"{heads} heads are no multiple of {kv_heads} heads of keys")
+        self.heads, self.kv_heads, self.width = int(heads), int(kv_heads), int(width)
+        self.causal, self.cap, self.scale = bool(causal), float(cap), scale
+        self.sections, self.interleaved = sections, bool(interleaved)
+        # (kept in their own types when the module's parameters change theirs)
+        self.freqs = None if freqs is None else freqs.detach().double()
+        self.slopes = None if slopes is None else slopes.detach().float()
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        for name, dtype in (("freqs", torch.float64), ("slopes", torch.float32)):
+            t = getattr(self, name)
+            if t is not None:
+                setattr(self, name, t.to(fn(torch.empty(0, device=t.device)).device, dtype))
+        return self
+
+    def positions(self, B, T, device):
+        return torch.arange(T, device=device).expand(B, T).contiguous()
+
+    def forward(self, rows, positions=None, docs=None, prefix=None, lengths=None):
+        B, T, n = rows.shape
+        if n != (self.heads + 2 * self.kv_heads) * self.width:
+            raise ValueError(f"rows of {n} are not [q | k | v] of {self.heads}, {self.kv_heads} and "
+                             f"{self.kv_heads} heads of {self.width}")
+        if self.freqs is None:
+            positions = None
+        elif positions is None:
+            positions = self.positions(B, T, rows.device)
+        args = _plain(dict(scale=self.scale, causal=self.causal, cap=self.cap, slopes=self.slopes,
+                           docs=docs, prefix=prefix, lengths=lengths))
+        turn = dict(sections=self.sections, interleaved=self.interleaved)
+        return _SelfAttend.apply(rows, _dense(positions), self.freqs,
+                                 (self.heads, self.kv_heads, self.width), turn, args,
+                                 torch.is_grad_enabled())

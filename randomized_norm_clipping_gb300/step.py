@@ -23,19 +23,20 @@ asks autograd only for the gradients with respect to the recorded layer
 outputs, so no weight gradient is formed before the clip factors are known.
 
 Scope: every trainable parameter must be the weight of an nn.Linear without
-bias, the weight or bias of a `layers.Linear`, or the weight of an embedding
-(`layers.Embedding`, or a plain nn.Embedding); the norms of biases and
-embeddings are exact and cheap (dprc_embed_norm: a group sum of the output
-gradients), other kinds (normalisation gains) would need their own per-sample
+bias, the weight or bias of a `layers.Linear`, the weight or bias of a
+`layers.LayerNorm`, or the weight of an embedding (`layers.Embedding`, or a plain
+nn.Embedding); the norms of biases, embeddings and normalisations are exact and cheap
+(dprc_embed_norm: a group sum of the output gradients; dprc_layernorm_grad: the
+per-sample gradients, vectors of the width), other kinds would need their own per-sample
 gradients, which the method does not cover.  Each layer runs once per
 forward pass on inputs (B, ..., d) (every position between the batch and the
 feature axis counts as a token), or on one sample after another; positions
 that the samples share (an embedding of arange(T)) are expanded to [B, T] first.
 A layer that runs twice and an input that mixes samples are refused, since a
 sample's norm would not be that of its gradient.  The per-sample losses must not
-couple samples.  An embedding's clipped gradient is formed from the recorded output
-gradients and the clip factors (dprc_embed_grad), so the second backward stops
-at the linear parameters.  Projections are drawn fresh per (layer, step) from a seeded
+couple samples.  The clipped gradient of an embedding or a normalisation is formed from the
+recorded output gradients and the clip factors (dprc_embed_grad, dprc_layernorm_grad), so
+the second backward stops at the linear parameters.  Projections are drawn fresh per (layer, step) from a seeded
 generator (a reading of the pages, which do not say how often P is redrawn):
 P ~ N(0, 1/k) for Hutchinson, S and P ~ N(0, 1) for Hutch++.  Dividing the
 noisy sum by the batch size is left to the optimiser.
@@ -66,7 +67,7 @@ class RandomizedClippingStep:
 
     Args:
       model: the module; its trainable parameters must be those of bias-free
-        nn.Linear, of `layers.Linear` and of embeddings.
+        nn.Linear, of `layers.Linear`, of `layers.LayerNorm` and of embeddings.
       C: clipping threshold.
       sigma: noise multiplier (0 disables the noise).
       k: projection width (Hutchinson) or r (Hutch++, k = 16).
@@ -101,10 +102,23 @@ class RandomizedClippingStep:
                 raise ValueError("nn.Embedding with max_norm, scale_grad_by_freq or sparse "
                                  "gradients is not supported")
         covered |= {id(m.bias) for m in self.biased}
+        self.norms = []
+        for m in model.modules():
+            own = [p for p in (m.weight, m.bias) if p is not None and p.requires_grad] \
+                if isinstance(m, lay.LayerNorm) else []
+            if not own:
+                continue
+            if any(id(p) in covered for p in own):
+                raise ValueError("a normalisation's parameter is shared with another layer; the "
+                                 "norm of a sum of two layers' gradients is not the sum of their "
+                                 "norms")
+            covered |= {id(p) for p in own}
+            self.norms.append(m)
         for name, prm in model.named_parameters():
             if prm.requires_grad and id(prm) not in covered:
                 raise ValueError(f"trainable parameter {name!r} has no per-sample norm here; covered "
-                                 "are linear weights, the biases of layers.Linear and embeddings")
+                                 "are linear weights, the biases of layers.Linear, layers.LayerNorm and "
+                                 "embeddings")
         for m in self.layers:
             if isinstance(m, torch.nn.Linear) and m.bias is not None and m.bias.requires_grad:
                 raise ValueError("nn.Linear layers with a trainable bias are not supported")
@@ -114,10 +128,13 @@ class RandomizedClippingStep:
         self._runs = {}
         self._mark = object()
         self._apart = set()
-        recorded = list(dict.fromkeys(self.layers + self.biased + self.embeddings))
+        recorded = self._recorded()
         self._handles = [m.register_forward_hook(self._record) for m in recorded]
         self._ws = {}
         self._bias_plans = {}
+
+    def _recorded(self):
+        return list(dict.fromkeys(self.layers + self.biased + self.embeddings + self.norms))
 
     def close(self):
         """Removes the hooks."""
@@ -134,7 +151,7 @@ class RandomizedClippingStep:
             self._runs[module] = self._runs.get(module, 0) + 1
             if output.grad_fn is not None:
                 output.grad_fn.metadata[self._mark] = module
-            if isinstance(module, lay.Linear):
+            if isinstance(module, (lay.Linear, lay.LayerNorm)):
                 self._lasts[module] = module._last
 
     def _refuse_repeats(self, losses):
@@ -190,9 +207,37 @@ class RandomizedClippingStep:
 
     def parameters(self):
         """The trainable parameters in the order the noise stream runs over
-        them: linear weights, biases, embeddings."""
+        them: linear weights, biases, embeddings, normalisations."""
         return ([m.weight for m in self.layers] + [m.bias for m in self.biased]
-                + [m.weight for m in self.embeddings])
+                + [m.weight for m in self.embeddings]
+                + [p for m in self.norms for p in self._norm_parameters(m)])
+
+    @staticmethod
+    def _norm_parameters(m):
+        return [p for p in (m.weight, m.bias) if p is not None and p.requires_grad]
+
+    def _norm_grad(self, m, G, n=None, c=None):
+        """A normalisation's per-sample norms into n, or with the clip factors c its clipped
+        gradient into its parameters."""
+        X = lay._dense(self._acts[m]).reshape(G.shape)
+        stats = self._lasts[m].reshape(*G.shape[:-1], 2)
+        w = None if m.weight is None else lay._dense(m.weight)
+        gain = m.weight is not None and m.weight.requires_grad
+        shift = m.bias is not None and m.bias.requires_grad
+        if n is not None and gain:
+            rnc.dprc_layernorm_grad(G, X, stats, w, center=m.center, n=n, norm_of_bias=shift,
+                                    accumulate=True)
+        elif n is not None:
+            rnc.dprc_embed_norm(G, self._bias_plan(G.shape[0], G.shape[1], G.device), n,
+                                accumulate=True)
+        else:
+            dW = torch.empty_like(m.weight) if gain else None
+            db = torch.empty_like(m.bias) if shift else None
+            rnc.dprc_layernorm_grad(G, X, stats, w, center=m.center, dW=dW, db=db, c=c)
+            if gain:
+                m.weight.grad = dW
+            if shift:
+                m.bias.grad = db
 
     def _bias_plan(self, B, T, device):
         """The plan of the one-row embedding that a bias is: every position 0.  Kept
@@ -267,14 +312,14 @@ class RandomizedClippingStep:
         if losses.dim() != 1:
             raise ValueError("per_sample_losses must have shape [B]")
         B = losses.shape[0]
-        recorded = list(dict.fromkeys(self.layers + self.biased + self.embeddings))
+        recorded = self._recorded()
         if any(m not in self._outs for m in self.layers):
             raise RuntimeError("no forward pass recorded for some linear layers")
         if any(m not in self._outs for m in recorded):
             raise RuntimeError("no forward pass recorded for some layers")
         self._refuse_repeats(losses)
         # step 2: gradients with respect to the layer outputs only
-        fused = [m for m in recorded if isinstance(m, lay.Linear)]
+        fused = [m for m in recorded if isinstance(m, (lay.Linear, lay.LayerNorm))]
         for m in fused:
             m.norm_pass = True
         try:
@@ -299,6 +344,8 @@ class RandomizedClippingStep:
         for m in self.biased:
             G = G_of[m]
             rnc.dprc_embed_norm(G, self._bias_plan(B, G.shape[1], G.device), n, accumulate=True)
+        for m in self.norms:
+            self._norm_grad(m, G_of[m], n=n)
         plans = {}
         for m in self.embeddings:
             tokens = self._acts[m].detach().reshape(B, -1)
@@ -313,7 +360,7 @@ class RandomizedClippingStep:
             # (B, ..., d): every position between batch and features is a token
             As.append(A.detach().reshape(B, -1, A.shape[-1]).contiguous())
             Gs.append(G_of[m])
-        more = bool(self.biased or self.embeddings)
+        more = bool(self.biased or self.embeddings or self.norms)
         one_call = (self.method == "hutch" and As and len({A.shape[1] for A in As}) == 1
                     and len({P.shape[1] for P in proj}) == 1 and len({A.dtype for A in As}) == 1)
         if one_call:
@@ -352,6 +399,8 @@ class RandomizedClippingStep:
             dW = torch.empty_like(m.weight)
             rnc.dprc_embed_grad(G_of[m], plans[m], dW, c=c, scale=getattr(m, "scale", 1.0))
             m.weight.grad = dW
+        for m in self.norms:
+            self._norm_grad(m, G_of[m], c=c)
         # step 5: noise on the aggregated gradient, in place: the parameters'
         # gradients laid end to end in parameters() order are that gradient, and each
         # gets the stretch of the one noise stream its position there selects
@@ -367,7 +416,7 @@ class RandomizedClippingStep:
         self._outs.clear()
         self._lasts.clear()
         self._runs.clear()
-        for m in self.layers + self.biased:
-            if isinstance(m, lay.Linear):
+        for m in recorded:
+            if isinstance(m, (lay.Linear, lay.LayerNorm)):
                 m._last = None
         return {"n": n, "c": c}
