@@ -81,9 +81,8 @@ __global__ void __launch_bounds__(128)
   const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (r >= rows) return;
-  const float* stats = a.part + rows * a.splits * a.D;
   float m = -INFINITY;
-  for (int z = lane; z < a.splits; z += 32) m = fmaxf(m, ld_l2(stats + (z * rows + r) * 2));
+  for (int z = lane; z < a.splits; z += 32) m = fmaxf(m, ld_l2(&a.part_stats[z * rows + r].x));
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float at = m == -INFINITY ? 0.f : m;
   float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -91,7 +90,7 @@ __global__ void __launch_bounds__(128)
     const int z = z0 + lane;
     float w = 0.f, mine = 0.f;
     if (z < a.splits) {
-      const float2 st = ld_l2(reinterpret_cast<const float2*>(stats + (z * rows + r) * 2));
+      const float2 st = ld_l2(a.part_stats + z * rows + r);
       w = exp2f(st.x - at);
       mine = w * st.y;
     }
@@ -120,6 +119,10 @@ __global__ void __launch_bounds__(128)
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t round16(size_t v) { return (v + 15) / 16 * 16; }
+
+size_t stats_bytes(const AttentionCall& c, int splits) {
+  return round16(static_cast<size_t>(splits) * c.B * c.Tq * c.H * sizeof(float2));
+}
 
 size_t span_bytes(const AttentionCall& c) {
   return c.docs != nullptr ? round16(c.B * cdiv(c.Tk, kDocSpan) * sizeof(DocSpan)) : 0;
@@ -201,7 +204,7 @@ cudaError_t delta_rows(const AttnArgs& a, cudaStream_t s) {
 size_t attention_ws_bytes(const AttentionCall& c) {
   const Split sp = plan_split(c);
   const size_t part = sp.splits > 1
-      ? static_cast<size_t>(sp.splits) * c.B * c.Tq * c.H * (c.D + 2) * 4 : 0;
+      ? stats_bytes(c, sp.splits) + static_cast<size_t>(sp.splits) * c.B * c.Tq * c.H * c.D * 4 : 0;
   return span_bytes(c) + part + 16;
 }
 
@@ -220,7 +223,8 @@ cudaError_t launch_attention(const AttentionCall& c, void* out, float* lse, void
   a.lse = lse;
   a.splits = sp.splits;
   a.per_split = sp.per;
-  a.part = reinterpret_cast<float*>(w + span_bytes(c));
+  a.part_stats = reinterpret_cast<float2*>(w + span_bytes(c));
+  a.part = reinterpret_cast<float*>(w + span_bytes(c) + stats_bytes(c, sp.splits));
   e = attention_tc_takes(c) ? launch_attention_tc(a, s) : launch_attention_simt(a, c.dtype, s);
   if (e != cudaSuccess || sp.splits == 1) return e;
   const long long rows = static_cast<long long>(c.B) * c.Tq * c.H;

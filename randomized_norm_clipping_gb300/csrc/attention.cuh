@@ -35,7 +35,8 @@ struct AttnArgs {
   void* out;             // [B][Tq][H][D]
   float* lse;            // [B][H][Tq] or null
   int splits, per_split; // shares of the keys, in tiles
-  float* part;           // [splits][B][Hkv][Tq G][D] sums, then [..][2] maximum and sum
+  float* part;           // [splits][B][Hkv][Tq G][D] sums of a share
+  float2* part_stats;    // [splits][B][Hkv][Tq G] maximum (in units of log2) and sum
   // gradient
   const void *dO, *O;    // [B][Tq][H][D]
   long long dob, dot, doh, ob, ot, oh;

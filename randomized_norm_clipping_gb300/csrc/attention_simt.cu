@@ -235,18 +235,13 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnArgs
     const int p = p0 + ty * kR + i, t = p / a.G, h = hk * a.G + p - t * a.G;
     if (p >= rows) continue;
     if (a.splits > 1) {
-      const long long all = static_cast<long long>(a.B) * a.Hkv * rows;
       const long long at = (static_cast<long long>(blockIdx.z) * a.B * a.Hkv + blockIdx.y) * rows + p;
 #pragma unroll
       for (int c = 0; c < 4 * kO; ++c) {
         const int col = (c / 4) * 64 + tx * 4 + c % 4;
         if (col < a.D) a.part[at * a.D + col] = o[i][c];
       }
-      if (tx == 0) {
-        float* st = a.part + all * a.splits * a.D + at * 2;
-        st[0] = m[i] * kLog2e;
-        st[1] = l[i];
-      }
+      if (tx == 0) a.part_stats[at] = make_float2(m[i] * kLog2e, l[i]);
       continue;
     }
     const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);

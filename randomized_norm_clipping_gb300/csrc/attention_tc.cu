@@ -651,9 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (mine && parts) {
-          float* st = a.part + static_cast<long long>(bhs) * rows * a.splits * a.D + prow * 2;
-          st[0] = m;
-          st[1] = l;
+          a.part_stats[prow] = make_float2(m, l);
         } else if (mine && a.lse != nullptr) {
           a.lse[(static_cast<long long>(b) * a.H + h) * a.Tq + tok] = m * kLn2 + logf(l);
         }

@@ -339,6 +339,15 @@ def test_attention_odd_widths(dtype, D):
     _attend(dtype, 2, 70, 70, 4, 2, D, {}, strided=True)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [1, 47, 127])
+@pytest.mark.parametrize("T", [943, 200, 450])
+def test_attention_of_few_tokens_of_odd_widths(dtype, D, T):
+    """Shares of odd numbers of odd rows, whose statistics lie at whole 8 bytes."""
+    _attend(dtype, 3, 5, T, 3, 3, D, _mask("lengths", 3, 5, T), slopes=True, grad=False)
+    _attend(dtype, 1, 1, T, 3, 1, D, {}, grad=False)
+
+
 def test_attention_of_nothing():
     for dtype in (F32, BF16):
         q, kv = _randn((2, 3, 4, 64), dtype, 1).to(DEV), torch.empty(2, 0, 2, 64, device=DEV, dtype=dtype)
