@@ -119,6 +119,34 @@ __device__ __forceinline__ void ld_shared4(const float* p, float (&v)[4]) {
                : "r"(smem_u32(p)));
 }
 
+// Two fp32 operations in one instruction.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(F2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Descriptors of a tile [128][64 kBlocks] at a 1024-byte boundary.  As the operand
 // whose width is summed over (K-major): a step of 16 is 32 bytes, a block of 64 kBlock
 // bytes.  As the operand whose rows are summed over (MN-major): a step is 16 rows.
@@ -555,22 +583,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           dirty = dirty || s.pad;
         }
         float z[kTile];
-#pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          float part[32];
-          tmem_ld_32cols(ts + c, part);
-#pragma unroll
-          for (int u = 0; u < 32; ++u) z[c + u] = part[u];
-        }
+        tmem_ld_128cols(ts, z);
         scores<kForm>(x, z, slope2, static_cast<float>(see.pos - j0));
         if (j0 + kTile > e.min_lim || by_doc) hide(z, see, docs, j0, a.Tk, by_doc);
         const float mul = kForm == 0 ? x.c : 1.f;
         float mx[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-        for (int c = 4; c < kTile; c += 4)
+        for (int c = 4; c + 8 <= kTile; c += 8)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], z[c + u]);
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+          for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], z[c + u], z[c + 4 + u]);
+        mx[0] = max3(mx[0], z[kTile - 4], z[kTile - 3]);
+        mx[1] = max3(mx[1], z[kTile - 2], z[kTile - 1]);
+        const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * mul;
         const bool grow = mt > m + kLazy || (m == -INFINITY && mt > m);
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? ex2(m - mt) : 1.f;
@@ -588,20 +612,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float off = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const F2 mul2 = f2(mul, mul), off2 = f2(off, off);
+        F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
         for (int c0 = 0; c0 < kTile; c0 += 64) {
           uint32_t p[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            const float p0 = ex2(fmaf(z[c0 + c], mul, off)), p1 = ex2(fmaf(z[c0 + c + 1], mul, off));
-            sum[c & 2] += p0;
-            sum[(c & 2) + 1] += p1;
+            float p0, p1;
+            split(fma2(f2(z[c0 + c], z[c0 + c + 1]), mul2, off2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], f2(p0, p1));
             p[c / 2] = pack_bf16(p0, p1);
           }
           tmem_st_32cols(ts + c0 / 2, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        {
+          float s0, s1;
+          split(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+        }
         tmem_st_wait();
         if (dirty && w == 0) {
           // values that no row of the CTA sees may be anything, and 0 times NaN is NaN
