@@ -42,7 +42,9 @@ constexpr float kLazy = 8.f;  // a row is rescaled when its maximum grows by 2^k
 
 constexpr uint32_t kSuspendNs = 20000;
 
+template <bool kSuspend>
 __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  if constexpr (!kSuspend) return mbar_try_wait(bar, parity);
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -55,12 +57,13 @@ __device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
 }
 
 // Bounded wait; false once it ran out (recorded) or another role has.
+template <bool kSuspend>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int code,
                                          volatile int* abort) {
-  if (try_wait_long(bar, parity)) return true;
+  if (try_wait_long<kSuspend>(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
   while (true) {
-    if (try_wait_long(bar, parity)) return true;
+    if (try_wait_long<kSuspend>(bar, parity)) return true;
     if (*abort != 0) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       record_error(code);
@@ -70,12 +73,25 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int cod
   }
 }
 
+// The warp's number, in a form that the compiler takes for the same in all its lanes.
+__device__ __forceinline__ int warp_index() {
+  return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+}
+
 // The same for a warp, which waits with one lane (polling lanes take issue slots).
+template <bool kSuspend>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int code,
                                           volatile int* abort) {
   int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity, code, abort) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar<kSuspend>(bar, parity, code, abort) ? 1 : 0;
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// The same by all lanes of a warp.
+template <bool kSuspend>
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, int code,
+                                         volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_bar<kSuspend>(bar, parity, code, abort)) != 0;
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -157,18 +173,34 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
   return make_sdesc(addr, kBlock, 1024, kSwz128);
 }
 
-// acc = A B^T over the width D (both tiles' widths are summed over).
-__device__ __forceinline__ void mma_width(uint32_t acc, uint64_t a, uint64_t b, uint32_t idesc,
-                                          int steps) {
-  for (int k = 0; k < steps; ++k) {
+__device__ __forceinline__ void commit(bool lead, uint64_t* bar) {
+  if (lead) umma_commit(bar);
+}
+
+// acc = A B^T over the width D (both tiles' widths are summed over), up to 64 kBlocks.
+// Unrolled, so that a step's operands are those of the first plus constants.
+template <int kBlocks, bool kUnroll>
+__device__ __forceinline__ void mma_width(bool lead, uint32_t acc, uint64_t a, uint64_t b,
+                                          uint32_t idesc, int steps) {
+  if (!lead) return;
+  const auto step = [&](int k) {
     const uint32_t at = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
     umma_bf16(acc, a + at, b + at, idesc, k > 0 ? 1u : 0u);
+  };
+  if constexpr (kUnroll) {
+#pragma unroll
+    for (int k = 0; k < 4 * kBlocks; ++k)
+      if (k < steps) step(k);
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) step(k);
   }
 }
 
 // acc (+)= A B with A [128][128] in tensor memory and B's rows summed over.
-__device__ __forceinline__ void mma_rows(uint32_t acc, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_rows(bool lead, uint32_t acc, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                          bool accumulate) {
+  if (!lead) return;
 #pragma unroll
   for (int k = 0; k < kTile / 16; ++k)
     umma_bf16_ts(acc, a_tmem + k * 8, b + ((k * 2048) >> 4), idesc, accumulate || k > 0 ? 1u : 0u);
@@ -404,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* ext = reinterpret_cast<int*>(tmem_slot + 2);  // greatest limit, least and greatest document
   uint32_t* bits = reinterpret_cast<uint32_t*>(ring + kStages * Cfg::kSlot + 512);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int bhs = a.B * a.Hkv;
   const int bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
   const int grp = x.groups - 1 - blockIdx.x / bhs;  // the longest rows first
@@ -483,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; j >= 0 && ok; j = it.next()) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (!wait_bar(&empty[pos.s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
+          if (!wait_bar<true>(&empty[pos.s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
             ok = false;
             break;
           }
@@ -500,7 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any) mbar_wait(qfull, 0, DPRC_DEVERR_PIPE_FULL);
       for (int k = issued - 1; k >= 0 && k >= issued - kStages; --k)
         mbar_wait(&full[k % kStages], (k / kStages) & 1, DPRC_DEVERR_PIPE_FULL);
-    } else if (warp == kWarps + 1 && lane == 0) {
+    } else if (warp == kWarps + 1) {
+      // all lanes keep step, one issues: the descriptors stay in the warp's common registers
+      const bool lead = elect_one() != 0;
       Bits it(bits, words);
       const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
       const uint32_t id_o = make_idesc_bf16(kTile, x.steps * 16, false, true);
@@ -510,17 +544,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       int j = it.next(), n = 0;
       bool ok = true, issued = false;
       if (j >= 0) {
-        ok = wait_bar(qfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
-             wait_bar(&full[0], 0, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        ok = wait_all<true>(qfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
+             wait_all<true>(&full[0], 0, DPRC_DEVERR_PIPE_FULL, abort_flag);
         if (ok) {
           tc_fence_after();
           issued = true;
 #pragma unroll
           for (int u = 0; u < kTiles; ++u) {
-            mma_width(tmem + u * 128, dq + ((u * kBlocks * kBlock) >> 4), dk, id_s, x.steps);
-            umma_commit(&sfull[u]);
+            mma_width<kBlocks, false>(lead, tmem + u * 128, dq + ((u * kBlocks * kBlock) >> 4), dk, id_s, x.steps);
+            commit(lead, &sfull[u]);
           }
-          umma_commit(&empty[0]);
+          commit(lead, &empty[0]);
           pos.next(kStages);
         }
       }
@@ -530,30 +564,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         pos.next(kStages);
         const Pos k = pos;
         if (j >= 0) pos.next(kStages);
-        ok = wait_bar(&full[v.s], v.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
-        if (ok && j >= 0) ok = wait_bar(&full[k.s], k.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        ok = wait_all<true>(&full[v.s], v.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        if (ok && j >= 0) ok = wait_all<true>(&full[k.s], k.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
 #pragma unroll
         for (int u = 0; u < kTiles; ++u) {
-          ok = ok && wait_bar(&pfull[u], n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+          ok = ok && wait_all<true>(&pfull[u], n & 1, DPRC_DEVERR_ACCUM, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          mma_rows(tmem + Cfg::kO + u * 128, tmem + u * 128, dv + ((v.s * Cfg::kSlot) >> 4), id_o,
+          mma_rows(lead, tmem + Cfg::kO + u * 128, tmem + u * 128, dv + ((v.s * Cfg::kSlot) >> 4), id_o,
                    n > 0);
           if (j >= 0) {
-            mma_width(tmem + u * 128, dq + ((u * kBlocks * kBlock) >> 4),
+            mma_width<kBlocks, false>(lead, tmem + u * 128, dq + ((u * kBlocks * kBlock) >> 4),
                       dk + ((k.s * Cfg::kSlot) >> 4), id_s, x.steps);
-            umma_commit(&sfull[u]);
+            commit(lead, &sfull[u]);
           } else {
-            umma_commit(&ofull[u]);
+            commit(lead, &ofull[u]);
           }
         }
         if (ok) {
-          umma_commit(&empty[v.s]);
-          if (j >= 0) umma_commit(&empty[k.s]);
+          commit(lead, &empty[v.s]);
+          if (j >= 0) commit(lead, &empty[k.s]);
         }
         ++n;
       }
-      if (issued) umma_drain(drain, kWaitLimitNs);
+      if (issued && lead) umma_drain(drain, kWaitLimitNs);
     }
   } else {
     regs_more<kRegsMore>();
@@ -572,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0;
       bool ok = true;
       for (int j = it.next(); j >= 0; j = it.next(), ++n) {
-        ok = wait_warp(&sfull[w], n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        ok = wait_warp<true>(&sfull[w], n & 1, DPRC_DEVERR_ACCUM, abort_flag);
         if (!ok) break;
         tc_fence_after();
         const int j0 = j * kTile;
@@ -636,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         if (dirty && w == 0) {
           // values that no row of the CTA sees may be anything, and 0 times NaN is NaN
-          ok = wait_warp(&full[vpos.s], vpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+          ok = wait_warp<true>(&full[vpos.s], vpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
           if (!ok) break;
           const int key = j0 + r;
           if (key >= top || (docs != nullptr && docs[key] < 0))
@@ -649,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[w]);
       }
-      if (n > 0 && ok) ok = wait_warp(&ofull[w], 0, DPRC_DEVERR_ACCUM, abort_flag);
+      if (n > 0 && ok) ok = wait_warp<true>(&ofull[w], 0, DPRC_DEVERR_ACCUM, abort_flag);
       tc_fence_after();
       if (ok) {
         const bool parts = a.splits > 1;
@@ -718,31 +752,40 @@ cudaError_t launch_fwd_form(int form, const CUtensorMap& q, const CUtensorMap& k
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  The eight warps of the softmax share a tile: a thread has a lane and 64 of
-// the 128 columns.  Its weights go back into the first half of the columns that it read
-// (a product's steps of 16 take their operand from there, mma_halves), so no other
-// thread's scores are overwritten.  While the weights' gradient is formed, the tensor
+// Backward.  Sixteen warps share a tile: a thread has a lane and 32 of the 128
+// columns (with eight and 64 columns, two warps a scheduler, the chain of a thread's
+// operations was what the kernels waited for: issue slots 35 % used).  Its weights go back
+// into the first half of the columns that it read (a product's steps of 16 take their
+// operand from there, mma_parts), so no other thread's scores are overwritten.  While the weights' gradient is formed, the tensor
 // core forms the next scores; while those are taken to the exponential, the gradients'
 // products and the next dP.
 // ---------------------------------------------------------------------------
-constexpr int kHalf = kTile / 2;
+constexpr int kGradWarps = 16, kGradThreads = 32 * (kGradWarps + 4);
+constexpr int kPart = kTile * 4 / kGradWarps;  // columns of a thread
 
-__device__ __forceinline__ void mma_halves(uint32_t acc, uint32_t a_tmem, uint64_t b,
+__device__ __forceinline__ void mma_parts(bool lead, uint32_t acc, uint32_t a_tmem, uint64_t b,
                                            uint32_t idesc, bool accumulate) {
+  if (!lead) return;
 #pragma unroll
   for (int k = 0; k < kTile / 16; ++k)
-    umma_bf16_ts(acc, a_tmem + (k >> 2) * kHalf + (k & 3) * 8, b + ((k * 2048) >> 4), idesc,
+    umma_bf16_ts(acc, a_tmem + (k / (kPart / 16)) * kPart + (k % (kPart / 16)) * 8, b + ((k * 2048) >> 4), idesc,
                  accumulate || k > 0 ? 1u : 0u);
 }
 
-// This thread's 64 columns: ds = w (dp - delta), 0 where `bits` says that the key is not
+template <int kN>
+__device__ __forceinline__ void tmem_ld_part(uint32_t taddr, float (&v)[kN]) {
+  if constexpr (kN == 64) tmem_ld_64cols(taddr, v);
+  else tmem_ld_32cols(taddr, v);
+}
+
+// This thread's columns: ds = w (dp - delta), 0 where `bits` says that the key is not
 // seen (dp may be anything there), as bf16 into the first 32 of them.
 // delta(c, d): those of columns c to c + 3.
 template <typename Delta>
-__device__ __forceinline__ void put_ds(uint32_t taddr, const float (&w)[kHalf], bool masked,
-                                       const uint32_t (&bits)[2], Delta delta) {
+__device__ __forceinline__ void put_ds(uint32_t taddr, const float (&w)[kPart], bool masked,
+                                       const uint32_t (&bits)[kPart / 32], Delta delta) {
 #pragma unroll
-  for (int c0 = 0; c0 < kHalf; c0 += 32) {
+  for (int c0 = 0; c0 < kPart; c0 += 32) {
     float dp[32];
     tmem_ld_32cols(taddr + c0, dp);
 #pragma unroll
@@ -760,7 +803,6 @@ __device__ __forceinline__ void put_ds(uint32_t taddr, const float (&w)[kHalf], 
     uint32_t p[16];
 #pragma unroll
     for (int u = 0; u < 16; ++u) p[u] = pack_bf16(dp[2 * u], dp[2 * u + 1]);
-    // (columns 0..15 of the half, then 16..31: read before, c0 = 0 holds them)
     tmem_st_16cols(taddr + c0 / 2, p);
   }
 }
@@ -776,10 +818,10 @@ __device__ __forceinline__ void store_any(__nv_bfloat16* p, const float* v) {
   }
 }
 
-// Rows of a gradient from tensor memory: this thread's lane, every second 16 columns.
-__device__ __forceinline__ void store_grad(__nv_bfloat16* out, bool mine, uint32_t taddr, int half,
+// Rows of a gradient from tensor memory: this thread's lane, and of its 16-column pieces those that are the part's.
+__device__ __forceinline__ void store_grad(__nv_bfloat16* out, bool mine, uint32_t taddr, int part,
                                            int cols, int D, float scale, bool any) {
-  for (int c = half * 16; c < cols; c += 32) {
+  for (int c = part * 16; c < cols; c += kGradWarps * 4) {
     float o[16];
     if (any) {
       tmem_ld_16cols(taddr + c, o);
@@ -808,7 +850,7 @@ struct DqCfg {
 };
 
 template <int kBlocks, int kForm>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kGradThreads, 1)
     attention_dq_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                            const __grid_constant__ CUtensorMap map_o,
                            const __grid_constant__ CUtensorMap map_k,
@@ -834,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* ext = reinterpret_cast<int*>(tmem_slot + 2);
   uint32_t* bits = reinterpret_cast<uint32_t*>(ring + kStages * Cfg::kSlot + 512);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int bhs = a.B * a.Hkv;
   const int bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
   const int grp = x.groups - 1 - blockIdx.x / bhs;  // the longest rows first
@@ -845,9 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(qfull, 1);
     mbar_init(sfull, 1);
-    mbar_init(sread, kWarps);
+    mbar_init(sread, kGradWarps);
     mbar_init(dpfull, 1);
-    mbar_init(dsfull, kWarps);
+    mbar_init(dsfull, kGradWarps);
     mbar_init(ofull, 1);
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -860,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
-  if (warp == kWarps + 1) {
+  if (warp == kGradWarps + 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -872,12 +914,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
 
   const int keys = attn_keys(a, b), first = attn_first(a, b);
-  const int r = threadIdx.x & (kTile - 1), half = warp >> 2;
+  const int r = threadIdx.x & (kTile - 1), part = warp >> 2;
   const int tt = r / a.G, tok = grp * x.nt + tt;
-  const bool mine = warp < kWarps && tt < x.nt && tok < a.Tq;
+  const bool mine = warp < kGradWarps && tt < x.nt && tok < a.Tq;
   RowSees see = {0, 0, -1};
   Extent e = {};
-  if (warp < kWarps) {
+  if (warp < kGradWarps) {
     if (mine) see = attn_row(a, b, tok, keys, first);
     e = warp_extent(mine, see, a.docs != nullptr);
     if (lane == 0) {
@@ -891,8 +933,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   key_tile_bits(a, b, 0, t1, ext[1], ext[2], bits, words);
   __syncthreads();
 
-  if (warp >= kWarps) {
-    if (warp == kWarps && lane == 0) {
+  if (warp >= kGradWarps) {
+    if (warp == kGradWarps && lane == 0) {
       Bits it(bits, words);
       Pos pos;
       int j = it.next(), issued = 0;
@@ -909,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; j >= 0 && ok; j = it.next()) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (!wait_bar(&empty[pos.s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
+          if (!wait_bar<false>(&empty[pos.s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
             ok = false;
             break;
           }
@@ -925,7 +967,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any) mbar_wait(qfull, 0, DPRC_DEVERR_PIPE_FULL);
       for (int k = issued - 1; k >= 0 && k >= issued - kStages; --k)
         mbar_wait(&full[k % kStages], (k / kStages) & 1, DPRC_DEVERR_PIPE_FULL);
-    } else if (warp == kWarps + 1 && lane == 0) {
+    } else if (warp == kGradWarps + 1) {
+      // all lanes keep step, one issues: the descriptors stay in the warp's common registers
+      const bool lead = elect_one() != 0;
       Bits it(bits, words);
       const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
       const uint32_t id_g = make_idesc_bf16(kTile, x.steps * 16, false, true);
@@ -935,24 +979,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       int j = it.next(), n = 0;
       bool ok = j >= 0, issued = false;
       const auto filled = [&](const Pos& p) {
-        const bool f = wait_bar(&full[p.s], p.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        const bool f = wait_all<false>(&full[p.s], p.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
         tc_fence_after();
         return f;
       };
       const auto scores_of = [&](const Pos& p) {
-        mma_width(tmem + Cfg::kS, dq, dk + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
-        umma_commit(sfull);
+        mma_width<kBlocks, true>(lead, tmem + Cfg::kS, dq, dk + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
+        commit(lead, sfull);
       };
       const auto dp_of = [&](const Pos& p) {
-        mma_width(tmem + Cfg::kDp, dO, dk + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
-        umma_commit(dpfull);
-        umma_commit(&empty[p.s]);
+        mma_width<kBlocks, true>(lead, tmem + Cfg::kDp, dO, dk + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
+        commit(lead, dpfull);
+        commit(lead, &empty[p.s]);
       };
       Pos kp = pos;
       pos.next(kStages);
       Pos vp = pos;
       pos.next(kStages);
-      ok = ok && wait_bar(qfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) && filled(kp);
+      ok = ok && wait_all<false>(qfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) && filled(kp);
       if (ok) {
         issued = true;
         scores_of(kp);
@@ -967,32 +1011,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           pos.next(kStages);
           vn = pos;
           pos.next(kStages);
-          ok = filled(kn) && wait_bar(sread, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+          ok = filled(kn) && wait_all<false>(sread, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
           if (!ok) break;
           tc_fence_after();
           scores_of(kn);
         }
-        ok = wait_bar(dsfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        ok = wait_all<false>(dsfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        mma_halves(tmem + Cfg::kAcc, tmem + Cfg::kDp, dkm + ((kp.s * Cfg::kSlot) >> 4), id_g, n > 0);
-        umma_commit(&empty[kp.s]);
+        mma_parts(lead, tmem + Cfg::kAcc, tmem + Cfg::kDp, dkm + ((kp.s * Cfg::kSlot) >> 4), id_g, n > 0);
+        commit(lead, &empty[kp.s]);
         if (j >= 0) {
           ok = filled(vn);
           if (ok) dp_of(vn);
         } else {
-          umma_commit(ofull);
+          commit(lead, ofull);
         }
         kp = kn;
         vp = vn;
         ++n;
       }
-      if (issued) umma_drain(drain, kWaitLimitNs);
+      if (issued && lead) umma_drain(drain, kWaitLimitNs);
     }
   } else {
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + Cfg::kS + half * kHalf;
-    const uint32_t td = tmem + lanes + Cfg::kDp + half * kHalf;
+    const uint32_t ts = tmem + lanes + Cfg::kS + part * kPart;
+    const uint32_t td = tmem + lanes + Cfg::kDp + part * kPart;
     const int h = hk * a.G + r - tt * a.G;
     const long long at = (static_cast<long long>(b) * a.H + h) * a.Tq + tok;
     const float slope2 = kForm > 0 && a.slopes != nullptr && mine ? a.slopes[h] * kLog2e : 0.f;
@@ -1004,34 +1048,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n = 0;
     bool ok = true;
     for (int j = it.next(); j >= 0; j = it.next(), ++n) {
-      ok = wait_warp(sfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      ok = wait_warp<false>(sfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
       if (!ok) break;
       tc_fence_after();
-      const int j0 = j * kTile, jh = j0 + half * kHalf;
+      const int j0 = j * kTile, jh = j0 + part * kPart;
       bool dirty = j0 + kTile > top, by_doc = false;
       if (docs != nullptr) {
         const DocSpan s = key_tile_docs(a, b, j);
         by_doc = s.pad || s.lo != s.hi || e.lo != s.lo || e.hi != s.lo;
         dirty = dirty || s.pad;
       }
-      float z[kHalf];
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 32) {
-        float part[32];
-        tmem_ld_32cols(ts + c, part);
-#pragma unroll
-        for (int u = 0; u < 32; ++u) z[c + u] = part[u];
-      }
+      float z[kPart];
+      tmem_ld_part(ts, z);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sread);
-      uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
-      const bool masked = jh + kHalf > e.min_lim || by_doc;
+      uint32_t seen[kPart / 32];
+#pragma unroll
+      for (int q = 0; q < kPart / 32; ++q) seen[q] = 0xffffffffu;
+      const bool masked = jh + kPart > e.min_lim || by_doc;
       if (masked) seen_bits(seen, see, docs, jh, a.Tk, by_doc);
       weights<kForm>(x, z, slope2, static_cast<float>(see.pos - jh), off);
-      if (dirty && half == 0) {
+      if (dirty && part == 0) {
         // keys that no row of the CTA sees may be anything, and 0 times NaN is NaN
-        ok = wait_warp(&full[kpos.s], kpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        ok = wait_warp<false>(&full[kpos.s], kpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
         if (!ok) break;
         const int key = j0 + r;
         if (key >= top || (docs != nullptr && docs[key] < 0))
@@ -1040,7 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       kpos.next(kStages);
       kpos.next(kStages);
-      ok = wait_warp(dpfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      ok = wait_warp<false>(dpfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
       if (!ok) break;
       tc_fence_after();
       put_ds(td, z, masked, seen, [&](int, float (&d)[4]) { d[0] = d[1] = d[2] = d[3] = delta; });
@@ -1049,22 +1089,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(dsfull);
     }
-    if (n > 0 && ok) ok = wait_warp(ofull, 0, DPRC_DEVERR_ACCUM, abort_flag);
+    if (n > 0 && ok) ok = wait_warp<false>(ofull, 0, DPRC_DEVERR_ACCUM, abort_flag);
     tc_fence_after();
     if (ok)
       store_grad(static_cast<__nv_bfloat16*>(a.dQ) + b * a.dqb + tok * a.dqt + h * a.dqh, mine,
-                 tmem + lanes + Cfg::kAcc, half, x.steps * 16, a.D, a.scale, n > 0);
+                 tmem + lanes + Cfg::kAcc, part, x.steps * 16, a.D, a.scale, n > 0);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarps + 1) {
+  if (warp == kGradWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-// What the keys' kernel reads of a tile's rows, two tiles in turn.
+// What the keys' kernel reads of a tile's rows, kRowStages tiles in turn.
 struct RowStage {
   float off[kTile];    // -lse log2(e)
   float delta[kTile];
@@ -1075,6 +1115,7 @@ struct RowStage {
   int min_lim, lo, hi, dirty;
 };
 constexpr int kMaxRowTiles = 1 << 16;
+constexpr int kRowStages = 4;
 
 template <int kBlocks>
 struct DkvCfg {
@@ -1082,13 +1123,13 @@ struct DkvCfg {
   static constexpr int kStages = kBlocks == 1 ? 6 : 4;
   static constexpr int kBits = kMaxRowTiles / 8;
   static constexpr int kSmem =
-      (2 + kStages) * kSlot + 1024 + 512 + kBits + 2 * static_cast<int>(sizeof(RowStage));
+      (2 + kStages) * kSlot + 1024 + 512 + kBits + kRowStages * static_cast<int>(sizeof(RowStage));
   static constexpr int kS = 0, kDp = 128, kDv = 256, kDk = 384;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
 template <int kBlocks, int kForm>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kGradThreads, 1)
     attention_dkv_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                             const __grid_constant__ CUtensorMap map_o,
                             const __grid_constant__ CUtensorMap map_k,
@@ -1108,16 +1149,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pfull = sfull + 1;
   uint64_t* dpfull = pfull + 1;
   uint64_t* dsfull = dpfull + 1;
-  uint64_t* rfull = dsfull + 1;   // [2]
-  uint64_t* rempty = rfull + 2;   // [2]
-  uint64_t* ofull = rempty + 2;
+  uint64_t* rfull = dsfull + 1;            // [kRowStages]
+  uint64_t* rempty = rfull + kRowStages;   // [kRowStages]
+  uint64_t* ofull = rempty + kRowStages;
   uint64_t* drain = ofull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* bits = reinterpret_cast<uint32_t*>(rest + 512);
   RowStage* stages = reinterpret_cast<RowStage*>(rest + 512 + Cfg::kBits);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int bhs = a.B * a.Hkv;
   const int bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
   const int jt = blockIdx.x / bhs, j0 = jt * kTile;  // (the first keys have the most rows)
@@ -1128,12 +1169,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(kvfull, 1);
     mbar_init(sfull, 1);
-    mbar_init(pfull, kWarps);
+    mbar_init(pfull, kGradWarps);
     mbar_init(dpfull, 1);
-    mbar_init(dsfull, kWarps);
-    for (int s = 0; s < 2; ++s) {
+    mbar_init(dsfull, kGradWarps);
+    for (int s = 0; s < kRowStages; ++s) {
       mbar_init(&rfull[s], 1);
-      mbar_init(&rempty[s], kWarps);
+      mbar_init(&rempty[s], kGradWarps);
     }
     mbar_init(ofull, 1);
     mbar_init(drain, 1);
@@ -1144,14 +1185,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
-  if (warp == kWarps + 1) {
+  if (warp == kGradWarps + 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   // rows of a slot behind the last whole token are never copied: zero, as they are
   // summed over
   const int tail = x.nt * a.G;
-  for (int i = threadIdx.x; i < kStages * (kTile - tail); i += kThreads)
+  for (int i = threadIdx.x; i < kStages * (kTile - tail); i += kGradThreads)
     zero_row<kBlocks>(ring + (i / (kTile - tail)) * Cfg::kSlot, tail + i % (kTile - tail));
   if (tail < kTile) fence_proxy_async_smem();
   tc_fence_before();
@@ -1166,7 +1207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   DocSpan kd = {0, 0, 0, 0};
   if (a.docs != nullptr) kd = key_tile_docs(a, b, jt);
   const int words = j0 < keys ? (x.row_tiles + 31) / 32 : 0;
-  for (int w = warp; w < words; w += kThreads / 32) {
+  for (int w = warp; w < words; w += kGradThreads / 32) {
     const int i = w * 32 + lane, tok0 = i * x.nt;
     bool ok = tok0 < a.Tq;
     if (ok) {
@@ -1192,8 +1233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  if (warp >= kWarps) {
-    if (warp == kWarps && lane == 0) {
+  if (warp >= kGradWarps) {
+    if (warp == kGradWarps && lane == 0) {
       Bits it(bits, words);
       Pos pos;
       int i = it.next(), issued = 0;
@@ -1210,7 +1251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; i >= 0 && ok; i = it.next()) {
 #pragma unroll
         for (int qo = 0; qo < 2; ++qo) {
-          if (!wait_bar(&empty[pos.s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
+          if (!wait_bar<false>(&empty[pos.s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
             ok = false;
             break;
           }
@@ -1226,7 +1267,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any) mbar_wait(kvfull, 0, DPRC_DEVERR_PIPE_FULL);
       for (int k = issued - 1; k >= 0 && k >= issued - kStages; --k)
         mbar_wait(&full[k % kStages], (k / kStages) & 1, DPRC_DEVERR_PIPE_FULL);
-    } else if (warp == kWarps + 1 && lane == 0) {
+    } else if (warp == kGradWarps + 1) {
+      // all lanes keep step, one issues: the descriptors stay in the warp's common registers
+      const bool lead = elect_one() != 0;
       Bits it(bits, words);
       const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
       const uint32_t id_g = make_idesc_bf16(kTile, x.steps * 16, false, true);
@@ -1236,23 +1279,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       int i = it.next(), n = 0;
       bool ok = i >= 0, issued = false;
       const auto filled = [&](const Pos& p) {
-        const bool f = wait_bar(&full[p.s], p.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        const bool f = wait_all<false>(&full[p.s], p.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
         tc_fence_after();
         return f;
       };
       const auto scores_of = [&](const Pos& p) {
-        mma_width(tmem + Cfg::kS, dk, dr + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
-        umma_commit(sfull);
+        mma_width<kBlocks, true>(lead, tmem + Cfg::kS, dk, dr + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
+        commit(lead, sfull);
       };
       const auto dp_of = [&](const Pos& p) {
-        mma_width(tmem + Cfg::kDp, dv, dr + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
-        umma_commit(dpfull);
+        mma_width<kBlocks, true>(lead, tmem + Cfg::kDp, dv, dr + ((p.s * Cfg::kSlot) >> 4), id_s, x.steps);
+        commit(lead, dpfull);
       };
       Pos qp = pos;
       pos.next(kStages);
       Pos op = pos;
       pos.next(kStages);
-      ok = ok && wait_bar(kvfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) && filled(qp);
+      ok = ok && wait_all<false>(kvfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) && filled(qp);
       if (ok) {
         issued = true;
         scores_of(qp);
@@ -1262,11 +1305,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && i >= 0) {
         i = it.next();
         Pos qn = qp, on = op;
-        ok = wait_bar(pfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        ok = wait_all<false>(pfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        mma_halves(tmem + Cfg::kDv, tmem + Cfg::kS, drm + ((op.s * Cfg::kSlot) >> 4), id_g, n > 0);
-        umma_commit(&empty[op.s]);
+        mma_parts(lead, tmem + Cfg::kDv, tmem + Cfg::kS, drm + ((op.s * Cfg::kSlot) >> 4), id_g, n > 0);
+        commit(lead, &empty[op.s]);
         if (i >= 0) {
           qn = pos;
           pos.next(kStages);
@@ -1276,23 +1319,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           scores_of(qn);
         }
-        ok = wait_bar(dsfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        ok = wait_all<false>(dsfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        mma_halves(tmem + Cfg::kDk, tmem + Cfg::kDp, drm + ((qp.s * Cfg::kSlot) >> 4), id_g, n > 0);
-        umma_commit(&empty[qp.s]);
+        mma_parts(lead, tmem + Cfg::kDk, tmem + Cfg::kDp, drm + ((qp.s * Cfg::kSlot) >> 4), id_g, n > 0);
+        commit(lead, &empty[qp.s]);
         if (i >= 0) {
           ok = filled(on);
           if (ok) dp_of(on);
         } else {
-          umma_commit(ofull);
+          commit(lead, ofull);
         }
         qp = qn;
         op = on;
         ++n;
       }
-      if (issued) umma_drain(drain, kWaitLimitNs);
-    } else if (warp == kWarps + 2) {
+      if (issued && lead) umma_drain(drain, kWaitLimitNs);
+    } else if (warp == kGradWarps + 2) {
       // what the rows see, their statistics and where they stand
       Bits it(bits, words);
       int n = 0;
@@ -1304,41 +1347,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.prefix != nullptr) all = max(all, min(keys, a.prefix[b]));
       }
       const int none = kd.pad || j0 + kTile > all ? 0 : 0x7fffffff;
-      for (int i = it.next(); i >= 0; i = it.next(), ++n) {
-        RowStage& st = stages[n & 1];
-        if (!wait_warp(&rempty[n & 1], ((n >> 1) & 1) ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) break;
+      // a tile's values are on their way while the stage is waited for
+      int tt[4];
+      long long at[4];  // of a head's first token
+      float slope[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = q * 32 + lane;
+        tt[q] = r / a.G;
+        const int h = hk * a.G + r - tt[q] * a.G;
+        at[q] = (static_cast<long long>(b) * a.H + h) * a.Tq;
+        slope[q] = kForm > 0 && a.slopes != nullptr && tt[q] < x.nt ? a.slopes[h] * kLog2e : 0.f;
+      }
+      RowSees see[4];
+      float lse[4], del[4];
+      const auto fetch = [&](int i) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int tok = i * x.nt + tt[q];
+          see[q] = {0, none, -3};
+          lse[q] = del[q] = 0.f;
+          if (tt[q] < x.nt && tok < a.Tq) {
+            lse[q] = ld_once(a.lse_in + at[q] + tok);
+            del[q] = ld_once(a.delta + at[q] + tok);
+            see[q] = attn_row(a, b, tok, keys, first);
+          }
+        }
+      };
+      int i = it.next();
+      if (i >= 0) fetch(i);
+      for (; i >= 0; ++n) {
+        RowStage& st = stages[n % kRowStages];
+        if (!wait_warp<false>(&rempty[n % kRowStages], ((n / kRowStages) & 1) ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) break;
         int min_lim = 0x7fffffff, lo = 0x7fffffff, hi = -1, dirty = 0;
 #pragma unroll
-        for (int q = 0; q < kTile; q += 32) {
-          const int r = q + lane, tt = r / a.G, tok = i * x.nt + tt, h = hk * a.G + r - tt * a.G;
-          RowSees see = {0, none, -3};
-          float lse = 0.f, del = 0.f, slope = 0.f;
-          if (tt < x.nt && tok < a.Tq) {
-            see = attn_row(a, b, tok, keys, first);
-            const long long at = (static_cast<long long>(b) * a.H + h) * a.Tq + tok;
-            lse = a.lse_in[at];
-            del = a.delta[at];
-            if (kForm > 0 && a.slopes != nullptr) slope = a.slopes[h] * kLog2e;
-            if (see.doc >= 0) {
-              lo = min(lo, see.doc);
-              hi = max(hi, see.doc);
+        for (int q = 0; q < 4; ++q) {
+          const int r = q * 32 + lane;
+          if (tt[q] < x.nt && i * x.nt + tt[q] < a.Tq) {
+            if (see[q].doc >= 0) {
+              lo = min(lo, see[q].doc);
+              hi = max(hi, see[q].doc);
             }
-            dirty |= see.lim == 0;
+            dirty |= see[q].lim == 0;
           }
-          min_lim = min(min_lim, see.lim);
-          st.off[r] = lse == -INFINITY ? 0.f : -lse * kLog2e;
-          st.delta[r] = del;
-          st.slope2[r] = slope;
-          st.pos[r] = static_cast<float>(see.pos - j0);
-          st.lim[r] = see.lim;
-          st.doc[r] = see.doc;
+          min_lim = min(min_lim, see[q].lim);
+          st.off[r] = lse[q] == -INFINITY ? 0.f : -lse[q] * kLog2e;
+          st.delta[r] = del[q];
+          st.slope2[r] = slope[q];
+          st.pos[r] = static_cast<float>(see[q].pos - j0);
+          st.lim[r] = see[q].lim;
+          st.doc[r] = see[q].doc;
         }
-        for (int o = 16; o > 0; o >>= 1) {
-          min_lim = min(min_lim, __shfl_xor_sync(0xffffffffu, min_lim, o));
-          lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-          dirty |= __shfl_xor_sync(0xffffffffu, dirty, o);
-        }
+        i = it.next();
+        if (i >= 0) fetch(i);
+        min_lim = __reduce_min_sync(0xffffffffu, min_lim);
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        dirty = __reduce_or_sync(0xffffffffu, dirty);
         if (lane == 0) {
           st.min_lim = min_lim;
           st.lo = lo;
@@ -1346,14 +1411,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           st.dirty = dirty;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&rfull[n & 1]);
+        if (lane == 0) mbar_arrive(&rfull[n % kRowStages]);
       }
     }
   } else {
-    const int r = threadIdx.x & (kTile - 1), half = warp >> 2, key = j0 + r;
+    const int r = threadIdx.x & (kTile - 1), part = warp >> 2, key = j0 + r;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + Cfg::kS + half * kHalf;
-    const uint32_t td = tmem + lanes + Cfg::kDp + half * kHalf;
+    const uint32_t ts = tmem + lanes + Cfg::kS + part * kPart;
+    const uint32_t td = tmem + lanes + Cfg::kDp + part * kPart;
     const float keyf = static_cast<float>(r);
     const int kdoc =
         a.docs != nullptr ? (key < a.Tk ? a.docs[static_cast<long long>(b) * a.Tk + key] : -2) : 0;
@@ -1365,27 +1430,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n = 0;
     bool ok = true;
     for (int i = it.next(); i >= 0; i = it.next(), ++n) {
-      const RowStage& st = stages[n & 1];
-      const int c0 = half * kHalf;
-      ok = wait_warp(&rfull[n & 1], (n >> 1) & 1, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
-           wait_warp(sfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      const RowStage& st = stages[n % kRowStages];
+      const int c0 = part * kPart;
+      ok = wait_warp<false>(&rfull[n % kRowStages], (n / kRowStages) & 1, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
+           wait_warp<false>(sfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
       if (!ok) break;
       tc_fence_after();
-      float z[kHalf];
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 32) {
-        float part[32];
-        tmem_ld_32cols(ts + c, part);
-#pragma unroll
-        for (int u = 0; u < 32; ++u) z[c + u] = part[u];
-      }
+      float z[kPart];
+      tmem_ld_part(ts, z);
       const bool by_doc =
           a.docs != nullptr && (!one_doc || st.lo != kdoc0 || st.hi != kdoc0);
       const bool masked = last_key >= st.min_lim || by_doc;
-      uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+      uint32_t seen[kPart / 32];
+#pragma unroll
+      for (int q = 0; q < kPart / 32; ++q) seen[q] = 0xffffffffu;
       if (masked) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < kPart / 32; ++q) {
           uint32_t m = 0u;
 #pragma unroll 1
           for (int u = 0; u < 32; u += 4) {
@@ -1399,7 +1460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // P into the scores' place; z becomes P (1 - t^2)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < kPart / 32; ++q) {
         uint32_t p[16];
 #pragma unroll
         for (int u = 0; u < 32; u += 4) {
@@ -1414,10 +1475,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             w[k] = weight<kForm>(x, z[c + k], sl[k], fabsf(ps[k] - keyf), of[k]);
-            if (masked && !((seen[q] >> (u + k)) & 1u)) w[k] = z[c + k] = 0.f;
           }
           p[u / 2] = pack_bf16(w[0], w[1]);
           p[u / 2 + 1] = pack_bf16(w[2], w[3]);
+        }
+        if (masked) {
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            if (!((seen[q] >> u) & 1u)) {
+              z[q * 32 + u] = 0.f;
+              p[u / 2] &= u & 1 ? 0x0000ffffu : 0xffff0000u;
+            }
         }
         tmem_st_16cols(ts + q * 16, p);
       }
@@ -1425,14 +1493,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (st.dirty) {
         // rows that see nothing may be anything, and 0 times NaN is NaN: their queries
         // and gradients are summed over (dP, which reads them too, is complete)
-        ok = wait_warp(dpfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        ok = wait_warp<false>(dpfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        if (half == 0) {
+        if (part == 0) {
           Pos op = pos;
           op.next(kStages);
-          ok = wait_warp(&full[pos.s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
-               wait_warp(&full[op.s], op.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+          ok = wait_warp<false>(&full[pos.s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
+               wait_warp<false>(&full[op.s], op.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
           if (!ok) break;
           if (st.lim[r] == 0) {
             zero_row<kBlocks>(ring + pos.s * Cfg::kSlot, r);
@@ -1446,7 +1514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(pfull);
-      ok = wait_warp(dpfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      ok = wait_warp<false>(dpfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
       if (!ok) break;
       tc_fence_after();
       put_ds(td, z, masked, seen, [&](int c, float (&d)[4]) { ld_shared4(&st.delta[c0 + c], d); });
@@ -1455,26 +1523,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(dsfull);
-        mbar_arrive(&rempty[n & 1]);
+        mbar_arrive(&rempty[n % kRowStages]);
       }
     }
-    if (n > 0 && ok) ok = wait_warp(ofull, 0, DPRC_DEVERR_ACCUM, abort_flag);
+    if (n > 0 && ok) ok = wait_warp<false>(ofull, 0, DPRC_DEVERR_ACCUM, abort_flag);
     tc_fence_after();
     if (ok) {
       const bool mine = key < a.Tk;
       const int cols = x.steps * 16;
       if (a.dV != nullptr)
         store_grad(static_cast<__nv_bfloat16*>(a.dV) + b * a.dvb + key * a.dvt + hk * a.dvh, mine,
-                   tmem + lanes + Cfg::kDv, half, cols, a.D, 1.f, n > 0);
+                   tmem + lanes + Cfg::kDv, part, cols, a.D, 1.f, n > 0);
       if (a.dK != nullptr)
         store_grad(static_cast<__nv_bfloat16*>(a.dK) + b * a.dkb + key * a.dkt + hk * a.dkh, mine,
-                   tmem + lanes + Cfg::kDk, half, cols, a.D, a.scale, n > 0);
+                   tmem + lanes + Cfg::kDk, part, cols, a.D, a.scale, n > 0);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarps + 1) {
+  if (warp == kGradWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1492,7 +1560,7 @@ cudaError_t launch_grad(const GradMaps& m, const TcArgs& x, cudaStream_t s) {
     constexpr int bytes = DqCfg<kBlocks>::kSmem;
     e = allow_smem<attention_dq_tc_kernel<kBlocks, kForm>>(bytes);
     if (e != cudaSuccess) return e;
-    e = launch_after(attention_dq_tc_kernel<kBlocks, kForm>, dim3(bhs * x.groups), kThreads, 1, s,
+    e = launch_after(attention_dq_tc_kernel<kBlocks, kForm>, dim3(bhs * x.groups), kGradThreads, 1, s,
                      bytes, m.q, m.o, m.k, m.v, x);
     if (e != cudaSuccess) return e;
   }
@@ -1501,7 +1569,7 @@ cudaError_t launch_grad(const GradMaps& m, const TcArgs& x, cudaStream_t s) {
   e = allow_smem<attention_dkv_tc_kernel<kBlocks, kForm>>(bytes);
   if (e != cudaSuccess) return e;
   return launch_after(attention_dkv_tc_kernel<kBlocks, kForm>,
-                      dim3(bhs * ((x.a.Tk + kTile - 1) / kTile)), kThreads, 1, s, bytes, m.q, m.o,
+                      dim3(bhs * ((x.a.Tk + kTile - 1) / kTile)), kGradThreads, 1, s, bytes, m.q, m.o,
                       m.k, m.v, x);
 }
 
