@@ -146,12 +146,11 @@ Split split_keys(const AttentionCall& c, int tile_rows, int tile_keys, int resid
 }
 
 Split plan_split(const AttentionCall& c) {
-  const int rows = static_cast<int>(c.Tq * (c.H / c.Hkv));
   if (attention_tc_takes(c)) {
     const int n = attention_tc_rows(c);
     return split_keys(c, n, 128, 152);
   }
-  return split_keys(c, attention_simt_rows(rows), 64, 304);
+  return split_keys(c, attention_simt_rows(c.Tq * (c.H / c.Hkv), c.B * c.Hkv), 64, 608);
 }
 
 AttnArgs args_of(const AttentionCall& c, char* ws) {

@@ -7,8 +7,6 @@
 // sums over the heads of a group (gradients of keys and values) are sums over rows.
 #pragma once
 
-#include <atomic>
-
 #include "common.cuh"
 #include "internal.h"
 #include "launch.cuh"
@@ -28,6 +26,7 @@ struct AttnArgs {
   int B, Tq, Tk, H, Hkv, D, G;
   float scale, cap;
   int causal;
+  int vec;               // CUDA cores: rows are whole accesses of four
   const float* slopes;
   const int *docs, *prefix, *lengths, *first;
   const DocSpan* spans;  // [B][ceil(Tk / kDocSpan)], with docs
@@ -82,34 +81,8 @@ __device__ __forceinline__ RowSees attn_row(const AttnArgs& a, int b, int t, int
   return r;
 }
 
-// The score of a key from the product z = q k scale, and its slope by z.
-__device__ __forceinline__ float attn_capped(const AttnArgs& a, float z, float* slope) {
-  if (a.cap <= 0.f) {
-    *slope = 1.f;
-    return z;
-  }
-  const float t = tanhf(z / a.cap);
-  *slope = 1.f - t * t;
-  return t * a.cap;
-}
-
-// Allows a kernel its shared memory, once per device.
-template <auto kKernel>
-cudaError_t allow_smem(int bytes) {
-  constexpr int kMaxDev = 64;
-  static std::atomic<int> done[kMaxDev];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const bool known = dev >= 0 && dev < kMaxDev;
-  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && known) done[dev].store(1, std::memory_order_release);
-  return e;
-}
-
 // The kernels (attention_simt.cu, attention_tc.cu).
-int attention_simt_rows(int rows);
+int attention_simt_rows(long long rows, long long heads);
 cudaError_t launch_attention_simt(const AttnArgs& a, dprc_dtype dt, cudaStream_t s);
 cudaError_t launch_attention_grad_simt(const AttnArgs& a, dprc_dtype dt, cudaStream_t s);
 bool attention_tc_takes(const AttentionCall& c);

@@ -1,48 +1,134 @@
 // Attention on the CUDA cores, in fp32: fp32 inputs, and bf16 ones whose widths
 // or strides the tensor copies do not take.  The same sums as the tensor-core kernels
-// (attention_tc.cu), in tiles of 64 rows and 64 keys.
+// (attention_tc.cu), in tiles of rows and 64 keys.
 //
-// A CTA of 128 threads holds kM rows (64, or 16 where a sample has few); a thread
-// has kM / 8 rows and four keys of the product, then the same rows and four columns
-// in sixteen of the values' width.  The rows' statistics are kept by the sixteen
-// threads that share them, so the sums over keys are shuffles.  Bound by the
-// shared memory's reads for the products: 12 floats read for 32 products (64 rows).
+// A CTA has 16 groups of 16 threads.  A group has kR rows of the tile (4, or fewer where
+// that leaves SMs idle); a thread forms kR x 4 products of rows and keys (keys 16 apart,
+// so that a warp reads whole lines of banks), four of the width at a time, then the
+// same rows times four of every 64 columns of the values.  A row's weights are written and
+// read by one group, so a warp's step orders them.  (Eight groups of eight rows read less
+// shared memory, but two warps a scheduler did not cover its latency: the gradient of
+// 2 x 1024 tokens, 16 heads of 64, took 1.66 ms.)
 
 #include <algorithm>
 
 #include "attention.cuh"
+#include "vec.cuh"
 
 namespace dprc {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int kGroups = kThreads / 16;
 constexpr int kN = 64;
 constexpr int kPad = 4;
 
-// rows [n] of width D from src (row stride rs, null rows are zero) into dst:
-// transposed [kD][n + kPad], or as they are [n][kD + kPad].
-template <typename T, int kRowsMax, int kD, bool kTrans, typename Src>
-__device__ __forceinline__ void load_tile(float* dst, int n, int D, Src src) {
-  for (int i = threadIdx.x; i < kRowsMax * kD; i += kThreads) {
-    const int r = i / kD, c = i - r * kD;
-    float v = 0.f;
-    if (r < n && c < D) {
-      const T* p = src(r);
-      if (p != nullptr) v = to_f32<T>(ld_once(p + c));
+__device__ __forceinline__ float4 four(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const float* p) {
+  return ld_once(reinterpret_cast<const float4*>(p));
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = ld_once(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+// Rows of width D from src(r) (null: zeros) into dst [kRows][kD + kPad], zeros behind n
+// rows and D columns.  vec: rows are whole accesses of four.
+template <typename T, int kRows, int kD, typename Src>
+__device__ __forceinline__ void load_tile(float* dst, int n, int D, bool vec, Src src) {
+  constexpr int kLanes = kD / 4, kStep = kThreads / kLanes;
+  const int c = (threadIdx.x % kLanes) * 4;
+#pragma unroll 4
+  for (int r = threadIdx.x / kLanes; r < kRows; r += kStep) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const T* p = r < n ? src(r) : nullptr;
+    if (p != nullptr) {
+      if (vec) {
+        if (c < D) v = load4(p + c);
+      } else {
+        if (c < D) v.x = to_f32<T>(ld_once(p + c));
+        if (c + 1 < D) v.y = to_f32<T>(ld_once(p + c + 1));
+        if (c + 2 < D) v.z = to_f32<T>(ld_once(p + c + 2));
+        if (c + 3 < D) v.w = to_f32<T>(ld_once(p + c + 3));
+      }
     }
-    if (kTrans) dst[c * (kRowsMax + kPad) + r] = v;
-    else dst[r * (kD + kPad) + c] = v;
+    *reinterpret_cast<float4*>(dst + r * (kD + kPad) + c) = v;
   }
 }
 
-template <int kD>
-struct FwdSmem {
-  template <int kM>
-  static constexpr int bytes() {
-    return 4 * (kD * (kM + kPad) + kD * (kN + kPad) + kN * (kD + kPad) + kN * (kM + kPad)) +
-           4 * (kM * 4 + kN);
+// acc[i][j] += row i of a times row 16 j of b, over the width (rows kD + kPad apart).
+template <int kR, int kC, int kD>
+__device__ __forceinline__ void dots(const float* a, const float* b, int D, float (&acc)[kR][kC]) {
+#pragma unroll 2
+  for (int d = 0; d < D; d += 4) {
+    float4 y[kC];
+#pragma unroll
+    for (int j = 0; j < kC; ++j) y[j] = four(b + j * 16 * (kD + kPad) + d);
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      const float4 x = four(a + i * (kD + kPad) + d);
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        acc[i][j] = fmaf(x.x, y[j].x, acc[i][j]);
+        acc[i][j] = fmaf(x.y, y[j].y, acc[i][j]);
+        acc[i][j] = fmaf(x.z, y[j].z, acc[i][j]);
+        acc[i][j] = fmaf(x.w, y[j].w, acc[i][j]);
+      }
+    }
   }
-};
+}
+
+// kR weights from p.
+template <int kR>
+__device__ __forceinline__ void load_weights(const float* p, float (&w)[kR]) {
+  if constexpr (kR >= 4) {
+#pragma unroll
+    for (int i = 0; i < kR; i += 4) {
+      const float4 v = four(p + i);
+      w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+    }
+  } else if constexpr (kR == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *p;
+  }
+}
+template <int kR>
+__device__ __forceinline__ void store_weights(float* p, const float (&w)[kR]) {
+  if constexpr (kR >= 4) {
+#pragma unroll
+    for (int i = 0; i < kR; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  } else if constexpr (kR == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(w[0], w[1]);
+  } else {
+    *p = w[0];
+  }
+}
+
+// acc[i][4 q ..] += sum over n terms of weight i (wt [n][kW]) and columns 64 q + 4 tx of v.
+template <int kR, int kO, int kD, int kW>
+__device__ __forceinline__ void add_rows(const float* wt, const float* v, int n,
+                                         float (&acc)[kR][4 * kO]) {
+#pragma unroll 2
+  for (int j = 0; j < n; ++j) {
+    float w[kR];
+    load_weights<kR>(wt + j * kW, w);
+#pragma unroll
+    for (int q = 0; q < kO; ++q) {
+      const float4 y = four(v + j * (kD + kPad) + q * 64);
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        acc[i][4 * q] = fmaf(w[i], y.x, acc[i][4 * q]);
+        acc[i][4 * q + 1] = fmaf(w[i], y.y, acc[i][4 * q + 1]);
+        acc[i][4 * q + 2] = fmaf(w[i], y.z, acc[i][4 * q + 2]);
+        acc[i][4 * q + 3] = fmaf(w[i], y.w, acc[i][4 * q + 3]);
+      }
+    }
+  }
+}
 
 __device__ __forceinline__ float half_max(float v) {
 #pragma unroll
@@ -56,12 +142,23 @@ __device__ __forceinline__ float half_sum(float v) {
 }
 
 __device__ __forceinline__ int block_max(int v, int* sm) {
-  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  v = __reduce_max_sync(0xffffffffu, v);
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = max(max(sm[0], sm[1]), max(sm[2], sm[3]));
+  for (int w = 0; w < kThreads / 32; ++w) v = max(v, sm[w]);
   __syncthreads();
   return v;
+}
+
+// The score of a product z = q k scale, and the cap's slope by z.
+__device__ __forceinline__ float capped(const AttnArgs& a, float z, float* slope) {
+  if (a.cap <= 0.f) {
+    *slope = 1.f;
+    return z;
+  }
+  const float t = 1.f - 2.f / (1.f + expf(2.f * z / a.cap));
+  *slope = 1.f - t * t;
+  return t * a.cap;
 }
 
 // Whether any row with documents in [lo, hi] may see a key of this span.
@@ -71,47 +168,22 @@ __device__ __forceinline__ bool span_meets(const AttnArgs& a, int b, int tile, i
   return s.lo <= hi && lo <= s.hi;
 }
 
-// Products of kR rows (from at, [kD][stride as]) and kC columns (from bt): acc += .
-template <int kR, int kC>
-__device__ __forceinline__ void dot_step(const float* at, const float* bt, float (&acc)[kR][kC]) {
-  float x[kR], y[kC];
-#pragma unroll
-  for (int i = 0; i < kR; i += (kR >= 4 ? 4 : 2)) {
-    if constexpr (kR >= 4) {
-      const float4 v = *reinterpret_cast<const float4*>(at + i);
-      x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(at + i);
-      x[i] = v.x; x[i + 1] = v.y;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kC; j += (kC >= 4 ? 4 : 2)) {
-    if constexpr (kC >= 4) {
-      const float4 v = *reinterpret_cast<const float4*>(bt + j);
-      y[j] = v.x; y[j + 1] = v.y; y[j + 2] = v.z; y[j + 3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(bt + j);
-      y[j] = v.x; y[j + 1] = v.y;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kR; ++i)
-#pragma unroll
-    for (int j = 0; j < kC; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
-}
+template <int kD, int kR>
+constexpr int kFwdSmem =
+    4 * ((kGroups * kR + 2 * kN) * (kD + kPad) + kN * (kGroups * kR + kPad) + kN + 8);
 
-template <typename T, int kD, int kM>
+template <typename T, int kD, int kR>
 __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnArgs a) {
   extern __shared__ float sm[];
-  constexpr int kR = kM / 8;          // rows of a thread
+  constexpr int kM = kGroups * kR;          // rows of the tile
   constexpr int kO = kD / 64;         // fours of the values' columns of a thread
-  float* qt = sm;                              // [kD][kM + kPad]
-  float* kt = qt + kD * (kM + kPad);           // [kD][kN + kPad]
-  float* vs = kt + kD * (kN + kPad);           // [kN][kD + kPad]
-  float* pt = vs + kN * (kD + kPad);           // [kN][kM + kPad]
+  constexpr int kRow = kD + kPad;
+  float* qs = sm;                     // [kM][kRow]
+  float* ks = qs + kM * kRow;         // [kN][kRow]
+  float* vs = ks + kN * kRow;         // [kN][kRow]
+  float* pt = vs + kN * kRow;         // [kN][kM + kPad]
   int* kdoc = reinterpret_cast<int*>(pt + kN * (kM + kPad));  // [kN]
-  int* red = kdoc + kN;                        // [4]
+  int* red = kdoc + kN;               // [8]
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.y / a.Hkv, hk = blockIdx.y - b * a.Hkv;
@@ -121,8 +193,9 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnArgs
   const T* Q = static_cast<const T*>(a.Q) + b * a.qb;
   const T* K = static_cast<const T*>(a.K) + b * a.kb + hk * a.kh;
   const T* V = static_cast<const T*>(a.V) + b * a.vb + hk * a.vh;
+  const bool vec = a.vec != 0;
 
-  load_tile<T, kM, kD, true>(qt, min(kM, rows - p0), a.D, [&](int r) {
+  load_tile<T, kM, kD>(qs, min(kM, rows - p0), a.D, vec, [&](int r) {
     const int p = p0 + r, t = p / a.G;
     return Q + t * a.qt + (hk * a.G + p - t * a.G) * a.qh;
   });
@@ -168,8 +241,8 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnArgs
     const int j0 = tile * kN;
     const int n = min(kN, min(keys, top) - j0);  // keys that no row sees are not read
     __syncthreads();
-    load_tile<T, kN, kD, true>(kt, n, a.D, [&](int r) { return K + (j0 + r) * a.kt; });
-    load_tile<T, kN, kD, false>(vs, n, a.D, [&](int r) -> const T* {
+    load_tile<T, kN, kD>(ks, n, a.D, vec, [&](int r) { return K + (j0 + r) * a.kt; });
+    load_tile<T, kN, kD>(vs, n, a.D, vec, [&](int r) -> const T* {
       return key_is(j0 + r) ? V + (j0 + r) * a.vt : nullptr;
     });
     if (a.docs != nullptr && threadIdx.x < kN)
@@ -181,19 +254,17 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnArgs
     for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < a.D; ++d)
-      dot_step<kR, 4>(qt + d * (kM + kPad) + ty * kR, kt + d * (kN + kPad) + tx * 4, s);
+    dots<kR, 4, kD>(qs + ty * kR * kRow, ks + tx * kRow, a.D, s);
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
       float top_s = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int key = j0 + tx * 4 + j;
+        const int col = tx + 16 * j, key = j0 + col;
         float unused;
-        float z = attn_capped(a, s[i][j] * a.scale, &unused);
+        float z = capped(a, s[i][j] * a.scale, &unused);
         z -= slope[i] * fabsf(static_cast<float>(see[i].pos - key));
-        const bool ok = key < see[i].lim && (a.docs == nullptr || kdoc[tx * 4 + j] == see[i].doc);
+        const bool ok = key < see[i].lim && (a.docs == nullptr || kdoc[col] == see[i].doc);
         s[i][j] = ok ? z : -INFINITY;
         top_s = fmaxf(top_s, s[i][j]);
       }
@@ -205,30 +276,21 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnArgs
       for (int j = 0; j < 4; ++j) {
         s[i][j] = expf(s[i][j] - at);
         sum += s[i][j];
-        pt[(tx * 4 + j) * (kM + kPad) + ty * kR + i] = s[i][j];
       }
       l[i] = l[i] * f + half_sum(sum);
       m[i] = mn;
 #pragma unroll
       for (int c = 0; c < 4 * kO; ++c) o[i][c] *= f;
     }
-    __syncwarp();  // (a row's weights are written and read by one half warp)
-#pragma unroll 2
-    for (int j = 0; j < n; ++j) {
 #pragma unroll
-      for (int q = 0; q < kO; ++q) {
-        float acc[kR][4];
+    for (int j = 0; j < 4; ++j) {
+      float w[kR];
 #pragma unroll
-        for (int i = 0; i < kR; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[i][c] = o[i][q * 4 + c];
-        dot_step<kR, 4>(pt + j * (kM + kPad) + ty * kR, vs + j * (kD + kPad) + q * 64 + tx * 4, acc);
-#pragma unroll
-        for (int i = 0; i < kR; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) o[i][q * 4 + c] = acc[i][c];
-      }
+      for (int i = 0; i < kR; ++i) w[i] = s[i][j];
+      store_weights<kR>(pt + (tx + 16 * j) * (kM + kPad) + ty * kR, w);
     }
+    __syncwarp();  // (a row's weights are written and read by one half warp)
+    add_rows<kR, kO, kD, kM + kPad>(pt + ty * kR, vs + tx * 4, n, o);
   }
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
@@ -262,36 +324,36 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnArgs
 // delta = sum of dO O over a row (attention.cu).  Two kernels, which form P twice and
 // so need neither sums from several CTAs in an order nor partial results.
 // ---------------------------------------------------------------------------
-constexpr int kMB = 32;  // rows of a step of the keys' kernel
-
-template <int kD>
-constexpr int kDqSmem = 4 * (4 * kD * (kN + kPad) + kN * (kD + kPad) + kN * (kN + kPad) + kN + 8);
-template <int kD>
+template <int kD, int kR>
+constexpr int kDqSmem = 4 * ((2 * kGroups * kR + 2 * kN) * (kD + kPad) + kN * (kGroups * kR + kPad) + kN + 8);
+// rows of a step of the keys' kernel
+constexpr int kMB = 64;
+template <int kD, int kR>
 constexpr int kDkvSmem =
-    4 * (2 * kD * (kN + kPad) + 2 * kD * (kMB + kPad) + 2 * kMB * (kD + kPad) + 2 * kMB * (kN + kPad) + 6 * kMB + 8);
+    4 * ((2 * kGroups * kR + 2 * kMB) * (kD + kPad) + 2 * kMB * (kGroups * kR + kPad) + 6 * kMB + 8);
 
-template <typename T, int kD>
+template <typename T, int kD, int kR>
 __global__ void __launch_bounds__(kThreads) attention_dq_simt_kernel(const AttnArgs a) {
   extern __shared__ float sm[];
-  constexpr int kR = 8, kO = kD / 64, kS = kN + kPad;
-  float* qt = sm;
-  float* ot = qt + kD * kS;
-  float* kt = ot + kD * kS;
-  float* vt = kt + kD * kS;
-  float* ks = vt + kD * kS;              // [kN][kD + kPad]
-  float* st = ks + kN * (kD + kPad);     // [kN][kS]
-  int* kdoc = reinterpret_cast<int*>(st + kN * kS);
+  constexpr int kM = kGroups * kR, kO = kD / 64, kRow = kD + kPad, kW = kM + kPad;
+  float* qs = sm;                        // [kM][kRow]
+  float* os = qs + kM * kRow;
+  float* ks = os + kM * kRow;            // [kN][kRow]
+  float* vs = ks + kN * kRow;
+  float* st = vs + kN * kRow;            // [kN][kW]
+  int* kdoc = reinterpret_cast<int*>(st + kN * kW);
   int* red = kdoc + kN;
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.y / a.Hkv, hk = blockIdx.y - b * a.Hkv;
-  const int rows = a.Tq * a.G, p0 = blockIdx.x * kN;
+  const int rows = a.Tq * a.G, p0 = blockIdx.x * kM;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int keys = attn_keys(a, b), first = attn_first(a, b);
   const T* Q = static_cast<const T*>(a.Q) + b * a.qb;
   const T* K = static_cast<const T*>(a.K) + b * a.kb + hk * a.kh;
   const T* V = static_cast<const T*>(a.V) + b * a.vb + hk * a.vh;
-  const T* dO = static_cast<const T*>(a.dO);
+  const T* dO = static_cast<const T*>(a.dO) + b * a.dob;
+  const bool vec = a.vec != 0;
   RowSees see[kR];
   float slope[kR], lse[kR], delta[kR];
   int top = 0, dlo = 0x7fffffff, dhi = -1;
@@ -317,20 +379,14 @@ __global__ void __launch_bounds__(kThreads) attention_dq_simt_kernel(const AttnA
   top = block_max(top, red);
   dhi = block_max(dhi, red);
   dlo = ~block_max(~dlo, red);
-  // rows that see nothing: what stands in them is not read
-  const auto row_of = [&](int r, int& t, int& h) {
-    const int p = p0 + r;
-    t = p / a.G;
-    h = hk * a.G + p - t * a.G;
-    return attn_row(a, b, t, keys, first).lim > 0;
-  };
-  load_tile<T, kN, kD, true>(qt, min(kN, rows - p0), a.D, [&](int r) -> const T* {
-    int t, h;
-    return row_of(r, t, h) ? Q + t * a.qt + h * a.qh : nullptr;
+  // (rows that see nothing may hold anything: their products are masked)
+  load_tile<T, kM, kD>(qs, min(kM, rows - p0), a.D, vec, [&](int r) {
+    const int p = p0 + r, t = p / a.G;
+    return Q + t * a.qt + (hk * a.G + p - t * a.G) * a.qh;
   });
-  load_tile<T, kN, kD, true>(ot, min(kN, rows - p0), a.D, [&](int r) -> const T* {
-    int t, h;
-    return row_of(r, t, h) ? dO + b * a.dob + t * a.dot + h * a.doh : nullptr;
+  load_tile<T, kM, kD>(os, min(kM, rows - p0), a.D, vec, [&](int r) {
+    const int p = p0 + r, t = p / a.G;
+    return dO + t * a.dot + (hk * a.G + p - t * a.G) * a.doh;
   });
   float dq[kR][4 * kO];
 #pragma unroll
@@ -346,12 +402,10 @@ __global__ void __launch_bounds__(kThreads) attention_dq_simt_kernel(const AttnA
     const int j0 = tile * kN;
     const int n = min(kN, min(keys, top) - j0);
     __syncthreads();
-    const auto k_row = [&](int r) -> const T* {
+    load_tile<T, kN, kD>(ks, n, a.D, vec, [&](int r) -> const T* {
       return key_is(j0 + r) ? K + (j0 + r) * a.kt : nullptr;
-    };
-    load_tile<T, kN, kD, true>(kt, n, a.D, k_row);
-    load_tile<T, kN, kD, false>(ks, n, a.D, k_row);
-    load_tile<T, kN, kD, true>(vt, n, a.D, [&](int r) { return V + (j0 + r) * a.vt; });
+    });
+    load_tile<T, kN, kD>(vs, n, a.D, vec, [&](int r) { return V + (j0 + r) * a.vt; });
     if (a.docs != nullptr && threadIdx.x < kN)
       kdoc[threadIdx.x] = j0 + static_cast<int>(threadIdx.x) < a.Tk
                               ? a.docs[static_cast<long long>(b) * a.Tk + j0 + threadIdx.x] : -1;
@@ -361,39 +415,24 @@ __global__ void __launch_bounds__(kThreads) attention_dq_simt_kernel(const AttnA
     for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = dp[i][j] = 0.f;
-#pragma unroll 2
-    for (int d = 0; d < a.D; ++d) {
-      dot_step<kR, 4>(qt + d * kS + ty * kR, kt + d * kS + tx * 4, s);
-      dot_step<kR, 4>(ot + d * kS + ty * kR, vt + d * kS + tx * 4, dp);
-    }
+    dots<kR, 4, kD>(qs + ty * kR * kRow, ks + tx * kRow, a.D, s);
+    dots<kR, 4, kD>(os + ty * kR * kRow, vs + tx * kRow, a.D, dp);
 #pragma unroll
-    for (int i = 0; i < kR; ++i)
+    for (int j = 0; j < 4; ++j) {
+      const int col = tx + 16 * j, key = j0 + col;
+      float w[kR];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int key = j0 + tx * 4 + j;
+      for (int i = 0; i < kR; ++i) {
         float sl;
-        float z = attn_capped(a, s[i][j] * a.scale, &sl);
+        float z = capped(a, s[i][j] * a.scale, &sl);
         z -= slope[i] * fabsf(static_cast<float>(see[i].pos - key));
-        const bool ok = key < see[i].lim && (a.docs == nullptr || kdoc[tx * 4 + j] == see[i].doc);
-        const float ds = expf(z - lse[i]) * (dp[i][j] - delta[i]) * sl * a.scale;
-        st[(tx * 4 + j) * kS + ty * kR + i] = ok ? ds : 0.f;
+        const bool ok = key < see[i].lim && (a.docs == nullptr || kdoc[col] == see[i].doc);
+        w[i] = ok ? expf(z - lse[i]) * (dp[i][j] - delta[i]) * sl * a.scale : 0.f;
       }
-    __syncwarp();
-    for (int j = 0; j < n; ++j) {
-#pragma unroll
-      for (int q = 0; q < kO; ++q) {
-        float acc[kR][4];
-#pragma unroll
-        for (int i = 0; i < kR; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[i][c] = dq[i][q * 4 + c];
-        dot_step<kR, 4>(st + j * kS + ty * kR, ks + j * (kD + kPad) + q * 64 + tx * 4, acc);
-#pragma unroll
-        for (int i = 0; i < kR; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) dq[i][q * 4 + c] = acc[i][c];
-      }
+      store_weights<kR>(st + col * kW + ty * kR, w);
     }
+    __syncwarp();
+    add_rows<kR, kO, kD, kW>(st + ty * kR, ks + tx * 4, n, dq);
   }
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
@@ -408,19 +447,18 @@ __global__ void __launch_bounds__(kThreads) attention_dq_simt_kernel(const AttnA
   }
 }
 
-template <typename T, int kD>
+// A thread's "rows" are keys here, and its columns rows of queries.
+template <typename T, int kD, int kR>
 __global__ void __launch_bounds__(kThreads) attention_dkv_simt_kernel(const AttnArgs a) {
   extern __shared__ float sm[];
-  constexpr int kR = 8, kO = kD / 64, kS = kN + kPad, kSB = kMB + kPad;
-  float* kt = sm;                          // [kD][kS]
-  float* vt = kt + kD * kS;
-  float* qt = vt + kD * kS;                // [kD][kSB]
-  float* ot = qt + kD * kSB;
-  float* qs = ot + kD * kSB;               // [kMB][kD + kPad]
-  float* os = qs + kMB * (kD + kPad);
-  float* pt = os + kMB * (kD + kPad);      // [kMB][kS]
-  float* st = pt + kMB * kS;
-  float* rlse = st + kMB * kS;             // of the step's rows
+  constexpr int kM = kGroups * kR, kO = kD / 64, kRow = kD + kPad, kW = kM + kPad;
+  float* ks = sm;                          // [kM][kRow]
+  float* vs = ks + kM * kRow;
+  float* qs = vs + kM * kRow;              // [kMB][kRow]
+  float* os = qs + kMB * kRow;
+  float* pt = os + kMB * kRow;             // [kMB][kW]
+  float* st = pt + kMB * kW;
+  float* rlse = st + kMB * kW;             // of the step's rows
   float* rdel = rlse + kMB;
   float* rslope = rdel + kMB;
   int* rpos = reinterpret_cast<int*>(rslope + kMB);
@@ -429,26 +467,22 @@ __global__ void __launch_bounds__(kThreads) attention_dkv_simt_kernel(const Attn
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.y / a.Hkv, hk = blockIdx.y - b * a.Hkv;
-  const int rows = a.Tq * a.G, j0 = blockIdx.x * kN;
+  const int rows = a.Tq * a.G, j0 = blockIdx.x * kM;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int keys = attn_keys(a, b), first = attn_first(a, b);
   const T* Q = static_cast<const T*>(a.Q) + b * a.qb;
   const T* K = static_cast<const T*>(a.K) + b * a.kb + hk * a.kh;
   const T* V = static_cast<const T*>(a.V) + b * a.vb + hk * a.vh;
-  const T* dO = static_cast<const T*>(a.dO);
-  const int n = max(0, min(kN, keys - j0));
+  const T* dO = static_cast<const T*>(a.dO) + b * a.dob;
+  const bool vec = a.vec != 0;
+  const int n = max(0, min(kM, keys - j0));
   const int* docs = a.docs != nullptr ? a.docs + static_cast<long long>(b) * a.Tk : nullptr;
   DocSpan span = {0, 0, 0, 0};
   if (docs != nullptr)
-    span = a.spans[static_cast<long long>(b) * ((a.Tk + kDocSpan - 1) / kDocSpan) + blockIdx.x];
-  // keys of no document may hold anything
-  const auto key_is = [&](int r) { return docs == nullptr || docs[j0 + r] >= 0; };
-  load_tile<T, kN, kD, true>(kt, n, a.D, [&](int r) -> const T* {
-    return key_is(r) ? K + (j0 + r) * a.kt : nullptr;
-  });
-  load_tile<T, kN, kD, true>(vt, n, a.D, [&](int r) -> const T* {
-    return key_is(r) ? V + (j0 + r) * a.vt : nullptr;
-  });
+    span = a.spans[static_cast<long long>(b) * ((a.Tk + kDocSpan - 1) / kDocSpan) + j0 / kDocSpan];
+  // (keys that nobody sees may hold anything: their products are masked)
+  load_tile<T, kM, kD>(ks, n, a.D, vec, [&](int r) { return K + (j0 + r) * a.kt; });
+  load_tile<T, kM, kD>(vs, n, a.D, vec, [&](int r) { return V + (j0 + r) * a.vt; });
   int kdoc[kR];
 #pragma unroll
   for (int i = 0; i < kR; ++i)
@@ -484,69 +518,44 @@ __global__ void __launch_bounds__(kThreads) attention_dkv_simt_kernel(const Attn
       any = r.lim > j0 && (docs == nullptr || (r.doc >= span.lo && r.doc <= span.hi));
     }
     if (!__syncthreads_or(any)) continue;
-    const auto q_row = [&](int r) -> const T* {
+    // rows that see nothing are not read: they are summed over
+    const int nr = min(kMB, rows - p0);
+    load_tile<T, kMB, kD>(qs, nr, a.D, vec, [&](int r) -> const T* {
       const int p = p0 + r, t = p / a.G;
       return rlim[r] > 0 ? Q + t * a.qt + (hk * a.G + p - t * a.G) * a.qh : nullptr;
-    };
-    const auto o_row = [&](int r) -> const T* {
-      const int p = p0 + r, t = p / a.G, h = hk * a.G + p - t * a.G;
-      return rlim[r] > 0 ? dO + b * a.dob + t * a.dot + h * a.doh : nullptr;
-    };
-    const int nr = min(kMB, rows - p0);
-    load_tile<T, kMB, kD, true>(qt, nr, a.D, q_row);
-    load_tile<T, kMB, kD, true>(ot, nr, a.D, o_row);
-    load_tile<T, kMB, kD, false>(qs, nr, a.D, q_row);
-    load_tile<T, kMB, kD, false>(os, nr, a.D, o_row);
+    });
+    load_tile<T, kMB, kD>(os, nr, a.D, vec, [&](int r) -> const T* {
+      const int p = p0 + r, t = p / a.G;
+      return rlim[r] > 0 ? dO + t * a.dot + (hk * a.G + p - t * a.G) * a.doh : nullptr;
+    });
     __syncthreads();
-    float s[kR][2], dp[kR][2];
+    float s[kR][4], dp[kR][4];
 #pragma unroll
     for (int i = 0; i < kR; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) s[i][j] = dp[i][j] = 0.f;
-#pragma unroll 2
-    for (int d = 0; d < a.D; ++d) {
-      dot_step<kR, 2>(kt + d * kS + ty * kR, qt + d * kSB + tx * 2, s);
-      dot_step<kR, 2>(vt + d * kS + ty * kR, ot + d * kSB + tx * 2, dp);
-    }
+      for (int j = 0; j < 4; ++j) s[i][j] = dp[i][j] = 0.f;
+    dots<kR, 4, kD>(ks + ty * kR * kRow, qs + tx * kRow, a.D, s);
+    dots<kR, 4, kD>(vs + ty * kR * kRow, os + tx * kRow, a.D, dp);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = tx * 2 + j;
+    for (int j = 0; j < 4; ++j) {
+      const int r = tx + 16 * j;
+      float w[kR], u[kR];
 #pragma unroll
       for (int i = 0; i < kR; ++i) {
         const int key = j0 + ty * kR + i;
         float sl;
-        float z = attn_capped(a, s[i][j] * a.scale, &sl);
+        float z = capped(a, s[i][j] * a.scale, &sl);
         z -= rslope[r] * fabsf(static_cast<float>(rpos[r] - key));
         const bool ok = key < rlim[r] && (docs == nullptr || kdoc[i] == rdoc[r]);
-        const float p = ok ? expf(z - rlse[r]) : 0.f;
-        pt[r * kS + ty * kR + i] = p;
-        st[r * kS + ty * kR + i] = ok ? p * (dp[i][j] - rdel[r]) * sl * a.scale : 0.f;
+        w[i] = ok ? expf(z - rlse[r]) : 0.f;
+        u[i] = ok ? w[i] * (dp[i][j] - rdel[r]) * sl * a.scale : 0.f;
       }
+      store_weights<kR>(pt + r * kW + ty * kR, w);
+      store_weights<kR>(st + r * kW + ty * kR, u);
     }
     __syncwarp();
-    for (int r = 0; r < nr; ++r) {
-#pragma unroll
-      for (int q = 0; q < kO; ++q) {
-        float acc[kR][4];
-#pragma unroll
-        for (int i = 0; i < kR; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[i][c] = dv[i][q * 4 + c];
-        dot_step<kR, 4>(pt + r * kS + ty * kR, os + r * (kD + kPad) + q * 64 + tx * 4, acc);
-#pragma unroll
-        for (int i = 0; i < kR; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            dv[i][q * 4 + c] = acc[i][c];
-            acc[i][c] = dk[i][q * 4 + c];
-          }
-        dot_step<kR, 4>(st + r * kS + ty * kR, qs + r * (kD + kPad) + q * 64 + tx * 4, acc);
-#pragma unroll
-        for (int i = 0; i < kR; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) dk[i][q * 4 + c] = acc[i][c];
-      }
-    }
+    add_rows<kR, kO, kD, kW>(pt + ty * kR, os + tx * 4, nr, dv);
+    add_rows<kR, kO, kD, kW>(st + ty * kR, qs + tx * 4, nr, dk);
   }
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
@@ -564,51 +573,95 @@ __global__ void __launch_bounds__(kThreads) attention_dkv_simt_kernel(const Attn
   }
 }
 
+// Rows of a group: four, or two where the tiles would not fill the SMs twice; one for few rows.
+int rows_of_group(long long rows, long long heads, bool one) {
+  const auto ctas = [&](int r) { return (rows + kGroups * r - 1) / (kGroups * r) * heads; };
+  if (one && rows <= 16) return 1;
+  return ctas(4) >= 304 ? 4 : 2;
+}
 
-template <typename T, int kD, int kM>
+template <typename T, int kD, int kR>
 cudaError_t forward(const AttnArgs& a, cudaStream_t s) {
-  constexpr int bytes = FwdSmem<kD>::template bytes<kM>();
-  cudaError_t e = allow_smem<attention_simt_kernel<T, kD, kM>>(bytes);
+  constexpr int bytes = kFwdSmem<kD, kR>;
+  const cudaError_t e = allow_smem<attention_simt_kernel<T, kD, kR>>(bytes);
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.Tq * a.G + kM - 1) / kM, a.B * a.Hkv, a.splits);
-  return launch_after(attention_simt_kernel<T, kD, kM>, grid, kThreads, 1, s, bytes, a);
+  const dim3 grid((a.Tq * a.G + kGroups * kR - 1) / (kGroups * kR), a.B * a.Hkv, a.splits);
+  return launch_after(attention_simt_kernel<T, kD, kR>, grid, kThreads, 1, s, bytes, a);
+}
+
+template <typename T, int kD>
+cudaError_t forward_rows(const AttnArgs& a, cudaStream_t s) {
+  switch (attention_simt_rows(a.Tq * a.G, a.B * a.Hkv)) {
+    case 16: return forward<T, kD, 1>(a, s);
+    case 32: return forward<T, kD, 2>(a, s);
+  }
+  return forward<T, kD, 4>(a, s);
+}
+
+template <typename T, int kD, int kR>
+cudaError_t rows_grad(const AttnArgs& a, cudaStream_t s) {
+  constexpr int bytes = kDqSmem<kD, kR>;
+  const cudaError_t e = allow_smem<attention_dq_simt_kernel<T, kD, kR>>(bytes);
+  if (e != cudaSuccess) return e;
+  return launch_after(attention_dq_simt_kernel<T, kD, kR>,
+                      dim3((a.Tq * a.G + kGroups * kR - 1) / (kGroups * kR), a.B * a.Hkv), kThreads, 1, s,
+                      bytes, a);
+}
+template <typename T, int kD, int kR>
+cudaError_t keys_grad(const AttnArgs& a, cudaStream_t s) {
+  constexpr int bytes = kDkvSmem<kD, kR>;
+  const cudaError_t e = allow_smem<attention_dkv_simt_kernel<T, kD, kR>>(bytes);
+  if (e != cudaSuccess) return e;
+  return launch_after(attention_dkv_simt_kernel<T, kD, kR>,
+                      dim3((a.Tk + kGroups * kR - 1) / (kGroups * kR), a.B * a.Hkv), kThreads, 1, s, bytes, a);
 }
 
 template <typename T, int kD>
 cudaError_t backward(const AttnArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
   if (a.dQ != nullptr) {
-    if ((e = allow_smem<attention_dq_simt_kernel<T, kD>>(kDqSmem<kD>)) != cudaSuccess) return e;
-    e = launch_after(attention_dq_simt_kernel<T, kD>, dim3((a.Tq * a.G + kN - 1) / kN, a.B * a.Hkv),
-                     kThreads, 1, s, kDqSmem<kD>, a);
+    const cudaError_t e = rows_of_group(a.Tq * a.G, a.B * a.Hkv, false) == 4
+                              ? rows_grad<T, kD, 4>(a, s) : rows_grad<T, kD, 2>(a, s);
     if (e != cudaSuccess) return e;
   }
-  if (a.dK == nullptr && a.dV == nullptr) return e;
-  if ((e = allow_smem<attention_dkv_simt_kernel<T, kD>>(kDkvSmem<kD>)) != cudaSuccess) return e;
-  return launch_after(attention_dkv_simt_kernel<T, kD>, dim3((a.Tk + kN - 1) / kN, a.B * a.Hkv),
-                      kThreads, 1, s, kDkvSmem<kD>, a);
+  if (a.dK == nullptr && a.dV == nullptr) return cudaSuccess;
+  return rows_of_group(a.Tk, a.B * a.Hkv, false) == 4 ? keys_grad<T, kD, 4>(a, s)
+                                                      : keys_grad<T, kD, 2>(a, s);
+}
+
+// Whether rows of the three (gradient: four) tensors are whole accesses of four.
+template <typename T>
+bool fours(const AttnArgs& a) {
+  const long long all = a.D | a.qb | a.qt | a.qh | a.kb | a.kt | a.kh | a.vb | a.vt | a.vh |
+                        a.dob | a.dot | a.doh;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.Q) | reinterpret_cast<uintptr_t>(a.K) |
+                       reinterpret_cast<uintptr_t>(a.V) | reinterpret_cast<uintptr_t>(a.dO);
+  return all % 4 == 0 && at % (4 * sizeof(T)) == 0;
 }
 
 }  // namespace
 
-int attention_simt_rows(int rows) { return rows <= 16 ? 16 : 64; }
-
-cudaError_t launch_attention_simt(const AttnArgs& a, dprc_dtype dt, cudaStream_t s) {
-  const bool few = attention_simt_rows(a.Tq * a.G) == 16, wide = a.D > 64;
-  using bf16 = __nv_bfloat16;
-  if (dt == DPRC_F32) {
-    if (few) return wide ? forward<float, 128, 16>(a, s) : forward<float, 64, 16>(a, s);
-    return wide ? forward<float, 128, 64>(a, s) : forward<float, 64, 64>(a, s);
-  }
-  if (few) return wide ? forward<bf16, 128, 16>(a, s) : forward<bf16, 64, 16>(a, s);
-  return wide ? forward<bf16, 128, 64>(a, s) : forward<bf16, 64, 64>(a, s);
+int attention_simt_rows(long long rows, long long heads) {
+  return kGroups * rows_of_group(rows, heads, true);
 }
 
-cudaError_t launch_attention_grad_simt(const AttnArgs& a, dprc_dtype dt, cudaStream_t s) {
-  const bool wide = a.D > 64;
-  using bf16 = __nv_bfloat16;
-  if (dt == DPRC_F32) return wide ? backward<float, 128>(a, s) : backward<float, 64>(a, s);
-  return wide ? backward<bf16, 128>(a, s) : backward<bf16, 64>(a, s);
+cudaError_t launch_attention_simt(const AttnArgs& args, dprc_dtype dt, cudaStream_t s) {
+  AttnArgs a = args;
+  if (dt == DPRC_F32) {
+    a.vec = fours<float>(a);
+    return a.D > 64 ? forward_rows<float, 128>(a, s) : forward_rows<float, 64>(a, s);
+  }
+  a.vec = fours<__nv_bfloat16>(a);
+  return a.D > 64 ? forward_rows<__nv_bfloat16, 128>(a, s) : forward_rows<__nv_bfloat16, 64>(a, s);
+}
+
+cudaError_t launch_attention_grad_simt(const AttnArgs& args, dprc_dtype dt, cudaStream_t s) {
+  AttnArgs a = args;
+  if (dt == DPRC_F32) {
+    a.vec = fours<float>(a);
+    return a.D > 64 ? backward<float, 128>(a, s) : backward<float, 64>(a, s);
+  }
+  a.vec = fours<__nv_bfloat16>(a);
+  return a.D > 64 ? backward<__nv_bfloat16, 128>(a, s) : backward<__nv_bfloat16, 64>(a, s);
 }
 
 cudaError_t read_device_error_attention_simt(int32_t* out, bool reset) {

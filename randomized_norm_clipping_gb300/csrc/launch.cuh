@@ -3,6 +3,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace dprc {
@@ -32,6 +34,21 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int cl, c
   cfg.attrs = attr;
   cfg.numAttrs = cl > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Allows a kernel its shared memory, once per device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> done[kMaxDev];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kMaxDev;
+  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev].store(1, std::memory_order_release);
+  return e;
 }
 
 // Loads of such a kernel with a cache policy: coherent, and volatile, so that the

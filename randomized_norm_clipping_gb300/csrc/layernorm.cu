@@ -11,10 +11,11 @@
 // threads that own a column.
 //
 // A row is shared by G threads (a power of two), each of which holds up to kNv
-// accesses of kE elements: 16 bytes where the width allows, else single
-// elements.  Up to 32 threads sum by shuffles; more through shared memory.
+// accesses of kE elements, 16 bytes.  Up to 32 threads sum by shuffles; more through
+// shared memory.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "launch.cuh"
@@ -52,11 +53,85 @@ __device__ __forceinline__ void row_sum(float (&v)[kN], int G, float* buf, int& 
     for (int i = 0; i < kN; ++i) v[i] += b[(w0 + w) * kN + i];
 }
 
+// A row's accesses.  A width that is no multiple of kE puts the rows at any element of
+// a 16-byte access: the accesses stay whole and lie `shift` elements ahead of the row, so
+// that the first and the last hold elements of its neighbours, which are masked; only
+// what would reach behind the tensor is read element by element.  kOdd: such widths.
+template <typename T, int kE, bool kOdd>
+struct RowAccess {
+  int d, shift;
+  long long end;  // elements of the tensor
+  __device__ __forceinline__ RowAccess(int d, long long row, long long rows)
+      : d(d), shift(kOdd ? static_cast<int>(row * d % kE) : 0), end(rows * d) {}
+  // the first column of access v
+  __device__ __forceinline__ int col(int v) const { return v * kE - shift; }
+  __device__ __forceinline__ bool any(int c) const { return c < d; }
+  __device__ __forceinline__ bool whole(int c) const { return !kOdd || (c >= 0 && c + kE <= d); }
+  __device__ __forceinline__ void load(Raw<T, kE>& r, const T* p, long long row, int c) const {
+    const long long at = row * d + c;
+    if (!kOdd || at + kE <= end) {
+      r.load(p + at);
+    } else {
+      T* e = reinterpret_cast<T*>(&r);
+      for (int i = 0; i < kE; ++i) e[i] = at + i < end ? ld_once(p + at + i) : T(0.f);
+    }
+  }
+  __device__ __forceinline__ void store(T* p, long long row, int c, const float* v) const {
+    T* out = p + row * d + c;
+    if (whole(c)) {
+      store_row<kE>(out, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        if (c + e >= 0 && c + e < d) store_row<1>(out + e, v + e);
+    }
+  }
+  // the parameters from column c (a multiple of kE) on, 0 outside the row
+  __device__ __forceinline__ void whole_param(float* v, const T* p, int c) const {
+    Raw<T, kE> u;
+    u.zero();
+    if (c >= 0 && c + kE <= d) {
+      u.a = *reinterpret_cast<const decltype(u.a)*>(p + c);
+    } else if (c >= 0) {
+      T* e = reinterpret_cast<T*>(&u);
+      for (int i = 0; c + i < d; ++i) e[i] = p[c + i];
+    }
+    u.get(v);
+  }
+  // parameters of the columns, `none` where there are none
+  __device__ __forceinline__ void param(float* v, const T* p, int c, float none) const {
+    if (p == nullptr) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) v[e] = none;
+    } else if constexpr (kOdd) {
+      // of two whole accesses, c - (kE - shift) and the next, the elements from kE - shift on
+      float two[2 * kE];
+      whole_param(two, p, c + shift - kE);
+      whole_param(two + kE, p, c + shift);
+      switch (shift) {  // (the same for a row)
+#define DPRC_SHIFT(n)                                                      \
+  case n:                                                                  \
+    if constexpr (n < kE) {                                                \
+      _Pragma("unroll") for (int e = 0; e < kE; ++e) v[e] = two[kE - n + e]; \
+    }                                                                      \
+    break;
+        DPRC_SHIFT(0) DPRC_SHIFT(1) DPRC_SHIFT(2) DPRC_SHIFT(3)
+        DPRC_SHIFT(4) DPRC_SHIFT(5) DPRC_SHIFT(6) DPRC_SHIFT(7)
+#undef DPRC_SHIFT
+      }
+    } else {
+      Raw<T, kE> u;
+      u.a = *reinterpret_cast<const decltype(u.a)*>(p + c);
+      u.get(v);
+    }
+  }
+};
+
 // The variance is summed of the differences from the mean, in registers: no
 // cancellation of large means.  What the mean lost in its rounding is the mean of
 // those differences, and taken off them too: two values that agree to a half
 // step of each other still come out at full accuracy.
-template <typename T, int kE, int kNv>
+template <typename T, int kE, int kNv, bool kOdd>
 __global__ void __launch_bounds__(kLnThreads)
     layernorm_kernel(const T* x, const T* w, const T* b, long long rows, int d, int G, float eps,
                      int center, T* y, float2* stats) {
@@ -67,70 +142,81 @@ __global__ void __launch_bounds__(kLnThreads)
   const int t = threadIdx.x & (G - 1);
   const long long row = static_cast<long long>(blockIdx.x) * (blockDim.x / G) + threadIdx.x / G;
   const bool mine = row < rows;
-  const T* xr = x + (mine ? row : 0) * d;
+  const RowAccess<T, kE, kOdd> at(d, mine ? row : 0, rows);
   Raw<T, kE> raw[kNv];
 #pragma unroll
   for (int k = 0; k < kNv; ++k) {
-    const int c = (k * G + t) * kE;
-    if (mine && c < d) raw[k].load(xr + c); else raw[k].zero();
+    const int c = at.col(k * G + t);
+    if (mine && at.any(c)) at.load(raw[k], x, row, c); else raw[k].zero();
   }
+  const auto values = [&](int k, float* v, float none) {  // of access k, `none` outside the row
+    const int c = at.col(k * G + t);
+    raw[k].get(v);
+    if (!at.whole(c)) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        if (c + e < 0 || c + e >= d) v[e] = none;
+    }
+  };
   const float inv = 1.f / static_cast<float>(d);
   float mean = 0.f;
   if (center) {
-    float s[1] = {0.f};
+    F2 sum = f2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kNv; ++k) {
       float v[kE];
-      raw[k].get(v);
+      values(k, v, 0.f);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) s[0] += v[e];
+      for (int e = 0; e < kE; e += 2) sum = add2(sum, f2(v[e], v[e + 1]));
     }
+    float s[1], u;
+    split(sum, s[0], u);
+    s[0] += u;
     row_sum<1>(s, G, buf, turn);
     mean = s[0] * inv;
   }
-  float q[2] = {0.f, 0.f};  // sums of the differences (what the mean's rounding left) and squares
+  const F2 off = f2(-mean, -mean);
+  F2 q0 = f2(0.f, 0.f), q1 = q0;  // of the differences (what the mean's rounding left), squares
 #pragma unroll
   for (int k = 0; k < kNv; ++k) {
-    const int c = (k * G + t) * kE;
-    if (c < d) {
+    if (at.any(at.col(k * G + t))) {
       float v[kE];
-      raw[k].get(v);
+      values(k, v, mean);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        q[0] += v[e] - mean;
-        q[1] = fmaf(v[e] - mean, v[e] - mean, q[1]);
+      for (int e = 0; e < kE; e += 2) {
+        const F2 dm = add2(f2(v[e], v[e + 1]), off);
+        q0 = add2(q0, dm);
+        q1 = fma2(dm, dm, q1);
       }
     }
   }
+  float q[2], u;
+  split(q0, q[0], u);
+  q[0] += u;
+  split(q1, q[1], u);
+  q[1] += u;
   row_sum<2>(q, G, buf, turn);
   const float left = center ? q[0] * inv : 0.f;
   const float rstd = 1.f / sqrtf(fmaxf(q[1] * inv - left * left, 0.f) + eps);
   if (!mine) return;
   if (stats != nullptr && t == 0) stats[row] = make_float2(mean + left, rstd);
-  T* yr = y + row * d;
+  const F2 rs2 = f2(rstd, rstd), left2 = f2(-left, -left);
 #pragma unroll
   for (int k = 0; k < kNv; ++k) {
-    const int c = (k * G + t) * kE;
-    if (c >= d) continue;
-    float v[kE], g[kE];
+    const int c = at.col(k * G + t);
+    if (!at.any(c)) continue;
+    // y = (x - mean) r w + (b - left r w)
+    float v[kE], wv[kE], bv[kE];
     raw[k].get(v);
+    at.param(wv, w, c, 1.f);
+    at.param(bv, b, c, 0.f);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) v[e] = (v[e] - mean - left) * rstd;
-    if (w != nullptr) {
-      Raw<T, kE> u;
-      u.load(w + c);
-      u.get(g);
-#pragma unroll
-      for (int e = 0; e < kE; ++e) v[e] *= g[e];
+    for (int e = 0; e < kE; e += 2) {
+      const F2 rw = mul2(f2(wv[e], wv[e + 1]), rs2);
+      const F2 y2 = fma2(add2(f2(v[e], v[e + 1]), off), rw, fma2(left2, rw, f2(bv[e], bv[e + 1])));
+      split(y2, v[e], v[e + 1]);
     }
-    if (b != nullptr) {
-      Raw<T, kE> u;
-      u.load(b + c);
-      u.get(g);
-#pragma unroll
-      for (int e = 0; e < kE; ++e) v[e] += g[e];
-    }
-    store_row<kE>(yr + c, v);
+    at.store(y, row, c, v);
   }
 }
 
@@ -138,143 +224,212 @@ struct LnGradArgs {
   const float2* stats;
   const float* c;        // factors of the samples' rows, or null: 1
   long long rows;        // of a sample (blockIdx.y)
-  long long per_chunk;   // rows of a CTA
+  long long per_chunk;   // rows of a chunk
   long long T;           // rows of a sample of c
+  long long all;         // rows of the tensor
   int d, G, center, sums;
-  float* part;           // [samples][chunks][2][d]
+  int classes;           // CTAs of a chunk (odd widths: rows of one shift have a CTA of their own)
+  float* part;           // [samples][CTAs][2][d]
 };
 
-// kRows rows of a group at a time, so that one round of sums serves them.
-// kReload: a row's values are read again (from L1) after the sums, not kept.
-template <typename T, int kE, int kNv, int kRows, bool kReload>
-__global__ void __launch_bounds__(kReload ? kLnWide : kLnThreads)
+// A group of G threads takes kRows rows at a time, so that one round of sums serves
+// them, and reads the next ones before it sums.  A group's rows are a multiple of kE
+// apart where the width is odd, so that they have the same shift and a thread the same
+// columns: its weights and sums stay in registers.  kWide: a row has all 512 threads,
+// and the sums stand in shared memory, each column's where its thread alone adds to it.
+template <typename T, int kE, int kNv, int kRows, bool kOdd, bool kWide>
+__global__ void __launch_bounds__(kWide ? kLnWide : kLnThreads)
     layernorm_grad_kernel(const T* dy, const T* x, const T* w, T* dx, const LnGradArgs a) {
+  constexpr int kC = kNv * kE;
   __shared__ float buf[2 * kMaxWarps * 2 * kRows];
-  __shared__ float fold[kReload ? 1 : kLnThreads];
+  extern __shared__ float sums[];  // kWide: [2][kC][512]; else [2][d], the groups in turn
   pdl_launch_dependents();
   pdl_wait();
   int turn = 0;
   const int d = a.d, G = a.G;
   const int t = threadIdx.x & (G - 1), groups = blockDim.x / G, grp = threadIdx.x / G;
   const long long base = blockIdx.y * a.rows;  // the sample's first row
-  const long long r0 = blockIdx.x * a.per_chunk;
+  const int chunk = blockIdx.x / a.classes, cls = blockIdx.x - chunk * a.classes;
+  const long long r0 = chunk * a.per_chunk;
   const long long r1 = min(r0 + a.per_chunk, a.rows);
+  const int stride = kOdd ? max(groups, kE) : groups;
+  const long long first = r0 + cls * groups + grp;
+  const RowAccess<T, kE, kOdd> at(d, base + first, a.all);
   const float inv = 1.f / static_cast<float>(d);
-  float wsum[kNv * kE], bsum[kNv * kE];
+  float wf[kWide ? 1 : kC];
+  F2 wsum[kWide ? 1 : kC / 2], bsum[kWide ? 1 : kC / 2];
 #pragma unroll
-  for (int i = 0; i < kNv * kE; ++i) wsum[i] = bsum[i] = 0.f;
-
-  for (long long rr = r0; rr < r1; rr += groups * kRows) {  // the same for a CTA
-    Raw<T, kE> xv[kRows][kNv], gv[kRows][kNv];
-    float2 st[kRows];
-    float s[2 * kRows];
+  for (int k = 0; k < kNv; ++k) {
+    const int c = at.col(k * G + t);
+    if (!kWide && at.any(c)) at.param(wf + (kWide ? 0 : k * kE), w, c, 1.f);
+  }
+#pragma unroll
+  for (int i = 0; i < kC / 2; ++i) {
+    if constexpr (kWide)
+      reinterpret_cast<F2*>(sums)[i * kLnWide + threadIdx.x] =
+          reinterpret_cast<F2*>(sums)[(kC / 2 + i) * kLnWide + threadIdx.x] = f2(0.f, 0.f);
+    else wsum[i] = bsum[i] = f2(0.f, 0.f);
+  }
+  Raw<T, kE> xv[kRows][kNv], gv[kRows][kNv];
+  float2 st[kRows];
+  const auto fetch = [&](long long r) {
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      const long long r = rr + grp * kRows + j;
-      const bool mine = r < r1;
-      const long long row = base + (mine ? r : r0);
-      st[j] = mine ? ld_once(a.stats + row) : make_float2(0.f, 0.f);
+      const long long q = r + j * stride;
+      const bool mine = q < r1;
+      if (mine) st[j] = ld_once(a.stats + base + q);
 #pragma unroll
       for (int k = 0; k < kNv; ++k) {
-        const int c = (k * G + t) * kE;
-        if (mine && c < d) {
-          xv[j][k].load(x + row * d + c);
-          gv[j][k].load(dy + row * d + c);
+        const int c = at.col(k * G + t);
+        if (mine && at.any(c)) {
+          at.load(xv[j][k], x, base + q, c);
+          at.load(gv[j][k], dy, base + q, c);
         } else {
           xv[j][k].zero();
           gv[j][k].zero();
         }
       }
+      if (!mine) st[j] = make_float2(0.f, 0.f);
     }
-    if (dx != nullptr) {
+  };
+  // x - mu and dy of an access in pairs, 0 outside the row
+  const auto values = [&](const Raw<T, kE>& xr, const Raw<T, kE>& gr, float mu, int c, F2* dm,
+                          F2* g) {
+    float u[kE], v[kE];
+    xr.get(u);
+    gr.get(v);
+    if (!at.whole(c)) {
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        s[2 * j] = s[2 * j + 1] = 0.f;
-#pragma unroll
-        for (int k = 0; k < kNv; ++k) {
-          const int c = (k * G + t) * kE;
-          if (c >= d) continue;
-          float xf[kE], gf[kE], wf[kE];
-          xv[j][k].get(xf);
-          gv[j][k].get(gf);
-          if (w != nullptr) {
-            Raw<T, kE> u;
-            u.load(w + c);
-            u.get(wf);
-          }
-#pragma unroll
-          for (int e = 0; e < kE; ++e) {
-            const float g = w != nullptr ? gf[e] * wf[e] : gf[e];
-            s[2 * j] += g;
-            s[2 * j + 1] = fmaf(g, (xf[e] - st[j].x) * st[j].y, s[2 * j + 1]);
-          }
+      for (int e = 0; e < kE; ++e)
+        if (c + e < 0 || c + e >= d) {
+          u[e] = mu;
+          v[e] = 0.f;
         }
-      }
-      row_sum<2 * kRows>(s, G, buf, turn);
     }
+    const F2 m = f2(-mu, -mu);
+#pragma unroll
+    for (int e = 0; e < kE / 2; ++e) {
+      dm[e] = add2(f2(u[2 * e], u[2 * e + 1]), m);
+      g[e] = f2(v[2 * e], v[2 * e + 1]);
+    }
+  };
+  // the weights of access k: a wide row's are read again (from L1)
+  const auto weights = [&](int k, F2* w2) {
+    float u[kE];
+    if constexpr (kWide) at.param(u, w, at.col(k * G + t), 1.f);
+#pragma unroll
+    for (int e = 0; e < kE / 2; ++e)
+      w2[e] = kWide ? f2(u[2 * e], u[2 * e + 1]) : f2(wf[kWide ? 0 : k * kE + 2 * e],
+                                                      wf[kWide ? 0 : k * kE + 2 * e + 1]);
+  };
+  fetch(first);
+  // (the same number of rounds for every group of the CTA)
+  for (long long r = first; r - grp < r1; r += stride * kRows) {
+    F2 dm[kRows][kC / 2], g[kRows][kC / 2];  // x - mu, dy
+    float2 sc[kRows];
+    float s[2 * kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      const long long r = rr + grp * kRows + j;
-      if (r >= r1) continue;
-      const long long row = base + r;
-      const float mg = a.center ? s[2 * j] * inv : 0.f, mh = s[2 * j + 1] * inv;
-      const float f = a.c != nullptr ? a.c[row / a.T] : 1.f;
+      sc[j] = st[j];
+      F2 s0 = f2(0.f, 0.f), s1 = s0;
 #pragma unroll
       for (int k = 0; k < kNv; ++k) {
-        const int c = (k * G + t) * kE;
-        if (c >= d) continue;
-        float xf[kE], gf[kE], wf[kE], out[kE];
-        if constexpr (kReload) {
-          Raw<T, kE> u;
-          u.load(x + row * d + c);
-          u.get(xf);
-          u.load(dy + row * d + c);
-          u.get(gf);
-        } else {
-          xv[j][k].get(xf);
-          gv[j][k].get(gf);
-        }
-        if (w != nullptr) {
-          Raw<T, kE> u;
-          u.load(w + c);
-          u.get(wf);
-        }
+        const int c = at.col(k * G + t);
+        if (!at.any(c)) continue;
+        values(xv[j][k], gv[j][k], sc[j].x, c, &dm[j][k * kE / 2], &g[j][k * kE / 2]);
+        F2 w2[kE / 2];
+        weights(k, w2);
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const float xh = (xf[e] - st[j].x) * st[j].y;
-          const float g = w != nullptr ? gf[e] * wf[e] : gf[e];
-          out[e] = (g - mg - xh * mh) * st[j].y;
-          const float gc = gf[e] * f;
-          wsum[k * kE + e] = fmaf(gc, xh, wsum[k * kE + e]);
-          bsum[k * kE + e] += gc;
+        for (int e = 0; e < kE / 2; ++e) {
+          const int i = k * kE / 2 + e;
+          const F2 gw = mul2(g[j][i], w2[e]);
+          s0 = add2(s0, gw);
+          s1 = fma2(gw, dm[j][i], s1);
         }
-        if (dx != nullptr) store_row<kE>(dx + row * d + c, out);
+      }
+      float u, v;
+      split(s0, u, v);
+      s[2 * j] = u + v;
+      split(s1, u, v);
+      s[2 * j + 1] = u + v;
+    }
+    fetch(r + stride * kRows);  // the next rows are on their way while these are summed
+    if (dx != nullptr) row_sum<2 * kRows>(s, G, buf, turn);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const long long q = r + j * stride;
+      if (q >= r1) continue;
+      // dx = r g + (x - mu) (-r^3 mean(g (x - mu))) - r mean(g)
+      const float rs = sc[j].y, f = a.c != nullptr ? a.c[(base + q) / a.T] : 1.f;
+      const float along = -rs * rs * rs * (s[2 * j + 1] * inv);
+      const float rest = a.center ? -rs * (s[2 * j] * inv) : 0.f;
+      const F2 rs2 = f2(rs, rs), along2 = f2(along, along), rest2 = f2(rest, rest);
+      const F2 fr2 = f2(f * rs, f * rs), f22 = f2(f, f);
+#pragma unroll
+      for (int k = 0; k < kNv; ++k) {
+        const int c = at.col(k * G + t);
+        if (!at.any(c)) continue;
+        float out[kE];
+        F2 w2[kE / 2];
+        weights(k, w2);
+#pragma unroll
+        for (int e = 0; e < kE / 2; ++e) {
+          const int i = k * kE / 2 + e;
+          const F2 o = fma2(dm[j][i], along2, fma2(mul2(g[j][i], w2[e]), rs2, rest2));
+          split(o, out[2 * e], out[2 * e + 1]);
+          const F2 gx = mul2(g[j][i], fr2);
+          if constexpr (kWide) {
+            F2* ws = reinterpret_cast<F2*>(sums) + i * kLnWide + threadIdx.x;
+            F2* bs = ws + kC / 2 * kLnWide;
+            *ws = fma2(gx, dm[j][i], *ws);
+            *bs = fma2(g[j][i], f22, *bs);
+          } else {
+            wsum[i] = fma2(gx, dm[j][i], wsum[i]);
+            bsum[i] = fma2(g[j][i], f22, bsum[i]);
+          }
+        }
+        if (dx != nullptr) at.store(dx, base + q, c, out);
       }
     }
   }
   if (!a.sums) return;
-  // the groups of the CTA in order
   float* part = a.part + (blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x) * 2 * d;
+  // the groups of the CTA in order, each adding its columns
+  for (int q = 0; q < groups; ++q) {
+    if (grp == q) {
 #pragma unroll
-  for (int i = 0; i < 2 * kNv * kE; ++i) {
-    float v = i < kNv * kE ? wsum[i < kNv * kE ? i : 0] : bsum[i < kNv * kE ? 0 : i - kNv * kE];
-    if (!kReload && groups > 1) {
-      __syncthreads();
-      fold[threadIdx.x] = v;
-      __syncthreads();
-      if (grp != 0) continue;
-      for (int q = 1; q < groups; ++q) v += fold[q * G + t];
+      for (int i = 0; i < kC / 2; ++i) {
+        float wv[2], bv[2];
+        if constexpr (kWide) {
+          split(reinterpret_cast<F2*>(sums)[i * kLnWide + threadIdx.x], wv[0], wv[1]);
+          split(reinterpret_cast<F2*>(sums)[(kC / 2 + i) * kLnWide + threadIdx.x], bv[0], bv[1]);
+        } else {
+          split(wsum[i], wv[0], wv[1]);
+          split(bsum[i], bv[0], bv[1]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c = at.col(2 * i / kE * G + t) + (2 * i + u) % kE;
+          if (c < 0 || c >= d) continue;
+          if (q > 0) {
+            wv[u] += sums[c];
+            bv[u] += sums[d + c];
+          }
+          float* out = q + 1 < groups ? sums : part;
+          out[c] = wv[u];
+          out[d + c] = bv[u];
+        }
+      }
     }
-    const int m = i % (kNv * kE), c = ((m / kE) * G + t) * kE + m % kE;
-    if (c < d && DPRC_IN(c >= 0)) part[(i < kNv * kE ? 0 : d) + c] = v;
+    if (q + 1 < groups) __syncthreads();
   }
 }
 
-constexpr int kFinWarps = 8;
+constexpr int kFinWarps = 32;
 
 // The samples' sums over their chunks, 32 columns of the weight's (blockIdx.y 0)
-// or the bias's a CTA: their squares, and the sum over the samples times c.  A
-// warp takes every eighth chunk of a sample (few samples) or every eighth sample.
+// or the bias's a CTA: their squares, and the sum over the samples times c.  A warp
+// takes every 32nd chunk of a sample (few samples) or every 32nd sample.
 template <typename T>
 __global__ void __launch_bounds__(32 * kFinWarps)
     layernorm_finish_kernel(const float* part, const float* c, int B, int chunks, int d, T* dw,
@@ -311,7 +466,7 @@ __global__ void __launch_bounds__(32 * kFinWarps)
       if (lane == 0) np[i] = q;
     }
   };
-  if (B < 8 * kFinWarps) {
+  if (B < 2 * kFinWarps) {
     for (int i = 0; i < B; ++i) {
       sm[i & 1][warp][lane] = chunk_sum(i, warp, kFinWarps);
       __syncthreads();
@@ -361,18 +516,42 @@ bool whole_vectors(int64_t d) {
   return d % kVec16<T> == 0;
 }
 
-// Chunks of rows: as many CTAs as are resident twice over, at least 8 rows each.
+// Chunks of rows: as many CTAs as are resident (two to an SM), at least 16 rows each.
+// Odd widths: up to `classes` CTAs a chunk.
 struct LnPlan {
   int64_t samples, rows, chunks, per_chunk;
 };
-LnPlan plan_grad(int64_t B, int64_t T, bool by_sample) {
+LnPlan plan_grad(int64_t B, int64_t T, bool by_sample, int64_t classes) {
   LnPlan p;
   p.samples = by_sample ? B : 1;
   p.rows = by_sample ? T : B * T;
-  const int64_t want = std::max<int64_t>(1, 4 * 152 / p.samples);
-  p.per_chunk = std::max<int64_t>(16, (p.rows + want - 1) / want);
+  const int64_t want = std::max<int64_t>(1, 2 * 152 / (p.samples * classes));
+  p.per_chunk = std::max<int64_t>(16 * classes, (p.rows + want - 1) / want);
   p.chunks = std::max<int64_t>(1, (p.rows + p.per_chunk - 1) / p.per_chunk);
   return p;
+}
+
+// Threads of a row and accesses of a thread: `acc` accesses of kE elements.
+struct RowShape {
+  bool odd;
+  int G;
+  int64_t nv;
+};
+template <typename T>
+RowShape grad_shape(int64_t d) {
+  constexpr int kV = kVec16<T>;
+  RowShape r;
+  r.odd = !whole_vectors<T>(d);
+  const int64_t acc = (d + kV - 1) / kV + (r.odd ? 1 : 0);  // (a shift adds one)
+  r.G = acc * kV > kLnThreads * 16 ? kLnWide : pow2_at_least(acc, 8, kLnThreads);
+  r.nv = (acc + r.G - 1) / r.G;
+  return r;
+}
+template <typename T>
+int64_t grad_classes(int64_t d) {
+  const RowShape r = grad_shape<T>(d);
+  const int groups = r.G == kLnWide ? 1 : kLnThreads / r.G;
+  return r.odd ? std::max(1, kVec16<T> / groups) : 1;
 }
 
 template <typename T>
@@ -383,11 +562,10 @@ cudaError_t forward(const LayernormCall& c, cudaStream_t s) {
   const T* b = static_cast<const T*>(c.bias);
   T* y = static_cast<T*>(c.Y);
   constexpr int kV = kVec16<T>;
-  const bool vec = whole_vectors<T>(d);
-  const int e = vec ? kV : 1;
-  const int64_t acc = (d + e - 1) / e;  // accesses of a row
+  const bool odd = !whole_vectors<T>(d);
+  const int64_t acc = (d + kV - 1) / kV + (odd ? 1 : 0);  // accesses of a row (a shift adds one)
   // a warp or less a row while its share fits 64 registers, else a CTA
-  const int G = acc * e <= 32 * 64 ? pow2_at_least(acc, 8, 32) : kLnThreads;
+  const int G = acc * kV <= 32 * 64 ? pow2_at_least(acc, 8, 32) : kLnThreads;
   const int64_t nv = (acc + G - 1) / G;
   const int64_t per = kLnThreads / G;
   const dim3 grid(static_cast<unsigned>((rows + per - 1) / per));
@@ -396,27 +574,25 @@ cudaError_t forward(const LayernormCall& c, cudaStream_t s) {
     return launch_after(kernel, grid, kLnThreads, 1, s, 0, x, w, b, static_cast<long long>(rows),
                         static_cast<int>(d), G, c.eps, c.center, y, st);
   };
-  if (vec) {
-    if (nv <= 1) return go(layernorm_kernel<T, kV, 1>);
-    if (nv <= 2) return go(layernorm_kernel<T, kV, 2>);
-    if (nv <= 4) return go(layernorm_kernel<T, kV, 4>);
-    if (nv <= 8) return go(layernorm_kernel<T, kV, 8>);
-    if constexpr (kV == 4) return go(layernorm_kernel<T, kV, 16>);
-  }
-  if (nv <= 4) return go(layernorm_kernel<T, 1, 4>);
-  if (nv <= 16) return go(layernorm_kernel<T, 1, 16>);
-  return go(layernorm_kernel<T, 1, 64>);
+  const auto by_odd = [&](auto n) {
+    constexpr int kN = decltype(n)::value;
+    return odd ? go(layernorm_kernel<T, kV, kN, true>) : go(layernorm_kernel<T, kV, kN, false>);
+  };
+  if (nv <= 1) return by_odd(std::integral_constant<int, 1>{});
+  if (nv <= 2) return by_odd(std::integral_constant<int, 2>{});
+  if (nv <= 4) return by_odd(std::integral_constant<int, 4>{});
+  if (nv <= 8) return by_odd(std::integral_constant<int, 8>{});
+  // (bf16: 16384 of an odd width have one access more than 256 threads of eight)
+  return by_odd(std::integral_constant<int, kV == 4 ? 17 : 9>{});
 }
 
 template <typename T>
 cudaError_t backward(const LayernormGradCall& c, void* ws, cudaStream_t s) {
   const bool by_sample = c.n != nullptr;
-  const LnPlan p = plan_grad(c.B, c.T, by_sample);
-  const int64_t d = c.d;
+  const int64_t d = c.d, classes = grad_classes<T>(d);
+  const RowShape shape = grad_shape<T>(d);
+  const LnPlan p = plan_grad(c.B, c.T, by_sample, classes);
   constexpr int kV = kVec16<T>;
-  const bool vec = whole_vectors<T>(d);
-  const int e = vec ? kV : 1;
-  const int64_t acc = (d + e - 1) / e;
   const bool sums = c.dW != nullptr || c.db != nullptr || by_sample;
   LnGradArgs a;
   a.stats = reinterpret_cast<const float2*>(c.stats);
@@ -424,42 +600,62 @@ cudaError_t backward(const LayernormGradCall& c, void* ws, cudaStream_t s) {
   a.rows = p.rows;
   a.per_chunk = p.per_chunk;
   a.T = std::max<int64_t>(1, c.T);
+  a.all = c.B * c.T;
   a.d = static_cast<int>(d);
+  a.G = shape.G;
   a.center = c.center;
   a.sums = sums;
+  a.classes = static_cast<int>(classes);
   a.part = static_cast<float*>(ws);
-  // columns of a thread: up to 16 in registers with their rows; wide rows have
-  // 512 threads, 32 columns each, and are read again behind the sums
-  const bool wide = acc * e > kLnThreads * 16;
-  a.G = wide ? kLnWide : pow2_at_least(acc, 8, kLnThreads);
-  const int threads = wide ? kLnWide : kLnThreads;
-  const int64_t nv = (acc + a.G - 1) / a.G;
-  const dim3 grid(static_cast<unsigned>(p.chunks), static_cast<unsigned>(p.samples));
-  const auto go = [&](auto kernel) {
-    return launch_after(kernel, grid, threads, 1, s, 0, static_cast<const T*>(c.dY),
+  const dim3 grid(static_cast<unsigned>(p.chunks * classes), static_cast<unsigned>(p.samples));
+  const auto go = [&](auto kernel, int threads, size_t smem) {
+    return launch_after(kernel, grid, threads, 1, s, smem, static_cast<const T*>(c.dY),
                         static_cast<const T*>(c.X), static_cast<const T*>(c.weight),
                         static_cast<T*>(c.dX), a);
   };
+  const auto narrow = [&](auto n) {
+    constexpr int kN = decltype(n)::value;
+    const size_t smem = shape.G < kLnThreads ? 2 * d * 4 : 0;  // (one group needs no turns)
+    constexpr int kR = kN * kV <= 8 ? 2 : 1;
+    return shape.odd ? go(layernorm_grad_kernel<T, kV, kN, kR, true, false>, kLnThreads, smem)
+                     : go(layernorm_grad_kernel<T, kV, kN, kR, false, false>, kLnThreads, smem);
+  };
+  const auto wide = [&](auto n) {
+    constexpr int kN = decltype(n)::value, bytes = 2 * kN * kV * kLnWide * 4;
+    cudaError_t e;
+    if (shape.odd) {
+      e = allow_smem<layernorm_grad_kernel<T, kV, kN, 1, true, true>>(bytes);
+      return e != cudaSuccess
+          ? e : go(layernorm_grad_kernel<T, kV, kN, 1, true, true>, kLnWide, bytes);
+    }
+    e = allow_smem<layernorm_grad_kernel<T, kV, kN, 1, false, true>>(bytes);
+    return e != cudaSuccess
+        ? e : go(layernorm_grad_kernel<T, kV, kN, 1, false, true>, kLnWide, bytes);
+  };
   cudaError_t err;
-  if (vec) {
-    if (wide) err = go(layernorm_grad_kernel<T, kV, 32 / kV, 1, true>);
-    else if (nv <= 1) err = go(layernorm_grad_kernel<T, kV, 1, 2, false>);
-    else if (nv <= 2) err = go(layernorm_grad_kernel<T, kV, 2, 2, false>);
-    else err = go(layernorm_grad_kernel<T, kV, 16 / kV, 2, false>);
+  if (shape.G == kLnWide) {
+    constexpr int kUnit = 8 / kV;  // accesses of eight elements
+    if (shape.nv <= 2 * kUnit) err = wide(std::integral_constant<int, 2 * kUnit>{});
+    else if (shape.nv <= 3 * kUnit) err = wide(std::integral_constant<int, 3 * kUnit>{});
+    else if (shape.nv <= 4 * kUnit) err = wide(std::integral_constant<int, 4 * kUnit>{});
+    else err = wide(std::integral_constant<int, 4 * kUnit + 1>{});  // (a shift's)
+  } else if (shape.nv <= 1) {
+    err = narrow(std::integral_constant<int, 1>{});
+  } else if (shape.nv <= 2) {
+    err = narrow(std::integral_constant<int, 2>{});
   } else {
-    if (wide) err = go(layernorm_grad_kernel<T, 1, 32, 1, true>);
-    else if (nv <= 4) err = go(layernorm_grad_kernel<T, 1, 4, 2, false>);
-    else err = go(layernorm_grad_kernel<T, 1, 16, 2, false>);
+    err = narrow(std::integral_constant<int, 16 / kV>{});
   }
   if (err != cudaSuccess || !sums) return err;
   const int tiles = static_cast<int>((d + 31) / 32);
-  float* npart = by_sample ? a.part + p.samples * p.chunks * 2 * d : nullptr;
+  const int64_t ctas = p.chunks * classes;
+  float* npart = by_sample ? a.part + p.samples * ctas * 2 * d : nullptr;
   const int parts = c.norm_of_bias ? 2 : 1;
   const float* cf = by_sample ? c.c : nullptr;
   const int which = c.db != nullptr || (by_sample && c.norm_of_bias) ? 2 : 1;
   err = launch_after(layernorm_finish_kernel<T>, dim3(tiles, which), 32 * kFinWarps, 1, s, 0,
                      static_cast<const float*>(a.part), cf, static_cast<int>(p.samples),
-                     static_cast<int>(p.chunks), static_cast<int>(d), static_cast<T*>(c.dW),
+                     static_cast<int>(ctas), static_cast<int>(d), static_cast<T*>(c.dW),
                      static_cast<T*>(c.db), npart, parts);
   if (err != cudaSuccess || !by_sample) return err;
   return launch_after(layernorm_norm_kernel, dim3(static_cast<unsigned>((c.B + 7) / 8)), 256, 1, s,
@@ -470,8 +666,11 @@ cudaError_t backward(const LayernormGradCall& c, void* ws, cudaStream_t s) {
 }  // namespace
 
 size_t layernorm_grad_ws_bytes(int64_t B, int64_t T, int64_t d, int with_norms) {
-  const LnPlan p = plan_grad(B, T, with_norms != 0);
-  const size_t part = static_cast<size_t>(p.samples) * p.chunks * 2 * d * 4;
+  size_t part = 0;
+  for (const int64_t classes : {grad_classes<float>(d), grad_classes<__nv_bfloat16>(d)}) {
+    const LnPlan p = plan_grad(B, T, with_norms != 0, classes);
+    part = std::max(part, static_cast<size_t>(p.samples) * p.chunks * classes * 2 * d * 4);
+  }
   const size_t np = with_norms ? static_cast<size_t>((d + 31) / 32) * 2 * B * 4 : 0;
   return part + np + 16;
 }

@@ -53,7 +53,8 @@ def _near(got, ref, tol, what="", terms=0.0):
 # sum, relative to a sum of positive terms: below 8 half steps for pairwise-like
 # trees of threads), 1 / sqrt, two products and a sum: 32 half steps.
 NORM = {F32: 32 * 2.0 ** -24, BF16: 2.0 ** -8}
-WIDTHS = [1, 2, 7, 8, 9, 64, 100, 256, 321, 1000, 2048, 2049, 4095, 4096, 4104, 8200, 16383, 16384]
+WIDTHS = [1, 2, 7, 8, 9, 12, 64, 100, 122, 256, 321, 1000, 2048, 2049, 2052, 4095, 4096, 4104, 8200, 12290,
+          16383, 16384]
 
 
 @pytest.mark.parametrize("d", WIDTHS)
