@@ -599,7 +599,8 @@ dprc_status dprc_rotary(const void* X, const int64_t* x_stride, dprc_dtype dtype
  *  others do not must be finite (a NaN or infinity in it may reach both).
  *  Scores, softmax and sums in fp32.  For bf16 the softmax's weights (and the
  *  gradient of the scores) enter the products rounded to bf16.
- *  1 <= D <= 128, Tq, Tk <= 2^20, B Hkv <= 65535, Tq H / Hkv <= 2^28, H / Hkv <= 4096.
+ *  1 <= D <= 128, Tq, Tk <= 2^20, B Hkv <= 65535, Tq H / Hkv <= 2^28, H / Hkv <= 4096,
+ *  (Tq H / Hkv + Tk) B Hkv <= 2^34.
  *  bf16 runs on the tensor cores where D, the strides and the addresses are multiples of
  *  8 elements (16 bytes) and H / Hkv <= 128, else on the CUDA cores (the gradient: dO's
  *  too).

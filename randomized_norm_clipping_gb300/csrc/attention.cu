@@ -117,6 +117,26 @@ __global__ void __launch_bounds__(128)
   if (a.lse != nullptr && lane == 0) a.lse[(b * a.H + h) * a.Tq + t] = m * kLn2 + logf(l);
 }
 
+// dK and dV from the shares of the rows, in order: a thread an element of both.
+template <typename T>
+__global__ void __launch_bounds__(256) attention_join_keys_kernel(const AttnArgs a, long long total) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= total) return;
+  const long long row = i / a.D, bh = row / a.Tk, b = bh / a.Hkv;
+  const int col = static_cast<int>(i - row * a.D), key = static_cast<int>(row - bh * a.Tk);
+  const int hk = static_cast<int>(bh - b * a.Hkv);
+  const float* p = a.key_part + row * 2 * a.D + col;
+  float k = 0.f, v = 0.f;
+  for (int z = 0; z < a.row_splits; ++z) {
+    k += ld_l2(p + z * total * 2);
+    v += ld_l2(p + z * total * 2 + a.D);
+  }
+  if (a.dK != nullptr) static_cast<T*>(a.dK)[b * a.dkb + key * a.dkt + hk * a.dkh + col] = T(k);
+  if (a.dV != nullptr) static_cast<T*>(a.dV)[b * a.dvb + key * a.dvt + hk * a.dvh + col] = T(v);
+}
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t round16(size_t v) { return (v + 15) / 16 * 16; }
 
@@ -151,6 +171,26 @@ Split plan_split(const AttentionCall& c) {
     return split_keys(c, n, 128, 152);
   }
   return split_keys(c, attention_simt_rows(c.Tq * (c.H / c.Hkv), c.B * c.Hkv), 64, 608);
+}
+
+// Shares of the rows for tiles of keys that are too few to fill the GPU; their partial
+// results stay below kMaxKeyPart.
+constexpr int64_t kMaxKeyPart = int64_t(256) << 20;
+int plan_row_splits(const AttentionCall& c, bool tc) {
+  const int64_t bhs = c.B * c.Hkv, rows = c.Tq * (c.H / c.Hkv);
+  const int64_t tile = tc ? 128 : attention_simt_keys(c.Tk, bhs);
+  const int64_t ctas = std::max<int64_t>(1, cdiv(c.Tk, tile) * bhs);
+  const int64_t steps = std::max<int64_t>(1, cdiv(rows, tc ? attention_tc_rows_grad(c) : 64));
+  int64_t s = std::min<int64_t>((tc ? 152 : 304) / ctas, std::min<int64_t>(steps, 16));
+  const int64_t bytes = std::max<int64_t>(1, bhs * c.Tk * 2 * c.D * 4);
+  s = std::min<int64_t>(s, kMaxKeyPart / bytes);
+  return static_cast<int>(std::max<int64_t>(1, s));
+}
+size_t key_part_bytes(const AttentionCall& c, int splits) {
+  return splits > 1 ? static_cast<size_t>(splits) * c.B * c.Hkv * c.Tk * 2 * c.D * 4 : 0;
+}
+size_t delta_bytes(const AttentionCall& c) {
+  return round16(static_cast<size_t>(c.B) * c.Tq * c.H * 4);
 }
 
 AttnArgs args_of(const AttentionCall& c, char* ws) {
@@ -208,7 +248,10 @@ size_t attention_ws_bytes(const AttentionCall& c) {
 }
 
 size_t attention_grad_ws_bytes(const AttentionCall& c) {
-  return span_bytes(c) + static_cast<size_t>(c.B) * c.Tq * c.H * 4 + 16;
+  // (either kind of kernel may come to run: the other tensors decide)
+  const size_t part = std::max(key_part_bytes(c, plan_row_splits(c, false)),
+                               attention_tc_takes(c) ? key_part_bytes(c, plan_row_splits(c, true)) : 0);
+  return span_bytes(c) + delta_bytes(c) + part + 16;
 }
 
 cudaError_t launch_attention(const AttentionCall& c, void* out, float* lse, void* ws,
@@ -255,8 +298,16 @@ cudaError_t launch_attention_grad(const AttentionGradCall& c, void* ws, cudaStre
     a.dQ = nullptr;
   }
   if (c.f.Tk == 0) a.dK = a.dV = nullptr;
-  if (attention_tc_takes_grad(c)) return launch_attention_grad_tc(a, s);
-  return launch_attention_grad_simt(a, c.f.dtype, s);
+  const bool tc = attention_tc_takes_grad(c);
+  a.row_splits = a.dK != nullptr || a.dV != nullptr ? plan_row_splits(c.f, tc) : 1;
+  a.key_part = reinterpret_cast<float*>(w + span_bytes(c.f) + delta_bytes(c.f));
+  e = tc ? launch_attention_grad_tc(a, s) : launch_attention_grad_simt(a, c.f.dtype, s);
+  if (e != cudaSuccess || a.row_splits == 1) return e;
+  const long long total = static_cast<long long>(c.f.B) * c.f.Hkv * c.f.Tk * c.f.D;
+  const dim3 grid(static_cast<unsigned>(cdiv(total, 256)));
+  if (c.f.dtype == DPRC_F32)
+    return launch_after(attention_join_keys_kernel<float>, grid, 256, 1, s, 0, a, total);
+  return launch_after(attention_join_keys_kernel<__nv_bfloat16>, grid, 256, 1, s, 0, a, total);
 }
 
 }  // namespace dprc

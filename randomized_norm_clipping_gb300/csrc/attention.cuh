@@ -42,6 +42,8 @@ struct AttnArgs {
   const float* lse_in;
   float* delta;          // [B][H][Tq]
   void *dQ, *dK, *dV;
+  int row_splits;        // shares of the rows in the sums of a tile of keys
+  float* key_part;       // [row_splits][B][Hkv][Tk][2][D]: dK and dV of a share
   long long dqb, dqt, dqh, dkb, dkt, dkh, dvb, dvt, dvh;
 };
 
@@ -83,11 +85,13 @@ __device__ __forceinline__ RowSees attn_row(const AttnArgs& a, int b, int t, int
 
 // The kernels (attention_simt.cu, attention_tc.cu).
 int attention_simt_rows(long long rows, long long heads);
+int attention_simt_keys(long long keys, long long heads);  // of a CTA, in the gradient
 cudaError_t launch_attention_simt(const AttnArgs& a, dprc_dtype dt, cudaStream_t s);
 cudaError_t launch_attention_grad_simt(const AttnArgs& a, dprc_dtype dt, cudaStream_t s);
 bool attention_tc_takes(const AttentionCall& c);
 bool attention_tc_takes_grad(const AttentionGradCall& c);
 int attention_tc_rows(const AttentionCall& c);  // of a CTA
+int attention_tc_rows_grad(const AttentionCall& c);
 cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attention_grad_tc(const AttnArgs& a, cudaStream_t s);
 

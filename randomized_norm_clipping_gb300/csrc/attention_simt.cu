@@ -60,7 +60,7 @@ __device__ __forceinline__ void load_tile(float* dst, int n, int D, bool vec, Sr
 // acc[i][j] += row i of a times row 16 j of b, over the width (rows kD + kPad apart).
 template <int kR, int kC, int kD>
 __device__ __forceinline__ void dots(const float* a, const float* b, int D, float (&acc)[kR][kC]) {
-#pragma unroll 2
+#pragma unroll(kR <= 2 ? 4 : 2)
   for (int d = 0; d < D; d += 4) {
     float4 y[kC];
 #pragma unroll
@@ -112,7 +112,7 @@ __device__ __forceinline__ void store_weights(float* p, const float (&w)[kR]) {
 template <int kR, int kO, int kD, int kW>
 __device__ __forceinline__ void add_rows(const float* wt, const float* v, int n,
                                          float (&acc)[kR][4 * kO]) {
-#pragma unroll 2
+#pragma unroll(kR <= 2 ? 8 : 4)
   for (int j = 0; j < n; ++j) {
     float w[kR];
     load_weights<kR>(wt + j * kW, w);
@@ -186,8 +186,9 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnArgs
   int* red = kdoc + kN;               // [8]
   pdl_launch_dependents();
   pdl_wait();
-  const int b = blockIdx.y / a.Hkv, hk = blockIdx.y - b * a.Hkv;
-  const int rows = a.Tq * a.G, p0 = blockIdx.x * kM;
+  const int bhs = a.B * a.Hkv, bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  const int rows = a.Tq * a.G;
+  const int p0 = (gridDim.x / bhs - 1 - blockIdx.x / bhs) * kM;  // (the longest rows first)
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int keys = attn_keys(a, b), first = attn_first(a, b);
   const T* Q = static_cast<const T*>(a.Q) + b * a.qb;
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnArgs
     const int p = p0 + ty * kR + i, t = p / a.G, h = hk * a.G + p - t * a.G;
     if (p >= rows) continue;
     if (a.splits > 1) {
-      const long long at = (static_cast<long long>(blockIdx.z) * a.B * a.Hkv + blockIdx.y) * rows + p;
+      const long long at = (static_cast<long long>(blockIdx.z) * bhs + bh) * rows + p;
 #pragma unroll
       for (int c = 0; c < 4 * kO; ++c) {
         const int col = (c / 4) * 64 + tx * 4 + c % 4;
@@ -345,8 +346,9 @@ __global__ void __launch_bounds__(kThreads) attention_dq_simt_kernel(const AttnA
   int* red = kdoc + kN;
   pdl_launch_dependents();
   pdl_wait();
-  const int b = blockIdx.y / a.Hkv, hk = blockIdx.y - b * a.Hkv;
-  const int rows = a.Tq * a.G, p0 = blockIdx.x * kM;
+  const int bhs = a.B * a.Hkv, bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  const int rows = a.Tq * a.G;
+  const int p0 = (gridDim.x / bhs - 1 - blockIdx.x / bhs) * kM;  // (the longest rows first)
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int keys = attn_keys(a, b), first = attn_first(a, b);
   const T* Q = static_cast<const T*>(a.Q) + b * a.qb;
@@ -466,8 +468,9 @@ __global__ void __launch_bounds__(kThreads) attention_dkv_simt_kernel(const Attn
   int* rdoc = rlim + kMB;
   pdl_launch_dependents();
   pdl_wait();
-  const int b = blockIdx.y / a.Hkv, hk = blockIdx.y - b * a.Hkv;
-  const int rows = a.Tq * a.G, j0 = blockIdx.x * kM;
+  const int bhs = a.B * a.Hkv, bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  const int rows = a.Tq * a.G;
+  const int j0 = blockIdx.x / bhs * kM;  // (the first keys have the most rows)
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int keys = attn_keys(a, b), first = attn_first(a, b);
   const T* Q = static_cast<const T*>(a.Q) + b * a.qb;
@@ -496,6 +499,7 @@ __global__ void __launch_bounds__(kThreads) attention_dkv_simt_kernel(const Attn
   int tok0 = 0;
   if (a.causal && (a.prefix == nullptr || a.prefix[b] <= j0)) tok0 = max(0, min(a.Tq, j0 - first));
   for (int p0 = tok0 * a.G / kMB * kMB; p0 < rows && n > 0; p0 += kMB) {
+    if (p0 / kMB % a.row_splits != static_cast<int>(blockIdx.z)) continue;  // another CTA's
     __syncthreads();
     int any = 0;
     if (threadIdx.x < kMB) {
@@ -561,6 +565,18 @@ __global__ void __launch_bounds__(kThreads) attention_dkv_simt_kernel(const Attn
   for (int i = 0; i < kR; ++i) {
     const int key = j0 + ty * kR + i;
     if (key >= a.Tk) continue;
+    if (a.row_splits > 1) {
+      float* part = a.key_part +
+                    ((static_cast<long long>(blockIdx.z) * bhs + bh) * a.Tk + key) * 2 * a.D;
+#pragma unroll
+      for (int c = 0; c < 4 * kO; ++c) {
+        const int col = (c / 4) * 64 + tx * 4 + c % 4;
+        if (col >= a.D) continue;
+        part[col] = dk[i][c];
+        part[a.D + col] = dv[i][c];
+      }
+      continue;
+    }
     T* k = static_cast<T*>(a.dK) + b * a.dkb + key * a.dkt + hk * a.dkh;
     T* v = static_cast<T*>(a.dV) + b * a.dvb + key * a.dvt + hk * a.dvh;
 #pragma unroll
@@ -585,7 +601,7 @@ cudaError_t forward(const AttnArgs& a, cudaStream_t s) {
   constexpr int bytes = kFwdSmem<kD, kR>;
   const cudaError_t e = allow_smem<attention_simt_kernel<T, kD, kR>>(bytes);
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.Tq * a.G + kGroups * kR - 1) / (kGroups * kR), a.B * a.Hkv, a.splits);
+  const dim3 grid((a.Tq * a.G + kGroups * kR - 1) / (kGroups * kR) * (a.B * a.Hkv), 1, a.splits);
   return launch_after(attention_simt_kernel<T, kD, kR>, grid, kThreads, 1, s, bytes, a);
 }
 
@@ -604,7 +620,7 @@ cudaError_t rows_grad(const AttnArgs& a, cudaStream_t s) {
   const cudaError_t e = allow_smem<attention_dq_simt_kernel<T, kD, kR>>(bytes);
   if (e != cudaSuccess) return e;
   return launch_after(attention_dq_simt_kernel<T, kD, kR>,
-                      dim3((a.Tq * a.G + kGroups * kR - 1) / (kGroups * kR), a.B * a.Hkv), kThreads, 1, s,
+                      dim3((a.Tq * a.G + kGroups * kR - 1) / (kGroups * kR) * (a.B * a.Hkv)), kThreads, 1, s,
                       bytes, a);
 }
 template <typename T, int kD, int kR>
@@ -613,7 +629,8 @@ cudaError_t keys_grad(const AttnArgs& a, cudaStream_t s) {
   const cudaError_t e = allow_smem<attention_dkv_simt_kernel<T, kD, kR>>(bytes);
   if (e != cudaSuccess) return e;
   return launch_after(attention_dkv_simt_kernel<T, kD, kR>,
-                      dim3((a.Tk + kGroups * kR - 1) / (kGroups * kR), a.B * a.Hkv), kThreads, 1, s, bytes, a);
+                      dim3((a.Tk + kGroups * kR - 1) / (kGroups * kR) * (a.B * a.Hkv), 1, a.row_splits),
+                      kThreads, 1, s, bytes, a);
 }
 
 template <typename T, int kD>
@@ -642,6 +659,10 @@ bool fours(const AttnArgs& a) {
 
 int attention_simt_rows(long long rows, long long heads) {
   return kGroups * rows_of_group(rows, heads, true);
+}
+
+int attention_simt_keys(long long keys, long long heads) {
+  return kGroups * rows_of_group(keys, heads, false);
 }
 
 cudaError_t launch_attention_simt(const AttnArgs& args, dprc_dtype dt, cudaStream_t s) {

@@ -796,9 +796,16 @@ __device__ __forceinline__ void store_any(__nv_bfloat16* p, const float* v) {
   }
 }
 
-// Rows of a gradient from tensor memory: this thread's lane, and of its 16-column pieces those that are the part's.
-__device__ __forceinline__ void store_grad(__nv_bfloat16* out, bool mine, uint32_t taddr, int part,
-                                           int cols, int D, float scale, bool any) {
+// Rows of a gradient from tensor memory: this thread's lane, and of its 16-column pieces
+// those that are the part's.
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) { store_any(p, v); }
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  store_row<4>(p, v);
+  store_row<4>(p + 4, v + 4);
+}
+template <typename T>
+__device__ __forceinline__ void store_grad(T* out, bool mine, uint32_t taddr, int part, int cols,
+                                           int D, float scale, bool any) {
   for (int c = part * 16; c < cols; c += kGradWarps * 4) {
     float o[16];
     if (any) {
@@ -813,7 +820,7 @@ __device__ __forceinline__ void store_grad(__nv_bfloat16* out, bool mine, uint32
       if (c + q >= D) continue;
 #pragma unroll
       for (int u = 0; u < 8; ++u) o[q + u] *= scale;
-      store_any(out + c + q, o + q);
+      store8(out + c + q, o + q);
     }
   }
 }
@@ -1187,7 +1194,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   const int words = j0 < keys ? (x.row_tiles + 31) / 32 : 0;
   for (int w = warp; w < words; w += kGradThreads / 32) {
     const int i = w * 32 + lane, tok0 = i * x.nt;
-    bool ok = tok0 < a.Tq;
+    bool ok = tok0 < a.Tq && i % a.row_splits == static_cast<int>(blockIdx.z);
     if (ok) {
       const int tok1 = min(tok0 + x.nt, a.Tq) - 1;
       if (a.causal) {
@@ -1509,10 +1516,16 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (ok) {
       const bool mine = key < a.Tk;
       const int cols = x.steps * 16;
-      if (a.dV != nullptr)
+      if (a.row_splits > 1) {
+        float* out = a.key_part +
+                     ((static_cast<long long>(blockIdx.z) * bhs + bh) * a.Tk + key) * 2 * a.D;
+        store_grad(out, mine, tmem + lanes + Cfg::kDk, part, cols, a.D, a.scale, n > 0);
+        store_grad(out + a.D, mine, tmem + lanes + Cfg::kDv, part, cols, a.D, 1.f, n > 0);
+      }
+      if (a.row_splits == 1 && a.dV != nullptr)
         store_grad(static_cast<__nv_bfloat16*>(a.dV) + b * a.dvb + key * a.dvt + hk * a.dvh, mine,
                    tmem + lanes + Cfg::kDv, part, cols, a.D, 1.f, n > 0);
-      if (a.dK != nullptr)
+      if (a.row_splits == 1 && a.dK != nullptr)
         store_grad(static_cast<__nv_bfloat16*>(a.dK) + b * a.dkb + key * a.dkt + hk * a.dkh, mine,
                    tmem + lanes + Cfg::kDk, part, cols, a.D, a.scale, n > 0);
     }
@@ -1547,7 +1560,7 @@ cudaError_t launch_grad(const GradMaps& m, const TcArgs& x, cudaStream_t s) {
   e = allow_smem<attention_dkv_tc_kernel<kBlocks, kForm>>(bytes);
   if (e != cudaSuccess) return e;
   return launch_after(attention_dkv_tc_kernel<kBlocks, kForm>,
-                      dim3(bhs * ((x.a.Tk + kTile - 1) / kTile)), kGradThreads, 1, s, bytes, m.q, m.o,
+                      dim3(bhs * ((x.a.Tk + kTile - 1) / kTile), 1, x.a.row_splits), kGradThreads, 1, s, bytes, m.q, m.o,
                       m.k, m.v, x);
 }
 
@@ -1611,6 +1624,11 @@ bool attention_tc_takes(const AttentionCall& c) {
 bool attention_tc_takes_grad(const AttentionGradCall& c) {
   return attention_tc_takes(c.f) && address_fits(c.dO) &&
          strides_fit(c.dos, c.f.B, c.f.Tq, c.f.H);
+}
+
+int attention_tc_rows_grad(const AttentionCall& c) {
+  const int G = static_cast<int>(c.H / c.Hkv);
+  return kTile / G * G;
 }
 
 int attention_tc_rows(const AttentionCall& c) {

@@ -87,6 +87,8 @@ dprc_status check_attention(const dprc_attention_args* a) {
   // grids and row numbers stay in range
   if (a->Hkv > kMaxSamples || a->B > kMaxSamples / a->Hkv) return DPRC_ERR_SHAPE;
   if (a->H / a->Hkv > 4096 || a->Tq * (a->H / a->Hkv) > (int64_t(1) << 28)) return DPRC_ERR_SHAPE;
+  if (a->Tq * (a->H / a->Hkv) / 16 + a->Tk / 16 > (int64_t(1) << 30) / (a->B * a->Hkv))
+    return DPRC_ERR_SHAPE;
   if (!finite_f(a->scale) || !finite_f(a->cap) || a->cap < 0.f) return DPRC_ERR_SHAPE;
   if (!strides_ok(a->q_stride) || !strides_ok(a->k_stride) || !strides_ok(a->v_stride))
     return DPRC_ERR_SHAPE;
