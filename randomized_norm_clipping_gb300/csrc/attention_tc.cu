@@ -31,12 +31,6 @@ namespace {
 
 constexpr int kTile = 128;           // rows, and keys, of a tile
 constexpr int kBlock = kTile * 128;  // bytes of a tile's 64 columns
-constexpr int kWarps = 8;            // of the softmax
-// A third group of four warps copies and issues; it gives registers to the softmax's,
-// which hold a row of 128 scores: 2 * 224 + 56 = 3 * 168, what the block is launched with.
-constexpr int kThreads = 32 * (kWarps + 4);
-constexpr int kRegsMore = 224, kRegsLess = 56;
-static_assert(kThreads * 168 == 256 * kRegsMore + 128 * kRegsLess, "registers of the block");
 constexpr int kMaxKeyTiles = (1 << 20) / kTile;
 constexpr float kLazy = 8.f;  // a row is rescaled when its maximum grows by 2^kLazy
 
@@ -382,17 +376,25 @@ template <int kBlocks, int kTiles>
 struct FwdCfg {
   static constexpr int kQ = kTiles * kBlocks * kBlock;
   static constexpr int kSlot = kBlocks * kBlock;
-  static constexpr int kStages = kBlocks == 1 ? 8 : (kTiles == 1 ? 5 : 4);
+  // one tile: two CTAs to an SM
+  static constexpr int kStages = kTiles == 1 ? (kBlocks == 1 ? 5 : 2) : (kBlocks == 1 ? 8 : 4);
+  static constexpr int kSoft = 4 * kTiles;  // warps of the softmax
+  static constexpr int kThreads = 32 * (kSoft + 4);
+  static constexpr int kRegs = kTiles == 1 ? 128 : 168;
+  static constexpr int kMore = kTiles == 1 ? 200 : 224, kLess = 56;
+  static_assert(kThreads * kRegs == 32 * kSoft * kMore + 128 * kLess, "registers of the block");
   static constexpr int kSmem = kQ + kStages * kSlot + 1024 + 1024 + kMaxKeyTiles / 8;
   static constexpr int kO = 128 * kTiles;  // first column of the sums
-  static constexpr int kTmem = kTiles == 2 || kBlocks == 2 ? (kTiles == 2 ? 512 : 256) : 256;
-  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  static constexpr int kTmem = 256 * kTiles;
+  static_assert((kTiles == 1 ? 2 : 1) * (kSmem + 1024) <= 228 * 1024, "shared memory of a CTA");
 };
 
 // Two tiles of rows in turn: while a group of four warps takes the exponentials of its
-// tile, the tensor core forms the other's products.  kTiles 1: few rows.
+// tile, the tensor core forms the other's products.  kTiles 1: few rows, whose keys are
+// shared out; two CTAs to an SM, one's copies and products under the other's
+// exponentials, and only the warps that have rows take part.
 template <int kBlocks, int kTiles, int kForm>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1 ? 2 : 1)
     attention_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                         const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const TcArgs x) {
@@ -418,6 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int bhs = a.B * a.Hkv;
   const int bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
   const int grp = x.groups - 1 - blockIdx.x / bhs;  // the longest rows first
+  // warps of a tile that have rows
+  const int active =
+      kTiles == 2 ? 4 : (min(x.nt, a.Tq - grp * x.nt) * a.G + 31) / 32;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -426,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(qfull, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&sfull[w], 1);
-      mbar_init(&pfull[w], 4);
+      mbar_init(&pfull[w], active);
       mbar_init(&ofull[w], 1);
     }
     mbar_init(drain, 1);
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
-  if (warp == kWarps + 1) {
+  if (warp == Cfg::kSoft + 1) {
     tmem_alloc(tmem_slot, Cfg::kTmem);
     tmem_relinquish();
   }
@@ -454,10 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int w = warp >> 2;  // the tile of rows of a softmax warp
   const int r = threadIdx.x & (kTile - 1);
   const int tt = r / a.G, tok = (grp * kTiles + w) * x.nt + tt;
-  const bool mine = warp < 4 * kTiles && tt < x.nt && tok < a.Tq;
+  const bool mine = warp < Cfg::kSoft && tt < x.nt && tok < a.Tq;
   RowSees see = {0, 0, -1};
   Extent e = {};
-  if (warp < 4 * kTiles) {
+  if (warp < Cfg::kSoft) {
     if (mine) see = attn_row(a, b, tok, keys, first);
     e = warp_extent(mine, see, a.docs != nullptr);
     if (lane == 0) {
@@ -473,9 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   key_tile_bits(a, b, t0, t1, ext[1], ext[2], bits, words);
   __syncthreads();
 
-  if (warp >= kWarps) {
-    regs_less<kRegsLess>();
-    if (warp == kWarps && lane == 0) {
+  if (warp >= Cfg::kSoft) {
+    regs_less<Cfg::kLess>();
+    if (warp == Cfg::kSoft && lane == 0) {
       Bits it(bits, words);
       Pos pos;
       int j = it.next(), issued = 0;
@@ -510,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (any) mbar_wait(qfull, 0, DPRC_DEVERR_PIPE_FULL);
       for (int k = issued - 1; k >= 0 && k >= issued - kStages; --k)
         mbar_wait(&full[k % kStages], (k / kStages) & 1, DPRC_DEVERR_PIPE_FULL);
-    } else if (warp == kWarps + 1) {
+    } else if (warp == Cfg::kSoft + 1) {
       // all lanes keep step, one issues: the descriptors stay in the warp's common registers
       const bool lead = elect_one() != 0;
       Bits it(bits, words);
@@ -568,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (issued && lead) umma_drain(drain, kWaitLimitNs);
     }
   } else {
-    regs_more<kRegsMore>();
-    if (warp < 4 * kTiles) {
+    regs_more<Cfg::kMore>();
+    if (kTiles == 2 || warp < active) {
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + Cfg::kO + w * 128;
       const int h = hk * a.G + r - tt * a.G;
@@ -595,7 +600,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           dirty = dirty || s.pad;
         }
         float z[kTile];
-        tmem_ld_128cols(ts, z);
+        if constexpr (kTiles == 2) {
+          tmem_ld_128cols(ts, z);
+        } else {  // (128 at once take more registers than the block is launched with)
+#pragma unroll
+          for (int c = 0; c < kTile; c += 64) {
+            float part[64];
+            tmem_ld_64cols(ts + c, part);
+#pragma unroll
+            for (int u = 0; u < 64; ++u) z[c + u] = part[u];
+          }
+        }
         scores<kForm>(x, z, slope2, static_cast<float>(see.pos - j0));
         if (j0 + kTile > e.min_lim || by_doc) hide(z, see, docs, j0, a.Tk, by_doc);
         const float mul = kForm == 0 ? x.c : 1.f;
@@ -650,9 +665,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           // values that no row of the CTA sees may be anything, and 0 times NaN is NaN
           ok = wait_warp<true>(&full[vpos.s], vpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
           if (!ok) break;
-          const int key = j0 + r;
-          if (key >= top || (docs != nullptr && docs[key] < 0))
-            zero_row<kBlocks>(ring + vpos.s * Cfg::kSlot, r);
+          for (int q = r; q < kTile; q += 32 * active) {
+            const int key = j0 + q;
+            if (key >= top || (docs != nullptr && docs[key] < 0))
+              zero_row<kBlocks>(ring + vpos.s * Cfg::kSlot, q);
+          }
           fence_proxy_async_smem();
         }
         vpos.next(kStages);
@@ -704,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarps + 1) {
+  if (warp == Cfg::kSoft + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, Cfg::kTmem);
   }
@@ -717,7 +734,8 @@ cudaError_t launch_fwd(const CUtensorMap& q, const CUtensorMap& k, const CUtenso
   const cudaError_t e = allow_smem<attention_tc_kernel<kBlocks, kTiles, kForm>>(bytes);
   if (e != cudaSuccess) return e;
   const dim3 grid(x.a.B * x.a.Hkv * x.groups, 1, x.a.splits);
-  return launch_after(attention_tc_kernel<kBlocks, kTiles, kForm>, grid, kThreads, 1, s, bytes, q,
+  return launch_after(attention_tc_kernel<kBlocks, kTiles, kForm>, grid, FwdCfg<kBlocks, kTiles>::kThreads, 1, s,
+                      bytes, q,
                       k, v, x);
 }
 
