@@ -167,9 +167,7 @@ Split split_keys(const AttentionCall& c, int tile_rows, int tile_keys, int resid
 
 Split plan_split(const AttentionCall& c) {
   if (attention_tc_takes(c)) {
-    // (few rows: one tile, two CTAs to an SM)
-    const int n = attention_tc_rows(c);
-    return split_keys(c, n, 128, n <= 128 ? 304 : 152);
+    return split_keys(c, attention_tc_rows(c), 128, attention_tc_resident(c));
   }
   return split_keys(c, attention_simt_rows(c.Tq * (c.H / c.Hkv), c.B * c.Hkv), 64, 608);
 }

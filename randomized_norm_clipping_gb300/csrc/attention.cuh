@@ -91,6 +91,7 @@ cudaError_t launch_attention_grad_simt(const AttnArgs& a, dprc_dtype dt, cudaStr
 bool attention_tc_takes(const AttentionCall& c);
 bool attention_tc_takes_grad(const AttentionGradCall& c);
 int attention_tc_rows(const AttentionCall& c);  // of a CTA
+int attention_tc_resident(const AttentionCall& c);  // CTAs of the forward pass on the GPU
 int attention_tc_rows_grad(const AttentionCall& c);
 cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attention_grad_tc(const AttnArgs& a, cudaStream_t s);

@@ -696,19 +696,21 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
 #pragma unroll
             for (int q = 0; q < 16; ++q) o[q] = 0.f;
           }
-          if (!mine) continue;
+          if (mine) {
 #pragma unroll
-          for (int q = 0; q < 16; q += 8) {
-            if (c + q >= a.D) continue;
+            for (int q = 0; q < 16; q += 8) {
+              if (c + q >= a.D) continue;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) o[q + u] *= inv;
-            if (parts) {
-              store_row<4>(a.part + prow * a.D + c + q, o + q);
-              store_row<4>(a.part + prow * a.D + c + q + 4, o + q + 4);
-            } else {
-              store_row<8>(out + c + q, o + q);
+              for (int u = 0; u < 8; ++u) o[q + u] *= inv;
+              if (parts) {
+                store_row<4>(a.part + prow * a.D + c + q, o + q);
+                store_row<4>(a.part + prow * a.D + c + q + 4, o + q + 4);
+              } else {
+                store_row<8>(out + c + q, o + q);
+              }
             }
           }
+          __syncwarp();  // (the next read is the whole warp's)
         }
         if (mine && parts) {
           a.part_stats[prow] = make_float2(m, l);
@@ -745,6 +747,375 @@ cudaError_t launch_fwd_form(int form, const CUtensorMap& q, const CUtensorMap& k
   if (form == 0) return launch_fwd<kBlocks, kTiles, 0>(q, k, v, x, s);
   if (form == 1) return launch_fwd<kBlocks, kTiles, 1>(q, k, v, x, s);
   return launch_fwd<kBlocks, kTiles, 2>(q, k, v, x, s);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (up to 32 of a head of keys): the rows stand four times in the tile, once for
+// each warp's lanes of tensor memory, and a warp takes a quarter of a tile's keys for
+// them, with a maximum, sum and accumulator of its own (the weights of the other quarters
+// are zeros that stand there from the start).  So the chain from a tile's scores to its
+// weights is a quarter as long.  The weights have columns of their own, so that the
+// next scores are formed meanwhile.  The four are joined in shared memory at the end.
+// Bound by the keys' and values' bytes.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 32;
+
+template <int kBlocks>
+struct FewCfg {
+  static constexpr int kSlot = kBlocks * kBlock;
+  static constexpr int kStages = 5;
+  static constexpr int kResident = kBlocks == 1 ? 2 : 1;  // CTAs to an SM
+  static constexpr int kThreads = 256;
+  static constexpr int kSmem = (1 + kStages) * kSlot + 1024 + 1024 + 1024 + kMaxKeyTiles / 8;
+  static constexpr int kS = 0, kP = 128, kO = 192, kTmem = kBlocks == 1 ? 256 : 512;
+  static_assert(kResident * (kSmem + 1024) <= 228 * 1024, "shared memory of a CTA");
+  static_assert(4 * kFewRows * 64 * kBlocks * 4 <= kStages * kSlot, "the joined rows");
+};
+
+template <int kBlocks, int kForm>
+__global__ void __launch_bounds__(FewCfg<kBlocks>::kThreads, FewCfg<kBlocks>::kResident)
+    attention_few_tc_kernel(const __grid_constant__ CUtensorMap map_q,
+                            const __grid_constant__ CUtensorMap map_k,
+                            const __grid_constant__ CUtensorMap map_v, const TcArgs x) {
+  using Cfg = FewCfg<kBlocks>;
+  constexpr int kStages = Cfg::kStages, kPart = 32;
+  const AttnArgs& a = x.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* qs = align_1024(smem_raw);
+  uint8_t* ring = qs + Cfg::kSlot;
+  uint8_t* rest = ring + kStages * Cfg::kSlot;
+  uint64_t* full = reinterpret_cast<uint64_t*>(rest);
+  uint64_t* empty = full + kStages;
+  uint64_t* qfull = empty + kStages;
+  uint64_t* sfull = qfull + 1;
+  uint64_t* sread = sfull + 1;
+  uint64_t* pfull = sread + 1;
+  uint64_t* pvfull = pfull + 1;
+  uint64_t* drain = pvfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* ext = reinterpret_cast<int*>(tmem_slot + 2);
+  int* done = ext + 3;  // [4]: the warps that came to their end
+  float2* stats = reinterpret_cast<float2*>(rest + 512);  // [4][kFewRows]
+  uint32_t* bits = reinterpret_cast<uint32_t*>(rest + 512 + 1024);
+
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int bhs = a.B * a.Hkv;
+  const int bh = blockIdx.x % bhs, b = bh / a.Hkv, hk = bh - b * a.Hkv;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(sfull, 1);
+    mbar_init(sread, 4);
+    mbar_init(pfull, 4);
+    mbar_init(pvfull, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+    ext[0] = 0;
+    ext[1] = 0x7fffffff;
+    ext[2] = -1;
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  if (warp == 5) {
+    tmem_alloc(tmem_slot, Cfg::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  const int keys = attn_keys(a, b), first = attn_first(a, b);
+  const int tok = lane / a.G, h = hk * a.G + lane - tok * a.G;
+  const bool mine = warp < 4 && tok < a.Tq;
+  RowSees see = {0, 0, -1};
+  Extent e = {};
+  if (warp < 4) {
+    if (mine) see = attn_row(a, b, tok, keys, first);
+    e = warp_extent(mine, see, a.docs != nullptr);
+    if (warp == 0 && lane == 0) {
+      ext[0] = e.max_lim;
+      ext[1] = e.lo;
+      ext[2] = e.hi;
+    }
+  }
+  __syncthreads();
+  const int top = ext[0];
+  const int t0 = blockIdx.z * a.per_split, t1 = min(t0 + a.per_split, (top + kTile - 1) / kTile);
+  const int words = max(0, (t1 + 31) / 32);
+  key_tile_bits(a, b, t0, t1, ext[1], ext[2], bits, words);
+  __syncthreads();
+
+  if (warp == 4 && lane == 0) {
+    Bits it(bits, words);
+    Pos pos;
+    int j = it.next(), issued = 0;
+    const bool any = j >= 0;
+    bool ok = true;
+    if (any) {
+      mbar_arrive_expect_tx(qfull, 4 * kBlocks * x.nt * a.G * 128);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int q = 0; q < kBlocks; ++q)
+          tma_load_4d(qs + q * kBlock + u * kFewRows * 128, &map_q, qfull, q * 64, hk * a.G, 0, b);
+    }
+    for (; j >= 0 && ok; j = it.next()) {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (!wait_bar<true>(&empty[pos.s], pos.parity ^ 1, DPRC_DEVERR_PIPE_EMPTY, abort_flag)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&full[pos.s], Cfg::kSlot);
+#pragma unroll
+        for (int q = 0; q < kBlocks; ++q)
+          tma_load_4d(ring + pos.s * Cfg::kSlot + q * kBlock, kv == 0 ? &map_k : &map_v,
+                      &full[pos.s], q * 64, hk, j * kTile, b);
+        ++issued;
+        pos.next(kStages);
+      }
+    }
+    if (any) mbar_wait(qfull, 0, DPRC_DEVERR_PIPE_FULL);
+    for (int k = issued - 1; k >= 0 && k >= issued - kStages; --k)
+      mbar_wait(&full[k % kStages], (k / kStages) & 1, DPRC_DEVERR_PIPE_FULL);
+  } else if (warp == 5) {
+    const bool lead = elect_one() != 0;
+    Bits it(bits, words);
+    const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
+    const uint32_t id_o = make_idesc_bf16(kTile, x.steps * 16, false, true);
+    const uint64_t dq = desc_k(smem_u32(qs));
+    const uint64_t dk = desc_k(smem_u32(ring)), dv = desc_mn(smem_u32(ring));
+    Pos pos;
+    int j = it.next(), n = 0;
+    bool ok = j >= 0, issued = false;
+    const auto filled = [&](const Pos& p) {
+      const bool f = wait_all<false>(&full[p.s], p.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+      tc_fence_after();
+      return f;
+    };
+    const auto scores_of = [&](const Pos& p) {
+      mma_width<kBlocks, false>(lead, tmem + Cfg::kS, dq, dk + ((p.s * Cfg::kSlot) >> 4), id_s,
+                                x.steps);
+      commit(lead, sfull);
+      commit(lead, &empty[p.s]);
+    };
+    ok = ok && wait_all<false>(qfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) && filled(pos);
+    if (ok) {
+      issued = true;
+      scores_of(pos);
+      pos.next(kStages);
+    }
+    while (ok && j >= 0) {
+      j = it.next();
+      const Pos v = pos;
+      pos.next(kStages);
+      if (j >= 0) {
+        ok = filled(pos) && wait_all<false>(sread, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        scores_of(pos);
+        pos.next(kStages);
+      }
+      ok = filled(v) && wait_all<false>(pfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      mma_rows(lead, tmem + Cfg::kO, tmem + Cfg::kP, dv + ((v.s * Cfg::kSlot) >> 4), id_o, n > 0);
+      commit(lead, pvfull);
+      commit(lead, &empty[v.s]);
+      ++n;
+    }
+    if (issued && lead) umma_drain(drain, kWaitLimitNs);
+  } else if (warp < 4) {
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t ts = tmem + lanes + Cfg::kS + warp * kPart;
+    const uint32_t tp = tmem + lanes + Cfg::kP, to = tmem + lanes + Cfg::kO;
+    const float slope2 = kForm > 0 && a.slopes != nullptr && mine ? a.slopes[h] * kLog2e : 0.f;
+    const int* docs = a.docs != nullptr ? a.docs + static_cast<long long>(b) * a.Tk : nullptr;
+    const int cols = x.steps * 16;
+    {
+      uint32_t zero[32];
+#pragma unroll
+      for (int u = 0; u < 32; ++u) zero[u] = 0u;
+      tmem_st_32cols(tp, zero);
+      tmem_st_32cols(tp + 32, zero);
+      tmem_st_wait();
+    }
+    Bits it(bits, words);
+    Pos vpos;
+    vpos.next(kStages);
+    float m = -INFINITY, l = 0.f;
+    int n = 0;
+    bool ok = true;
+    for (int j = it.next(); j >= 0; j = it.next(), ++n) {
+      ok = wait_warp<false>(sfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const int j0 = j * kTile, jq = j0 + warp * kPart;
+      bool dirty = j0 + kTile > top, by_doc = false;
+      if (docs != nullptr) {
+        const DocSpan s = key_tile_docs(a, b, j);
+        by_doc = s.pad || s.lo != s.hi || e.lo != s.lo || e.hi != s.lo;
+        dirty = dirty || s.pad;
+      }
+      float z[kPart];
+      tmem_ld_32cols(ts, z);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sread);
+      scores<kForm>(x, z, slope2, static_cast<float>(see.pos - jq));
+      if (jq + kPart > e.min_lim || by_doc) hide(z, see, docs, jq, a.Tk, by_doc);
+      const float mul = kForm == 0 ? x.c : 1.f;
+      float mt = z[0];
+#pragma unroll
+      for (int c = 1; c + 2 <= kPart; c += 2) mt = max3(mt, z[c], z[c + 1]);
+      mt = fmaxf(mt, z[kPart - 1]) * mul;
+      const bool grow = mt > m + kLazy || (m == -INFINITY && mt > m);
+      const bool rescale = __any_sync(0xffffffffu, grow);
+      const float f = grow ? ex2(m - mt) : 1.f;
+      if (grow) m = mt;
+      l *= f;
+      const float off = m == -INFINITY ? 0.f : -m;
+      float sum = 0.f;
+      uint32_t p[kPart / 2];
+#pragma unroll
+      for (int c = 0; c < kPart; c += 2) {
+        const float p0 = ex2(fmaf(z[c], mul, off)), p1 = ex2(fmaf(z[c + 1], mul, off));
+        sum += p0 + p1;
+        p[c / 2] = pack_bf16(p0, p1);
+      }
+      l += sum;
+      // the product of the tile before has read its weights and written its sums
+      if (n > 0) {
+        ok = wait_warp<false>(pvfull, (n - 1) & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (rescale) {
+          for (int c = 0; c < cols; c += 16) {
+            float o[16];
+            tmem_ld_16cols(to + c, o);
+            uint32_t u[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(o[q] * f);
+            tmem_st_16cols(to + c, u);
+          }
+        }
+      }
+      tmem_st_16cols(tp + warp * (kPart / 2), p);
+      tmem_st_wait();
+      if (dirty) {
+        // values that no row of the CTA sees may be anything, and 0 times NaN is NaN
+        ok = wait_warp<false>(&full[vpos.s], vpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        if (!ok) break;
+        const int r = threadIdx.x, key = j0 + r;
+        if (key >= top || (docs != nullptr && docs[key] < 0))
+          zero_row<kBlocks>(ring + vpos.s * Cfg::kSlot, r);
+        fence_proxy_async_smem();
+      }
+      vpos.next(kStages);
+      vpos.next(kStages);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pfull);
+    }
+    if (n > 0 && ok) ok = wait_warp<false>(pvfull, (n - 1) & 1, DPRC_DEVERR_ACCUM, abort_flag);
+    tc_fence_after();
+    // the four quarters: their maxima and sums, then their sums of values
+    stats[warp * kFewRows + lane] = make_float2(m, l);
+    if (lane == 0) done[warp] = ok ? 1 : 0;
+    named_bar_sync(1, 128);
+    ok = (done[0] & done[1] & done[2] & done[3]) != 0;  // the same for the four
+    const float2 s0 = stats[lane], s1 = stats[kFewRows + lane], s2 = stats[2 * kFewRows + lane],
+                 s3 = stats[3 * kFewRows + lane];
+    const float all = fmaxf(fmaxf(s0.x, s1.x), fmaxf(s2.x, s3.x));
+    const float at = all == -INFINITY ? 0.f : all, f = ex2(m - at);
+    const float total =
+        s0.y * ex2(s0.x - at) + s1.y * ex2(s1.x - at) + s2.y * ex2(s2.x - at) + s3.y * ex2(s3.x - at);
+    const int rows = a.Tq * a.G;
+    float* joined = reinterpret_cast<float*>(ring);  // [4][kFewRows][cols]
+    if (ok && n > 0) {
+      for (int c = 0; c < cols; c += 16) {
+        float o[16];
+        tmem_ld_16cols(to + c, o);
+        if (mine) {
+#pragma unroll
+          for (int q = 0; q < 16; q += 4) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[q + u] *= f;
+            store_row<4>(joined + (warp * kFewRows + lane) * cols + c + q, o + q);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    named_bar_sync(1, 128);
+    if (ok) {
+      const bool parts = a.splits > 1;
+      const long long prow = (static_cast<long long>(blockIdx.z) * bhs + bh) * rows;
+      if (warp == 0 && mine) {
+        stats[lane].y = parts ? 1.f : total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
+        if (parts) a.part_stats[prow + lane] = make_float2(all, total);
+        else if (a.lse != nullptr)
+          a.lse[(static_cast<long long>(b) * a.H + h) * a.Tq + tok] = all * kLn2 + logf(total);
+      }
+      named_bar_sync(1, 128);
+      const int eights = a.D / 8;
+      for (int i = threadIdx.x; i < rows * eights; i += 128) {
+        const int r = i / eights, c = (i - r * eights) * 8, t = r / a.G;
+        float o[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          o[u] = 0.f;
+          if (n > 0)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[u] += joined[(q * kFewRows + r) * cols + c + u];
+          o[u] *= stats[r].y;
+        }
+        if (parts) {
+          store_row<4>(a.part + (prow + r) * a.D + c, o);
+          store_row<4>(a.part + (prow + r) * a.D + c + 4, o + 4);
+        } else {
+          __nv_bfloat16* out =
+              static_cast<__nv_bfloat16*>(a.out) +
+              ((static_cast<long long>(b) * a.Tq + t) * a.H + hk * a.G + r - t * a.G) * a.D;
+          store_row<8>(out + c, o);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg::kTmem);
+  }
+}
+
+template <int kBlocks, int kForm>
+cudaError_t launch_few(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                       const TcArgs& x, cudaStream_t s) {
+  constexpr int bytes = FewCfg<kBlocks>::kSmem;
+  const cudaError_t e = allow_smem<attention_few_tc_kernel<kBlocks, kForm>>(bytes);
+  if (e != cudaSuccess) return e;
+  return launch_after(attention_few_tc_kernel<kBlocks, kForm>,
+                      dim3(x.a.B * x.a.Hkv, 1, x.a.splits), FewCfg<kBlocks>::kThreads, 1, s, bytes,
+                      q, k, v, x);
+}
+template <int kBlocks>
+cudaError_t launch_few_form(int form, const CUtensorMap& q, const CUtensorMap& k,
+                            const CUtensorMap& v, const TcArgs& x, cudaStream_t s) {
+  if (form == 0) return launch_few<kBlocks, 0>(q, k, v, x, s);
+  if (form == 1) return launch_few<kBlocks, 1>(q, k, v, x, s);
+  return launch_few<kBlocks, 2>(q, k, v, x, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -832,14 +1203,16 @@ __device__ __forceinline__ void store_grad(T* out, bool mine, uint32_t taddr, in
 #pragma unroll
       for (int q = 0; q < 16; ++q) o[q] = 0.f;
     }
-    if (!mine) continue;
+    if (mine) {
 #pragma unroll
-    for (int q = 0; q < 16; q += 8) {
-      if (c + q >= D) continue;
+      for (int q = 0; q < 16; q += 8) {
+        if (c + q >= D) continue;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) o[q + u] *= scale;
-      store8(out + c + q, o + q);
+        for (int u = 0; u < 8; ++u) o[q + u] *= scale;
+        store8(out + c + q, o + q);
+      }
     }
+    __syncwarp();  // (the next read is the whole warp's)
   }
 }
 
@@ -1654,14 +2027,25 @@ int attention_tc_rows(const AttentionCall& c) {
   return c.Tq > nt ? 2 * nt * G : nt * G;
 }
 
+int attention_tc_resident(const AttentionCall& c) {
+  const int G = static_cast<int>(c.H / c.Hkv);
+  if (c.Tq * G <= kFewRows) return c.D <= 64 ? 304 : 152;
+  return c.Tq > kTile / G ? 152 : 304;
+}
+
 cudaError_t launch_attention_tc(const AttnArgs& a, cudaStream_t s) {
-  const int nt = kTile / a.G, tiles = a.Tq > nt ? 2 : 1, form = form_of(a);
-  const TcArgs x = tc_args(a, tiles);
+  const bool few = a.Tq * a.G <= kFewRows;
+  const int nt = (few ? kFewRows : kTile) / a.G, tiles = a.Tq > nt ? 2 : 1, form = form_of(a);
+  TcArgs x = tc_args(a, tiles);
+  x.nt = nt;
   CUtensorMap q, k, v;
   if (!map_of(&q, a.Q, a.B, a.Tq, a.H, a.D, a.qb, a.qt, a.qh, a.G, nt) ||
       !map_of(&k, a.K, a.B, a.Tk, a.Hkv, a.D, a.kb, a.kt, a.kh, 1, kTile) ||
       !map_of(&v, a.V, a.B, a.Tk, a.Hkv, a.D, a.vb, a.vt, a.vh, 1, kTile))
     return cudaErrorInvalidValue;
+  if (few)
+    return a.D <= 64 ? launch_few_form<1>(form, q, k, v, x, s)
+                     : launch_few_form<2>(form, q, k, v, x, s);
   if (a.D <= 64)
     return tiles == 2 ? launch_fwd_form<1, 2>(form, q, k, v, x, s)
                       : launch_fwd_form<1, 1>(form, q, k, v, x, s);
