@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -787,25 +788,39 @@ def _rows(X):
     return B, (X.numel() // (B * d) if B * d > 0 else 0), d
 
 
+def _vector(name, t, dtype, n, dev):
+    """An optional contiguous vector of n."""
+    if t is not None:
+        _need_cuda(t)
+        _same(name, t, dtype, (n,), dev)
+        return t.data_ptr()
+    return None
+
+
 def dprc_layernorm(X, weight=None, bias=None, eps=1e-5, center=True, out=None, stats=None,
                    stream=None):
     """Layer normalisation of X [..., d] (center False: RMS normalisation) times weight
     plus bias; stats [..., 2] (fp32) receives (mean, 1 / deviation) for the gradient."""
-    _need_cuda(X, weight, bias, out, stats)
-    dt, dev = X.dtype, X.device
+    _need_cuda(X)
+    dt, dev, shape = X.dtype, X.device, X.shape
     code = _dtype_code(X)
-    B, T, d = _rows(X)
-    _same("weight", weight, dt, (d,), dev)
-    _same("bias", bias, dt, (d,), dev)
-    _same("out", out, dt, X.shape, dev)
-    _same("stats", stats, torch.float32, (*X.shape[:-1], 2), dev)
+    d = shape[-1]
+    w = _vector("weight", weight, dt, d, dev)
+    b = _vector("bias", bias, dt, d, dev)
     st = _stream(X, stream)
     if out is None:
-        out = _empty(X, X.shape, st, stream)
-    if X.numel() == 0 and d > 0:
+        out = _empty(X, shape, st, stream)
+    else:
+        _need_cuda(out)
+        _same("out", out, dt, shape, dev)
+    if stats is not None:
+        _need_cuda(stats)
+        _same("stats", stats, torch.float32, (*shape[:-1], 2), dev)
+    n = X.numel()
+    if n == 0 and d > 0:
         return out
     _check("dprc_layernorm",
-           lib().dprc_layernorm(X.data_ptr(), _ptr(weight), _ptr(bias), code, 1, B * T, d, eps,
+           lib().dprc_layernorm(X.data_ptr(), w, b, code, 1, n // max(d, 1), d, eps,
                                 1 if center else 0, out.data_ptr(), _ptr(stats), st))
     return out
 
@@ -815,18 +830,19 @@ def dprc_layernorm_grad(dY, X, stats, weight=None, center=True, dX=None, dW=None
     """Gradient of dprc_layernorm into those of dX [..., d], dW [d], db [d] that are given, and
     into n [B] the squared norms of each sample's dW (and db with norm_of_bias); c [B]:
     factors of the samples in dW and db.  X is [B, ..., d]; stats are the forward call's."""
-    _need_cuda(dY, X, stats, weight, dX, dW, db, n, c, ws)
-    dt, dev = dY.dtype, dY.device
+    _need_cuda(dY, X, stats, dX, ws)
+    dt, dev, shape = dY.dtype, dY.device, dY.shape
     code = _dtype_code(dY)
     B, T, d = _rows(X)
-    _same("X", X, dt, dY.shape, dev)
-    _same("stats", stats, torch.float32, (*X.shape[:-1], 2), dev)
-    _same("weight", weight, dt, (d,), dev)
-    _same("dX", dX, dt, dY.shape, dev)
-    _same("dW", dW, dt, (d,), dev)
-    _same("db", db, dt, (d,), dev)
-    _same("n", n, torch.float32, (B,), dev)
-    _same("c", c, torch.float32, (B,), dev)
+    _same("X", X, dt, shape, dev)
+    _same("stats", stats, torch.float32, (*shape[:-1], 2), dev)
+    if dX is not None:
+        _same("dX", dX, dt, shape, dev)
+    w = _vector("weight", weight, dt, d, dev)
+    dw = _vector("dW", dW, dt, d, dev)
+    dbias = _vector("db", db, dt, d, dev)
+    norms = _vector("n", n, torch.float32, B, dev)
+    factors = _vector("c", c, torch.float32, B, dev)
     _beside("ws", ws, dY)
     st = _stream(dY, stream)
     if ws is None:
@@ -835,27 +851,28 @@ def dprc_layernorm_grad(dY, X, stats, weight=None, center=True, dX=None, dW=None
             raise DprcError("dprc_layernorm_workspace_bytes", 2)
         ws = _scratch(size, dY, st, stream)
     _check("dprc_layernorm_grad",
-           lib().dprc_layernorm_grad(dY.data_ptr(), X.data_ptr(), stats.data_ptr(), _ptr(weight),
-                                     code, B, T, d, 1 if center else 0, _ptr(dX), _ptr(dW),
-                                     _ptr(db), _ptr(n), 1 if norm_of_bias else 0,
-                                     1 if accumulate else 0, _ptr(c), ws.data_ptr(), ws.numel(),
-                                     st))
+           lib().dprc_layernorm_grad(dY.data_ptr(), X.data_ptr(), stats.data_ptr(), w, code, B, T, d,
+                                     1 if center else 0, _ptr(dX), dw, dbias, norms,
+                                     1 if norm_of_bias else 0, 1 if accumulate else 0, factors,
+                                     ws.data_ptr(), ws.numel(), st))
 
 
 def _head_strides(name, t):
-    """The strides of [B][T][H][D] as the library takes them."""
-    if t.dim() != 4:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, four axes [B][T][H][D] are needed")
+    """The strides of [B][T][H][D] (of the first three axes) as the library takes them."""
+    if not t.is_cuda:
+        raise ValueError("libdprc takes device tensors")
     s = t.stride()
+    if len(s) != 4:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, four axes [B][T][H][D] are needed")
     if s[3] != 1 and t.shape[3] > 1:
         raise ValueError(f"{name}: a head's elements must lie together (stride {s[3]})")
-    return (ctypes.c_int64 * 3)(*s[:3])
+    return s[:3]
 
 
-def _on_cuda(*ts):
-    for t in ts:
-        if t is not None and not t.is_cuda:
-            raise ValueError("libdprc takes device tensors")
+# Arrays and structures of the C calls as bytes (a third of the time of ctypes objects).
+_I3 = struct.Struct("3q")
+# dprc_attention_args
+_ATTENTION_ARGS = struct.Struct("3P9qi4x6q2fi4x5P")
 
 
 def dprc_rotary(X, positions, freqs, sections=None, interleaved=False, inverse=False, out=None,
@@ -863,71 +880,65 @@ def dprc_rotary(X, positions, freqs, sections=None, interleaved=False, inverse=F
     """X [B][T][H][D] (any strides) with its pairs turned by positions times freqs (radians,
     float64 [P]); positions [B][T], or [B][T][axes] with the pairs of each axis in
     sections; out: a tensor of X's shape, X itself among them."""
-    _on_cuda(X, out)
-    _need_cuda(positions, freqs)
     xs = _head_strides("X", X)
-    B, T, H, D = X.shape
-    axes = 1 if positions.dim() == 2 else positions.shape[-1]
-    if tuple(positions.shape) not in ((B, T, axes), (B, T)) or axes < 1:
-        raise ValueError(f"positions have shape {tuple(positions.shape)}, X {tuple(X.shape)}")
+    _need_cuda(positions, freqs)
+    shape, dev = X.shape, X.device
+    B, T, H, D = shape
+    where = positions.shape
+    axes = where[2] if len(where) == 3 else 1
+    if where[:2] != (B, T) or not 2 <= len(where) <= 3 or axes < 1:
+        raise ValueError(f"positions have shape {tuple(where)}, X {tuple(shape)}")
     P = freqs.numel()
-    sections = [P] if sections is None else [int(v) for v in sections]
+    if sections is None:
+        sections = (P,)
     if len(sections) != axes or sum(sections) != P or min(sections) < 0:
         raise ValueError(f"sections {sections} of {axes} axes do not add up to {P} pairs")
     size = _token_bytes(positions)
-    _same("freqs", freqs, torch.float64, (P,), X.device)
+    _same("freqs", freqs, torch.float64, (P,), dev)
     _beside("positions", positions, X)
     st = _stream(X, stream)
     if out is None:
-        out = _empty(X, X.shape, st, stream)
+        out = _empty(X, shape, st, stream)
     else:
-        _same("out", out, X.dtype, X.shape, X.device)
+        _same("out", out, X.dtype, shape, dev)
     _check("dprc_rotary",
-           lib().dprc_rotary(X.data_ptr(), xs, _dtype_code(X), B, T, H, D, positions.data_ptr(),
-                             size, axes, (ctypes.c_int64 * axes)(*sections), freqs.data_ptr(),
-                             1 if interleaved else 0, 1 if inverse else 0, out.data_ptr(),
-                             _head_strides("out", out), st))
+           lib().dprc_rotary(X.data_ptr(), _I3.pack(*xs), _dtype_code(X), B, T, H, D,
+                             positions.data_ptr(), size, axes, struct.pack(f"{axes}q", *sections),
+                             freqs.data_ptr(), 1 if interleaved else 0, 1 if inverse else 0,
+                             out.data_ptr(), _I3.pack(*_head_strides("out", out)), st))
     return out
 
 
-class _AttentionArgs(ctypes.Structure):
-    _fields_ = [("Q", _c.c_void_p), ("K", _c.c_void_p), ("V", _c.c_void_p),
-                ("q_stride", _c.c_int64 * 3), ("k_stride", _c.c_int64 * 3),
-                ("v_stride", _c.c_int64 * 3), ("dtype", _c.c_int), ("B", _c.c_int64),
-                ("Tq", _c.c_int64), ("Tk", _c.c_int64), ("H", _c.c_int64), ("Hkv", _c.c_int64),
-                ("D", _c.c_int64), ("scale", _c.c_float), ("cap", _c.c_float),
-                ("causal", _c.c_int), ("slopes", _c.c_void_p), ("docs", _c.c_void_p),
-                ("prefix", _c.c_void_p), ("lengths", _c.c_void_p), ("first", _c.c_void_p)]
-
-
 def _attention_args(Q, K, V, scale, causal, cap, slopes, docs, prefix, lengths, first):
-    _on_cuda(Q, K, V)
-    _need_cuda(slopes, docs, prefix, lengths, first)
     qs, ks, vs = _head_strides("Q", Q), _head_strides("K", K), _head_strides("V", V)
     B, Tq, H, D = Q.shape
-    Tk, Hkv = K.shape[1], K.shape[2]
-    dev = Q.device
-    _same("K", K, Q.dtype, (B, Tk, Hkv, D), dev)
-    _same("V", V, Q.dtype, (B, Tk, Hkv, D), dev)
-    _same("slopes", slopes, torch.float32, (H,), dev)
-    _same("docs", docs, torch.int32, (B, Tk), dev)
-    _same("prefix", prefix, torch.int32, (B,), dev)
-    _same("lengths", lengths, torch.int32, (B,), dev)
-    _same("first", first, torch.int32, (B,), dev)
+    _, Tk, Hkv, _ = kshape = K.shape
+    dev, dt = Q.device, Q.dtype
+    if kshape != (B, Tk, Hkv, D):
+        raise ValueError(f"K has shape {tuple(kshape)}, Q {tuple(Q.shape)}")
+    _same("K", K, dt, kshape, dev)
+    _same("V", V, dt, kshape, dev)
+    if docs is not None:
+        _need_cuda(docs)
+        _same("docs", docs, torch.int32, (B, Tk), dev)
     if scale is None:
         scale = D ** -0.5 if D > 0 else 1.0
-    return _AttentionArgs(Q.data_ptr(), K.data_ptr(), V.data_ptr(), qs, ks, vs, _dtype_code(Q), B,
-                          Tq, Tk, H, Hkv, D, scale, cap, 1 if causal else 0, _ptr(slopes),
-                          _ptr(docs), _ptr(prefix), _ptr(lengths), _ptr(first))
+    i32 = torch.int32
+    return _ATTENTION_ARGS.pack(
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), *qs, *ks, *vs, _dtype_code(Q), B, Tq, Tk, H, Hkv,
+        D, scale, cap, 1 if causal else 0, _vector("slopes", slopes, torch.float32, H, dev) or 0,
+        0 if docs is None else docs.data_ptr(), _vector("prefix", prefix, i32, B, dev) or 0,
+        _vector("lengths", lengths, i32, B, dev) or 0, _vector("first", first, i32, B, dev) or 0)
 
 
 def _attention_ws(a, grad, like, ws, stream, given):
-    _beside("ws", ws, like)
     if ws is None:
-        size = lib().dprc_attention_workspace_bytes(ctypes.byref(a), grad)
+        size = lib().dprc_attention_workspace_bytes(a, grad)
         if size == 0:
             raise DprcError("dprc_attention_workspace_bytes", 2)
-        ws = _scratch(size, like, stream, given)
+        return _scratch(size, like, stream, given)
+    _need_cuda(ws)
+    _beside("ws", ws, like)
     return ws
 
 
@@ -939,17 +950,19 @@ def dprc_attention(Q, K, V, scale=None, causal=True, cap=0.0, slopes=None, docs=
     first[b] + t, Tk - Tq + t if not given).  lse [B][H][Tq] receives what the gradient
     needs."""
     a = _attention_args(Q, K, V, scale, causal, cap, slopes, docs, prefix, lengths, first)
-    B, Tq, H, D = Q.shape
-    _need_cuda(out, lse, ws)
-    _same("out", out, Q.dtype, Q.shape, Q.device)
-    _same("lse", lse, torch.float32, (B, H, Tq), Q.device)
+    shape = Q.shape
     st = _stream(Q, stream)
     if out is None:
-        out = _empty(Q, Q.shape, st, stream)
+        out = _empty(Q, shape, st, stream)
+    else:
+        _need_cuda(out)
+        _same("out", out, Q.dtype, shape, Q.device)
+    if lse is not None:
+        _need_cuda(lse)
+        _same("lse", lse, torch.float32, (shape[0], shape[2], shape[1]), Q.device)
     ws = _attention_ws(a, 0, Q, ws, st, stream)
     _check("dprc_attention",
-           lib().dprc_attention(ctypes.byref(a), out.data_ptr(), _ptr(lse), ws.data_ptr(),
-                                ws.numel(), st))
+           lib().dprc_attention(a, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), st))
     return out
 
 
@@ -959,20 +972,20 @@ def dprc_attention_grad(dO, Q, K, V, O, lse, scale=None, causal=True, cap=0.0, s
     """Gradient of dprc_attention (with the arguments of its call, its output O and lse)
     into those of dQ, dK and dV that are given; dO, O and these of any strides."""
     a = _attention_args(Q, K, V, scale, causal, cap, slopes, docs, prefix, lengths, first)
-    B, Tq, H, D = Q.shape
-    _need_cuda(lse, ws)
-    _on_cuda(dO, O, dQ, dK, dV)
-    _same("dO", dO, Q.dtype, Q.shape, Q.device)
-    _same("O", O, Q.dtype, Q.shape, Q.device)
-    _same("lse", lse, torch.float32, (B, H, Tq), Q.device)
-    _same("dQ", dQ, Q.dtype, Q.shape, Q.device)
-    _same("dK", dK, Q.dtype, K.shape, Q.device)
-    _same("dV", dV, Q.dtype, K.shape, Q.device)
-    strides = [None if t is None else _head_strides(name, t)
-               for name, t in (("dQ", dQ), ("dK", dK), ("dV", dV))]
+    shape, dt, dev = Q.shape, Q.dtype, Q.device
+    _need_cuda(lse)
+    _same("lse", lse, torch.float32, (shape[0], shape[2], shape[1]), dev)
+    strides = []
+    for name, t, like in (("dO", dO, shape), ("O", O, shape), ("dQ", dQ, shape), ("dK", dK, K.shape),
+                          ("dV", dV, K.shape)):
+        if t is None:
+            strides.append(None)
+            continue
+        strides.append(_I3.pack(*_head_strides(name, t)))
+        _same(name, t, dt, like, dev)
     st = _stream(Q, stream)
     ws = _attention_ws(a, 1, Q, ws, st, stream)
     _check("dprc_attention_grad",
-           lib().dprc_attention_grad(ctypes.byref(a), dO.data_ptr(), _head_strides("dO", dO),
-                                     O.data_ptr(), _head_strides("O", O), lse.data_ptr(), _ptr(dQ), strides[0], _ptr(dK), strides[1], _ptr(dV),
-                                     strides[2], ws.data_ptr(), ws.numel(), st))
+           lib().dprc_attention_grad(a, dO.data_ptr(), strides[0], O.data_ptr(), strides[1],
+                                     lse.data_ptr(), _ptr(dQ), strides[2], _ptr(dK), strides[3],
+                                     _ptr(dV), strides[4], ws.data_ptr(), ws.numel(), st))

@@ -162,8 +162,25 @@ def _strides(*v):
     return (ctypes.c_int64 * 3)(*v)
 
 
+class Args(ctypes.Structure):
+    """dprc_attention_args."""
+    _fields_ = [(n, ctypes.c_void_p) for n in "QKV"] + [
+        (n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride")] + [
+        ("dtype", ctypes.c_int)] + [(n, ctypes.c_int64) for n in ("B", "Tq", "Tk", "H", "Hkv", "D")] + [
+        ("scale", ctypes.c_float), ("cap", ctypes.c_float), ("causal", ctypes.c_int)] + [
+        (n, ctypes.c_void_p) for n in ("slopes", "docs", "prefix", "lengths", "first")]
+
+
+def test_packed_arguments_are_the_structure():
+    a = _args()
+    packed = binding._ATTENTION_ARGS.pack(A16, A16, A16, 1 << 20, 256, 64, 1 << 20, 128, 64, 1 << 20,
+                                          128, 64, 1, 2, 100, 100, 4, 2, 64, 0.125, 0.0, 1, 0, 0, 0,
+                                          0, 0)
+    assert packed == bytes(a)
+
+
 def _args(**kw):
-    a = binding._AttentionArgs(A16, A16, A16, _strides(1 << 20, 256, 64), _strides(1 << 20, 128, 64),
+    a = Args(A16, A16, A16, _strides(1 << 20, 256, 64), _strides(1 << 20, 128, 64),
                                _strides(1 << 20, 128, 64), 1, 2, 100, 100, 4, 2, 64, 0.125, 0.0, 1,
                                None, None, None, None, None)
     for k, v in kw.items():
