@@ -219,21 +219,17 @@ struct Bits {
   }
 };
 
-// Scores of one row in units of log2: what stands in z is q k; kForm 0: z times c is
-// the score (taken by the caller); 1: with the bias; 2: capped, with the bias.
+// Scores of one row in units of log2, from the products q k: kForm 0 leaves them (times c
+// they are the scores, which the caller takes); 1: with the bias; 2: capped; 3: both.
+// The cap: tanh(u) = 1 - 2 / (1 + exp(2 u)), to 2^-22 of it.
 template <int kForm, int kN>
 __device__ __forceinline__ void scores(const TcArgs& x, float (&z)[kN], float slope2, float dist0) {
-  if constexpr (kForm == 2) {
-    // tanh(u) = 1 - 2 / (1 + exp(2 u)), to 2^-22 of the cap
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const float t = fmaf(-2.f, rcp(1.f + ex2(z[j] * x.c_cap)), 1.f);
-      z[j] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(j)), t * x.cap2);
-    }
-  } else if constexpr (kForm == 1) {
-#pragma unroll
-    for (int j = 0; j < kN; ++j)
-      z[j] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(j)), z[j] * x.c);
+  for (int j = 0; j < kN; ++j) {
+    if constexpr (kForm >= 2) z[j] = fmaf(-2.f * x.cap2, rcp(1.f + ex2(z[j] * x.c_cap)), x.cap2);
+    else if constexpr (kForm == 1) z[j] *= x.c;
+    if constexpr (kForm == 1 || kForm == 3)
+      z[j] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(j)), z[j]);
   }
 }
 
@@ -281,21 +277,31 @@ __device__ __forceinline__ void hide(float (&z)[kN], const RowSees& see, const i
     if (!((bits[j / 32] >> (j & 31)) & 1u)) z[j] = -INFINITY;
 }
 
-// The softmax's weight of the product z (off: -lse, in units of log2), and in z that
-// weight times the cap's slope 1 - t^2.
+// The softmax's weights p of two products z (off: -lse, in units of log2), and in z those
+// weights times the cap's slope 1 - t^2.  The two capped scores share a reciprocal (beyond
+// 2^60 the sum of 1 and the exponential is held: tanh is 1 there); in the forward
+// pass, which waits for chains and not for the special functions, that was slower.
 template <int kForm>
-__device__ __forceinline__ float weight(const TcArgs& x, float& z, float slope2, float dist,
-                                        float off) {
-  if constexpr (kForm == 2) {
-    const float t = fmaf(-2.f, rcp(1.f + ex2(z * x.c_cap)), 1.f);
-    const float p = ex2(fmaf(-slope2, dist, fmaf(t, x.cap2, off)));
-    z = p * fmaf(-t, t, 1.f);
-    return p;
+__device__ __forceinline__ void weights2(const TcArgs& x, float* z, float* p, const float* slope2,
+                                         const float* dist, const float* off) {
+  if constexpr (kForm >= 2) {
+    const float a = 1.f + ex2(fminf(z[0] * x.c_cap, 60.f)), b = 1.f + ex2(fminf(z[1] * x.c_cap, 60.f));
+    const float r = -2.f * rcp(a * b);
+    const float t[2] = {fmaf(r, b, 1.f), fmaf(r, a, 1.f)};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float s = fmaf(t[u], x.cap2, off[u]);
+      if constexpr (kForm == 3) s = fmaf(-slope2[u], dist[u], s);
+      p[u] = ex2(s);
+      z[u] = p[u] * fmaf(-t[u], t[u], 1.f);
+    }
   } else {
-    float s = fmaf(z, x.c, off);
-    if constexpr (kForm == 1) s = fmaf(-slope2, dist, s);
-    z = ex2(s);
-    return z;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float s = fmaf(z[u], x.c, off[u]);
+      if constexpr (kForm == 1) s = fmaf(-slope2[u], dist[u], s);
+      z[u] = p[u] = ex2(s);
+    }
   }
 }
 
@@ -303,9 +309,14 @@ __device__ __forceinline__ float weight(const TcArgs& x, float& z, float slope2,
 template <int kForm, int kN>
 __device__ __forceinline__ void weights(const TcArgs& x, float (&z)[kN], float slope2, float dist0,
                                         float off) {
+  const float sl[2] = {slope2, slope2}, of[2] = {off, off};
 #pragma unroll
-  for (int j = 0; j < kN; ++j)
-    weight<kForm>(x, z[j], slope2, fabsf(dist0 - static_cast<float>(j)), off);
+  for (int j = 0; j < kN; j += 2) {
+    const float dist[2] = {fabsf(dist0 - static_cast<float>(j)),
+                           fabsf(dist0 - static_cast<float>(j + 1))};
+    float p[2];
+    weights2<kForm>(x, &z[j], p, sl, dist, of);
+  }
 }
 
 // What the rows of this warp, of this CTA see, for the choice of tiles and masks.
@@ -384,7 +395,11 @@ struct FwdCfg {
   static constexpr int kMore = kTiles == 1 ? 200 : 224, kLess = 56;
   static_assert(kThreads * kRegs == 32 * kSoft * kMore + 128 * kLess, "registers of the block");
   static constexpr int kSmem = kQ + kStages * kSlot + 1024 + 1024 + kMaxKeyTiles / 8;
-  static constexpr int kO = 128 * kTiles;  // first column of the sums
+  // Tiles of scores in tensor memory: a third one for narrow heads, so that a group's next
+  // scores are formed while it still has its last ones
+  static constexpr int kBufs = kTiles == 2 && kBlocks == 1 ? 3 : kTiles;
+  static constexpr int kO = 128 * kBufs;  // first column of the sums
+  static constexpr int kWide = kBufs == 3 ? 64 : 128;  // columns of a tile's sums
   static constexpr int kTmem = 256 * kTiles;
   static_assert((kTiles == 1 ? 2 : 1) * (kSmem + 1024) <= 228 * 1024, "shared memory of a CTA");
 };
@@ -407,10 +422,10 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * Cfg::kSlot);
   uint64_t* empty = full + kStages;
   uint64_t* qfull = empty + kStages;
-  uint64_t* sfull = qfull + 1;   // [2]
-  uint64_t* pfull = sfull + 2;   // [2]
-  uint64_t* ofull = pfull + 2;   // [2]
-  uint64_t* drain = ofull + 2;
+  uint64_t* sfull = qfull + 1;   // [kBufs], up to 3
+  uint64_t* pfull = sfull + 3;   // [2]
+  uint64_t* pvfull = pfull + 2;  // [2]
+  uint64_t* drain = pvfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* ext = reinterpret_cast<int*>(tmem_slot + 2);  // greatest limit, least and greatest document
@@ -429,10 +444,10 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
       mbar_init(&empty[s], 1);
     }
     mbar_init(qfull, 1);
+    for (int w = 0; w < 3; ++w) mbar_init(&sfull[w], 1);
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&sfull[w], 1);
       mbar_init(&pfull[w], active);
-      mbar_init(&ofull[w], 1);
+      mbar_init(&pvfull[w], 1);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -518,57 +533,64 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
     } else if (warp == Cfg::kSoft + 1) {
       // all lanes keep step, one issues: the descriptors stay in the warp's common registers
       const bool lead = elect_one() != 0;
-      Bits it(bits, words);
       const uint32_t id_s = make_idesc_bf16(kTile, kTile, false, false);
       const uint32_t id_o = make_idesc_bf16(kTile, x.steps * 16, false, true);
       const uint64_t dq = desc_k(smem_u32(qs));
       const uint64_t dk = desc_k(smem_u32(ring)), dv = desc_mn(smem_u32(ring));
-      Pos pos;
-      int j = it.next(), n = 0;
+      int tiles = 0;
+      for (int i = 0; i < words; ++i) tiles += __popc(bits[i]);
+      const int total = tiles * kTiles;
+      // Step i is tile i / kTiles of the keys and tile i % kTiles of the rows, its scores in
+      // buffer i % kBufs; unrolled over the steps after which these repeat, so that they
+      // are constants (with running numbers the issue of a step took longer than its products).
+      constexpr int kBufs = Cfg::kBufs, kPeriod = kBufs == 3 ? 6 : kBufs;
+      Pos kpos, vpos;  // keys lie in every second stage, values behind them
+      vpos.next(kStages);
       bool ok = true, issued = false;
-      if (j >= 0) {
-        ok = wait_all<true>(qfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
-             wait_all<true>(&full[0], 0, DPRC_DEVERR_PIPE_FULL, abort_flag);
-        if (ok) {
+      const auto scores_of = [&](int u) {
+        const int rows = u % kTiles, buf = u % kBufs;
+        if (rows == 0) {
+          if (!wait_all<false>(&full[kpos.s], kpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag)) return false;
           tc_fence_after();
-          issued = true;
-#pragma unroll
-          for (int u = 0; u < kTiles; ++u) {
-            mma_width<kBlocks, false>(lead, tmem + u * 128, dq + ((u * kBlocks * kBlock) >> 4), dk, id_s, x.steps);
-            commit(lead, &sfull[u]);
-          }
-          commit(lead, &empty[0]);
-          pos.next(kStages);
         }
-      }
-      while (j >= 0 && ok) {
-        j = it.next();
-        const Pos v = pos;
-        pos.next(kStages);
-        const Pos k = pos;
-        if (j >= 0) pos.next(kStages);
-        ok = wait_all<true>(&full[v.s], v.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
-        if (ok && j >= 0) ok = wait_all<true>(&full[k.s], k.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+        mma_width<kBlocks, kBlocks == 1>(lead, tmem + buf * 128,
+                                         dq + ((rows * kBlocks * kBlock) >> 4),
+                                         dk + ((kpos.s * Cfg::kSlot) >> 4), id_s, x.steps);
+        commit(lead, &sfull[buf]);
+        issued = true;
+        if (rows == kTiles - 1) {
+          commit(lead, &empty[kpos.s]);
+          kpos.next(kStages);
+          kpos.next(kStages);
+        }
+        return true;
+      };
+      if (total > 0) ok = wait_all<false>(qfull, 0, DPRC_DEVERR_PIPE_FULL, abort_flag);
 #pragma unroll
-        for (int u = 0; u < kTiles; ++u) {
-          ok = ok && wait_all<true>(&pfull[u], n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+      for (int u = 0; u < kBufs; ++u)
+        if (u < total) ok = ok && scores_of(u);
+      for (int i = 0; i < total && ok; i += kPeriod) {
+#pragma unroll
+        for (int u = 0; u < kPeriod; ++u) {
+          const int rows = u % kTiles, buf = u % kBufs;
+          if (i + u >= total) break;
+          const int t = i / kTiles + u / kTiles;
+          if (rows == 0)
+            ok = ok && wait_all<false>(&full[vpos.s], vpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+          ok = ok && wait_all<false>(&pfull[rows], t & 1, DPRC_DEVERR_ACCUM, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          mma_rows(lead, tmem + Cfg::kO + u * 128, tmem + u * 128, dv + ((v.s * Cfg::kSlot) >> 4), id_o,
-                   n > 0);
-          if (j >= 0) {
-            mma_width<kBlocks, false>(lead, tmem + u * 128, dq + ((u * kBlocks * kBlock) >> 4),
-                      dk + ((k.s * Cfg::kSlot) >> 4), id_s, x.steps);
-            commit(lead, &sfull[u]);
-          } else {
-            commit(lead, &ofull[u]);
+          mma_rows(lead, tmem + Cfg::kO + rows * Cfg::kWide, tmem + buf * 128,
+                   dv + ((vpos.s * Cfg::kSlot) >> 4), id_o, t > 0);
+          // (where a group's next scores are formed behind its product, they tell of it)
+          if (kBufs > kTiles || i + u + kTiles >= total) commit(lead, &pvfull[rows]);
+          if (rows == kTiles - 1) {
+            commit(lead, &empty[vpos.s]);
+            vpos.next(kStages);
+            vpos.next(kStages);
           }
+          if (i + u + kBufs < total) ok = scores_of(u + kBufs);
         }
-        if (ok) {
-          commit(lead, &empty[v.s]);
-          if (j >= 0) commit(lead, &empty[k.s]);
-        }
-        ++n;
       }
       if (issued && lead) umma_drain(drain, kWaitLimitNs);
     }
@@ -576,22 +598,29 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
     regs_more<Cfg::kMore>();
     if (kTiles == 2 || warp < active) {
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + Cfg::kO + w * 128;
+      const uint32_t to = tmem + lanes + Cfg::kO + w * Cfg::kWide;
       const int h = hk * a.G + r - tt * a.G;
       const float slope2 =
-          kForm > 0 && a.slopes != nullptr && mine ? a.slopes[h] * kLog2e : 0.f;
+          (kForm & 1) != 0 && a.slopes != nullptr && mine ? a.slopes[h] * kLog2e : 0.f;
       const int* docs = a.docs != nullptr ? a.docs + static_cast<long long>(b) * a.Tk : nullptr;
       const int cols = x.steps * 16;
       Bits it(bits, words);
       Pos vpos;  // the ring's place of this tile's values
       vpos.next(kStages);
       float m = -INFINITY, l = 0.f;
-      int n = 0;
+      int n = 0, buf = w;
+      uint32_t round = 0;  // of buf
       bool ok = true;
       for (int j = it.next(); j >= 0; j = it.next(), ++n) {
-        ok = wait_warp<true>(&sfull[w], n & 1, DPRC_DEVERR_ACCUM, abort_flag);
+        ok = wait_warp<kBlocks == 2>(&sfull[buf], round, DPRC_DEVERR_ACCUM, abort_flag);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t ts = tmem + lanes + buf * 128;
+        buf += kTiles;
+        if (buf >= Cfg::kBufs) {
+          buf -= Cfg::kBufs;
+          round ^= 1u;
+        }
         const int j0 = j * kTile;
         bool dirty = j0 + kTile > top, by_doc = false;
         if (docs != nullptr) {
@@ -599,21 +628,17 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
           by_doc = s.pad || s.lo != s.hi || e.lo != s.lo || e.hi != s.lo;
           dirty = dirty || s.pad;
         }
+        const float mul = kForm == 0 ? x.c : 1.f;
         float z[kTile];
         if constexpr (kTiles == 2) {
           tmem_ld_128cols(ts, z);
         } else {  // (128 at once take more registers than the block is launched with)
 #pragma unroll
-          for (int c = 0; c < kTile; c += 64) {
-            float part[64];
-            tmem_ld_64cols(ts + c, part);
-#pragma unroll
-            for (int u = 0; u < 64; ++u) z[c + u] = part[u];
-          }
+          for (int c = 0; c < kTile; c += 32)
+            tmem_ld_32cols(ts + c, reinterpret_cast<float(&)[32]>(z[c]));
         }
         scores<kForm>(x, z, slope2, static_cast<float>(see.pos - j0));
         if (j0 + kTile > e.min_lim || by_doc) hide(z, see, docs, j0, a.Tk, by_doc);
-        const float mul = kForm == 0 ? x.c : 1.f;
         float mx[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
         for (int c = 4; c + 8 <= kTile; c += 8)
@@ -628,6 +653,11 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
           if (grow) m = mt;
           l *= f;
           if (n > 0) {
+            if constexpr (Cfg::kBufs > kTiles) {
+              ok = wait_warp<kBlocks == 2>(&pvfull[w], (n - 1) & 1, DPRC_DEVERR_ACCUM, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+            }
             for (int c = 0; c < cols; c += 16) {
               float o[16];
               tmem_ld_16cols(to + c, o);
@@ -663,7 +693,7 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
         tmem_st_wait();
         if (dirty && w == 0) {
           // values that no row of the CTA sees may be anything, and 0 times NaN is NaN
-          ok = wait_warp<true>(&full[vpos.s], vpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
+          ok = wait_warp<kBlocks == 2>(&full[vpos.s], vpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
           if (!ok) break;
           for (int q = r; q < kTile; q += 32 * active) {
             const int key = j0 + q;
@@ -678,7 +708,8 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[w]);
       }
-      if (n > 0 && ok) ok = wait_warp<true>(&ofull[w], 0, DPRC_DEVERR_ACCUM, abort_flag);
+      if (n > 0 && ok)
+        ok = wait_warp<kBlocks == 2>(&pvfull[w], Cfg::kBufs > kTiles ? (n - 1) & 1 : 0, DPRC_DEVERR_ACCUM, abort_flag);
       tc_fence_after();
       if (ok) {
         const bool parts = a.splits > 1;
@@ -746,7 +777,8 @@ cudaError_t launch_fwd_form(int form, const CUtensorMap& q, const CUtensorMap& k
                             const CUtensorMap& v, const TcArgs& x, cudaStream_t s) {
   if (form == 0) return launch_fwd<kBlocks, kTiles, 0>(q, k, v, x, s);
   if (form == 1) return launch_fwd<kBlocks, kTiles, 1>(q, k, v, x, s);
-  return launch_fwd<kBlocks, kTiles, 2>(q, k, v, x, s);
+  if (form == 2) return launch_fwd<kBlocks, kTiles, 2>(q, k, v, x, s);
+  return launch_fwd<kBlocks, kTiles, 3>(q, k, v, x, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -938,7 +970,7 @@ __global__ void __launch_bounds__(FewCfg<kBlocks>::kThreads, FewCfg<kBlocks>::kR
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t ts = tmem + lanes + Cfg::kS + warp * kPart;
     const uint32_t tp = tmem + lanes + Cfg::kP, to = tmem + lanes + Cfg::kO;
-    const float slope2 = kForm > 0 && a.slopes != nullptr && mine ? a.slopes[h] * kLog2e : 0.f;
+    const float slope2 = (kForm & 1) != 0 && a.slopes != nullptr && mine ? a.slopes[h] * kLog2e : 0.f;
     const int* docs = a.docs != nullptr ? a.docs + static_cast<long long>(b) * a.Tk : nullptr;
     const int cols = x.steps * 16;
     {
@@ -1115,7 +1147,8 @@ cudaError_t launch_few_form(int form, const CUtensorMap& q, const CUtensorMap& k
                             const CUtensorMap& v, const TcArgs& x, cudaStream_t s) {
   if (form == 0) return launch_few<kBlocks, 0>(q, k, v, x, s);
   if (form == 1) return launch_few<kBlocks, 1>(q, k, v, x, s);
-  return launch_few<kBlocks, 2>(q, k, v, x, s);
+  if (form == 2) return launch_few<kBlocks, 2>(q, k, v, x, s);
+  return launch_few<kBlocks, 3>(q, k, v, x, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -1415,7 +1448,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     const uint32_t td = tmem + lanes + Cfg::kDp + part * kPart;
     const int h = hk * a.G + r - tt * a.G;
     const long long at = (static_cast<long long>(b) * a.H + h) * a.Tq + tok;
-    const float slope2 = kForm > 0 && a.slopes != nullptr && mine ? a.slopes[h] * kLog2e : 0.f;
+    const float slope2 = (kForm & 1) != 0 && a.slopes != nullptr && mine ? a.slopes[h] * kLog2e : 0.f;
     const float lse = mine ? a.lse_in[at] : 0.f, delta = mine ? a.delta[at] : 0.f;
     const float off = lse == -INFINITY ? 0.f : -lse * kLog2e;
     const int* docs = a.docs != nullptr ? a.docs + static_cast<long long>(b) * a.Tk : nullptr;
@@ -1733,7 +1766,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         tt[q] = r / a.G;
         const int h = hk * a.G + r - tt[q] * a.G;
         at[q] = (static_cast<long long>(b) * a.H + h) * a.Tq;
-        slope[q] = kForm > 0 && a.slopes != nullptr && tt[q] < x.nt ? a.slopes[h] * kLog2e : 0.f;
+        slope[q] = (kForm & 1) != 0 && a.slopes != nullptr && tt[q] < x.nt ? a.slopes[h] * kLog2e : 0.f;
       }
       RowSees see[4];
       float lse[4], del[4];
@@ -1843,14 +1876,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           const int c = q * 32 + u;
           float of[4], sl[4] = {0.f, 0.f, 0.f, 0.f}, ps[4] = {0.f, 0.f, 0.f, 0.f};
           ld_shared4(&st.off[c0 + c], of);
-          if constexpr (kForm > 0) {
+          if constexpr ((kForm & 1) != 0) {
             ld_shared4(&st.slope2[c0 + c], sl);
             ld_shared4(&st.pos[c0 + c], ps);
           }
           float w[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            w[k] = weight<kForm>(x, z[c + k], sl[k], fabsf(ps[k] - keyf), of[k]);
+          for (int k = 0; k < 4; k += 2) {
+            const float dist[2] = {fabsf(ps[k] - keyf), fabsf(ps[k + 1] - keyf)};
+            weights2<kForm>(x, &z[c + k], &w[k], &sl[k], dist, &of[k]);
           }
           p[u / 2] = pack_bf16(w[0], w[1]);
           p[u / 2 + 1] = pack_bf16(w[2], w[3]);
@@ -1959,7 +1993,8 @@ template <int kBlocks>
 cudaError_t launch_grad_form(int form, const GradMaps& m, const TcArgs& x, cudaStream_t s) {
   if (form == 0) return launch_grad<kBlocks, 0>(m, x, s);
   if (form == 1) return launch_grad<kBlocks, 1>(m, x, s);
-  return launch_grad<kBlocks, 2>(m, x, s);
+  if (form == 2) return launch_grad<kBlocks, 2>(m, x, s);
+  return launch_grad<kBlocks, 3>(m, x, s);
 }
 
 // A tensor [B][T][H][D] as boxes of 64 of the width, `heads` heads and `tokens` tokens.
@@ -1989,7 +2024,8 @@ TcArgs tc_args(const AttnArgs& a, int tiles) {
 }
 
 int form_of(const AttnArgs& a) {
-  return a.cap > 0.f ? 2 : a.slopes != nullptr || !(a.scale > 0.f) ? 1 : 0;
+  if (a.cap > 0.f) return a.slopes != nullptr ? 3 : 2;
+  return a.slopes != nullptr || !(a.scale > 0.f) ? 1 : 0;  // (1: any sign of the scale)
 }
 
 bool strides_fit(const int64_t* s, int64_t B, int64_t T, int64_t H) {
