@@ -33,15 +33,28 @@ constexpr int kMaxWarps = kLnWide / 32;
 // barrier is enough.
 template <int kN>
 __device__ __forceinline__ void row_sum(float (&v)[kN], int G, float* buf, int& turn) {
-  const int lim = G < 32 ? G : 32;
-  for (int o = 1; o < lim; o <<= 1)
+  const int lane = threadIdx.x & 31;
+  if (G >= 32 && kN == 2) {
+    // the upper half of the lanes sums the second value, so that one shuffle serves both
+    const bool upper = (lane & 16) != 0;
+    const float give = upper ? v[0] : v[1];
+    float keep = upper ? v[kN - 1] : v[0];
+    keep += __shfl_xor_sync(0xffffffffu, give, 16);
+    for (int o = 8; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+    const float other = __shfl_xor_sync(0xffffffffu, keep, 16);
+    v[0] = upper ? other : keep;
+    v[kN - 1] = upper ? keep : other;
+  } else {
+    const int lim = G < 32 ? G : 32;
+    for (int o = 1; o < lim; o <<= 1)
 #pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      for (int i = 0; i < kN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  }
   if (G <= 32) return;
   const int warp = threadIdx.x >> 5, per = G >> 5;
   float* b = buf + (turn & 1) * kMaxWarps * kN;
   ++turn;
-  if ((threadIdx.x & 31) == 0)
+  if (lane == 0)
 #pragma unroll
     for (int i = 0; i < kN; ++i) b[warp * kN + i] = v[i];
   __syncthreads();
@@ -86,39 +99,14 @@ struct RowAccess {
         if (c + e >= 0 && c + e < d) store_row<1>(out + e, v + e);
     }
   }
-  // the parameters from column c (a multiple of kE) on, 0 outside the row
-  __device__ __forceinline__ void whole_param(float* v, const T* p, int c) const {
-    Raw<T, kE> u;
-    u.zero();
-    if (c >= 0 && c + kE <= d) {
-      u.a = *reinterpret_cast<const decltype(u.a)*>(p + c);
-    } else if (c >= 0) {
-      T* e = reinterpret_cast<T*>(&u);
-      for (int i = 0; c + i < d; ++i) e[i] = p[c + i];
-    }
-    u.get(v);
-  }
   // parameters of the columns, `none` where there are none
   __device__ __forceinline__ void param(float* v, const T* p, int c, float none) const {
     if (p == nullptr) {
 #pragma unroll
       for (int e = 0; e < kE; ++e) v[e] = none;
     } else if constexpr (kOdd) {
-      // of two whole accesses, c - (kE - shift) and the next, the elements from kE - shift on
-      float two[2 * kE];
-      whole_param(two, p, c + shift - kE);
-      whole_param(two + kE, p, c + shift);
-      switch (shift) {  // (the same for a row)
-#define DPRC_SHIFT(n)                                                      \
-  case n:                                                                  \
-    if constexpr (n < kE) {                                                \
-      _Pragma("unroll") for (int e = 0; e < kE; ++e) v[e] = two[kE - n + e]; \
-    }                                                                      \
-    break;
-        DPRC_SHIFT(0) DPRC_SHIFT(1) DPRC_SHIFT(2) DPRC_SHIFT(3)
-        DPRC_SHIFT(4) DPRC_SHIFT(5) DPRC_SHIFT(6) DPRC_SHIFT(7)
-#undef DPRC_SHIFT
-      }
+#pragma unroll
+      for (int e = 0; e < kE; ++e) v[e] = c + e >= 0 && c + e < d ? to_f32<T>(p[c + e]) : 0.f;
     } else {
       Raw<T, kE> u;
       u.a = *reinterpret_cast<const decltype(u.a)*>(p + c);
@@ -232,64 +220,44 @@ struct LnGradArgs {
   float* part;           // [samples][CTAs][2][d]
 };
 
-// A group of G threads takes kRows rows at a time, so that one round of sums serves
-// them, and reads the next ones before it sums.  A group's rows are a multiple of kE
-// apart where the width is odd, so that they have the same shift and a thread the same
-// columns: its weights and sums stay in registers.  kWide: a row has all 512 threads,
-// and the sums stand in shared memory, each column's where its thread alone adds to it.
-template <typename T, int kE, int kNv, int kRows, bool kOdd, bool kWide>
-__global__ void __launch_bounds__(kWide ? kLnWide : kLnThreads)
+// Wide rows: a CTA of 512 threads takes a row at a time and reads the next one before it
+// sums.  The sums over rows stand in shared memory, each column's where its thread alone
+// adds to it.  A CTA's rows are kE apart where the width is odd, so that they have the
+// same shift and a thread the same columns.
+template <typename T, int kE, int kNv, bool kOdd>
+__global__ void __launch_bounds__(kLnWide)
     layernorm_grad_kernel(const T* dy, const T* x, const T* w, T* dx, const LnGradArgs a) {
   constexpr int kC = kNv * kE;
-  __shared__ float buf[2 * kMaxWarps * 2 * kRows];
-  extern __shared__ float sums[];  // kWide: [2][kC][512]; else [2][d], the groups in turn
+  __shared__ float buf[2 * kMaxWarps * 2];
+  extern __shared__ __align__(16) float sums[];  // [2][kC / 2][512] pairs
   pdl_launch_dependents();
   pdl_wait();
   int turn = 0;
-  const int d = a.d, G = a.G;
-  const int t = threadIdx.x & (G - 1), groups = blockDim.x / G, grp = threadIdx.x / G;
+  const int d = a.d, G = kLnWide, t = threadIdx.x;
   const long long base = blockIdx.y * a.rows;  // the sample's first row
   const int chunk = blockIdx.x / a.classes, cls = blockIdx.x - chunk * a.classes;
   const long long r0 = chunk * a.per_chunk;
   const long long r1 = min(r0 + a.per_chunk, a.rows);
-  const int stride = kOdd ? max(groups, kE) : groups;
-  const long long first = r0 + cls * groups + grp;
+  const int stride = kOdd ? kE : 1;
+  const long long first = r0 + cls;
   const RowAccess<T, kE, kOdd> at(d, base + first, a.all);
   const float inv = 1.f / static_cast<float>(d);
-  float wf[kWide ? 1 : kC];
-  F2 wsum[kWide ? 1 : kC / 2], bsum[kWide ? 1 : kC / 2];
+  F2* wsum = reinterpret_cast<F2*>(sums) + t;
+  F2* bsum = wsum + kC / 2 * kLnWide;
 #pragma unroll
-  for (int k = 0; k < kNv; ++k) {
-    const int c = at.col(k * G + t);
-    if (!kWide && at.any(c)) at.param(wf + (kWide ? 0 : k * kE), w, c, 1.f);
-  }
+  for (int i = 0; i < kC / 2; ++i) wsum[i * kLnWide] = bsum[i * kLnWide] = f2(0.f, 0.f);
+  Raw<T, kE> xv[kNv], gv[kNv];
+  float2 st = make_float2(0.f, 0.f);
+  const auto fetch = [&](long long q) {
+    if (q >= r1) return;
+    st = ld_once(a.stats + base + q);
 #pragma unroll
-  for (int i = 0; i < kC / 2; ++i) {
-    if constexpr (kWide)
-      reinterpret_cast<F2*>(sums)[i * kLnWide + threadIdx.x] =
-          reinterpret_cast<F2*>(sums)[(kC / 2 + i) * kLnWide + threadIdx.x] = f2(0.f, 0.f);
-    else wsum[i] = bsum[i] = f2(0.f, 0.f);
-  }
-  Raw<T, kE> xv[kRows][kNv], gv[kRows][kNv];
-  float2 st[kRows];
-  const auto fetch = [&](long long r) {
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const long long q = r + j * stride;
-      const bool mine = q < r1;
-      if (mine) st[j] = ld_once(a.stats + base + q);
-#pragma unroll
-      for (int k = 0; k < kNv; ++k) {
-        const int c = at.col(k * G + t);
-        if (mine && at.any(c)) {
-          at.load(xv[j][k], x, base + q, c);
-          at.load(gv[j][k], dy, base + q, c);
-        } else {
-          xv[j][k].zero();
-          gv[j][k].zero();
-        }
+    for (int k = 0; k < kNv; ++k) {
+      const int c = at.col(k * G + t);
+      if (at.any(c)) {
+        at.load(xv[k], x, base + q, c);
+        at.load(gv[k], dy, base + q, c);
       }
-      if (!mine) st[j] = make_float2(0.f, 0.f);
     }
   };
   // x - mu and dy of an access in pairs, 0 outside the row
@@ -313,115 +281,313 @@ __global__ void __launch_bounds__(kWide ? kLnWide : kLnThreads)
       g[e] = f2(v[2 * e], v[2 * e + 1]);
     }
   };
-  // the weights of access k: a wide row's are read again (from L1)
+  // the weights of access k, read again (from L1)
   const auto weights = [&](int k, F2* w2) {
     float u[kE];
-    if constexpr (kWide) at.param(u, w, at.col(k * G + t), 1.f);
+    at.param(u, w, at.col(k * G + t), 1.f);
 #pragma unroll
-    for (int e = 0; e < kE / 2; ++e)
-      w2[e] = kWide ? f2(u[2 * e], u[2 * e + 1]) : f2(wf[kWide ? 0 : k * kE + 2 * e],
-                                                      wf[kWide ? 0 : k * kE + 2 * e + 1]);
+    for (int e = 0; e < kE / 2; ++e) w2[e] = f2(u[2 * e], u[2 * e + 1]);
   };
   fetch(first);
-  // (the same number of rounds for every group of the CTA)
-  for (long long r = first; r - grp < r1; r += stride * kRows) {
-    F2 dm[kRows][kC / 2], g[kRows][kC / 2];  // x - mu, dy
-    float2 sc[kRows];
-    float s[2 * kRows];
+  for (long long r = first; r < r1; r += stride) {  // (the same for the CTA)
+    F2 dm[kC / 2], g[kC / 2];  // x - mu, dy
+    const float2 sc = st;
+    F2 s0 = f2(0.f, 0.f), s1 = s0;
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      sc[j] = st[j];
-      F2 s0 = f2(0.f, 0.f), s1 = s0;
+    for (int k = 0; k < kNv; ++k) {
+      const int c = at.col(k * G + t);
+      if (!at.any(c)) continue;
+      values(xv[k], gv[k], sc.x, c, &dm[k * kE / 2], &g[k * kE / 2]);
+      F2 w2[kE / 2];
+      weights(k, w2);
 #pragma unroll
-      for (int k = 0; k < kNv; ++k) {
-        const int c = at.col(k * G + t);
-        if (!at.any(c)) continue;
-        values(xv[j][k], gv[j][k], sc[j].x, c, &dm[j][k * kE / 2], &g[j][k * kE / 2]);
-        F2 w2[kE / 2];
-        weights(k, w2);
-#pragma unroll
-        for (int e = 0; e < kE / 2; ++e) {
-          const int i = k * kE / 2 + e;
-          const F2 gw = mul2(g[j][i], w2[e]);
-          s0 = add2(s0, gw);
-          s1 = fma2(gw, dm[j][i], s1);
-        }
+      for (int e = 0; e < kE / 2; ++e) {
+        const int i = k * kE / 2 + e;
+        const F2 gw = mul2(g[i], w2[e]);
+        s0 = add2(s0, gw);
+        s1 = fma2(gw, dm[i], s1);
       }
-      float u, v;
-      split(s0, u, v);
-      s[2 * j] = u + v;
-      split(s1, u, v);
-      s[2 * j + 1] = u + v;
     }
-    fetch(r + stride * kRows);  // the next rows are on their way while these are summed
-    if (dx != nullptr) row_sum<2 * kRows>(s, G, buf, turn);
+    float s[2], u;
+    split(s0, s[0], u);
+    s[0] += u;
+    split(s1, s[1], u);
+    s[1] += u;
+    fetch(r + stride);  // the next row is on its way while this one is summed
+    if (dx != nullptr) row_sum<2>(s, G, buf, turn);
+    // dx = r g + (x - mu) (-r^3 mean(g (x - mu))) - r mean(g)
+    const float rs = sc.y, f = a.c != nullptr ? a.c[(base + r) / a.T] : 1.f;
+    const float along = -rs * rs * rs * (s[1] * inv);
+    const float rest = a.center ? -rs * (s[0] * inv) : 0.f;
+    const F2 rs2 = f2(rs, rs), along2 = f2(along, along), rest2 = f2(rest, rest);
+    const F2 fr2 = f2(f * rs, f * rs), f22 = f2(f, f);
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+      const int c = at.col(k * G + t);
+      if (!at.any(c)) continue;
+      float out[kE];
+      F2 w2[kE / 2];
+      weights(k, w2);
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e) {
+        const int i = k * kE / 2 + e;
+        const F2 o = fma2(dm[i], along2, fma2(mul2(g[i], w2[e]), rs2, rest2));
+        split(o, out[2 * e], out[2 * e + 1]);
+        wsum[i * kLnWide] = fma2(mul2(g[i], fr2), dm[i], wsum[i * kLnWide]);
+        bsum[i * kLnWide] = fma2(g[i], f22, bsum[i * kLnWide]);
+      }
+      if (dx != nullptr) at.store(dx, base + r, c, out);
+    }
+  }
+  if (!a.sums) return;
+  float* part = a.part + (blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x) * 2 * d;
+#pragma unroll
+  for (int i = 0; i < kC / 2; ++i) {
+    float wv[2], bv[2];
+    split(wsum[i * kLnWide], wv[0], wv[1]);
+    split(bsum[i * kLnWide], bv[0], bv[1]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int c = at.col(2 * i / kE * G + t) + (2 * i + q) % kE;
+      if (c < 0 || c >= d) continue;
+      part[c] = wv[q];
+      part[d + c] = bv[q];
+    }
+  }
+}
+
+// Rows of up to 4096 elements: blocks of rows of both tensors come by bulk copies into a
+// ring of stages in shared memory, several blocks ahead, so that the memory always has
+// enough to do; the registers hold a block's values and the columns' sums.  A block
+// starts at any element (odd widths): its copy starts at the 16 bytes before, and what it
+// leaves of the tensor's last bytes is read element by element.  Odd widths are taken
+// an element an access (kE = 1), neighbouring threads neighbouring columns.
+constexpr int kRingBytes = 96 * 1024;
+constexpr int kMaxRing = 8;
+constexpr int kRingMost = 112 * 1024;  // what a CTA may take, two to an SM
+
+struct RingPlan {
+  int rows, stages, bytes;  // rows of a block; bytes of a tensor's block in a stage
+};
+__host__ __device__ inline RingPlan ring_plan(int d, int size, int G, int rows) {
+  RingPlan p;
+  p.rows = kLnThreads / G * rows;
+  p.bytes = (p.rows * d * size + 15) / 16 * 16 + 16;
+  p.stages = kRingBytes / (2 * p.bytes);
+  p.stages = p.stages < 2 ? 2 : p.stages > kMaxRing ? kMaxRing : p.stages;
+  return p;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+template <typename T, int kE, int kNv, int kRows>
+__global__ void __launch_bounds__(kLnThreads, 2)
+    layernorm_grad_ring_kernel(const T* dy, const T* x, const T* w, T* dx, const LnGradArgs a) {
+  constexpr int kC = kNv * kE;
+  static_assert(kC % 2 == 0, "pairs");
+  __shared__ float buf[2 * kMaxWarps * 2 * kRows];
+  __shared__ uint64_t full[kMaxRing];
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  const int d = a.d, G = a.G;
+  const RingPlan plan = ring_plan(d, sizeof(T), G, kRows);
+  uint8_t* ring = ring_raw;  // [stages][x, dy][bytes]; at the end the groups' sums [2][d]
+  float* sums = reinterpret_cast<float*>(ring_raw);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < plan.stages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  __syncthreads();
+  pdl_wait();
+  int turn = 0;
+  const int t = threadIdx.x & (G - 1), groups = kLnThreads / G, grp = threadIdx.x / G;
+  const long long base = blockIdx.y * a.rows;  // the sample's first row
+  const long long r0 = blockIdx.x * a.per_chunk;
+  const long long r1 = min(r0 + a.per_chunk, a.rows);
+  const int blocks = r1 > r0 ? static_cast<int>((r1 - r0 + plan.rows - 1) / plan.rows) : 0;
+  const long long end = a.all * d;  // elements of a tensor
+  constexpr int kU = 16 / static_cast<int>(sizeof(T));
+  // block k: its first element, and the whole 16 bytes that the copies bring
+  const auto first_of = [&](int k) { return (base + r0 + static_cast<long long>(k) * plan.rows) * d; };
+  const auto copied = [&](int k, long long& from) {  // elements
+    const long long e0 = first_of(k);
+    const long long e1 = min(e0 + static_cast<long long>(plan.rows) * d, (base + r1) * d);
+    from = e0 / kU * kU;
+    return static_cast<int>(min((e1 + kU - 1) / kU * kU, end / kU * kU) - from);
+  };
+  const auto issue = [&](int k, int s) {
+    long long from;
+    const int n = copied(k, from);
+    const int bytes = n * static_cast<int>(sizeof(T));
+    uint8_t* to = ring + s * 2 * plan.bytes;
+    mbar_arrive_expect_tx(&full[s], 2 * (bytes > 0 ? bytes : 0));
+    if (bytes > 0) {
+      bulk_load(to, x + from, bytes, &full[s]);
+      bulk_load(to + plan.bytes, dy + from, bytes, &full[s]);
+    }
+  };
+  if (threadIdx.x == 0)
+    for (int k = 0; k < plan.stages && k < blocks; ++k) issue(k, k);
+  const float inv = 1.f / static_cast<float>(d);
+  F2 w2[kC / 2], wsum[kC / 2], bsum[kC / 2];
+  const auto col = [&](int f) { return (f / kE * G + t) * kE + f % kE; };
+#pragma unroll
+  for (int i = 0; i < kC / 2; ++i) {
+    float u[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int c = col(2 * i + q);
+      u[q] = c < d ? (w != nullptr ? to_f32<T>(w[c]) : 1.f) : 0.f;
+    }
+    w2[i] = f2(u[0], u[1]);
+    wsum[i] = bsum[i] = f2(0.f, 0.f);
+  }
+  // (running values: an index formed anew for each block took a third of the instructions)
+  int left = static_cast<int>(r1 - r0) - grp;  // rows from the group's on
+  const float2* sp = a.stats + base + r0 + grp;
+  T* dxp = dx != nullptr ? dx + (base + r0 + grp) * d + t * kE : nullptr;
+  const long long dx_step = static_cast<long long>(plan.rows) * d;
+  float2 ahead[kRows];
+  const auto stats_of = [&]() {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+      ahead[j] = j * groups < left ? ld_once(sp + j * groups) : make_float2(0.f, 0.f);
+  };
+  stats_of();
+  int s = 0;
+  uint32_t round = 0;
+  for (int k = 0; k < blocks; ++k) {
+    long long from = 0;
+    int n = 0, shift = 0;
+    if constexpr (kE == 1) {
+      n = copied(k, from);
+      shift = static_cast<int>(first_of(k) - from);
+    }
+    const T* xs = reinterpret_cast<const T*>(ring + s * 2 * plan.bytes);
+    const T* gs = reinterpret_cast<const T*>(ring + s * 2 * plan.bytes + plan.bytes);
+    const int have = left;
+    float2 st[kRows];
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) st[j] = ahead[j];
+    sp += plan.rows;
+    left -= plan.rows;
+    stats_of();  // the next block's are on their way while this one is taken
+    // (a copy that was started ends; a wait that runs out is recorded)
+    mbar_wait(&full[s], round, DPRC_DEVERR_PIPE_FULL);
+    F2 dm[kRows][kC / 2], g[kRows][kC / 2];  // x - mu, dy
+    float sum[2 * kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      const long long q = r + j * stride;
-      if (q >= r1) continue;
-      // dx = r g + (x - mu) (-r^3 mean(g (x - mu))) - r mean(g)
-      const float rs = sc[j].y, f = a.c != nullptr ? a.c[(base + q) / a.T] : 1.f;
-      const float along = -rs * rs * rs * (s[2 * j + 1] * inv);
-      const float rest = a.center ? -rs * (s[2 * j] * inv) : 0.f;
-      const F2 rs2 = f2(rs, rs), along2 = f2(along, along), rest2 = f2(rest, rest);
-      const F2 fr2 = f2(f * rs, f * rs), f22 = f2(f, f);
+      const int lr = j * groups + grp;
+      const bool mine = j * groups < have;
+      F2 s0 = f2(0.f, 0.f), s1 = s0;
+      float xv[kC], gv[kC];
 #pragma unroll
-      for (int k = 0; k < kNv; ++k) {
-        const int c = at.col(k * G + t);
-        if (!at.any(c)) continue;
-        float out[kE];
-        F2 w2[kE / 2];
-        weights(k, w2);
-#pragma unroll
-        for (int e = 0; e < kE / 2; ++e) {
-          const int i = k * kE / 2 + e;
-          const F2 o = fma2(dm[j][i], along2, fma2(mul2(g[j][i], w2[e]), rs2, rest2));
-          split(o, out[2 * e], out[2 * e + 1]);
-          const F2 gx = mul2(g[j][i], fr2);
-          if constexpr (kWide) {
-            F2* ws = reinterpret_cast<F2*>(sums) + i * kLnWide + threadIdx.x;
-            F2* bs = ws + kC / 2 * kLnWide;
-            *ws = fma2(gx, dm[j][i], *ws);
-            *bs = fma2(g[j][i], f22, *bs);
+      for (int v = 0; v < kNv; ++v) {
+        const int c = (v * G + t) * kE, at = shift + lr * d + c;
+        if (mine && c < d) {
+          if constexpr (kE == 1) {
+            // the tensor's last bytes, which the copies leave, are read where they are
+            xv[v] = to_f32<T>(at < n ? xs[at] : x[from + at]);
+            gv[v] = to_f32<T>(at < n ? gs[at] : dy[from + at]);
           } else {
-            wsum[i] = fma2(gx, dm[j][i], wsum[i]);
-            bsum[i] = fma2(g[j][i], f22, bsum[i]);
+            Raw<T, kE> u;
+            u.a = *reinterpret_cast<const decltype(u.a)*>(xs + at);
+            u.get(xv + v * kE);
+            u.a = *reinterpret_cast<const decltype(u.a)*>(gs + at);
+            u.get(gv + v * kE);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            xv[v * kE + e] = st[j].x;
+            gv[v * kE + e] = 0.f;
           }
         }
-        if (dx != nullptr) at.store(dx, base + q, c, out);
+      }
+      const F2 mu = f2(-st[j].x, -st[j].x);
+#pragma unroll
+      for (int i = 0; i < kC / 2; ++i) {
+        dm[j][i] = add2(f2(xv[2 * i], xv[2 * i + 1]), mu);
+        g[j][i] = f2(gv[2 * i], gv[2 * i + 1]);
+        const F2 gw = mul2(g[j][i], w2[i]);
+        s0 = add2(s0, gw);
+        s1 = fma2(gw, dm[j][i], s1);
+      }
+      float u;
+      split(s0, sum[2 * j], u);
+      sum[2 * j] += u;
+      split(s1, sum[2 * j + 1], u);
+      sum[2 * j + 1] += u;
+    }
+    row_sum<2 * kRows>(sum, G, buf, turn);
+    if (G <= 32) __syncthreads();  // (else the sums' barrier)
+    // everyone has read the stage
+    if (threadIdx.x == 0 && k + plan.stages < blocks) issue(k + plan.stages, s);
+    if (++s == plan.stages) {
+      s = 0;
+      round ^= 1u;
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      if (j * groups >= have) continue;
+      // dx = r g + (x - mu) (-r^3 mean(g (x - mu))) - r mean(g)
+      float f = 1.f;
+      if (a.c != nullptr)
+        f = a.c[(base + r0 + static_cast<long long>(k) * plan.rows + j * groups + grp) / a.T];
+      const float rs = st[j].y;
+      const float along = -rs * rs * rs * (sum[2 * j + 1] * inv);
+      const float rest = a.center ? -rs * (sum[2 * j] * inv) : 0.f;
+      const F2 rs2 = f2(rs, rs), along2 = f2(along, along), rest2 = f2(rest, rest);
+      const F2 fr2 = f2(f * rs, f * rs), f22 = f2(f, f);
+      float out[kC];
+#pragma unroll
+      for (int i = 0; i < kC / 2; ++i) {
+        const F2 o = fma2(dm[j][i], along2, fma2(mul2(g[j][i], w2[i]), rs2, rest2));
+        split(o, out[2 * i], out[2 * i + 1]);
+        wsum[i] = fma2(mul2(g[j][i], fr2), dm[j][i], wsum[i]);
+        bsum[i] = fma2(g[j][i], f22, bsum[i]);
+      }
+      if (dx != nullptr) {
+#pragma unroll
+        for (int v = 0; v < kNv; ++v) {
+          const int c = (v * G + t) * kE;
+          if (c < d) store_row<kE>(dxp + j * groups * d + v * G * kE, out + v * kE);
+        }
       }
     }
+    if (dx != nullptr) dxp += dx_step;
   }
   if (!a.sums) return;
   float* part = a.part + (blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x) * 2 * d;
   // the groups of the CTA in order, each adding its columns
   for (int q = 0; q < groups; ++q) {
-    if (grp == q) {
+    __syncthreads();
+    if (grp != q) continue;
 #pragma unroll
-      for (int i = 0; i < kC / 2; ++i) {
-        float wv[2], bv[2];
-        if constexpr (kWide) {
-          split(reinterpret_cast<F2*>(sums)[i * kLnWide + threadIdx.x], wv[0], wv[1]);
-          split(reinterpret_cast<F2*>(sums)[(kC / 2 + i) * kLnWide + threadIdx.x], bv[0], bv[1]);
-        } else {
-          split(wsum[i], wv[0], wv[1]);
-          split(bsum[i], bv[0], bv[1]);
-        }
+    for (int i = 0; i < kC / 2; ++i) {
+      float wv[2], bv[2];
+      split(wsum[i], wv[0], wv[1]);
+      split(bsum[i], bv[0], bv[1]);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int c = at.col(2 * i / kE * G + t) + (2 * i + u) % kE;
-          if (c < 0 || c >= d) continue;
-          if (q > 0) {
-            wv[u] += sums[c];
-            bv[u] += sums[d + c];
-          }
-          float* out = q + 1 < groups ? sums : part;
-          out[c] = wv[u];
-          out[d + c] = bv[u];
+      for (int u = 0; u < 2; ++u) {
+        const int c = col(2 * i + u);
+        if (c >= d) continue;
+        if (q > 0) {
+          wv[u] += sums[c];
+          bv[u] += sums[d + c];
         }
+        float* out = q + 1 < groups ? sums : part;
+        out[c] = wv[u];
+        out[d + c] = bv[u];
       }
     }
-    if (q + 1 < groups) __syncthreads();
   }
 }
 
@@ -531,9 +697,11 @@ LnPlan plan_grad(int64_t B, int64_t T, bool by_sample, int64_t classes) {
   return p;
 }
 
-// Threads of a row and accesses of a thread: `acc` accesses of kE elements.
+// Threads of a row and accesses of a thread.  Up to 4096 elements (16 a thread): the ring,
+// of accesses of 16 bytes or of an element; wider: accesses of 16 bytes, shifted (one more)
+// where the width is odd.
 struct RowShape {
-  bool odd;
+  bool odd, wide;
   int G;
   int64_t nv;
 };
@@ -542,16 +710,19 @@ RowShape grad_shape(int64_t d) {
   constexpr int kV = kVec16<T>;
   RowShape r;
   r.odd = !whole_vectors<T>(d);
-  const int64_t acc = (d + kV - 1) / kV + (r.odd ? 1 : 0);  // (a shift adds one)
-  r.G = acc * kV > kLnThreads * 16 ? kLnWide : pow2_at_least(acc, 8, kLnThreads);
+  r.wide = d > kLnThreads * 16;
+  int64_t acc = r.odd && !r.wide ? d : (d + kV - 1) / kV;
+  if (r.wide && r.odd) ++acc;
+  // 16 elements a thread: the sums of a row, whose operations a thread has whatever its
+  // share, are spread over fewer threads
+  r.G = r.wide ? kLnWide : pow2_at_least((acc * (r.odd ? 1 : kV) + 15) / 16, 8, kLnThreads);
   r.nv = (acc + r.G - 1) / r.G;
   return r;
 }
 template <typename T>
 int64_t grad_classes(int64_t d) {
   const RowShape r = grad_shape<T>(d);
-  const int groups = r.G == kLnWide ? 1 : kLnThreads / r.G;
-  return r.odd ? std::max(1, kVec16<T> / groups) : 1;
+  return r.odd && r.wide ? kVec16<T> : 1;
 }
 
 template <typename T>
@@ -613,38 +784,44 @@ cudaError_t backward(const LayernormGradCall& c, void* ws, cudaStream_t s) {
                         static_cast<const T*>(c.X), static_cast<const T*>(c.weight),
                         static_cast<T*>(c.dX), a);
   };
-  const auto narrow = [&](auto n) {
-    constexpr int kN = decltype(n)::value;
-    const size_t smem = shape.G < kLnThreads ? 2 * d * 4 : 0;  // (one group needs no turns)
-    constexpr int kR = kN * kV <= 8 ? 2 : 1;
-    return shape.odd ? go(layernorm_grad_kernel<T, kV, kN, kR, true, false>, kLnThreads, smem)
-                     : go(layernorm_grad_kernel<T, kV, kN, kR, false, false>, kLnThreads, smem);
+  const auto ring = [&](auto e, auto n) {
+    constexpr int kE = decltype(e)::value, kN = decltype(n)::value, kR = kE * kN <= 4 ? 2 : 1;
+    const RingPlan rp = ring_plan(static_cast<int>(d), sizeof(T), shape.G, kR);
+    const int bytes = std::max<int>(rp.stages * 2 * rp.bytes, 2 * static_cast<int>(d) * 4);
+    const cudaError_t err = allow_smem<layernorm_grad_ring_kernel<T, kE, kN, kR>>(kRingMost);
+    return err != cudaSuccess
+        ? err : go(layernorm_grad_ring_kernel<T, kE, kN, kR>, kLnThreads, bytes);
   };
   const auto wide = [&](auto n) {
     constexpr int kN = decltype(n)::value, bytes = 2 * kN * kV * kLnWide * 4;
     cudaError_t e;
     if (shape.odd) {
-      e = allow_smem<layernorm_grad_kernel<T, kV, kN, 1, true, true>>(bytes);
-      return e != cudaSuccess
-          ? e : go(layernorm_grad_kernel<T, kV, kN, 1, true, true>, kLnWide, bytes);
+      e = allow_smem<layernorm_grad_kernel<T, kV, kN, true>>(bytes);
+      return e != cudaSuccess ? e : go(layernorm_grad_kernel<T, kV, kN, true>, kLnWide, bytes);
     }
-    e = allow_smem<layernorm_grad_kernel<T, kV, kN, 1, false, true>>(bytes);
-    return e != cudaSuccess
-        ? e : go(layernorm_grad_kernel<T, kV, kN, 1, false, true>, kLnWide, bytes);
+    e = allow_smem<layernorm_grad_kernel<T, kV, kN, false>>(bytes);
+    return e != cudaSuccess ? e : go(layernorm_grad_kernel<T, kV, kN, false>, kLnWide, bytes);
   };
   cudaError_t err;
-  if (shape.G == kLnWide) {
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, kV> vec{};
+  if (shape.wide) {
     constexpr int kUnit = 8 / kV;  // accesses of eight elements
     if (shape.nv <= 2 * kUnit) err = wide(std::integral_constant<int, 2 * kUnit>{});
     else if (shape.nv <= 3 * kUnit) err = wide(std::integral_constant<int, 3 * kUnit>{});
     else if (shape.nv <= 4 * kUnit) err = wide(std::integral_constant<int, 4 * kUnit>{});
     else err = wide(std::integral_constant<int, 4 * kUnit + 1>{});  // (a shift's)
+  } else if (shape.odd) {
+    if (shape.nv <= 2) err = ring(one, std::integral_constant<int, 2>{});
+    else if (shape.nv <= 4) err = ring(one, std::integral_constant<int, 4>{});
+    else if (shape.nv <= 8) err = ring(one, std::integral_constant<int, 8>{});
+    else err = ring(one, std::integral_constant<int, 16>{});
   } else if (shape.nv <= 1) {
-    err = narrow(std::integral_constant<int, 1>{});
+    err = ring(vec, std::integral_constant<int, 1>{});
   } else if (shape.nv <= 2) {
-    err = narrow(std::integral_constant<int, 2>{});
+    err = ring(vec, std::integral_constant<int, 2>{});
   } else {
-    err = narrow(std::integral_constant<int, 16 / kV>{});
+    err = ring(vec, std::integral_constant<int, 16 / kV>{});
   }
   if (err != cudaSuccess || !sums) return err;
   const int tiles = static_cast<int>((d + 31) / 32);

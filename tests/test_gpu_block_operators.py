@@ -127,6 +127,27 @@ def test_layernorm_grad(d, dtype):
         _near(n, (Ws ** 2).sum(1), 64 * 2.0 ** -24, "n of the weight")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,d", [(3, 333, 5), (1, 1001, 31), (5, 77, 129), (2, 500, 257), (2, 701, 1023),
+                                   (1, 400, 3001), (1, 130, 5003)])
+def test_layernorm_grad_of_many_odd_rows(B, T, d, dtype):
+    """Blocks of rows that start at every element of 16 bytes and end with the tensor; the
+    gradient in the place of dY."""
+    X, dY = _randn((B, T, d), dtype, d, 1.5), _randn((B, T, d), dtype, d + 1)
+    W = (1 + _randn((d,), F32, d + 2, 0.2)).to(dtype)
+    dX, Ws, bs = block.layernorm_grad(_np(dY), _np(X), _np(W), center=False)
+    _, mu, r = block.layernorm(_np(X), center=False)
+    stats = torch.from_numpy(np.stack((mu, r), -1)).float().to(DEV)
+    g = dY.to(DEV)
+    dw, db, n = (torch.empty(k, device=DEV, dtype=t) for k, t in ((d, dtype), (d, dtype), (B, F32)))
+    rnc.dprc_layernorm_grad(g, X.to(DEV), stats, W.to(DEV), center=False, dX=g, dW=dw, db=db, n=n,
+                            norm_of_bias=True)
+    _near(g, dX, NORM[dtype])
+    _near(dw, Ws.sum(0), NORM[dtype])
+    _near(db, bs.sum(0), NORM[dtype])
+    _near(n, (Ws ** 2).sum(1) + (bs ** 2).sum(1), 64 * 2.0 ** -24)
+
+
 def test_layernorm_large_mean_and_empty():
     """A mean of 1000 deviations: the variance is summed of differences."""
     X = _randn((4, 5, 512), F32, 3) + 1000.0
