@@ -43,7 +43,7 @@ __device__ __forceinline__ void load_tile(float* dst, int n, int D, bool vec, Sr
   for (int r = threadIdx.x / kLanes; r < kRows; r += kStep) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     const T* p = r < n ? src(r) : nullptr;
-    if (p != nullptr) {
+    if (p != nullptr && DPRC_IN(n <= kRows && (!vec || reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0))) {
       if (vec) {
         if (c < D) v = load4(p + c);
       } else {

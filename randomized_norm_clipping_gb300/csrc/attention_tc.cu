@@ -9,7 +9,7 @@
 // P and dS never leave the SM: a thread owns a lane of tensor memory (a row, or a key),
 // reads the scores, and writes the weights back as the bf16 first operand of the next
 // product.  One warp copies tiles by TMA into a ring, one thread issues the products,
-// eight warps do the softmax.
+// four warps a tile of rows do the softmax (forward), sixteen the gradient's weights.
 //
 // The rows of a tile are the queries of all G heads that share a head of keys
 // (attention.cuh): 128 / G tokens, brought by one box of G heads by tokens.  So few
@@ -342,6 +342,7 @@ __device__ __forceinline__ Extent warp_extent(bool mine, const RowSees& r, bool 
 __device__ __forceinline__ DocSpan key_tile_docs(const AttnArgs& a, int b, int tile) {
   const int spans = (a.Tk + kDocSpan - 1) / kDocSpan;
   const DocSpan* s = a.spans + static_cast<long long>(b) * spans;
+  if (!DPRC_IN(tile >= 0 && 2 * tile < spans)) return {0, -1, 1, 0};
   DocSpan r = s[2 * tile];
   if (2 * tile + 1 < spans) {
     const DocSpan q = s[2 * tile + 1];
@@ -364,7 +365,7 @@ __device__ __forceinline__ void key_tile_bits(const AttnArgs& a, int b, int t0, 
       ok = s.lo <= hi && lo <= s.hi;
     }
     const uint32_t m = __ballot_sync(0xffffffffu, ok);
-    if (lane == 0) bits[w] = m;
+    if (lane == 0 && DPRC_IN(w < kMaxKeyTiles / 32)) bits[w] = m;
   }
 }
 
@@ -1156,12 +1157,13 @@ cudaError_t launch_few_form(int form, const CUtensorMap& q, const CUtensorMap& k
 // columns (with eight and 64 columns, two warps a scheduler, the chain of a thread's
 // operations was what the kernels waited for: issue slots 35 % used).  Its weights go back
 // into the first half of the columns that it read (a product's steps of 16 take their
-// operand from there, mma_parts), so no other thread's scores are overwritten.  While the weights' gradient is formed, the tensor
-// core forms the next scores; while those are taken to the exponential, the gradients'
-// products and the next dP.
+// operand from there, mma_parts), so no other thread's scores are overwritten.  While the
+// weights' gradient is formed, the tensor core forms the next scores; while those are
+// taken to the exponential, the gradients' products and the next dP.
 // ---------------------------------------------------------------------------
 constexpr int kGradWarps = 16, kGradThreads = 32 * (kGradWarps + 4);
 constexpr int kPart = kTile * 4 / kGradWarps;  // columns of a thread
+static_assert(kPart == 32, "columns of a load");
 
 __device__ __forceinline__ void mma_parts(bool lead, uint32_t acc, uint32_t a_tmem, uint64_t b,
                                            uint32_t idesc, bool accumulate) {
@@ -1170,12 +1172,6 @@ __device__ __forceinline__ void mma_parts(bool lead, uint32_t acc, uint32_t a_tm
   for (int k = 0; k < kTile / 16; ++k)
     umma_bf16_ts(acc, a_tmem + (k / (kPart / 16)) * kPart + (k % (kPart / 16)) * 8, b + ((k * 2048) >> 4), idesc,
                  accumulate || k > 0 ? 1u : 0u);
-}
-
-template <int kN>
-__device__ __forceinline__ void tmem_ld_part(uint32_t taddr, float (&v)[kN]) {
-  if constexpr (kN == 64) tmem_ld_64cols(taddr, v);
-  else tmem_ld_32cols(taddr, v);
 }
 
 // This thread's columns: ds = w (dp - delta), 0 where `bits` says that the key is not
@@ -1468,7 +1464,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         dirty = dirty || s.pad;
       }
       float z[kPart];
-      tmem_ld_part(ts, z);
+      tmem_ld_32cols(ts, z);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sread);
@@ -1638,7 +1634,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
     }
     const uint32_t m = __ballot_sync(0xffffffffu, ok);
-    if (lane == 0) bits[w] = m;
+    if (lane == 0 && DPRC_IN(w < kMaxRowTiles / 32)) bits[w] = m;
   }
   __syncthreads();
 
@@ -1846,7 +1842,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (!ok) break;
       tc_fence_after();
       float z[kPart];
-      tmem_ld_part(ts, z);
+      tmem_ld_32cols(ts, z);
       const bool by_doc =
           a.docs != nullptr && (!one_doc || st.lo != kdoc0 || st.hi != kdoc0);
       const bool masked = last_key >= st.min_lim || by_doc;
