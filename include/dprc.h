@@ -567,7 +567,8 @@ dprc_status dprc_layernorm_grad(const void* dY, const void* X, const float* stat
  * the gradient of the call without it).  Elements behind the pairs are copied.
  *  X and out device, [B][T][H][D] of dtype with the strides x_stride and out_stride
  *  (host, of B, T and H, in elements; a head's elements lie together); any alignment
- *  of the type.  out may be X (with the same strides), else the two do not overlap.
+ *  of the type.  out's rows lie apart (an axis steps over all that lies within it); it
+ *  may be X (with the same strides), else the two do not overlap.
  *  positions device [B][T][axes], int32 (position_bytes 4) or int64 (8); freqs device
  *  double [P], radians; sections host [axes].
  *  B, T >= 0, 1 <= H <= 65535, 1 <= D <= 4096, 1 <= axes <= 8, 2 P <= D.
@@ -602,8 +603,8 @@ dprc_status dprc_rotary(const void* X, const int64_t* x_stride, dprc_dtype dtype
  *  1 <= D <= 128, Tq, Tk <= 2^20, B Hkv <= 65535, Tq H / Hkv <= 2^28, H / Hkv <= 4096,
  *  (Tq H / Hkv + Tk) B Hkv <= 2^34.
  *  bf16 runs on the tensor cores where D, the strides and the addresses are multiples of
- *  8 elements (16 bytes) and H / Hkv <= 128, else on the CUDA cores (the gradient: dO's
- *  too).
+ *  8 elements (16 bytes), H / Hkv <= 128 and cap <= 4096 (a capped score is off by
+ *  2^-22 of the cap there), else on the CUDA cores (the gradient: dO's too).
  *  ws device, dprc_attention_workspace_bytes(a, 0) bytes.
  */
 typedef struct {
@@ -622,8 +623,9 @@ dprc_status dprc_attention(const dprc_attention_args* a, void* out, float* lse, 
 
 /*
  * Gradient of dprc_attention (the same arguments): dQ, dK and dV, each with strides as
- * Q, K and V have them (the tensors' elements do not overlap); any may be NULL and is
- * then not formed, not all.  A head of keys gets the sum over its queries' heads.
+ * Q, K and V have them, but apart (an axis steps over all that lies within it, else
+ * DPRC_ERR_SHAPE; the tensors do not overlap either); any may be NULL and is then not
+ * formed, not all.  A head of keys gets the sum over its queries' heads.
  *  dO and O device [B][Tq][H][D] of dtype with strides like Q's, and lse: the output's
  *  gradient and what the forward call gave.  Every element of the gradients is written; those of
  *  queries that see nothing and keys that are not seen are zero.  dO of a query that

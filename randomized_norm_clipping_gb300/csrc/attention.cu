@@ -43,33 +43,51 @@ __global__ void __launch_bounds__(256) attention_spans_kernel(const int* docs, i
 }
 
 // delta[b][h][t] = sum over the width of dO O: eight threads a row, 16 bytes of
-// both at a time where the width allows.  Bound by bytes: both are read once.
+// both at a time where the width allows, four rows 32 apart, whose loads are all on their
+// way before the first is used.  Bound by bytes: both are read once.
+constexpr int kDeltaRows = 4;
 template <typename T, int kE>
-__global__ void __launch_bounds__(256)
-    attention_delta_kernel(const AttnArgs a, long long rows) {
+__global__ void __launch_bounds__(256) attention_delta_kernel(const AttnArgs a, long long rows) {
   pdl_launch_dependents();
   pdl_wait();
-  const long long r = static_cast<long long>(blockIdx.x) * 32 + (threadIdx.x >> 3);
-  const int t = threadIdx.x & 7;
-  float s = 0.f;
-  const long long bt = r / a.H, b = bt / a.Tq, h = r - bt * a.H, tok = bt - b * a.Tq;
-  if (r < rows) {
-    const T* dO = static_cast<const T*>(a.dO) + b * a.dob + tok * a.dot + h * a.doh;
-    const T* O = static_cast<const T*>(a.O) + b * a.ob + tok * a.ot + h * a.oh;
-    for (int c = t * kE; c < a.D; c += 8 * kE) {
-      Raw<T, kE> x, y;
-      float u[kE], v[kE];
-      x.load(dO + c);
-      y.load(O + c);
-      x.get(u);
-      y.get(v);
+  const long long r0 = static_cast<long long>(blockIdx.x) * 32 * kDeltaRows, b = blockIdx.y;
+  const long long tok0 = r0 / a.H;
+  const int h0 = static_cast<int>(r0 - tok0 * a.H), t = threadIdx.x & 7;
+  const T *dO[kDeltaRows], *O[kDeltaRows];
+  float s[kDeltaRows];
 #pragma unroll
-      for (int e = 0; e < kE; ++e) s = fmaf(u[e], v[e], s);
+  for (int k = 0; k < kDeltaRows; ++k) {
+    const int i = k * 32 + (threadIdx.x >> 3), over = (h0 + i) / a.H;
+    const long long tok = tok0 + over, h = h0 + i - over * a.H;
+    const bool in = r0 + i < rows;  // (else the CTA's first row, which is not written)
+    dO[k] = static_cast<const T*>(a.dO) + b * a.dob + (in ? tok * a.dot + h * a.doh : tok0 * a.dot + h0 * a.doh);
+    O[k] = static_cast<const T*>(a.O) + b * a.ob + (in ? tok * a.ot + h * a.oh : tok0 * a.ot + h0 * a.oh);
+    s[k] = 0.f;
+  }
+  for (int c = t * kE; c < a.D; c += 8 * kE) {
+    Raw<T, kE> x[kDeltaRows], y[kDeltaRows];
+#pragma unroll
+    for (int k = 0; k < kDeltaRows; ++k) {
+      x[k].load(dO[k] + c);
+      y[k].load(O[k] + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kDeltaRows; ++k) {
+      float u[kE], v[kE];
+      x[k].get(u);
+      y[k].get(v);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) s[k] = fmaf(u[e], v[e], s[k]);
     }
   }
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (r < rows && t == 0) a.delta[(b * a.H + h) * a.Tq + tok] = s;
+  for (int k = 0; k < kDeltaRows; ++k) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+    const int i = k * 32 + (threadIdx.x >> 3), over = (h0 + i) / a.H;
+    if (r0 + i < rows && t == 0)
+      a.delta[(b * a.H + h0 + i - over * a.H) * a.Tq + tok0 + over] = s[k];
+  }
 }
 
 // The shares of a row's keys, in order: a warp a row.
@@ -228,8 +246,8 @@ cudaError_t prepare_spans(const AttentionCall& c, char* ws, cudaStream_t s) {
 
 template <typename T>
 cudaError_t delta_rows(const AttnArgs& a, cudaStream_t s) {
-  const long long rows = static_cast<long long>(a.B) * a.Tq * a.H;
-  const dim3 grid(static_cast<unsigned>(cdiv(rows, 32)));
+  const long long rows = static_cast<long long>(a.Tq) * a.H;  // of a sample
+  const dim3 grid(static_cast<unsigned>(cdiv(rows, 32 * kDeltaRows)), a.B);
   const long long all = a.D | a.dob | a.dot | a.doh | a.ob | a.ot | a.oh;
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.dO) | reinterpret_cast<uintptr_t>(a.O);
   if (all % kVec16<T> == 0 && at % 16 == 0)

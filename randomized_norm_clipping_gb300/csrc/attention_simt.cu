@@ -156,7 +156,7 @@ __device__ __forceinline__ float capped(const AttnArgs& a, float z, float* slope
     *slope = 1.f;
     return z;
   }
-  const float t = 1.f - 2.f / (1.f + expf(2.f * z / a.cap));
+  const float t = tanhf(z / a.cap);  // (1 - 2 / (1 + exp) is off by 2^-24 cap: too much of large caps)
   *slope = 1.f - t * t;
   return t * a.cap;
 }

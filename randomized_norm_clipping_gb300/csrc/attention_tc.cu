@@ -21,6 +21,7 @@
 // roundings change from run to run.
 
 #include <algorithm>
+#include <cfloat>
 
 #include "attention.cuh"
 #include "tmem.cuh"
@@ -353,6 +354,36 @@ __device__ __forceinline__ DocSpan key_tile_docs(const AttnArgs& a, int b, int t
   return r;
 }
 
+// What the rows of tokens [tok0, tok1) may see, without a look at each of them: a limit, and
+// the documents of the spans that they stand in.  So the copies start a load's and a
+// barrier's time earlier than with the rows' own.
+struct Reach {
+  int top, lo, hi;
+};
+__device__ __forceinline__ Reach reach_of(const AttnArgs& a, int b, int tok0, int tok1, int keys,
+                                          int first) {
+  Reach r = {tok0 < tok1 ? keys : 0, 0, 0};
+  if (a.causal && tok0 < tok1) {
+    int see = first + tok1;
+    if (a.prefix != nullptr) see = max(see, a.prefix[b]);
+    r.top = max(0, min(see, keys));
+  }
+  if (a.docs != nullptr) {
+    r.lo = 0x7fffffff;
+    r.hi = -1;
+    const int spans = (a.Tk + kDocSpan - 1) / kDocSpan;
+    const int p0 = max(0, first + tok0), p1 = min(a.Tk, first + tok1);  // positions
+    for (int q = p0 / kDocSpan + (threadIdx.x & 31); p0 < p1 && q <= (p1 - 1) / kDocSpan; q += 32) {
+      const DocSpan s = a.spans[static_cast<long long>(b) * spans + q];
+      r.lo = min(r.lo, s.lo);
+      r.hi = max(r.hi, s.hi);
+    }
+    r.lo = __reduce_min_sync(0xffffffffu, r.lo);
+    r.hi = __reduce_max_sync(0xffffffffu, r.hi);
+  }
+  return r;
+}
+
 // Key tiles [t0, t1) that some row of the CTA may see, as bits.
 __device__ __forceinline__ void key_tile_bits(const AttnArgs& a, int b, int t0, int t1, int lo,
                                               int hi, uint32_t* bits, int words) {
@@ -429,7 +460,6 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
   uint64_t* drain = pvfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* ext = reinterpret_cast<int*>(tmem_slot + 2);  // greatest limit, least and greatest document
   uint32_t* bits = reinterpret_cast<uint32_t*>(ring + kStages * Cfg::kSlot + 512);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -453,9 +483,6 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
     mbar_init(drain, 1);
     fence_mbar_init();
     *abort_flag = 0;
-    ext[0] = 0;
-    ext[1] = 0x7fffffff;
-    ext[2] = -1;
     tma_prefetch_desc(&map_q);
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
@@ -478,21 +505,14 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
   const bool mine = warp < Cfg::kSoft && tt < x.nt && tok < a.Tq;
   RowSees see = {0, 0, -1};
   Extent e = {};
-  if (warp < Cfg::kSoft) {
-    if (mine) see = attn_row(a, b, tok, keys, first);
-    e = warp_extent(mine, see, a.docs != nullptr);
-    if (lane == 0) {
-      atomicMax(&ext[0], e.max_lim);
-      atomicMin(&ext[1], e.lo);
-      atomicMax(&ext[2], e.hi);
-    }
-  }
-  __syncthreads();
-  const int top = ext[0];
+  const Reach reach = reach_of(a, b, grp * kTiles * x.nt, min((grp + 1) * kTiles * x.nt, a.Tq), keys, first);
+  const int top = reach.top;
   const int t0 = blockIdx.z * a.per_split, t1 = min(t0 + a.per_split, (top + kTile - 1) / kTile);
   const int words = max(0, (t1 + 31) / 32);
-  key_tile_bits(a, b, t0, t1, ext[1], ext[2], bits, words);
+  key_tile_bits(a, b, t0, t1, reach.lo, reach.hi, bits, words);
+  if (mine) see = attn_row(a, b, tok, keys, first);
   __syncthreads();
+  if (warp < Cfg::kSoft) e = warp_extent(mine, see, a.docs != nullptr);
 
   if (warp >= Cfg::kSoft) {
     regs_less<Cfg::kLess>();
@@ -1278,7 +1298,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   uint64_t* drain = ofull + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* ext = reinterpret_cast<int*>(tmem_slot + 2);
   uint32_t* bits = reinterpret_cast<uint32_t*>(ring + kStages * Cfg::kSlot + 512);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -1299,9 +1318,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     mbar_init(drain, 1);
     fence_mbar_init();
     *abort_flag = 0;
-    ext[0] = 0;
-    ext[1] = 0x7fffffff;
-    ext[2] = -1;
     tma_prefetch_desc(&map_q);
     tma_prefetch_desc(&map_o);
     tma_prefetch_desc(&map_k);
@@ -1324,19 +1340,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   const bool mine = warp < kGradWarps && tt < x.nt && tok < a.Tq;
   RowSees see = {0, 0, -1};
   Extent e = {};
-  if (warp < kGradWarps) {
-    if (mine) see = attn_row(a, b, tok, keys, first);
-    e = warp_extent(mine, see, a.docs != nullptr);
-    if (lane == 0) {
-      atomicMax(&ext[0], e.max_lim);
-      atomicMin(&ext[1], e.lo);
-      atomicMax(&ext[2], e.hi);
-    }
-  }
+  const Reach reach = reach_of(a, b, grp * x.nt, min((grp + 1) * x.nt, a.Tq), keys, first);
+  const int top = reach.top, t1 = (top + kTile - 1) / kTile, words = (t1 + 31) / 32;
+  key_tile_bits(a, b, 0, t1, reach.lo, reach.hi, bits, words);
+  if (mine) see = attn_row(a, b, tok, keys, first);
   __syncthreads();
-  const int top = ext[0], t1 = (top + kTile - 1) / kTile, words = (t1 + 31) / 32;
-  key_tile_bits(a, b, 0, t1, ext[1], ext[2], bits, words);
-  __syncthreads();
+  if (warp < kGradWarps) e = warp_extent(mine, see, a.docs != nullptr);
 
   if (warp >= kGradWarps) {
     if (warp == kGradWarps && lane == 0) {
@@ -2014,7 +2023,9 @@ TcArgs tc_args(const AttnArgs& a, int tiles) {
   x.groups = (x.row_tiles + tiles - 1) / tiles;
   x.steps = (a.D + 15) / 16;
   x.c = a.scale * kLog2e;
-  x.c_cap = a.cap > 0.f ? 2.f * a.scale * kLog2e / a.cap : 0.f;
+  // (finite, so that a product of 0 stays one)
+  x.c_cap = a.cap > 0.f
+      ? std::clamp(2.f * a.scale * kLog2e / a.cap, -FLT_MAX, FLT_MAX) : 0.f;
   x.cap2 = a.cap * kLog2e;
   return x;
 }
@@ -2034,10 +2045,14 @@ bool address_fits(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 ==
 
 }  // namespace
 
+// The tanh by an exponential is good to 2^-22, a score to 2^-22 of the cap: up to this cap the
+// weights are better than their half step in bf16, 2^-9.
+constexpr float kMaxTcCap = 4096.f;
+
 // What the tensor copies take: 16-byte boundaries, and a group's heads in a tile.
 bool attention_tc_takes(const AttentionCall& c) {
   const int64_t G = c.H / c.Hkv;
-  return c.dtype == DPRC_BF16 && c.D % 8 == 0 && G <= kTile && c.Tk > 0 && c.Tq > 0 &&
+  return c.dtype == DPRC_BF16 && c.cap <= kMaxTcCap && c.D % 8 == 0 && G <= kTile && c.Tk > 0 && c.Tq > 0 &&
          c.Tq <= (int64_t(1) << 16) * (kTile / G) && address_fits(c.Q) && address_fits(c.K) &&
          address_fits(c.V) && strides_fit(c.qs, c.B, c.Tq, c.H) &&
          strides_fit(c.ks, c.B, c.Tk, c.Hkv) && strides_fit(c.vs, c.B, c.Tk, c.Hkv) &&

@@ -2,6 +2,8 @@
 // the linear map, normalisation, rotary positions, attention): argument checks,
 // then the launchers.
 
+#include <algorithm>
+
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -71,6 +73,21 @@ bool strides_ok(const int64_t* s) {
   return true;
 }
 
+// Whether rows of D elements at these strides (of B, T and H of them) lie apart, so that each
+// element of a result has one writer: every axis steps over all that lies within.
+bool apart(const int64_t* s, int64_t B, int64_t T, int64_t H, int64_t D) {
+  const int64_t n[3] = {B, T, H};
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return s[a] < s[b]; });
+  __int128 span = D;
+  for (const int k : order) {
+    if (n[k] < 2) continue;
+    if (s[k] < span) return false;
+    span += static_cast<__int128>(n[k] - 1) * s[k];
+  }
+  return true;
+}
+
 // An array of elements of `size` bytes, from an address of its own type's alignment on.
 bool element_aligned(const void* p, size_t size) {
   return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0;
@@ -124,7 +141,8 @@ AttentionCall attention_call(const dprc_attention_args* a) {
   c.Hkv = a->Hkv;
   c.D = a->D;
   c.scale = a->scale;
-  c.cap = a->cap;
+  // (cap tanh(s / cap) is s to a half step while s < 2^-12 cap)
+  c.cap = a->cap < 0x1p60f ? a->cap : 0.f;
   c.causal = a->causal != 0;
   c.slopes = a->slopes;
   c.docs = a->docs;
@@ -399,7 +417,7 @@ dprc_status dprc_rotary(const void* X, const int64_t* x_stride, dprc_dtype dtype
     if (sections[k] < 0 || sections[k] > D) return DPRC_ERR_SHAPE;
     pairs += sections[k];
   }
-  if (2 * pairs > D) return DPRC_ERR_SHAPE;
+  if (2 * pairs > D || !apart(out_stride, B, T, H, D)) return DPRC_ERR_SHAPE;
   if (B * T > 0 && (!X || !out || (pairs > 0 && (!positions || !freqs)))) return DPRC_ERR_NULL;
   const size_t e = size_of(dtype);
   if (!element_aligned(X, e) || !element_aligned(out, e) ||
@@ -466,11 +484,15 @@ dprc_status dprc_attention_grad(const dprc_attention_args* a, const void* dO,
   if ((dQ && !strides_ok(dq_stride)) || (dK && !strides_ok(dk_stride)) ||
       (dV && !strides_ok(dv_stride)))
     return DPRC_ERR_SHAPE;
+  if ((dQ && !apart(dq_stride, a->B, a->Tq, a->H, a->D)) ||
+      (dK && !apart(dk_stride, a->B, a->Tk, a->Hkv, a->D)) ||
+      (dV && !apart(dv_stride, a->B, a->Tk, a->Hkv, a->D)))
+    return DPRC_ERR_SHAPE;
   if (a->Tq > 0 && (!dO || !O || !lse || !do_stride || !o_stride)) return DPRC_ERR_NULL;
   if (a->Tq > 0 && (!strides_ok(do_stride) || !strides_ok(o_stride))) return DPRC_ERR_SHAPE;
   const size_t e = size_of(a->dtype);
-  if (!element_aligned(dO, e) || !element_aligned(O, e) || !element_aligned(lse, 4) || !element_aligned(dQ, e) ||
-      !element_aligned(dK, e) || !element_aligned(dV, e))
+  if (!element_aligned(dO, e) || !element_aligned(O, e) || !element_aligned(lse, 4) ||
+      !element_aligned(dQ, e) || !element_aligned(dK, e) || !element_aligned(dV, e))
     return DPRC_ERR_ALIGN;
   AttentionGradCall g;
   g.f = attention_call(a);

@@ -230,6 +230,23 @@ def test_attention_call_refusals(lib):
     assert g(ctypes.byref(a), A16, s, A16, s, A16, A16, s, None, s, None, s, A16, grad - 1, None) == 5
 
 
+def test_results_whose_rows_overlap_are_refused(lib):
+    a, s = _args(Hkv=4), _strides(1 << 20, 256, 64)  # (B 2, 100 tokens, 4 heads of 64)
+    n = 1 << 40
+    for bad in (_strides(0, 256, 64), _strides(1 << 20, 0, 64), _strides(1 << 20, 256, 0),
+                _strides(1 << 20, 192, 64), _strides(1 << 20, 256, 63), _strides(25599, 256, 64)):
+        for where in range(3):
+            out = [x for k in range(3) for x in ((A16, bad) if k == where else (None, s))]
+            assert lib.dprc_attention_grad(ctypes.byref(a), A16, s, A16, s, A16, *out, A16, n, None) == 2
+        assert lib.dprc_rotary(A16, s, 1, 2, 100, 4, 64, A16, 8, 1, (ctypes.c_int64 * 1)(8), A16, 0, 0,
+                               A16, bad, None) == 2
+    # (an axis of one has any stride: this call gets as far as its workspace)
+    one = _args(B=1, Tq=1, Tk=1, H=1, Hkv=1)
+    z = _strides(0, 0, 0)
+    assert lib.dprc_attention_grad(ctypes.byref(one), A16, z, A16, z, A16, A16, z, A16, z, A16, z, None,
+                                   0, None) == 5
+
+
 def test_layernorm_refusals(lib):
     f, g = lib.dprc_layernorm, lib.dprc_layernorm_grad
     ok = (A16, None, None, 1, 2, 3, 64, 1e-5, 1, A16, None, None)

@@ -433,3 +433,32 @@ def test_attention_grad_against_differences():
             f.append(float((block.attention(*args, **host)[0] * _np(u)).sum()))
         diff = (f[0] - f[1]) / (2 * h)
         assert abs(float((_np(g[i]) * step).sum()) - diff) <= 1e-4 * max(1.0, abs(diff)), i
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cap", [1e-30, 300.0, 4000.0, 1e5, 1e17, 3e38])
+def test_attention_of_any_cap(dtype, cap):
+    """A score is off by at most 2^-22 of a cap up to 4096 (bf16, an exponential's tanh), else
+    by a few half steps of itself; the weights, lse and delta by as much."""
+    off = cap * 2.0 ** -22 if dtype is BF16 and cap <= 4096 else 0.0
+    for Tq, T in ((150, 150), (3, 500)):
+        Q, K, V, dO = (_randn((2, t, h, 64), dtype, i, g) for i, (t, h, g) in
+                       enumerate(((Tq, 4, 3.0), (T, 2, 1.0), (T, 2, 1.0), (Tq, 4, 1.0))))
+        q, k, v, do = (t.to(DEV) for t in (Q, K, V, dO))
+        lse = torch.empty(2, 4, Tq, device=DEV)
+        out = rnc.dprc_attention(q, k, v, cap=cap, lse=lse)
+        ref = block.attention(_np(Q), _np(K), _np(V), cap=cap, dO=_np(dO))
+        _near(out, ref[0], ATT[dtype] + off)
+        assert np.abs(_np(lse) - ref[1]).max() <= 1e-5 * (1 + np.abs(ref[1]).max()) + off
+        dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
+        rnc.dprc_attention_grad(do, q, k, v, out, lse, cap=cap, dQ=dq, dK=dk, dV=dv)
+        # Where t is near 1 (a tiny cap's slope is 0), 1 - t^2 is off by the reciprocal's half
+        # steps: 12 of them.  A row's weights add up to 1 and |dp|, |delta| <= |do| max |v|,
+        # so dS is off by 24 half steps of that at most, and dQ, dK by the sums of it.
+        size = lambda t: np.linalg.norm(_np(t), axis=-1).max()  # noqa: E731
+        lost = 32 * 2.0 ** -24 * 64 ** -0.5 * np.linalg.norm(_np(dO)) * size(V)
+        for name, a, b, terms, by in (("dQ", dq, ref[2], ref[5], size(K)),
+                                      ("dK", dk, ref[3], ref[6], np.linalg.norm(_np(Q))),
+                                      ("dV", dv, ref[4], 0.0, 0.0)):
+            _near(a, b, ATT_GRAD[dtype] + 2 * off, name,
+                  CANCEL[dtype] * np.linalg.norm(terms) + lost * by)
