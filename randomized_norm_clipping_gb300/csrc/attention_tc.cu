@@ -455,9 +455,10 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
   uint64_t* empty = full + kStages;
   uint64_t* qfull = empty + kStages;
   uint64_t* sfull = qfull + 1;   // [kBufs], up to 3
-  uint64_t* pfull = sfull + 3;   // [2]
-  uint64_t* pvfull = pfull + 2;  // [2]
-  uint64_t* drain = pvfull + 2;
+  uint64_t* pfull = sfull + 3;   // [kBufs]
+  uint64_t* pvfull = pfull + 3;  // [2]: a product of values, where scores run ahead of it
+  uint64_t* ofull = pvfull + 2;  // [2]: the last one
+  uint64_t* drain = ofull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* bits = reinterpret_cast<uint32_t*>(ring + kStages * Cfg::kSlot + 512);
@@ -475,10 +476,13 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
       mbar_init(&empty[s], 1);
     }
     mbar_init(qfull, 1);
-    for (int w = 0; w < 3; ++w) mbar_init(&sfull[w], 1);
+    for (int u = 0; u < 3; ++u) {
+      mbar_init(&sfull[u], 1);
+      mbar_init(&pfull[u], active);
+    }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&pfull[w], active);
       mbar_init(&pvfull[w], 1);
+      mbar_init(&ofull[w], 1);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -598,13 +602,16 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
           const int t = i / kTiles + u / kTiles;
           if (rows == 0)
             ok = ok && wait_all<false>(&full[vpos.s], vpos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
-          ok = ok && wait_all<false>(&pfull[rows], t & 1, DPRC_DEVERR_ACCUM, abort_flag);
+          // (a barrier a buffer: with one a group, a group whose next scores are there could
+          // end two tiles while their values are waited for, and the wait would miss the first)
+          ok = ok && wait_all<false>(&pfull[buf], ((i + u) / kBufs) & 1, DPRC_DEVERR_ACCUM, abort_flag);
           if (!ok) break;
           tc_fence_after();
           mma_rows(lead, tmem + Cfg::kO + rows * Cfg::kWide, tmem + buf * 128,
                    dv + ((vpos.s * Cfg::kSlot) >> 4), id_o, t > 0);
           // (where a group's next scores are formed behind its product, they tell of it)
-          if (kBufs > kTiles || i + u + kTiles >= total) commit(lead, &pvfull[rows]);
+          if (kBufs > kTiles) commit(lead, &pvfull[rows]);
+          if (i + u + kTiles >= total) commit(lead, &ofull[rows]);
           if (rows == kTiles - 1) {
             commit(lead, &empty[vpos.s]);
             vpos.next(kStages);
@@ -637,6 +644,7 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
         if (!ok) break;
         tc_fence_after();
         const uint32_t ts = tmem + lanes + buf * 128;
+        uint64_t* const taken = &pfull[buf];
         buf += kTiles;
         if (buf >= Cfg::kBufs) {
           buf -= Cfg::kBufs;
@@ -674,6 +682,8 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
           if (grow) m = mt;
           l *= f;
           if (n > 0) {
+            // (these scores were formed behind the product before the last, so that the
+            // barrier stands at the last or behind it; at the end it need not)
             if constexpr (Cfg::kBufs > kTiles) {
               ok = wait_warp<kBlocks == 2>(&pvfull[w], (n - 1) & 1, DPRC_DEVERR_ACCUM, abort_flag);
               if (!ok) break;
@@ -727,10 +737,10 @@ __global__ void __launch_bounds__(FwdCfg<kBlocks, kTiles>::kThreads, kTiles == 1
         vpos.next(kStages);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[w]);
+        if (lane == 0) mbar_arrive(taken);
       }
       if (n > 0 && ok)
-        ok = wait_warp<kBlocks == 2>(&pvfull[w], Cfg::kBufs > kTiles ? (n - 1) & 1 : 0, DPRC_DEVERR_ACCUM, abort_flag);
+        ok = wait_warp<kBlocks == 2>(&ofull[w], 0, DPRC_DEVERR_ACCUM, abort_flag);
       tc_fence_after();
       if (ok) {
         const bool parts = a.splits > 1;

@@ -462,3 +462,22 @@ def test_attention_of_any_cap(dtype, cap):
                                       ("dV", dv, ref[4], 0.0, 0.0)):
             _near(a, b, ATT_GRAD[dtype] + 2 * off, name,
                   CANCEL[dtype] * np.linalg.norm(terms) + lost * by)
+
+
+@pytest.mark.parametrize("H,Hkv,D", [(32, 8, 64), (8, 2, 128)])
+@pytest.mark.parametrize("mask", ["documents", "causal", "full"])
+def test_attention_whose_values_come_late(mask, H, Hkv, D):
+    """Many CTAs at a time, whose groups of rows get ahead of the copies of the values: every wait
+    ends (the fixture reads the error word), and a sample's head is right."""
+    B, T = 4, 4096
+    m = _mask(mask, B, T, T)
+    rows = _randn((B, T, H + 2 * Hkv, D), BF16, 1)
+    dev = rows.to(DEV)
+    on = {n: x.to(DEV) if isinstance(x, torch.Tensor) else x for n, x in m.items()}
+    outs = [rnc.dprc_attention(dev[:, :, :H], dev[:, :, H:H + Hkv], dev[:, :, H + Hkv:], **on)
+            for _ in range(3)]
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    one = {n: _np(x[B - 1:]) if isinstance(x, torch.Tensor) else x for n, x in m.items()}
+    ref = block.attention(_np(rows[B - 1:, :, H - 1:H]), _np(rows[B - 1:, :, H + Hkv - 1:H + Hkv]),
+                          _np(rows[B - 1:, :, H + 2 * Hkv - 1:]), **one)[0]
+    _near(outs[0][B - 1:, :, H - 1:], ref, ATT[BF16])
