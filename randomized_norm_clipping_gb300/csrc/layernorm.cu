@@ -8,8 +8,8 @@
 //
 // Bound by bytes: each pass reads its tensors once; a row's values stay in the
 // registers of the threads that share it, and the sums over rows in those of the
-// threads that own a column.  Measured, bf16: forward 16384 x 2048 26 us (0.75 of the copy
-// rate: 134 MB, of which L2 keeps some), x 2049 94 (accesses of rows at any element of
+// threads that own a column.  Measured, bf16: forward 16384 x 2048 29 us (0.68 of the copy
+// rate), x 2049 94 (accesses of rows at any element of
 // theirs); gradient with norms and weights 61 (201 MB in 30 us at the copy rate; the join of
 // the chunks and the norms' sum are 10 of it), x 2049 143; 2048 x 16384 96, x 16383 166.
 //

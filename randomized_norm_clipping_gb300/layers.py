@@ -5,7 +5,8 @@
 run on libdprc (dprc_embed_*, dprc_linear*, dprc_dropout, dprc_layernorm*,
 dprc_rotary, dprc_attention*) in both directions, and `RandomizedClippingStep` takes
 their parameters: the embedding, the biases and the normalisations by their exact
-per-sample norms, the linear weights by the estimates.  Device tensors of float32 or bfloat16 only; the library raises on
+per-sample norms, the linear weights by the estimates.  Device tensors of float32 or
+bfloat16 only; the library raises on
 anything else.  Gradients can be taken once; a gradient of a gradient raises.
 
 Dropout masks come from the library's Philox stream under (seed, step): `seed`

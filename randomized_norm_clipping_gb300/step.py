@@ -36,7 +36,8 @@ A layer that runs twice and an input that mixes samples are refused, since a
 sample's norm would not be that of its gradient.  The per-sample losses must not
 couple samples.  The clipped gradient of an embedding or a normalisation is formed from the
 recorded output gradients and the clip factors (dprc_embed_grad, dprc_layernorm_grad), so
-the second backward stops at the linear parameters.  Projections are drawn fresh per (layer, step) from a seeded
+the second backward stops at the linear parameters.  Projections are drawn fresh per
+(layer, step) from a seeded
 generator (a reading of the pages, which do not say how often P is redrawn):
 P ~ N(0, 1/k) for Hutchinson, S and P ~ N(0, 1) for Hutch++.  Dividing the
 noisy sum by the batch size is left to the optimiser.
