@@ -1773,8 +1773,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       // what the rows see, their statistics and where they stand
       Bits it(bits, words);
       int n = 0;
-      // Rows that are none stand as zeros, and their weights are of no account, unless
-      // the tile has keys that nobody sees: those may be anything, and NaN times 0 is NaN.
+      // Rows that are none stand as zeros, and their weights are of no account while they are
+      // finite (so no bias: exp of a rising one is not, and inf times 0 is NaN), unless
+      // the tile has keys that nobody sees: those may be anything.
       int all = keys;
       if (a.causal) {
         all = min(keys, first + a.Tq);
@@ -1817,7 +1818,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int r = q * 32 + lane;
-          if (tt[q] < x.nt && i * x.nt + tt[q] < a.Tq) {
+          const bool is = tt[q] < x.nt && i * x.nt + tt[q] < a.Tq;
+          if (is) {
             if (see[q].doc >= 0) {
               lo = min(lo, see[q].doc);
               hi = max(hi, see[q].doc);
@@ -1827,7 +1829,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           min_lim = min(min_lim, see[q].lim);
           st.off[r] = lse[q] == -INFINITY ? 0.f : -lse[q] * kLog2e;
           st.delta[r] = del[q];
-          st.slope2[r] = slope[q];
+          st.slope2[r] = is ? slope[q] : 0.f;
           st.pos[r] = static_cast<float>(see[q].pos - j0);
           st.lim[r] = see[q].lim;
           st.doc[r] = see[q].doc;

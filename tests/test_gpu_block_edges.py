@@ -1,0 +1,67 @@
+"""Normalisation and attention at the borders of their ranges, against the float64 oracle, with the
+tolerances of test_gpu_block_operators.py.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import randomized_norm_clipping_gb300 as rnc
+from oracle import block
+from randomized_norm_clipping_gb300 import layers as lay
+from test_gpu_block_operators import ATT, ATT_GRAD, CANCEL, NORM, _mask, _near, _np, _randn
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    torch.cuda.synchronize()
+    assert rnc.dprc_device_error(reset=True) == 0
+
+
+def _check(dtype, Q, K, V, dO, kw, off=0.0, grad=True, dev=None):
+    """Forward and gradient of host tensors (dev: the same on the device, if strided) against the
+    oracle.  off: what the scores' size adds to the relative error of a weight, and
+    so to the lse, to delta (of its terms) and, twice, to a gradient."""
+    on = {n: x.to(DEV) if isinstance(x, torch.Tensor) else x for n, x in kw.items()}
+    host = {n: _np(x) if isinstance(x, torch.Tensor) else x for n, x in kw.items()}
+    q, k, v = (t.to(DEV) for t in (Q, K, V)) if dev is None else dev
+    do = dO.to(DEV)
+    lse = torch.empty(Q.shape[0], Q.shape[2], Q.shape[1], device=DEV)
+    out = rnc.dprc_attention(q, k, v, lse=lse, **on)
+    ref = block.attention(_np(Q), _np(K), _np(V), dO=_np(dO), **host)
+    _near(out, ref[0], ATT[dtype] + off, "out")
+    got, want = _np(lse), ref[1]
+    none = np.isinf(want)
+    assert (got[none] == -np.inf).all()
+    assert np.abs(got[~none] - want[~none]).max(initial=0.0) <= \
+        1e-5 * (1 + np.abs(want[~none]).max(initial=0.0)) + off
+    if not grad:
+        return
+    dq, dk, dv = (torch.full(t.shape, 7.0, dtype=dtype, device=DEV) for t in (Q, K, V))
+    rnc.dprc_attention_grad(do, q, k, v, out, lse, dQ=dq, dK=dk, dV=dv, **on)
+    for name, a, b, terms in (("dQ", dq, ref[2], ref[5]), ("dK", dk, ref[3], ref[6]),
+                              ("dV", dv, ref[4], 0.0)):
+        _near(a, b, ATT_GRAD[dtype] + 2 * off, name, (CANCEL[dtype] + off) * np.linalg.norm(terms))
+
+
+def _heads(dtype, B, Tq, Tk, H, Hkv, D, seed=0):
+    return (_randn((B, Tq, H, D), dtype, seed + 1), _randn((B, Tk, Hkv, D), dtype, seed + 2),
+            _randn((B, Tk, Hkv, D), dtype, seed + 3), _randn((B, Tq, H, D), dtype, seed + 4))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("mask", ["causal", "full", "documents"])
+@pytest.mark.parametrize("cap", [0.0, 5.0])
+@pytest.mark.parametrize("T,H,Hkv,D", [(300, 4, 2, 64), (130, 6, 2, 128), (200, 1, 1, 64)])
+def test_attention_of_rising_biases(dtype, mask, cap, T, H, Hkv, D):
+    """Slopes below zero: scores rise with the distance, also beside a last tile of rows that is not
+    full.  A score of size s is rounded some eight times (the bias, the lse and its units)."""
+    slopes = -0.6 * torch.ones(H)
+    slopes[H // 2:] = -1.25
+    kw = dict(_mask(mask, 1, T, T), slopes=slopes, cap=cap)
+    _check(dtype, *_heads(dtype, 1, T, T, H, Hkv, D), kw, off=8 * 2.0 ** -24 * 1.25 * T)
