@@ -512,6 +512,8 @@ __global__ void __launch_bounds__(kThreads) attention_dkv_simt_kernel(const Attn
         r = attn_row(a, b, t, keys, first);
         const long long at = (static_cast<long long>(b) * a.H + h) * a.Tq + t;
         lse = a.lse_in[at];
+        // (a document behind its sample's length: the position sees keys, the query none)
+        if (lse == -INFINITY) r.lim = 0;
         del = a.delta[at];
         if (a.slopes != nullptr) slope = a.slopes[h];
       }

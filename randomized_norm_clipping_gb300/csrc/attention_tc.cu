@@ -1820,6 +1820,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           const int r = q * 32 + lane;
           const bool is = tt[q] < x.nt && i * x.nt + tt[q] < a.Tq;
           if (is) {
+            // (a document behind its sample's length: the position sees keys, the query none)
+            if (lse[q] == -INFINITY) see[q].lim = 0;
             if (see[q].doc >= 0) {
               lo = min(lo, see[q].doc);
               hi = max(hi, see[q].doc);

@@ -65,3 +65,20 @@ def test_attention_of_rising_biases(dtype, mask, cap, T, H, Hkv, D):
     slopes[H // 2:] = -1.25
     kw = dict(_mask(mask, 1, T, T), slopes=slopes, cap=cap)
     _check(dtype, *_heads(dtype, 1, T, T, H, Hkv, D), kw, off=8 * 2.0 ** -24 * 1.25 * T)
+
+
+@pytest.mark.parametrize("dtype,D", [(F32, 64), (BF16, 64), (BF16, 128), (BF16, 33)])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_of_documents_behind_the_length(dtype, D, causal, bad):
+    """A document that lies behind its sample's length as a whole: its queries see nothing, although
+    their position does, and may hold anything, as may their output's gradient."""
+    B, T, H, Hkv = 2, 300, 4, 2
+    lengths = torch.tensor([130, 290], dtype=torch.int32)
+    docs = torch.zeros(B, T, dtype=torch.int32)
+    docs[0, 150:], docs[1, 295:] = 1, 3
+    Q, K, V, dO = _heads(dtype, B, T, T, H, Hkv, D)
+    gone = torch.arange(T)[None] >= lengths[:, None]
+    K[gone], V[gone] = bad, bad
+    Q[docs > 0], dO[docs > 0] = bad, bad
+    _check(dtype, Q, K, V, dO, dict(causal=causal, docs=docs, lengths=lengths))
