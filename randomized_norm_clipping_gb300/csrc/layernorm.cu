@@ -320,8 +320,9 @@ __global__ void __launch_bounds__(kLnWide)
     fetch(r + stride);  // the next row is on its way while this one is summed
     if (dx != nullptr) row_sum<2>(s, G, buf, turn);
     // dx = r g + (x - mu) (-r^3 mean(g (x - mu))) - r mean(g)
+    // (r by r: r^3 leaves fp32's range where a deviation is above 10^13 or below 10^-12)
     const float rs = sc.y, f = a.c != nullptr ? a.c[(base + r) / a.T] : 1.f;
-    const float along = -rs * rs * rs * (s[1] * inv);
+    const float along = -rs * (rs * (rs * (s[1] * inv)));
     const float rest = a.center ? -rs * (s[0] * inv) : 0.f;
     const F2 rs2 = f2(rs, rs), along2 = f2(along, along), rest2 = f2(rest, rest);
     const F2 fr2 = f2(f * rs, f * rs), f22 = f2(f, f);
@@ -545,11 +546,12 @@ __global__ void __launch_bounds__(kLnThreads, 2)
     for (int j = 0; j < kRows; ++j) {
       if (j * groups >= have) continue;
       // dx = r g + (x - mu) (-r^3 mean(g (x - mu))) - r mean(g)
+      // (r by r: r^3 leaves fp32's range where a deviation is above 10^13 or below 10^-12)
       float f = 1.f;
       if (a.c != nullptr)
         f = a.c[(base + r0 + static_cast<long long>(k) * plan.rows + j * groups + grp) / a.T];
       const float rs = st[j].y;
-      const float along = -rs * rs * rs * (sum[2 * j + 1] * inv);
+      const float along = -rs * (rs * (rs * (sum[2 * j + 1] * inv)));
       const float rest = a.center ? -rs * (sum[2 * j] * inv) : 0.f;
       const F2 rs2 = f2(rs, rs), along2 = f2(along, along), rest2 = f2(rest, rest);
       const F2 fr2 = f2(f * rs, f * rs), f22 = f2(f, f);

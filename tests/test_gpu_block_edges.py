@@ -82,3 +82,36 @@ def test_rows_of_documents_behind_the_length(dtype, D, causal, bad):
     K[gone], V[gone] = bad, bad
     Q[docs > 0], dO[docs > 0] = bad, bad
     _check(dtype, Q, K, V, dO, dict(causal=causal, docs=docs, lengths=lengths))
+
+
+def _terms(dY, X, W, mu, r):
+    """The sizes of the terms of which dX is the sum."""
+    g = np.abs(_np(dY) * _np(W))
+    xh = np.abs((_np(X) - mu[..., None]) * r[..., None])
+    return (g + g.mean(-1, keepdims=True) + xh * (g * xh).mean(-1, keepdims=True)) * r[..., None]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [64, 321, 2048, 4104, 5003])
+@pytest.mark.parametrize("size,eps", [(1e17, 1e-5), (1e15, 1e-5), (1e13, 1e-5), (1e-2, 1e-5), (1.0, 0.5),
+                                      (1e-13, 0.0)])
+def test_normalisation_of_any_size(size, eps, d, dtype):
+    """Rows whose deviation's square, or its reciprocal's, is far from 1; sums of squares stay below
+    2^127 (5003 1e34)."""
+    for center in (True, False):
+        X, dY = _randn((2, 9, d), F32, d).mul(size).to(dtype), _randn((2, 9, d), dtype, d + 1)
+        W = (1 + _randn((d,), F32, d + 2, 0.2)).to(dtype)
+        y, mu, r = block.layernorm(_np(X), _np(W), None, eps, center)
+        x, w, stats = X.to(DEV), W.to(DEV), torch.empty(2, 9, 2, device=DEV)
+        _near(rnc.dprc_layernorm(x, w, eps=eps, center=center, stats=stats), y, NORM[dtype], "y")
+        _near(stats[..., 1], r, 64 * 2.0 ** -24, "r")
+        dX, Ws, bs = block.layernorm_grad(_np(dY), _np(X), _np(W), eps, center)
+        dx, dw, db, n = (torch.empty(s, device=DEV, dtype=t) for s, t in
+                         ((X.shape, dtype), ((d,), dtype), ((d,), dtype), ((2,), F32)))
+        rnc.dprc_layernorm_grad(dY.to(DEV), x, stats, w, center=center, dX=dx, dW=dw, db=db, n=n)
+        # (relative to 1 / size, so that no square of the test's own norms leaves the range)
+        terms = np.linalg.norm(_terms(dY, X, W, mu, r) * size)
+        _near(_np(dx) * size, dX * size, NORM[dtype], "dX", 8 * 2.0 ** -24 * terms)
+        _near(dw, Ws.sum(0), NORM[dtype], "dW")
+        _near(db, bs.sum(0), NORM[dtype], "db")
+        _near(n, (Ws ** 2).sum(1), 64 * 2.0 ** -24, "n")
