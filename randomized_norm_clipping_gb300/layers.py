@@ -343,6 +343,15 @@ def _plain(mask):
     return mask
 
 
+_MASKS = ("slopes", "docs", "prefix", "lengths", "first")
+
+
+def _saved(args):
+    """The masks among the arguments, which the graph saves (one that changes before the backward
+    pass then raises there), and the others."""
+    return [args.get(n) for n in _MASKS], {n: v for n, v in args.items() if n not in _MASKS}
+
+
 class _Attend(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, args, keep):
@@ -352,19 +361,19 @@ class _Attend(torch.autograd.Function):
             lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
                               device=q.device)
         out = rnc.dprc_attention(q, k, v, lse=lse, **args)
-        ctx.save_for_backward(q, k, v, out, lse)
-        ctx.args = args
+        masks, ctx.args = _saved(args)
+        ctx.save_for_backward(q, k, v, out, lse, *masks)
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
-        q, k, v, out, lse = ctx.saved_tensors
+        q, k, v, out, lse, *masks = ctx.saved_tensors
         d = [torch.empty(t.shape, dtype=t.dtype, device=t.device) if need else None
              for t, need in zip((q, k, v), ctx.needs_input_grad)]
         if any(t is not None for t in d):
             rnc.dprc_attention_grad(_heads(grad), q, k, v, out, lse, dQ=d[0], dK=d[1], dV=d[2],
-                                    **ctx.args)
+                                    **dict(zip(_MASKS, masks)), **ctx.args)
         return *d, None, None
 
 
@@ -391,20 +400,22 @@ class _SelfAttend(torch.autograd.Function):
         q, k = qk[:, :, :H], qk[:, :, H:]
         lse = torch.empty((B, H, T), dtype=torch.float32, device=rows.device) if keep else None
         out = rnc.dprc_attention(q, k, v, lse=lse, **args)
-        ctx.save_for_backward(q, k, v, out, lse, positions, freqs)
-        ctx.heads, ctx.turn, ctx.args = heads, turn, args
+        masks, ctx.args = _saved(args)
+        ctx.save_for_backward(q, k, v, out, lse, positions, freqs, *masks)
+        ctx.heads, ctx.turn = heads, turn
         return out.view(B, T, H * D)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
-        q, k, v, out, lse, positions, freqs = ctx.saved_tensors
+        q, k, v, out, lse, positions, freqs, *masks = ctx.saved_tensors
         H, Hkv, D = ctx.heads
         B, T = q.shape[:2]
         d = torch.empty((B, T, H + 2 * Hkv, D), dtype=q.dtype, device=q.device)
         dqk = d[:, :, :H + Hkv]
         rnc.dprc_attention_grad(_dense(grad).view(B, T, H, D), q, k, v, out, lse, dQ=d[:, :, :H],
-                                dK=dqk[:, :, H:], dV=d[:, :, H + Hkv:], **ctx.args)
+                                dK=dqk[:, :, H:], dV=d[:, :, H + Hkv:],
+                                **dict(zip(_MASKS, masks)), **ctx.args)
         if freqs is not None:
             rnc.dprc_rotary(dqk, positions, freqs, inverse=True, out=dqk, **ctx.turn)
         return d.view(B, T, -1), None, None, None, None, None, None
