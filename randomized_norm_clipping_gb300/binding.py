@@ -829,7 +829,8 @@ def dprc_layernorm_grad(dY, X, stats, weight=None, center=True, dX=None, dW=None
                         norm_of_bias=False, accumulate=False, c=None, ws=None, stream=None):
     """Gradient of dprc_layernorm into those of dX [..., d], dW [d], db [d] that are given, and
     into n [B] the squared norms of each sample's dW (and db with norm_of_bias); c [B]:
-    factors of the samples in dW and db.  X is [B, ..., d]; stats are the forward call's."""
+    factors of the samples in dW and db.  X is [B, ..., d] (without n and c any rows of d);
+    stats are the forward call's."""
     _need_cuda(dY, X, stats, dX, ws)
     dt, dev, shape = dY.dtype, dY.device, dY.shape
     code = _dtype_code(dY)
@@ -844,6 +845,8 @@ def dprc_layernorm_grad(dY, X, stats, weight=None, center=True, dX=None, dW=None
     norms = _vector("n", n, torch.float32, B, dev)
     factors = _vector("c", c, torch.float32, B, dev)
     _beside("ws", ws, dY)
+    if n is None and c is None:
+        B, T = 1, B * T  # (rows, whose first axis may be longer than a batch)
     st = _stream(dY, stream)
     if ws is None:
         size = lib().dprc_layernorm_workspace_bytes(B, T, d, 0 if n is None else 1)

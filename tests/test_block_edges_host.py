@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import block_library
+from randomized_norm_clipping_gb300 import binding
 from randomized_norm_clipping_gb300 import layers as lay
 
 
@@ -45,3 +46,62 @@ def test_a_mask_that_changes_before_the_backward_pass_raises(host, name, module)
         y.backward()
     (after,) = torch.autograd.grad((call() * u).sum(), rows)
     assert not torch.equal(before, after)  # (the change is one that the gradient shows)
+
+
+class Fake:
+    """What a call looks at of a device tensor."""
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.float32):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device("cuda", 0)
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def stride(self):
+        return torch.empty(self.shape, device="meta").stride()
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 0x10000
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The names and arguments of the library's calls, which do nothing."""
+    made = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: made.append((name, a)) or (64 if name.endswith("_bytes") else 0)
+
+    monkeypatch.setattr(binding, "lib", Lib)
+    return made
+
+
+def _sizes(calls):
+    """(B, T, d) of the normalisation's gradient and of its workspace, as they were called."""
+    at = dict(dprc_layernorm_workspace_bytes=0, dprc_layernorm_grad=5)
+    return [a[at[name]:at[name] + 3] for name, a in calls]
+
+
+def test_rows_are_samples_only_where_samples_count(calls, monkeypatch):
+    monkeypatch.setattr(binding, "_scratch", lambda *a: Fake(64, dtype=torch.uint8))
+    f = lambda *shape, **kw: binding.dprc_layernorm_grad(  # noqa: E731
+        Fake(*shape), Fake(*shape), Fake(*shape[:-1], 2), stream=0, **kw)
+    f(70000, 8, dX=Fake(70000, 8), dW=Fake(8))
+    f(70000, 3, 8, dW=Fake(8))
+    assert _sizes(calls) == [(1, 70000, 8)] * 2 + [(1, 210000, 8)] * 2
+    del calls[:]
+    f(7, 3, 8, dW=Fake(8), c=Fake(7))
+    f(7, 3, 8, n=Fake(7))
+    f(8, dX=Fake(8))
+    assert _sizes(calls) == [(7, 3, 8)] * 4 + [(1, 1, 8)] * 2

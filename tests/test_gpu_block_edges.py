@@ -115,3 +115,18 @@ def test_normalisation_of_any_size(size, eps, d, dtype):
         _near(dw, Ws.sum(0), NORM[dtype], "dW")
         _near(db, bs.sum(0), NORM[dtype], "db")
         _near(n, (Ws ** 2).sum(1), 64 * 2.0 ** -24, "n")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_normalisation_of_rows_without_an_axis_of_samples(dtype):
+    """More rows in the first axis than there may be samples."""
+    N, d = 70001, 24
+    X, u = _randn((N, d), dtype, 1), _randn((N, d), dtype, 2)
+    m = lay.LayerNorm(d, device=DEV, dtype=dtype)
+    x = X.to(DEV).requires_grad_()
+    (m(x) * u.to(DEV)).sum().backward()
+    dX, Ws, bs = block.layernorm_grad(_np(u)[None], _np(X)[None])
+    # (dX: a sum of three terms of the size of u, r being near 1)
+    _near(x.grad, dX[0], NORM[dtype], "dX", 8 * 2.0 ** -24 * np.linalg.norm(_np(u)) * 3)
+    _near(m.weight.grad, Ws[0], NORM[dtype], "dW")
+    _near(m.bias.grad, bs[0], NORM[dtype], "db")
