@@ -845,6 +845,12 @@ def dprc_layernorm_grad(dY, X, stats, weight=None, center=True, dX=None, dW=None
     norms = _vector("n", n, torch.float32, B, dev)
     factors = _vector("c", c, torch.float32, B, dev)
     _beside("ws", ws, dY)
+    if T == 0 and d > 0:
+        asked = not (dX is None and n is None)
+        if B == 0:  # no samples have no norms and no factors
+            n = c = norms = factors = None
+        if asked and dW is None and db is None and n is None:
+            return
     if n is None and c is None:
         B, T = 1, B * T  # (rows, whose first axis may be longer than a batch)
     st = _stream(dY, stream)
@@ -867,7 +873,7 @@ def _head_strides(name, t):
     s = t.stride()
     if len(s) != 4:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, four axes [B][T][H][D] are needed")
-    if s[3] != 1 and t.shape[3] > 1:
+    if s[3] != 1 and t.shape[3] > 1 and t.numel() > 0:
         raise ValueError(f"{name}: a head's elements must lie together (stride {s[3]})")
     return s[:3]
 
@@ -963,6 +969,8 @@ def dprc_attention(Q, K, V, scale=None, causal=True, cap=0.0, slopes=None, docs=
     if lse is not None:
         _need_cuda(lse)
         _same("lse", lse, torch.float32, (shape[0], shape[2], shape[1]), Q.device)
+    if shape[0] == 0:
+        return out
     ws = _attention_ws(a, 0, Q, ws, st, stream)
     _check("dprc_attention",
            lib().dprc_attention(a, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), st))
@@ -986,6 +994,9 @@ def dprc_attention_grad(dO, Q, K, V, O, lse, scale=None, causal=True, cap=0.0, s
             continue
         strides.append(_I3.pack(*_head_strides(name, t)))
         _same(name, t, dt, like, dev)
+    given = [t for t in (dQ, dK, dV) if t is not None]
+    if given and all(t.numel() == 0 for t in given):
+        return
     st = _stream(Q, stream)
     ws = _attention_ws(a, 1, Q, ws, st, stream)
     _check("dprc_attention_grad",

@@ -418,7 +418,7 @@ class _SelfAttend(torch.autograd.Function):
                                 **dict(zip(_MASKS, masks)), **ctx.args)
         if freqs is not None:
             rnc.dprc_rotary(dqk, positions, freqs, inverse=True, out=dqk, **ctx.turn)
-        return d.view(B, T, -1), None, None, None, None, None, None
+        return d.view(B, T, (H + 2 * Hkv) * D), None, None, None, None, None, None
 
 
 class Attention(torch.nn.Module):

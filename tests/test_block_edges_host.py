@@ -105,3 +105,27 @@ def test_rows_are_samples_only_where_samples_count(calls, monkeypatch):
     f(7, 3, 8, n=Fake(7))
     f(8, dX=Fake(8))
     assert _sizes(calls) == [(7, 3, 8)] * 4 + [(1, 1, 8)] * 2
+
+
+def test_batches_without_samples(calls, monkeypatch):
+    """A gradient of no samples is zeros (a call of no tokens), norms of none are nothing."""
+    monkeypatch.setattr(binding, "_scratch", lambda *a: Fake(64, dtype=torch.uint8))
+    x, st = Fake(0, 5, 8), Fake(0, 5, 2)
+    binding.dprc_layernorm_grad(x, x, st, dX=x, dW=Fake(8), n=Fake(0), c=Fake(0), stream=0)
+    assert _sizes(calls) == [(1, 0, 8)] * 2 and calls[1][1][12] is None and calls[1][1][15] is None
+    del calls[:]
+    binding.dprc_layernorm_grad(x, x, st, n=Fake(0), stream=0)
+    q, kv, lse = Fake(0, 5, 4, 8), Fake(0, 9, 2, 8), Fake(0, 4, 5)
+    assert binding.dprc_attention(q, kv, kv, out=q, lse=lse, stream=0) is q
+    binding.dprc_attention_grad(q, q, kv, kv, q, lse, dQ=q, dK=kv, dV=kv, stream=0)
+    binding.dprc_layernorm_grad(Fake(2, 0, 8), Fake(2, 0, 8), Fake(2, 0, 2), dX=Fake(2, 0, 8), stream=0)
+    binding.dprc_attention_grad(Fake(2, 0, 4, 8), Fake(2, 0, 4, 8), Fake(2, 9, 2, 8), Fake(2, 9, 2, 8),
+                                Fake(2, 0, 4, 8), Fake(2, 4, 0), dQ=Fake(2, 0, 4, 8), stream=0)
+    assert calls == []
+    # a call that asks for nothing is the library's to refuse, as any such call
+    binding.dprc_attention_grad(q, q, kv, kv, q, lse, stream=0)
+    binding.dprc_layernorm_grad(x, x, st, stream=0)
+    assert [name for name, _ in calls if not name.endswith("_bytes")] == [
+        "dprc_attention_grad", "dprc_layernorm_grad"]
+    with pytest.raises(ValueError):  # (arguments are looked at all the same)
+        binding.dprc_attention(q, kv, Fake(0, 8, 2, 8), out=q, stream=0)

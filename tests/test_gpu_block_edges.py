@@ -130,3 +130,26 @@ def test_normalisation_of_rows_without_an_axis_of_samples(dtype):
     _near(x.grad, dX[0], NORM[dtype], "dX", 8 * 2.0 ** -24 * np.linalg.norm(_np(u)) * 3)
     _near(m.weight.grad, Ws[0], NORM[dtype], "dW")
     _near(m.bias.grad, bs[0], NORM[dtype], "db")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T", [(0, 0), (0, 5), (2, 0)])
+def test_modules_on_batches_of_nothing(dtype, B, T):
+    norm = lay.LayerNorm(48, device=DEV, dtype=dtype)
+    att = lay.Attention(4, 2, 6, freqs=lay.rotary_freqs(3)).to(DEV)
+    x = torch.zeros(B, T, 48, device=DEV, dtype=dtype, requires_grad=True)
+    y = att(norm(x))
+    assert y.shape == (B, T, 24)
+    y.sum().backward()
+    assert x.grad.shape == x.shape
+    for p in (norm.weight, norm.bias):
+        assert p.grad.shape == p.shape and (p.grad == 0).all()
+    plain = lay.LayerNorm(48, weight=False, bias=False)
+    (g,) = torch.autograd.grad(plain(x).sum(), x)
+    assert g.shape == x.shape
+    q, kv = x.detach().view(B, T, 8, 6).requires_grad_(), torch.zeros(B, 9, 2, 6, device=DEV, dtype=dtype)
+    lay.attend(q, kv, kv).sum().backward()
+    assert q.grad.shape == q.shape
+    kv.requires_grad_()
+    for t in torch.autograd.grad(lay.attend(q, kv, kv).sum(), (q, kv)):
+        assert (t == 0).all()
