@@ -153,3 +153,64 @@ def test_modules_on_batches_of_nothing(dtype, B, T):
     kv.requires_grad_()
     for t in torch.autograd.grad(lay.attend(q, kv, kv).sum(), (q, kv)):
         assert (t == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("mask", ["documents", "lengths"])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 0.5])
+@pytest.mark.parametrize("cap,slope", [(0.0, 0.0), (4.0, 0.0), (0.0, 0.1)])
+@pytest.mark.parametrize("Tq,T,H,Hkv,D", [(150, 150, 6, 2, 64), (2, 700, 8, 2, 64), (40, 200, 4, 1, 128)])
+def test_attention_of_any_scale(dtype, mask, scale, cap, slope, Tq, T, H, Hkv, D):
+    """A scale below zero turns the order of the products; one of zero takes all alike."""
+    kw = dict(_mask(mask, 2, Tq, T), scale=scale, cap=cap)
+    if slope:
+        kw["slopes"] = torch.full((H,), slope)
+    _check(dtype, *_heads(dtype, 2, Tq, T, H, Hkv, D), kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Tq", [200, 3])
+def test_attention_of_expanded_keys(dtype, Tq):
+    """One prompt's keys and values for all samples, and one head's for all heads."""
+    Q, K, V, dO = _heads(dtype, 3, Tq, 200, 4, 2, 64)
+    for axis in (0, 2):
+        k, v = (t.narrow(axis, 0, 1) for t in (K, V))
+        dev = [Q.to(DEV)] + [t.to(DEV).expand(K.shape) for t in (k, v)]
+        assert dev[1].stride(axis) == 0
+        _check(dtype, Q, k.expand(K.shape), v.expand(V.shape), dO, {}, dev=dev)
+
+
+@pytest.mark.parametrize("Tq,T,H,Hkv,D", [(640, 640, 8, 2, 64), (600, 777, 4, 4, 64), (500, 500, 4, 1, 128)])
+def test_attention_to_the_roundings_of_its_parts(Tq, T, H, Hkv, D):
+    """bf16, all keys, independent inputs: the errors of the many terms of a sum do not add up
+    but in the mean square.  A rounding to bf16 is off by 2^-8 at most, spread evenly over that,
+    2^-8 / sqrt(3) in the mean square; a result has up to three in a row (the weights P or dS,
+    delta's output, itself): 2^-8 together, in the 2-norm of 10^5 values.  A term that is wrong
+    by one part in a hundred of the result shows."""
+    Q, K, V, dO = _heads(BF16, 2, Tq, T, H, Hkv, D)
+    ref = block.attention(_np(Q), _np(K), _np(V), causal=False, dO=_np(dO))
+    q, k, v, do = (t.to(DEV) for t in (Q, K, V, dO))
+    lse = torch.empty(2, H, Tq, device=DEV)
+    out = rnc.dprc_attention(q, k, v, causal=False, lse=lse)
+    dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
+    rnc.dprc_attention_grad(do, q, k, v, out, lse, causal=False, dQ=dq, dK=dk, dV=dv)
+    for name, a, b in (("out", out, ref[0]), ("dQ", dq, ref[2]), ("dK", dk, ref[3]), ("dV", dv, ref[4])):
+        _near(a, b, 2.0 ** -8, name)
+
+
+@pytest.mark.parametrize("mask", ["causal", "all", "full documents"])
+@pytest.mark.parametrize("Tq,T,H,Hkv,D", [(37, 37, 128, 1, 64), (90, 90, 100, 1, 128), (50, 50, 96, 2, 72),
+                                          (1, 500, 128, 1, 64), (2, 300, 32, 2, 64), (9, 300, 3, 1, 40)])
+def test_attention_of_wide_groups(mask, Tq, T, H, Hkv, D):
+    """Groups of heads that fill a tile of rows by themselves, or leave part of it; all masks at once
+    over few tokens."""
+    _check(BF16, *_heads(BF16, 2, Tq, T, H, Hkv, D), _mask(mask, 2, Tq, T))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("d", [7, 64, 1027, 2048, 5003, 16383])
+def test_normalisation_in_place(dtype, d):
+    x = _randn((3, 41, d), dtype, d).to(DEV)
+    w = _randn((d,), dtype, d + 1).to(DEV)
+    y = rnc.dprc_layernorm(x, w)
+    assert rnc.dprc_layernorm(x, w, out=x) is x and torch.equal(x, y)
