@@ -572,7 +572,8 @@ dprc_status dprc_layernorm_grad(const void* dY, const void* X, const float* stat
  *  positions device [B][T][axes], int32 (position_bytes 4) or int64 (8); freqs device
  *  double [P], radians; sections host [axes].
  *  B, T >= 0, 1 <= H <= 65535, 1 <= D <= 4096, 1 <= axes <= 8, 2 P <= D.
- *  Angles are reduced in fp64 (positions to 2^53 count); sines and products in fp32.
+ *  Angles are reduced in fp64, off by 3 2^-53 of themselves at most (7e-7 radians at 2^31);
+ *  sines and products in fp32.
  */
 dprc_status dprc_rotary(const void* X, const int64_t* x_stride, dprc_dtype dtype, int64_t B,
                         int64_t T, int64_t H, int64_t D, const void* positions,
@@ -590,14 +591,14 @@ dprc_status dprc_rotary(const void* X, const int64_t* x_stride, dprc_dtype dtype
  * A query that sees nothing gets zeros, and lse -inf.
  *  Q device [B][Tq][H][D], K and V [B][Tk][Hkv][D], of dtype, with strides (of B, T
  *  and H, in elements; a head's elements lie together; any alignment of the type).
- *  slopes float [H]; docs int32 [B][Tk] (a negative id is padding); prefix, lengths
- *  (clamped to 0..Tk) and first int32 [B]; NULL: slopes 0, one document, no prefix,
- *  all Tk keys, first = Tk - Tq.
+ *  slopes float [H], finite, of either sign; docs int32 [B][Tk] (a negative id is
+ *  padding); prefix, lengths (clamped to 0..Tk) and first int32 [B]; NULL: slopes 0, one
+ *  document, no prefix, all Tk keys, first = Tk - Tq.
  *  out [B][Tq][H][D] of dtype, dense; lse float [B][H][Tq] or NULL: the logarithm of
  *  the sum of exp(s), which the gradient needs.
- *  Keys behind lengths[b], behind what any query of the call sees, or of a negative
- *  document are not used, whatever they hold.  A key that some queries see and
- *  others do not must be finite (a NaN or infinity in it may reach both).
+ *  Keys behind lengths[b], behind the last that any query of the call sees, or of a negative
+ *  document are not used, whatever they hold.  Every other key must be finite, whether
+ *  queries see it or not (a NaN or infinity in it may reach those that do not).
  *  Scores, softmax and sums in fp32.  For bf16 the softmax's weights (and the
  *  gradient of the scores) enter the products rounded to bf16.
  *  1 <= D <= 128, Tq, Tk <= 2^20, B Hkv <= 65535, Tq H / Hkv <= 2^28, H / Hkv <= 4096,

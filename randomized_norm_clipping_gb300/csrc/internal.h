@@ -123,11 +123,12 @@ size_t plan_exact_bytes(dprc_dtype dt, int64_t B, int64_t T, int64_t d, int64_t 
 // 3-D bf16 tensor map over [dim2][dim1][dim0] (dim0 contiguous) with row
 // strides in elements, a box of (box0, box1, 1) and the given swizzle bytes
 // (0, 32, 64 or 128).
-bool make_tmap_4d_bf16(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
-                       const uint64_t (&strides)[3], const uint32_t (&box)[4]);
 bool make_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t dim1,
                        uint64_t dim2, uint64_t stride1_elems, uint64_t stride2_elems,
                        uint32_t box0, uint32_t box1, int swizzle_bytes);
+// The same of four axes, 128-byte swizzle; dims and box width first, strides in elements.
+bool make_tmap_4d_bf16(CUtensorMap* map, const void* base, const uint64_t (&dims)[4],
+                       const uint64_t (&strides)[3], const uint32_t (&box)[4]);
 
 // ---- launchers (return cudaSuccess or the launch error) --------------------
 // Row projection on tensor cores: W[i] = X[i] R[i] with X [B][T][c] bf16 and

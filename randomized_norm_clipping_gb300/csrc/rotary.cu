@@ -6,8 +6,10 @@
 // Bound by bytes: every element is read and written once.  A CTA takes a piece of
 // tokens, forms the sines of its tokens and pairs once, in shared memory, for all
 // heads, and streams the heads past them.  The angle is reduced to a part of a
-// turn in fp64 (a few operations per token and pair, shared by the heads), so
-// that a position of 2^31 costs no accuracy; the sine itself is fp32.  Measured: 4 x 4096
+// turn in fp64 (a few operations per token and pair, shared by the heads), whose three
+// roundings, of 1 / (2 pi), of its product with the frequency and of that with the position,
+// put it off by 3 2^-53 of itself at most: below fp32's half step of a radian up to 1.7e8
+// radians, 7e-7 at 2^31; the sine itself is fp32.  Measured: 4 x 4096
 // tokens of 40 heads of 64, bf16, 34.7 us (168 MB: 4.8 TB/s, 0.71 of the copy rate).
 
 #include <algorithm>
