@@ -1546,7 +1546,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 
 // What the keys' kernel reads of a tile's rows, kRowStages tiles in turn.
 struct RowStage {
-  float off[kTile];    // -lse log2(e)
+  float off[kTile];    // -lse log2(e); -inf: a row that sees nothing, or is none
   float delta[kTile];
   float slope2[kTile];
   float pos[kTile];    // against the first key of the tile
@@ -1779,9 +1779,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       // what the rows see, their statistics and where they stand
       Bits it(bits, words);
       int n = 0;
-      // Rows that are none stand as zeros, and their weights are of no account while they are
-      // finite (so no bias: exp of a rising one is not, and inf times 0 is NaN), unless
-      // the tile has keys that nobody sees: those may be anything.
+      // Rows that are none stand as zeros, and their weights are 0 whatever their bias (lse inf),
+      // unless the tile has keys that nobody sees: those may be anything, and NaN stays NaN.
       int all = keys;
       if (a.causal) {
         all = min(keys, first + a.Tq);
@@ -1807,7 +1806,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         for (int q = 0; q < 4; ++q) {
           const int tok = i * x.nt + tt[q];
           see[q] = {0, none, -3};
-          lse[q] = del[q] = 0.f;
+          lse[q] = INFINITY;
+          del[q] = 0.f;
           if (tt[q] < x.nt && tok < a.Tq) {
             lse[q] = ld_once(a.lse_in + at[q] + tok);
             del[q] = ld_once(a.delta + at[q] + tok);
@@ -1824,20 +1824,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int r = q * 32 + lane;
-          const bool is = tt[q] < x.nt && i * x.nt + tt[q] < a.Tq;
-          if (is) {
-            // (a document behind its sample's length: the position sees keys, the query none)
-            if (lse[q] == -INFINITY) see[q].lim = 0;
-            if (see[q].doc >= 0) {
-              lo = min(lo, see[q].doc);
-              hi = max(hi, see[q].doc);
-            }
-            dirty |= see[q].lim == 0;
+          if (tt[q] < x.nt && i * x.nt + tt[q] < a.Tq && see[q].doc >= 0) {
+            lo = min(lo, see[q].doc);
+            hi = max(hi, see[q].doc);
           }
+          dirty |= lse[q] == -INFINITY;
           min_lim = min(min_lim, see[q].lim);
-          st.off[r] = lse[q] == -INFINITY ? 0.f : -lse[q] * kLog2e;
+          st.off[r] = lse[q] == -INFINITY ? -INFINITY : -lse[q] * kLog2e;
           st.delta[r] = del[q];
-          st.slope2[r] = is ? slope[q] : 0.f;
+          st.slope2[r] = slope[q];
           st.pos[r] = static_cast<float>(see[q].pos - j0);
           st.lim[r] = see[q].lim;
           st.doc[r] = see[q].doc;
@@ -1936,7 +1931,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
       tmem_st_wait();
       if (st.dirty) {
-        // rows that see nothing may be anything, and 0 times NaN is NaN: their queries
+        // rows that see nothing (also those whose position does, but of whose document no key
+        // is below the length) may be anything, and 0 times NaN is NaN: their queries
         // and gradients are summed over (dP, which reads them too, is complete)
         ok = wait_warp<false>(dpfull, n & 1, DPRC_DEVERR_ACCUM, abort_flag);
         if (!ok) break;
@@ -1947,7 +1943,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
           ok = wait_warp<false>(&full[pos.s], pos.parity, DPRC_DEVERR_PIPE_FULL, abort_flag) &&
                wait_warp<false>(&full[op.s], op.parity, DPRC_DEVERR_PIPE_FULL, abort_flag);
           if (!ok) break;
-          if (st.lim[r] == 0) {
+          if (st.off[r] == -INFINITY) {
             zero_row<kBlocks>(ring + pos.s * Cfg::kSlot, r);
             zero_row<kBlocks>(ring + op.s * Cfg::kSlot, r);
           }
